@@ -26,7 +26,6 @@ from __future__ import annotations
 
 import argparse
 import ctypes
-import glob
 import hashlib
 import json
 import math
@@ -136,11 +135,16 @@ def measured_peaks():
         return FALLBACK_HBM_GBS, "fallback"
 
 
+# the files that the kernels of the traffic record are compiled from
+TRAFFIC_SOURCES = ("cluster.cuh", "dense_row.cuh", "device_common.cuh", "fibatt_internal.h", "resident.cu",
+                   "row_math.cuh", "row_run.cuh", "stream.cu", "tma_common.cuh")
+
+
 def kernel_source_hash() -> str:
     h = hashlib.sha256()
-    for p in sorted(glob.glob(os.path.join(ROOT, "sparse_head_self_gb300", "csrc", "*"))):
-        with open(p, "rb") as f:
-            h.update(os.path.basename(p).encode())
+    for name in TRAFFIC_SOURCES:
+        with open(os.path.join(ROOT, "sparse_head_self_gb300", "csrc", name), "rb") as f:
+            h.update(name.encode())
             h.update(f.read())
     return h.hexdigest()[:16]
 

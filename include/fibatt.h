@@ -17,7 +17,12 @@
  *       O_j  = sum_{k:(j,k) in Omega_h} exp(s_jk - LSE_j) V_k
  *   (README, Algorithm 3: scores, mask, row softmax, weighted sum of V).
  *
- * Conventions shared by every call below:
+ * Beside it, for the layers around it: the norms of queries and keys with the
+ * position rotation (fibatt_qk_norm_fwd, _bwd) and the attention to another
+ * sequence's states (fibatt_cross_fwd, _bwd).
+ *
+ * Conventions shared by every call below (the two beside it state their own
+ * layouts):
  *   - Tensors are dense, row-major [B, H, N, D] with D = 64 (one row = 64
  *     contiguous elements), in the I/O dtype fibatt_dtype; LSE is fp32
  *     [B, H, N].  All tensor pointers are DEVICE pointers owned by the
@@ -197,6 +202,131 @@ fibatt_status fibatt_bwd_noalloc(fibatt_support_t s, int B, int D, fibatt_dtype 
                                  const float *LSE, const void *dO, float scale,
                                  void *dQ, void *dK, void *dV, cudaStream_t stream);
 
+/* ------------------------------------------------- query and key norms --- */
+
+/* Norm of every query and key head with the position rotation, from the
+ * packed projection of a layer straight to the [B, H, N, 64] tensors that the
+ * attention calls read:
+ *     X [B, N, (Hq + Hk + Hv) 64]:  Hq query heads, Hk key heads, Hv value
+ *     heads of each token side by side (any of the three counts may be 0).
+ * One query head's values x, with the weight w = q_weight, and likewise one
+ * key head's with k_weight:
+ *     y = w x / sqrt(<x, x> / 64 + eps)     (y = x where the weight is NULL)
+ * then the first rot_dims values of y in pairs (y1, y2), pair i of a token at
+ * position p by the angle whose cosine and sine are c = cos[p, i], s = sin[p, i]:
+ *     (y1, y2) -> (y1 c - y2 s, y1 s + y2 c)
+ * Pairs are dims (i, i + rot_dims / 2), or neighbours (2 i, 2 i + 1) when
+ * interleaved is set.  Value heads are copied.  Arithmetic in fp32, one
+ * rounding to the I/O type. */
+typedef struct {
+    int B, N;                    /* sequences, tokens                               */
+    int Hq, Hk, Hv;              /* heads of each kind, >= 0, one at least           */
+    int D;                       /* head dim, FIBATT_HEAD_DIM                        */
+    fibatt_dtype dtype;          /* of X, the weights, Q, K, V and their gradients   */
+    const void *q_weight;        /* [64] or NULL: queries are not normalised         */
+    const void *k_weight;        /* [64] or NULL: keys are not normalised            */
+    float eps;                   /* finite, >= 0                                     */
+    int rot_dims;                /* 0 (no rotation), 16, 32, 48 or 64                */
+    int interleaved;             /* pairs are neighbours                             */
+    const float *cos, *sin;      /* [table_len, rot_dims / 2] fp32; unused when rot_dims is 0 */
+    int table_len;
+    const int32_t *positions;    /* [B, N] (rows positions_stride_b apart; 0: one row for
+                                    every sequence) or NULL: token n is at position n.
+                                    A token at a negative position is not rotated (a class
+                                    token, say); one at table_len or behind it is not rotated
+                                    either, and sets bit 3 of the device error word.   */
+    int64_t positions_stride_b;
+} fibatt_qk_norm;
+
+/* X: token rows of (Hq + Hk + Hv) 64 contiguous elements, x_stride_n elements
+ * between the tokens and x_stride_b between the sequences of one.  Writes
+ * Q [B, Hq, N, 64], K [B, Hk, N, 64] and V [B, Hv, N, 64], dense (a part
+ * without heads may be NULL).  INVALID_ARG: B or N < 1, a negative head count
+ * or none, a NULL or misaligned pointer (16 bytes; positions 4), a stride
+ * that is not a multiple of 16 bytes, eps, rot_dims or table_len out of their range,
+ * positions NULL with table_len < N.  UNSUPPORTED: D, dtype. */
+fibatt_status fibatt_qk_norm_fwd(const fibatt_qk_norm *d, const void *X, int64_t x_stride_b,
+                                 int64_t x_stride_n, void *Q, void *K, void *V, cudaStream_t stream);
+
+/* Device scratch of fibatt_qk_norm_bwd, in bytes (the blocks' sums of the
+ * weights' gradients). */
+size_t fibatt_qk_norm_bwd_workspace_bytes(void);
+
+/* Gradient of the call above: from dQ, dK, dV (dense, as Q, K, V) to dX
+ * (strides as X's; may not overlap X) and to the weights' gradients
+ * dq_weight, dk_weight [64] in the I/O type, summed over all tokens and heads
+ * in fp32 in a fixed order (written only where the weight is not NULL; either
+ * may be NULL when its gradient is not wanted).  workspace: 16-byte aligned,
+ * for one call at a time. */
+fibatt_status fibatt_qk_norm_bwd(const fibatt_qk_norm *d, const void *X, int64_t x_stride_b,
+                                 int64_t x_stride_n, const void *dQ, const void *dK, const void *dV,
+                                 void *dX, int64_t dx_stride_b, int64_t dx_stride_n, void *dq_weight,
+                                 void *dk_weight, void *workspace, size_t ws_bytes, cudaStream_t stream);
+
+/* ------------------------------------------------------ cross attention --- */
+
+/* Attention of the queries of one sequence to the states of another (a
+ * decoder's to an encoder's): Nq queries, Nk keys and values, every query head
+ * h reading key/value head h / (Hq / Hkv).  Sequence b attends the keys
+ *     k < kv_len[b] (every key when kv_len is NULL)   and
+ *     key_mask[b, k] != 0 (every key when key_mask is NULL),
+ * the same for all its queries:
+ *     s_jk = scale <Q_j, K_k>,  LSE_j = log sum_k exp(s_jk),
+ *     O_j = sum_k exp(s_jk - LSE_j) V_k
+ * A sequence that attends no key gets O = 0 and LSE = -inf.  What memory
+ * holds in keys and values that are not attended (NaN, infinities) reaches no
+ * result, and their gradients are zeros. */
+typedef struct {
+    int B, Hq, Hkv;              /* >= 1; Hkv divides Hq                             */
+    int Nq, Nk;                  /* >= 1                                             */
+    int D;                       /* head dim, FIBATT_HEAD_DIM                        */
+    fibatt_dtype dtype;
+    float scale;                 /* any finite value                                 */
+    const int32_t *kv_len;       /* device, [B], or NULL; clamped to [0, Nk]          */
+    const uint8_t *key_mask;     /* device, [B, Nk] bytes, or NULL                    */
+    int64_t key_mask_stride_b;   /* bytes between the mask's rows (0: one for all)    */
+} fibatt_cross;
+
+/* A tensor of heads: element [b, h, n, d] at ptr + b stride_b + h stride_h +
+ * n stride_n + d (strides in elements), so that [B, H, N, 64] and
+ * [B, N, H, 64] tensors and slices of packed projections are all read and
+ * written in place.  ptr 16-byte aligned, strides >= 0 and multiples of 16
+ * bytes; a tensor that a call writes has no two rows in one place (strides
+ * of 0 only over one element), one that it reads may (a stride of 0
+ * broadcasts). */
+typedef struct {
+    void *ptr;
+    int64_t stride_b, stride_h, stride_n;
+} fibatt_heads;
+
+/* Forward pass.  Q, O: Hq heads of Nq rows; K, V: Hkv heads of Nk rows; LSE:
+ * [B, Hq, Nq] fp32, dense, natural log.  Arithmetic is fp32 with fp32
+ * accumulation; for bf16 the softmax weights are rounded to bf16 before their
+ * product with V (the sums and the LSE use the unrounded ones), and O once at
+ * the end.  INVALID_ARG: a size or stride out of its range, a NULL or
+ * misaligned pointer, a scale that is not finite, more than 2^31 - 1 blocks.
+ * UNSUPPORTED: D, dtype. */
+fibatt_status fibatt_cross_fwd(const fibatt_cross *d, const fibatt_heads *Q, const fibatt_heads *K,
+                               const fibatt_heads *V, const fibatt_heads *O, float *LSE,
+                               cudaStream_t stream);
+
+/* Device scratch of fibatt_cross_bwd, in bytes (two floats a query row). */
+size_t fibatt_cross_bwd_workspace_bytes(const fibatt_cross *d);
+
+/* Backward pass for the loss whose gradient with respect to O is dO:
+ *     P_jk = exp(s_jk - LSE_j),  D_j = <dO_j, O_j>,  dS_jk = P_jk (<dO_j, V_k> - D_j),
+ *     dQ_j = scale sum_k dS_jk K_k,   dK_k = scale sum_j dS_jk Q_j,   dV_k = sum_j P_jk dO_j,
+ * the last two over the queries of every head that shares the key head.  No
+ * atomics: results do not depend on scheduling.  For bf16, P and dS are
+ * rounded to bf16 before the products that sum them.  O and LSE are
+ * fibatt_cross_fwd's.  workspace: 16-byte aligned, for one call at a time.
+ * Errors as fibatt_cross_fwd, plus INVALID_ARG for a workspace too small. */
+fibatt_status fibatt_cross_bwd(const fibatt_cross *d, const fibatt_heads *Q, const fibatt_heads *K,
+                               const fibatt_heads *V, const fibatt_heads *O, const float *LSE,
+                               const fibatt_heads *dO, const fibatt_heads *dQ, const fibatt_heads *dK,
+                               const fibatt_heads *dV, void *workspace, size_t ws_bytes,
+                               cudaStream_t stream);
+
 /* Message for the last failing call on this thread ("" if none). */
 const char *fibatt_last_error(void);
 
@@ -209,7 +339,8 @@ const char *fibatt_version(void);
  * (2) when a producer left before its last copies had landed (also after
  * about 2 s); bit 2 (4), in the bounds-checked debug build only (built with
  * -DFIBATT_CHECKS), when a kernel's bounds check failed and it skipped the
- * access (the first failing source line is then printed to stderr).  The
+ * access (the first failing source line is then printed to stderr); bit 3
+ * (8) when fibatt_qk_norm_fwd or _bwd met a position behind its tables.  The
  * word is the OR over every kernel file's copy.  This call synchronises with
  * the device.  With clear != 0 the word is reset.  CUDA on a failed copy. */
 fibatt_status fibatt_device_error(int clear, unsigned *code);

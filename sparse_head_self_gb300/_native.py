@@ -54,6 +54,38 @@ _SIGS = {
 }
 
 
+class Heads(ctypes.Structure):
+    """fibatt_heads: a head tensor by pointer and strides (elements)."""
+    _fields_ = [("ptr", _vp), ("stride_b", ctypes.c_int64), ("stride_h", ctypes.c_int64), ("stride_n", ctypes.c_int64)]
+
+
+class Cross(ctypes.Structure):
+    """fibatt_cross: the sizes and key sets of a cross attention."""
+    _fields_ = [(n, ctypes.c_int) for n in ("B", "Hq", "Hkv", "Nq", "Nk", "D", "dtype")] + [
+        ("scale", ctypes.c_float), ("kv_len", _vp), ("key_mask", _vp), ("key_mask_stride_b", ctypes.c_int64)]
+
+
+class QkNorm(ctypes.Structure):
+    """fibatt_qk_norm: the sizes, weights and angles of a query/key norm."""
+    _fields_ = [(n, ctypes.c_int) for n in ("B", "N", "Hq", "Hk", "Hv", "D", "dtype")] + [
+        ("q_weight", _vp), ("k_weight", _vp), ("eps", ctypes.c_float), ("rot_dims", ctypes.c_int),
+        ("interleaved", ctypes.c_int), ("cos", _vp), ("sin", _vp), ("table_len", ctypes.c_int),
+        ("positions", _vp), ("positions_stride_b", ctypes.c_int64)]
+
+
+_headsp, _i64 = ctypes.POINTER(Heads), ctypes.c_int64
+_SIGS.update({
+    "fibatt_qk_norm_fwd": (ctypes.c_int, [ctypes.POINTER(QkNorm), _vp, _i64, _i64, _vp, _vp, _vp, _vp]),
+    "fibatt_qk_norm_bwd_workspace_bytes": (ctypes.c_size_t, []),
+    "fibatt_qk_norm_bwd": (ctypes.c_int, [ctypes.POINTER(QkNorm), _vp, _i64, _i64, _vp, _vp, _vp, _vp, _i64, _i64,
+                                          _vp, _vp, _vp, ctypes.c_size_t, _vp]),
+    "fibatt_cross_fwd": (ctypes.c_int, [ctypes.POINTER(Cross), _headsp, _headsp, _headsp, _headsp, _vp, _vp]),
+    "fibatt_cross_bwd_workspace_bytes": (ctypes.c_size_t, [ctypes.POINTER(Cross)]),
+    "fibatt_cross_bwd": (ctypes.c_int, [ctypes.POINTER(Cross)] + [_headsp] * 4 + [_vp] + [_headsp] * 4
+                         + [_vp, ctypes.c_size_t, _vp]),
+})
+
+
 class FibattError(RuntimeError):
     def __init__(self, status: int, message: str):
         super().__init__(f"libfibatt {STATUS_NAMES.get(status, status)}: {message}")

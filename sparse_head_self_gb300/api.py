@@ -6,6 +6,7 @@ calls on CPU tensors are rejected.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 
 import torch
@@ -265,5 +266,281 @@ def fibottention(Q, K, V, support: Support, scale: float | None = None):
     return FibottentionFunction.apply(Q, K, V, support, float(scale))
 
 
+# ---------------------------------------------------- query and key norms
+
+def _check_tensor(name: str, t, dtype, device) -> None:
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.device.type != "cuda":
+        raise ValueError(f"{name} must be a CUDA tensor (libfibatt has no CPU path)")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} has dtype {t.dtype}, expected {dtype}")
+
+
+def _on(stream, device):
+    """The launching stream current, with its device: what a call allocates
+    then belongs to the stream that uses it."""
+    if stream is not None:
+        return torch.cuda.stream(stream)
+    if device.index != torch.cuda.current_device():
+        return torch.cuda.device(device)
+    return contextlib.nullcontext()
+
+
+def rotary_tables(angles: torch.Tensor):
+    """(cos, sin) for qk_norm from a table of angles [positions, pairs] (any
+    float type; far positions want float64): fp32, contiguous."""
+    if angles.dim() != 2 or angles.shape[1] not in (8, 16, 24, 32):
+        raise ValueError("angles must be [positions, pairs] with 8, 16, 24 or 32 pairs")
+    return angles.cos().float().contiguous(), angles.sin().float().contiguous()
+
+
+def rotary_angles(positions: int, rot_dims: int = HEAD_DIM, theta: float = 10000.0, device=None) -> torch.Tensor:
+    """Angles p theta^(-2 i / rot_dims) of positions 0..positions - 1, float64."""
+    half = rot_dims // 2
+    freq = theta ** (-torch.arange(half, dtype=torch.float64, device=device) / half)
+    return torch.arange(positions, dtype=torch.float64, device=device)[:, None] * freq
+
+
+def rotary_angles_2d(height: int, width: int, rot_dims: int = HEAD_DIM, theta: float = 100.0,
+                     device=None) -> torch.Tensor:
+    """Angles of a height x width grid of patches, row by row: the first half
+    of the pairs turns with the patch's row, the second with its column."""
+    if rot_dims % 4:
+        raise ValueError("rot_dims must be a multiple of 4")
+    rows = rotary_angles(height, rot_dims // 2, theta, device)
+    cols = rotary_angles(width, rot_dims // 2, theta, device)
+    return torch.cat([rows[:, None].expand(-1, width, -1), cols[None].expand(height, -1, -1)], -1).reshape(
+        height * width, rot_dims // 2)
+
+
+def _norm_desc(x, heads, q_weight, k_weight, eps, rotary, positions, interleaved):
+    if not isinstance(x, torch.Tensor) or x.dim() != 3:
+        raise ValueError("x must be [B, N, (Hq + Hk + Hv) * 64]")
+    if x.dtype not in _DTYPES:
+        raise ValueError(f"dtype {x.dtype} unsupported (float32 or bfloat16)")
+    dev = x.device
+    _check_tensor("x", x, x.dtype, dev)
+    Hq, Hk, Hv = (int(h) for h in heads)
+    B, N, C = x.shape
+    if min(Hq, Hk, Hv) < 0 or C != (Hq + Hk + Hv) * HEAD_DIM:
+        raise ValueError(f"x has {C} values a token, heads {(Hq, Hk, Hv)} of {HEAD_DIM} need {(Hq + Hk + Hv) * HEAD_DIM}")
+    if x.stride(2) != 1:
+        raise ValueError("x must have contiguous tokens")
+    d = _native.QkNorm(B=B, N=N, Hq=Hq, Hk=Hk, Hv=Hv, D=HEAD_DIM, dtype=_DTYPES[x.dtype], eps=float(eps),
+                       interleaved=int(bool(interleaved)))
+    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
+        if w is not None:
+            _check_io(name, w, (HEAD_DIM,), x.dtype, dev)
+            setattr(d, name, w.data_ptr())
+    if rotary is not None:
+        cos, sin = rotary
+        _check_io("cos", cos, cos.shape, torch.float32, dev)
+        _check_io("sin", sin, cos.shape, torch.float32, dev)
+        if cos.dim() != 2:
+            raise ValueError("cos and sin must be [positions, rot_dims / 2]")
+        d.rot_dims, d.table_len = 2 * cos.shape[1], cos.shape[0]
+        d.cos, d.sin = cos.data_ptr(), sin.data_ptr()
+        if positions is not None:
+            _check_tensor("positions", positions, torch.int32, dev)
+            if tuple(positions.shape) not in ((N,), (B, N)) or (N > 1 and positions.stride(-1) != 1):
+                raise ValueError(f"positions must be [N] or [B, N] with contiguous rows, got {tuple(positions.shape)}")
+            d.positions = positions.data_ptr()
+            d.positions_stride_b = positions.stride(0) if positions.dim() == 2 else 0
+    elif positions is not None:
+        raise ValueError("positions without rotary tables")
+    return d, (B, N, Hq, Hk, Hv)
+
+
+def qk_norm_fwd(x: torch.Tensor, heads, q_weight=None, k_weight=None, eps: float = 1e-6, rotary=None, positions=None,
+                interleaved: bool = False, stream=None):
+    """fibatt_qk_norm_fwd on a packed projection x [B, N, (Hq + Hk + Hv) * 64]
+    with heads = (Hq, Hk, Hv); returns (Q, K, V), [B, H, N, 64] each, None for
+    a kind without heads.  rotary = (cos, sin), [positions, rot_dims / 2] fp32;
+    positions int32 [N] or [B, N]."""
+    d, (B, N, Hq, Hk, Hv) = _norm_desc(x, heads, q_weight, k_weight, eps, rotary, positions, interleaved)
+    with _on(stream, x.device):
+        out = [torch.empty((B, h, N, HEAD_DIM), dtype=x.dtype, device=x.device) if h else None for h in (Hq, Hk, Hv)]
+        check(lib().fibatt_qk_norm_fwd(ctypes.byref(d), x.data_ptr(), x.stride(0), x.stride(1),
+                                       *(None if t is None else t.data_ptr() for t in out),
+                                       _stream_ptr(stream, x.device)))
+    return tuple(out)
+
+
+def qk_norm_bwd(x: torch.Tensor, heads, q_weight, k_weight, dQ, dK, dV, eps: float = 1e-6, rotary=None,
+                positions=None, interleaved: bool = False, workspace: torch.Tensor | None = None, stream=None):
+    """fibatt_qk_norm_bwd: from the gradients of qk_norm_fwd's results (None
+    for a kind without heads) to (dx, dq_weight, dk_weight); a weight that is
+    None has the gradient None."""
+    d, (B, N, Hq, Hk, Hv) = _norm_desc(x, heads, q_weight, k_weight, eps, rotary, positions, interleaved)
+    grads = []
+    for name, g, h in (("dQ", dQ, Hq), ("dK", dK, Hk), ("dV", dV, Hv)):
+        if h:
+            _check_io(name, g, (B, h, N, HEAD_DIM), x.dtype, x.device)
+        grads.append(g.data_ptr() if h else None)
+    with _on(stream, x.device):
+        dx = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        dqw = None if q_weight is None else torch.empty_like(q_weight)
+        dkw = None if k_weight is None else torch.empty_like(k_weight)
+        if workspace is None:
+            workspace = torch.empty(int(lib().fibatt_qk_norm_bwd_workspace_bytes()), dtype=torch.uint8, device=x.device)
+        check(lib().fibatt_qk_norm_bwd(ctypes.byref(d), x.data_ptr(), x.stride(0), x.stride(1), *grads, dx.data_ptr(),
+                                       dx.stride(0), dx.stride(1), None if dqw is None else dqw.data_ptr(),
+                                       None if dkw is None else dkw.data_ptr(), workspace.data_ptr(),
+                                       workspace.numel() * workspace.element_size(), _stream_ptr(stream, x.device)))
+    return dx, dqw, dkw
+
+
+class QkNormFunction(torch.autograd.Function):
+    """Autograd wrapper: forward = fibatt_qk_norm_fwd, backward = fibatt_qk_norm_bwd."""
+
+    @staticmethod
+    def forward(ctx, x, q_weight, k_weight, heads, eps, rotary, positions, interleaved):
+        ctx.how = (tuple(heads), float(eps), rotary, positions, bool(interleaved))
+        ctx.save_for_backward(x, q_weight, k_weight)
+        ctx.set_materialize_grads(False)
+        out = qk_norm_fwd(x, heads, q_weight, k_weight, eps, rotary, positions, interleaved)
+        ctx.shapes = [None if t is None else t.shape for t in out]
+        return out
+
+    @staticmethod
+    def backward(ctx, *grads):
+        x, q_weight, k_weight = ctx.saved_tensors
+        heads, eps, rotary, positions, interleaved = ctx.how
+        grads = [g if s is None else torch.zeros(s, dtype=x.dtype, device=x.device) if g is None else g.contiguous()
+                 for g, s in zip(grads, ctx.shapes)]
+        dx, dqw, dkw = qk_norm_bwd(x, heads, q_weight, k_weight, *grads, eps, rotary, positions, interleaved)
+        return dx, dqw, dkw, None, None, None, None, None
+
+
+def qk_norm(x, heads, q_weight=None, k_weight=None, eps: float = 1e-6, rotary=None, positions=None,
+            interleaved: bool = False):
+    """Differentiable norm of query and key heads with the position rotation:
+    packed projection x [B, N, (Hq + Hk + Hv) * 64] -> (Q, K, V) as
+    qk_norm_fwd (gradients reach x and the weights)."""
+    return QkNormFunction.apply(x, q_weight, k_weight, tuple(int(h) for h in heads), float(eps), rotary, positions,
+                                bool(interleaved))
+
+
+# --------------------------------------------------------- cross attention
+
+def _heads_arg(name: str, t, shape, dtype, device):
+    _check_tensor(name, t, dtype, device)
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.stride(3) != 1:
+        raise ValueError(f"{name} must have contiguous rows")
+    # a dim of one element has no stride that matters
+    s = [st if n > 1 else 0 for st, n in zip(t.stride(), t.shape)]
+    return ctypes.byref(_native.Heads(t.data_ptr(), s[0], s[1], s[2]))
+
+
+def _cross_desc(Q, K, V, scale, kv_len, key_mask):
+    for name, t in (("Q", Q), ("K", K), ("V", V)):
+        if not isinstance(t, torch.Tensor) or t.dim() != 4:
+            raise ValueError(f"{name} must be a [B, H, N, D] tensor")
+    if Q.dtype not in _DTYPES:
+        raise ValueError(f"dtype {Q.dtype} unsupported (float32 or bfloat16)")
+    B, Hq, Nq, D = Q.shape
+    Hkv, Nk = K.shape[1], K.shape[2]
+    d = _native.Cross(B=B, Hq=Hq, Hkv=Hkv, Nq=Nq, Nk=Nk, D=D, dtype=_DTYPES[Q.dtype], scale=float(scale))
+    dev = Q.device
+    if kv_len is not None:
+        _check_io("kv_len", kv_len, (B,), torch.int32, dev)
+        d.kv_len = kv_len.data_ptr()
+    if key_mask is not None:
+        if not isinstance(key_mask, torch.Tensor) or key_mask.dtype not in (torch.bool, torch.uint8):
+            raise ValueError("key_mask must be a bool or uint8 tensor")
+        _check_tensor("key_mask", key_mask, key_mask.dtype, dev)
+        if tuple(key_mask.shape) != (B, Nk) or (Nk > 1 and key_mask.stride(1) != 1):
+            raise ValueError(f"key_mask must be [B, Nk] = {(B, Nk)} with contiguous rows, got {tuple(key_mask.shape)}")
+        d.key_mask, d.key_mask_stride_b = key_mask.data_ptr(), key_mask.stride(0)
+    q = _heads_arg("Q", Q, (B, Hq, Nq, D), Q.dtype, dev)
+    k = _heads_arg("K", K, (B, Hkv, Nk, D), Q.dtype, dev)
+    v = _heads_arg("V", V, (B, Hkv, Nk, D), Q.dtype, dev)
+    return d, q, k, v
+
+
+def cross_fwd(Q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, scale: float, kv_len: torch.Tensor | None = None,
+              key_mask: torch.Tensor | None = None, O: torch.Tensor | None = None, LSE: torch.Tensor | None = None,
+              stream=None):
+    """fibatt_cross_fwd: queries Q [B, Hq, Nq, 64] on keys and values K, V
+    [B, Hkv, Nk, 64] (Hkv divides Hq; any strides whose rows are contiguous);
+    returns (O, LSE), O in Q's layout.  kv_len: int32 [B], the keys each
+    sequence has; key_mask: bool [B, Nk], the keys it attends."""
+    d, q, k, v = _cross_desc(Q, K, V, scale, kv_len, key_mask)
+    dev = Q.device
+    with _on(stream, dev):
+        if O is None:
+            O = torch.empty_like(Q)
+        if LSE is None:
+            LSE = torch.empty(Q.shape[:3], dtype=torch.float32, device=dev)
+        _check_io("LSE", LSE, Q.shape[:3], torch.float32, dev)
+        check(lib().fibatt_cross_fwd(ctypes.byref(d), q, k, v, _heads_arg("O", O, Q.shape, Q.dtype, dev),
+                                     LSE.data_ptr(), _stream_ptr(stream, dev)))
+    return O, LSE
+
+
+def cross_bwd(Q, K, V, O, LSE, dO, scale: float, kv_len=None, key_mask=None, dQ=None, dK=None, dV=None,
+              workspace: torch.Tensor | None = None, stream=None):
+    """fibatt_cross_bwd: (dQ, dK, dV) from cross_fwd's O and LSE and the
+    gradient dO of O; each gradient in its input's layout unless given."""
+    d, q, k, v = _cross_desc(Q, K, V, scale, kv_len, key_mask)
+    dev = Q.device
+    _check_io("LSE", LSE, Q.shape[:3], torch.float32, dev)
+    o, do = _heads_arg("O", O, Q.shape, Q.dtype, dev), _heads_arg("dO", dO, Q.shape, Q.dtype, dev)
+    with _on(stream, dev):
+        dQ = torch.empty_like(Q) if dQ is None else dQ
+        dK = torch.empty_like(K) if dK is None else dK
+        dV = torch.empty_like(V) if dV is None else dV
+        need = int(lib().fibatt_cross_bwd_workspace_bytes(ctypes.byref(d)))
+        if workspace is None:
+            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        check(lib().fibatt_cross_bwd(ctypes.byref(d), q, k, v, o, LSE.data_ptr(), do,
+                                     _heads_arg("dQ", dQ, Q.shape, Q.dtype, dev),
+                                     _heads_arg("dK", dK, K.shape, Q.dtype, dev),
+                                     _heads_arg("dV", dV, V.shape, Q.dtype, dev), workspace.data_ptr(),
+                                     workspace.numel() * workspace.element_size(), _stream_ptr(stream, dev)))
+    return dQ, dK, dV
+
+
+def _readable(t):
+    """t, or a copy that the library reads: contiguous rows, strides and start
+    on 16 bytes."""
+    step = 16 // t.element_size()
+    ok = t.stride(-1) == 1 and t.data_ptr() % 16 == 0 and all(s % step == 0 for s, n in zip(t.stride()[:-1], t.shape) if n > 1)
+    return t if ok else t.clone(memory_format=torch.contiguous_format)
+
+
+class CrossAttentionFunction(torch.autograd.Function):
+    """Autograd wrapper: forward = fibatt_cross_fwd, backward = fibatt_cross_bwd."""
+
+    @staticmethod
+    def forward(ctx, Q, K, V, scale, kv_len, key_mask):
+        Q, K, V = _readable(Q), _readable(K), _readable(V)
+        O, LSE = cross_fwd(Q, K, V, scale, kv_len, key_mask)
+        ctx.save_for_backward(Q, K, V, O, LSE, kv_len, key_mask)
+        ctx.scale = scale
+        return O
+
+    @staticmethod
+    def backward(ctx, dO):
+        Q, K, V, O, LSE, kv_len, key_mask = ctx.saved_tensors
+        dQ, dK, dV = cross_bwd(Q, K, V, O, LSE, _readable(dO), ctx.scale, kv_len, key_mask)
+        return dQ, dK, dV, None, None, None
+
+
+def cross_attention(Q, K, V, scale: float | None = None, kv_len=None, key_mask=None):
+    """Differentiable cross attention: Q [B, Hq, Nq, 64] on K, V [B, Hkv, Nk, 64]
+    (arguments as cross_fwd)."""
+    if scale is None:
+        scale = Q.shape[-1] ** -0.5
+    return CrossAttentionFunction.apply(Q, K, V, float(scale), kv_len, key_mask)
+
+
 __all__ = ["FibattError", "Support", "fwd", "bwd", "bwd_noalloc", "fibottention", "FibottentionFunction",
+           "qk_norm_fwd", "qk_norm_bwd", "qk_norm", "QkNormFunction", "rotary_tables", "rotary_angles",
+           "rotary_angles_2d", "cross_fwd", "cross_bwd", "cross_attention", "CrossAttentionFunction",
            "wythoff_row", "wythoff_row_modified", "window_schedule", "HEAD_DIM"]

@@ -15,6 +15,7 @@
 #include <string>
 #include <vector>
 
+#include "cross.h"
 #include "fibatt_internal.h"
 
 struct fibatt_support {
@@ -22,6 +23,15 @@ struct fibatt_support {
 };
 
 namespace fibatt {
+
+// Host-side fault injection for the error paths: FIBATT_FAULT=launch makes
+// a call report a CUDA launch failure without launching anything,
+// FIBATT_FAULT=arg makes it report an invalid argument.
+bool fault(const char *kind) {
+    const char *e = std::getenv("FIBATT_FAULT");
+    return e && std::strcmp(e, kind) == 0;
+}
+
 namespace {
 
 thread_local std::string g_last_error;
@@ -34,14 +44,6 @@ std::string fmt(const char *f, ...) {
     vsnprintf(buf, sizeof buf, f, ap);
     va_end(ap);
     return buf;
-}
-
-// Host-side fault injection for the error paths: FIBATT_FAULT=launch makes
-// fwd/bwd report a CUDA launch failure without launching anything,
-// FIBATT_FAULT=arg makes them report an invalid argument.
-bool fault(const char *kind) {
-    const char *e = std::getenv("FIBATT_FAULT");
-    return e && std::strcmp(e, kind) == 0;
 }
 
 // floor(sqrt(n)) for 0 <= n <= 2^62: start from the long double root and
@@ -482,6 +484,11 @@ fibatt_status fibatt_device_error(int clear, unsigned *code) {
     if (!code) return set_error(FIBATT_ERR_INVALID_ARG, "code is NULL");
     *code = 0;
     cudaError_t e = read_device_error(code, clear != 0);
+    for (auto reader : {read_error_cross_simt, read_error_qk_norm}) {
+        unsigned c = 0;
+        if (e == cudaSuccess) e = reader(&c, clear != 0);
+        *code |= c;
+    }
     if (e != cudaSuccess) return cuda_error(e, "fibatt_device_error");
     return FIBATT_OK;
 }

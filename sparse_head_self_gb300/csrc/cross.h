@@ -1,0 +1,117 @@
+// Internal declarations of the cross attention (queries of one sequence,
+// keys and values of another) and of the query/key norm with rotation.  The
+// operations and every argument rule are documented in include/fibatt.h.
+#pragma once
+
+#include <cstdint>
+
+#include <cuda_runtime.h>
+
+#include "fibatt.h"
+#include "fibatt_internal.h"
+
+namespace fibatt {
+
+// One head tensor as a kernel sees it: element [b, h, n, d] at
+// p + b sb + h sh + n sn + d (strides in elements).
+template <typename T>
+struct Rows {
+    T *p;
+    int64_t sb, sh, sn;
+    __host__ __device__ T *row(int64_t b, int64_t h, int64_t n) const { return p + b * sb + h * sh + n * sn; }
+};
+
+template <typename T>
+Rows<T> rows_of(const fibatt_heads &v) {
+    return Rows<T>{static_cast<T *>(v.ptr), v.stride_b, v.stride_h, v.stride_n};
+}
+
+// Which keys a sequence attends: k < len[b] and mask[b][k] != 0.
+struct KeySet {
+    const int32_t *len;      // [B] or null
+    const uint8_t *mask;     // [B][Nk] or null
+    int64_t mask_sb;
+    int Nk;
+#ifdef __CUDACC__
+    // keys at or behind the result are not attended
+    __device__ int bound(int b) const { return len ? max(0, min(__ldg(len + b), Nk)) : Nk; }
+    __device__ bool has(int b, int k) const { return !mask || __ldg(mask + b * mask_sb + k) != 0; }
+#endif
+};
+
+struct CrossArgs {
+    int B, Hq, Hkv, Nq, Nk;
+    fibatt_dtype dtype;
+    float scale;
+    KeySet keys;
+    fibatt_heads Q, K, V, O, dO, dQ, dK, dV;
+    float *LSE;              // [B, Hq, Nq]
+    float2 *stats;           // backward: (LSE log2 e, D) of every query row
+    cudaStream_t stream;
+};
+
+// Whether FIBATT_FAULT injects a fault of this kind (api.cpp).
+bool fault(const char *kind);
+
+// Streaming multiprocessors of the current device.
+int sm_count();
+
+// Launch `kern` on clusters of `c` CTAs along x, programmatic dependent when
+// the library launches that way.
+template <typename... KArgs, typename... Args>
+cudaError_t launch_clusters(void (*kern)(KArgs...), unsigned grid, unsigned c, unsigned threads, size_t smem,
+                            cudaStream_t stream, Args &&...args) {
+    const ProfileLaunch prof(stream, reinterpret_cast<const void *>(kern));
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = pdl_enabled() ? 1 : 0;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = c;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, std::forward<Args>(args)...);
+    if (e == cudaSuccess) count_launches(1);
+    return e;
+}
+
+// ---- launchers (return the CUDA launch status) -----------------------------
+cudaError_t launch_cross_fwd_simt(const CrossArgs &a);
+cudaError_t launch_cross_bwd_simt(const CrossArgs &a);
+
+struct QkNormArgs {
+    int B, N, Hq, Hk, Hv;
+    fibatt_dtype dtype;
+    const void *X;
+    int64_t x_sb, x_sn;      // elements
+    const void *wq, *wk;     // [64] in the I/O type, or null: that part is not normalised
+    float eps;
+    int rot;                 // leading dims rotated (0: none)
+    int interleaved;
+    const float *cos, *sin;  // [P, rot / 2]
+    int P;
+    const int32_t *pos;      // [B, N] with batch stride pos_sb (0: one row for all), or null: 0..N-1
+    int64_t pos_sb;
+    void *Q, *K, *V;         // [B, H, N, 64]
+    const void *dQ, *dK, *dV;
+    void *dX;
+    int64_t dx_sb, dx_sn;
+    void *dwq, *dwk;         // [64] in the I/O type
+    float *ws;
+    cudaStream_t stream;
+};
+size_t qk_norm_bwd_workspace();
+cudaError_t launch_qk_norm_fwd(const QkNormArgs &a);
+cudaError_t launch_qk_norm_bwd(const QkNormArgs &a);
+
+// Each kernel file's device error word (device_common.cuh).
+cudaError_t read_error_cross_simt(unsigned *code, bool clear);
+cudaError_t read_error_qk_norm(unsigned *code, bool clear);
+
+}  // namespace fibatt
