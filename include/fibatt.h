@@ -291,9 +291,8 @@ typedef struct {
  * n stride_n + d (strides in elements), so that [B, H, N, 64] and
  * [B, N, H, 64] tensors and slices of packed projections are all read and
  * written in place.  ptr 16-byte aligned, strides >= 0 and multiples of 16
- * bytes; a tensor that a call writes has no two rows in one place (strides
- * of 0 only over one element), one that it reads may (a stride of 0
- * broadcasts). */
+ * bytes; a tensor that a call writes has no two rows in one place, one that it
+ * reads may be broadcast over sequences and heads (stride_b, stride_h of 0). */
 typedef struct {
     void *ptr;
     int64_t stride_b, stride_h, stride_n;

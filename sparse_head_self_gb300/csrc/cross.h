@@ -84,6 +84,7 @@ cudaError_t launch_clusters(void (*kern)(KArgs...), unsigned grid, unsigned c, u
 // ---- launchers (return the CUDA launch status) -----------------------------
 cudaError_t launch_cross_fwd_simt(const CrossArgs &a);
 cudaError_t launch_cross_bwd_simt(const CrossArgs &a);
+cudaError_t launch_cross_fwd_mma(const CrossArgs &a);   // bf16
 
 struct QkNormArgs {
     int B, N, Hq, Hk, Hv;
@@ -112,6 +113,7 @@ cudaError_t launch_qk_norm_bwd(const QkNormArgs &a);
 
 // Each kernel file's device error word (device_common.cuh).
 cudaError_t read_error_cross_simt(unsigned *code, bool clear);
+cudaError_t read_error_cross_mma_fwd(unsigned *code, bool clear);
 cudaError_t read_error_qk_norm(unsigned *code, bool clear);
 
 }  // namespace fibatt

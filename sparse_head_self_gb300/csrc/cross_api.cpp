@@ -47,6 +47,7 @@ fibatt_status check_heads(const fibatt_heads *v, const char *name, fibatt_dtype 
     for (int i = 0; i < 3; ++i) {
         if (strides[i] < 0 || strides[i] > (int64_t)1 << 38 || strides[i] * size_of(t) % 16)
             return invalid(fmt("%s: stride %lld is not a multiple of 16 bytes in [0, 2^38]", name, (long long)strides[i]));
+        if (i == 2 && N > 1 && strides[i] == 0) return invalid(fmt("%s: rows with a stride of 0", name));
         if (out && sizes[i] > 1 && strides[i] < kHeadDim)
             return invalid(fmt("%s is written, but a stride of %lld lets its rows overlap", name, (long long)strides[i]));
     }
@@ -207,7 +208,7 @@ fibatt_status fibatt_cross_fwd(const fibatt_cross *d, const fibatt_heads *Q, con
     if (fault("launch")) return set_error(FIBATT_ERR_CUDA, "injected launch failure (FIBATT_FAULT=launch)");
     CrossArgs a = cross_args(d, Q, K, V, O, stream);
     a.LSE = LSE;
-    const cudaError_t e = launch_cross_fwd_simt(a);
+    const cudaError_t e = a.dtype == FIBATT_BF16 ? launch_cross_fwd_mma(a) : launch_cross_fwd_simt(a);
     return e == cudaSuccess ? FIBATT_OK : cuda_error(e, "fibatt_cross_fwd launch");
 }
 

@@ -65,6 +65,7 @@ def test_cross_refusals(bwd, _no_launch):
         assert st(**{name: _heads(ptr=P + 8)}) == INVALID
         assert st(**{name: _heads(n=68)}) == INVALID      # 136 bytes between the rows
         assert st(**{name: _heads(h=-64)}) == INVALID
+        assert st(**{name: _heads(n=0)}) == INVALID       # no broadcast rows
         assert st(**{name: _heads(b=1 << 39)}) == INVALID
     for name in ("q", "k", "v"):
         assert st(**{name: _heads(b=0)}) == CUDA          # broadcast inputs are read
