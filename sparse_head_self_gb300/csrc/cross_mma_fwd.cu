@@ -7,8 +7,8 @@
 //                      need no exchange with other threads
 //   O += P V           P back to tensor memory as bf16, V across its rows
 // Warps: 4 per tile for the softmax, one that copies (tensor copies into a ring of
-// K/V stages) and clears masked value rows, one that issues the matrix
-// instructions.  S of the next key tile is formed while the softmax works on
+// K/V stages), one that finds each tile's attended keys and clears the other value
+// rows, one that issues the matrix instructions.  S of the next key tile is formed while the softmax works on
 // this one (S and P have columns of their own), so the tensor cores and the
 // exponentials, which take about as long at a head dim of 64, overlap.
 //
@@ -35,7 +35,8 @@ constexpr int kJoinLd = 68;      // floats between rows of a partial O in shared
 template <int NT>
 struct Cfg {
     static constexpr int kSoftmaxWarps = 4 * NT;
-    static constexpr int kCopyWarp = kSoftmaxWarps, kMmaWarp = kSoftmaxWarps + 1;
+    static constexpr int kCopyWarp = kSoftmaxWarps, kKeysWarp = kSoftmaxWarps + 1;
+    static constexpr int kMmaWarp = kSoftmaxWarps + 2;
     static constexpr int kThreads = 32 * (kSoftmaxWarps + 4);   // whole warp groups
     static constexpr int kStages = NT == 2 ? 5 : 2;
     static constexpr uint32_t kCols = NT * 256;        // S 128, P 64, O 64 a tile
@@ -75,7 +76,7 @@ cross_fwd_mma_kernel(const __grid_constant__ FwdMmaArgs a) {
     __shared__ float join_m[NT * kTileRows], join_l[NT * kTileRows];
     volatile int *abort = &abort_flag;
 
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = warp_number(), lane = threadIdx.x & 31;
     const int CS = (int)cluster_size(), rank = (int)cluster_rank();
     const int64_t unit = blockIdx.x / CS;
     const int pair = (int)(unit % a.pairs), hk = (int)(unit / a.pairs % a.Hkv), b = (int)(unit / a.pairs / a.Hkv);
@@ -123,10 +124,8 @@ cross_fwd_mma_kernel(const __grid_constant__ FwdMmaArgs a) {
         bool ok = true;
         if (t < nt) {
             for (int j = 0; j < n; ++j) {
-                const int st = j % C::kStages;
-                ok = mbar_wait(&bar_ready[st], (j / C::kStages) & 1, abort) && mbar_wait(&bar_s[t], j & 1, abort);
+                ok = pipe_wait(&bar_s[t], j & 1, abort);
                 if (!ok) break;
-                const uint4 w = keys[st];
                 tc_after_sync();
                 uint32_t s[4][32];
 #pragma unroll
@@ -137,7 +136,11 @@ cross_fwd_mma_kernel(const __grid_constant__ FwdMmaArgs a) {
                 tc_before_sync();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bar_sfree[t]);
-                if (!all_keys(w)) {
+                if (a.ks.mask || (lo + j + 1) * kTileRows > bound) {
+                    const int st = j % C::kStages;
+                    ok = pipe_wait(&bar_ready[st], (j / C::kStages) & 1, abort);   // keys[st] is written
+                    if (!ok) break;
+                    const uint4 w = keys[st];
                     const uint32_t words[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
@@ -156,14 +159,29 @@ cross_fwd_mma_kernel(const __grid_constant__ FwdMmaArgs a) {
                 }
                 const float next = fmaxf(max3(top[0], top[1], top[2]), top[3]) * a.c;
                 const bool raise = next > m + kRaise;     // also the first finite maximum: m = -inf
+                const float keep = raise ? fast_exp2(m - next) : 1.f;
+                if (raise) m = next;
+                const float base = m == kNegInf ? 0.f : -m;
+                float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+                uint32_t p[2][32];
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int k = 0; k < 32; ++k) {
+                        const int i = 2 * h + (k >> 4), e = 2 * (k & 15);
+                        const float2 x = fma2(make_float2(__uint_as_float(s[i][e]), __uint_as_float(s[i][e + 1])),
+                                              make_float2(a.c, a.c), make_float2(base, base));
+                        const float2 y = make_float2(fast_exp2(x.x), fast_exp2(x.y));
+                        sum[k & 1] = add2(sum[k & 1], y);
+                        p[h][k] = pack_bf16x2(y.x, y.y);
+                    }
                 if (j > 0) {
                     // the product with the last P has read it and written O
-                    ok = mbar_wait(&bar_o[t], (j - 1) & 1, abort);
+                    ok = pipe_wait(&bar_o[t], (j - 1) & 1, abort);
                     if (!ok) break;
+                    tc_after_sync();
                     if (__any_sync(kFullMask, raise)) {
-                        const float keep = raise ? fast_exp2(m - next) : 1.f;
                         l *= keep;
-                        tc_after_sync();
 #pragma unroll
                         for (int i = 0; i < 2; ++i) {
                             uint32_t o[32];
@@ -175,23 +193,8 @@ cross_fwd_mma_kernel(const __grid_constant__ FwdMmaArgs a) {
                         }
                     }
                 }
-                if (raise) m = next;
-                const float base = m == kNegInf ? 0.f : -m;
-                float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    uint32_t p[32];
-#pragma unroll
-                    for (int k = 0; k < 32; ++k) {
-                        const int i = 2 * h + (k >> 4), e = 2 * (k & 15);
-                        const float2 x = fma2(make_float2(__uint_as_float(s[i][e]), __uint_as_float(s[i][e + 1])),
-                                              make_float2(a.c, a.c), make_float2(base, base));
-                        const float2 y = make_float2(fast_exp2(x.x), fast_exp2(x.y));
-                        sum[k & 1] = add2(sum[k & 1], y);
-                        p[k] = pack_bf16x2(y.x, y.y);
-                    }
-                    tmem_st32(tp + 32 * h, p);
-                }
+                for (int h = 0; h < 2; ++h) tmem_st32(tp + 32 * h, p[h]);
                 sum[0] = add2(sum[0], sum[1]);
                 l += sum[0].x + sum[0].y;
                 tmem_wait_st();
@@ -199,7 +202,7 @@ cross_fwd_mma_kernel(const __grid_constant__ FwdMmaArgs a) {
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bar_p[t]);
             }
-            if (n > 0 && ok) ok = mbar_wait(&bar_o[t], (n - 1) & 1, abort);
+            if (n > 0 && ok) ok = pipe_wait(&bar_o[t], (n - 1) & 1, abort);
             tc_after_sync();
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
@@ -243,42 +246,26 @@ cross_fwd_mma_kernel(const __grid_constant__ FwdMmaArgs a) {
             // ---- copies -----------------------------------------------------------
             if (n > 0) {
                 int issued = 0;
-                const auto issue = [&](int j) {   // lane 0: key tile j into its stage
+                const auto issue = [&](int j) {   // key tile j into its stage
                     const int s = j % C::kStages;
-                    mbar_expect_tx(&bar_full[s], 2 * kTileBytes);
-                    load_tile(skv + (2 * s) * kTileBytes, a.k, (lo + j) * kTileRows, hk, b, &bar_full[s]);
-                    load_tile(skv + (2 * s + 1) * kTileBytes, a.v, (lo + j) * kTileRows, hk, b, &bar_full[s]);
+                    if (elect_one()) {
+                        mbar_expect_tx(&bar_full[s], 2 * kTileBytes);
+                        load_tile(skv + (2 * s) * kTileBytes, a.k, (lo + j) * kTileRows, hk, b, &bar_full[s]);
+                        load_tile(skv + (2 * s + 1) * kTileBytes, a.v, (lo + j) * kTileRows, hk, b, &bar_full[s]);
+                    }
+                    __syncwarp();
                 };
-                if (lane == 0) {
+                if (elect_one()) {
                     mbar_expect_tx(&bar_q, nt * a.qt.bytes());
                     for (int t = 0; t < nt; ++t)
                         load_tile(sq + t * kTileBytes, a.q, a.qt.first_row(t0 + t), hk * a.qt.G + a.qt.first_head(t0 + t), b,
                                   &bar_q);
-                    for (; issued < min(n, C::kStages); ++issued) issue(issued);
                 }
-                issued = min(n, C::kStages);
-                for (int j = 0; j < n; ++j) {
-                    // clear the value rows that are not attended, publish which are
-                    const int s = j % C::kStages;
-                    const uint4 w = tile_keys(a.ks, b, (lo + j) * kTileRows, bound);
-                    if (!mbar_wait(&bar_full[s], (j / C::kStages) & 1, abort)) break;
-                    if (!all_keys(w)) {
-                        clear_rows(skv + (2 * s + 1) * kTileBytes, w);
-                        fence_smem_async();
-                    }
-                    __syncwarp();
-                    if (lane == 0) {
-                        keys[s] = w;
-                        mbar_arrive(&bar_ready[s]);
-                    }
-                    // refill the stage of the tile before this one: tile j is ready
-                    // for the tensor cores while its product is waited for
-                    if (j > 0 && issued < n) {
-                        if (!mbar_wait(&bar_empty[(j - 1) % C::kStages], ((j - 1) / C::kStages) & 1, abort)) break;
-                        if (lane == 0) issue(issued);
-                        ++issued;
-                    }
-                    __syncwarp();
+                __syncwarp();
+                for (; issued < n; ++issued) {
+                    const int last = issued - C::kStages;     // the stage's tile before
+                    if (last >= 0 && !pipe_wait(&bar_empty[last % C::kStages], (last / C::kStages) & 1, abort)) break;
+                    issue(issued);
                 }
                 // leave no copy in flight
                 if (lane == 0) {
@@ -287,46 +274,74 @@ cross_fwd_mma_kernel(const __grid_constant__ FwdMmaArgs a) {
                         mbar_drain(&bar_full[j % C::kStages], (j / C::kStages) & 1);
                 }
             }
+        } else if (warp == C::kKeysWarp) {
+            // ---- which keys of each tile are attended; the others' value rows cleared ----
+            for (int j = 0; j < n; ++j) {
+                const int s = j % C::kStages;
+                const uint4 w = tile_keys(a.ks, b, (lo + j) * kTileRows, bound);
+                if (!pipe_wait(&bar_full[s], (j / C::kStages) & 1, abort)) break;
+                if (!all_keys(w)) {
+                    clear_rows(skv + (2 * s + 1) * kTileBytes, w);
+                    fence_smem_async();
+                }
+                __syncwarp();
+                if (lane == 0) {
+                    keys[s] = w;
+                    mbar_arrive(&bar_ready[s]);
+                }
+            }
         } else if (warp == C::kMmaWarp) {
             // ---- matrix instructions --------------------------------------------------
-            if (n > 0 && lane == 0) {
+            // The loop's course depends on uniform values only (a wait that gives up is
+            // not looked at: what follows is not trusted, since the error word is set, and
+            // stays in bounds), which keeps descriptors and counters in uniform registers.
+            const int nu = __shfl_sync(kFullMask, n, 0), ntu = __shfl_sync(kFullMask, nt, 0);
+            if (nu > 0) {
                 const uint32_t id_s = mma_desc(128, 128, false, a.negative), id_o = mma_desc(128, 64, true);
-                const auto scores = [&](int j, int t) {   // S_t = Q_t K_j^T
-                    const uint64_t dq = tile_desc(sq + t * kTileBytes), dk = tile_desc(skv + 2 * (j % C::kStages) * kTileBytes);
-    #pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        mma_ss(col_s + t * 128, dq + i * kStepRowwise, dk + i * kStepRowwise, id_s, i > 0);
-                    mma_commit(&bar_s[t]);
-                };
-                const auto values = [&](int j, int t) {   // O_t += P_t V_j
-                    const uint64_t dv = tile_desc(skv + (2 * (j % C::kStages) + 1) * kTileBytes);
-    #pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        mma_ts(col_o + t * 64, col_p + t * 64 + i * 8, dv + i * kStepAcross, id_o, j > 0 || i > 0);
-                    mma_commit(&bar_o[t]);
-                };
-                bool ok = mbar_wait(&bar_q, 0, abort);
-                for (int j = 0; ok && j <= n; ++j) {
-                    if (j < n) {
-                        ok = mbar_wait(&bar_ready[j % C::kStages], (j / C::kStages) & 1, abort);
-                        for (int t = 0; ok && t < nt; ++t) {
-                            if (j > 0) ok = mbar_wait(&bar_sfree[t], (j - 1) & 1, abort);
-                            if (!ok) break;
+                const uint64_t dq = tile_desc(sq), dk = tile_desc(skv), dv = tile_desc(skv + kTileBytes);
+                int s = 0, ring = 0, s1 = 0;        // stage of tile j and its pass through the ring, stage of tile j - 1
+                pipe_wait(&bar_q, 0, abort);
+                for (int j = 0; j <= nu; ++j) {
+                    if (j < nu) {
+                        pipe_wait(&bar_ready[s], ring, abort);
+                        const uint64_t dks = dk + (uint64_t)(s * (2 * kTileBytes >> 4));
+                        for (int t = 0; t < ntu; ++t) {   // S_t = Q_t K_j^T
+                            if (j > 0) pipe_wait(&bar_sfree[t], (j - 1) & 1, abort);
                             tc_after_sync();
-                            scores(j, t);
+                            const uint64_t dqt = dq + (uint64_t)(t * (kTileBytes >> 4));
+                            if (elect_one()) {
+#pragma unroll
+                                for (int i = 0; i < 4; ++i)
+                                    mma_ss(col_s + t * 128, dqt + i * kStepRowwise, dks + i * kStepRowwise, id_s, i > 0);
+                                mma_commit(&bar_s[t]);
+                            }
+                            __syncwarp();
                         }
                     }
                     if (j > 0) {
-                        for (int t = 0; ok && t < nt; ++t) {
-                            ok = mbar_wait(&bar_p[t], (j - 1) & 1, abort);
-                            if (!ok) break;
+                        const uint64_t dvs = dv + (uint64_t)(s1 * (2 * kTileBytes >> 4));
+                        for (int t = 0; t < ntu; ++t) {   // O_t += P_t V_(j-1)
+                            pipe_wait(&bar_p[t], (j - 1) & 1, abort);
                             tc_after_sync();
-                            values(j - 1, t);
+                            if (elect_one()) {
+#pragma unroll
+                                for (int i = 0; i < 8; ++i)
+                                    mma_ts(col_o + t * 64, col_p + t * 64 + i * 8, dvs + i * kStepAcross, id_o,
+                                           j > 1 || i > 0);
+                                mma_commit(&bar_o[t]);
+                                if (t == ntu - 1) mma_commit(&bar_empty[s1]);
+                            }
+                            __syncwarp();
                         }
-                        if (ok) mma_commit(&bar_empty[(j - 1) % C::kStages]);
+                    }
+                    s1 = s;
+                    if (++s == C::kStages) {
+                        s = 0;
+                        ring ^= 1;
                     }
                 }
-                mma_commit(&bar_end);
+                if (elect_one()) mma_commit(&bar_end);
+                __syncwarp();
                 mbar_drain(&bar_end, 0);   // no matrix instruction in flight when the tensor memory is freed
             }
         }

@@ -91,6 +91,33 @@ __device__ __forceinline__ void give_registers() {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R));
 }
 
+// mbar_wait (tma_common.cuh) for the short waits between the warps of a
+// pipeline: polls without the suspend hint, whose wake-up costs more than such a
+// wait.  Bounded in the same way.
+__device__ __forceinline__ bool pipe_wait(uint64_t *bar, uint32_t parity, volatile int *abort) {
+    const uint32_t b = smem_u32(bar);
+    unsigned long long t0 = 0;
+    for (uint32_t i = 1;; ++i) {
+        uint32_t done;
+        asm volatile(
+            "{ .reg .pred p; mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2; selp.u32 %0, 1, 0, p; }"
+            : "=r"(done)
+            : "r"(b), "r"(parity)
+            : "memory");
+        if (done) return true;
+        if ((i & 63) != 1) continue;
+        if (*abort) return false;
+        const unsigned long long now = global_ns();
+        if (t0 == 0) {
+            t0 = now;
+        } else if (now - t0 > kWaitLimitNs) {
+            atomicOr(&g_device_error, kErrWaitTimeout);
+            *abort = 1;
+            return false;
+        }
+    }
+}
+
 // ---- descriptors --------------------------------------------------------------
 // A swizzled tile at `p` (shared memory): start address in 16-byte units,
 // 1024 bytes between groups of eight rows, version 1, 128-byte swizzle.  The
@@ -108,6 +135,18 @@ __host__ __device__ constexpr uint32_t mma_desc(uint32_t M, uint32_t N, bool acr
     return (1u << 4) | (1u << 7) | (1u << 10) | ((negate_a ? 1u : 0u) << 13) | ((across_b ? 1u : 0u) << 16) |
            ((N >> 3) << 17) | ((M >> 4) << 24);
 }
+
+// One lane of a converged warp.  Matrix instructions and copies are issued
+// inside `if (elect_one())` from code that the whole warp runs, so that their
+// descriptors are formed in uniform registers: from a branch on the lane number
+// each instruction took about 100 cycles to issue.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{ .reg .pred p; elect.sync _|p, 0xffffffff; selp.u32 %0, 1, 0, p; }" : "=r"(p));
+    return p != 0;
+}
+// The warp's number, the same register for the whole warp.
+__device__ __forceinline__ int warp_number() { return __shfl_sync(kFullMask, (int)(threadIdx.x >> 5), 0); }
 
 // ---- matrix instructions (one thread issues them) ------------------------------
 // D (tensor memory) = A B or += A B, A and B from shared memory.
