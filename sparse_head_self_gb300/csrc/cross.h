@@ -81,10 +81,23 @@ cudaError_t launch_clusters(void (*kern)(KArgs...), unsigned grid, unsigned c, u
     return e;
 }
 
+// A kernel that shares its registers out anew (setmaxnreg) is written for the
+// number it is launched with; shares that do not add up would wait for ever.
+template <typename K>
+cudaError_t prepare_kernel(K kern, size_t smem, int regs) {
+    cudaFuncAttributes at;
+    cudaError_t e = cudaFuncGetAttributes(&at, kern);
+    if (e != cudaSuccess) return e;
+    if (at.numRegs != regs) return cudaErrorInvalidKernelImage;
+    return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+}
+
 // ---- launchers (return the CUDA launch status) -----------------------------
 cudaError_t launch_cross_fwd_simt(const CrossArgs &a);
 cudaError_t launch_cross_bwd_simt(const CrossArgs &a);
 cudaError_t launch_cross_fwd_mma(const CrossArgs &a);   // bf16
+cudaError_t launch_cross_bwd_mma(const CrossArgs &a);   // bf16
+cudaError_t launch_cross_stats(const CrossArgs &a);     // a.stats from a.O, a.dO and a.LSE
 
 struct QkNormArgs {
     int B, N, Hq, Hk, Hv;
@@ -114,6 +127,7 @@ cudaError_t launch_qk_norm_bwd(const QkNormArgs &a);
 // Each kernel file's device error word (device_common.cuh).
 cudaError_t read_error_cross_simt(unsigned *code, bool clear);
 cudaError_t read_error_cross_mma_fwd(unsigned *code, bool clear);
+cudaError_t read_error_cross_mma_bwd(unsigned *code, bool clear);
 cudaError_t read_error_qk_norm(unsigned *code, bool clear);
 
 }  // namespace fibatt

@@ -398,7 +398,7 @@ cudaError_t fwd(const CrossArgs &a, const QueryTiles &qt) {
     f.c = std::max(std::fabs(a.scale) * kLog2e, 1e-36f);
     f.negative = a.scale < 0.f;
     const auto kern = cross_fwd_mma_kernel<NT>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kSmem);
+    const cudaError_t e = prepare_kernel(kern, C::kSmem, C::kRegs);
     if (e != cudaSuccess) return e;
     const int64_t units = (int64_t)a.B * a.Hkv * f.pairs;
     const int tiles = (a.Nk + kTileRows - 1) / kTileRows;

@@ -41,9 +41,6 @@ __device__ __forceinline__ float4 load4(const __nv_bfloat16 *p) {
     return make_float4(bf16_lo(v.x), bf16_hi(v.x), bf16_lo(v.y), bf16_hi(v.y));
 }
 __device__ __forceinline__ void store4(float *p, float4 v) { *reinterpret_cast<float4 *>(p) = v; }
-__device__ __forceinline__ void store4(__nv_bfloat16 *p, float4 v) {
-    *reinterpret_cast<uint2 *>(p) = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
-}
 
 // Rows [n0, n0 + 64) of a head into `dst`; rows that `ok` (one bit a row)
 // leaves out are zeros, whatever memory holds there.
@@ -454,9 +451,7 @@ cudaError_t bwd(const CrossArgs &a) {
     if (e != cudaSuccess) return e;
     const auto Q = rows_of<const T>(a.Q), K = rows_of<const T>(a.K), V = rows_of<const T>(a.V),
                dO = rows_of<const T>(a.dO);
-    const int64_t rows = (int64_t)a.B * a.Hq * a.Nq;
-    e = launch_clusters(cross_stats_kernel<T>, (unsigned)((rows + 15) / 16), 1, 256, 0, a.stream, a.Hq, a.Nq, rows,
-                        rows_of<const T>(a.O), dO, static_cast<const float *>(a.LSE), a.stats);
+    e = launch_cross_stats(a);
     if (e != cudaSuccess) return e;
     const int qtiles = (a.Nq + kT - 1) / kT, ktiles = (a.Nk + kT - 1) / kT;
     const int64_t qunits = (int64_t)a.B * a.Hq * qtiles, kunits = (int64_t)a.B * a.Hkv * ktiles;
@@ -469,15 +464,22 @@ cudaError_t bwd(const CrossArgs &a) {
                            ktiles);
 }
 
+template <typename T>
+cudaError_t stats(const CrossArgs &a) {
+    const int64_t rows = (int64_t)a.B * a.Hq * a.Nq;
+    return launch_clusters(cross_stats_kernel<T>, (unsigned)((rows + 15) / 16), 1, 256, 0, a.stream, a.Hq, a.Nq, rows,
+                           rows_of<const T>(a.O), rows_of<const T>(a.dO), static_cast<const float *>(a.LSE), a.stats);
+}
+
 }  // namespace
 
-cudaError_t launch_cross_fwd_simt(const CrossArgs &a) {
-    return a.dtype == FIBATT_F32 ? fwd<float>(a) : fwd<__nv_bfloat16>(a);
+cudaError_t launch_cross_stats(const CrossArgs &a) {
+    return a.dtype == FIBATT_F32 ? stats<float>(a) : stats<__nv_bfloat16>(a);
 }
 
-cudaError_t launch_cross_bwd_simt(const CrossArgs &a) {
-    return a.dtype == FIBATT_F32 ? bwd<float>(a) : bwd<__nv_bfloat16>(a);
-}
+cudaError_t launch_cross_fwd_simt(const CrossArgs &a) { return fwd<float>(a); }
+
+cudaError_t launch_cross_bwd_simt(const CrossArgs &a) { return bwd<float>(a); }
 
 FIBATT_DEFINE_ERROR_READER(read_error_cross_simt, "cross_simt.cu")
 
