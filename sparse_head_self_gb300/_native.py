@@ -9,6 +9,7 @@ from __future__ import annotations
 import ctypes
 import os
 import re
+import struct
 import threading
 
 from .build import LIB, LIB_CHECKS, ROOT
@@ -54,35 +55,21 @@ _SIGS = {
 }
 
 
-class Heads(ctypes.Structure):
-    """fibatt_heads: a head tensor by pointer and strides (elements)."""
-    _fields_ = [("ptr", _vp), ("stride_b", ctypes.c_int64), ("stride_h", ctypes.c_int64), ("stride_n", ctypes.c_int64)]
+# The structures of the calls below, packed as C lays them out: a bytes object
+# per call costs less than a ctypes structure.
+HEADS = struct.Struct("@Pqqq")                       # fibatt_heads: ptr, stride_b, stride_h, stride_n
+CROSS = struct.Struct("@7ifPPq")                     # fibatt_cross
+QK_NORM = struct.Struct("@7iPPfiiPPiPq")             # fibatt_qk_norm
 
-
-class Cross(ctypes.Structure):
-    """fibatt_cross: the sizes and key sets of a cross attention."""
-    _fields_ = [(n, ctypes.c_int) for n in ("B", "Hq", "Hkv", "Nq", "Nk", "D", "dtype")] + [
-        ("scale", ctypes.c_float), ("kv_len", _vp), ("key_mask", _vp), ("key_mask_stride_b", ctypes.c_int64)]
-
-
-class QkNorm(ctypes.Structure):
-    """fibatt_qk_norm: the sizes, weights and angles of a query/key norm."""
-    _fields_ = [(n, ctypes.c_int) for n in ("B", "N", "Hq", "Hk", "Hv", "D", "dtype")] + [
-        ("q_weight", _vp), ("k_weight", _vp), ("eps", ctypes.c_float), ("rot_dims", ctypes.c_int),
-        ("interleaved", ctypes.c_int), ("cos", _vp), ("sin", _vp), ("table_len", ctypes.c_int),
-        ("positions", _vp), ("positions_stride_b", ctypes.c_int64)]
-
-
-_headsp, _i64 = ctypes.POINTER(Heads), ctypes.c_int64
+_i64 = ctypes.c_int64
 _SIGS.update({
-    "fibatt_qk_norm_fwd": (ctypes.c_int, [ctypes.POINTER(QkNorm), _vp, _i64, _i64, _vp, _vp, _vp, _vp]),
+    "fibatt_qk_norm_fwd": (ctypes.c_int, [_vp, _vp, _i64, _i64, _vp, _vp, _vp, _vp]),
     "fibatt_qk_norm_bwd_workspace_bytes": (ctypes.c_size_t, []),
-    "fibatt_qk_norm_bwd": (ctypes.c_int, [ctypes.POINTER(QkNorm), _vp, _i64, _i64, _vp, _vp, _vp, _vp, _i64, _i64,
-                                          _vp, _vp, _vp, ctypes.c_size_t, _vp]),
-    "fibatt_cross_fwd": (ctypes.c_int, [ctypes.POINTER(Cross), _headsp, _headsp, _headsp, _headsp, _vp, _vp]),
-    "fibatt_cross_bwd_workspace_bytes": (ctypes.c_size_t, [ctypes.POINTER(Cross)]),
-    "fibatt_cross_bwd": (ctypes.c_int, [ctypes.POINTER(Cross)] + [_headsp] * 4 + [_vp] + [_headsp] * 4
-                         + [_vp, ctypes.c_size_t, _vp]),
+    "fibatt_qk_norm_bwd": (ctypes.c_int, [_vp, _vp, _i64, _i64, _vp, _vp, _vp, _vp, _i64, _i64, _vp, _vp, _vp,
+                                          ctypes.c_size_t, _vp]),
+    "fibatt_cross_fwd": (ctypes.c_int, [_vp] * 7),
+    "fibatt_cross_bwd_workspace_bytes": (ctypes.c_size_t, [_vp]),
+    "fibatt_cross_bwd": (ctypes.c_int, [_vp] * 11 + [ctypes.c_size_t, _vp]),
 })
 
 
@@ -104,6 +91,8 @@ def header_functions() -> list[str]:
 def lib():
     """The loaded libfibatt (raises if it has not been built)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib

@@ -6,7 +6,6 @@ calls on CPU tensors are rejected.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 
 import torch
@@ -268,25 +267,45 @@ def fibottention(Q, K, V, support: Support, scale: float | None = None):
 
 # ---------------------------------------------------- query and key norms
 
-def _check_tensor(name: str, t, dtype, device) -> None:
+def _check_tensor(name: str, t, dtype, index: int) -> None:
+    """A CUDA tensor of this type on device `index`."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.device.type != "cuda":
+    if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor (libfibatt has no CPU path)")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if t.get_device() != index:
+        raise ValueError(f"{name} is on {t.device}, expected cuda:{index}")
     if t.dtype != dtype:
         raise ValueError(f"{name} has dtype {t.dtype}, expected {dtype}")
 
 
-def _on(stream, device):
-    """The launching stream current, with its device: what a call allocates
-    then belongs to the stream that uses it."""
+def _check_dense(name: str, t, shape, dtype, index: int) -> None:
+    _check_tensor(name, t, dtype, index)
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+
+
+def _index(name: str, t) -> int:
+    """The device index of a CUDA tensor."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor (libfibatt has no CPU path)")
+    return t.get_device()
+
+
+def _launch(index: int, stream, call):
+    """call(stream pointer) with the launching stream and its device current:
+    what a call allocates then belongs to the stream that uses it."""
     if stream is not None:
-        return torch.cuda.stream(stream)
-    if device.index != torch.cuda.current_device():
-        return torch.cuda.device(device)
-    return contextlib.nullcontext()
+        with torch.cuda.stream(stream):
+            return call(stream.cuda_stream)
+    if index != torch.cuda.current_device():
+        with torch.cuda.device(index):
+            return call(torch._C._cuda_getCurrentRawStream(index))
+    return call(torch._C._cuda_getCurrentRawStream(index))
 
 
 def rotary_tables(angles: torch.Tensor):
@@ -317,41 +336,47 @@ def rotary_angles_2d(height: int, width: int, rot_dims: int = HEAD_DIM, theta: f
 
 
 def _norm_desc(x, heads, q_weight, k_weight, eps, rotary, positions, interleaved):
+    """(packed fibatt_qk_norm, device index, B, N, Hq, Hk, Hv)."""
     if not isinstance(x, torch.Tensor) or x.dim() != 3:
-        raise ValueError("x must be [B, N, (Hq + Hk + Hv) * 64]")
-    if x.dtype not in _DTYPES:
-        raise ValueError(f"dtype {x.dtype} unsupported (float32 or bfloat16)")
-    dev = x.device
-    _check_tensor("x", x, x.dtype, dev)
-    Hq, Hk, Hv = (int(h) for h in heads)
+        raise ValueError("x must be a [B, N, (Hq + Hk + Hv) * 64] tensor")
+    dtype = x.dtype
+    code = _DTYPES.get(dtype)
+    if code is None:
+        raise ValueError(f"dtype {dtype} unsupported (float32 or bfloat16)")
+    index = _index("x", x)
+    Hq, Hk, Hv = heads
     B, N, C = x.shape
     if min(Hq, Hk, Hv) < 0 or C != (Hq + Hk + Hv) * HEAD_DIM:
         raise ValueError(f"x has {C} values a token, heads {(Hq, Hk, Hv)} of {HEAD_DIM} need {(Hq + Hk + Hv) * HEAD_DIM}")
     if x.stride(2) != 1:
         raise ValueError("x must have contiguous tokens")
-    d = _native.QkNorm(B=B, N=N, Hq=Hq, Hk=Hk, Hv=Hv, D=HEAD_DIM, dtype=_DTYPES[x.dtype], eps=float(eps),
-                       interleaved=int(bool(interleaved)))
-    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
-        if w is not None:
-            _check_io(name, w, (HEAD_DIM,), x.dtype, dev)
-            setattr(d, name, w.data_ptr())
+    wq = wk = cos_ptr = sin_ptr = rot = table = pos = pos_sb = 0
+    if q_weight is not None:
+        _check_dense("q_weight", q_weight, (HEAD_DIM,), dtype, index)
+        wq = q_weight.data_ptr()
+    if k_weight is not None:
+        _check_dense("k_weight", k_weight, (HEAD_DIM,), dtype, index)
+        wk = k_weight.data_ptr()
     if rotary is not None:
         cos, sin = rotary
-        _check_io("cos", cos, cos.shape, torch.float32, dev)
-        _check_io("sin", sin, cos.shape, torch.float32, dev)
+        _check_dense("cos", cos, cos.shape, torch.float32, index)
+        _check_dense("sin", sin, cos.shape, torch.float32, index)
         if cos.dim() != 2:
             raise ValueError("cos and sin must be [positions, rot_dims / 2]")
-        d.rot_dims, d.table_len = 2 * cos.shape[1], cos.shape[0]
-        d.cos, d.sin = cos.data_ptr(), sin.data_ptr()
+        table, rot = cos.shape
+        rot *= 2
+        cos_ptr, sin_ptr = cos.data_ptr(), sin.data_ptr()
         if positions is not None:
-            _check_tensor("positions", positions, torch.int32, dev)
-            if tuple(positions.shape) not in ((N,), (B, N)) or (N > 1 and positions.stride(-1) != 1):
+            _check_tensor("positions", positions, torch.int32, index)
+            if positions.shape not in ((N,), (B, N)) or (N > 1 and positions.stride(-1) != 1):
                 raise ValueError(f"positions must be [N] or [B, N] with contiguous rows, got {tuple(positions.shape)}")
-            d.positions = positions.data_ptr()
-            d.positions_stride_b = positions.stride(0) if positions.dim() == 2 else 0
+            pos = positions.data_ptr()
+            pos_sb = positions.stride(0) if positions.dim() == 2 else 0
     elif positions is not None:
         raise ValueError("positions without rotary tables")
-    return d, (B, N, Hq, Hk, Hv)
+    d = _native.QK_NORM.pack(B, N, Hq, Hk, Hv, HEAD_DIM, code, wq, wk, eps, rot, 1 if interleaved else 0, cos_ptr,
+                             sin_ptr, table, pos, pos_sb)
+    return d, index, B, N, Hq, Hk, Hv
 
 
 def qk_norm_fwd(x: torch.Tensor, heads, q_weight=None, k_weight=None, eps: float = 1e-6, rotary=None, positions=None,
@@ -360,13 +385,19 @@ def qk_norm_fwd(x: torch.Tensor, heads, q_weight=None, k_weight=None, eps: float
     with heads = (Hq, Hk, Hv); returns (Q, K, V), [B, H, N, 64] each, None for
     a kind without heads.  rotary = (cos, sin), [positions, rot_dims / 2] fp32;
     positions int32 [N] or [B, N]."""
-    d, (B, N, Hq, Hk, Hv) = _norm_desc(x, heads, q_weight, k_weight, eps, rotary, positions, interleaved)
-    with _on(stream, x.device):
-        out = [torch.empty((B, h, N, HEAD_DIM), dtype=x.dtype, device=x.device) if h else None for h in (Hq, Hk, Hv)]
-        check(lib().fibatt_qk_norm_fwd(ctypes.byref(d), x.data_ptr(), x.stride(0), x.stride(1),
-                                       *(None if t is None else t.data_ptr() for t in out),
-                                       _stream_ptr(stream, x.device)))
-    return tuple(out)
+    d, index, B, N, Hq, Hk, Hv = _norm_desc(x, heads, q_weight, k_weight, eps, rotary, positions, interleaved)
+
+    def call(s):
+        new = x.new_empty
+        q = new((B, Hq, N, HEAD_DIM)) if Hq else None
+        k = new((B, Hk, N, HEAD_DIM)) if Hk else None
+        v = new((B, Hv, N, HEAD_DIM)) if Hv else None
+        sb, sn, _ = x.stride()
+        check(lib().fibatt_qk_norm_fwd(d, x.data_ptr(), sb, sn, q.data_ptr() if Hq else None,
+                                       k.data_ptr() if Hk else None, v.data_ptr() if Hv else None, s))
+        return q, k, v
+
+    return _launch(index, stream, call)
 
 
 def qk_norm_bwd(x: torch.Tensor, heads, q_weight, k_weight, dQ, dK, dV, eps: float = 1e-6, rotary=None,
@@ -374,23 +405,27 @@ def qk_norm_bwd(x: torch.Tensor, heads, q_weight, k_weight, dQ, dK, dV, eps: flo
     """fibatt_qk_norm_bwd: from the gradients of qk_norm_fwd's results (None
     for a kind without heads) to (dx, dq_weight, dk_weight); a weight that is
     None has the gradient None."""
-    d, (B, N, Hq, Hk, Hv) = _norm_desc(x, heads, q_weight, k_weight, eps, rotary, positions, interleaved)
+    d, index, B, N, Hq, Hk, Hv = _norm_desc(x, heads, q_weight, k_weight, eps, rotary, positions, interleaved)
     grads = []
     for name, g, h in (("dQ", dQ, Hq), ("dK", dK, Hk), ("dV", dV, Hv)):
         if h:
-            _check_io(name, g, (B, h, N, HEAD_DIM), x.dtype, x.device)
+            _check_dense(name, g, (B, h, N, HEAD_DIM), x.dtype, index)
         grads.append(g.data_ptr() if h else None)
-    with _on(stream, x.device):
-        dx = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+
+    def call(s):
+        dx = x.new_empty(x.shape)
         dqw = None if q_weight is None else torch.empty_like(q_weight)
         dkw = None if k_weight is None else torch.empty_like(k_weight)
-        if workspace is None:
-            workspace = torch.empty(int(lib().fibatt_qk_norm_bwd_workspace_bytes()), dtype=torch.uint8, device=x.device)
-        check(lib().fibatt_qk_norm_bwd(ctypes.byref(d), x.data_ptr(), x.stride(0), x.stride(1), *grads, dx.data_ptr(),
-                                       dx.stride(0), dx.stride(1), None if dqw is None else dqw.data_ptr(),
-                                       None if dkw is None else dkw.data_ptr(), workspace.data_ptr(),
-                                       workspace.numel() * workspace.element_size(), _stream_ptr(stream, x.device)))
-    return dx, dqw, dkw
+        ws = workspace
+        if ws is None:
+            ws = x.new_empty(lib().fibatt_qk_norm_bwd_workspace_bytes(), dtype=torch.uint8)
+        sb, sn, _ = x.stride()
+        check(lib().fibatt_qk_norm_bwd(d, x.data_ptr(), sb, sn, *grads, dx.data_ptr(), dx.stride(0), dx.stride(1),
+                                       None if dqw is None else dqw.data_ptr(), None if dkw is None else dkw.data_ptr(),
+                                       ws.data_ptr(), ws.numel() * ws.element_size(), s))
+        return dx, dqw, dkw
+
+    return _launch(index, stream, call)
 
 
 class QkNormFunction(torch.autograd.Function):
@@ -426,41 +461,46 @@ def qk_norm(x, heads, q_weight=None, k_weight=None, eps: float = 1e-6, rotary=No
 
 # --------------------------------------------------------- cross attention
 
-def _heads_arg(name: str, t, shape, dtype, device):
-    _check_tensor(name, t, dtype, device)
-    if tuple(t.shape) != tuple(shape):
+def _heads_arg(name: str, t, shape, dtype, index: int) -> bytes:
+    """t as a packed fibatt_heads."""
+    _check_tensor(name, t, dtype, index)
+    if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if t.stride(3) != 1:
+    sb, sh, sn, sd = t.stride()
+    if sd != 1:
         raise ValueError(f"{name} must have contiguous rows")
     # a dim of one element has no stride that matters
-    s = [st if n > 1 else 0 for st, n in zip(t.stride(), t.shape)]
-    return ctypes.byref(_native.Heads(t.data_ptr(), s[0], s[1], s[2]))
+    return _native.HEADS.pack(t.data_ptr(), sb if shape[0] > 1 else 0, sh if shape[1] > 1 else 0,
+                              sn if shape[2] > 1 else 0)
 
 
 def _cross_desc(Q, K, V, scale, kv_len, key_mask):
+    """(packed fibatt_cross, Q, K, V as packed fibatt_heads, device index)."""
     for name, t in (("Q", Q), ("K", K), ("V", V)):
         if not isinstance(t, torch.Tensor) or t.dim() != 4:
             raise ValueError(f"{name} must be a [B, H, N, D] tensor")
-    if Q.dtype not in _DTYPES:
-        raise ValueError(f"dtype {Q.dtype} unsupported (float32 or bfloat16)")
-    B, Hq, Nq, D = Q.shape
-    Hkv, Nk = K.shape[1], K.shape[2]
-    d = _native.Cross(B=B, Hq=Hq, Hkv=Hkv, Nq=Nq, Nk=Nk, D=D, dtype=_DTYPES[Q.dtype], scale=float(scale))
-    dev = Q.device
+    dtype = Q.dtype
+    code = _DTYPES.get(dtype)
+    if code is None:
+        raise ValueError(f"dtype {dtype} unsupported (float32 or bfloat16)")
+    index = _index("Q", Q)
+    B, Hq, Nq, D = shape = Q.shape
+    _, Hkv, Nk, _ = K.shape
+    lens = mask = mask_sb = 0
     if kv_len is not None:
-        _check_io("kv_len", kv_len, (B,), torch.int32, dev)
-        d.kv_len = kv_len.data_ptr()
+        _check_dense("kv_len", kv_len, (B,), torch.int32, index)
+        lens = kv_len.data_ptr()
     if key_mask is not None:
         if not isinstance(key_mask, torch.Tensor) or key_mask.dtype not in (torch.bool, torch.uint8):
             raise ValueError("key_mask must be a bool or uint8 tensor")
-        _check_tensor("key_mask", key_mask, key_mask.dtype, dev)
-        if tuple(key_mask.shape) != (B, Nk) or (Nk > 1 and key_mask.stride(1) != 1):
+        _check_tensor("key_mask", key_mask, key_mask.dtype, index)
+        if key_mask.shape != (B, Nk) or (Nk > 1 and key_mask.stride(1) != 1):
             raise ValueError(f"key_mask must be [B, Nk] = {(B, Nk)} with contiguous rows, got {tuple(key_mask.shape)}")
-        d.key_mask, d.key_mask_stride_b = key_mask.data_ptr(), key_mask.stride(0)
-    q = _heads_arg("Q", Q, (B, Hq, Nq, D), Q.dtype, dev)
-    k = _heads_arg("K", K, (B, Hkv, Nk, D), Q.dtype, dev)
-    v = _heads_arg("V", V, (B, Hkv, Nk, D), Q.dtype, dev)
-    return d, q, k, v
+        mask, mask_sb = key_mask.data_ptr(), key_mask.stride(0)
+    kv_shape = (B, Hkv, Nk, D)
+    return (_native.CROSS.pack(B, Hq, Hkv, Nq, Nk, D, code, scale, lens, mask, mask_sb),
+            _heads_arg("Q", Q, shape, dtype, index), _heads_arg("K", K, kv_shape, dtype, index),
+            _heads_arg("V", V, kv_shape, dtype, index), index)
 
 
 def cross_fwd(Q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, scale: float, kv_len: torch.Tensor | None = None,
@@ -470,40 +510,45 @@ def cross_fwd(Q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, scale: float, k
     [B, Hkv, Nk, 64] (Hkv divides Hq; any strides whose rows are contiguous);
     returns (O, LSE), O in Q's layout.  kv_len: int32 [B], the keys each
     sequence has; key_mask: bool [B, Nk], the keys it attends."""
-    d, q, k, v = _cross_desc(Q, K, V, scale, kv_len, key_mask)
-    dev = Q.device
-    with _on(stream, dev):
-        if O is None:
-            O = torch.empty_like(Q)
+    d, q, k, v, index = _cross_desc(Q, K, V, scale, kv_len, key_mask)
+
+    def call(s):
+        o = torch.empty_like(Q) if O is None else O
+        shape = Q.shape
         if LSE is None:
-            LSE = torch.empty(Q.shape[:3], dtype=torch.float32, device=dev)
-        _check_io("LSE", LSE, Q.shape[:3], torch.float32, dev)
-        check(lib().fibatt_cross_fwd(ctypes.byref(d), q, k, v, _heads_arg("O", O, Q.shape, Q.dtype, dev),
-                                     LSE.data_ptr(), _stream_ptr(stream, dev)))
-    return O, LSE
+            lse = Q.new_empty(shape[:3], dtype=torch.float32)
+        else:
+            lse = LSE
+            _check_dense("LSE", lse, shape[:3], torch.float32, index)
+        check(lib().fibatt_cross_fwd(d, q, k, v, _heads_arg("O", o, shape, Q.dtype, index), lse.data_ptr(), s))
+        return o, lse
+
+    return _launch(index, stream, call)
 
 
 def cross_bwd(Q, K, V, O, LSE, dO, scale: float, kv_len=None, key_mask=None, dQ=None, dK=None, dV=None,
               workspace: torch.Tensor | None = None, stream=None):
     """fibatt_cross_bwd: (dQ, dK, dV) from cross_fwd's O and LSE and the
     gradient dO of O; each gradient in its input's layout unless given."""
-    d, q, k, v = _cross_desc(Q, K, V, scale, kv_len, key_mask)
-    dev = Q.device
-    _check_io("LSE", LSE, Q.shape[:3], torch.float32, dev)
-    o, do = _heads_arg("O", O, Q.shape, Q.dtype, dev), _heads_arg("dO", dO, Q.shape, Q.dtype, dev)
-    with _on(stream, dev):
-        dQ = torch.empty_like(Q) if dQ is None else dQ
-        dK = torch.empty_like(K) if dK is None else dK
-        dV = torch.empty_like(V) if dV is None else dV
-        need = int(lib().fibatt_cross_bwd_workspace_bytes(ctypes.byref(d)))
-        if workspace is None:
-            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-        check(lib().fibatt_cross_bwd(ctypes.byref(d), q, k, v, o, LSE.data_ptr(), do,
-                                     _heads_arg("dQ", dQ, Q.shape, Q.dtype, dev),
-                                     _heads_arg("dK", dK, K.shape, Q.dtype, dev),
-                                     _heads_arg("dV", dV, V.shape, Q.dtype, dev), workspace.data_ptr(),
-                                     workspace.numel() * workspace.element_size(), _stream_ptr(stream, dev)))
-    return dQ, dK, dV
+    d, q, k, v, index = _cross_desc(Q, K, V, scale, kv_len, key_mask)
+    shape, dtype = Q.shape, Q.dtype
+    _check_dense("LSE", LSE, shape[:3], torch.float32, index)
+    o, do = _heads_arg("O", O, shape, dtype, index), _heads_arg("dO", dO, shape, dtype, index)
+
+    def call(s):
+        dq = torch.empty_like(Q) if dQ is None else dQ
+        dk = torch.empty_like(K) if dK is None else dK
+        dv = torch.empty_like(V) if dV is None else dV
+        ws = workspace
+        if ws is None:
+            ws = Q.new_empty(lib().fibatt_cross_bwd_workspace_bytes(d), dtype=torch.uint8)
+        check(lib().fibatt_cross_bwd(d, q, k, v, o, LSE.data_ptr(), do, _heads_arg("dQ", dq, shape, dtype, index),
+                                     _heads_arg("dK", dk, K.shape, dtype, index),
+                                     _heads_arg("dV", dv, K.shape, dtype, index), ws.data_ptr(),
+                                     ws.numel() * ws.element_size(), s))
+        return dq, dk, dv
+
+    return _launch(index, stream, call)
 
 
 def _readable(t):

@@ -3,6 +3,7 @@
 // operations and every argument rule are documented in include/fibatt.h.
 #pragma once
 
+#include <atomic>
 #include <cstdint>
 
 #include <cuda_runtime.h>
@@ -81,15 +82,23 @@ cudaError_t launch_clusters(void (*kern)(KArgs...), unsigned grid, unsigned c, u
     return e;
 }
 
-// A kernel that shares its registers out anew (setmaxnreg) is written for the
-// number it is launched with; shares that do not add up would wait for ever.
-template <typename K>
-cudaError_t prepare_kernel(K kern, size_t smem, int regs) {
-    cudaFuncAttributes at;
-    cudaError_t e = cudaFuncGetAttributes(&at, kern);
+// Before the first launch of kernel K on a device: its shared memory, and a
+// check of its registers (0: none).  A kernel that shares its registers out
+// anew (setmaxnreg) is written for the number it is launched with; shares that
+// do not add up would wait for ever.
+template <auto K>
+cudaError_t prepare_kernel(size_t smem, int regs) {
+    static std::atomic<bool> done[64];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
-    if (at.numRegs != regs) return cudaErrorInvalidKernelImage;
-    return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (dev < 64 && done[dev].load(std::memory_order_acquire)) return cudaSuccess;
+    cudaFuncAttributes at;
+    if ((e = cudaFuncGetAttributes(&at, K)) != cudaSuccess) return e;
+    if (regs && at.numRegs != regs) return cudaErrorInvalidKernelImage;
+    e = cudaFuncSetAttribute(K, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e == cudaSuccess && dev < 64) done[dev].store(true, std::memory_order_release);
+    return e;
 }
 
 // ---- launchers (return the CUDA launch status) -----------------------------

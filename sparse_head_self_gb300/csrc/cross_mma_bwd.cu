@@ -420,7 +420,7 @@ cudaError_t launch_cross_bwd_mma(const CrossArgs &a) {
     f.Hq = a.Hq, f.Hkv = a.Hkv;
     f.ktiles = (a.Nk + kTileRows - 1) / kTileRows;
     f.scale = a.scale;
-    e = prepare_kernel(cross_bwd_mma_kernel, kSmem, kRegs);
+    e = prepare_kernel<cross_bwd_mma_kernel>(kSmem, kRegs);
     if (e != cudaSuccess) return e;
     const int64_t key_units = (int64_t)a.B * a.Hkv * f.ktiles, units = key_units + (int64_t)a.B * a.Hkv * f.qt.tiles;
     f.key_blocks = (int)key_units;

@@ -397,14 +397,13 @@ cudaError_t fwd(const CrossArgs &a, const QueryTiles &qt) {
     // and -inf of a masked key times c is still -inf
     f.c = std::max(std::fabs(a.scale) * kLog2e, 1e-36f);
     f.negative = a.scale < 0.f;
-    const auto kern = cross_fwd_mma_kernel<NT>;
-    const cudaError_t e = prepare_kernel(kern, C::kSmem, C::kRegs);
+    const cudaError_t e = prepare_kernel<cross_fwd_mma_kernel<NT>>(C::kSmem, C::kRegs);
     if (e != cudaSuccess) return e;
     const int64_t units = (int64_t)a.B * a.Hkv * f.pairs;
     const int tiles = (a.Nk + kTileRows - 1) / kTileRows;
     int c = 1;
     while (c < 8 && units * c * 2 <= (int64_t)C::kMinBlocks * sm_count() && tiles >= 2 * c) c *= 2;
-    return launch_clusters(kern, (unsigned)(units * c), c, C::kThreads, C::kSmem, a.stream, f);
+    return launch_clusters(cross_fwd_mma_kernel<NT>, (unsigned)(units * c), c, C::kThreads, C::kSmem, a.stream, f);
 }
 
 }  // namespace

@@ -431,7 +431,7 @@ template <typename T>
 cudaError_t fwd(const CrossArgs &a) {
     constexpr size_t smem = 4 * kTile * sizeof(float);
     const auto kern = cross_fwd_simt_kernel<T>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    const cudaError_t e = prepare_kernel<cross_fwd_simt_kernel<T>>(smem, 0);
     if (e != cudaSuccess) return e;
     const int qtiles = (a.Nq + kT - 1) / kT;
     const int64_t units = (int64_t)a.B * a.Hq * qtiles;
@@ -446,8 +446,8 @@ cudaError_t bwd(const CrossArgs &a) {
     constexpr size_t smem = 5 * kTile * sizeof(float);
     const auto qkern = cross_dq_simt_kernel<T>;
     const auto kkern = cross_dkv_simt_kernel<T>;
-    cudaError_t e = cudaFuncSetAttribute(qkern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e == cudaSuccess) e = cudaFuncSetAttribute(kkern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    cudaError_t e = prepare_kernel<cross_dq_simt_kernel<T>>(smem, 0);
+    if (e == cudaSuccess) e = prepare_kernel<cross_dkv_simt_kernel<T>>(smem, 0);
     if (e != cudaSuccess) return e;
     const auto Q = rows_of<const T>(a.Q), K = rows_of<const T>(a.K), V = rows_of<const T>(a.V),
                dO = rows_of<const T>(a.dO);

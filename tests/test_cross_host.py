@@ -1,7 +1,6 @@
 """Host-side tests of the query/key norm and the cross attention (no GPU
 needed): every refusal of the two C calls and of their Python entry points,
 each before anything is launched, and the rotary angle helpers."""
-import ctypes
 import math
 
 import pytest
@@ -21,18 +20,23 @@ def _built():
 
 
 def _heads(ptr=P, b=64 * 9 * 2, h=64 * 9, n=64):
-    return _native.Heads(ptr, b, h, n)
+    return _native.HEADS.pack(ptr or 0, b, h, n)
+
+
+def _cross_desc(**kw):
+    d = {**dict(B=2, Hq=4, Hkv=2, Nq=9, Nk=9, D=64, dtype=1, scale=0.125, kv_len=0, key_mask=0, key_mask_stride_b=0), **kw}
+    return _native.CROSS.pack(*d.values())
 
 
 def _cross(bwd=False, q=None, k=None, v=None, o=None, lse=P, do=None, dq=None, dk=None, dv=None, ws=P, ws_bytes=1 << 20,
            **kw):
     L = _native.lib()
-    d = _native.Cross(**{**dict(B=2, Hq=4, Hkv=2, Nq=9, Nk=9, D=64, dtype=1, scale=0.125), **kw})
-    r = [ctypes.byref(x or _heads()) for x in (q, k, v, o)]
+    d = _cross_desc(**kw)
+    r = [x or _heads() for x in (q, k, v, o)]
     if not bwd:
-        return L.fibatt_cross_fwd(ctypes.byref(d), *r, lse, None)
-    g = [ctypes.byref(x or _heads()) for x in (do, dq, dk, dv)]
-    return L.fibatt_cross_bwd(ctypes.byref(d), *r, lse, *g, ws, ws_bytes, None)
+        return L.fibatt_cross_fwd(d, *r, lse, None)
+    g = [x or _heads() for x in (do, dq, dk, dv)]
+    return L.fibatt_cross_bwd(d, *r, lse, *g, ws, ws_bytes, None)
 
 
 @pytest.fixture
@@ -86,21 +90,20 @@ def test_cross_refusals(bwd, _no_launch):
 
 def test_cross_workspace_size():
     L = _native.lib()
-    d = _native.Cross(B=2, Hq=4, Hkv=2, Nq=9, Nk=9, D=64, dtype=1, scale=1.0)
-    assert L.fibatt_cross_bwd_workspace_bytes(ctypes.byref(d)) >= 2 * 4 * 9 * 8
-    d.B = 0
-    assert L.fibatt_cross_bwd_workspace_bytes(ctypes.byref(d)) == 0
+    assert L.fibatt_cross_bwd_workspace_bytes(_cross_desc()) >= 2 * 4 * 9 * 8
+    assert L.fibatt_cross_bwd_workspace_bytes(_cross_desc(B=0)) == 0
     assert L.fibatt_cross_bwd_workspace_bytes(None) == 0
 
 
 def _norm(bwd=False, x=P, sb=9 * 8 * 64, sn=8 * 64, q=P, k=P, v=P, dx=P, dsb=9 * 8 * 64, dsn=8 * 64, ws=P, ws_bytes=1 << 20,
           dw=P, **kw):
     L = _native.lib()
-    d = _native.QkNorm(**{**dict(B=2, N=9, Hq=4, Hk=2, Hv=2, D=64, dtype=1, q_weight=P, k_weight=P, eps=1e-6,
-                                 rot_dims=64, cos=P, sin=P, table_len=9), **kw})
+    d = {**dict(B=2, N=9, Hq=4, Hk=2, Hv=2, D=64, dtype=1, q_weight=P, k_weight=P, eps=1e-6, rot_dims=64, interleaved=0,
+                cos=P, sin=P, table_len=9, positions=0, positions_stride_b=0), **kw}
+    d = _native.QK_NORM.pack(*(0 if f is None else f for f in d.values()))
     if not bwd:
-        return L.fibatt_qk_norm_fwd(ctypes.byref(d), x, sb, sn, q, k, v, None)
-    return L.fibatt_qk_norm_bwd(ctypes.byref(d), x, sb, sn, q, k, v, dx, dsb, dsn, dw, dw, ws, ws_bytes, None)
+        return L.fibatt_qk_norm_fwd(d, x, sb, sn, q, k, v, None)
+    return L.fibatt_qk_norm_bwd(d, x, sb, sn, q, k, v, dx, dsb, dsn, dw, dw, ws, ws_bytes, None)
 
 
 @pytest.mark.parametrize("bwd", [False, True])
@@ -152,6 +155,40 @@ def test_python_entry_points_reject_what_they_cannot_take():
         api.qk_norm_fwd(x.double(), (2, 2, 2))
     with pytest.raises(ValueError, match="B, N"):
         api.qk_norm_fwd(x[0], (2, 2, 2))
+
+
+def test_packed_structures_are_as_c_lays_them_out(tmp_path):
+    # sizes and field offsets of the header's structures against the packed formats'
+    import os
+    import subprocess
+
+    fields = {
+        "fibatt_heads": (_native.HEADS, ["ptr", "stride_b", "stride_h", "stride_n"]),
+        "fibatt_cross": (_native.CROSS, ["B", "Hq", "Hkv", "Nq", "Nk", "D", "dtype", "scale", "kv_len", "key_mask",
+                                         "key_mask_stride_b"]),
+        "fibatt_qk_norm": (_native.QK_NORM, ["B", "N", "Hq", "Hk", "Hv", "D", "dtype", "q_weight", "k_weight", "eps",
+                                             "rot_dims", "interleaved", "cos", "sin", "table_len", "positions",
+                                             "positions_stride_b"]),
+    }
+    lines = []
+    for name, (_, names) in fields.items():
+        lines.append(f'printf("%zu\\n", sizeof({name}));')
+        lines += [f'printf("%zu\\n", offsetof({name}, {f}));' for f in names]
+    src = tmp_path / "layout.c"
+    src.write_text('#include <stddef.h>\n#include <stdint.h>\n#include <stdio.h>\n#include "fibatt.h"\n'
+                   "int main(void) { " + " ".join(lines) + " return 0; }\n")
+    cuda = os.path.join(os.environ.get("CUDA_HOME", "/usr/local/cuda"), "include")
+    subprocess.run(["gcc", "-I", os.path.dirname(_native.HEADER), "-I", cuda, "-o", str(tmp_path / "layout"), str(src)], check=True)
+    got = [int(x) for x in subprocess.run([str(tmp_path / "layout")], capture_output=True, text=True, check=True).stdout.split()]
+    for name, (fmt, names) in fields.items():
+        size, offsets, got = got[0], got[1:1 + len(names)], got[1 + len(names):]
+        assert fmt.size == size, name
+        for i in range(len(names)):
+            # a value in field i alone: its first byte stands at the field's offset
+            blob = fmt.pack(*(1.0 if names[k] in ("scale", "eps") and k == i else int(k == i) for k in range(len(names))))
+            at = next(p for p, x in enumerate(blob) if x)
+            want = offsets[i] + (2 if names[i] in ("scale", "eps") else 0)      # 1.0f is 00 00 80 3f
+            assert at == want, (name, names[i])
 
 
 def test_rotary_angles():
