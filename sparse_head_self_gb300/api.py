@@ -388,10 +388,10 @@ def qk_norm_fwd(x: torch.Tensor, heads, q_weight=None, k_weight=None, eps: float
     d, index, B, N, Hq, Hk, Hv = _norm_desc(x, heads, q_weight, k_weight, eps, rotary, positions, interleaved)
 
     def call(s):
-        new = x.new_empty
-        q = new((B, Hq, N, HEAD_DIM)) if Hq else None
-        k = new((B, Hk, N, HEAD_DIM)) if Hk else None
-        v = new((B, Hv, N, HEAD_DIM)) if Hv else None
+        how = {"dtype": x.dtype, "device": x.device}
+        q = torch.empty((B, Hq, N, HEAD_DIM), **how) if Hq else None
+        k = torch.empty((B, Hk, N, HEAD_DIM), **how) if Hk else None
+        v = torch.empty((B, Hv, N, HEAD_DIM), **how) if Hv else None
         sb, sn, _ = x.stride()
         check(lib().fibatt_qk_norm_fwd(d, x.data_ptr(), sb, sn, q.data_ptr() if Hq else None,
                                        k.data_ptr() if Hk else None, v.data_ptr() if Hv else None, s))
@@ -413,12 +413,12 @@ def qk_norm_bwd(x: torch.Tensor, heads, q_weight, k_weight, dQ, dK, dV, eps: flo
         grads.append(g.data_ptr() if h else None)
 
     def call(s):
-        dx = x.new_empty(x.shape)
+        dx = torch.empty(x.shape, dtype=x.dtype, device=x.device)
         dqw = None if q_weight is None else torch.empty_like(q_weight)
         dkw = None if k_weight is None else torch.empty_like(k_weight)
         ws = workspace
         if ws is None:
-            ws = x.new_empty(lib().fibatt_qk_norm_bwd_workspace_bytes(), dtype=torch.uint8)
+            ws = torch.empty(lib().fibatt_qk_norm_bwd_workspace_bytes(), dtype=torch.uint8, device=x.device)
         sb, sn, _ = x.stride()
         check(lib().fibatt_qk_norm_bwd(d, x.data_ptr(), sb, sn, *grads, dx.data_ptr(), dx.stride(0), dx.stride(1),
                                        None if dqw is None else dqw.data_ptr(), None if dkw is None else dkw.data_ptr(),
@@ -516,7 +516,7 @@ def cross_fwd(Q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, scale: float, k
         o = torch.empty_like(Q) if O is None else O
         shape = Q.shape
         if LSE is None:
-            lse = Q.new_empty(shape[:3], dtype=torch.float32)
+            lse = torch.empty(shape[:3], dtype=torch.float32, device=Q.device)
         else:
             lse = LSE
             _check_dense("LSE", lse, shape[:3], torch.float32, index)
@@ -541,7 +541,7 @@ def cross_bwd(Q, K, V, O, LSE, dO, scale: float, kv_len=None, key_mask=None, dQ=
         dv = torch.empty_like(V) if dV is None else dV
         ws = workspace
         if ws is None:
-            ws = Q.new_empty(lib().fibatt_cross_bwd_workspace_bytes(d), dtype=torch.uint8)
+            ws = torch.empty(lib().fibatt_cross_bwd_workspace_bytes(d), dtype=torch.uint8, device=Q.device)
         check(lib().fibatt_cross_bwd(d, q, k, v, o, LSE.data_ptr(), do, _heads_arg("dQ", dq, shape, dtype, index),
                                      _heads_arg("dK", dk, K.shape, dtype, index),
                                      _heads_arg("dV", dv, K.shape, dtype, index), ws.data_ptr(),

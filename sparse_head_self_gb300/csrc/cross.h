@@ -106,6 +106,8 @@ cudaError_t launch_cross_fwd_simt(const CrossArgs &a);
 cudaError_t launch_cross_bwd_simt(const CrossArgs &a);
 cudaError_t launch_cross_fwd_mma(const CrossArgs &a);   // bf16
 cudaError_t launch_cross_bwd_mma(const CrossArgs &a);   // bf16
+bool cross_rows_takes(const CrossArgs &a);               // few enough query rows for the next
+cudaError_t launch_cross_rows(const CrossArgs &a);
 cudaError_t launch_cross_stats(const CrossArgs &a);     // a.stats from a.O, a.dO and a.LSE
 
 struct QkNormArgs {
@@ -137,6 +139,7 @@ cudaError_t launch_qk_norm_bwd(const QkNormArgs &a);
 cudaError_t read_error_cross_simt(unsigned *code, bool clear);
 cudaError_t read_error_cross_mma_fwd(unsigned *code, bool clear);
 cudaError_t read_error_cross_mma_bwd(unsigned *code, bool clear);
+cudaError_t read_error_cross_rows(unsigned *code, bool clear);
 cudaError_t read_error_qk_norm(unsigned *code, bool clear);
 
 }  // namespace fibatt

@@ -208,7 +208,9 @@ fibatt_status fibatt_cross_fwd(const fibatt_cross *d, const fibatt_heads *Q, con
     if (fault("launch")) return set_error(FIBATT_ERR_CUDA, "injected launch failure (FIBATT_FAULT=launch)");
     CrossArgs a = cross_args(d, Q, K, V, O, stream);
     a.LSE = LSE;
-    const cudaError_t e = a.dtype == FIBATT_BF16 ? launch_cross_fwd_mma(a) : launch_cross_fwd_simt(a);
+    const cudaError_t e = cross_rows_takes(a)         ? launch_cross_rows(a)
+                          : a.dtype == FIBATT_BF16 ? launch_cross_fwd_mma(a)
+                                                   : launch_cross_fwd_simt(a);
     return e == cudaSuccess ? FIBATT_OK : cuda_error(e, "fibatt_cross_fwd launch");
 }
 
