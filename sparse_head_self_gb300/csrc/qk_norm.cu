@@ -10,13 +10,16 @@
 //   (dy1, dy2) = (dz1 cos a + dz2 sin a, -dz1 sin a + dz2 cos a),
 //   dw = sum over rows of dy n,  g = w dy,  dx = r (g - n <g, n> / 64).
 //
-// Both directions only move data: they read and write each element once.
-// Eight lanes share a head (eight dims each), a warp takes four heads of one
-// token per step and up to kSteps steps at once, so that a warp has up to
-// 2 KB (16-bit) or 4 KB of loads in flight; the token's angles are loaded once
-// for its heads.  Token rows of X are contiguous and every head row of Q, K
-// and V is a whole 128- or 256-byte segment, so all traffic is full sectors.
-// The values' heads are copied unconverted.
+// Both directions only move data: they read and write each element once, and
+// with 16-bit elements the instructions a head takes cost about as much as its
+// bytes.  Eight lanes share a head, a lane has two runs of four dims, chosen so
+// that both values of every rotated pair are its own (halves: dims 4 i.. and
+// rot / 2 + 4 i..), which leaves the two sums over a head as the only exchange;
+// the arithmetic is on packed pairs of floats.  A warp takes four heads of one
+// token per step, kSteps steps at once, and the next ones' loads are in flight
+// while these are worked on; a token's angles are loaded once for its heads.
+// Every head row is a whole 128- or 256-byte segment, so all traffic is full
+// sectors.  The values' heads are copied unconverted.
 //
 // dw: each lane keeps sums of its eight dims, the block joins its warps in
 // shared memory, and a second kernel adds the blocks' sums in block order:
@@ -25,54 +28,61 @@
 
 #include "cross.h"
 #include "device_common.cuh"
+#include "row_math.cuh"
 
 namespace fibatt {
 namespace {
 
 constexpr int kWarps = 8;
-constexpr int kSteps = 4;             // head groups of four that a warp loads at once
+constexpr int kSteps = 2;             // head groups of four that a warp loads at once
 constexpr int kMaxBlocks = 1024;      // rows of the dw partial sums
 constexpr unsigned kErrPosition = 8u; // a position at or behind the end of the tables
 
+// A lane's eight dims of a head: runs of four at a0 and a1 (elements).
 template <typename T>
-struct Eight;   // eight consecutive elements of a lane
+struct Eight;
 template <>
 struct Eight<__nv_bfloat16> {
-    uint4 w;
-    __device__ __forceinline__ void load(const __nv_bfloat16 *p) { w = __ldg(reinterpret_cast<const uint4 *>(p)); }
-    __device__ __forceinline__ void store(__nv_bfloat16 *p) const { *reinterpret_cast<uint4 *>(p) = w; }
-    __device__ __forceinline__ void zero() { w = make_uint4(0, 0, 0, 0); }
-    __device__ __forceinline__ void get(float (&x)[8]) const {
-        const uint32_t v[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            x[2 * i] = bf16_lo(v[i]);
-            x[2 * i + 1] = bf16_hi(v[i]);
-        }
+    uint2 u, v;
+    __device__ __forceinline__ void load(const __nv_bfloat16 *p, int a0, int a1) {
+        u = __ldg(reinterpret_cast<const uint2 *>(p + a0));
+        v = __ldg(reinterpret_cast<const uint2 *>(p + a1));
     }
-    __device__ __forceinline__ void put(const float (&x)[8]) {   // the only rounding of a result
-        w = make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
-                       pack_bf16x2(x[6], x[7]));
+    __device__ __forceinline__ void store(__nv_bfloat16 *p, int a0, int a1) const {
+        *reinterpret_cast<uint2 *>(p + a0) = u;
+        *reinterpret_cast<uint2 *>(p + a1) = v;
+    }
+    __device__ __forceinline__ void zero() { u = v = make_uint2(0, 0); }
+    __device__ __forceinline__ void get(float2 (&x)[4]) const {
+        x[0] = make_float2(bf16_lo(u.x), bf16_hi(u.x));
+        x[1] = make_float2(bf16_lo(u.y), bf16_hi(u.y));
+        x[2] = make_float2(bf16_lo(v.x), bf16_hi(v.x));
+        x[3] = make_float2(bf16_lo(v.y), bf16_hi(v.y));
+    }
+    __device__ __forceinline__ void put(const float2 (&x)[4]) {   // the only rounding of a result
+        u = make_uint2(pack_bf16x2(x[0].x, x[0].y), pack_bf16x2(x[1].x, x[1].y));
+        v = make_uint2(pack_bf16x2(x[2].x, x[2].y), pack_bf16x2(x[3].x, x[3].y));
     }
 };
 template <>
 struct Eight<float> {
     float4 a, b;
-    __device__ __forceinline__ void load(const float *p) {
-        a = __ldg(reinterpret_cast<const float4 *>(p));
-        b = __ldg(reinterpret_cast<const float4 *>(p) + 1);
+    __device__ __forceinline__ void load(const float *p, int a0, int a1) {
+        a = __ldg(reinterpret_cast<const float4 *>(p + a0));
+        b = __ldg(reinterpret_cast<const float4 *>(p + a1));
     }
-    __device__ __forceinline__ void store(float *p) const {
-        reinterpret_cast<float4 *>(p)[0] = a;
-        reinterpret_cast<float4 *>(p)[1] = b;
+    __device__ __forceinline__ void store(float *p, int a0, int a1) const {
+        *reinterpret_cast<float4 *>(p + a0) = a;
+        *reinterpret_cast<float4 *>(p + a1) = b;
     }
     __device__ __forceinline__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
-    __device__ __forceinline__ void get(float (&x)[8]) const {
-        x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+    __device__ __forceinline__ void get(float2 (&x)[4]) const {
+        x[0] = make_float2(a.x, a.y), x[1] = make_float2(a.z, a.w);
+        x[2] = make_float2(b.x, b.y), x[3] = make_float2(b.z, b.w);
     }
-    __device__ __forceinline__ void put(const float (&x)[8]) {
-        a = make_float4(x[0], x[1], x[2], x[3]);
-        b = make_float4(x[4], x[5], x[6], x[7]);
+    __device__ __forceinline__ void put(const float2 (&x)[4]) {
+        a = make_float4(x[0].x, x[0].y, x[1].x, x[1].y);
+        b = make_float4(x[2].x, x[2].y, x[3].x, x[3].y);
     }
 };
 
@@ -89,65 +99,57 @@ struct NormArgs {
     int64_t pos_sb;
 };
 
-// The angles of one token for a lane's eight dims.  Pairs of halves: dim d
-// and d + rot / 2, the partner's values come from lane `peer`; neighbours:
-// dims 2 i and 2 i + 1, both in the lane (c[i], s[i] of pair i).
+// Where lane `sub` of a head has its two runs of four dims.
+template <bool PAIRS_INSIDE>
+__device__ __forceinline__ void lane_dims(int rot, int sub, int &a0, int &a1) {
+    const bool split = !PAIRS_INSIDE && 8 * sub < rot;
+    a0 = split ? 4 * sub : 8 * sub;
+    a1 = split ? rot / 2 + 4 * sub : 8 * sub + 4;
+}
+
+// The angles of one token for a lane's four pairs: value i of the first run
+// and of the second (halves), or neighbours (PAIRS_INSIDE).
 template <bool PAIRS_INSIDE>
 struct Turn {
-    float c[PAIRS_INSIDE ? 4 : 8], s[PAIRS_INSIDE ? 4 : 8];
-    int peer;
+    float c[4], s[4];
 
-    __device__ __forceinline__ void none(int lane) {
+    template <typename T>
+    __device__ __forceinline__ void load(const NormArgs<T> &a, int64_t b, int n, int sub) {
 #pragma unroll
-        for (int i = 0; i < (PAIRS_INSIDE ? 4 : 8); ++i) {
+        for (int i = 0; i < 4; ++i) {
             c[i] = 1.f;
             s[i] = 0.f;
         }
-        peer = lane;
-    }
-    template <typename T>
-    __device__ __forceinline__ void load(const NormArgs<T> &a, int64_t b, int n, int lane) {
-        none(lane);
-        const int sub = lane & 7;
         if (8 * sub >= a.rot) return;
-        const int half = a.rot / 2, hl = half / 8;
-        int at = PAIRS_INSIDE ? 4 * sub : 8 * sub;
-        float sign = 1.f;
-        if (!PAIRS_INSIDE) {
-            const bool second = sub >= hl;
-            peer = second ? lane - hl : lane + hl;
-            if (second) at -= half;
-            else sign = -1.f;      // z1 = y1 c - y2 s
-        }
         const int p = a.pos ? __ldg(a.pos + b * a.pos_sb + n) : n;
         if (p < 0) return;         // not rotated
         if (p >= a.P) {
             atomicOr(&g_device_error, kErrPosition);
             return;
         }
-        const float4 *pc = reinterpret_cast<const float4 *>(a.cos + (int64_t)p * half + at);
-        const float4 *ps = reinterpret_cast<const float4 *>(a.sin + (int64_t)p * half + at);
-#pragma unroll
-        for (int i = 0; i < (PAIRS_INSIDE ? 1 : 2); ++i) {
-            const float4 vc = __ldg(pc + i), vs = __ldg(ps + i);
-            c[4 * i] = vc.x, c[4 * i + 1] = vc.y, c[4 * i + 2] = vc.z, c[4 * i + 3] = vc.w;
-            s[4 * i] = sign * vs.x, s[4 * i + 1] = sign * vs.y, s[4 * i + 2] = sign * vs.z, s[4 * i + 3] = sign * vs.w;
-        }
+        const int64_t at = (int64_t)p * (a.rot / 2) + 4 * sub;
+        const float4 vc = __ldg(reinterpret_cast<const float4 *>(a.cos + at));
+        const float4 vs = __ldg(reinterpret_cast<const float4 *>(a.sin + at));
+        c[0] = vc.x, c[1] = vc.y, c[2] = vc.z, c[3] = vc.w;
+        s[0] = vs.x, s[1] = vs.y, s[2] = vs.z, s[3] = vs.w;
     }
-    // Every lane of the warp calls it; dir = -1 turns back.
-    __device__ __forceinline__ void apply(float (&y)[8], float dir) const {
+    // BACK: by minus the angle
+    template <bool BACK>
+    __device__ __forceinline__ void apply(float2 (&y)[4]) const {
         if (PAIRS_INSIDE) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const float u = y[2 * i], v = y[2 * i + 1], t = dir * s[i % (PAIRS_INSIDE ? 4 : 8)];
-                y[2 * i] = u * c[i] - v * t;
-                y[2 * i + 1] = u * t + v * c[i];
+                const float t = BACK ? -s[i] : s[i];
+                y[i] = fma2(y[i], make_float2(c[i], c[i]), mul2(make_float2(y[i].y, y[i].x), make_float2(-t, t)));
             }
         } else {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float o = __shfl_sync(kFullMask, y[i], peer);
-                y[i] = y[i] * c[i % (PAIRS_INSIDE ? 4 : 8)] + dir * s[i % (PAIRS_INSIDE ? 4 : 8)] * o;
+            for (int i = 0; i < 2; ++i) {
+                const float2 cc = make_float2(c[2 * i], c[2 * i + 1]);
+                const float2 ss = make_float2(BACK ? -s[2 * i] : s[2 * i], BACK ? -s[2 * i + 1] : s[2 * i + 1]);
+                const float2 u = y[i], v = y[2 + i];
+                y[i] = fma2(u, cc, mul2(v, make_float2(-ss.x, -ss.y)));
+                y[2 + i] = fma2(v, cc, mul2(u, ss));
             }
         }
     }
@@ -169,154 +171,232 @@ __device__ __forceinline__ void stage_weights(const NormArgs<T> &a, float (*sw)[
     __syncthreads();
 }
 
-// A unit of a warp: one token, `steps` groups of four heads from group g0.
-struct Unit {
+// The head groups (four heads) that a warp works through: those of one token
+// after another, kSteps at a time; a token's groups are shared by `chunks`
+// warps where there are fewer tokens than warps.
+struct Walk {
+    int64_t u, units, step;
+    int N, chunks, groups;
     int64_t b;
-    int n, g0, steps;
-    __device__ __forceinline__ Unit(int64_t u, int N, int chunks, int groups) {
+    int n, g, end;         // token and groups [g, end) left of it
+    bool first;            // at the first groups of its part
+    __device__ __forceinline__ Walk(int64_t u, int64_t units, int64_t step, int N, int chunks, int groups)
+        : u(u), units(units), step(step), N(N), chunks(chunks), groups(groups) {
+        enter();
+    }
+    __device__ __forceinline__ bool left() const { return u < units; }
+    __device__ __forceinline__ void enter() {
         const int64_t token = u / chunks;
         const int c = (int)(u - token * chunks);
         b = token / N;
         n = (int)(token - b * N);
-        g0 = (int)((int64_t)groups * c / chunks);
-        steps = (int)((int64_t)groups * (c + 1) / chunks) - g0;
+        g = (int)((int64_t)groups * c / chunks);
+        end = (int)((int64_t)groups * (c + 1) / chunks);
+        first = true;
+    }
+    __device__ __forceinline__ void next() {
+        first = false;
+        g += kSteps;
+        if (g < end) return;
+        u += step;
+        if (left()) enter();
     }
 };
 
+// A token's rows within Q, K and V (dense).
+template <typename T>
+struct HeadRows {
+    T *q, *k, *v;
+    __device__ __forceinline__ void token(T *Q, T *K, T *V, int Hq, int Hk, int Hv, int64_t b, int n, int N) {
+        q = Q + (b * Hq * N + n) * 64;
+        k = K + (b * Hk * N + n) * 64;
+        v = V + (b * Hv * N + n) * 64;
+    }
+    __device__ __forceinline__ T *row(int h, int Hq, int Hn, int N) const {
+        T *p = h < Hq ? q : h < Hn ? k : v;
+        const int i = h < Hq ? h : h < Hn ? h - Hq : h - Hn;
+        return p + (int64_t)i * N * 64;
+    }
+};
+
+__device__ __forceinline__ float squares(const float2 (&x)[4]) {
+    float2 s = mul2(x[0], x[0]);
+#pragma unroll
+    for (int e = 1; e < 4; ++e) s = fma2(x[e], x[e], s);
+    return s.x + s.y;
+}
+__device__ __forceinline__ void weights(const float *sw, int a0, int a1, float2 (&w)[4]) {
+    const float4 u = *reinterpret_cast<const float4 *>(sw + a0), v = *reinterpret_cast<const float4 *>(sw + a1);
+    w[0] = make_float2(u.x, u.y), w[1] = make_float2(u.z, u.w);
+    w[2] = make_float2(v.x, v.y), w[3] = make_float2(v.z, v.w);
+}
+
 template <typename T, bool PAIRS_INSIDE>
-__global__ void __launch_bounds__(kWarps * 32)
+__global__ void __launch_bounds__(kWarps * 32, sizeof(T) == 2 ? 4 : 3)
 qk_norm_fwd_kernel(const __grid_constant__ NormArgs<T> a, const T *__restrict__ X, int64_t x_sb, int64_t x_sn,
                    T *__restrict__ Q, T *__restrict__ K, T *__restrict__ V, int64_t units, int chunks) {
-    __shared__ float sw[2][64];
+    __shared__ __align__(16) float sw[2][64];
     grid_dep_wait();
-    stage_weights(a, sw);
-    const int lane = threadIdx.x & 31, sub = lane & 7;
-    const int H = a.Hq + a.Hk + a.Hv, groups = (H + 3) / 4;
-    for (int64_t u = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5); u < units; u += (int64_t)gridDim.x * kWarps) {
-        const Unit t(u, a.N, chunks, groups);
-        const T *row = X + t.b * x_sb + t.n * x_sn + sub * 8;
-        Eight<T> raw[kSteps];
+    grid_dep_launch();
+    const int lane = threadIdx.x & 31, sub = lane & 7, grp = lane >> 3;
+    const int Hn = a.Hq + a.Hk, H = Hn + a.Hv;
+    int a0, a1;
+    lane_dims<PAIRS_INSIDE>(a.rot, sub, a0, a1);
+    Walk t((int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5), units, (int64_t)gridDim.x * kWarps, a.N, chunks,
+           (H + 3) / 4);
+    Eight<T> raw[kSteps], ahead[kSteps];
+    const auto load = [&](Eight<T> (&r)[kSteps]) {
+        const T *row = X + t.b * x_sb + t.n * x_sn;
 #pragma unroll
         for (int i = 0; i < kSteps; ++i) {
-            const int h = 4 * (t.g0 + i) + (lane >> 3);
-            if (i < t.steps && h < H) raw[i].load(row + (int64_t)h * 64);
-            else raw[i].zero();
+            const int h = 4 * (t.g + i) + grp;
+            if (t.g + i < t.end && h < H) r[i].load(row + h * 64, a0, a1);
+            else r[i].zero();
         }
-        Turn<PAIRS_INSIDE> turn;
-        turn.load(a, t.b, t.n, lane);
+    };
+    if (t.left()) load(raw);
+    stage_weights(a, sw);
+    Turn<PAIRS_INSIDE> turn;
+    HeadRows<T> out;
+    while (t.left()) {
+        if (t.first) {
+            turn.load(a, t.b, t.n, sub);
+            out.token(Q, K, V, a.Hq, a.Hk, a.Hv, t.b, t.n, a.N);
+        }
+        const int g0 = t.g, end = t.end;
+        const HeadRows<T> to = out;
+        t.next();
+        if (t.left()) load(ahead);
 #pragma unroll
         for (int i = 0; i < kSteps; ++i) {
-            if (i >= t.steps) break;
-            const int g = t.g0 + i, h = 4 * g + (lane >> 3);
-            if (4 * g < a.Hq + a.Hk) {   // some head of the group is a query or a key
-                float x[8], y[8];
+            const int g = g0 + i, h = 4 * g + grp;
+            if (g >= end) break;
+            if (4 * g < Hn) {   // some head of the group is a query or a key
+                float2 x[4];
                 raw[i].get(x);
                 const bool isq = h < a.Hq;
-                float ss = 0.f;
+                const float r = (isq ? a.wq : a.wk) ? rsqrtf(sum8(squares(x)) * (1.f / 64.f) + a.eps) : 1.f;
+                float2 w[4];
+                weights(sw[isq ? 0 : 1], a0, a1, w);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) ss = fmaf(x[e], x[e], ss);
-                ss = sum8(ss);
-                const float r = (isq ? a.wq : a.wk) ? rsqrtf(ss * (1.f / 64.f) + a.eps) : 1.f;
-                const float4 *w4 = reinterpret_cast<const float4 *>(sw[isq ? 0 : 1] + sub * 8);
-                const float4 wa = w4[0], wb = w4[1];
-                const float w[8] = {wa.x, wa.y, wa.z, wa.w, wb.x, wb.y, wb.z, wb.w};
-#pragma unroll
-                for (int e = 0; e < 8; ++e) y[e] = x[e] * r * w[e];
-                turn.apply(y, 1.f);
-                if (h < a.Hq + a.Hk) raw[i].put(y);
+                for (int e = 0; e < 4; ++e) x[e] = mul2(x[e], mul2(w[e], make_float2(r, r)));
+                turn.template apply<false>(x);
+                if (h < Hn) raw[i].put(x);
             }
-            if (h < H) {
-                T *out = h < a.Hq          ? Q + ((t.b * a.Hq + h) * a.N + t.n) * 64
-                         : h < a.Hq + a.Hk ? K + ((t.b * a.Hk + (h - a.Hq)) * a.N + t.n) * 64
-                                           : V + ((t.b * a.Hv + (h - a.Hq - a.Hk)) * a.N + t.n) * 64;
-                raw[i].store(out + sub * 8);
-            }
+            if (h < H) raw[i].store(to.row(h, a.Hq, Hn, a.N), a0, a1);
         }
+#pragma unroll
+        for (int i = 0; i < kSteps; ++i) raw[i] = ahead[i];
     }
 }
 
 template <typename T, bool PAIRS_INSIDE>
-__global__ void __launch_bounds__(kWarps * 32)
+__global__ void __launch_bounds__(kWarps * 32, 2)
 qk_norm_bwd_kernel(const __grid_constant__ NormArgs<T> a, const T *__restrict__ X, int64_t x_sb, int64_t x_sn,
                    const T *__restrict__ dQ, const T *__restrict__ dK, const T *__restrict__ dV, T *__restrict__ dX,
                    int64_t dx_sb, int64_t dx_sn, float *__restrict__ partial, int64_t units, int chunks) {
-    __shared__ float sw[2][64];
+    __shared__ __align__(16) float sw[2][64];
     __shared__ float part[kWarps][128];
     grid_dep_wait();
-    stage_weights(a, sw);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = lane & 7;
-    const int H = a.Hq + a.Hk + a.Hv, groups = (H + 3) / 4;
-    float dwq[8], dwk[8];
+    grid_dep_launch();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = lane & 7, grp = lane >> 3;
+    const int Hn = a.Hq + a.Hk, H = Hn + a.Hv;
+    int a0, a1;
+    lane_dims<PAIRS_INSIDE>(a.rot, sub, a0, a1);
+    float2 dwq[4], dwk[4];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) dwq[e] = dwk[e] = 0.f;
-    for (int64_t u = (int64_t)blockIdx.x * kWarps + warp; u < units; u += (int64_t)gridDim.x * kWarps) {
-        const Unit t(u, a.N, chunks, groups);
-        const T *row = X + t.b * x_sb + t.n * x_sn + sub * 8;
-        T *drow = dX + t.b * dx_sb + t.n * dx_sn + sub * 8;
-        Eight<T> raw[kSteps], grad[kSteps];
+    for (int e = 0; e < 4; ++e) dwq[e] = dwk[e] = make_float2(0.f, 0.f);
+    Walk t((int64_t)blockIdx.x * kWarps + warp, units, (int64_t)gridDim.x * kWarps, a.N, chunks, (H + 3) / 4);
+    Eight<T> raw[kSteps], grad[kSteps], raw_ahead[kSteps], grad_ahead[kSteps];
+    const auto load = [&](Eight<T> (&r)[kSteps], Eight<T> (&d)[kSteps]) {
+        const T *row = X + t.b * x_sb + t.n * x_sn;
+        HeadRows<const T> from;
+        from.token(dQ, dK, dV, a.Hq, a.Hk, a.Hv, t.b, t.n, a.N);
 #pragma unroll
         for (int i = 0; i < kSteps; ++i) {
-            const int h = 4 * (t.g0 + i) + (lane >> 3);
-            raw[i].zero();
-            grad[i].zero();
-            if (i < t.steps && h < H) {
-                if (h < a.Hq + a.Hk) raw[i].load(row + (int64_t)h * 64);
-                const T *src = h < a.Hq          ? dQ + ((t.b * a.Hq + h) * a.N + t.n) * 64
-                               : h < a.Hq + a.Hk ? dK + ((t.b * a.Hk + (h - a.Hq)) * a.N + t.n) * 64
-                                                 : dV + ((t.b * a.Hv + (h - a.Hq - a.Hk)) * a.N + t.n) * 64;
-                grad[i].load(src + sub * 8);
+            const int h = 4 * (t.g + i) + grp;
+            r[i].zero();
+            d[i].zero();
+            if (t.g + i < t.end && h < H) {
+                if (h < Hn) r[i].load(row + h * 64, a0, a1);
+                d[i].load(from.row(h, a.Hq, Hn, a.N), a0, a1);
             }
         }
-        Turn<PAIRS_INSIDE> turn;
-        turn.load(a, t.b, t.n, lane);
+    };
+    if (t.left()) load(raw, grad);
+    stage_weights(a, sw);
+    Turn<PAIRS_INSIDE> turn;
+    while (t.left()) {
+        if (t.first) turn.load(a, t.b, t.n, sub);
+        T *drow = dX + t.b * dx_sb + t.n * dx_sn;
+        const int g0 = t.g, end = t.end;
+        t.next();
+        if (t.left()) load(raw_ahead, grad_ahead);
 #pragma unroll
         for (int i = 0; i < kSteps; ++i) {
-            if (i >= t.steps) break;
-            const int g = t.g0 + i, h = 4 * g + (lane >> 3);
-            if (4 * g < a.Hq + a.Hk) {
-                float x[8], dy[8];
+            const int g = g0 + i, h = 4 * g + grp;
+            if (g >= end) break;
+            if (4 * g < Hn) {
+                float2 x[4], dy[4], w[4];
                 raw[i].get(x);
                 grad[i].get(dy);
-                const bool isq = h < a.Hq, isk = !isq && h < a.Hq + a.Hk;
-                turn.apply(dy, -1.f);
-                float ss = 0.f;
-#pragma unroll
-                for (int e = 0; e < 8; ++e) ss = fmaf(x[e], x[e], ss);
-                ss = sum8(ss);
+                const bool isq = h < a.Hq, isk = !isq && h < Hn;
+                turn.template apply<true>(dy);
                 const bool norm = (isq ? a.wq : a.wk) != nullptr;
-                const float r = norm ? rsqrtf(ss * (1.f / 64.f) + a.eps) : 1.f;
-                const float4 *w4 = reinterpret_cast<const float4 *>(sw[isq ? 0 : 1] + sub * 8);
-                const float4 wa = w4[0], wb = w4[1];
-                const float w[8] = {wa.x, wa.y, wa.z, wa.w, wb.x, wb.y, wb.z, wb.w};
-                float dot = 0.f;
+                const float r = norm ? rsqrtf(sum8(squares(x)) * (1.f / 64.f) + a.eps) : 1.f;
+                weights(sw[isq ? 0 : 1], a0, a1, w);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const float n = x[e] * r, d = dy[e] * n;
-                    dwq[e] += isq ? d : 0.f;   // selected, not multiplied: another head's NaN stays out
-                    dwk[e] += isk ? d : 0.f;
-                    x[e] = n;
-                    dy[e] *= w[e];
-                    dot = fmaf(dy[e], n, dot);
+                for (int e = 0; e < 4; ++e) x[e] = mul2(x[e], make_float2(r, r));
+                if (4 * g + 4 <= a.Hq) {            // four queries
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) dwq[e] = fma2(dy[e], x[e], dwq[e]);
+                } else if (4 * g >= a.Hq && 4 * g + 4 <= Hn) {     // four keys
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) dwk[e] = fma2(dy[e], x[e], dwk[e]);
+                } else {
+                    // selected, not multiplied by 0: another kind's NaN stays out
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float2 d = mul2(dy[e], x[e]);
+                        dwq[e] = add2(dwq[e], make_float2(isq ? d.x : 0.f, isq ? d.y : 0.f));
+                        dwk[e] = add2(dwk[e], make_float2(isk ? d.x : 0.f, isk ? d.y : 0.f));
+                    }
                 }
-                dot = sum8(dot) * (norm ? 1.f / 64.f : 0.f);
+                float2 dot = make_float2(0.f, 0.f);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) dy[e] = r * (dy[e] - x[e] * dot);
-                if (h < a.Hq + a.Hk) grad[i].put(dy);
+                for (int e = 0; e < 4; ++e) {
+                    dy[e] = mul2(dy[e], w[e]);
+                    dot = fma2(dy[e], x[e], dot);
+                }
+                const float m = sum8(dot.x + dot.y) * (norm ? -1.f / 64.f : 0.f);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) dy[e] = mul2(make_float2(r, r), fma2(x[e], make_float2(m, m), dy[e]));
+                if (h < Hn) grad[i].put(dy);
             }
-            if (h < H) grad[i].store(drow + (int64_t)h * 64);
+            if (h < H) grad[i].store(drow + h * 64, a0, a1);
+        }
+#pragma unroll
+        for (int i = 0; i < kSteps; ++i) {
+            raw[i] = raw_ahead[i];
+            grad[i] = grad_ahead[i];
         }
     }
     // the block's sums: over the four heads of a warp, then over its warps
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
+    for (int e = 0; e < 4; ++e) {
 #pragma unroll
         for (int m = 8; m < 32; m <<= 1) {
-            dwq[e] += __shfl_xor_sync(kFullMask, dwq[e], m);
-            dwk[e] += __shfl_xor_sync(kFullMask, dwk[e], m);
+            dwq[e].x += __shfl_xor_sync(kFullMask, dwq[e].x, m);
+            dwq[e].y += __shfl_xor_sync(kFullMask, dwq[e].y, m);
+            dwk[e].x += __shfl_xor_sync(kFullMask, dwk[e].x, m);
+            dwk[e].y += __shfl_xor_sync(kFullMask, dwk[e].y, m);
         }
         if (lane < 8) {
-            part[warp][sub * 8 + e] = dwq[e];
-            part[warp][64 + sub * 8 + e] = dwk[e];
+            const int d = (e < 2 ? a0 : a1) + 2 * (e & 1);
+            part[warp][d] = dwq[e].x;
+            part[warp][d + 1] = dwq[e].y;
+            part[warp][64 + d] = dwk[e].x;
+            part[warp][64 + d + 1] = dwk[e].y;
         }
     }
     __syncthreads();
@@ -347,17 +427,30 @@ __global__ void __launch_bounds__(1024) qk_norm_dw_kernel(const float *__restric
     if (out) out[c & 63] = (T)s;
 }
 
-// Units of work and blocks: chunks of a token's heads small enough for
-// kSteps, four blocks an SM at most (a block then takes several units).
+// One wave of blocks, each warp walking over its tokens: the next groups are
+// loaded while these are worked on.  Fewer tokens than warps: a token's
+// groups are cut into chunks of at least kSteps.
+template <auto Kernel>
+int resident_blocks() {
+    static std::atomic<int> per_sm{0};
+    int n = per_sm.load(std::memory_order_relaxed);
+    if (n == 0) {
+        if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, Kernel, kWarps * 32, 0) != cudaSuccess || n < 1) n = 1;
+        per_sm.store(n, std::memory_order_relaxed);
+    }
+    return std::min(kMaxBlocks, n * sm_count());
+}
+
 struct Grid {
     int chunks;
     int64_t units;
     unsigned blocks;
-    explicit Grid(const QkNormArgs &q) {
-        const int groups = (q.Hq + q.Hk + q.Hv + 3) / 4;
-        chunks = (groups + kSteps - 1) / kSteps;
-        units = (int64_t)q.B * q.N * chunks;
-        blocks = (unsigned)std::min<int64_t>((units + kWarps - 1) / kWarps, std::min(kMaxBlocks, 4 * sm_count()));
+    Grid(const QkNormArgs &q, int resident) {
+        const int groups = (q.Hq + q.Hk + q.Hv + 3) / 4, most = (groups + kSteps - 1) / kSteps;
+        const int64_t tokens = (int64_t)q.B * q.N, warps = (int64_t)resident * kWarps;
+        chunks = (int)std::min<int64_t>(most, std::max<int64_t>(1, (warps + tokens - 1) / tokens));
+        units = tokens * chunks;
+        blocks = (unsigned)std::min<int64_t>((units + kWarps - 1) / kWarps, resident);
     }
 };
 
@@ -367,26 +460,25 @@ NormArgs<T> norm_args(const QkNormArgs &q) {
                        q.rot, q.cos, q.sin, q.P,  q.pos,                        q.pos_sb};
 }
 
-template <typename T>
+template <typename T, bool PAIRS_INSIDE>
 cudaError_t fwd(const QkNormArgs &q) {
-    const Grid g(q);
-    const auto kern = q.interleaved ? qk_norm_fwd_kernel<T, true> : qk_norm_fwd_kernel<T, false>;
-    const cudaError_t e = launch_kernel(kern, dim3(g.blocks), dim3(kWarps * 32), 0, q.stream, pdl_enabled(),
-                                        norm_args<T>(q), static_cast<const T *>(q.X), q.x_sb, q.x_sn,
-                                        static_cast<T *>(q.Q), static_cast<T *>(q.K), static_cast<T *>(q.V), g.units,
-                                        g.chunks);
+    const Grid g(q, resident_blocks<qk_norm_fwd_kernel<T, PAIRS_INSIDE>>());
+    const cudaError_t e = launch_kernel(qk_norm_fwd_kernel<T, PAIRS_INSIDE>, dim3(g.blocks), dim3(kWarps * 32), 0,
+                                        q.stream, pdl_enabled(), norm_args<T>(q), static_cast<const T *>(q.X), q.x_sb,
+                                        q.x_sn, static_cast<T *>(q.Q), static_cast<T *>(q.K), static_cast<T *>(q.V),
+                                        g.units, g.chunks);
     if (e == cudaSuccess) count_launches(1);
     return e;
 }
 
-template <typename T>
+template <typename T, bool PAIRS_INSIDE>
 cudaError_t bwd(const QkNormArgs &q) {
-    const Grid g(q);
-    const auto kern = q.interleaved ? qk_norm_bwd_kernel<T, true> : qk_norm_bwd_kernel<T, false>;
-    cudaError_t e = launch_kernel(kern, dim3(g.blocks), dim3(kWarps * 32), 0, q.stream, pdl_enabled(), norm_args<T>(q),
-                                  static_cast<const T *>(q.X), q.x_sb, q.x_sn, static_cast<const T *>(q.dQ),
-                                  static_cast<const T *>(q.dK), static_cast<const T *>(q.dV), static_cast<T *>(q.dX),
-                                  q.dx_sb, q.dx_sn, q.ws, g.units, g.chunks);
+    const Grid g(q, resident_blocks<qk_norm_bwd_kernel<T, PAIRS_INSIDE>>());
+    cudaError_t e = launch_kernel(qk_norm_bwd_kernel<T, PAIRS_INSIDE>, dim3(g.blocks), dim3(kWarps * 32), 0, q.stream,
+                                  pdl_enabled(), norm_args<T>(q), static_cast<const T *>(q.X), q.x_sb, q.x_sn,
+                                  static_cast<const T *>(q.dQ), static_cast<const T *>(q.dK),
+                                  static_cast<const T *>(q.dV), static_cast<T *>(q.dX), q.dx_sb, q.dx_sn, q.ws, g.units,
+                                  g.chunks);
     if (e != cudaSuccess) return e;
     count_launches(1);
     if (!q.dwq && !q.dwk) return cudaSuccess;
@@ -402,10 +494,12 @@ cudaError_t bwd(const QkNormArgs &q) {
 size_t qk_norm_bwd_workspace() { return (size_t)kMaxBlocks * 128 * sizeof(float); }
 
 cudaError_t launch_qk_norm_fwd(const QkNormArgs &q) {
-    return q.dtype == FIBATT_F32 ? fwd<float>(q) : fwd<__nv_bfloat16>(q);
+    if (q.interleaved) return q.dtype == FIBATT_F32 ? fwd<float, true>(q) : fwd<__nv_bfloat16, true>(q);
+    return q.dtype == FIBATT_F32 ? fwd<float, false>(q) : fwd<__nv_bfloat16, false>(q);
 }
 cudaError_t launch_qk_norm_bwd(const QkNormArgs &q) {
-    return q.dtype == FIBATT_F32 ? bwd<float>(q) : bwd<__nv_bfloat16>(q);
+    if (q.interleaved) return q.dtype == FIBATT_F32 ? bwd<float, true>(q) : bwd<__nv_bfloat16, true>(q);
+    return q.dtype == FIBATT_F32 ? bwd<float, false>(q) : bwd<__nv_bfloat16, false>(q);
 }
 
 FIBATT_DEFINE_ERROR_READER(read_error_qk_norm, "qk_norm.cu")

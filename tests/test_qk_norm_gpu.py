@@ -73,8 +73,11 @@ def test_positions(dtype, interleaved):
     wide = torch.randint(-1, 5000, (3, 17), generator=g, device="cuda", dtype=torch.int32)[:, 3:14]
     for p in (each, one, wide, one[None].expand(3, 11)):
         out, _ = _check(x, (4, 2, 2), w, rotary, grads, p, interleaved)
-    plain = api.qk_norm_fwd(x, (4, 2, 2), *w)
-    assert torch.equal(out[0][:, :, 0], plain[0][:, :, 0])             # position -1: not rotated
+    # a token at a negative position is not rotated: as in a call where none is (which _check
+    # compares with the norm alone)
+    off = torch.full((11,), -1, dtype=torch.int32, device="cuda")
+    none, _ = _check(x, (4, 2, 2), w, rotary, grads, off, interleaved)
+    assert torch.equal(out[0][:, :, 0], none[0][:, :, 0])
 
 
 def test_position_behind_the_table_is_reported():
