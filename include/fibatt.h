@@ -241,7 +241,7 @@ typedef struct {
 /* X: token rows of (Hq + Hk + Hv) 64 contiguous elements, x_stride_n elements
  * between the tokens and x_stride_b between the sequences of one.  Writes
  * Q [B, Hq, N, 64], K [B, Hk, N, 64] and V [B, Hv, N, 64], dense (a part
- * without heads may be NULL).  INVALID_ARG: B or N < 1, a negative head count
+ * without heads may be NULL).  INVALID_ARG: B or N < 1, B N above 2^31 - 256, a negative head count
  * or none, a NULL or misaligned pointer (16 bytes; positions 4), a stride
  * that is not a multiple of 16 bytes, eps, rot_dims or table_len out of their range,
  * positions NULL with table_len < N.  UNSUPPORTED: D, dtype. */

@@ -105,11 +105,10 @@ fibatt_status check_norm(const fibatt_qk_norm *d, const void *X, int64_t sb, int
         if (d->positions && d->positions_stride_b < 0) return invalid("positions_stride_b is negative");
     }
     if (fibatt_status st = check_ptr(X, "X")) return st;
-    const int64_t row = ((int64_t)d->Hq + d->Hk + d->Hv) * kHeadDim;
     for (int64_t s : {sb, sn})
         if (s < 0 || s > (int64_t)1 << 38 || s * size_of(d->dtype) % 16)
             return invalid(fmt("X: stride %lld is not a multiple of 16 bytes in [0, 2^38]", (long long)s));
-    if ((int64_t)d->B * d->N > 0x7fffffffffLL / row) return invalid("too many tokens for one call");
+    if ((int64_t)d->B * d->N > 0x7fffff00LL) return invalid("too many tokens for one call (2^31 - 256)");
     if (fault("arg")) return invalid("injected argument fault (FIBATT_FAULT=arg)");
     return FIBATT_OK;
 }

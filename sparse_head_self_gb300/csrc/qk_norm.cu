@@ -12,12 +12,15 @@
 //
 // Both directions only move data: they read and write each element once, and
 // with 16-bit elements the instructions a head takes cost about as much as its
-// bytes.  Eight lanes share a head, a lane has two runs of four dims, chosen so
-// that both values of every rotated pair are its own (halves: dims 4 i.. and
-// rot / 2 + 4 i..), which leaves the two sums over a head as the only exchange;
-// the arithmetic is on packed pairs of floats.  A warp takes four heads of one
-// token per step, kSteps steps at once, and the next ones' loads are in flight
-// while these are worked on; a token's angles are loaded once for its heads.
+// bytes.  A block takes 16 consecutive tokens at a time (over the sequences'
+// ends: a token's rows are found once), its warps eight of them and every
+// fourth head, so that a warp's head is of one kind.  Eight lanes share a
+// head row; a lane has two runs of four dims, chosen so that both values of
+// every rotated pair are its own (halves: dims 4 i.. and rot / 2 + 4 i..),
+// which leaves the two sums over a head as the only exchange; the arithmetic
+// is on packed pairs of floats.  Rows arrive by asynchronous copies in a ring of
+// each warp's own, kDepth heads ahead and over the units' ends, without holding
+// registers; the tokens' angles are brought into shared memory once for all heads.
 // Every head row is a whole 128- or 256-byte segment, so all traffic is full
 // sectors.  The values' heads are copied unconverted.
 //
@@ -34,25 +37,37 @@ namespace fibatt {
 namespace {
 
 constexpr int kWarps = 8;
-constexpr int kSteps = 2;             // head groups of four that a warp loads at once
+constexpr int kTokens = 16;           // of a unit
+constexpr int kSteps = 2;             // four tokens each: a warp's half of a unit
+constexpr int kDepth = 4;             // heads in a warp's ring
 constexpr int kMaxBlocks = 1024;      // rows of the dw partial sums
 constexpr unsigned kErrPosition = 8u; // a position at or behind the end of the tables
 
-// A lane's eight dims of a head: runs of four at a0 and a1 (elements).
+__device__ __forceinline__ void copy_async(void *smem, const void *gmem) {   // 16 bytes
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(smem)), "l"(gmem)
+                 : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// All but the newest N groups of this thread's copies have arrived.
+template <int N>
+__device__ __forceinline__ void copies_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// A lane's eight dims of a head row: runs of four at a0 and a1 (elements).
 template <typename T>
 struct Eight;
 template <>
 struct Eight<__nv_bfloat16> {
     uint2 u, v;
     __device__ __forceinline__ void load(const __nv_bfloat16 *p, int a0, int a1) {
-        u = __ldg(reinterpret_cast<const uint2 *>(p + a0));
-        v = __ldg(reinterpret_cast<const uint2 *>(p + a1));
+        u = *reinterpret_cast<const uint2 *>(p + a0);
+        v = *reinterpret_cast<const uint2 *>(p + a1);
     }
     __device__ __forceinline__ void store(__nv_bfloat16 *p, int a0, int a1) const {
         *reinterpret_cast<uint2 *>(p + a0) = u;
         *reinterpret_cast<uint2 *>(p + a1) = v;
     }
-    __device__ __forceinline__ void zero() { u = v = make_uint2(0, 0); }
     __device__ __forceinline__ void get(float2 (&x)[4]) const {
         x[0] = make_float2(bf16_lo(u.x), bf16_hi(u.x));
         x[1] = make_float2(bf16_lo(u.y), bf16_hi(u.y));
@@ -68,14 +83,13 @@ template <>
 struct Eight<float> {
     float4 a, b;
     __device__ __forceinline__ void load(const float *p, int a0, int a1) {
-        a = __ldg(reinterpret_cast<const float4 *>(p + a0));
-        b = __ldg(reinterpret_cast<const float4 *>(p + a1));
+        a = *reinterpret_cast<const float4 *>(p + a0);
+        b = *reinterpret_cast<const float4 *>(p + a1);
     }
     __device__ __forceinline__ void store(float *p, int a0, int a1) const {
         *reinterpret_cast<float4 *>(p + a0) = a;
         *reinterpret_cast<float4 *>(p + a1) = b;
     }
-    __device__ __forceinline__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
     __device__ __forceinline__ void get(float2 (&x)[4]) const {
         x[0] = make_float2(a.x, a.y), x[1] = make_float2(a.z, a.w);
         x[2] = make_float2(b.x, b.y), x[3] = make_float2(b.z, b.w);
@@ -113,23 +127,16 @@ template <bool PAIRS_INSIDE>
 struct Turn {
     float c[4], s[4];
 
-    template <typename T>
-    __device__ __forceinline__ void load(const NormArgs<T> &a, int64_t b, int n, int sub) {
+    // from a token's 32 cosines and 32 sines in shared memory
+    __device__ __forceinline__ void load(const float *angles, int rot, int sub) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             c[i] = 1.f;
             s[i] = 0.f;
         }
-        if (8 * sub >= a.rot) return;
-        const int p = a.pos ? __ldg(a.pos + b * a.pos_sb + n) : n;
-        if (p < 0) return;         // not rotated
-        if (p >= a.P) {
-            atomicOr(&g_device_error, kErrPosition);
-            return;
-        }
-        const int64_t at = (int64_t)p * (a.rot / 2) + 4 * sub;
-        const float4 vc = __ldg(reinterpret_cast<const float4 *>(a.cos + at));
-        const float4 vs = __ldg(reinterpret_cast<const float4 *>(a.sin + at));
+        if (8 * sub >= rot) return;
+        const float4 vc = *reinterpret_cast<const float4 *>(angles + 4 * sub);
+        const float4 vs = *reinterpret_cast<const float4 *>(angles + 32 + 4 * sub);
         c[0] = vc.x, c[1] = vc.y, c[2] = vc.z, c[3] = vc.w;
         s[0] = vs.x, s[1] = vs.y, s[2] = vs.z, s[3] = vs.w;
     }
@@ -171,53 +178,76 @@ __device__ __forceinline__ void stage_weights(const NormArgs<T> &a, float (*sw)[
     __syncthreads();
 }
 
-// The head groups (four heads) that a warp works through: those of one token
-// after another, kSteps at a time; a token's groups are shared by `chunks`
-// warps where there are fewer tokens than warps.
-struct Walk {
-    int64_t u, units, step;
-    int N, chunks, groups;
-    int64_t b;
-    int n, g, end;         // token and groups [g, end) left of it
-    bool first;            // at the first groups of its part
-    __device__ __forceinline__ Walk(int64_t u, int64_t units, int64_t step, int N, int chunks, int groups)
-        : u(u), units(units), step(step), N(N), chunks(chunks), groups(groups) {
-        enter();
+// Bring the angles of the unit's 16 tokens into `to` [16][64]: thread 16 i + j
+// copies the j-th 16 bytes of token i's cosines (j < 8) and sines.  Tokens that
+// are not rotated get (1, 0).
+template <typename T>
+__device__ __forceinline__ void stage_angles(const NormArgs<T> &a, float *to, unsigned unit, unsigned tokens) {
+    const int i = threadIdx.x >> 4, j = threadIdx.x & 15, half = a.rot / 2, at = 4 * (j & 7);
+    const unsigned token = unit * kTokens + i;
+    if (at >= half || token >= tokens) return;
+    const unsigned b = token / (unsigned)a.N;
+    const int n = (int)(token - b * a.N);
+    const int p = a.pos ? __ldg(a.pos + b * a.pos_sb + n) : n;
+    float *dst = to + 64 * i + 4 * j;
+    if (p >= 0 && p < a.P) {
+        copy_async(dst, (j < 8 ? a.cos : a.sin) + (int64_t)p * half + at);
+    } else {
+        const float v = j < 8 ? 1.f : 0.f;
+        *reinterpret_cast<float4 *>(dst) = make_float4(v, v, v, v);
+        if (p >= a.P) atomicOr(&g_device_error, kErrPosition);
     }
-    __device__ __forceinline__ bool left() const { return u < units; }
-    __device__ __forceinline__ void enter() {
-        const int64_t token = u / chunks;
-        const int c = (int)(u - token * chunks);
-        b = token / N;
-        n = (int)(token - b * N);
-        g = (int)((int64_t)groups * c / chunks);
-        end = (int)((int64_t)groups * (c + 1) / chunks);
-        first = true;
+}
+
+// A lane's two tokens of a unit, and where their rows are.
+struct Tokens {
+    unsigned b[kSteps], n[kSteps];
+    bool in[kSteps];
+    __device__ __forceinline__ void set(unsigned unit, unsigned tokens, int N) {
+        const unsigned first = (threadIdx.x >> 5 & 1) * 8 + (threadIdx.x >> 3 & 3);
+#pragma unroll
+        for (int s = 0; s < kSteps; ++s) {
+            const unsigned t = unit * kTokens + first + 4 * s;
+            in[s] = t < tokens;
+            b[s] = t / (unsigned)N;
+            n[s] = t - b[s] * N;
+        }
     }
-    __device__ __forceinline__ void next() {
-        first = false;
-        g += kSteps;
-        if (g < end) return;
-        u += step;
-        if (left()) enter();
+    // in the packed tensor
+    __device__ __forceinline__ int64_t packed(int s, int h, int64_t sb, int64_t sn) const {
+        return (int64_t)b[s] * sb + (int64_t)n[s] * sn + h * 64;
+    }
+    // head h of H in a dense [B, H, N, 64] tensor
+    __device__ __forceinline__ int64_t dense(int s, int h, int H, int N) const {
+        return (((int64_t)b[s] * H + h) * N + n[s]) * 64;
     }
 };
 
-// A token's rows within Q, K and V (dense).
+// The tensor of head h (the same kind for the whole warp): its heads, and h's
+// number among them.
 template <typename T>
-struct HeadRows {
-    T *q, *k, *v;
-    __device__ __forceinline__ void token(T *Q, T *K, T *V, int Hq, int Hk, int Hv, int64_t b, int n, int N) {
-        q = Q + (b * Hq * N + n) * 64;
-        k = K + (b * Hk * N + n) * 64;
-        v = V + (b * Hv * N + n) * 64;
+__device__ __forceinline__ T *kind_of(T *q, T *k, T *v, int Hq, int Hk, int Hv, int h, int &i, int &H) {
+    if (h < Hq) {
+        i = h, H = Hq;
+        return q;
     }
-    __device__ __forceinline__ T *row(int h, int Hq, int Hn, int N) const {
-        T *p = h < Hq ? q : h < Hn ? k : v;
-        const int i = h < Hq ? h : h < Hn ? h - Hq : h - Hn;
-        return p + (int64_t)i * N * 64;
+    if (h < Hq + Hk) {
+        i = h - Hq, H = Hk;
+        return k;
     }
-};
+    i = h - Hq - Hk, H = Hv;
+    return v;
+}
+
+// One head row of 64 elements from `src` into the warp's slot: lane's share of
+// 16-byte copies.
+template <typename T>
+__device__ __forceinline__ void copy_row(T *dst, const T *src) {
+    constexpr int kPer = 16 / sizeof(T);
+    const int sub = threadIdx.x & 7;
+#pragma unroll
+    for (int i = 0; i < 8 / kPer; ++i) copy_async(dst + (8 * i + sub) * kPer, src + (8 * i + sub) * kPer);
+}
 
 __device__ __forceinline__ float squares(const float2 (&x)[4]) {
     float2 s = mul2(x[0], x[0]);
@@ -231,156 +261,217 @@ __device__ __forceinline__ void weights(const float *sw, int a0, int a1, float2 
     w[2] = make_float2(v.x, v.y), w[3] = make_float2(v.z, v.w);
 }
 
+// Shared memory of a block: two units' angles, and every warp's ring of kDepth
+// heads of RT tensors, eight rows each.
+template <typename T, int RT>
+constexpr size_t ring_bytes() {
+    return 2 * kTokens * 64 * sizeof(float) + (size_t)kWarps * kDepth * RT * 8 * 64 * sizeof(T);
+}
+
+// Where a warp is in its sequence of (unit, head) pairs.
+struct Place {
+    unsigned unit;
+    int h;
+    __device__ __forceinline__ Place(unsigned unit, int h) : unit(unit), h(h) {}
+    // the next pair; true when the unit changed
+    __device__ __forceinline__ bool next(int H, int first, unsigned step) {
+        h += kWarps / 2;
+        if (h < H) return false;
+        h = first;
+        unit += step;
+        return true;
+    }
+};
+
 template <typename T, bool PAIRS_INSIDE>
 __global__ void __launch_bounds__(kWarps * 32, sizeof(T) == 2 ? 4 : 3)
 qk_norm_fwd_kernel(const __grid_constant__ NormArgs<T> a, const T *__restrict__ X, int64_t x_sb, int64_t x_sn,
-                   T *__restrict__ Q, T *__restrict__ K, T *__restrict__ V, int64_t units, int chunks) {
+                   T *__restrict__ Q, T *__restrict__ K, T *__restrict__ V, unsigned tokens, unsigned units) {
+    extern __shared__ float4 smem4[];
     __shared__ __align__(16) float sw[2][64];
-    grid_dep_wait();
-    grid_dep_launch();
-    const int lane = threadIdx.x & 31, sub = lane & 7, grp = lane >> 3;
-    const int Hn = a.Hq + a.Hk, H = Hn + a.Hv;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = lane & 7, grp = lane >> 3;
+    float *angles = reinterpret_cast<float *>(smem4);
+    T *ring = reinterpret_cast<T *>(angles + 2 * kTokens * 64) + (size_t)warp * kDepth * 8 * 64;
+    const int Hn = a.Hq + a.Hk, H = Hn + a.Hv, first = warp >> 1;
+    const unsigned step = gridDim.x;
+    const bool few = H < 4 * kDepth;     // a warp may have fewer heads than its ring
     int a0, a1;
     lane_dims<PAIRS_INSIDE>(a.rot, sub, a0, a1);
-    Walk t((int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5), units, (int64_t)gridDim.x * kWarps, a.N, chunks,
-           (H + 3) / 4);
-    Eight<T> raw[kSteps], ahead[kSteps];
-    const auto load = [&](Eight<T> (&r)[kSteps]) {
-        const T *row = X + t.b * x_sb + t.n * x_sn;
+    grid_dep_wait();
+    grid_dep_launch();
+
+    Tokens ahead, here;
+    Place load(blockIdx.x, first), work(blockIdx.x, first);
+    // copies of the next (unit, head) into slot `slot`; one group each, empty at the end
+    const auto fetch = [&](int slot) {
+        if (load.unit < units && load.h < H) {
 #pragma unroll
-        for (int i = 0; i < kSteps; ++i) {
-            const int h = 4 * (t.g + i) + grp;
-            if (t.g + i < t.end && h < H) r[i].load(row + h * 64, a0, a1);
-            else r[i].zero();
+            for (int s = 0; s < kSteps; ++s)
+                if (ahead.in[s])
+                    copy_row(ring + (slot * 8 + 4 * s + grp) * 64, X + ahead.packed(s, load.h, x_sb, x_sn));
+            if (load.next(H, first, step)) ahead.set(load.unit, tokens, a.N);
         }
+        copies_commit();
     };
-    if (t.left()) load(raw);
+    if (a.rot) stage_angles(a, angles, blockIdx.x, tokens);
+    copies_commit();
+    ahead.set(blockIdx.x, tokens, a.N);
+#pragma unroll
+    for (int i = 0; i < kDepth - 1; ++i) fetch(i);
     stage_weights(a, sw);
-    Turn<PAIRS_INSIDE> turn;
-    HeadRows<T> out;
-    while (t.left()) {
-        if (t.first) {
-            turn.load(a, t.b, t.n, sub);
-            out.token(Q, K, V, a.Hq, a.Hk, a.Hv, t.b, t.n, a.N);
-        }
-        const int g0 = t.g, end = t.end;
-        const HeadRows<T> to = out;
-        t.next();
-        if (t.left()) load(ahead);
+
+    int slot = 0;
+    for (int buf = 0; work.unit < units; buf ^= 1) {
+        const unsigned unit = work.unit;
+        here.set(unit, tokens, a.N);
+        // this unit's angles: the oldest group at the start; later they were asked for
+        // with the first head of the unit before, at least kDepth groups ago
+        if (few) copies_wait<0>();
+        else copies_wait<kDepth - 1>();
+        __syncthreads();
+        if (a.rot && unit + step < units) stage_angles(a, angles + (buf ^ 1) * kTokens * 64, unit + step, tokens);
+        if (few) copies_commit();
+        for (; work.unit == unit && work.h < H;) {
+            fetch((slot + kDepth - 1) % kDepth);     // also takes along the next unit's angles
+            copies_wait<kDepth - 1>();
+            __syncwarp();
+            int hi, Hs;
+            T *out = kind_of(Q, K, V, a.Hq, a.Hk, a.Hv, work.h, hi, Hs);
+            const bool isq = work.h < a.Hq, isn = work.h < Hn, norm = (isq ? a.wq : a.wk) != nullptr;
+            float2 w[4];
+            weights(sw[isq ? 0 : 1], a0, a1, w);
 #pragma unroll
-        for (int i = 0; i < kSteps; ++i) {
-            const int g = g0 + i, h = 4 * g + grp;
-            if (g >= end) break;
-            if (4 * g < Hn) {   // some head of the group is a query or a key
-                float2 x[4];
-                raw[i].get(x);
-                const bool isq = h < a.Hq;
-                const float r = (isq ? a.wq : a.wk) ? rsqrtf(sum8(squares(x)) * (1.f / 64.f) + a.eps) : 1.f;
-                float2 w[4];
-                weights(sw[isq ? 0 : 1], a0, a1, w);
+            for (int s = 0; s < kSteps; ++s) {
+                Eight<T> raw;
+                raw.load(ring + (slot * 8 + 4 * s + grp) * 64, a0, a1);
+                if (isn) {
+                    float2 x[4];
+                    raw.get(x);
+                    const float r = norm ? rsqrtf(sum8(squares(x)) * (1.f / 64.f) + a.eps) : 1.f;
 #pragma unroll
-                for (int e = 0; e < 4; ++e) x[e] = mul2(x[e], mul2(w[e], make_float2(r, r)));
-                turn.template apply<false>(x);
-                if (h < Hn) raw[i].put(x);
+                    for (int e = 0; e < 4; ++e) x[e] = mul2(x[e], mul2(w[e], make_float2(r, r)));
+                    if (a.rot) {
+                        Turn<PAIRS_INSIDE> turn;
+                        turn.load(angles + (buf * kTokens + (warp & 1) * 8 + 4 * s + grp) * 64, a.rot, sub);
+                        turn.template apply<false>(x);
+                    }
+                    raw.put(x);
+                }
+                if (here.in[s]) raw.store(out + here.dense(s, hi, Hs, a.N), a0, a1);
             }
-            if (h < H) raw[i].store(to.row(h, a.Hq, Hn, a.N), a0, a1);
+            __syncwarp();
+            slot = (slot + 1) % kDepth;
+            work.next(H, first, step);
         }
-#pragma unroll
-        for (int i = 0; i < kSteps; ++i) raw[i] = ahead[i];
+        if (work.unit == unit) work.unit += step;    // a warp without heads
     }
+    copies_wait<0>();
 }
 
 template <typename T, bool PAIRS_INSIDE>
 __global__ void __launch_bounds__(kWarps * 32, 2)
 qk_norm_bwd_kernel(const __grid_constant__ NormArgs<T> a, const T *__restrict__ X, int64_t x_sb, int64_t x_sn,
                    const T *__restrict__ dQ, const T *__restrict__ dK, const T *__restrict__ dV, T *__restrict__ dX,
-                   int64_t dx_sb, int64_t dx_sn, float *__restrict__ partial, int64_t units, int chunks) {
+                   int64_t dx_sb, int64_t dx_sn, float *__restrict__ partial, unsigned tokens, unsigned units) {
+    extern __shared__ float4 smem4[];
     __shared__ __align__(16) float sw[2][64];
     __shared__ float part[kWarps][128];
-    grid_dep_wait();
-    grid_dep_launch();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = lane & 7, grp = lane >> 3;
-    const int Hn = a.Hq + a.Hk, H = Hn + a.Hv;
+    float *angles = reinterpret_cast<float *>(smem4);
+    T *ring = reinterpret_cast<T *>(angles + 2 * kTokens * 64) + (size_t)warp * kDepth * 2 * 8 * 64;
+    const int Hn = a.Hq + a.Hk, H = Hn + a.Hv, first = warp >> 1;
+    const unsigned step = gridDim.x;
+    const bool few = H < 4 * kDepth;     // a warp may have fewer heads than its ring
     int a0, a1;
     lane_dims<PAIRS_INSIDE>(a.rot, sub, a0, a1);
+    grid_dep_wait();
+    grid_dep_launch();
+
+    Tokens ahead, here;
+    Place load(blockIdx.x, first), work(blockIdx.x, first);
+    // the next (unit, head): its rows of X (not those of values) and of the gradient
+    const auto fetch = [&](int slot) {
+        if (load.unit < units && load.h < H) {
+            int hi, Hs;
+            const T *src = kind_of(dQ, dK, dV, a.Hq, a.Hk, a.Hv, load.h, hi, Hs);
+#pragma unroll
+            for (int s = 0; s < kSteps; ++s)
+                if (ahead.in[s]) {
+                    T *dst = ring + (slot * 16 + 4 * s + grp) * 64;
+                    if (load.h < Hn) copy_row(dst, X + ahead.packed(s, load.h, x_sb, x_sn));
+                    copy_row(dst + 8 * 64, src + ahead.dense(s, hi, Hs, a.N));
+                }
+            if (load.next(H, first, step)) ahead.set(load.unit, tokens, a.N);
+        }
+        copies_commit();
+    };
+    if (a.rot) stage_angles(a, angles, blockIdx.x, tokens);
+    copies_commit();
+    ahead.set(blockIdx.x, tokens, a.N);
+#pragma unroll
+    for (int i = 0; i < kDepth - 1; ++i) fetch(i);
+    stage_weights(a, sw);
     float2 dwq[4], dwk[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e) dwq[e] = dwk[e] = make_float2(0.f, 0.f);
-    Walk t((int64_t)blockIdx.x * kWarps + warp, units, (int64_t)gridDim.x * kWarps, a.N, chunks, (H + 3) / 4);
-    Eight<T> raw[kSteps], grad[kSteps], raw_ahead[kSteps], grad_ahead[kSteps];
-    const auto load = [&](Eight<T> (&r)[kSteps], Eight<T> (&d)[kSteps]) {
-        const T *row = X + t.b * x_sb + t.n * x_sn;
-        HeadRows<const T> from;
-        from.token(dQ, dK, dV, a.Hq, a.Hk, a.Hv, t.b, t.n, a.N);
+
+    int slot = 0;
+    for (int buf = 0; work.unit < units; buf ^= 1) {
+        const unsigned unit = work.unit;
+        here.set(unit, tokens, a.N);
+        if (few) copies_wait<0>();
+        else copies_wait<kDepth - 1>();
+        __syncthreads();
+        if (a.rot && unit + step < units) stage_angles(a, angles + (buf ^ 1) * kTokens * 64, unit + step, tokens);
+        if (few) copies_commit();
+        for (; work.unit == unit && work.h < H;) {
+            fetch((slot + kDepth - 1) % kDepth);
+            copies_wait<kDepth - 1>();
+            __syncwarp();
+            const bool isq = work.h < a.Hq, isn = work.h < Hn, norm = (isq ? a.wq : a.wk) != nullptr;
+            float2 w[4];
+            weights(sw[isq ? 0 : 1], a0, a1, w);
 #pragma unroll
-        for (int i = 0; i < kSteps; ++i) {
-            const int h = 4 * (t.g + i) + grp;
-            r[i].zero();
-            d[i].zero();
-            if (t.g + i < t.end && h < H) {
-                if (h < Hn) r[i].load(row + h * 64, a0, a1);
-                d[i].load(from.row(h, a.Hq, Hn, a.N), a0, a1);
-            }
-        }
-    };
-    if (t.left()) load(raw, grad);
-    stage_weights(a, sw);
-    Turn<PAIRS_INSIDE> turn;
-    while (t.left()) {
-        if (t.first) turn.load(a, t.b, t.n, sub);
-        T *drow = dX + t.b * dx_sb + t.n * dx_sn;
-        const int g0 = t.g, end = t.end;
-        t.next();
-        if (t.left()) load(raw_ahead, grad_ahead);
-#pragma unroll
-        for (int i = 0; i < kSteps; ++i) {
-            const int g = g0 + i, h = 4 * g + grp;
-            if (g >= end) break;
-            if (4 * g < Hn) {
-                float2 x[4], dy[4], w[4];
-                raw[i].get(x);
-                grad[i].get(dy);
-                const bool isq = h < a.Hq, isk = !isq && h < Hn;
-                turn.template apply<true>(dy);
-                const bool norm = (isq ? a.wq : a.wk) != nullptr;
-                const float r = norm ? rsqrtf(sum8(squares(x)) * (1.f / 64.f) + a.eps) : 1.f;
-                weights(sw[isq ? 0 : 1], a0, a1, w);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) x[e] = mul2(x[e], make_float2(r, r));
-                if (4 * g + 4 <= a.Hq) {            // four queries
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) dwq[e] = fma2(dy[e], x[e], dwq[e]);
-                } else if (4 * g >= a.Hq && 4 * g + 4 <= Hn) {     // four keys
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) dwk[e] = fma2(dy[e], x[e], dwk[e]);
-                } else {
-                    // selected, not multiplied by 0: another kind's NaN stays out
+            for (int s = 0; s < kSteps; ++s) {
+                const T *src = ring + (slot * 16 + 4 * s + grp) * 64;
+                Eight<T> grad;
+                grad.load(src + 8 * 64, a0, a1);
+                if (isn) {
+                    Eight<T> raw;
+                    raw.load(src, a0, a1);
+                    float2 x[4], dy[4];
+                    raw.get(x);
+                    grad.get(dy);
+                    if (a.rot) {
+                        Turn<PAIRS_INSIDE> turn;
+                        turn.load(angles + (buf * kTokens + (warp & 1) * 8 + 4 * s + grp) * 64, a.rot, sub);
+                        turn.template apply<true>(dy);
+                    }
+                    const float r = norm ? rsqrtf(sum8(squares(x)) * (1.f / 64.f) + a.eps) : 1.f;
+                    float2 dot = make_float2(0.f, 0.f);
+                    const bool in = here.in[s];      // the slot of no token holds anything: its sums are left out
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        const float2 d = mul2(dy[e], x[e]);
-                        dwq[e] = add2(dwq[e], make_float2(isq ? d.x : 0.f, isq ? d.y : 0.f));
-                        dwk[e] = add2(dwk[e], make_float2(isk ? d.x : 0.f, isk ? d.y : 0.f));
+                        x[e] = mul2(x[e], make_float2(r, r));
+                        if (in && isq) dwq[e] = fma2(dy[e], x[e], dwq[e]);
+                        else if (in) dwk[e] = fma2(dy[e], x[e], dwk[e]);
+                        dy[e] = mul2(dy[e], w[e]);
+                        dot = fma2(dy[e], x[e], dot);
                     }
-                }
-                float2 dot = make_float2(0.f, 0.f);
+                    const float m = sum8(dot.x + dot.y) * (norm ? -1.f / 64.f : 0.f);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    dy[e] = mul2(dy[e], w[e]);
-                    dot = fma2(dy[e], x[e], dot);
+                    for (int e = 0; e < 4; ++e) dy[e] = mul2(make_float2(r, r), fma2(x[e], make_float2(m, m), dy[e]));
+                    grad.put(dy);
                 }
-                const float m = sum8(dot.x + dot.y) * (norm ? -1.f / 64.f : 0.f);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) dy[e] = mul2(make_float2(r, r), fma2(x[e], make_float2(m, m), dy[e]));
-                if (h < Hn) grad[i].put(dy);
+                if (here.in[s]) grad.store(dX + here.packed(s, work.h, dx_sb, dx_sn), a0, a1);
             }
-            if (h < H) grad[i].store(drow + h * 64, a0, a1);
+            __syncwarp();
+            slot = (slot + 1) % kDepth;
+            work.next(H, first, step);
         }
-#pragma unroll
-        for (int i = 0; i < kSteps; ++i) {
-            raw[i] = raw_ahead[i];
-            grad[i] = grad_ahead[i];
-        }
+        if (work.unit == unit) work.unit += step;    // a warp without heads
     }
+    copies_wait<0>();
     // the block's sums: over the four heads of a warp, then over its warps
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
@@ -427,32 +518,22 @@ __global__ void __launch_bounds__(1024) qk_norm_dw_kernel(const float *__restric
     if (out) out[c & 63] = (T)s;
 }
 
-// One wave of blocks, each warp walking over its tokens: the next groups are
-// loaded while these are worked on.  Fewer tokens than warps: a token's
-// groups are cut into chunks of at least kSteps.
+// One wave of blocks, each walking over its units.
 template <auto Kernel>
-int resident_blocks() {
+cudaError_t resident_blocks(size_t smem, int64_t units, unsigned *blocks) {
+    cudaError_t e = prepare_kernel<Kernel>(smem, 0);
+    if (e != cudaSuccess) return e;
     static std::atomic<int> per_sm{0};
     int n = per_sm.load(std::memory_order_relaxed);
     if (n == 0) {
-        if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, Kernel, kWarps * 32, 0) != cudaSuccess || n < 1) n = 1;
+        e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, Kernel, kWarps * 32, smem);
+        if (e != cudaSuccess) return e;
+        n = std::max(n, 1);
         per_sm.store(n, std::memory_order_relaxed);
     }
-    return std::min(kMaxBlocks, n * sm_count());
+    *blocks = (unsigned)std::min<int64_t>(units, std::min(kMaxBlocks, n * sm_count()));
+    return cudaSuccess;
 }
-
-struct Grid {
-    int chunks;
-    int64_t units;
-    unsigned blocks;
-    Grid(const QkNormArgs &q, int resident) {
-        const int groups = (q.Hq + q.Hk + q.Hv + 3) / 4, most = (groups + kSteps - 1) / kSteps;
-        const int64_t tokens = (int64_t)q.B * q.N, warps = (int64_t)resident * kWarps;
-        chunks = (int)std::min<int64_t>(most, std::max<int64_t>(1, (warps + tokens - 1) / tokens));
-        units = tokens * chunks;
-        blocks = (unsigned)std::min<int64_t>((units + kWarps - 1) / kWarps, resident);
-    }
-};
 
 template <typename T>
 NormArgs<T> norm_args(const QkNormArgs &q) {
@@ -462,28 +543,34 @@ NormArgs<T> norm_args(const QkNormArgs &q) {
 
 template <typename T, bool PAIRS_INSIDE>
 cudaError_t fwd(const QkNormArgs &q) {
-    const Grid g(q, resident_blocks<qk_norm_fwd_kernel<T, PAIRS_INSIDE>>());
-    const cudaError_t e = launch_kernel(qk_norm_fwd_kernel<T, PAIRS_INSIDE>, dim3(g.blocks), dim3(kWarps * 32), 0,
-                                        q.stream, pdl_enabled(), norm_args<T>(q), static_cast<const T *>(q.X), q.x_sb,
-                                        q.x_sn, static_cast<T *>(q.Q), static_cast<T *>(q.K), static_cast<T *>(q.V),
-                                        g.units, g.chunks);
+    constexpr size_t smem = ring_bytes<T, 1>();
+    const unsigned tokens = (unsigned)q.B * (unsigned)q.N, units = (tokens + kTokens - 1) / kTokens;
+    unsigned blocks = 0;
+    cudaError_t e = resident_blocks<qk_norm_fwd_kernel<T, PAIRS_INSIDE>>(smem, units, &blocks);
+    if (e != cudaSuccess) return e;
+    e = launch_kernel(qk_norm_fwd_kernel<T, PAIRS_INSIDE>, dim3(blocks), dim3(kWarps * 32), smem, q.stream,
+                      pdl_enabled(), norm_args<T>(q), static_cast<const T *>(q.X), q.x_sb, q.x_sn,
+                      static_cast<T *>(q.Q), static_cast<T *>(q.K), static_cast<T *>(q.V), tokens, units);
     if (e == cudaSuccess) count_launches(1);
     return e;
 }
 
 template <typename T, bool PAIRS_INSIDE>
 cudaError_t bwd(const QkNormArgs &q) {
-    const Grid g(q, resident_blocks<qk_norm_bwd_kernel<T, PAIRS_INSIDE>>());
-    cudaError_t e = launch_kernel(qk_norm_bwd_kernel<T, PAIRS_INSIDE>, dim3(g.blocks), dim3(kWarps * 32), 0, q.stream,
-                                  pdl_enabled(), norm_args<T>(q), static_cast<const T *>(q.X), q.x_sb, q.x_sn,
-                                  static_cast<const T *>(q.dQ), static_cast<const T *>(q.dK),
-                                  static_cast<const T *>(q.dV), static_cast<T *>(q.dX), q.dx_sb, q.dx_sn, q.ws, g.units,
-                                  g.chunks);
+    constexpr size_t smem = ring_bytes<T, 2>();
+    const unsigned tokens = (unsigned)q.B * (unsigned)q.N, units = (tokens + kTokens - 1) / kTokens;
+    unsigned blocks = 0;
+    cudaError_t e = resident_blocks<qk_norm_bwd_kernel<T, PAIRS_INSIDE>>(smem, units, &blocks);
+    if (e != cudaSuccess) return e;
+    e = launch_kernel(qk_norm_bwd_kernel<T, PAIRS_INSIDE>, dim3(blocks), dim3(kWarps * 32), smem, q.stream,
+                      pdl_enabled(), norm_args<T>(q), static_cast<const T *>(q.X), q.x_sb, q.x_sn,
+                      static_cast<const T *>(q.dQ), static_cast<const T *>(q.dK), static_cast<const T *>(q.dV),
+                      static_cast<T *>(q.dX), q.dx_sb, q.dx_sn, q.ws, tokens, units);
     if (e != cudaSuccess) return e;
     count_launches(1);
     if (!q.dwq && !q.dwk) return cudaSuccess;
     e = launch_kernel(qk_norm_dw_kernel<T>, dim3(1), dim3(1024), 0, q.stream, pdl_enabled(),
-                      static_cast<const float *>(q.ws), (int)g.blocks, static_cast<T *>(q.dwq),
+                      static_cast<const float *>(q.ws), (int)blocks, static_cast<T *>(q.dwq),
                       static_cast<T *>(q.dwk));
     if (e == cudaSuccess) count_launches(1);
     return e;

@@ -117,7 +117,7 @@ def test_qk_norm_refusals(bwd, _no_launch):
                dict(sin=None), dict(cos=P + 4), dict(table_len=8), dict(table_len=0, positions=P),
                dict(positions=P + 2), dict(positions=P, positions_stride_b=-1), dict(q_weight=P + 2),
                dict(x=None), dict(x=P + 8), dict(sn=8 * 64 + 4), dict(sb=-64), dict(q=None), dict(k=None), dict(v=None),
-               dict(q=P + 8)):
+               dict(q=P + 8), dict(B=1 << 16, N=1 << 15, positions=P)):
         assert st(**kw) == INVALID, kw
     assert st(D=32) == UNSUPPORTED
     assert st(dtype=9) == UNSUPPORTED
