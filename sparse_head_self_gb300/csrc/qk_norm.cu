@@ -13,13 +13,13 @@
 // Both directions only move data: they read and write each element once, and
 // with 16-bit elements the instructions a head takes cost about as much as its
 // bytes.  A block takes 16 consecutive tokens at a time (over the sequences'
-// ends: a token's rows are found once), its warps eight of them and every
-// fourth head, so that a warp's head is of one kind.  Eight lanes share a
+// ends: a token's rows are found once) and some or all heads, its warps eight of the
+// tokens and every fourth head, so that a warp's head is of one kind.  Eight lanes share a
 // head row; a lane has two runs of four dims, chosen so that both values of
 // every rotated pair are its own (halves: dims 4 i.. and rot / 2 + 4 i..),
 // which leaves the two sums over a head as the only exchange; the arithmetic
 // is on packed pairs of floats.  Rows arrive by asynchronous copies in a ring of
-// each warp's own, kDepth heads ahead and over the units' ends, without holding
+// each warp's own, kDepth heads ahead and over the items' ends, without holding
 // registers; the tokens' angles are brought into shared memory once for all heads.
 // Every head row is a whole 128- or 256-byte segment, so all traffic is full
 // sectors.  The values' heads are copied unconverted.
@@ -268,70 +268,78 @@ constexpr size_t ring_bytes() {
     return 2 * kTokens * 64 * sizeof(float) + (size_t)kWarps * kDepth * RT * 8 * 64 * sizeof(T);
 }
 
-// Where a warp is in its sequence of (unit, head) pairs.
+// Where a warp is in its sequence of heads: an item is a unit's tokens and one of
+// `chunks` parts of the heads, [lo, hi).
 struct Place {
-    unsigned unit;
-    int h;
-    __device__ __forceinline__ Place(unsigned unit, int h) : unit(unit), h(h) {}
-    // the next pair; true when the unit changed
-    __device__ __forceinline__ bool next(int H, int first, unsigned step) {
+    unsigned item, unit;
+    int h, lo, hi;
+    __device__ __forceinline__ Place(int H, int chunks) { enter(blockIdx.x, H, chunks); }
+    __device__ __forceinline__ void enter(unsigned i, int H, int chunks) {
+        item = i;
+        unit = i / (unsigned)chunks;
+        const int c = (int)(i - unit * chunks);
+        lo = H * c / chunks;
+        hi = H * (c + 1) / chunks;
+        h = lo + (threadIdx.x >> 6);
+    }
+    // the next head; true when the item changed
+    __device__ __forceinline__ bool next(int H, int chunks) {
         h += kWarps / 2;
-        if (h < H) return false;
-        h = first;
-        unit += step;
+        if (h < hi) return false;
+        enter(item + gridDim.x, H, chunks);
         return true;
     }
 };
 
-template <typename T, bool PAIRS_INSIDE>
-__global__ void __launch_bounds__(kWarps * 32, sizeof(T) == 2 ? 4 : 3)
+// CUT: the heads are cut into `cuts` chunks; else cuts is not looked at.
+template <typename T, bool PAIRS_INSIDE, bool CUT>
+__global__ void __launch_bounds__(kWarps * 32, 3)
 qk_norm_fwd_kernel(const __grid_constant__ NormArgs<T> a, const T *__restrict__ X, int64_t x_sb, int64_t x_sn,
-                   T *__restrict__ Q, T *__restrict__ K, T *__restrict__ V, unsigned tokens, unsigned units) {
+                   T *__restrict__ Q, T *__restrict__ K, T *__restrict__ V, unsigned tokens, unsigned items, int cuts) {
     extern __shared__ float4 smem4[];
     __shared__ __align__(16) float sw[2][64];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = lane & 7, grp = lane >> 3;
     float *angles = reinterpret_cast<float *>(smem4);
     T *ring = reinterpret_cast<T *>(angles + 2 * kTokens * 64) + (size_t)warp * kDepth * 8 * 64;
-    const int Hn = a.Hq + a.Hk, H = Hn + a.Hv, first = warp >> 1;
-    const unsigned step = gridDim.x;
-    const bool few = H < 4 * kDepth;     // a warp may have fewer heads than its ring
+    const int Hn = a.Hq + a.Hk, H = Hn + a.Hv, chunks = CUT ? cuts : 1;
+    const bool few = H / chunks < 4 * kDepth;     // a warp may have fewer heads of an item than its ring holds
     int a0, a1;
     lane_dims<PAIRS_INSIDE>(a.rot, sub, a0, a1);
     grid_dep_wait();
     grid_dep_launch();
 
     Tokens ahead, here;
-    Place load(blockIdx.x, first), work(blockIdx.x, first);
+    Place load(H, chunks), work(H, chunks);
     // copies of the next (unit, head) into slot `slot`; one group each, empty at the end
     const auto fetch = [&](int slot) {
-        if (load.unit < units && load.h < H) {
+        if (load.item < items && load.h < load.hi) {
 #pragma unroll
             for (int s = 0; s < kSteps; ++s)
                 if (ahead.in[s])
                     copy_row(ring + (slot * 8 + 4 * s + grp) * 64, X + ahead.packed(s, load.h, x_sb, x_sn));
-            if (load.next(H, first, step)) ahead.set(load.unit, tokens, a.N);
+            if (load.next(H, chunks)) ahead.set(load.unit, tokens, a.N);
         }
         copies_commit();
     };
-    if (a.rot) stage_angles(a, angles, blockIdx.x, tokens);
+    if (a.rot) stage_angles(a, angles, work.unit, tokens);
     copies_commit();
-    ahead.set(blockIdx.x, tokens, a.N);
+    ahead.set(work.unit, tokens, a.N);
 #pragma unroll
     for (int i = 0; i < kDepth - 1; ++i) fetch(i);
     stage_weights(a, sw);
 
     int slot = 0;
-    for (int buf = 0; work.unit < units; buf ^= 1) {
-        const unsigned unit = work.unit;
-        here.set(unit, tokens, a.N);
+    for (int buf = 0; work.item < items; buf ^= 1) {
+        const unsigned item = work.item, after = item + gridDim.x;
+        here.set(work.unit, tokens, a.N);
         // this unit's angles: the oldest group at the start; later they were asked for
         // with the first head of the unit before, at least kDepth groups ago
         if (few) copies_wait<0>();
         else copies_wait<kDepth - 1>();
         __syncthreads();
-        if (a.rot && unit + step < units) stage_angles(a, angles + (buf ^ 1) * kTokens * 64, unit + step, tokens);
+        if (a.rot && after < items) stage_angles(a, angles + (buf ^ 1) * kTokens * 64, after / (unsigned)chunks, tokens);
         if (few) copies_commit();
-        for (; work.unit == unit && work.h < H;) {
+        while (work.item == item && work.h < work.hi) {
             fetch((slot + kDepth - 1) % kDepth);     // also takes along the next unit's angles
             copies_wait<kDepth - 1>();
             __syncwarp();
@@ -361,37 +369,36 @@ qk_norm_fwd_kernel(const __grid_constant__ NormArgs<T> a, const T *__restrict__ 
             }
             __syncwarp();
             slot = (slot + 1) % kDepth;
-            work.next(H, first, step);
+            work.next(H, chunks);
         }
-        if (work.unit == unit) work.unit += step;    // a warp without heads
+        if (work.item == item) work.enter(after, H, chunks);    // a warp without heads
     }
     copies_wait<0>();
 }
 
-template <typename T, bool PAIRS_INSIDE>
+template <typename T, bool PAIRS_INSIDE, bool CUT>
 __global__ void __launch_bounds__(kWarps * 32, 2)
 qk_norm_bwd_kernel(const __grid_constant__ NormArgs<T> a, const T *__restrict__ X, int64_t x_sb, int64_t x_sn,
                    const T *__restrict__ dQ, const T *__restrict__ dK, const T *__restrict__ dV, T *__restrict__ dX,
-                   int64_t dx_sb, int64_t dx_sn, float *__restrict__ partial, unsigned tokens, unsigned units) {
+                   int64_t dx_sb, int64_t dx_sn, float *__restrict__ partial, unsigned tokens, unsigned items, int cuts) {
     extern __shared__ float4 smem4[];
     __shared__ __align__(16) float sw[2][64];
     __shared__ float part[kWarps][128];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = lane & 7, grp = lane >> 3;
     float *angles = reinterpret_cast<float *>(smem4);
     T *ring = reinterpret_cast<T *>(angles + 2 * kTokens * 64) + (size_t)warp * kDepth * 2 * 8 * 64;
-    const int Hn = a.Hq + a.Hk, H = Hn + a.Hv, first = warp >> 1;
-    const unsigned step = gridDim.x;
-    const bool few = H < 4 * kDepth;     // a warp may have fewer heads than its ring
+    const int Hn = a.Hq + a.Hk, H = Hn + a.Hv, chunks = CUT ? cuts : 1;
+    const bool few = H / chunks < 4 * kDepth;     // a warp may have fewer heads of an item than its ring holds
     int a0, a1;
     lane_dims<PAIRS_INSIDE>(a.rot, sub, a0, a1);
     grid_dep_wait();
     grid_dep_launch();
 
     Tokens ahead, here;
-    Place load(blockIdx.x, first), work(blockIdx.x, first);
+    Place load(H, chunks), work(H, chunks);
     // the next (unit, head): its rows of X (not those of values) and of the gradient
     const auto fetch = [&](int slot) {
-        if (load.unit < units && load.h < H) {
+        if (load.item < items && load.h < load.hi) {
             int hi, Hs;
             const T *src = kind_of(dQ, dK, dV, a.Hq, a.Hk, a.Hv, load.h, hi, Hs);
 #pragma unroll
@@ -401,13 +408,13 @@ qk_norm_bwd_kernel(const __grid_constant__ NormArgs<T> a, const T *__restrict__ 
                     if (load.h < Hn) copy_row(dst, X + ahead.packed(s, load.h, x_sb, x_sn));
                     copy_row(dst + 8 * 64, src + ahead.dense(s, hi, Hs, a.N));
                 }
-            if (load.next(H, first, step)) ahead.set(load.unit, tokens, a.N);
+            if (load.next(H, chunks)) ahead.set(load.unit, tokens, a.N);
         }
         copies_commit();
     };
-    if (a.rot) stage_angles(a, angles, blockIdx.x, tokens);
+    if (a.rot) stage_angles(a, angles, work.unit, tokens);
     copies_commit();
-    ahead.set(blockIdx.x, tokens, a.N);
+    ahead.set(work.unit, tokens, a.N);
 #pragma unroll
     for (int i = 0; i < kDepth - 1; ++i) fetch(i);
     stage_weights(a, sw);
@@ -416,15 +423,15 @@ qk_norm_bwd_kernel(const __grid_constant__ NormArgs<T> a, const T *__restrict__ 
     for (int e = 0; e < 4; ++e) dwq[e] = dwk[e] = make_float2(0.f, 0.f);
 
     int slot = 0;
-    for (int buf = 0; work.unit < units; buf ^= 1) {
-        const unsigned unit = work.unit;
-        here.set(unit, tokens, a.N);
+    for (int buf = 0; work.item < items; buf ^= 1) {
+        const unsigned item = work.item, after = item + gridDim.x;
+        here.set(work.unit, tokens, a.N);
         if (few) copies_wait<0>();
         else copies_wait<kDepth - 1>();
         __syncthreads();
-        if (a.rot && unit + step < units) stage_angles(a, angles + (buf ^ 1) * kTokens * 64, unit + step, tokens);
+        if (a.rot && after < items) stage_angles(a, angles + (buf ^ 1) * kTokens * 64, after / (unsigned)chunks, tokens);
         if (few) copies_commit();
-        for (; work.unit == unit && work.h < H;) {
+        while (work.item == item && work.h < work.hi) {
             fetch((slot + kDepth - 1) % kDepth);
             copies_wait<kDepth - 1>();
             __syncwarp();
@@ -467,9 +474,9 @@ qk_norm_bwd_kernel(const __grid_constant__ NormArgs<T> a, const T *__restrict__ 
             }
             __syncwarp();
             slot = (slot + 1) % kDepth;
-            work.next(H, first, step);
+            work.next(H, chunks);
         }
-        if (work.unit == unit) work.unit += step;    // a warp without heads
+        if (work.item == item) work.enter(after, H, chunks);    // a warp without heads
     }
     copies_wait<0>();
     // the block's sums: over the four heads of a warp, then over its warps
@@ -518,9 +525,17 @@ __global__ void __launch_bounds__(1024) qk_norm_dw_kernel(const float *__restric
     if (out) out[c & 63] = (T)s;
 }
 
-// One wave of blocks, each walking over its units.
+// The launch of `Kernel`: one wave of blocks, each walking over its items.  With
+// fewer units than blocks the heads are cut into chunks, of four at least (one
+// token of eight sequences, 24 heads: 5.9 -> 3.0 us); with more they are not,
+// since a warp's ring drains at an item's end when the item is shorter than the
+// ring (ViT-B, B=64, in chunks of eight heads: 36 us instead of 27).
+struct Launch {
+    unsigned tokens, items, blocks;
+    int chunks;
+};
 template <auto Kernel>
-cudaError_t resident_blocks(size_t smem, int64_t units, unsigned *blocks) {
+cudaError_t plan(const QkNormArgs &q, size_t smem, Launch *l) {
     cudaError_t e = prepare_kernel<Kernel>(smem, 0);
     if (e != cudaSuccess) return e;
     static std::atomic<int> per_sm{0};
@@ -531,7 +546,13 @@ cudaError_t resident_blocks(size_t smem, int64_t units, unsigned *blocks) {
         n = std::max(n, 1);
         per_sm.store(n, std::memory_order_relaxed);
     }
-    *blocks = (unsigned)std::min<int64_t>(units, std::min(kMaxBlocks, n * sm_count()));
+    const int64_t resident = std::min(kMaxBlocks, n * sm_count());
+    const int H = q.Hq + q.Hk + q.Hv;
+    l->tokens = (unsigned)q.B * (unsigned)q.N;
+    const int64_t units = ((int64_t)l->tokens + kTokens - 1) / kTokens;
+    l->chunks = units < resident ? (int)std::min<int64_t>(std::max(1, H / 4), (resident + units - 1) / units) : 1;
+    l->items = (unsigned)(units * l->chunks);
+    l->blocks = (unsigned)std::min<int64_t>(l->items, resident);
     return cudaSuccess;
 }
 
@@ -541,36 +562,36 @@ NormArgs<T> norm_args(const QkNormArgs &q) {
                        q.rot, q.cos, q.sin, q.P,  q.pos,                        q.pos_sb};
 }
 
-template <typename T, bool PAIRS_INSIDE>
+template <typename T, bool PAIRS_INSIDE, bool CUT>
 cudaError_t fwd(const QkNormArgs &q) {
     constexpr size_t smem = ring_bytes<T, 1>();
-    const unsigned tokens = (unsigned)q.B * (unsigned)q.N, units = (tokens + kTokens - 1) / kTokens;
-    unsigned blocks = 0;
-    cudaError_t e = resident_blocks<qk_norm_fwd_kernel<T, PAIRS_INSIDE>>(smem, units, &blocks);
+    Launch l;
+    cudaError_t e = plan<qk_norm_fwd_kernel<T, PAIRS_INSIDE, CUT>>(q, smem, &l);
     if (e != cudaSuccess) return e;
-    e = launch_kernel(qk_norm_fwd_kernel<T, PAIRS_INSIDE>, dim3(blocks), dim3(kWarps * 32), smem, q.stream,
+    if (!CUT && l.chunks > 1) return fwd<T, PAIRS_INSIDE, true>(q);
+    e = launch_kernel(qk_norm_fwd_kernel<T, PAIRS_INSIDE, CUT>, dim3(l.blocks), dim3(kWarps * 32), smem, q.stream,
                       pdl_enabled(), norm_args<T>(q), static_cast<const T *>(q.X), q.x_sb, q.x_sn,
-                      static_cast<T *>(q.Q), static_cast<T *>(q.K), static_cast<T *>(q.V), tokens, units);
+                      static_cast<T *>(q.Q), static_cast<T *>(q.K), static_cast<T *>(q.V), l.tokens, l.items, l.chunks);
     if (e == cudaSuccess) count_launches(1);
     return e;
 }
 
-template <typename T, bool PAIRS_INSIDE>
+template <typename T, bool PAIRS_INSIDE, bool CUT>
 cudaError_t bwd(const QkNormArgs &q) {
     constexpr size_t smem = ring_bytes<T, 2>();
-    const unsigned tokens = (unsigned)q.B * (unsigned)q.N, units = (tokens + kTokens - 1) / kTokens;
-    unsigned blocks = 0;
-    cudaError_t e = resident_blocks<qk_norm_bwd_kernel<T, PAIRS_INSIDE>>(smem, units, &blocks);
+    Launch l;
+    cudaError_t e = plan<qk_norm_bwd_kernel<T, PAIRS_INSIDE, CUT>>(q, smem, &l);
     if (e != cudaSuccess) return e;
-    e = launch_kernel(qk_norm_bwd_kernel<T, PAIRS_INSIDE>, dim3(blocks), dim3(kWarps * 32), smem, q.stream,
+    if (!CUT && l.chunks > 1) return bwd<T, PAIRS_INSIDE, true>(q);
+    e = launch_kernel(qk_norm_bwd_kernel<T, PAIRS_INSIDE, CUT>, dim3(l.blocks), dim3(kWarps * 32), smem, q.stream,
                       pdl_enabled(), norm_args<T>(q), static_cast<const T *>(q.X), q.x_sb, q.x_sn,
                       static_cast<const T *>(q.dQ), static_cast<const T *>(q.dK), static_cast<const T *>(q.dV),
-                      static_cast<T *>(q.dX), q.dx_sb, q.dx_sn, q.ws, tokens, units);
+                      static_cast<T *>(q.dX), q.dx_sb, q.dx_sn, q.ws, l.tokens, l.items, l.chunks);
     if (e != cudaSuccess) return e;
     count_launches(1);
     if (!q.dwq && !q.dwk) return cudaSuccess;
     e = launch_kernel(qk_norm_dw_kernel<T>, dim3(1), dim3(1024), 0, q.stream, pdl_enabled(),
-                      static_cast<const float *>(q.ws), (int)blocks, static_cast<T *>(q.dwq),
+                      static_cast<const float *>(q.ws), (int)l.blocks, static_cast<T *>(q.dwq),
                       static_cast<T *>(q.dwk));
     if (e == cudaSuccess) count_launches(1);
     return e;
@@ -581,12 +602,12 @@ cudaError_t bwd(const QkNormArgs &q) {
 size_t qk_norm_bwd_workspace() { return (size_t)kMaxBlocks * 128 * sizeof(float); }
 
 cudaError_t launch_qk_norm_fwd(const QkNormArgs &q) {
-    if (q.interleaved) return q.dtype == FIBATT_F32 ? fwd<float, true>(q) : fwd<__nv_bfloat16, true>(q);
-    return q.dtype == FIBATT_F32 ? fwd<float, false>(q) : fwd<__nv_bfloat16, false>(q);
+    if (q.interleaved) return q.dtype == FIBATT_F32 ? fwd<float, true, false>(q) : fwd<__nv_bfloat16, true, false>(q);
+    return q.dtype == FIBATT_F32 ? fwd<float, false, false>(q) : fwd<__nv_bfloat16, false, false>(q);
 }
 cudaError_t launch_qk_norm_bwd(const QkNormArgs &q) {
-    if (q.interleaved) return q.dtype == FIBATT_F32 ? bwd<float, true>(q) : bwd<__nv_bfloat16, true>(q);
-    return q.dtype == FIBATT_F32 ? bwd<float, false>(q) : bwd<__nv_bfloat16, false>(q);
+    if (q.interleaved) return q.dtype == FIBATT_F32 ? bwd<float, true, false>(q) : bwd<__nv_bfloat16, true, false>(q);
+    return q.dtype == FIBATT_F32 ? bwd<float, false, false>(q) : bwd<__nv_bfloat16, false, false>(q);
 }
 
 FIBATT_DEFINE_ERROR_READER(read_error_qk_norm, "qk_norm.cu")
