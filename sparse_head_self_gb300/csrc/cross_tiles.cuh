@@ -52,8 +52,10 @@ struct TensorArg {
     CUtensorMap map;
     int head_step, seq_step;   // 1, or 0 where the dimension is broadcast
 };
-// Boxes of `rows` rows by `heads` heads; false when the map cannot be made.
-bool make_tensor(TensorArg *t, const fibatt_heads &v, int B, int H, int N, int rows, int heads);
+// Boxes of `rows` rows by `heads` heads, which arrive with the 128-byte swizzle
+// (bf16) or as they are; false when the map cannot be made.
+bool make_tensor(TensorArg *t, const fibatt_heads &v, int B, int H, int N, int rows, int heads,
+                 fibatt_dtype dtype = FIBATT_BF16, bool swizzle = true);
 
 #ifdef __CUDACC__
 __device__ __forceinline__ void load_tile(void *dst, const TensorArg &t, int row, int head, int seq, uint64_t *bar) {
