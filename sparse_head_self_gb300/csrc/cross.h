@@ -47,7 +47,7 @@ struct CrossArgs {
     KeySet keys;
     fibatt_heads Q, K, V, O, dO, dQ, dK, dV;
     float *LSE;              // [B, Hq, Nq]
-    float2 *stats;           // backward: (LSE log2 e, D) of every query row
+    float2 *stats;           // backward's workspace: (LSE log2 e, D) of every query row, and more in 16 bits
     cudaStream_t stream;
 };
 
@@ -106,9 +106,9 @@ cudaError_t launch_cross_fwd_simt(const CrossArgs &a);
 cudaError_t launch_cross_bwd_simt(const CrossArgs &a);
 cudaError_t launch_cross_fwd_mma(const CrossArgs &a);   // bf16
 cudaError_t launch_cross_bwd_mma(const CrossArgs &a);   // bf16
+size_t cross_bwd_mma_workspace(int B, int Hq, int Nq);
 bool cross_rows_takes(const CrossArgs &a);               // few enough query rows for the next
 cudaError_t launch_cross_rows(const CrossArgs &a);
-cudaError_t launch_cross_stats(const CrossArgs &a);     // a.stats from a.O, a.dO and a.LSE
 
 struct QkNormArgs {
     int B, N, Hq, Hk, Hv;

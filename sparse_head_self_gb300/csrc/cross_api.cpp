@@ -215,7 +215,9 @@ fibatt_status fibatt_cross_fwd(const fibatt_cross *d, const fibatt_heads *Q, con
 
 size_t fibatt_cross_bwd_workspace_bytes(const fibatt_cross *d) {
     if (!d || d->B < 1 || d->Hq < 1 || d->Nq < 1) return 0;
-    return ((size_t)d->B * d->Hq * d->Nq * sizeof(float2) + 255) / 256 * 256;
+    const size_t bytes = d->dtype == FIBATT_BF16 ? cross_bwd_mma_workspace(d->B, d->Hq, d->Nq)
+                                                 : (size_t)d->B * d->Hq * d->Nq * sizeof(float2);
+    return (bytes + 255) / 256 * 256;
 }
 
 fibatt_status fibatt_cross_bwd(const fibatt_cross *d, const fibatt_heads *Q, const fibatt_heads *K,

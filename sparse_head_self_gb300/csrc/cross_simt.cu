@@ -36,10 +36,6 @@ constexpr int kTile = kT * kLd; // floats of one staged tile
 constexpr float kNegInf = -__builtin_inff();
 
 __device__ __forceinline__ float4 load4(const float *p) { return __ldg(reinterpret_cast<const float4 *>(p)); }
-__device__ __forceinline__ float4 load4(const __nv_bfloat16 *p) {
-    const uint2 v = __ldg(reinterpret_cast<const uint2 *>(p));
-    return make_float4(bf16_lo(v.x), bf16_hi(v.x), bf16_lo(v.y), bf16_hi(v.y));
-}
 __device__ __forceinline__ void store4(float *p, float4 v) { *reinterpret_cast<float4 *>(p) = v; }
 
 // Rows [n0, n0 + 64) of a head into `dst`; rows that `ok` (one bit a row)
@@ -451,7 +447,9 @@ cudaError_t bwd(const CrossArgs &a) {
     if (e != cudaSuccess) return e;
     const auto Q = rows_of<const T>(a.Q), K = rows_of<const T>(a.K), V = rows_of<const T>(a.V),
                dO = rows_of<const T>(a.dO);
-    e = launch_cross_stats(a);
+    const int64_t rows = (int64_t)a.B * a.Hq * a.Nq;
+    e = launch_clusters(cross_stats_kernel<T>, (unsigned)((rows + 15) / 16), 1, 256, 0, a.stream, a.Hq, a.Nq, rows,
+                        rows_of<const T>(a.O), dO, static_cast<const float *>(a.LSE), a.stats);
     if (e != cudaSuccess) return e;
     const int qtiles = (a.Nq + kT - 1) / kT, ktiles = (a.Nk + kT - 1) / kT;
     const int64_t qunits = (int64_t)a.B * a.Hq * qtiles, kunits = (int64_t)a.B * a.Hkv * ktiles;
@@ -464,18 +462,7 @@ cudaError_t bwd(const CrossArgs &a) {
                            ktiles);
 }
 
-template <typename T>
-cudaError_t stats(const CrossArgs &a) {
-    const int64_t rows = (int64_t)a.B * a.Hq * a.Nq;
-    return launch_clusters(cross_stats_kernel<T>, (unsigned)((rows + 15) / 16), 1, 256, 0, a.stream, a.Hq, a.Nq, rows,
-                           rows_of<const T>(a.O), rows_of<const T>(a.dO), static_cast<const float *>(a.LSE), a.stats);
-}
-
 }  // namespace
-
-cudaError_t launch_cross_stats(const CrossArgs &a) {
-    return a.dtype == FIBATT_F32 ? stats<float>(a) : stats<__nv_bfloat16>(a);
-}
 
 cudaError_t launch_cross_fwd_simt(const CrossArgs &a) { return fwd<float>(a); }
 

@@ -128,6 +128,17 @@ __device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t (&r)[16]
         : "memory");
 }
 
+// Whether the phase has completed, without waiting: asked for ahead of work whose
+// end needs it, the answer costs nothing there.
+__device__ __forceinline__ bool pipe_ready(uint64_t *bar, uint32_t parity) {
+    uint32_t done;
+    asm volatile("{ .reg .pred p; mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2; selp.u32 %0, 1, 0, p; }"
+                 : "=r"(done)
+                 : "r"(smem_u32(bar)), "r"(parity)
+                 : "memory");
+    return done != 0;
+}
+
 // ---- descriptors --------------------------------------------------------------
 // A swizzled tile at `p` (shared memory): start address in 16-byte units,
 // 1024 bytes between groups of eight rows, version 1, 128-byte swizzle.  The
@@ -135,6 +146,12 @@ __device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t (&r)[16]
 __device__ __forceinline__ uint64_t tile_desc(const void *p) {
     return (uint64_t)((smem_u32(p) & 0x3ffffu) >> 4) | (1ull << 16) | ((uint64_t)(1024 >> 4) << 32) | (1ull << 46) |
            (2ull << 61);
+}
+// A tile of 128 rows of 16 elements, one k-step wide, not swizzled: the rows'
+// first eight elements (16 bytes each) one after another, then their last eight.
+__device__ __forceinline__ uint64_t narrow_desc(const void *p) {
+    return (uint64_t)((smem_u32(p) & 0x3ffffu) >> 4) | ((uint64_t)(2048 >> 4) << 16) | ((uint64_t)(128 >> 4) << 32) |
+           (1ull << 46);
 }
 constexpr uint64_t kStepRowwise = 32 >> 4;     // 16 elements along the rows
 constexpr uint64_t kStepAcross = 2048 >> 4;    // 16 rows

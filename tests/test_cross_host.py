@@ -83,8 +83,8 @@ def test_cross_refusals(bwd, _no_launch):
     assert st(B=1 << 20, Nq=1 << 18) == INVALID           # 2^34 blocks
     if bwd:
         assert st(ws=None) == INVALID
-        need = 2 * 4 * 9 * 8
-        assert st(ws_bytes=need - 1) == INVALID
+        need = _native.lib().fibatt_cross_bwd_workspace_bytes(_cross_desc())
+        assert st(ws_bytes=need - 1) == INVALID and st(ws_bytes=need) == CUDA
         assert st(do=_heads(ptr=P + 4)) == INVALID
 
 
