@@ -16,6 +16,7 @@ from ._native import FibattError, check, lib
 HEAD_DIM = 64
 
 _DTYPES = {torch.float32: _native.F32, torch.bfloat16: _native.BF16}
+_WEIGHT_SHAPE = (HEAD_DIM,)
 
 
 # ------------------------------------------------------------------ helpers
@@ -269,43 +270,49 @@ def fibottention(Q, K, V, support: Support, scale: float | None = None):
 
 def _check_tensor(name: str, t, dtype, index: int) -> None:
     """A CUDA tensor of this type on device `index`."""
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == index:
+        return
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor (libfibatt has no CPU path)")
     if t.get_device() != index:
         raise ValueError(f"{name} is on {t.device}, expected cuda:{index}")
-    if t.dtype != dtype:
-        raise ValueError(f"{name} has dtype {t.dtype}, expected {dtype}")
+    raise ValueError(f"{name} has dtype {t.dtype}, expected {dtype}")
 
 
-def _check_dense(name: str, t, shape, dtype, index: int) -> None:
+def _check_dense(name: str, t, shape, dtype, index: int) -> int:
+    """The address of a contiguous tensor of this shape."""
     _check_tensor(name, t, dtype, index)
     if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
 
 
 def _index(name: str, t) -> int:
     """The device index of a CUDA tensor."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if not t.is_cuda:
+    index = t.get_device()
+    if index < 0 or not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor (libfibatt has no CPU path)")
-    return t.get_device()
+    return index
 
 
-def _launch(index: int, stream, call):
-    """call(stream pointer) with the launching stream and its device current:
-    what a call allocates then belongs to the stream that uses it."""
+_device_of_thread = torch._C._cuda_getDevice
+_stream_of_thread = torch._C._cuda_getCurrentRawStream
+
+
+def _launch(index: int, stream, call, *args):
+    """call(*args, stream pointer) with the launching stream and its device
+    current: what a call allocates then belongs to the stream that uses it."""
     if stream is not None:
         with torch.cuda.stream(stream):
-            return call(stream.cuda_stream)
-    if index != torch.cuda.current_device():
+            return call(*args, stream.cuda_stream)
+    if index != _device_of_thread():
         with torch.cuda.device(index):
-            return call(torch._C._cuda_getCurrentRawStream(index))
-    return call(torch._C._cuda_getCurrentRawStream(index))
+            return call(*args, _stream_of_thread(index))
+    return call(*args, _stream_of_thread(index))
 
 
 def rotary_tables(angles: torch.Tensor):
@@ -336,7 +343,7 @@ def rotary_angles_2d(height: int, width: int, rot_dims: int = HEAD_DIM, theta: f
 
 
 def _norm_desc(x, heads, q_weight, k_weight, eps, rotary, positions, interleaved):
-    """(packed fibatt_qk_norm, device index, B, N, Hq, Hk, Hv)."""
+    """(packed fibatt_qk_norm, device index, B, N, Hq, Hk, Hv, x's strides)."""
     if not isinstance(x, torch.Tensor) or x.dim() != 3:
         raise ValueError("x must be a [B, N, (Hq + Hk + Hv) * 64] tensor")
     dtype = x.dtype
@@ -348,35 +355,35 @@ def _norm_desc(x, heads, q_weight, k_weight, eps, rotary, positions, interleaved
     B, N, C = x.shape
     if min(Hq, Hk, Hv) < 0 or C != (Hq + Hk + Hv) * HEAD_DIM:
         raise ValueError(f"x has {C} values a token, heads {(Hq, Hk, Hv)} of {HEAD_DIM} need {(Hq + Hk + Hv) * HEAD_DIM}")
-    if x.stride(2) != 1:
+    sb, sn, sc = x.stride()
+    if sc != 1:
         raise ValueError("x must have contiguous tokens")
     wq = wk = cos_ptr = sin_ptr = rot = table = pos = pos_sb = 0
     if q_weight is not None:
-        _check_dense("q_weight", q_weight, (HEAD_DIM,), dtype, index)
-        wq = q_weight.data_ptr()
+        wq = _check_dense("q_weight", q_weight, _WEIGHT_SHAPE, dtype, index)
     if k_weight is not None:
-        _check_dense("k_weight", k_weight, (HEAD_DIM,), dtype, index)
-        wk = k_weight.data_ptr()
+        wk = _check_dense("k_weight", k_weight, _WEIGHT_SHAPE, dtype, index)
     if rotary is not None:
         cos, sin = rotary
-        _check_dense("cos", cos, cos.shape, torch.float32, index)
-        _check_dense("sin", sin, cos.shape, torch.float32, index)
-        if cos.dim() != 2:
+        shape = cos.shape
+        cos_ptr = _check_dense("cos", cos, shape, torch.float32, index)
+        sin_ptr = _check_dense("sin", sin, shape, torch.float32, index)
+        if len(shape) != 2:
             raise ValueError("cos and sin must be [positions, rot_dims / 2]")
-        table, rot = cos.shape
+        table, rot = shape
         rot *= 2
-        cos_ptr, sin_ptr = cos.data_ptr(), sin.data_ptr()
         if positions is not None:
             _check_tensor("positions", positions, torch.int32, index)
-            if positions.shape not in ((N,), (B, N)) or (N > 1 and positions.stride(-1) != 1):
-                raise ValueError(f"positions must be [N] or [B, N] with contiguous rows, got {tuple(positions.shape)}")
+            shape, strides = positions.shape, positions.stride()
+            if (shape != (N,) and shape != (B, N)) or (N > 1 and strides[-1] != 1):
+                raise ValueError(f"positions must be [N] or [B, N] with contiguous rows, got {tuple(shape)}")
             pos = positions.data_ptr()
-            pos_sb = positions.stride(0) if positions.dim() == 2 else 0
+            pos_sb = strides[0] if len(shape) == 2 else 0
     elif positions is not None:
         raise ValueError("positions without rotary tables")
     d = _native.QK_NORM.pack(B, N, Hq, Hk, Hv, HEAD_DIM, code, wq, wk, eps, rot, 1 if interleaved else 0, cos_ptr,
                              sin_ptr, table, pos, pos_sb)
-    return d, index, B, N, Hq, Hk, Hv
+    return d, index, B, N, Hq, Hk, Hv, sb, sn
 
 
 def qk_norm_fwd(x: torch.Tensor, heads, q_weight=None, k_weight=None, eps: float = 1e-6, rotary=None, positions=None,
@@ -385,19 +392,29 @@ def qk_norm_fwd(x: torch.Tensor, heads, q_weight=None, k_weight=None, eps: float
     with heads = (Hq, Hk, Hv); returns (Q, K, V), [B, H, N, 64] each, None for
     a kind without heads.  rotary = (cos, sin), [positions, rot_dims / 2] fp32;
     positions int32 [N] or [B, N]."""
-    d, index, B, N, Hq, Hk, Hv = _norm_desc(x, heads, q_weight, k_weight, eps, rotary, positions, interleaved)
+    d, index, B, N, Hq, Hk, Hv, sb, sn = _norm_desc(x, heads, q_weight, k_weight, eps, rotary, positions, interleaved)
 
-    def call(s):
-        how = {"dtype": x.dtype, "device": x.device}
-        q = torch.empty((B, Hq, N, HEAD_DIM), **how) if Hq else None
-        k = torch.empty((B, Hk, N, HEAD_DIM), **how) if Hk else None
-        v = torch.empty((B, Hv, N, HEAD_DIM), **how) if Hv else None
-        sb, sn, _ = x.stride()
-        check(lib().fibatt_qk_norm_fwd(d, x.data_ptr(), sb, sn, q.data_ptr() if Hq else None,
-                                       k.data_ptr() if Hk else None, v.data_ptr() if Hv else None, s))
-        return q, k, v
+    return _launch(index, stream, _qk_norm_fwd, d, x, x.dtype, x.device, B, N, Hq, Hk, Hv, sb, sn)
 
-    return _launch(index, stream, call)
+
+def _qk_norm_fwd(d, x, dtype, device, B, N, Hq, Hk, Hv, sb, sn, s):
+    q = k = v = qp = kp = vp = None
+    if Hq:
+        q = torch.empty((B, Hq, N, HEAD_DIM), dtype=dtype, device=device)
+        qp = q.data_ptr()
+    if Hk:
+        k = torch.empty((B, Hk, N, HEAD_DIM), dtype=dtype, device=device)
+        kp = k.data_ptr()
+    if Hv == Hk and Hk:
+        v = torch.empty_like(k)
+        vp = v.data_ptr()
+    elif Hv:
+        v = torch.empty((B, Hv, N, HEAD_DIM), dtype=dtype, device=device)
+        vp = v.data_ptr()
+    status = lib().fibatt_qk_norm_fwd(d, x.data_ptr(), sb, sn, qp, kp, vp, s)
+    if status:
+        check(status)
+    return q, k, v
 
 
 def qk_norm_bwd(x: torch.Tensor, heads, q_weight, k_weight, dQ, dK, dV, eps: float = 1e-6, rotary=None,
@@ -405,12 +422,13 @@ def qk_norm_bwd(x: torch.Tensor, heads, q_weight, k_weight, dQ, dK, dV, eps: flo
     """fibatt_qk_norm_bwd: from the gradients of qk_norm_fwd's results (None
     for a kind without heads) to (dx, dq_weight, dk_weight); a weight that is
     None has the gradient None."""
-    d, index, B, N, Hq, Hk, Hv = _norm_desc(x, heads, q_weight, k_weight, eps, rotary, positions, interleaved)
+    d, index, B, N, Hq, Hk, Hv, sb, sn = _norm_desc(x, heads, q_weight, k_weight, eps, rotary, positions, interleaved)
     grads = []
     for name, g, h in (("dQ", dQ, Hq), ("dK", dK, Hk), ("dV", dV, Hv)):
         if h:
-            _check_dense(name, g, (B, h, N, HEAD_DIM), x.dtype, index)
-        grads.append(g.data_ptr() if h else None)
+            grads.append(_check_dense(name, g, (B, h, N, HEAD_DIM), x.dtype, index))
+        else:
+            grads.append(None)
 
     def call(s):
         dx = torch.empty(x.shape, dtype=x.dtype, device=x.device)
@@ -419,7 +437,6 @@ def qk_norm_bwd(x: torch.Tensor, heads, q_weight, k_weight, dQ, dK, dV, eps: flo
         ws = workspace
         if ws is None:
             ws = torch.empty(lib().fibatt_qk_norm_bwd_workspace_bytes(), dtype=torch.uint8, device=x.device)
-        sb, sn, _ = x.stride()
         check(lib().fibatt_qk_norm_bwd(d, x.data_ptr(), sb, sn, *grads, dx.data_ptr(), dx.stride(0), dx.stride(1),
                                        None if dqw is None else dqw.data_ptr(), None if dkw is None else dkw.data_ptr(),
                                        ws.data_ptr(), ws.numel() * ws.element_size(), s))
@@ -461,6 +478,9 @@ def qk_norm(x, heads, q_weight=None, k_weight=None, eps: float = 1e-6, rotary=No
 
 # --------------------------------------------------------- cross attention
 
+_pack_heads = _native.HEADS.pack
+
+
 def _heads_arg(name: str, t, shape, dtype, index: int) -> bytes:
     """t as a packed fibatt_heads."""
     _check_tensor(name, t, dtype, index)
@@ -470,8 +490,8 @@ def _heads_arg(name: str, t, shape, dtype, index: int) -> bytes:
     if sd != 1:
         raise ValueError(f"{name} must have contiguous rows")
     # a dim of one element has no stride that matters
-    return _native.HEADS.pack(t.data_ptr(), sb if shape[0] > 1 else 0, sh if shape[1] > 1 else 0,
-                              sn if shape[2] > 1 else 0)
+    b, h, n, _ = shape
+    return _pack_heads(t.data_ptr(), sb if b > 1 else 0, sh if h > 1 else 0, sn if n > 1 else 0)
 
 
 def _cross_desc(Q, K, V, scale, kv_len, key_mask):
@@ -488,8 +508,7 @@ def _cross_desc(Q, K, V, scale, kv_len, key_mask):
     _, Hkv, Nk, _ = K.shape
     lens = mask = mask_sb = 0
     if kv_len is not None:
-        _check_dense("kv_len", kv_len, (B,), torch.int32, index)
-        lens = kv_len.data_ptr()
+        lens = _check_dense("kv_len", kv_len, (B,), torch.int32, index)
     if key_mask is not None:
         if not isinstance(key_mask, torch.Tensor) or key_mask.dtype not in (torch.bool, torch.uint8):
             raise ValueError("key_mask must be a bool or uint8 tensor")
@@ -511,19 +530,22 @@ def cross_fwd(Q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, scale: float, k
     returns (O, LSE), O in Q's layout.  kv_len: int32 [B], the keys each
     sequence has; key_mask: bool [B, Nk], the keys it attends."""
     d, q, k, v, index = _cross_desc(Q, K, V, scale, kv_len, key_mask)
+    return _launch(index, stream, _cross_fwd, d, q, k, v, Q, O, LSE, index)
 
-    def call(s):
-        o = torch.empty_like(Q) if O is None else O
-        shape = Q.shape
-        if LSE is None:
-            lse = torch.empty(shape[:3], dtype=torch.float32, device=Q.device)
-        else:
-            lse = LSE
-            _check_dense("LSE", lse, shape[:3], torch.float32, index)
-        check(lib().fibatt_cross_fwd(d, q, k, v, _heads_arg("O", o, shape, Q.dtype, index), lse.data_ptr(), s))
-        return o, lse
 
-    return _launch(index, stream, call)
+def _cross_fwd(d, q, k, v, Q, O, LSE, index, s):
+    shape = Q.shape
+    if O is None:
+        O = torch.empty_like(Q)
+    if LSE is None:
+        LSE = torch.empty(shape[:3], dtype=torch.float32, device=Q.device)
+        lse = LSE.data_ptr()
+    else:
+        lse = _check_dense("LSE", LSE, shape[:3], torch.float32, index)
+    status = lib().fibatt_cross_fwd(d, q, k, v, _heads_arg("O", O, shape, Q.dtype, index), lse, s)
+    if status:
+        check(status)
+    return O, LSE
 
 
 def cross_bwd(Q, K, V, O, LSE, dO, scale: float, kv_len=None, key_mask=None, dQ=None, dK=None, dV=None,
