@@ -40,8 +40,7 @@ __device__ __forceinline__ void store4(float *p, float4 v) { *reinterpret_cast<f
 
 // Rows [n0, n0 + 64) of a head into `dst`; rows that `ok` (one bit a row)
 // leaves out are zeros, whatever memory holds there.
-template <typename T>
-__device__ __forceinline__ void stage(float *dst, const T *head, int64_t sn, int n0, uint64_t ok) {
+__device__ __forceinline__ void stage(float *dst, const float *head, int64_t sn, int n0, uint64_t ok) {
     for (int i = threadIdx.x; i < kT * 16; i += kThreads) {
         const int r = i >> 4, c = (i & 15) * 4;
         const float4 v = (ok >> r) & 1 ? load4(head + (int64_t)(n0 + r) * sn + c) : make_float4(0.f, 0.f, 0.f, 0.f);
@@ -64,23 +63,24 @@ __device__ __forceinline__ uint64_t key_bits(const KeySet &ks, int b, int n0, in
     return (uint64_t)__ballot_sync(kFullMask, lo) | ((uint64_t)__ballot_sync(kFullMask, hi) << 32);
 }
 
-// acc[i][j] = <A row 8 tr + i, B row tc + 16 j>
-__device__ __forceinline__ void mm_nt(float (&acc)[8][4], const float *A, const float *B, int tr, int tc) {
-    float2 s[8][4];
+// acc[i][j] = <A row 8 tr + i, B row tc + 16 j>, j < J (0 for the others)
+template <int J>
+__device__ __forceinline__ void mm_nt_of(float (&acc)[8][4], const float *A, const float *B, int tr, int tc) {
+    float2 s[8][J];
 #pragma unroll
     for (int i = 0; i < 8; ++i)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) s[i][j] = make_float2(0.f, 0.f);
+        for (int j = 0; j < J; ++j) s[i][j] = make_float2(0.f, 0.f);
 #pragma unroll 4
     for (int d = 0; d < 64; d += 4) {
-        float4 b[4];
+        float4 b[J];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) b[j] = *reinterpret_cast<const float4 *>(B + (tc + 16 * j) * kLd + d);
+        for (int j = 0; j < J; ++j) b[j] = *reinterpret_cast<const float4 *>(B + (tc + 16 * j) * kLd + d);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             const float4 a = *reinterpret_cast<const float4 *>(A + (8 * tr + i) * kLd + d);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
+            for (int j = 0; j < J; ++j) {
                 s[i][j] = fma2(make_float2(a.x, a.y), make_float2(b[j].x, b[j].y), s[i][j]);
                 s[i][j] = fma2(make_float2(a.z, a.w), make_float2(b[j].z, b[j].w), s[i][j]);
             }
@@ -89,13 +89,19 @@ __device__ __forceinline__ void mm_nt(float (&acc)[8][4], const float *A, const 
 #pragma unroll
     for (int i = 0; i < 8; ++i)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] = s[i][j].x + s[i][j].y;
+        for (int j = 0; j < 4; ++j) acc[i][j] = j < J ? s[i][j < J ? j : 0].x + s[i][j < J ? j : 0].y : 0.f;
 }
 
-// acc[i] += sum_k W[8 tr + i][k] B[k][4 tc .. 4 tc + 3]
-__device__ __forceinline__ void mm_nn(float4 (&acc)[8], const float *W, const float *B, int tr, int tc) {
+// The columns' tile holds `cols` rows.
+__device__ __forceinline__ void mm_nt(float (&acc)[8][4], const float *A, const float *B, int tr, int tc, int cols) {
+    if (cols <= 16) mm_nt_of<1>(acc, A, B, tr, tc);
+    else mm_nt_of<4>(acc, A, B, tr, tc);
+}
+
+// acc[i] += sum_k W[8 tr + i][k] B[k][4 tc .. 4 tc + 3] over the first `rows` k (to the next four)
+__device__ __forceinline__ void mm_nn(float4 (&acc)[8], const float *W, const float *B, int tr, int tc, int rows) {
 #pragma unroll 2
-    for (int k = 0; k < 64; k += 4) {
+    for (int k = 0; k < rows; k += 4) {
         float4 b[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) b[j] = *reinterpret_cast<const float4 *>(B + (k + j) * kLd + 4 * tc);
@@ -139,9 +145,8 @@ __device__ __forceinline__ float row_sum(float x) {
 // The part of `tiles` that CTA `r` of `c` walks over.
 __device__ __forceinline__ int part(int tiles, int r, int c) { return (int)((int64_t)tiles * r / c); }
 
-template <typename T>
 __global__ void __launch_bounds__(kThreads, 2)
-cross_fwd_simt_kernel(int Hq, int Hkv, int Nq, KeySet ks, Rows<const T> Q, Rows<const T> K, Rows<const T> V, Rows<T> O,
+cross_fwd_simt_kernel(int Hq, int Hkv, int Nq, KeySet ks, Rows<const float> Q, Rows<const float> K, Rows<const float> V, Rows<float> O,
                       float *__restrict__ LSE, float scale_log2, int qtiles) {
     extern __shared__ float4 smem4[];
     float *sq = reinterpret_cast<float *>(smem4), *sk = sq + kTile, *sv = sk + kTile, *sw = sv + kTile;
@@ -156,6 +161,7 @@ cross_fwd_simt_kernel(int Hq, int Hkv, int Nq, KeySet ks, Rows<const T> Q, Rows<
     const int bound = ks.bound(b), tiles = (bound + kT - 1) / kT;
     const int lo = part(tiles, rank, C), hi = part(tiles, rank + 1, C);
     const uint64_t rows = first_bits(Nq - q0);
+    const bool mine = (tid & ~31) / 2 < Nq - q0;     // the warp's 16 rows begin within the queries
     stage(sq, Q.row(b, h, 0), Q.sn, q0, rows);
     float m[8], l[8];
     float4 acc[8];
@@ -172,8 +178,10 @@ cross_fwd_simt_kernel(int Hq, int Hkv, int Nq, KeySet ks, Rows<const T> Q, Rows<
         stage(sk, K.row(b, hk, 0), K.sn, t * kT, ok);
         stage(sv, V.row(b, hk, 0), V.sn, t * kT, ok);
         __syncthreads();
+        if (!mine) continue;
+        const int cols = min(kT, bound - t * kT);
         float s[8][4];
-        mm_nt(s, sq, sk, tr, tc);
+        mm_nt(s, sq, sk, tr, tc, cols);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             float top = kNegInf;
@@ -199,7 +207,7 @@ cross_fwd_simt_kernel(int Hq, int Hkv, int Nq, KeySet ks, Rows<const T> Q, Rows<
             acc[i].w *= keep;
         }
         put_weights(sw, s, tr, tc);
-        mm_nn(acc, sw, sv, tr, tc);
+        mm_nn(acc, sw, sv, tr, tc, cols);
     }
 #pragma unroll
     for (int i = 0; i < 8; ++i) l[i] = row_sum(l[i]);
@@ -252,9 +260,8 @@ cross_fwd_simt_kernel(int Hq, int Hkv, int Nq, KeySet ks, Rows<const T> Q, Rows<
 
 // (LSE log2 e, D = <dO, O>) of every query row; a row without keys gets
 // +infinity, which makes each of its weights exp2(s - inf) = 0.
-template <typename T>
 __global__ void __launch_bounds__(256)
-cross_stats_kernel(int Hq, int Nq, int64_t rows, Rows<const T> O, Rows<const T> dO, const float *__restrict__ LSE,
+cross_stats_kernel(int Hq, int Nq, int64_t rows, Rows<const float> O, Rows<const float> dO, const float *__restrict__ LSE,
                    float2 *__restrict__ stats) {
     grid_dep_wait();
     const int64_t row = (int64_t)blockIdx.x * 16 + (threadIdx.x >> 4);
@@ -274,8 +281,7 @@ cross_stats_kernel(int Hq, int Nq, int64_t rows, Rows<const T> O, Rows<const T> 
 
 // Sum over the cluster of the 64 x 64 accumulator (`part` in shared memory,
 // 64 rows of kLd floats), times `scale`, into rows n0.. of `out`.
-template <typename T>
-__device__ __forceinline__ void finish(float4 (&acc)[8], float *parts, Rows<T> out, int64_t b, int64_t h, int n0, int N,
+__device__ __forceinline__ void finish(float4 (&acc)[8], float *parts, Rows<float> out, int64_t b, int64_t h, int n0, int N,
                                        float scale, int tr, int tc) {
     const int C = (int)cluster_size(), rank = (int)cluster_rank();
     if (C == 1) {
@@ -305,44 +311,51 @@ __device__ __forceinline__ void finish(float4 (&acc)[8], float *parts, Rows<T> o
     cluster_sync();
 }
 
-template <typename T>
-__global__ void __launch_bounds__(kThreads, 2)
-cross_dq_simt_kernel(int Hq, int Hkv, int Nq, KeySet ks, Rows<const T> Q, Rows<const T> K, Rows<const T> V,
-                     Rows<const T> dO, const float2 *__restrict__ stats, Rows<T> dQ, float scale, int qtiles) {
-    extern __shared__ float4 smem4[];
-    float *sq = reinterpret_cast<float *>(smem4), *sg = sq + kTile, *sk = sg + kTile, *sv = sk + kTile,
-          *sw = sv + kTile;
+struct BwdArgs32 {
+    int Hq, Hkv, Nq;
+    KeySet ks;
+    Rows<const float> Q, K, V, dO;
+    const float2 *stats;
+    Rows<float> dQ, dK, dV;
+    float scale;
+    int qtiles, ktiles;
+    int key_units;        // units that hold keys; the others hold queries
+};
+
+// Holds 64 queries and walks over the keys.
+__device__ __forceinline__ void hold_queries(const BwdArgs32 &a, float *smem, int64_t unit) {
+    float *sq = smem, *sg = sq + kTile, *sk = sg + kTile, *sv = sk + kTile, *sw = sv + kTile;
     const int tid = threadIdx.x, tr = tid >> 4, tc = tid & 15;
     const int C = (int)cluster_size(), rank = (int)cluster_rank();
-    const int64_t unit = blockIdx.x / C;
-    const int qt = (int)(unit % qtiles), h = (int)(unit / qtiles % Hq), b = (int)(unit / qtiles / Hq);
-    const int hk = h / (Hq / Hkv), q0 = qt * kT;
-    const float scale_log2 = scale * kLog2e;
-
-    grid_dep_wait();
-    const int bound = ks.bound(b), tiles = (bound + kT - 1) / kT;
+    const int qt = (int)(unit % a.qtiles), h = (int)(unit / a.qtiles % a.Hq), b = (int)(unit / a.qtiles / a.Hq);
+    const int hk = h / (a.Hq / a.Hkv), q0 = qt * kT;
+    const float scale_log2 = a.scale * kLog2e;
+    const int bound = a.ks.bound(b), tiles = (bound + kT - 1) / kT;
     const int lo = part(tiles, rank, C), hi = part(tiles, rank + 1, C);
-    const uint64_t rows = first_bits(Nq - q0);
-    stage(sq, Q.row(b, h, 0), Q.sn, q0, rows);
-    stage(sg, dO.row(b, h, 0), dO.sn, q0, rows);
+    const uint64_t rows = first_bits(a.Nq - q0);
+    const bool mine = (tid & ~31) / 2 < a.Nq - q0;     // the warp's 16 rows begin within the queries
+    stage(sq, a.Q.row(b, h, 0), a.Q.sn, q0, rows);
+    stage(sg, a.dO.row(b, h, 0), a.dO.sn, q0, rows);
     float2 st[8];
     float4 acc[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         const int n = q0 + 8 * tr + i;
-        st[i] = n < Nq ? stats[((int64_t)b * Hq + h) * Nq + n] : make_float2(-kNegInf, 0.f);
+        st[i] = n < a.Nq ? a.stats[((int64_t)b * a.Hq + h) * a.Nq + n] : make_float2(-kNegInf, 0.f);
         acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
     }
     for (int t = lo; t < hi; ++t) {
-        const uint64_t ok = key_bits(ks, b, t * kT, bound);
+        const uint64_t ok = key_bits(a.ks, b, t * kT, bound);
         if (ok == 0) continue;
         __syncthreads();
-        stage(sk, K.row(b, hk, 0), K.sn, t * kT, ok);
-        stage(sv, V.row(b, hk, 0), V.sn, t * kT, ok);
+        stage(sk, a.K.row(b, hk, 0), a.K.sn, t * kT, ok);
+        stage(sv, a.V.row(b, hk, 0), a.V.sn, t * kT, ok);
         __syncthreads();
+        if (!mine) continue;
+        const int cols = min(kT, bound - t * kT);
         float s[8][4], dp[8][4];
-        mm_nt(s, sq, sk, tr, tc);
-        mm_nt(dp, sg, sv, tr, tc);
+        mm_nt(s, sq, sk, tr, tc, cols);
+        mm_nt(dp, sg, sv, tr, tc, cols);
 #pragma unroll
         for (int i = 0; i < 8; ++i)
 #pragma unroll
@@ -351,52 +364,48 @@ cross_dq_simt_kernel(int Hq, int Hkv, int Nq, KeySet ks, Rows<const T> Q, Rows<c
                 s[i][j] = (ok >> (tc + 16 * j)) & 1 ? p * (dp[i][j] - st[i].y) : 0.f;
             }
         put_weights(sw, s, tr, tc);
-        mm_nn(acc, sw, sk, tr, tc);
+        mm_nn(acc, sw, sk, tr, tc, cols);
     }
-    finish(acc, sv, dQ, b, h, q0, Nq, scale, tr, tc);
+    finish(acc, sv, a.dQ, b, h, q0, a.Nq, a.scale, tr, tc);
 }
 
-template <typename T>
-__global__ void __launch_bounds__(kThreads, 2)
-cross_dkv_simt_kernel(int Hq, int Hkv, int Nq, KeySet ks, Rows<const T> Q, Rows<const T> K, Rows<const T> V,
-                      Rows<const T> dO, const float2 *__restrict__ stats, Rows<T> dK, Rows<T> dV, float scale,
-                      int ktiles) {
-    extern __shared__ float4 smem4[];
-    float *sk = reinterpret_cast<float *>(smem4), *sv = sk + kTile, *sq = sv + kTile, *sg = sq + kTile,
-          *sw = sg + kTile;
+// Holds 64 keys and walks over the queries of every head that shares them.
+__device__ __forceinline__ void hold_keys(const BwdArgs32 &a, float *smem, int64_t unit) {
+    float *sk = smem, *sv = sk + kTile, *sq = sv + kTile, *sg = sq + kTile, *sw = sg + kTile;
     const int tid = threadIdx.x, tr = tid >> 4, tc = tid & 15;
     const int C = (int)cluster_size(), rank = (int)cluster_rank();
-    const int64_t unit = blockIdx.x / C;
-    const int kt = (int)(unit % ktiles), hk = (int)(unit / ktiles % Hkv), b = (int)(unit / ktiles / Hkv);
-    const int G = Hq / Hkv, k0 = kt * kT, qtiles = (Nq + kT - 1) / kT;
-    const float scale_log2 = scale * kLog2e;
-
-    grid_dep_wait();
-    const uint64_t ok = key_bits(ks, b, k0, ks.bound(b));
+    const int kt = (int)(unit % a.ktiles), hk = (int)(unit / a.ktiles % a.Hkv), b = (int)(unit / a.ktiles / a.Hkv);
+    const int G = a.Hq / a.Hkv, k0 = kt * kT, qtiles = a.qtiles;
+    const float scale_log2 = a.scale * kLog2e;
+    const int bound = a.ks.bound(b);
+    const uint64_t ok = key_bits(a.ks, b, k0, bound);
+    const bool mine = (tid & ~31) / 2 < bound - k0;    // the warp's 16 rows begin within the keys
     // the walk: the query tiles of each of the G heads in turn; none for a tile without keys
     const int64_t tiles = ok ? (int64_t)G * qtiles : 0;
     const int64_t lo = tiles * rank / C, hi = tiles * (rank + 1) / C;
-    stage(sk, K.row(b, hk, 0), K.sn, k0, ok);
-    stage(sv, V.row(b, hk, 0), V.sn, k0, ok);
+    stage(sk, a.K.row(b, hk, 0), a.K.sn, k0, ok);
+    stage(sv, a.V.row(b, hk, 0), a.V.sn, k0, ok);
     float4 ak[8], av[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) ak[i] = av[i] = make_float4(0.f, 0.f, 0.f, 0.f);
     for (int64_t t = lo; t < hi; ++t) {
         const int h = hk * G + (int)(t / qtiles), q0 = (int)(t % qtiles) * kT;
-        const uint64_t rows = first_bits(Nq - q0);
+        const uint64_t rows = first_bits(a.Nq - q0);
         __syncthreads();
-        stage(sq, Q.row(b, h, 0), Q.sn, q0, rows);
-        stage(sg, dO.row(b, h, 0), dO.sn, q0, rows);
+        stage(sq, a.Q.row(b, h, 0), a.Q.sn, q0, rows);
+        stage(sg, a.dO.row(b, h, 0), a.dO.sn, q0, rows);
         float2 st[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             const int n = q0 + tc + 16 * j;
-            st[j] = n < Nq ? stats[((int64_t)b * Hq + h) * Nq + n] : make_float2(-kNegInf, 0.f);
+            st[j] = n < a.Nq ? a.stats[((int64_t)b * a.Hq + h) * a.Nq + n] : make_float2(-kNegInf, 0.f);
         }
         __syncthreads();
+        if (!mine) continue;
+        const int cols = min(kT, a.Nq - q0);
         float p[8][4], ds[8][4];
-        mm_nt(p, sk, sq, tr, tc);
-        mm_nt(ds, sv, sg, tr, tc);
+        mm_nt(p, sk, sq, tr, tc, cols);
+        mm_nt(ds, sv, sg, tr, tc, cols);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             const bool in = (ok >> (8 * tr + i)) & 1;
@@ -407,12 +416,22 @@ cross_dkv_simt_kernel(int Hq, int Hkv, int Nq, KeySet ks, Rows<const T> Q, Rows<
             }
         }
         put_weights(sw, p, tr, tc);
-        mm_nn(av, sw, sg, tr, tc);
+        mm_nn(av, sw, sg, tr, tc, cols);
         put_weights(sw, ds, tr, tc);
-        mm_nn(ak, sw, sq, tr, tc);
+        mm_nn(ak, sw, sq, tr, tc, cols);
     }
-    finish(av, sg, dV, b, hk, k0, ks.Nk, 1.f, tr, tc);
-    finish(ak, sq, dK, b, hk, k0, ks.Nk, scale, tr, tc);
+    finish(av, sg, a.dV, b, hk, k0, a.ks.Nk, 1.f, tr, tc);
+    finish(ak, sq, a.dK, b, hk, k0, a.ks.Nk, a.scale, tr, tc);
+}
+
+// Both kinds of unit in one launch, the longer ones (keys) first.
+__global__ void __launch_bounds__(kThreads, 2) cross_bwd_simt_kernel(const __grid_constant__ BwdArgs32 a) {
+    extern __shared__ float4 smem4[];
+    float *smem = reinterpret_cast<float *>(smem4);
+    grid_dep_wait();
+    const int64_t unit = blockIdx.x / cluster_size();
+    if (unit < a.key_units) hold_keys(a, smem, unit);
+    else hold_queries(a, smem, unit - a.key_units);
 }
 
 // CTAs of a cluster for `units` units of `tiles` tiles each: enough to give
@@ -423,50 +442,42 @@ int split(int64_t units, int64_t tiles) {
     return c;
 }
 
-template <typename T>
-cudaError_t fwd(const CrossArgs &a) {
+}  // namespace
+
+cudaError_t launch_cross_fwd_simt(const CrossArgs &a) {
     constexpr size_t smem = 4 * kTile * sizeof(float);
-    const auto kern = cross_fwd_simt_kernel<T>;
-    const cudaError_t e = prepare_kernel<cross_fwd_simt_kernel<T>>(smem, 0);
+    const cudaError_t e = prepare_kernel<cross_fwd_simt_kernel>(smem, 0);
     if (e != cudaSuccess) return e;
     const int qtiles = (a.Nq + kT - 1) / kT;
     const int64_t units = (int64_t)a.B * a.Hq * qtiles;
     const int c = split(units, (a.Nk + kT - 1) / kT);
-    return launch_clusters(kern, (unsigned)(units * c), c, kThreads, smem, a.stream, a.Hq, a.Hkv, a.Nq, a.keys,
-                           rows_of<const T>(a.Q), rows_of<const T>(a.K), rows_of<const T>(a.V), rows_of<T>(a.O), a.LSE,
-                           a.scale * kLog2e, qtiles);
+    return launch_clusters(cross_fwd_simt_kernel, (unsigned)(units * c), c, kThreads, smem, a.stream, a.Hq, a.Hkv, a.Nq,
+                           a.keys, rows_of<const float>(a.Q), rows_of<const float>(a.K), rows_of<const float>(a.V),
+                           rows_of<float>(a.O), a.LSE, a.scale * kLog2e, qtiles);
 }
 
-template <typename T>
-cudaError_t bwd(const CrossArgs &a) {
+cudaError_t launch_cross_bwd_simt(const CrossArgs &a) {
     constexpr size_t smem = 5 * kTile * sizeof(float);
-    const auto qkern = cross_dq_simt_kernel<T>;
-    const auto kkern = cross_dkv_simt_kernel<T>;
-    cudaError_t e = prepare_kernel<cross_dq_simt_kernel<T>>(smem, 0);
-    if (e == cudaSuccess) e = prepare_kernel<cross_dkv_simt_kernel<T>>(smem, 0);
+    cudaError_t e = prepare_kernel<cross_bwd_simt_kernel>(smem, 0);
     if (e != cudaSuccess) return e;
-    const auto Q = rows_of<const T>(a.Q), K = rows_of<const T>(a.K), V = rows_of<const T>(a.V),
-               dO = rows_of<const T>(a.dO);
+    BwdArgs32 f;
+    f.Hq = a.Hq, f.Hkv = a.Hkv, f.Nq = a.Nq;
+    f.ks = a.keys;
+    f.Q = rows_of<const float>(a.Q), f.K = rows_of<const float>(a.K), f.V = rows_of<const float>(a.V);
+    f.dO = rows_of<const float>(a.dO);
+    f.stats = a.stats;
+    f.dQ = rows_of<float>(a.dQ), f.dK = rows_of<float>(a.dK), f.dV = rows_of<float>(a.dV);
+    f.scale = a.scale;
+    f.qtiles = (a.Nq + kT - 1) / kT, f.ktiles = (a.Nk + kT - 1) / kT;
     const int64_t rows = (int64_t)a.B * a.Hq * a.Nq;
-    e = launch_clusters(cross_stats_kernel<T>, (unsigned)((rows + 15) / 16), 1, 256, 0, a.stream, a.Hq, a.Nq, rows,
-                        rows_of<const T>(a.O), dO, static_cast<const float *>(a.LSE), a.stats);
+    e = launch_clusters(cross_stats_kernel, (unsigned)((rows + 15) / 16), 1, 256, 0, a.stream, a.Hq, a.Nq, rows,
+                        rows_of<const float>(a.O), f.dO, static_cast<const float *>(a.LSE), a.stats);
     if (e != cudaSuccess) return e;
-    const int qtiles = (a.Nq + kT - 1) / kT, ktiles = (a.Nk + kT - 1) / kT;
-    const int64_t qunits = (int64_t)a.B * a.Hq * qtiles, kunits = (int64_t)a.B * a.Hkv * ktiles;
-    const int cq = split(qunits, ktiles), ck = split(kunits, (int64_t)(a.Hq / a.Hkv) * qtiles);
-    e = launch_clusters(qkern, (unsigned)(qunits * cq), cq, kThreads, smem, a.stream, a.Hq, a.Hkv, a.Nq, a.keys, Q, K, V,
-                        dO, static_cast<const float2 *>(a.stats), rows_of<T>(a.dQ), a.scale, qtiles);
-    if (e != cudaSuccess) return e;
-    return launch_clusters(kkern, (unsigned)(kunits * ck), ck, kThreads, smem, a.stream, a.Hq, a.Hkv, a.Nq, a.keys, Q, K,
-                           V, dO, static_cast<const float2 *>(a.stats), rows_of<T>(a.dK), rows_of<T>(a.dV), a.scale,
-                           ktiles);
+    const int64_t key_units = (int64_t)a.B * a.Hkv * f.ktiles, units = key_units + (int64_t)a.B * a.Hq * f.qtiles;
+    f.key_units = (int)key_units;
+    const int c = split(units, std::max<int64_t>(f.ktiles, (int64_t)(a.Hq / a.Hkv) * f.qtiles));
+    return launch_clusters(cross_bwd_simt_kernel, (unsigned)(units * c), c, kThreads, smem, a.stream, f);
 }
-
-}  // namespace
-
-cudaError_t launch_cross_fwd_simt(const CrossArgs &a) { return fwd<float>(a); }
-
-cudaError_t launch_cross_bwd_simt(const CrossArgs &a) { return bwd<float>(a); }
 
 FIBATT_DEFINE_ERROR_READER(read_error_cross_simt, "cross_simt.cu")
 
