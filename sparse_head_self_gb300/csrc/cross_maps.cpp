@@ -43,9 +43,19 @@ bool make_tensor(TensorArg *t, const fibatt_heads &v, int B, int H, int N, int r
         strides[i] = (cuuint64_t)stride[i] * size_of;
     }
     const cuuint32_t box[4] = {64, (cuuint32_t)rows, (cuuint32_t)heads, 1}, estr[4] = {1, 1, 1, 1};
-    return f(&t->map, dtype == FIBATT_F32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, v.ptr, dims, strides, box, estr,
+    const auto encode = [&] {
+        return f(&t->map, dtype == FIBATT_F32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, v.ptr, dims, strides, box, estr,
              CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
-             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    };
+    CUresult r = encode();
+    if (r == CUDA_ERROR_INVALID_CONTEXT) {
+        // the first call of a thread whose device the runtime has not made current yet
+        int dev = 0;
+        if (cudaGetDevice(&dev) != cudaSuccess || cudaSetDevice(dev) != cudaSuccess) return false;
+        r = encode();
+    }
+    return r == CUDA_SUCCESS;
 }
 
 }  // namespace fibatt

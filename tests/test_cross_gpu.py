@@ -3,6 +3,7 @@ in 64 bits (tests/cross_ref.py, elementwise bounds from counted roundings),
 over head layouts, lengths, masks, strides and scales; differences of the
 forward pass; streams, graphs and repeated calls."""
 import math
+import threading
 
 import pytest
 import torch
@@ -284,6 +285,30 @@ def test_captured_and_replayed_on_new_inputs(dtype, Nq):
         want = _run(q, k, v, do, 0.125, n)
         for name, t in zip(("O", "LSE", "dQ", "dK", "dV"), (o, lse) + tuple(grads)):
             assert torch.equal(want[name], t), name
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("Nq", [1, 70])
+def test_from_threads_that_made_no_other_call(dtype, Nq):
+    # a fresh thread has no current context until something makes the device's current
+    q, k, v, do = _inputs(dtype, 2, 4, 2, Nq, 90)
+    want = _run(q, k, v, do, 0.125)
+    got = {}
+
+    def fwd():
+        got["O"], got["LSE"] = api.cross_fwd(q, k, v, 0.125)
+
+    def bwd():
+        got["dQ"], got["dK"], got["dV"] = api.cross_bwd(q, k, v, want["O"], want["LSE"], do, 0.125)
+
+    for f in (fwd, bwd):
+        t = threading.Thread(target=f)
+        t.start()
+        t.join()
+    torch.cuda.synchronize()
+    assert set(got) == set(want)
+    for name in want:
+        assert torch.equal(want[name], got[name]), name
 
 
 @pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
