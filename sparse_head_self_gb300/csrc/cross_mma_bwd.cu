@@ -42,9 +42,9 @@ constexpr int kGroups = 4;                        // column groups of a tile, 32
 constexpr int kWeightWarps = 4 * kGroups;
 constexpr int kCopyWarp = kWeightWarps, kPrepWarp = kWeightWarps + 1, kScoreWarp = kWeightWarps + 2, kSumWarp = kWeightWarps + 3;
 constexpr int kThreads = 32 * (kWeightWarps + 4);
-constexpr int kStages = 3;
-constexpr int kNarrow = kTileRows * 32;           // bytes of a tile one k-step wide
-constexpr size_t kSmem = 1024 + (4 + 2 * kStages) * kTileBytes + (1 + 2 * kStages) * kNarrow;
+constexpr int kStages = 4;
+constexpr int kNarrow = kTileRows * 16;           // bytes of half a k-step of a tile (the other half: zeros for all)
+constexpr size_t kSmem = 1024 + (4 + 2 * kStages) * kTileBytes + (2 + 2 * kStages) * kNarrow;
 constexpr int kJoinLd = 68;                       // floats between rows of a partial sum in shared memory
 static_assert(2 * kTileRows * kJoinLd * 4 <= 2 * kStages * kTileBytes, "partial sums fit");
 // registers a thread: at launch, and after the weight warps took what the others gave
@@ -152,9 +152,10 @@ struct Unit {
 
 // The CTA's shared memory.
 struct Tiles {
-    uint8_t *held, *ring, *ones, *parts;
+    uint8_t *held, *ring, *ones, *parts, *zeros;
     __device__ __forceinline__ explicit Tiles(uint8_t *smem)
-        : held(smem), ring(smem + 4 * kTileBytes), ones(ring + 2 * kStages * kTileBytes), parts(ones + kNarrow) {}
+        : held(smem), ring(smem + 4 * kTileBytes), ones(ring + 2 * kStages * kTileBytes), parts(ones + kNarrow),
+          zeros(parts + 2 * kStages * kNarrow) {}
     // pair i of the held tiles (Q, dO or K, V); stage s: K or Q, V or dO behind it; LSE parts, D parts behind them
     __device__ __forceinline__ uint8_t *pair(int i) const { return held + 2 * i * kTileBytes; }
     __device__ __forceinline__ uint8_t *stage(int s) const { return ring + 2 * s * kTileBytes; }
@@ -371,12 +372,12 @@ __device__ __forceinline__ void scores(const BwdMmaArgs &a, Shared &sh, const Ti
     const uint32_t id = mma_desc(128, 128, false), tmem = sh.tmem;
     const int pair = units & 1;
     const uint64_t h0 = tile_desc(tl.pair(pair)), h1 = h0 + (kTileBytes >> 4);
-    const uint64_t one = narrow_desc(tl.ones);
+    const uint64_t one = narrow_desc(tl.ones, tl.zeros);
     pipe_wait(&sh.held[pair], (units >> 1) & 1, abort);
     ++units;
     for (int j = 0; j < u.n; ++j, ++it, at.next()) {
         const uint64_t r0 = tile_desc(tl.ring) + (uint64_t)(at.s * (2 * kTileBytes >> 4)), r1 = r0 + (kTileBytes >> 4);
-        const uint64_t part = narrow_desc(tl.parts) + (uint64_t)(at.s * (2 * kNarrow >> 4));
+        const uint64_t lse = narrow_desc(tl.part(at.s), tl.zeros), d = narrow_desc(tl.part(at.s) + kNarrow, tl.zeros);
         pipe_wait(&sh.ready[at.s], at.pass, abort);
         if (it > 0) pipe_wait(&sh.sfree, (it - 1) & 1, abort);
         tc_after_sync();
@@ -388,8 +389,8 @@ __device__ __forceinline__ void scores(const BwdMmaArgs &a, Shared &sh, const Ti
             for (int i = 0; i < 4; ++i)
                 mma_ss(tmem + kColDp, h1 + i * kStepRowwise, r1 + i * kStepRowwise, id, i > 0);
             if (KEYS) {
-                mma_ss(tmem + kColS, one, part, id, true);
-                mma_ss(tmem + kColDp, one, part + (kNarrow >> 4), id, true);
+                mma_ss(tmem + kColS, one, lse, id, true);
+                mma_ss(tmem + kColDp, one, d, id, true);
             }
             mma_commit(&sh.s);
             if (j == u.n - 1) mma_commit(&sh.held_free[pair]);
@@ -483,11 +484,11 @@ __global__ void __launch_bounds__(kThreads, 1) cross_bwd_mma_kernel(const __grid
             reinterpret_cast<uint4 *>(tl.ring)[i] = make_uint4(0, 0, 0, 0);
     // ones in the first three elements of a row; rows of no query until copies bring some
     const uint4 none = no_query(a.c);
-    for (int i = threadIdx.x; i < (1 + 2 * kStages) * kNarrow / 16; i += kThreads) {
-        const int tile = i / (kNarrow / 16), r = i % (kNarrow / 16);
+    for (int i = threadIdx.x; i < (2 + 2 * kStages) * kTileRows; i += kThreads) {
+        const int tile = i / kTileRows;    // ones, then LSE and D of each stage, then zeros
         uint4 v = make_uint4(0, 0, 0, 0);
-        if (r < kTileRows && tile == 0) v = make_uint4(0x3f803f80u, 0x3f80u, 0u, 0u);
-        else if (r < kTileRows && (tile & 1)) v = none;
+        if (tile == 0) v = make_uint4(0x3f803f80u, 0x3f80u, 0u, 0u);
+        else if ((tile & 1) && tile < 1 + 2 * kStages) v = none;
         reinterpret_cast<uint4 *>(tl.ones)[i] = v;
     }
     fence_smem_async();

@@ -148,10 +148,11 @@ __device__ __forceinline__ uint64_t tile_desc(const void *p) {
            (2ull << 61);
 }
 // A tile of 128 rows of 16 elements, one k-step wide, not swizzled: the rows'
-// first eight elements (16 bytes each) one after another, then their last eight.
-__device__ __forceinline__ uint64_t narrow_desc(const void *p) {
-    return (uint64_t)((smem_u32(p) & 0x3ffffu) >> 4) | ((uint64_t)(2048 >> 4) << 16) | ((uint64_t)(128 >> 4) << 32) |
-           (1ull << 46);
+// first eight elements (16 bytes each) one after another at `p`, their last eight
+// at `last`, behind it.
+__device__ __forceinline__ uint64_t narrow_desc(const void *p, const void *last) {
+    return (uint64_t)((smem_u32(p) & 0x3ffffu) >> 4) | ((uint64_t)((smem_u32(last) - smem_u32(p)) >> 4) << 16) |
+           ((uint64_t)(128 >> 4) << 32) | (1ull << 46);
 }
 constexpr uint64_t kStepRowwise = 32 >> 4;     // 16 elements along the rows
 constexpr uint64_t kStepAcross = 2048 >> 4;    // 16 rows
