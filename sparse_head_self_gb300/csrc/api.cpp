@@ -484,7 +484,7 @@ fibatt_status fibatt_device_error(int clear, unsigned *code) {
     if (!code) return set_error(FIBATT_ERR_INVALID_ARG, "code is NULL");
     *code = 0;
     cudaError_t e = read_device_error(code, clear != 0);
-    for (auto reader : {read_error_cross_simt, read_error_cross_mma_fwd, read_error_cross_mma_bwd, read_error_cross_rows,
+    for (auto reader : {read_error_cross_f32, read_error_cross_mma_fwd, read_error_cross_mma_bwd, read_error_cross_rows,
                         read_error_qk_norm}) {
         unsigned c = 0;
         if (e == cudaSuccess) e = reader(&c, clear != 0);

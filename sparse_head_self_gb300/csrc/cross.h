@@ -102,8 +102,8 @@ cudaError_t prepare_kernel(size_t smem, int regs) {
 }
 
 // ---- launchers (return the CUDA launch status) -----------------------------
-cudaError_t launch_cross_fwd_simt(const CrossArgs &a);
-cudaError_t launch_cross_bwd_simt(const CrossArgs &a);
+cudaError_t launch_cross_fwd_f32(const CrossArgs &a);
+cudaError_t launch_cross_bwd_f32(const CrossArgs &a);
 cudaError_t launch_cross_fwd_mma(const CrossArgs &a);   // bf16
 cudaError_t launch_cross_bwd_mma(const CrossArgs &a);   // bf16
 size_t cross_bwd_mma_workspace(int B, int Hq, int Nq);
@@ -136,7 +136,7 @@ cudaError_t launch_qk_norm_fwd(const QkNormArgs &a);
 cudaError_t launch_qk_norm_bwd(const QkNormArgs &a);
 
 // Each kernel file's device error word (device_common.cuh).
-cudaError_t read_error_cross_simt(unsigned *code, bool clear);
+cudaError_t read_error_cross_f32(unsigned *code, bool clear);
 cudaError_t read_error_cross_mma_fwd(unsigned *code, bool clear);
 cudaError_t read_error_cross_mma_bwd(unsigned *code, bool clear);
 cudaError_t read_error_cross_rows(unsigned *code, bool clear);

@@ -209,7 +209,7 @@ fibatt_status fibatt_cross_fwd(const fibatt_cross *d, const fibatt_heads *Q, con
     a.LSE = LSE;
     const cudaError_t e = cross_rows_takes(a)         ? launch_cross_rows(a)
                           : a.dtype == FIBATT_BF16 ? launch_cross_fwd_mma(a)
-                                                   : launch_cross_fwd_simt(a);
+                                                   : launch_cross_fwd_f32(a);
     return e == cudaSuccess ? FIBATT_OK : cuda_error(e, "fibatt_cross_fwd launch");
 }
 
@@ -244,7 +244,7 @@ fibatt_status fibatt_cross_bwd(const fibatt_cross *d, const fibatt_heads *Q, con
     a.LSE = const_cast<float *>(LSE);
     a.dO = *dO, a.dQ = *dQ, a.dK = *dK, a.dV = *dV;
     a.stats = static_cast<float2 *>(workspace);
-    const cudaError_t e = a.dtype == FIBATT_BF16 ? launch_cross_bwd_mma(a) : launch_cross_bwd_simt(a);
+    const cudaError_t e = a.dtype == FIBATT_BF16 ? launch_cross_bwd_mma(a) : launch_cross_bwd_f32(a);
     return e == cudaSuccess ? FIBATT_OK : cuda_error(e, "fibatt_cross_bwd launch");
 }
 
