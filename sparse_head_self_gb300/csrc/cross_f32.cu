@@ -93,14 +93,28 @@ __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint3
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-// c += a (b0, b1) to 22 bits
-__device__ __forceinline__ void mma3(float (&c)[4], const uint32_t (&ah)[4], const uint32_t (&al)[4], float b0, float b1) {
-    uint32_t h0, l0, h1, l1;
-    cut(b0, h0, l0);
-    cut(b1, h1, l1);
-    mma(c, ah, l0, l1);
-    mma(c, al, h0, h1);
-    mma(c, ah, h0, h1);
+// c[i] += a b[i] to 22 bits for four b: the instructions that add to one c lie
+// four apart, since each waits for the one before it.
+__device__ __forceinline__ void mma3(float (&c0)[4], float (&c1)[4], float (&c2)[4], float (&c3)[4], const uint32_t (&ah)[4],
+                                     const uint32_t (&al)[4], const float2 (&b)[4]) {
+    uint32_t h[4][2], l[4][2];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        cut(b[i].x, h[i][0], l[i][0]);
+        cut(b[i].y, h[i][1], l[i][1]);
+    }
+    mma(c0, ah, l[0][0], l[0][1]);
+    mma(c1, ah, l[1][0], l[1][1]);
+    mma(c2, ah, l[2][0], l[2][1]);
+    mma(c3, ah, l[3][0], l[3][1]);
+    mma(c0, al, h[0][0], h[0][1]);
+    mma(c1, al, h[1][0], h[1][1]);
+    mma(c2, al, h[2][0], h[2][1]);
+    mma(c3, al, h[3][0], h[3][1]);
+    mma(c0, ah, h[0][0], h[0][1]);
+    mma(c1, ah, h[1][0], h[1][1]);
+    mma(c2, ah, h[2][0], h[2][1]);
+    mma(c3, ah, h[3][0], h[3][1]);
 }
 
 // A lane's fragment of 16 rows by 64 columns: [j][0], [j][1] are row g (of the
@@ -113,7 +127,7 @@ struct Lane {
 };
 
 // c = A B^T: rows of A from the warp's first; columns: the first `cols` rows of B
-// (to the next eight; 0 for the others).
+// (to the next 32; 0 for the others).
 __device__ __forceinline__ void nt(float (&c)[8][4], const float *A, const float *B, const Lane &l, int cols) {
 #pragma unroll
     for (int j = 0; j < 8; ++j)
@@ -130,10 +144,12 @@ __device__ __forceinline__ void nt(float (&c)[8][4], const float *A, const float
         cut(u.y, ah[2], al[2]);
         cut(v.y, ah[3], al[3]);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
+        for (int j = 0; j < 8; j += 4) {
             if (8 * j >= cols) break;
-            const float2 b = *reinterpret_cast<const float2 *>(pb + 8 * j * kLd + k);
-            mma3(c[j], ah, al, b.x, b.y);
+            float2 b[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) b[i] = *reinterpret_cast<const float2 *>(pb + 8 * (j + i) * kLd + k);
+            mma3(c[j], c[j + 1], c[j + 2], c[j + 3], ah, al, b);
         }
     }
 }
@@ -150,7 +166,13 @@ __device__ __forceinline__ void nn(float (&o)[8][4], const float (&W)[8][4], con
         cut(W[j][1], ah[2], al[2]);
         cut(W[j][3], ah[3], al[3]);
 #pragma unroll
-        for (int n = 0; n < 8; ++n) mma3(o[n], ah, al, pb[8 * j * kLd + 8 * n], pb[(8 * j + 1) * kLd + 8 * n]);
+        for (int n = 0; n < 8; n += 4) {
+            float2 b[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                b[i] = make_float2(pb[8 * j * kLd + 8 * (n + i)], pb[(8 * j + 1) * kLd + 8 * (n + i)]);
+            mma3(o[n], o[n + 1], o[n + 2], o[n + 3], ah, al, b);
+        }
     }
 }
 
