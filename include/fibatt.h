@@ -292,7 +292,8 @@ typedef struct {
  * [B, N, H, 64] tensors and slices of packed projections are all read and
  * written in place.  ptr 16-byte aligned, strides >= 0 and multiples of 16
  * bytes; a tensor that a call writes has no two rows in one place, one that it
- * reads may be broadcast over sequences and heads (stride_b, stride_h of 0). */
+ * reads may be broadcast over sequences and heads (stride_b, stride_h of 0).
+ * What a call writes overlaps nothing that it reads. */
 typedef struct {
     void *ptr;
     int64_t stride_b, stride_h, stride_n;
@@ -302,7 +303,9 @@ typedef struct {
  * [B, Hq, Nq] fp32, dense, natural log.  Arithmetic is fp32 with fp32
  * accumulation; for bf16 the softmax weights are rounded to bf16 before their
  * product with V (the sums and the LSE use the unrounded ones), and O once at
- * the end.  INVALID_ARG: a size or stride out of its range, a NULL or
+ * the end; for fp32 products keep 22 bits of each operand (with more than eight
+ * query rows to a key head), so that an infinite value that is attended may
+ * give NaN where 24-bit products give infinity.  INVALID_ARG: a size or stride out of its range, a NULL or
  * misaligned pointer, a scale that is not finite, more than 2^31 - 1 blocks.
  * UNSUPPORTED: D, dtype. */
 fibatt_status fibatt_cross_fwd(const fibatt_cross *d, const fibatt_heads *Q, const fibatt_heads *K,
@@ -340,8 +343,9 @@ const char *fibatt_version(void);
  * about 2 s); bit 2 (4), in the bounds-checked debug build only (built with
  * -DFIBATT_CHECKS), when a kernel's bounds check failed and it skipped the
  * access (the first failing source line is then printed to stderr); bit 3
- * (8) when fibatt_qk_norm_fwd or _bwd met a position behind its tables.  The
- * word is the OR over every kernel file's copy.  This call synchronises with
+ * (8) when fibatt_qk_norm_fwd or _bwd met a position behind its tables.
+ * (fibatt_cross_fwd and _bwd may write outputs after bit 0 or 1: not to be
+ * trusted.)  The word is the OR over every kernel file's copy.  This call synchronises with
  * the device.  With clear != 0 the word is reset.  CUDA on a failed copy. */
 fibatt_status fibatt_device_error(int clear, unsigned *code);
 

@@ -445,11 +445,22 @@ def qk_norm_bwd(x: torch.Tensor, heads, q_weight, k_weight, dQ, dK, dV, eps: flo
     return _launch(index, stream, call)
 
 
+def _readable(t):
+    """t, or a copy that the library reads: contiguous rows, strides and start
+    on 16 bytes, and (the dim before the last) no row repeated."""
+    step = 16 // t.element_size()
+    strides, shape = t.stride(), t.shape
+    ok = (strides[-1] == 1 and t.data_ptr() % 16 == 0 and (strides[-2] > 0 or shape[-2] == 1)
+          and all(s % step == 0 for s, n in zip(strides[:-1], shape) if n > 1))
+    return t if ok else t.clone(memory_format=torch.contiguous_format)
+
+
 class QkNormFunction(torch.autograd.Function):
     """Autograd wrapper: forward = fibatt_qk_norm_fwd, backward = fibatt_qk_norm_bwd."""
 
     @staticmethod
     def forward(ctx, x, q_weight, k_weight, heads, eps, rotary, positions, interleaved):
+        x = _readable(x)
         ctx.how = (tuple(heads), float(eps), rotary, positions, bool(interleaved))
         ctx.save_for_backward(x, q_weight, k_weight)
         ctx.set_materialize_grads(False)
@@ -571,14 +582,6 @@ def cross_bwd(Q, K, V, O, LSE, dO, scale: float, kv_len=None, key_mask=None, dQ=
         return dq, dk, dv
 
     return _launch(index, stream, call)
-
-
-def _readable(t):
-    """t, or a copy that the library reads: contiguous rows, strides and start
-    on 16 bytes."""
-    step = 16 // t.element_size()
-    ok = t.stride(-1) == 1 and t.data_ptr() % 16 == 0 and all(s % step == 0 for s, n in zip(t.stride()[:-1], t.shape) if n > 1)
-    return t if ok else t.clone(memory_format=torch.contiguous_format)
 
 
 class CrossAttentionFunction(torch.autograd.Function):

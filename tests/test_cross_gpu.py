@@ -331,6 +331,49 @@ def test_autograd_with_shared_states_and_odd_layouts(dtype):
     assert bool((kv.grad[..., 0] == 0).all())
 
 
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("Nq", [1, 50, 150])
+def test_heads_and_masks_that_are_broadcast(dtype, Nq):
+    # one row of queries (and of dO) for all heads, one key head for all, one mask for all sequences
+    g = torch.Generator(device="cuda").manual_seed(31)
+    q, do = (_rand(g, 2, 1, Nq, 64, dtype=dtype).expand(-1, 6, -1, -1) for _ in range(2))
+    k, v = (_rand(g, 2, 1, 140, 64, dtype=dtype).expand(-1, 3, -1, -1) for _ in range(2))
+    m = (torch.rand(1, 140, generator=g, device="cuda") < 0.6).expand(2, -1)
+    _check_all(q, k, v, do, 0.125, None, m)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("loss", ["sum", "mean over queries", "one head"])
+def test_gradients_that_arrive_broadcast(dtype, loss):
+    q, k, v, _ = (t.detach().clone().requires_grad_() for t in _inputs(dtype, 2, 4, 2, 20, 60))
+    w = torch.randn(2, 4, 64, generator=torch.Generator(device="cuda").manual_seed(4), device="cuda").to(dtype)
+    o = api.cross_attention(q, k, v)
+    if loss == "sum":
+        o.sum().backward()
+        do = torch.ones_like(o)
+    elif loss == "mean over queries":     # rows of dO with a stride of 0
+        (o.sum(2) * w).sum().backward()
+        do = w[:, :, None].expand_as(o)
+    else:
+        o[:, 1].sum().backward()
+        do = torch.zeros_like(o)
+        do[:, 1] = 1
+    want = cross(q.detach(), k.detach(), v.detach(), 0.125, None, None, do, o.detach())
+    for name, t in (("dQ", q), ("dK", k), ("dV", v)):
+        check(name, t.grad, want[name])
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("size", [(40, 2, 2, 150, 260), (6, 24, 2, 40, 700), (3, 12, 12, 1, 5000), (50, 12, 4, 6, 90), (2, 32, 2, 1, 300)],
+                         ids=lambda s: "x".join(map(str, s)))
+def test_more_units_than_the_gpu_holds(dtype, size):
+    # several units a block, of both kinds in the backward, some without keys; rows of shared heads from 6 to 18
+    q, k, v, do = _inputs(dtype, *size, seed=37)
+    n, _ = _masks("len", size[0], size[4], seed=3)
+    n[size[0] // 2] = 0
+    _check_all(q, k, v, do, 0.125, n)
+
+
 def test_gpu_refusals():
     q, k, v, do = _inputs(BF16, 2, 4, 2, 5, 9)
     with pytest.raises(ValueError, match="contiguous rows"):

@@ -195,6 +195,22 @@ def test_autograd(dtype):
     check("dx", x.grad, qk_norm(x.detach(), heads, wq.detach(), wk.detach(), 1e-6, rotary, None, False, zero)["dx"])
 
 
+def test_autograd_of_inputs_that_have_to_be_copied():
+    heads = (2, 1, 1)
+    g = torch.Generator(device="cuda").manual_seed(6)
+    base = torch.randn(2, 9, 4 * 64 + 1, generator=g, device="cuda", requires_grad=True)
+    grads = [torch.randn(2, h, 9, 64, generator=g, device="cuda") for h in heads]
+    x = base[..., 1:]                       # tokens off 16 bytes
+    torch.autograd.backward(list(api.qk_norm(x, heads)), grads)
+    want = qk_norm(x.detach(), heads, None, None, 1e-6, None, None, False, grads)
+    check("dx", base.grad[..., 1:], want["dx"])
+    y = torch.randn(1, 1, 4 * 64, generator=g, device="cuda", requires_grad=True)    # one token everywhere
+    torch.autograd.backward(list(api.qk_norm(y.expand(2, 9, -1), heads)), grads)
+    value, bound = qk_norm(y.detach().expand(2, 9, -1), heads, None, None, 1e-6, None, None, False, grads)["dx"]
+    # autograd's sum of eighteen: as many roundings of the largest partial sum
+    check("dx", y.grad, (value.sum((0, 1), keepdim=True), (bound + 18 * 2.0 ** -24 * value.abs()).sum((0, 1), keepdim=True)))
+
+
 def test_gpu_refusals():
     x, w, rotary, grads = _case(BF16, 2, 5, (2, 1, 1), 64)
     with pytest.raises(ValueError, match="values a token"):
