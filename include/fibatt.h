@@ -306,7 +306,8 @@ typedef struct {
  * the end; for fp32 products keep 22 bits of each operand (with more than eight
  * query rows to a key head), so that an infinite value that is attended may
  * give NaN where 24-bit products give infinity.  INVALID_ARG: a size or stride out of its range, a NULL or
- * misaligned pointer, a scale that is not finite, more than 2^31 - 1 blocks.
+ * misaligned pointer, a scale that is not finite, 2^31 query rows (a head's
+ * rounded up to 128) or more.
  * UNSUPPORTED: D, dtype. */
 fibatt_status fibatt_cross_fwd(const fibatt_cross *d, const fibatt_heads *Q, const fibatt_heads *K,
                                const fibatt_heads *V, const fibatt_heads *O, float *LSE,

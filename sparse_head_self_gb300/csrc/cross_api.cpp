@@ -66,8 +66,8 @@ fibatt_status check_cross(const fibatt_cross *d) {
     // blocks of the kernels: one a 64-row tile and head at most, times a cluster of eight
     const int64_t qb = (int64_t)d->B * d->Hq, kb = (int64_t)d->B * d->Hkv;
     if (qb > 0x7fffffffLL || qb * ((d->Nq + 63LL) / 64) > 0x7fffffffLL / 8 || kb * ((d->Nk + 63LL) / 64) > 0x7fffffffLL / 8 ||
-        qb * ((d->Nq + 15LL) / 16) > 0x7fffffffLL)
-        return invalid("too many rows for one call (2^31 - 1 blocks)");
+        qb * ((d->Nq + 127LL) / 128 * 128) > 0x7fffffffLL - 256)
+        return invalid("too many rows for one call (2^31 query rows, 2^31 - 1 blocks)");
     if (d->Nq > 0x7fffff00 || d->Nk > 0x7fffff00) return invalid("Nq and Nk must be below 2^31 - 256");
     if (fault("arg")) return invalid("injected argument fault (FIBATT_FAULT=arg)");
     return FIBATT_OK;

@@ -89,37 +89,38 @@ __device__ __forceinline__ uint4 three_parts(float x) {
 __device__ __forceinline__ uint4 no_query(float c) { return three_parts(-1000.f / c); }
 
 // (LSE log2 e, D = <dO, O>) of every query row, and -LSE log2 e / c and -D in
-// parts, rows padded to `npad` a head and 128 rows of no query at the end.  16
+// parts, rows padded to `npad` a head and 128 rows of no query at the end.  Eight
 // threads a row.
 __global__ void __launch_bounds__(256)
-cross_parts_kernel(int Hq, int Nq, int npad, int64_t rows, Rows<const __nv_bfloat16> O, Rows<const __nv_bfloat16> dO,
+cross_parts_kernel(int Hq, int Nq, int npad, unsigned rows, Rows<const __nv_bfloat16> O, Rows<const __nv_bfloat16> dO,
                    const float *__restrict__ LSE, float c, float2 *__restrict__ stats, uint4 *__restrict__ lse_parts,
                    uint4 *__restrict__ d_parts) {
     grid_dep_wait();
     grid_dep_launch();
-    const int64_t row = (int64_t)blockIdx.x * 16 + (threadIdx.x >> 4);
-    const int i = threadIdx.x & 15;
-    if (row >= rows + kTileRows) return;   // whole half warps: the shuffles below stay within 16 lanes
-    const int64_t bh = row / npad, n = row - bh * npad;
-    if (row >= rows || n >= Nq) {
+    const unsigned row = blockIdx.x * 32 + (threadIdx.x >> 3);
+    const int i = threadIdx.x & 7;
+    if (row >= rows + kTileRows) return;   // whole groups of eight: the shuffles below stay within them
+    const unsigned bh = row / (unsigned)npad, n = row - bh * npad;
+    if (row >= rows || n >= (unsigned)Nq) {
         if (i == 0) lse_parts[row] = no_query(c);
         if (i == 1) d_parts[row] = make_uint4(0, 0, 0, 0);
         return;
     }
-    const int64_t b = bh / Hq, h = bh - b * Hq;
-    const uint2 o = __ldg(reinterpret_cast<const uint2 *>(O.row(b, h, n)) + i);
-    const uint2 g = __ldg(reinterpret_cast<const uint2 *>(dO.row(b, h, n)) + i);
-    float d = dot2_bf16(o.x, g.x, dot2_bf16(o.y, g.y, 0.f));
-    const unsigned half = 0xffffu << (threadIdx.x & 16);
+    const unsigned b = bh / (unsigned)Hq, h = bh - b * Hq;
+    const uint4 o = __ldg(reinterpret_cast<const uint4 *>(O.row(b, h, n)) + i);
+    const uint4 g = __ldg(reinterpret_cast<const uint4 *>(dO.row(b, h, n)) + i);
+    const int64_t at = (int64_t)bh * Nq + n;
+    const float lse = __ldg(LSE + at);
+    float d = dot2_bf16(o.x, g.x, dot2_bf16(o.y, g.y, 0.f)) + dot2_bf16(o.z, g.z, dot2_bf16(o.w, g.w, 0.f));
+    const unsigned eight = 0xffu << (threadIdx.x & 24);
 #pragma unroll
-    for (int m = 1; m < 16; m <<= 1) d += __shfl_xor_sync(half, d, m);
-    const float lse = __ldg(LSE + bh * Nq + n);
+    for (int m = 1; m < 8; m <<= 1) d += __shfl_xor_sync(eight, d, m);
     // a row without keys: its weights are exp2(s - inf) = 0 (and no block meets it)
     const bool none = lse == -kInf;
     const float lse2 = none ? kInf : lse * kLog2e;
     if (i == 0) lse_parts[row] = none ? no_query(c) : three_parts(-lse2 / c);
     if (i == 1) d_parts[row] = three_parts(-d);
-    if (i == 2) stats[bh * Nq + n] = make_float2(lse2, d);
+    if (i == 2) stats[at] = make_float2(lse2, d);
 }
 
 // One unit of work: 128 rows of one side of one key/value head, and the part of
@@ -582,8 +583,8 @@ cudaError_t launch_cross_bwd_mma(const CrossArgs &a) {
     f.c = std::copysign(std::max(std::fabs(a.scale) * kLog2e, 1e-36f), a.scale);
     cudaError_t e = prepare_kernel<cross_bwd_mma_kernel>(kSmem, kRegs);
     if (e != cudaSuccess) return e;
-    e = launch_clusters(cross_parts_kernel, (unsigned)((rows + kTileRows + 15) / 16), 1, 256, 0, a.stream, a.Hq, a.Nq,
-                        f.npad, rows, rows_of<const __nv_bfloat16>(a.O), rows_of<const __nv_bfloat16>(a.dO),
+    e = launch_clusters(cross_parts_kernel, (unsigned)((rows + kTileRows + 31) / 32), 1, 256, 0, a.stream, a.Hq, a.Nq,
+                        f.npad, (unsigned)rows, rows_of<const __nv_bfloat16>(a.O), rows_of<const __nv_bfloat16>(a.dO),
                         static_cast<const float *>(a.LSE), f.c, stats, lse_parts, d_parts);
     if (e != cudaSuccess) return e;
     const int64_t key_units = (int64_t)a.B * a.Hkv * f.ktiles, units = key_units + (int64_t)a.B * a.Hkv * f.qt.tiles;
