@@ -9,6 +9,7 @@ from __future__ import annotations
 import ctypes
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import _native
 from ._native import FibattError, check, lib
@@ -299,6 +300,14 @@ def _index(name: str, t) -> int:
     return index
 
 
+def _workspace(ws, need: int, index: int):
+    """The caller's scratch memory, or fresh memory of `need` bytes."""
+    if ws is None:
+        return torch.empty(need, dtype=torch.uint8, device=f"cuda:{index}")
+    _check_dense("workspace", ws, ws.shape if isinstance(ws, torch.Tensor) else None, getattr(ws, "dtype", None), index)
+    return ws
+
+
 _device_of_thread = torch._C._cuda_getDevice
 _stream_of_thread = torch._C._cuda_getCurrentRawStream
 
@@ -307,6 +316,8 @@ def _launch(index: int, stream, call, *args):
     """call(*args, stream pointer) with the launching stream and its device
     current: what a call allocates then belongs to the stream that uses it."""
     if stream is not None:
+        if stream.device_index != index:
+            raise ValueError(f"stream is on cuda:{stream.device_index}, the tensors on cuda:{index}")
         with torch.cuda.stream(stream):
             return call(*args, stream.cuda_stream)
     if index != _device_of_thread():
@@ -434,9 +445,7 @@ def qk_norm_bwd(x: torch.Tensor, heads, q_weight, k_weight, dQ, dK, dV, eps: flo
         dx = torch.empty(x.shape, dtype=x.dtype, device=x.device)
         dqw = None if q_weight is None else torch.empty_like(q_weight)
         dkw = None if k_weight is None else torch.empty_like(k_weight)
-        ws = workspace
-        if ws is None:
-            ws = torch.empty(lib().fibatt_qk_norm_bwd_workspace_bytes(), dtype=torch.uint8, device=x.device)
+        ws = _workspace(workspace, lib().fibatt_qk_norm_bwd_workspace_bytes(), index)
         check(lib().fibatt_qk_norm_bwd(d, x.data_ptr(), sb, sn, *grads, dx.data_ptr(), dx.stride(0), dx.stride(1),
                                        None if dqw is None else dqw.data_ptr(), None if dkw is None else dkw.data_ptr(),
                                        ws.data_ptr(), ws.numel() * ws.element_size(), s))
@@ -461,17 +470,20 @@ class QkNormFunction(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, q_weight, k_weight, heads, eps, rotary, positions, interleaved):
         x = _readable(x)
-        ctx.how = (tuple(heads), float(eps), rotary, positions, bool(interleaved))
-        ctx.save_for_backward(x, q_weight, k_weight)
+        ctx.how = (tuple(heads), float(eps), bool(interleaved))
+        cos, sin = (None, None) if rotary is None else rotary
+        ctx.save_for_backward(x, q_weight, k_weight, cos, sin, positions)
         ctx.set_materialize_grads(False)
         out = qk_norm_fwd(x, heads, q_weight, k_weight, eps, rotary, positions, interleaved)
         ctx.shapes = [None if t is None else t.shape for t in out]
         return out
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, *grads):
-        x, q_weight, k_weight = ctx.saved_tensors
-        heads, eps, rotary, positions, interleaved = ctx.how
+        x, q_weight, k_weight, cos, sin, positions = ctx.saved_tensors
+        heads, eps, interleaved = ctx.how
+        rotary = None if cos is None else (cos, sin)
         grads = [g if s is None else torch.zeros(s, dtype=x.dtype, device=x.device) if g is None else g.contiguous()
                  for g, s in zip(grads, ctx.shapes)]
         dx, dqw, dkw = qk_norm_bwd(x, heads, q_weight, k_weight, *grads, eps, rotary, positions, interleaved)
@@ -482,7 +494,7 @@ def qk_norm(x, heads, q_weight=None, k_weight=None, eps: float = 1e-6, rotary=No
             interleaved: bool = False):
     """Differentiable norm of query and key heads with the position rotation:
     packed projection x [B, N, (Hq + Hk + Hv) * 64] -> (Q, K, V) as
-    qk_norm_fwd (gradients reach x and the weights)."""
+    qk_norm_fwd (gradients reach x and the weights; captured as cross_attention)."""
     return QkNormFunction.apply(x, q_weight, k_weight, tuple(int(h) for h in heads), float(eps), rotary, positions,
                                 bool(interleaved))
 
@@ -572,9 +584,7 @@ def cross_bwd(Q, K, V, O, LSE, dO, scale: float, kv_len=None, key_mask=None, dQ=
         dq = torch.empty_like(Q) if dQ is None else dQ
         dk = torch.empty_like(K) if dK is None else dK
         dv = torch.empty_like(V) if dV is None else dV
-        ws = workspace
-        if ws is None:
-            ws = torch.empty(lib().fibatt_cross_bwd_workspace_bytes(d), dtype=torch.uint8, device=Q.device)
+        ws = _workspace(workspace, lib().fibatt_cross_bwd_workspace_bytes(d), index)
         check(lib().fibatt_cross_bwd(d, q, k, v, o, LSE.data_ptr(), do, _heads_arg("dQ", dq, shape, dtype, index),
                                      _heads_arg("dK", dk, K.shape, dtype, index),
                                      _heads_arg("dV", dv, K.shape, dtype, index), ws.data_ptr(),
@@ -596,6 +606,7 @@ class CrossAttentionFunction(torch.autograd.Function):
         return O
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dO):
         Q, K, V, O, LSE, kv_len, key_mask = ctx.saved_tensors
         dQ, dK, dV = cross_bwd(Q, K, V, O, LSE, _readable(dO), ctx.scale, kv_len, key_mask)
@@ -604,7 +615,9 @@ class CrossAttentionFunction(torch.autograd.Function):
 
 def cross_attention(Q, K, V, scale: float | None = None, kv_len=None, key_mask=None):
     """Differentiable cross attention: Q [B, Hq, Nq, 64] on K, V [B, Hkv, Nk, 64]
-    (arguments as cross_fwd)."""
+    (arguments as cross_fwd).  To capture a backward pass into a graph, capture
+    its forward pass with it, with no eager graph of the same leaves alive: torch
+    would make their gradients wait on the stream of the eager pass."""
     if scale is None:
         scale = Q.shape[-1] ** -0.5
     return CrossAttentionFunction.apply(Q, K, V, float(scale), kv_len, key_mask)

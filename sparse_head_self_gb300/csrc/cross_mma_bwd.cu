@@ -77,9 +77,9 @@ struct Shared {
 };
 
 // x as the sum of three bf16 values, the first of eight elements of a row (cut to
-// what a bf16 holds: at a scale of 0, 1000 / c is beyond it).
+// what a bf16 holds: at a scale of 0, 1000 / c is beyond it; NaN stays).
 __device__ __forceinline__ uint4 three_parts(float x) {
-    x = fminf(fmaxf(x, -3.0e38f), 3.0e38f);
+    if (x == x) x = fminf(fmaxf(x, -3.0e38f), 3.0e38f);
     const float hi = __bfloat162float(__float2bfloat16_rn(x)), rest = x - hi;
     const float mid = __bfloat162float(__float2bfloat16_rn(rest));
     return make_uint4(pack_bf16x2(hi, mid), pack_bf16x2(rest - mid, 0.f), 0u, 0u);
@@ -326,8 +326,8 @@ __device__ __forceinline__ bool copies(const BwdMmaArgs &a, Shared &sh, const Ti
 }
 
 // Which keys of a streamed tile are attended; K's other rows, which are read across
-// with weights of 0, cleared.  (Streamed queries need nothing.)  false: a wait
-// gave up.
+// with weights of 0, cleared.  Of streamed queries, the rows behind the group's
+// last head, which are the next group's.  false: a wait gave up.
 template <bool KEYS>
 __device__ __forceinline__ bool prepare(const BwdMmaArgs &a, Shared &sh, const Tiles &tl, int unit, int &it) {
     volatile int *abort = &sh.abort;
@@ -335,9 +335,19 @@ __device__ __forceinline__ bool prepare(const BwdMmaArgs &a, Shared &sh, const T
     for (int j = 0; j < u.n; ++j, ++it) {
         const int s = it % kStages;
         uint4 w = make_uint4(0, 0, 0, 0);
+        int rows = kTileRows;
         if (!KEYS) w = tile_keys(a.ks, u.b, (u.lo + j) * kTileRows, u.bound);
+        else if (a.qt.first_head(u.lo + j) + a.qt.gb > a.qt.G) rows = (a.qt.G - a.qt.first_head(u.lo + j)) * a.qt.nb;
         if (!pipe_wait(&sh.full[s], (it / kStages) & 1, abort)) return false;
-        if (!KEYS) {
+        if (KEYS) {
+            if (rows < kTileRows) {
+                uint4 *q = reinterpret_cast<uint4 *>(tl.stage(s));       // 8 a row; dO's behind Q's
+                for (int i = 8 * rows + (int)(threadIdx.x & 31); i < 8 * kTileRows; i += 32)
+                    q[i] = q[i + kTileBytes / 16] = make_uint4(0, 0, 0, 0);
+                fence_smem_async();
+                __syncwarp();
+            }
+        } else {
             if (!all_keys(w)) {
                 clear_rows(tl.stage(s), w);
                 fence_smem_async();

@@ -397,3 +397,49 @@ def test_gpu_refusals():
     o, lse = api.cross_fwd(q, k, v, 0.125)
     with pytest.raises(api.FibattError, match="workspace"):
         api.cross_bwd(q, k, v, o, lse, do, 0.125, workspace=torch.empty(8, dtype=torch.uint8, device="cuda"))
+
+
+def test_workspaces_and_streams_of_other_places_are_refused():
+    q, k, v, do = _inputs(BF16, 2, 4, 2, 5, 9)
+    o, lse = api.cross_fwd(q, k, v, 0.125)
+    with pytest.raises(ValueError, match="workspace must be a CUDA tensor"):
+        api.cross_bwd(q, k, v, o, lse, do, 0.125, workspace=torch.empty(1 << 20, dtype=torch.uint8))
+    with pytest.raises(TypeError, match="workspace"):
+        api.cross_bwd(q, k, v, o, lse, do, 0.125, workspace=1 << 20)
+    with pytest.raises(ValueError, match="workspace must be contiguous"):
+        api.cross_bwd(q, k, v, o, lse, do, 0.125, workspace=torch.empty(1 << 20, 2, dtype=torch.uint8, device="cuda")[:, 0])
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("size", [(2, 6, 2, 50, 150), (1, 9, 3, 33, 300), (2, 10, 2, 1, 70)], ids=lambda s: "x".join(map(str, s)))
+@pytest.mark.parametrize("bad", [math.nan, 1e6])
+def test_other_groups_queries_reach_no_gradient(dtype, size, bad):
+    # a tile of query rows may end behind its group's last head
+    q, k, v, do = _inputs(dtype, *size, layout="bhnd", seed=41)
+    G = size[1] // size[2]
+    want = _run(q, k, v, do, 0.125)
+    q, do = q.clone(), do.clone()
+    q[:, G:] = bad
+    do[:, G:] = bad
+    got = _run(q, k, v, do, 0.125)
+    for name, n in (("O", G), ("LSE", G), ("dQ", G), ("dK", 1), ("dV", 1)):
+        assert torch.equal(got[name][:, :n], want[name][:, :n]), name
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("Nq", [1, 40, 200])
+def test_nan_in_attended_places_reaches_its_head(dtype, Nq):
+    q, k, v, do = _inputs(dtype, 2, 4, 2, Nq, 150, layout="bhnd", seed=43)
+    want = _run(q, k, v, do, 0.125)
+    k[0, 0, 5, 3] = math.nan
+    got = _run(q, k, v, do, 0.125)
+    for name, n in (("O", 2), ("LSE", 2), ("dQ", 2), ("dK", 1), ("dV", 1)):
+        assert bool(got[name][0, :n].isnan().all()), name
+        assert torch.equal(got[name][0, n:], want[name][0, n:]) and torch.equal(got[name][1], want[name][1]), name
+
+
+def test_gradients_of_gradients_are_refused():
+    q, k, v, _ = (t.detach().clone().requires_grad_() for t in _inputs(F32, 1, 2, 2, 5, 9))
+    dq, = torch.autograd.grad(api.cross_attention(q, k, v).square().sum(), q, create_graph=True)
+    with pytest.raises(RuntimeError, match="once_differentiable"):
+        dq.sum().backward()

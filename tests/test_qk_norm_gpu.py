@@ -229,3 +229,19 @@ def test_gpu_refusals():
         api.qk_norm_bwd(x, (2, 1, 1), *w, grads[0], grads[0], grads[2])
     with pytest.raises(api.FibattError, match="workspace"):
         api.qk_norm_bwd(x, (2, 1, 1), *w, *grads, workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
+
+
+def test_what_the_backward_reads_may_not_change_before_it():
+    x, w, rotary, _ = _case(BF16, 2, 5, (2, 1, 1), 64)
+    x = x.detach().requires_grad_()
+    pos = torch.arange(5, dtype=torch.int32, device="cuda")
+    q, _, _ = api.qk_norm(x, (2, 1, 1), *w, rotary=tuple(t.clone() for t in rotary), positions=pos)
+    pos -= 1
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        q.sum().backward()
+
+
+def test_workspaces_of_other_places_are_refused():
+    x, w, _, grads = _case(BF16, 2, 5, (2, 1, 1), 64)
+    with pytest.raises(ValueError, match="workspace must be a CUDA tensor"):
+        api.qk_norm_bwd(x, (2, 1, 1), *w, *grads, workspace=torch.empty(1 << 20, dtype=torch.uint8))
