@@ -63,7 +63,8 @@ struct BwdMmaArgs {
     int npad;                   // rows of a head there
     Rows<__nv_bfloat16> dQ, dK, dV;
     int B, Hq, Hkv, ktiles;
-    int key_units, units;       // units that hold keys, which come first, and all of them
+    int query_units, units;     // units that hold queries, which come first, and all of them
+    int *next_unit;             // units given out behind every CTA's first
     float scale;
     float c;                    // scale log2 e, not 0
     BwdMmaArgs() : qt(1, 1, false) {}
@@ -71,7 +72,9 @@ struct BwdMmaArgs {
 
 struct Shared {
     uint64_t held[2], held_free[2], full[kStages], ready[kStages], empty[kStages], s, sfree, p, done, end[2];
+    uint64_t unit_full[2], unit_empty[2];
     uint4 keys[kStages];
+    int unit[2];                // the CTA's next, in turn
     uint32_t tmem;
     int abort;
 };
@@ -94,11 +97,12 @@ __device__ __forceinline__ uint4 no_query(float c) { return three_parts(-1000.f 
 __global__ void __launch_bounds__(256)
 cross_parts_kernel(int Hq, int Nq, int npad, unsigned rows, Rows<const __nv_bfloat16> O, Rows<const __nv_bfloat16> dO,
                    const float *__restrict__ LSE, float c, float2 *__restrict__ stats, uint4 *__restrict__ lse_parts,
-                   uint4 *__restrict__ d_parts) {
+                   uint4 *__restrict__ d_parts, int *__restrict__ next_unit) {
     grid_dep_wait();
     grid_dep_launch();
     const unsigned row = blockIdx.x * 32 + (threadIdx.x >> 3);
     const int i = threadIdx.x & 7;
+    if (blockIdx.x == 0 && threadIdx.x == 0) *next_unit = 0;
     if (row >= rows + kTileRows) return;   // whole groups of eight: the shuffles below stay within them
     const unsigned bh = row / (unsigned)npad, n = row - bh * npad;
     if (row >= rows || n >= (unsigned)Nq) {
@@ -326,8 +330,8 @@ __device__ __forceinline__ bool copies(const BwdMmaArgs &a, Shared &sh, const Ti
 }
 
 // Which keys of a streamed tile are attended; K's other rows, which are read across
-// with weights of 0, cleared.  Of streamed queries, the rows behind the group's
-// last head, which are the next group's.  false: a wait gave up.
+// with weights of 0, cleared.  Of streamed queries, the rows behind the tile's last,
+// which hold what was there before or the next group's.  false: a wait gave up.
 template <bool KEYS>
 __device__ __forceinline__ bool prepare(const BwdMmaArgs &a, Shared &sh, const Tiles &tl, int unit, int &it) {
     volatile int *abort = &sh.abort;
@@ -337,7 +341,7 @@ __device__ __forceinline__ bool prepare(const BwdMmaArgs &a, Shared &sh, const T
         uint4 w = make_uint4(0, 0, 0, 0);
         int rows = kTileRows;
         if (!KEYS) w = tile_keys(a.ks, u.b, (u.lo + j) * kTileRows, u.bound);
-        else if (a.qt.first_head(u.lo + j) + a.qt.gb > a.qt.G) rows = (a.qt.G - a.qt.first_head(u.lo + j)) * a.qt.nb;
+        else rows = min(a.qt.gb, a.qt.G - a.qt.first_head(u.lo + j)) * a.qt.nb;
         if (!pipe_wait(&sh.full[s], (it / kStages) & 1, abort)) return false;
         if (KEYS) {
             if (rows < kTileRows) {
@@ -470,6 +474,8 @@ __global__ void __launch_bounds__(kThreads, 1) cross_bwd_mma_kernel(const __grid
             mbar_init(&sh.held[i], 1);
             mbar_init(&sh.held_free[i], 1);
             mbar_init(&sh.end[i], 1);
+            mbar_init(&sh.unit_full[i], 1);
+            mbar_init(&sh.unit_empty[i], kWeightWarps + 3);
         }
         for (int s = 0; s < kStages; ++s) {
             mbar_init(&sh.full[s], 1);
@@ -487,12 +493,6 @@ __global__ void __launch_bounds__(kThreads, 1) cross_bwd_mma_kernel(const __grid
         prefetch_map(&a.v.map);
     }
     if (warp == kSumWarp) tmem_alloc(&sh.tmem, kCols);
-    // A query tile of fewer than 128 rows leaves the end of its stage as it is: zeros
-    // there, so that weights of 0 meet no NaN (such a CTA's units that hold keys
-    // come before those that stream them).
-    if (a.qt.nb * a.qt.gb < kTileRows)
-        for (int i = threadIdx.x; i < 2 * kStages * kTileBytes / 16; i += kThreads)
-            reinterpret_cast<uint4 *>(tl.ring)[i] = make_uint4(0, 0, 0, 0);
     // ones in the first three elements of a row; rows of no query until copies bring some
     const uint4 none = no_query(a.c);
     for (int i = threadIdx.x; i < (2 + 2 * kStages) * kTileRows; i += kThreads) {
@@ -509,40 +509,70 @@ __global__ void __launch_bounds__(kThreads, 1) cross_bwd_mma_kernel(const __grid
     grid_dep_wait();
     grid_dep_launch();
 
-    // the CTA's units: those that hold keys, then those that hold queries
-    const int CS = (int)cluster_size(), first = (int)(blockIdx.x / CS), step = (int)(gridDim.x / CS);
-    const auto each = [&](auto keys, auto queries) {
+    // The CTA's units: its first, then what it draws from a counter, which the copying
+    // warp does and passes on (CTAs that finish early take more; a unit's results do
+    // not depend on who works on it).  A cluster has one unit.
+    const int CS = (int)cluster_size(), first = (int)(blockIdx.x / CS);
+    const auto each = [&](auto next, auto queries, auto keys) {
         int u = first;
 #pragma unroll 1
-        for (; u < a.key_units; u += step) keys(u);
+        for (; u < a.query_units; u = next()) queries(u);
 #pragma unroll 1
-        for (; u < a.units; u += step) queries(u - a.key_units);
+        for (; u < a.units; u = next()) keys(u - a.query_units);
+    };
+    int passed = 0;         // units handed over
+    const auto take = [&] {
+        const int i = passed & 1;
+        int u = a.units;
+        if (pipe_wait(&sh.unit_full[i], (passed >> 1) & 1, &sh.abort)) u = *(volatile int *)&sh.unit[i];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.unit_empty[i]);
+        ++passed;
+        return __shfl_sync(kFullMask, u, 0);
     };
     int it = 0, units = 0;
     if (warp < kWeightWarps) {
         take_registers<kRegsMany>();
-        each([&](int u) { it = weights<true>(a, sh, tl.ring, u, it); }, [&](int u) { it = weights<false>(a, sh, tl.ring, u, it); });
+        each(take, [&](int u) { it = weights<false>(a, sh, tl.ring, u, it); },
+             [&](int u) { it = weights<true>(a, sh, tl.ring, u, it); });
     } else {
         give_registers<kRegsFew>();
         if (warp == kCopyWarp) {
             bool ok = true;
-            each([&](int u) { ok = ok && copies<true>(a, sh, tl, u, it, units); },
-                 [&](int u) { ok = ok && copies<false>(a, sh, tl, u, it, units); });
+            int drawn = 0;
+            const auto draw = [&] {      // its answer is not needed before this unit's copies are out
+                drawn = a.units;
+                if (CS == 1 && lane == 0) drawn = (int)gridDim.x + atomicAdd(a.next_unit, 1);
+            };
+            const auto pass = [&] {
+                const int i = passed & 1, u = __shfl_sync(kFullMask, drawn, 0);
+                ok = ok && (passed < 2 || pipe_wait(&sh.unit_empty[i], ((passed >> 1) - 1) & 1, &sh.abort));
+                if (!ok) return a.units;
+                if (lane == 0) {
+                    *(volatile int *)&sh.unit[i] = u;
+                    mbar_arrive(&sh.unit_full[i]);
+                }
+                __syncwarp();
+                ++passed;
+                return u;
+            };
+            each(pass, [&](int u) { draw(); ok = ok && copies<false>(a, sh, tl, u, it, units); },
+                 [&](int u) { draw(); ok = ok && copies<true>(a, sh, tl, u, it, units); });
             if (lane == 0) {   // leave no copy in flight
                 for (int i = max(0, units - 2); i < units; ++i) mbar_drain(&sh.held[i & 1], (i >> 1) & 1);
                 for (int i = max(0, it - kStages); i < it; ++i) mbar_drain(&sh.full[i % kStages], (i / kStages) & 1);
             }
         } else if (warp == kPrepWarp) {
             bool ok = true;
-            each([&](int u) { ok = ok && prepare<true>(a, sh, tl, u, it); },
-                 [&](int u) { ok = ok && prepare<false>(a, sh, tl, u, it); });
+            each(take, [&](int u) { ok = ok && prepare<false>(a, sh, tl, u, it); },
+                 [&](int u) { ok = ok && prepare<true>(a, sh, tl, u, it); });
         } else {
             Turn at;
             if (warp == kScoreWarp)
-                each([&](int u) { scores<true>(a, sh, tl, u, it, units, at); },
-                     [&](int u) { scores<false>(a, sh, tl, u, it, units, at); });
+                each(take, [&](int u) { scores<false>(a, sh, tl, u, it, units, at); },
+                     [&](int u) { scores<true>(a, sh, tl, u, it, units, at); });
             else
-                each([&](int u) { sums<true>(a, sh, tl, u, it, at); }, [&](int u) { sums<false>(a, sh, tl, u, it, at); });
+                each(take, [&](int u) { sums<false>(a, sh, tl, u, it, at); }, [&](int u) { sums<true>(a, sh, tl, u, it, at); });
             // no matrix instruction in flight when the tensor memory is freed
             uint64_t *end = &sh.end[warp == kSumWarp];
             if (elect_one()) mma_commit(end);
@@ -556,7 +586,8 @@ __global__ void __launch_bounds__(kThreads, 1) cross_bwd_mma_kernel(const __grid
     if (warp == kSumWarp) tmem_free(sh.tmem, kCols);
     if (CS == 1) return;
     cluster_sync();
-    each([&](int u) { join<true>(a, tl, u); }, [&](int u) { join<false>(a, tl, u); });
+    if (first < a.query_units) join<false>(a, tl, first);
+    else join<true>(a, tl, first - a.query_units);
     cluster_sync();   // the others may still read this CTA's part
 }
 
@@ -567,7 +598,7 @@ int padded_rows(int Nq) { return Nq < kTileRows ? Nq : (Nq + kTileRows - 1) / kT
 
 size_t cross_bwd_mma_workspace(int B, int Hq, int Nq) {
     const size_t rows = (size_t)B * Hq * padded_rows(Nq);
-    return 2 * (rows + kTileRows) * sizeof(uint4) + (size_t)B * Hq * Nq * sizeof(float2);
+    return 2 * (rows + kTileRows) * sizeof(uint4) + (size_t)B * Hq * Nq * sizeof(float2) + sizeof(int);
 }
 
 cudaError_t launch_cross_bwd_mma(const CrossArgs &a) {
@@ -584,6 +615,7 @@ cudaError_t launch_cross_bwd_mma(const CrossArgs &a) {
     uint4 *lse_parts = reinterpret_cast<uint4 *>(a.stats), *d_parts = lse_parts + rows + kTileRows;
     float2 *stats = reinterpret_cast<float2 *>(d_parts + rows + kTileRows);
     f.stats = stats;
+    f.next_unit = reinterpret_cast<int *>(stats + (int64_t)a.B * a.Hq * a.Nq);
     f.lse_parts = lse_parts, f.d_parts = d_parts;
     f.dQ = rows_of<__nv_bfloat16>(a.dQ), f.dK = rows_of<__nv_bfloat16>(a.dK), f.dV = rows_of<__nv_bfloat16>(a.dV);
     f.B = a.B, f.Hq = a.Hq, f.Hkv = a.Hkv;
@@ -595,10 +627,10 @@ cudaError_t launch_cross_bwd_mma(const CrossArgs &a) {
     if (e != cudaSuccess) return e;
     e = launch_clusters(cross_parts_kernel, (unsigned)((rows + kTileRows + 31) / 32), 1, 256, 0, a.stream, a.Hq, a.Nq,
                         f.npad, (unsigned)rows, rows_of<const __nv_bfloat16>(a.O), rows_of<const __nv_bfloat16>(a.dO),
-                        static_cast<const float *>(a.LSE), f.c, stats, lse_parts, d_parts);
+                        static_cast<const float *>(a.LSE), f.c, stats, lse_parts, d_parts, f.next_unit);
     if (e != cudaSuccess) return e;
-    const int64_t key_units = (int64_t)a.B * a.Hkv * f.ktiles, units = key_units + (int64_t)a.B * a.Hkv * f.qt.tiles;
-    f.key_units = (int)key_units;
+    const int64_t query_units = (int64_t)a.B * a.Hkv * f.qt.tiles, units = query_units + (int64_t)a.B * a.Hkv * f.ktiles;
+    f.query_units = (int)query_units;
     f.units = (int)units;
     // clusters, one unit each, while they all find a place; else one wave of CTAs that walk over the units
     int c = 1;
