@@ -43,6 +43,7 @@ struct Cfg {
     static constexpr uint32_t kCols = NT * 256;        // S 128, P 64, O 64 a tile
     static constexpr size_t kSmem = 1024 + NT * kTileBytes + kStages * 2 * kTileBytes;
     static constexpr int kMinBlocks = NT == 2 ? 1 : 2;
+    static constexpr bool kWalks = NT == 1;            // one wave of CTAs for all units
     // registers a thread: at launch, and after the softmax warps took what the others gave
     static constexpr int kRegs = NT == 2 ? 96 : 80, kRegsFew = 32, kRegsMany = NT == 2 ? 112 : 104;
     static_assert(2 * NT * kRegsMany + kRegsFew == (2 * NT + 1) * kRegs, "the shares add up");
@@ -57,9 +58,34 @@ struct FwdMmaArgs {
     float *LSE;
     int Hq, Hkv;
     int pairs;               // NT-tile units of one key/value head
+    int units;               // of all heads and sequences
     float c;                 // |scale| log2 e (> 0)
     int negative;            // scale < 0
     FwdMmaArgs() : qt(1, 1, false) {}
+};
+
+// One unit of work: NT query tiles of one key/value head, ...
+template <int NT>
+struct Place {
+    int t0, nt, hk, b;
+    __device__ __forceinline__ Place(const FwdMmaArgs &a, int unit) {
+        t0 = unit % a.pairs * NT;
+        hk = unit / a.pairs % a.Hkv;
+        b = unit / a.pairs / a.Hkv;
+        nt = min(NT, a.qt.tiles - t0);      // tiles of this unit
+    }
+};
+// ... and the part of its sequence's key tiles that this CTA of the cluster walks
+// over.  Every warp works it out for itself.
+template <int NT>
+struct Unit : Place<NT> {
+    int bound, lo, n;
+    __device__ __forceinline__ Unit(const FwdMmaArgs &a, const Place<NT> &p) : Place<NT>(p) {
+        bound = a.ks.bound(p.b);
+        const int ktiles = (bound + kTileRows - 1) / kTileRows, CS = (int)cluster_size(), rank = (int)cluster_rank();
+        lo = (int)((int64_t)ktiles * rank / CS);
+        n = (int)((int64_t)ktiles * (rank + 1) / CS) - lo;
+    }
 };
 
 template <int NT>
@@ -69,23 +95,26 @@ cross_fwd_mma_kernel(const __grid_constant__ FwdMmaArgs a) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
     uint8_t *sq = smem, *skv = smem + NT * kTileBytes;   // stage s: K at skv + 2 s tiles, V behind it
-    __shared__ uint64_t bar_q, bar_full[C::kStages], bar_ready[C::kStages], bar_empty[C::kStages];
+    __shared__ uint64_t bar_q, bar_qfree, bar_full[C::kStages], bar_ready[C::kStages], bar_empty[C::kStages];
     __shared__ uint64_t bar_s[NT], bar_sfree[NT], bar_p[NT], bar_o[NT], bar_end[2];
     __shared__ uint4 keys[C::kStages];
     __shared__ uint32_t tmem_base;
     __shared__ int abort_flag;
     __shared__ float join_m[NT * kTileRows], join_l[NT * kTileRows];
-    __shared__ float half_of[2][2][NT * kTileRows];    // [turn][half]: what the halves of a row exchange
+    // what the halves of a row exchange: maxima, [turn][half], and sums at a unit's end
+    __shared__ float half_of[2][2][NT * kTileRows], sum_of[2][NT * kTileRows];
     volatile int *abort = &abort_flag;
 
     const int warp = warp_number(), lane = threadIdx.x & 31;
     const int CS = (int)cluster_size(), rank = (int)cluster_rank();
-    const int64_t unit = blockIdx.x / CS;
-    const int pair = (int)(unit % a.pairs), hk = (int)(unit / a.pairs % a.Hkv), b = (int)(unit / a.pairs / a.Hkv);
-    const int t0 = pair * NT, nt = min(NT, a.qt.tiles - t0);   // tiles of this unit
+    // the CTA's units: a cluster has one, the CTAs of one wave walk over all of them
+    const int first = (int)(blockIdx.x / CS), step = (int)(gridDim.x / CS);
+    const Place<NT> first_place(a, first);
+    const auto place = [&](int unit) { return C::kWalks && unit != first ? Place<NT>(a, unit) : first_place; };
 
     if (threadIdx.x == 0) {
         mbar_init(&bar_q, 1);
+        mbar_init(&bar_qfree, 1);
         for (int s = 0; s < C::kStages; ++s) {
             mbar_init(&bar_full[s], 1);
             mbar_init(&bar_ready[s], 1);
@@ -113,9 +142,10 @@ cross_fwd_mma_kernel(const __grid_constant__ FwdMmaArgs a) {
 
     grid_dep_wait();
     grid_dep_launch();
-    const int bound = a.ks.bound(b), ktiles = (bound + kTileRows - 1) / kTileRows;
-    const int lo = (int)((int64_t)ktiles * rank / CS), n = (int)((int64_t)ktiles * (rank + 1) / CS) - lo;
 
+    // `ring` counts the key tiles over all units of the CTA: tile `ring` is in stage
+    // ring mod kStages.  A query tile's barriers complete a phase for each key tile of
+    // the units that have it, which `it` counts.
     if (warp < C::kSoftmaxWarps) {
         take_registers<C::kRegsMany>();
         // ---- softmax: two threads a row, in warps four apart, 64 columns each ----------------------
@@ -126,11 +156,24 @@ cross_fwd_mma_kernel(const __grid_constant__ FwdMmaArgs a) {
         const uint32_t lanes = (uint32_t)quarter << 21;   // 32 lanes, in the upper 16 bits
         const uint32_t ts = col_s + t * 128 + 64 * half + lanes, tp = col_p + t * 64 + 32 * half + lanes;
         const uint32_t to = col_o + t * 64 + 32 * half + lanes;
-        float m = kNegInf, l = 0.f;
-        uint32_t o[32];
-        if (t < nt) {
-            for (int j = 0; j < n; ++j) {
-                pipe_wait(&bar_s[t], j & 1, abort);
+        int it = 0, skipped = 0;
+#pragma unroll 1
+        for (int unit = first; C::kWalks ? unit < a.units : unit == first; unit = C::kWalks ? unit + step : -1) {
+            // (of the unit, only this is needed within the loop, which has no register to spare)
+            int n, whole;      // key tiles; the first of them are attended wholly
+            {
+                const Unit<NT> u(a, place(unit));
+                if (t >= u.nt) {
+                    skipped += u.n;
+                    continue;
+                }
+                n = u.n;
+                whole = a.ks.mask ? 0 : u.bound / kTileRows - u.lo;
+            }
+            float m = kNegInf, l = 0.f;
+            uint32_t o[32];
+            for (int j = 0; j < n; ++j, ++it) {
+                pipe_wait(&bar_s[t], it & 1, abort);
                 tc_after_sync();
                 uint32_t s[2][32];
                 tmem_ld32(s[0], ts);
@@ -140,9 +183,9 @@ cross_fwd_mma_kernel(const __grid_constant__ FwdMmaArgs a) {
                 tc_before_sync();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bar_sfree[t]);
-                if (a.ks.mask || (lo + j + 1) * kTileRows > bound) {
-                    const int st = j % C::kStages;
-                    pipe_wait(&bar_ready[st], (j / C::kStages) & 1, abort);   // keys[st] is written
+                if (j >= whole) {
+                    const int ring = it + skipped, st = ring % C::kStages;
+                    pipe_wait(&bar_ready[st], (ring / C::kStages) & 1, abort);   // keys[st] is written
                     const uint4 w = keys[st];
                     const uint32_t words[2] = {half ? w.z : w.x, half ? w.w : w.y};
 #pragma unroll
@@ -161,10 +204,10 @@ cross_fwd_mma_kernel(const __grid_constant__ FwdMmaArgs a) {
                     top[i] = fmaxf(top[i], __uint_as_float(x[15]));
                 }
                 const float mine = fmaxf(max3(top[0], top[1], top[2]), top[3]);
-                half_of[j & 1][half][at] = mine;
+                half_of[it & 1][half][at] = mine;
                 named_sync(pair_bar, 64);
-                const float next = fmaxf(mine, half_of[j & 1][half ^ 1][at]) * a.c;
-                const bool free = j == 0 || pipe_ready(&bar_o[t], (j - 1) & 1);
+                const float next = fmaxf(mine, half_of[it & 1][half ^ 1][at]) * a.c;
+                const bool free = j == 0 || pipe_ready(&bar_o[t], (it - 1) & 1);
                 const bool raise = next > m + kRaise;     // also the first finite maximum: m = -inf
                 const float keep = raise ? fast_exp2(m - next) : 1.f;
                 if (raise) m = next;
@@ -181,7 +224,7 @@ cross_fwd_mma_kernel(const __grid_constant__ FwdMmaArgs a) {
                     p[k] = pack_bf16x2(y.x, y.y);
                 }
                 // the product with the last P has read it and written O
-                if (!free) pipe_wait(&bar_o[t], (j - 1) & 1, abort);
+                if (!free) pipe_wait(&bar_o[t], (it - 1) & 1, abort);
                 tc_after_sync();
                 if (j > 0 && __any_sync(kFullMask, raise)) {
                     l *= keep;
@@ -199,26 +242,28 @@ cross_fwd_mma_kernel(const __grid_constant__ FwdMmaArgs a) {
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bar_p[t]);
             }
-            half_of[n & 1][half][at] = l;
-            named_sync(pair_bar, 64);
-            l += half_of[n & 1][half ^ 1][at];
             if (n > 0) {
-                pipe_wait(&bar_o[t], (n - 1) & 1, abort);
+                sum_of[half][at] = l;
+                named_sync(pair_bar, 64);
+                l += sum_of[half ^ 1][at];
+                pipe_wait(&bar_o[t], (it - 1) & 1, abort);
                 tc_after_sync();
                 tmem_ld32(o, to);
                 tmem_wait_ld(o);
+                tc_before_sync();
             } else {
 #pragma unroll
                 for (int k = 0; k < 32; ++k) o[k] = 0u;
             }
-        }
-        int g, q;
-        const bool row = t < nt && a.qt.at(t0 + t, r, g, q);
-        if (CS == 1) {
-            if (row) {
-                const int h = hk * a.qt.G + g;
+            int again = unit;
+            if (C::kWalks) asm volatile("" : "+r"(again));      // worked out anew, not kept over the loop
+            const Unit<NT> u(a, place(again));
+            if (CS == 1) {
+                int g, q;
+                if (!a.qt.at(u.t0 + t, r, g, q)) continue;
+                const int h = u.hk * a.qt.G + g;
                 const float inv = l == 0.f ? 0.f : 1.f / l;
-                uint4 *out = reinterpret_cast<uint4 *>(a.O.row(b, h, q) + 32 * half);
+                uint4 *out = reinterpret_cast<uint4 *>(a.O.row(u.b, h, q) + 32 * half);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     uint32_t w[4];
@@ -227,121 +272,162 @@ cross_fwd_mma_kernel(const __grid_constant__ FwdMmaArgs a) {
                         w[k] = pack_bf16x2(__uint_as_float(o[8 * i + 2 * k]) * inv, __uint_as_float(o[8 * i + 2 * k + 1]) * inv);
                     out[i] = make_uint4(w[0], w[1], w[2], w[3]);
                 }
-                if (half == 0) a.LSE[((int64_t)b * a.Hq + h) * a.qt.Nq + q] = l == 0.f ? kNegInf : (m + log2f(l)) * kLn2;
-            }
-        } else if (t < nt) {
-            // every copy and product of this tile has completed (bar_o); the other
-            // tile's may still read the ring, so a barrier of both comes first
-            named_sync(2, 32 * 8 * nt);
-            float4 *out =
-                reinterpret_cast<float4 *>(reinterpret_cast<float *>(smem) + (t * kTileRows + r) * kJoinLd + 32 * half);
+                if (half == 0) a.LSE[((int64_t)u.b * a.Hq + h) * a.qt.Nq + q] = l == 0.f ? kNegInf : (m + log2f(l)) * kLn2;
+            } else {
+                // every copy and product of this tile has completed (bar_o); the other
+                // tile's may still read the ring, so a barrier of both comes first
+                named_sync(2, 32 * 8 * u.nt);
+                float4 *out =
+                    reinterpret_cast<float4 *>(reinterpret_cast<float *>(smem) + (t * kTileRows + r) * kJoinLd + 32 * half);
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-                out[i] = make_float4(__uint_as_float(o[4 * i]), __uint_as_float(o[4 * i + 1]), __uint_as_float(o[4 * i + 2]),
-                                     __uint_as_float(o[4 * i + 3]));
-            if (half == 0) {
-                join_m[t * kTileRows + r] = m;
-                join_l[t * kTileRows + r] = l;
+                for (int i = 0; i < 8; ++i)
+                    out[i] = make_float4(__uint_as_float(o[4 * i]), __uint_as_float(o[4 * i + 1]),
+                                         __uint_as_float(o[4 * i + 2]), __uint_as_float(o[4 * i + 3]));
+                if (half == 0) {
+                    join_m[t * kTileRows + r] = m;
+                    join_l[t * kTileRows + r] = l;
+                }
             }
         }
     } else {
         give_registers<C::kRegsFew>();
         if (warp == C::kCopyWarp) {
-            // ---- copies -----------------------------------------------------------
-            if (n > 0) {
-                int issued = 0;
-                const auto issue = [&](int j) {   // key tile j into its stage
-                    const int s = j % C::kStages;
-                    if (elect_one()) {
-                        mbar_expect_tx(&bar_full[s], 2 * kTileBytes);
-                        load_tile(skv + (2 * s) * kTileBytes, a.k, (lo + j) * kTileRows, hk, b, &bar_full[s]);
-                        load_tile(skv + (2 * s + 1) * kTileBytes, a.v, (lo + j) * kTileRows, hk, b, &bar_full[s]);
-                    }
-                    __syncwarp();
-                };
+            // ---- copies: they run ahead into the next unit ------------------------------
+            int ring = 0, units = 0;      // issued: key tiles, units' queries
+            bool ok = true;
+            const auto queries = [&](const Unit<NT> &u) {
                 if (elect_one()) {
-                    mbar_expect_tx(&bar_q, nt * a.qt.bytes());
-                    for (int t = 0; t < nt; ++t)
-                        load_tile(sq + t * kTileBytes, a.q, a.qt.first_row(t0 + t), hk * a.qt.G + a.qt.first_head(t0 + t), b,
-                                  &bar_q);
+                    mbar_expect_tx(&bar_q, u.nt * a.qt.bytes());
+                    for (int t = 0; t < u.nt; ++t)
+                        load_tile(sq + t * kTileBytes, a.q, a.qt.first_row(u.t0 + t), u.hk * a.qt.G + a.qt.first_head(u.t0 + t),
+                                  u.b, &bar_q);
                 }
                 __syncwarp();
-                for (; issued < n; ++issued) {
-                    const int last = issued - C::kStages;     // the stage's tile before
-                    if (last >= 0 && !pipe_wait(&bar_empty[last % C::kStages], (last / C::kStages) & 1, abort)) break;
-                    issue(issued);
+                ++units;
+            };
+#pragma unroll 1
+            for (int unit = first; ok && (C::kWalks ? unit < a.units : unit == first); unit = C::kWalks ? unit + step : -1) {
+                const Unit<NT> u(a, place(unit));
+                const bool later = C::kWalks && units > 0;
+                for (int j = 0; ok && j < u.n; ++j) {
+                    if (j == 0 && !later) queries(u);
+                    const int s = ring % C::kStages;
+                    ok = ring < C::kStages || pipe_wait(&bar_empty[s], (ring / C::kStages - 1) & 1, abort);
+                    if (!ok) break;
+                    if (elect_one()) {
+                        mbar_expect_tx(&bar_full[s], 2 * kTileBytes);
+                        load_tile(skv + (2 * s) * kTileBytes, a.k, (u.lo + j) * kTileRows, u.hk, u.b, &bar_full[s]);
+                        load_tile(skv + (2 * s + 1) * kTileBytes, a.v, (u.lo + j) * kTileRows, u.hk, u.b, &bar_full[s]);
+                    }
+                    __syncwarp();
+                    ++ring;
+                    if (j == 0 && later) {      // once the scores have read the last queries
+                        ok = pipe_wait(&bar_qfree, (units - 1) & 1, abort);
+                        if (ok) queries(u);
+                    }
                 }
-                // leave no copy in flight
-                if (lane == 0) {
-                    mbar_drain(&bar_q, 0);
-                    for (int j = max(0, issued - C::kStages); j < issued; ++j)
-                        mbar_drain(&bar_full[j % C::kStages], (j / C::kStages) & 1);
-                }
+            }
+            // leave no copy in flight
+            if (lane == 0) {
+                if (units > 0) mbar_drain(&bar_q, (units - 1) & 1);
+                for (int i = max(0, ring - C::kStages); i < ring; ++i)
+                    mbar_drain(&bar_full[i % C::kStages], (i / C::kStages) & 1);
             }
         } else if (warp == C::kKeysWarp) {
             // ---- which keys of each tile are attended; the others' value rows cleared ----
-            for (int j = 0; j < n; ++j) {
-                const int s = j % C::kStages;
-                const uint4 w = tile_keys(a.ks, b, (lo + j) * kTileRows, bound);
-                if (!pipe_wait(&bar_full[s], (j / C::kStages) & 1, abort)) break;
-                if (!all_keys(w)) {
-                    clear_rows(skv + (2 * s + 1) * kTileBytes, w);
-                    fence_smem_async();
-                }
-                __syncwarp();
-                if (lane == 0) {
-                    keys[s] = w;
-                    mbar_arrive(&bar_ready[s]);
+            int ring = 0;
+            bool ok = true;
+#pragma unroll 1
+            for (int unit = first; ok && (C::kWalks ? unit < a.units : unit == first); unit = C::kWalks ? unit + step : -1) {
+                const Unit<NT> u(a, place(unit));
+                for (int j = 0; j < u.n; ++j, ++ring) {
+                    const int s = ring % C::kStages;
+                    const uint4 w = tile_keys(a.ks, u.b, (u.lo + j) * kTileRows, u.bound);
+                    ok = pipe_wait(&bar_full[s], (ring / C::kStages) & 1, abort);
+                    if (!ok) break;
+                    if (!all_keys(w)) {
+                        clear_rows(skv + (2 * s + 1) * kTileBytes, w);
+                        fence_smem_async();
+                    }
+                    __syncwarp();
+                    if (lane == 0) {
+                        keys[s] = w;
+                        mbar_arrive(&bar_ready[s]);
+                    }
                 }
             }
         } else {
             // ---- matrix instructions: the scores by one warp, the values by another, so that
             // neither waits for what the other needs.  The loops' course depends on uniform values
             // only, which keeps descriptors and counters in uniform registers.
-            const int nu = __shfl_sync(kFullMask, n, 0), ntu = __shfl_sync(kFullMask, nt, 0);
-            int s = 0, ring = 0;                    // stage of tile j and its pass through the ring
+            int s = 0, pass = 0;                    // stage of the key tile and its pass through the ring
+            int it[NT];
+#pragma unroll
+            for (int t = 0; t < NT; ++t) it[t] = 0;
             if (warp == C::kScoreWarp) {
                 const uint32_t id = mma_desc(128, 128, false, a.negative);
                 const uint64_t dq = tile_desc(sq), dk = tile_desc(skv);
-                if (nu > 0) pipe_wait(&bar_q, 0, abort);
-                for (int j = 0; j < nu; ++j) {
-                    pipe_wait(&bar_ready[s], ring, abort);
-                    const uint64_t dks = dk + (uint64_t)(s * (2 * kTileBytes >> 4));
-                    for (int t = 0; t < ntu; ++t) {   // S_t = Q_t K_j^T
-                        if (j > 0) pipe_wait(&bar_sfree[t], (j - 1) & 1, abort);
-                        tc_after_sync();
-                        const uint64_t dqt = dq + (uint64_t)(t * (kTileBytes >> 4));
-                        if (elect_one()) {
+                int units = 0;
+#pragma unroll 1
+                for (int unit = first; C::kWalks ? unit < a.units : unit == first; unit = C::kWalks ? unit + step : -1) {
+                    const Unit<NT> u(a, place(unit));
+                    const int n = __shfl_sync(kFullMask, u.n, 0), nt = __shfl_sync(kFullMask, u.nt, 0);
+                    if (n > 0) pipe_wait(&bar_q, units++ & 1, abort);
+                    for (int j = 0; j < n; ++j) {
+                        pipe_wait(&bar_full[s], pass, abort);      // masked keys' scores are not looked at
+                        const uint64_t dks = dk + (uint64_t)(s * (2 * kTileBytes >> 4));
 #pragma unroll
-                            for (int i = 0; i < 4; ++i)
-                                mma_ss(col_s + t * 128, dqt + i * kStepRowwise, dks + i * kStepRowwise, id, i > 0);
-                            mma_commit(&bar_s[t]);
+                        for (int t = 0; t < NT; ++t) {   // S_t = Q_t K_j^T
+                            if (t >= nt) break;
+                            if (it[t] > 0) pipe_wait(&bar_sfree[t], (it[t] - 1) & 1, abort);
+                            ++it[t];
+                            tc_after_sync();
+                            const uint64_t dqt = dq + (uint64_t)(t * (kTileBytes >> 4));
+                            if (elect_one()) {
+#pragma unroll
+                                for (int i = 0; i < 4; ++i)
+                                    mma_ss(col_s + t * 128, dqt + i * kStepRowwise, dks + i * kStepRowwise, id, i > 0);
+                                mma_commit(&bar_s[t]);
+                                if (j == n - 1 && t == nt - 1) mma_commit(&bar_qfree);
+                            }
+                            __syncwarp();
                         }
-                        __syncwarp();
-                    }
-                    if (++s == C::kStages) {
-                        s = 0;
-                        ring ^= 1;
+                        if (++s == C::kStages) {
+                            s = 0;
+                            pass ^= 1;
+                        }
                     }
                 }
             } else {
                 const uint32_t id = mma_desc(128, 64, true);
                 const uint64_t dv = tile_desc(skv + kTileBytes);
-                for (int j = 0; j < nu; ++j) {
-                    const uint64_t dvs = dv + (uint64_t)(s * (2 * kTileBytes >> 4));
-                    for (int t = 0; t < ntu; ++t) {   // O_t += P_t V_j
-                        pipe_wait(&bar_p[t], j & 1, abort);
-                        tc_after_sync();
-                        if (elect_one()) {
+#pragma unroll 1
+                for (int unit = first; C::kWalks ? unit < a.units : unit == first; unit = C::kWalks ? unit + step : -1) {
+                    const Unit<NT> u(a, place(unit));
+                    const int n = __shfl_sync(kFullMask, u.n, 0), nt = __shfl_sync(kFullMask, u.nt, 0);
+                    for (int j = 0; j < n; ++j) {
+                        pipe_wait(&bar_ready[s], pass, abort);
+                        const uint64_t dvs = dv + (uint64_t)(s * (2 * kTileBytes >> 4));
 #pragma unroll
-                            for (int i = 0; i < 8; ++i)
-                                mma_ts(col_o + t * 64, col_p + t * 64 + i * 8, dvs + i * kStepAcross, id, j > 0 || i > 0);
-                            mma_commit(&bar_o[t]);
-                            if (t == ntu - 1) mma_commit(&bar_empty[s]);
+                        for (int t = 0; t < NT; ++t) {   // O_t += P_t V_j
+                            if (t >= nt) break;
+                            pipe_wait(&bar_p[t], it[t] & 1, abort);
+                            ++it[t];
+                            tc_after_sync();
+                            if (elect_one()) {
+#pragma unroll
+                                for (int i = 0; i < 8; ++i)
+                                    mma_ts(col_o + t * 64, col_p + t * 64 + i * 8, dvs + i * kStepAcross, id, j > 0 || i > 0);
+                                mma_commit(&bar_o[t]);
+                                if (t == nt - 1) mma_commit(&bar_empty[s]);
+                            }
+                            __syncwarp();
                         }
-                        __syncwarp();
+                        if (++s == C::kStages) {
+                            s = 0;
+                            pass ^= 1;
+                        }
                     }
-                    if (++s == C::kStages) s = 0;
                 }
             }
             // no matrix instruction in flight when the tensor memory is freed
@@ -359,11 +445,12 @@ cross_fwd_mma_kernel(const __grid_constant__ FwdMmaArgs a) {
 
     // ---- join: CTA r of the cluster finishes every CS-th row ------------------------
     cluster_sync();
+    const Unit<NT> u(a, first_place);
     const float *part = reinterpret_cast<const float *>(smem);
     const int groups = C::kThreads / 16, c4 = (threadIdx.x & 15) * 4;
-    for (int i = rank + CS * (int)(threadIdx.x >> 4); i < nt * kTileRows; i += CS * groups) {
+    for (int i = rank + CS * (int)(threadIdx.x >> 4); i < u.nt * kTileRows; i += CS * groups) {
         int g, q;
-        if (!a.qt.at(t0 + i / kTileRows, i % kTileRows, g, q)) continue;
+        if (!a.qt.at(u.t0 + i / kTileRows, i % kTileRows, g, q)) continue;
         float top = kNegInf;
         for (int k = 0; k < CS; ++k) top = fmaxf(top, ld_cluster(cluster_addr(join_m + i, k)));
         const float base = top == kNegInf ? 0.f : top;
@@ -376,17 +463,81 @@ cross_fwd_mma_kernel(const __grid_constant__ FwdMmaArgs a) {
             x = fma2(make_float2(w, w), ld_cluster2(at), x);
             y = fma2(make_float2(w, w), ld_cluster2(at + 8), y);
         }
-        const int h = hk * a.qt.G + g;
+        const int h = u.hk * a.qt.G + g;
         const float inv = sum == 0.f ? 0.f : 1.f / sum;
-        *reinterpret_cast<uint2 *>(a.O.row(b, h, q) + c4) =
+        *reinterpret_cast<uint2 *>(a.O.row(u.b, h, q) + c4) =
             make_uint2(pack_bf16x2(x.x * inv, x.y * inv), pack_bf16x2(y.x * inv, y.y * inv));
-        if (c4 == 0) a.LSE[((int64_t)b * a.Hq + h) * a.qt.Nq + q] = sum == 0.f ? kNegInf : (top + log2f(sum)) * kLn2;
+        if (c4 == 0) a.LSE[((int64_t)u.b * a.Hq + h) * a.qt.Nq + q] = sum == 0.f ? kNegInf : (top + log2f(sum)) * kLn2;
     }
     cluster_sync();   // the others may still read this CTA's part
 }
 
+// How many clusters of 2^i CTAs the GPU holds at once.
 template <int NT>
-cudaError_t fwd(const CrossArgs &a, const QueryTiles &qt) {
+cudaError_t clusters_held(int i, int *held) {
+    using C = Cfg<NT>;
+    static std::atomic<int> known[4];
+    *held = known[i].load(std::memory_order_relaxed);
+    if (*held) return cudaSuccess;
+    if (i == 0) {
+        *held = C::kMinBlocks * sm_count();
+    } else {
+        cudaLaunchConfig_t cfg = {};
+        cudaLaunchAttribute attr;
+        attr.id = cudaLaunchAttributeClusterDimension;
+        attr.val.clusterDim.x = 1u << i;
+        attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+        cfg.gridDim = dim3(1u << i);
+        cfg.blockDim = dim3(C::kThreads);
+        cfg.dynamicSmemBytes = C::kSmem;
+        cfg.attrs = &attr;
+        cfg.numAttrs = 1;
+        const cudaError_t e = cudaOccupancyMaxActiveClusters(held, cross_fwd_mma_kernel<NT>, &cfg);
+        if (e != cudaSuccess) return e;
+        *held = std::max(*held, 1);
+    }
+    known[i].store(*held, std::memory_order_relaxed);
+    return cudaSuccess;
+}
+
+// Query tiles of a CTA and CTAs of a cluster: those with the shortest estimate
+//   rounds (key tiles of a CTA x time of one + start, end and join)
+// in us, from what was measured: a key tile takes a CTA with both of its query
+// tiles 1.0, with one 0.78, a CTA of one tile 0.83, or 1.28 with another on its SM; a
+// round's other time is 5, of a cluster 9.5, of CTAs that walk over their units 3.
+// (2 sequences, 16 heads, 1569 x 16385, 224 units of 152: clusters of one 266 us, of
+// two 229, of four 289; 8 sequences, 12 heads, 197 x 1569, 96 units: 20, 35, 48; one
+// sequence, 16 heads, 197 x 4096: one-tile CTAs, clusters of one 31, of four 16.5, of
+// eight 18, two-tile CTAs 37, 19 and 31; 768 units of one tile by two: one-tile CTAs
+// 17.6, two-tile ones 23.)
+struct Plan {
+    int nt = 0, c = 1;
+    float cost = 0.f;
+};
+template <int NT>
+cudaError_t consider(const CrossArgs &a, const QueryTiles &qt, Plan *best) {
+    using C = Cfg<NT>;
+    const cudaError_t e = prepare_kernel<cross_fwd_mma_kernel<NT>>(C::kSmem, C::kRegs);
+    if (e != cudaSuccess) return e;
+    const int64_t units = (int64_t)a.B * a.Hkv * ((qt.tiles + NT - 1) / NT);
+    const int tiles = (a.Nk + kTileRows - 1) / kTileRows;
+    for (int i = 0; i < 4 && (i == 0 || tiles >= 1 << i); ++i) {
+        int held;
+        const cudaError_t f = clusters_held<NT>(i, &held);
+        if (f != cudaSuccess) return f;
+        const int c = 1 << i;
+        const float tile = NT == 2 ? (qt.tiles > 1 ? 1.f : 0.78f) : units * c > sm_count() ? 1.28f : 0.83f;
+        const float rounds = (float)((units + held - 1) / held), mine = (float)((tiles + c - 1) / c) * tile;
+        const float cost = i > 0          ? rounds * (mine + 9.5f)
+                           : C::kWalks ? rounds * (mine + 3.f) + 2.f
+                                       : rounds * (mine + 5.f);
+        if (!best->nt || cost < best->cost) *best = Plan{NT, c, cost};
+    }
+    return cudaSuccess;
+}
+
+template <int NT>
+cudaError_t fwd(const CrossArgs &a, const QueryTiles &qt, int c) {
     using C = Cfg<NT>;
     FwdMmaArgs f;
     f.qt = qt;
@@ -402,20 +553,21 @@ cudaError_t fwd(const CrossArgs &a, const QueryTiles &qt) {
     // and -inf of a masked key times c is still -inf
     f.c = std::max(std::fabs(a.scale) * kLog2e, 1e-36f);
     f.negative = a.scale < 0.f;
-    const cudaError_t e = prepare_kernel<cross_fwd_mma_kernel<NT>>(C::kSmem, C::kRegs);
-    if (e != cudaSuccess) return e;
     const int64_t units = (int64_t)a.B * a.Hkv * f.pairs;
-    const int tiles = (a.Nk + kTileRows - 1) / kTileRows;
-    int c = 1;
-    while (c < 8 && units * c * 2 <= (int64_t)C::kMinBlocks * sm_count() && tiles >= 2 * c) c *= 2;
-    return launch_clusters(cross_fwd_mma_kernel<NT>, (unsigned)(units * c), c, C::kThreads, C::kSmem, a.stream, f);
+    f.units = (int)units;
+    const int64_t grid = c > 1 || !C::kWalks ? units * c : std::min<int64_t>(units, C::kMinBlocks * sm_count());
+    return launch_clusters(cross_fwd_mma_kernel<NT>, (unsigned)grid, c, C::kThreads, C::kSmem, a.stream, f);
 }
 
 }  // namespace
 
 cudaError_t launch_cross_fwd_mma(const CrossArgs &a) {
     const QueryTiles qt(a.Hq / a.Hkv, a.Nq, a.Hq > 1 && a.Q.stride_h == 0);
-    return qt.tiles > 1 ? fwd<2>(a, qt) : fwd<1>(a, qt);
+    Plan plan;
+    cudaError_t e = consider<1>(a, qt, &plan);
+    if (e == cudaSuccess) e = consider<2>(a, qt, &plan);
+    if (e != cudaSuccess) return e;
+    return plan.nt == 2 ? fwd<2>(a, qt, plan.c) : fwd<1>(a, qt, plan.c);
 }
 
 FIBATT_DEFINE_ERROR_READER(read_error_cross_mma_fwd, "cross_mma_fwd.cu")

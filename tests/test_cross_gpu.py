@@ -443,3 +443,13 @@ def test_gradients_of_gradients_are_refused():
     dq, = torch.autograd.grad(api.cross_attention(q, k, v).square().sum(), q, create_graph=True)
     with pytest.raises(RuntimeError, match="once_differentiable"):
         dq.sum().backward()
+
+
+@pytest.mark.parametrize("size", [(110, 6, 6, 20, 200), (60, 8, 8, 130, 300), (90, 6, 2, 50, 140)], ids=lambda s: "x".join(map(str, s)))
+@pytest.mark.parametrize("mask", ["none", "len", "both"])
+def test_blocks_that_walk_over_their_units(size, mask):
+    q, k, v, do = _inputs(BF16, *size, seed=47)
+    n, m = _masks(mask, size[0], size[4], seed=5)
+    if n is not None:
+        n[size[0] // 3:size[0] // 2] = 0       # runs of units without keys
+    _check_all(q, k, v, do, 0.125, n, m)
