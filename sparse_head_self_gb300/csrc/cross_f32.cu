@@ -8,6 +8,10 @@
 // gave 34 here, held up by the shared memory's bandwidth.  (The 5th-generation
 // cores' TF32 form reads its second operand along the summed index only, which
 // P V and dS K do not have, and needs every tile twice in shared memory.)
+// Measured: gradient of 4 sequences, 12 heads, 197 x 197, masked: 65 us (FP32 units:
+// 85.5), 384 blocks of which some SMs have three and some two, the warp-wide
+// instructions 33% busy: a scheduler's three warps wait for their own chains of cuts and
+// products, for their copies, and for instructions.
 //
 // A CTA of four warps holds 64 rows and walks over the 64-row tiles of the
 // other side, a warp 16 rows by all 64 columns:

