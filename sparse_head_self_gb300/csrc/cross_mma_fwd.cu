@@ -489,13 +489,13 @@ cross_fwd_mma_kernel(const __grid_constant__ FwdMmaArgs a) {
 
 // How many clusters of 2^i CTAs the GPU holds at once.
 template <int NT>
-cudaError_t clusters_held(int i, int *held) {
+int clusters_held(int i) {
     using C = Cfg<NT>;
     static std::atomic<int> known[4];
-    *held = known[i].load(std::memory_order_relaxed);
-    if (*held) return cudaSuccess;
+    int held = known[i].load(std::memory_order_relaxed);
+    if (held) return held;
     if (i == 0) {
-        *held = C::kMinBlocks * sm_count();
+        held = C::kMinBlocks * sm_count();
     } else {
         cudaLaunchConfig_t cfg = {};
         cudaLaunchAttribute attr;
@@ -507,12 +507,12 @@ cudaError_t clusters_held(int i, int *held) {
         cfg.dynamicSmemBytes = C::kSmem;
         cfg.attrs = &attr;
         cfg.numAttrs = 1;
-        const cudaError_t e = cudaOccupancyMaxActiveClusters(held, cross_fwd_mma_kernel<NT>, &cfg);
-        if (e != cudaSuccess) return e;
-        *held = std::max(*held, 1);
+        // none that size: as if it held one, which no plan prefers
+        if (cudaOccupancyMaxActiveClusters(&held, cross_fwd_mma_kernel<NT>, &cfg) != cudaSuccess) (void)cudaGetLastError();
+        held = std::max(held, 1);
     }
-    known[i].store(*held, std::memory_order_relaxed);
-    return cudaSuccess;
+    known[i].store(held, std::memory_order_relaxed);
+    return held;
 }
 
 // Query tiles of a CTA and CTAs of a cluster: those with the shortest estimate
@@ -537,10 +537,7 @@ cudaError_t consider(const CrossArgs &a, const QueryTiles &qt, Plan *best) {
     const int64_t units = (int64_t)a.B * a.Hkv * ((qt.tiles + NT - 1) / NT);
     const int tiles = (a.Nk + kTileRows - 1) / kTileRows;
     for (int i = 0; i < 4 && (i == 0 || tiles >= 1 << i); ++i) {
-        int held;
-        const cudaError_t f = clusters_held<NT>(i, &held);
-        if (f != cudaSuccess) return f;
-        const int c = 1 << i;
+        const int c = 1 << i, held = clusters_held<NT>(i);
         const float tile = NT == 2 ? (qt.tiles > 1 ? 1.f : 0.78f) : units * c > sm_count() ? 1.28f : 0.83f;
         const float rounds = (float)((units + held - 1) / held), mine = (float)((tiles + c - 1) / c) * tile;
         const float cost = i > 0          ? rounds * (mine + 9.5f)

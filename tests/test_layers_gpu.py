@@ -2,6 +2,10 @@
 attention, alone and together as an encoder-decoder: outputs and every
 gradient against the same layers in torch operations, in 64 bits (their 32-bit
 run is the tolerance: a kernel's run may be a few times as far off)."""
+import os
+import subprocess
+import sys
+
 import pytest
 import torch
 
@@ -163,3 +167,41 @@ def test_layers_in_16_bits_keep_their_angles():
     assert y.dtype == torch.bfloat16
     # ten roundings of activations and weights of 2^-8 each, most of them averaged out
     assert float((y.float() - wide).abs().mean()) <= 10 * 2.0 ** -8 * float(wide.abs().mean())
+
+
+FIRST_CALL = """
+import sys, torch
+from sparse_head_self_gb300 import api
+what, dtype, Nq = sys.argv[1], getattr(torch, sys.argv[2]), int(sys.argv[3])
+g = torch.Generator(device="cuda").manual_seed(0)
+r = lambda *s: torch.randn(*s, generator=g, device="cuda").to(dtype)
+q, k, v, do = r(2, 4, Nq, 64), r(2, 2, 300, 64), r(2, 2, 300, 64), r(2, 4, Nq, 64)
+x, w = r(2, Nq, 8 * 64), r(64)
+tables = api.rotary_tables(api.rotary_angles(Nq, 64, device="cuda"))
+
+def call():
+    if what == "norm":
+        out = api.qk_norm_fwd(x, (4, 2, 2), w, w, 1e-6, tables)
+        return out + api.qk_norm_bwd(x, (4, 2, 2), w, w, *out, 1e-6, tables)
+    o, lse = api.cross_fwd(q, k, v, 0.125)
+    return (o, lse) + api.cross_bwd(q, k, v, o, lse, do, 0.125)
+
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    got = call()
+graph.replay()
+torch.cuda.synchronize()
+got = [t.clone() for t in got]
+assert all(torch.equal(a, b) for a, b in zip(got, call()))
+assert all(bool(t.isfinite().all()) for t in got)
+"""
+
+
+@pytest.mark.parametrize("what,dtype,Nq", [("norm", "bfloat16", 40), ("cross", "bfloat16", 1), ("cross", "bfloat16", 150),
+                                           ("cross", "float32", 1), ("cross", "float32", 150)])
+def test_the_first_call_of_a_process_may_be_captured(what, dtype, Nq):
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    child = subprocess.run([sys.executable, "-c", FIRST_CALL, what, dtype, str(Nq)], cwd=root, capture_output=True, text=True,
+                           timeout=300)
+    assert child.returncode == 0, child.stderr[-2000:]
