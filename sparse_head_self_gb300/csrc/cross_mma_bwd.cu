@@ -78,15 +78,6 @@ struct BwdMmaArgs {
     BwdMmaArgs() : qt(1, 1, false) {}
 };
 
-struct Shared {
-    uint64_t held[2], held_free[2], full[kStages], ready[kStages], empty[kStages], s, sfree, p, done, end[2];
-    uint64_t unit_full[2], unit_empty[2];
-    uint4 keys[kStages];
-    int unit[2];                // the CTA's next, in turn
-    uint32_t tmem;
-    int abort;
-};
-
 // x as the sum of three bf16 values, the first of eight elements of a row (cut to
 // what a bf16 holds: at a scale of 0, 1000 / c is beyond it; NaN stays).
 __device__ __forceinline__ uint4 three_parts(float x) {
@@ -135,15 +126,121 @@ cross_parts_kernel(int Hq, int Nq, int npad, unsigned rows, Rows<const __nv_bflo
     if (i == 2) stats[at] = make_float2(lse2, d);
 }
 
+// c += A (16 x 16) B (16 x 8)
+__device__ __forceinline__ void warp_mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// A lane's 16 dims of a row: 32 bytes.
+struct Dims {
+    uint32_t x[8];
+    __device__ __forceinline__ void load(const __nv_bfloat16 *row, int t) {
+        const uint4 *p = reinterpret_cast<const uint4 *>(row) + 2 * t;
+        const uint4 u = __ldg(p), v = __ldg(p + 1);
+        x[0] = u.x, x[1] = u.y, x[2] = u.z, x[3] = u.w, x[4] = v.x, x[5] = v.y, x[6] = v.z, x[7] = v.w;
+    }
+    __device__ __forceinline__ void zero() {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = 0u;
+    }
+};
+
+// The same for at most kFewKeys keys, with D summed from the weights themselves,
+// D = sum_k P_k dP_k: O's rounding to bf16 is one of the larger errors of dS when a
+// row has few keys (against 64 bits, 3 keys: dQ and dK 0.0032 with <dO, O>, 0.0024 with
+// this; from 64 keys on both 0.0025 to 0.0024, and 128 keys, 192 heads of 1000 queries, cost
+// 17 of 92 us).  A warp takes 16 queries of a head,
+// its eight keys at a time by warp-wide products; lane (g, t) gives them dims 16 t
+// to 16 t + 15 of rows g and g + 8 and of key g, four at a time in both operands
+// (the order of a sum does not matter), so that it loads 16 bytes at once.
+constexpr int kFewWarps = 4, kFewKeys = 64;
+__global__ void __launch_bounds__(32 * kFewWarps)
+cross_parts_few_kernel(int Hq, int Hkv, int Nq, int npad, unsigned heads, KeySet ks, Rows<const __nv_bfloat16> Q,
+                       Rows<const __nv_bfloat16> K, Rows<const __nv_bfloat16> V, Rows<const __nv_bfloat16> dO,
+                       const float *__restrict__ LSE, float c, float2 *__restrict__ stats, uint4 *__restrict__ lse_parts,
+                       uint4 *__restrict__ d_parts, int *__restrict__ next_unit) {
+    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    const unsigned groups = (unsigned)(npad + 15) / 16, at = blockIdx.x * kFewWarps + warp_number();
+    const unsigned bh = at / groups, b = bh / (unsigned)Hq, h = bh - b * Hq;
+    const int n0 = 16 * (int)(at - bh * groups);
+    grid_dep_wait();
+    grid_dep_launch();
+    if (at == 0 && lane == 0) *next_unit = 0;
+    if (bh >= heads) {      // rows of no query, behind the heads'
+        const unsigned i = (at - heads * groups) * 16 + (lane >> 1);
+        if (i >= (unsigned)kTileRows) return;
+        const int64_t row = (int64_t)heads * npad + i;
+        if (lane & 1) d_parts[row] = make_uint4(0, 0, 0, 0);
+        else lse_parts[row] = no_query(c);
+        return;
+    }
+    const int hk = (int)h / (Hq / Hkv);
+    Dims q[2], w[2];
+    float lse2[2], d[2] = {0.f, 0.f};
+    bool none[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int n = n0 + g + 8 * i;
+        q[i].zero();
+        w[i].zero();
+        float lse = -kInf;
+        if (n < Nq) {
+            q[i].load(Q.row(b, h, n), t);
+            w[i].load(dO.row(b, h, n), t);
+            lse = __ldg(LSE + (int64_t)bh * Nq + n);
+        }
+        none[i] = lse == -kInf;        // a row without keys: weights of exp2(s - inf) = 0
+        lse2[i] = none[i] ? kInf : lse * kLog2e;
+    }
+    const int bound = ks.bound((int)b);
+    for (int k0 = 0; k0 < bound; k0 += 8) {
+        const int mine = k0 + (lane & 7);
+        const uint32_t in = __ballot_sync(kFullMask, mine < bound && ks.has((int)b, min(mine, bound - 1)));
+        Dims k, v;
+        k.load(K.row(b, hk, min(k0 + g, bound - 1)), t);
+        v.load(V.row(b, hk, min(k0 + g, bound - 1)), t);
+        float s[4] = {0.f, 0.f, 0.f, 0.f}, dp[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t aq[4] = {q[0].x[2 * i], q[1].x[2 * i], q[0].x[2 * i + 1], q[1].x[2 * i + 1]};
+            const uint32_t aw[4] = {w[0].x[2 * i], w[1].x[2 * i], w[0].x[2 * i + 1], w[1].x[2 * i + 1]};
+            warp_mma(s, aq, k.x[2 * i], k.x[2 * i + 1]);
+            warp_mma(dp, aw, v.x[2 * i], v.x[2 * i + 1]);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float p = fast_exp2(fmaf(s[i], c, -lse2[i >> 1]));
+            if ((in >> (2 * t + (i & 1))) & 1) d[i >> 1] = fmaf(p, dp[i], d[i >> 1]);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        d[i] += __shfl_xor_sync(kFullMask, d[i], 1);
+        d[i] += __shfl_xor_sync(kFullMask, d[i], 2);
+        const int n = n0 + g + 8 * i;
+        if (n >= npad) continue;
+        const int64_t row = (int64_t)bh * npad + n;
+        const bool query = n < Nq;
+        if (t == 0) lse_parts[row] = none[i] ? no_query(c) : three_parts(-lse2[i] / c);
+        if (t == 1) d_parts[row] = query ? three_parts(-d[i]) : make_uint4(0, 0, 0, 0);
+        if (t == 2 && query) stats[(int64_t)bh * Nq + n] = make_float2(lse2[i], d[i]);
+    }
+}
+
 // One unit of work: 128 rows of one side of one key/value head, and the part of
-// the other side's tiles that this CTA of the cluster streams.  Every warp works
-// it out for itself.
-template <bool KEYS>
+// the other side's tiles that this CTA of the cluster streams.  The copying warp works
+// it out and passes it on: its divisions and loads would otherwise stand at the start
+// of every unit in every warp.
 struct Unit {
+    int index;               // queries held first, then keys held
     int mine, hk, b, bound, lo, n;
-    uint4 keys;              // KEYS: which rows are attended
-    __device__ __forceinline__ Unit(const BwdMmaArgs &a, int unit) {
-        const int held = KEYS ? a.ktiles : a.qt.tiles;
+    uint4 keys;              // keys held: which rows are attended
+    template <bool KEYS>
+    __device__ __forceinline__ void set(const BwdMmaArgs &a, int i) {
+        index = i;
+        const int unit = KEYS ? i - a.query_units : i, held = KEYS ? a.ktiles : a.qt.tiles;
         mine = unit % held;
         hk = unit / held % a.Hkv;
         b = unit / held / a.Hkv;
@@ -159,8 +256,23 @@ struct Unit {
         }
         const int CS = (int)cluster_size(), rank = (int)cluster_rank();
         lo = (int)(tiles * rank / CS);
-        n = __shfl_sync(kFullMask, (int)(tiles * (rank + 1) / CS) - lo, 0);
+        n = (int)(tiles * (rank + 1) / CS) - lo;
     }
+    // the whole warp calls it; an index behind the last unit stands for the end
+    __device__ __forceinline__ void enter(const BwdMmaArgs &a, int i) {
+        if (i < a.query_units) set<false>(a, i);
+        else if (i < a.units) set<true>(a, i);
+        else index = i, mine = hk = b = bound = lo = n = 0, keys = make_uint4(0, 0, 0, 0);
+    }
+};
+
+struct Shared {
+    uint64_t held[2], held_free[2], full[kStages], ready[kStages], empty[kStages], s, sfree, p, done, end[2];
+    uint64_t unit_full[2], unit_empty[2];
+    uint4 keys[kStages];
+    Unit unit[2];               // the CTA's, in turn
+    uint32_t tmem;
+    int abort;
 };
 
 // The CTA's shared memory.
@@ -181,9 +293,8 @@ struct Tiles {
 
 // P and dS: row = lane of the quarter, 32 columns
 template <bool KEYS>
-__device__ __forceinline__ int weights(const BwdMmaArgs &a, Shared &sh, uint8_t *ring, int unit, int it) {
+__device__ __forceinline__ int weights(const BwdMmaArgs &a, Shared &sh, uint8_t *ring, const Unit &u, int it) {
     volatile int *abort = &sh.abort;
-    const Unit<KEYS> u(a, unit);
     const int warp = warp_number(), lane = threadIdx.x & 31;
     const int cg = warp >> 2, r = (warp & 3) * 32 + lane;
     const uint32_t lanes = (uint32_t)(warp & 3) << 21, tmem = sh.tmem;
@@ -289,9 +400,8 @@ __device__ __forceinline__ int weights(const BwdMmaArgs &a, Shared &sh, uint8_t 
 // Copies; false: a wait gave up.  `units` counts the units with tiles, whose held
 // rows are in pairs of tiles in turn.
 template <bool KEYS>
-__device__ __forceinline__ bool copies(const BwdMmaArgs &a, Shared &sh, const Tiles &tl, int unit, int &it, int &units) {
+__device__ __forceinline__ bool copies(const BwdMmaArgs &a, Shared &sh, const Tiles &tl, const Unit &u, int &it, int &units) {
     volatile int *abort = &sh.abort;
-    const Unit<KEYS> u(a, unit);
     if (u.n == 0) return true;
     const auto query_tile = [&](uint8_t *dst, int t, uint64_t *bar) {
         load_tile(dst, a.q, a.qt.first_row(t), u.hk * a.qt.G + a.qt.first_head(t), u.b, bar);
@@ -341,9 +451,8 @@ __device__ __forceinline__ bool copies(const BwdMmaArgs &a, Shared &sh, const Ti
 // with weights of 0, cleared.  Of streamed queries, the rows behind the tile's last,
 // which hold what was there before or the next group's.  false: a wait gave up.
 template <bool KEYS>
-__device__ __forceinline__ bool prepare(const BwdMmaArgs &a, Shared &sh, const Tiles &tl, int unit, int &it) {
+__device__ __forceinline__ bool prepare(const BwdMmaArgs &a, Shared &sh, const Tiles &tl, const Unit &u, int &it) {
     volatile int *abort = &sh.abort;
-    const Unit<KEYS> u(a, unit);
     for (int j = 0; j < u.n; ++j, ++it) {
         const int s = it % kStages;
         uint4 w = make_uint4(0, 0, 0, 0);
@@ -387,10 +496,9 @@ struct Turn {   // a place in the ring
 
 // S and dP
 template <bool KEYS>
-__device__ __forceinline__ void scores(const BwdMmaArgs &a, Shared &sh, const Tiles &tl, int unit, int &it, int &units,
+__device__ __forceinline__ void scores(const BwdMmaArgs &a, Shared &sh, const Tiles &tl, const Unit &u, int &it, int &units,
                                        Turn &at) {
     volatile int *abort = &sh.abort;
-    const Unit<KEYS> u(a, unit);
     if (u.n == 0) return;
     const uint32_t id = mma_desc(128, 128, false), tmem = sh.tmem;
     const int pair = units & 1;
@@ -424,9 +532,8 @@ __device__ __forceinline__ void scores(const BwdMmaArgs &a, Shared &sh, const Ti
 
 // dQ, or dK and dV
 template <bool KEYS>
-__device__ __forceinline__ void sums(const BwdMmaArgs &a, Shared &sh, const Tiles &tl, int unit, int &it, Turn &at) {
+__device__ __forceinline__ void sums(const BwdMmaArgs &a, Shared &sh, const Tiles &tl, const Unit &u, int &it, Turn &at) {
     volatile int *abort = &sh.abort;
-    const Unit<KEYS> u(a, unit);
     const uint32_t id = mma_desc(128, 64, true), tmem = sh.tmem;
     for (int j = 0; j < u.n; ++j, ++it, at.next()) {
         const uint64_t r0 = tile_desc(tl.ring) + (uint64_t)(at.s * (2 * kTileBytes >> 4)), r1 = r0 + (kTileBytes >> 4);
@@ -450,8 +557,7 @@ __device__ __forceinline__ void sums(const BwdMmaArgs &a, Shared &sh, const Tile
 
 // Join of a cluster's partial sums: CTA r finishes every CS-th row.
 template <bool KEYS>
-__device__ __forceinline__ void join(const BwdMmaArgs &a, const Tiles &tl, int unit) {
-    const Unit<KEYS> u(a, unit);
+__device__ __forceinline__ void join(const BwdMmaArgs &a, const Tiles &tl, const Unit &u) {
     const int CS = (int)cluster_size(), rank = (int)cluster_rank();
     const float *part = reinterpret_cast<const float *>(tl.ring);
     const int c4 = (threadIdx.x & 15) * 4;
@@ -522,65 +628,68 @@ __global__ void __launch_bounds__(kThreads, 1) cross_bwd_mma_kernel(const __grid
     // not depend on who works on it).  A cluster has one unit.
     const int CS = (int)cluster_size(), first = (int)(blockIdx.x / CS);
     const auto each = [&](auto next, auto queries, auto keys) {
-        int u = first;
+        Unit u = next();
 #pragma unroll 1
-        for (; u < a.query_units; u = next()) queries(u);
+        for (; u.index < a.query_units; u = next()) queries(u);
 #pragma unroll 1
-        for (; u < a.units; u = next()) keys(u - a.query_units);
+        for (; u.index < a.units; u = next()) keys(u);
     };
     int passed = 0;         // units handed over
     const auto take = [&] {
         const int i = passed & 1;
-        int u = a.units;
-        if (pipe_wait(&sh.unit_full[i], (passed >> 1) & 1, &sh.abort)) u = *(volatile int *)&sh.unit[i];
+        Unit u;
+        const bool ok = pipe_wait(&sh.unit_full[i], (passed >> 1) & 1, &sh.abort);
+        u = sh.unit[i];
+        u.index = __shfl_sync(kFullMask, ok ? u.index : a.units, 0);
+        u.n = __shfl_sync(kFullMask, u.n, 0);
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh.unit_empty[i]);
         ++passed;
-        return __shfl_sync(kFullMask, u, 0);
+        return u;
     };
     int it = 0, units = 0;
     if (warp < kWeightWarps) {
         take_registers<kRegsMany>();
-        each(take, [&](int u) { it = weights<false>(a, sh, tl.ring, u, it); },
-             [&](int u) { it = weights<true>(a, sh, tl.ring, u, it); });
+        each(take, [&](const Unit &u) { it = weights<false>(a, sh, tl.ring, u, it); },
+             [&](const Unit &u) { it = weights<true>(a, sh, tl.ring, u, it); });
     } else {
         give_registers<kRegsFew>();
         if (warp == kCopyWarp) {
             bool ok = true;
-            int drawn = 0;
-            const auto draw = [&] {      // its answer is not needed before this unit's copies are out
+            int drawn = first;
+            const auto pass = [&] {      // (its copies being out, the next unit's number has come meanwhile)
+                const int i = passed & 1;
+                Unit u;
+                u.enter(a, __shfl_sync(kFullMask, drawn, 0));
                 drawn = a.units;
-                if (CS == 1 && lane == 0) drawn = (int)gridDim.x + atomicAdd(a.next_unit, 1);
-            };
-            const auto pass = [&] {
-                const int i = passed & 1, u = __shfl_sync(kFullMask, drawn, 0);
+                if (CS == 1 && lane == 0 && u.index < a.units) drawn = (int)gridDim.x + atomicAdd(a.next_unit, 1);
                 ok = ok && (passed < 2 || pipe_wait(&sh.unit_empty[i], ((passed >> 1) - 1) & 1, &sh.abort));
-                if (!ok) return a.units;
-                if (lane == 0) {
-                    *(volatile int *)&sh.unit[i] = u;
+                if (!ok) u.index = a.units;
+                else if (lane == 0) {
+                    sh.unit[i] = u;
                     mbar_arrive(&sh.unit_full[i]);
                 }
                 __syncwarp();
                 ++passed;
                 return u;
             };
-            each(pass, [&](int u) { draw(); ok = ok && copies<false>(a, sh, tl, u, it, units); },
-                 [&](int u) { draw(); ok = ok && copies<true>(a, sh, tl, u, it, units); });
+            each(pass, [&](const Unit &u) { ok = ok && copies<false>(a, sh, tl, u, it, units); },
+                 [&](const Unit &u) { ok = ok && copies<true>(a, sh, tl, u, it, units); });
             if (lane == 0) {   // leave no copy in flight
                 for (int i = max(0, units - 2); i < units; ++i) mbar_drain(&sh.held[i & 1], (i >> 1) & 1);
                 for (int i = max(0, it - kStages); i < it; ++i) mbar_drain(&sh.full[i % kStages], (i / kStages) & 1);
             }
         } else if (warp == kPrepWarp) {
             bool ok = true;
-            each(take, [&](int u) { ok = ok && prepare<false>(a, sh, tl, u, it); },
-                 [&](int u) { ok = ok && prepare<true>(a, sh, tl, u, it); });
+            each(take, [&](const Unit &u) { ok = ok && prepare<false>(a, sh, tl, u, it); },
+                 [&](const Unit &u) { ok = ok && prepare<true>(a, sh, tl, u, it); });
         } else {
             Turn at;
             if (warp == kScoreWarp)
-                each(take, [&](int u) { scores<false>(a, sh, tl, u, it, units, at); },
-                     [&](int u) { scores<true>(a, sh, tl, u, it, units, at); });
+                each(take, [&](const Unit &u) { scores<false>(a, sh, tl, u, it, units, at); },
+                     [&](const Unit &u) { scores<true>(a, sh, tl, u, it, units, at); });
             else
-                each(take, [&](int u) { sums<false>(a, sh, tl, u, it, at); }, [&](int u) { sums<true>(a, sh, tl, u, it, at); });
+                each(take, [&](const Unit &u) { sums<false>(a, sh, tl, u, it, at); }, [&](const Unit &u) { sums<true>(a, sh, tl, u, it, at); });
             // no matrix instruction in flight when the tensor memory is freed
             uint64_t *end = &sh.end[warp == kSumWarp];
             if (elect_one()) mma_commit(end);
@@ -594,8 +703,10 @@ __global__ void __launch_bounds__(kThreads, 1) cross_bwd_mma_kernel(const __grid
     if (warp == kSumWarp) tmem_free(sh.tmem, kCols);
     if (CS == 1) return;
     cluster_sync();
-    if (first < a.query_units) join<false>(a, tl, first);
-    else join<true>(a, tl, first - a.query_units);
+    Unit u;
+    u.enter(a, first);
+    if (first < a.query_units) join<false>(a, tl, u);
+    else join<true>(a, tl, u);
     cluster_sync();   // the others may still read this CTA's part
 }
 
@@ -633,9 +744,18 @@ cudaError_t launch_cross_bwd_mma(const CrossArgs &a) {
     f.c = std::copysign(std::max(std::fabs(a.scale) * kLog2e, 1e-36f), a.scale);
     cudaError_t e = prepare_kernel<cross_bwd_mma_kernel>(kSmem, kRegs);
     if (e != cudaSuccess) return e;
-    e = launch_clusters(cross_parts_kernel, (unsigned)((rows + kTileRows + 31) / 32), 1, 256, 0, a.stream, a.Hq, a.Nq,
-                        f.npad, (unsigned)rows, rows_of<const __nv_bfloat16>(a.O), rows_of<const __nv_bfloat16>(a.dO),
-                        static_cast<const float *>(a.LSE), f.c, stats, lse_parts, d_parts, f.next_unit);
+    if (a.Nk <= kFewKeys) {
+        const int64_t warps = (int64_t)a.B * a.Hq * ((f.npad + 15) / 16) + kTileRows / 16;
+        e = launch_clusters(cross_parts_few_kernel, (unsigned)((warps + kFewWarps - 1) / kFewWarps), 1, 32 * kFewWarps, 0,
+                            a.stream, a.Hq, a.Hkv, a.Nq, f.npad, (unsigned)(a.B * a.Hq), a.keys,
+                            rows_of<const __nv_bfloat16>(a.Q), rows_of<const __nv_bfloat16>(a.K),
+                            rows_of<const __nv_bfloat16>(a.V), rows_of<const __nv_bfloat16>(a.dO),
+                            static_cast<const float *>(a.LSE), f.c, stats, lse_parts, d_parts, f.next_unit);
+    } else {
+        e = launch_clusters(cross_parts_kernel, (unsigned)((rows + kTileRows + 31) / 32), 1, 256, 0, a.stream, a.Hq, a.Nq,
+                            f.npad, (unsigned)rows, rows_of<const __nv_bfloat16>(a.O), rows_of<const __nv_bfloat16>(a.dO),
+                            static_cast<const float *>(a.LSE), f.c, stats, lse_parts, d_parts, f.next_unit);
+    }
     if (e != cudaSuccess) return e;
     const int64_t query_units = (int64_t)a.B * a.Hkv * f.qt.tiles, units = query_units + (int64_t)a.B * a.Hkv * f.ktiles;
     f.query_units = (int)query_units;

@@ -453,3 +453,27 @@ def test_blocks_that_walk_over_their_units(size, mask):
     if n is not None:
         n[size[0] // 3:size[0] // 2] = 0       # runs of units without keys
     _check_all(q, k, v, do, 0.125, n, m)
+
+
+@pytest.mark.parametrize("Nk", [3, 4, 7, 16, 40, 128, 200])
+@pytest.mark.parametrize("mask", ["none", "mask"])
+def test_gradients_of_few_keys_have_two_roundings(Nk, mask):
+    # dS and the result are each rounded once to 16 bits: at most 2^-8 of the value, uniform below
+    # that, so 2^-8 / sqrt(3) in the mean square; two independent ones are sqrt(2) of it
+    q, k, v, do = _inputs(BF16, 8, 4, 4, 60, Nk, layout="bhnd", seed=53)
+    m = None
+    if mask == "mask":
+        m = torch.ones(8, Nk, dtype=torch.bool, device="cuda")
+        m[:, ::3] = False
+    got = _run(q, k, v, do, 0.125, None, m)
+    want = cross(q, k, v, 0.125, None, m, do, got["O"])
+    x, y, z, w = (t.double() for t in (q, k, v, do))
+    s = 0.125 * x @ y.transpose(-1, -2)
+    if m is not None:
+        s = s.masked_fill(~m[:, None, None], -math.inf)
+    p, dp = s.softmax(-1), w @ z.transpose(-1, -2)
+    ds = p * (dp - (p * dp).sum(-1, keepdim=True))
+    for name, exact in (("dQ", 0.125 * ds @ y), ("dK", 0.125 * ds.transpose(-1, -2) @ x)):
+        check(name, got[name], want[name])
+        err = float((got[name].double() - exact).norm() / exact.norm())
+        assert err <= math.sqrt(2 / 3) * 2.0 ** -8, (name, err)
