@@ -83,6 +83,7 @@ struct FwdMmaArgs {
 template <int NT>
 struct Place {
     int t0, nt, hk, b;
+    __device__ __forceinline__ Place() {}
     __device__ __forceinline__ Place(const FwdMmaArgs &a, int unit) {
         t0 = unit % a.pairs * NT;
         hk = unit / a.pairs % a.Hkv;
@@ -91,17 +92,30 @@ struct Place {
     }
 };
 // ... and the part of its sequence's key tiles that this CTA of the cluster walks
-// over.  Every warp works it out for itself.
+// over.  CTAs that walk over their units have them from the copying warp.
 template <int NT>
 struct Unit : Place<NT> {
     int bound, lo, n;
-    __device__ __forceinline__ Unit(const FwdMmaArgs &a, const Place<NT> &p) : Place<NT>(p) {
+    __device__ __forceinline__ Unit() {}
+    __device__ __forceinline__ Unit(const FwdMmaArgs &a, const Place<NT> &p) : Place<NT>(p) { set(a); }
+    __device__ __forceinline__ void set(const FwdMmaArgs &a) {
+        const Place<NT> &p = *this;
         bound = a.ks.bound(p.b);
         const int ktiles = (bound + kTileRows - 1) / kTileRows, CS = (int)cluster_size(), rank = (int)cluster_rank();
         lo = (int)((int64_t)ktiles * rank / CS);
         n = (int)((int64_t)ktiles * (rank + 1) / CS) - lo;
     }
 };
+
+// A named barrier of `threads` threads (whole warps), and whether `p` holds in all of them.
+__device__ __forceinline__ bool all_of(int id, int threads, bool p) {
+    int r;
+    asm volatile("{ .reg .pred p, q; setp.ne.s32 p, %1, 0; bar.red.and.pred q, %2, %3, p; selp.s32 %0, 1, 0, q; }"
+                 : "=r"(r)
+                 : "r"((int)p), "r"(id), "r"(threads)
+                 : "memory");
+    return r != 0;
+}
 
 template <int NT>
 __global__ void __launch_bounds__(Cfg<NT>::kThreads, Cfg<NT>::kMinBlocks)
@@ -112,6 +126,8 @@ cross_fwd_mma_kernel(const __grid_constant__ FwdMmaArgs a) {
     uint8_t *sq = smem, *skv = smem + NT * kTileBytes;   // stage s: K at skv + 2 s tiles, V behind it
     __shared__ uint64_t bar_q, bar_qfree, bar_full[C::kStages], bar_ready[C::kStages], bar_empty[C::kStages];
     __shared__ uint64_t bar_s[NT], bar_sfree[NT], bar_p[NT], bar_o[NT], bar_end[2];
+    __shared__ uint64_t bar_unit[2], bar_unitfree[2];
+    __shared__ Unit<NT> units[2];       // of a CTA that walks, in turn; n < 0: no more
     __shared__ uint4 keys[C::kStages];
     __shared__ uint32_t tmem_base;
     __shared__ int abort_flag;
@@ -125,7 +141,6 @@ cross_fwd_mma_kernel(const __grid_constant__ FwdMmaArgs a) {
     // the CTA's units: a cluster has one, the CTAs of one wave walk over all of them
     const int first = (int)(blockIdx.x / CS), step = (int)(gridDim.x / CS);
     const Place<NT> first_place(a, first);
-    const auto place = [&](int unit) { return C::kWalks && unit != first ? Place<NT>(a, unit) : first_place; };
 
     if (threadIdx.x == 0) {
         mbar_init(&bar_q, 1);
@@ -141,8 +156,11 @@ cross_fwd_mma_kernel(const __grid_constant__ FwdMmaArgs a) {
             mbar_init(&bar_p[t], 8);
             mbar_init(&bar_o[t], 1);
         }
-        mbar_init(&bar_end[0], 1);
-        mbar_init(&bar_end[1], 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&bar_end[i], 1);
+            mbar_init(&bar_unit[i], 1);
+            mbar_init(&bar_unitfree[i], C::kSoftmaxWarps + 3);
+        }
         abort_flag = 0;
         prefetch_map(&a.q.map);
         prefetch_map(&a.k.map);
@@ -158,13 +176,31 @@ cross_fwd_mma_kernel(const __grid_constant__ FwdMmaArgs a) {
     grid_dep_wait();
     grid_dep_launch();
 
+    // body(unit) for each of the CTA's units
+    const auto each = [&](auto body) {
+        if constexpr (C::kWalks) {
+#pragma unroll 1
+            for (int k = 0;; ++k) {
+                bool go = pipe_wait(&bar_unit[k & 1], (k >> 1) & 1, abort);
+                __syncwarp();
+                // the softmax warps meet at barriers within a unit: all of them go on, or none
+                if (warp < C::kSoftmaxWarps) go = all_of(2, 32 * C::kSoftmaxWarps, go);
+                if (!go || units[k & 1].n < 0) break;
+                body(units[k & 1]);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bar_unitfree[k & 1]);
+            }
+        } else {
+            body(Unit<NT>(a, first_place));
+        }
+    };
     // `ring` counts the key tiles over all units of the CTA: tile `ring` is in stage
     // ring mod kStages.  A query tile's barriers complete a phase for each key tile of
     // the units that have it, which `it` counts.
     if (warp < C::kSoftmaxWarps) {
         take_registers<C::kRegsMany>();
         // ---- softmax: two threads a row, in warps four apart, 64 columns each ----------------------
-        // (No wait's failure ends the loop: a warp's partner at the named barriers must find it
+        // (No wait's failure ends the loop over a unit's tiles: a warp's partner at the named barriers must find it
         // there; what follows is not trusted, since the error word is set.)
         const int t = warp >> 3, half = (warp >> 2) & 1, quarter = warp & 3, r = quarter * 32 + lane;
         const int at = t * kTileRows + r, pair_bar = 3 + 4 * t + quarter;
@@ -172,19 +208,12 @@ cross_fwd_mma_kernel(const __grid_constant__ FwdMmaArgs a) {
         const uint32_t ts = col_s + t * 128 + 64 * half + lanes, tp = col_p + t * 64 + 32 * half + lanes;
         const uint32_t to = col_o + t * 64 + 32 * half + lanes;
         int it = 0, skipped = 0;
-#pragma unroll 1
-        for (int unit = first; C::kWalks ? unit < a.units : unit == first; unit = C::kWalks ? unit + step : -1) {
-            // (of the unit, only this is needed within the loop, which has no register to spare)
-            int n, whole;      // key tiles; the first of them are attended wholly
-            {
-                const Unit<NT> u(a, place(unit));
-                if (t >= u.nt) {
-                    skipped += u.n;
-                    continue;
-                }
-                n = u.n;
-                whole = a.ks.mask ? 0 : u.bound / kTileRows - u.lo;
+        each([&](const Unit<NT> &u) {
+            if (t >= u.nt) {
+                skipped += u.n;
+                return;
             }
+            const int n = u.n, whole = a.ks.mask ? 0 : u.bound / kTileRows - u.lo;   // the tiles attended wholly come first
             float m = kNegInf, l = 0.f;
             uint32_t o[32];
             for (int j = 0; j < n; ++j, ++it) {
@@ -270,12 +299,9 @@ cross_fwd_mma_kernel(const __grid_constant__ FwdMmaArgs a) {
 #pragma unroll
                 for (int k = 0; k < 32; ++k) o[k] = 0u;
             }
-            int again = unit;
-            if (C::kWalks) asm volatile("" : "+r"(again));      // worked out anew, not kept over the loop
-            const Unit<NT> u(a, place(again));
             if (CS == 1) {
                 int g, q;
-                if (!a.qt.at(u.t0 + t, r, g, q)) continue;
+                if (!a.qt.at(u.t0 + t, r, g, q)) return;
                 const int h = u.hk * a.qt.G + g;
                 const float inv = l == 0.f ? 0.f : 1.f / l;
                 uint4 *out = reinterpret_cast<uint4 *>(a.O.row(u.b, h, q) + 32 * half);
@@ -303,12 +329,12 @@ cross_fwd_mma_kernel(const __grid_constant__ FwdMmaArgs a) {
                     join_l[t * kTileRows + r] = l;
                 }
             }
-        }
+        });
     } else {
         give_registers<C::kRegsFew>();
         if (warp == C::kCopyWarp) {
             // ---- copies: they run ahead into the next unit ------------------------------
-            int ring = 0, units = 0;      // issued: key tiles, units' queries
+            int ring = 0, loaded = 0;      // issued: key tiles, units' queries
             bool ok = true;
             const auto queries = [&](const Unit<NT> &u) {
                 if (elect_one()) {
@@ -318,12 +344,10 @@ cross_fwd_mma_kernel(const __grid_constant__ FwdMmaArgs a) {
                                   u.b, &bar_q);
                 }
                 __syncwarp();
-                ++units;
+                ++loaded;
             };
-#pragma unroll 1
-            for (int unit = first; ok && (C::kWalks ? unit < a.units : unit == first); unit = C::kWalks ? unit + step : -1) {
-                const Unit<NT> u(a, place(unit));
-                const bool later = C::kWalks && units > 0;
+            const auto copies = [&](const Unit<NT> &u) {
+                const bool later = C::kWalks && loaded > 0;
                 for (int j = 0; ok && j < u.n; ++j) {
                     if (j == 0 && !later) queries(u);
                     const int s = ring % C::kStages;
@@ -337,14 +361,33 @@ cross_fwd_mma_kernel(const __grid_constant__ FwdMmaArgs a) {
                     __syncwarp();
                     ++ring;
                     if (j == 0 && later) {      // once the scores have read the last queries
-                        ok = pipe_wait(&bar_qfree, (units - 1) & 1, abort);
+                        ok = pipe_wait(&bar_qfree, (loaded - 1) & 1, abort);
                         if (ok) queries(u);
                     }
                 }
+            };
+            if constexpr (C::kWalks) {
+#pragma unroll 1
+                for (int k = 0, unit = first; ok; ++k, unit += step) {
+                    Unit<NT> u;
+                    if (unit < a.units) u = Unit<NT>(a, k ? Place<NT>(a, unit) : first_place);
+                    else u.n = -1;
+                    ok = k < 2 || pipe_wait(&bar_unitfree[k & 1], ((k >> 1) - 1) & 1, abort);
+                    if (!ok) break;
+                    if (lane == 0) {
+                        units[k & 1] = u;
+                        mbar_arrive(&bar_unit[k & 1]);
+                    }
+                    __syncwarp();
+                    if (u.n < 0) break;
+                    copies(u);
+                }
+            } else {
+                copies(Unit<NT>(a, first_place));
             }
             // leave no copy in flight
             if (lane == 0) {
-                if (units > 0) mbar_drain(&bar_q, (units - 1) & 1);
+                if (loaded > 0) mbar_drain(&bar_q, (loaded - 1) & 1);
                 for (int i = max(0, ring - C::kStages); i < ring; ++i)
                     mbar_drain(&bar_full[i % C::kStages], (i / C::kStages) & 1);
             }
@@ -352,10 +395,9 @@ cross_fwd_mma_kernel(const __grid_constant__ FwdMmaArgs a) {
             // ---- which keys of each tile are attended; the others' value rows cleared ----
             int ring = 0;
             bool ok = true;
-#pragma unroll 1
-            for (int unit = first; ok && (C::kWalks ? unit < a.units : unit == first); unit = C::kWalks ? unit + step : -1) {
-                const Unit<NT> u(a, place(unit));
-                for (int j = 0; j < u.n; ++j, ++ring) {
+            each([&](const Unit<NT> &u) {
+                const int n = u.n;
+                for (int j = 0; ok && j < n; ++j, ++ring) {
                     const int s = ring % C::kStages;
                     const uint4 w = tile_keys(a.ks, u.b, (u.lo + j) * kTileRows, u.bound);
                     ok = pipe_wait(&bar_full[s], (ring / C::kStages) & 1, abort);
@@ -370,7 +412,7 @@ cross_fwd_mma_kernel(const __grid_constant__ FwdMmaArgs a) {
                         mbar_arrive(&bar_ready[s]);
                     }
                 }
-            }
+            });
         } else {
             // ---- matrix instructions: the scores by one warp, the values by another, so that
             // neither waits for what the other needs.  The loops' course depends on uniform values
@@ -382,12 +424,10 @@ cross_fwd_mma_kernel(const __grid_constant__ FwdMmaArgs a) {
             if (warp == C::kScoreWarp) {
                 const uint32_t id = mma_desc(128, 128, false, a.negative);
                 const uint64_t dq = tile_desc(sq), dk = tile_desc(skv);
-                int units = 0;
-#pragma unroll 1
-                for (int unit = first; C::kWalks ? unit < a.units : unit == first; unit = C::kWalks ? unit + step : -1) {
-                    const Unit<NT> u(a, place(unit));
+                int loaded = 0;
+                each([&](const Unit<NT> &u) {
                     const int n = __shfl_sync(kFullMask, u.n, 0), nt = __shfl_sync(kFullMask, u.nt, 0);
-                    if (n > 0) pipe_wait(&bar_q, units++ & 1, abort);
+                    if (n > 0) pipe_wait(&bar_q, loaded++ & 1, abort);
                     for (int j = 0; j < n; ++j) {
                         pipe_wait(&bar_full[s], pass, abort);      // masked keys' scores are not looked at
                         const uint64_t dks = dk + (uint64_t)(s * (2 * kTileBytes >> 4));
@@ -412,13 +452,11 @@ cross_fwd_mma_kernel(const __grid_constant__ FwdMmaArgs a) {
                             pass ^= 1;
                         }
                     }
-                }
+                });
             } else {
                 const uint32_t id = mma_desc(128, 64, true);
                 const uint64_t dv = tile_desc(skv + kTileBytes);
-#pragma unroll 1
-                for (int unit = first; C::kWalks ? unit < a.units : unit == first; unit = C::kWalks ? unit + step : -1) {
-                    const Unit<NT> u(a, place(unit));
+                each([&](const Unit<NT> &u) {
                     const int n = __shfl_sync(kFullMask, u.n, 0), nt = __shfl_sync(kFullMask, u.nt, 0);
                     for (int j = 0; j < n; ++j) {
                         pipe_wait(&bar_ready[s], pass, abort);
@@ -443,7 +481,7 @@ cross_fwd_mma_kernel(const __grid_constant__ FwdMmaArgs a) {
                             pass ^= 1;
                         }
                     }
-                }
+                });
             }
             // no matrix instruction in flight when the tensor memory is freed
             uint64_t *end = &bar_end[warp == C::kValueWarp];
