@@ -314,7 +314,7 @@ fibatt_status fibatt_cross_fwd(const fibatt_cross *d, const fibatt_heads *Q, con
                                cudaStream_t stream);
 
 /* Device scratch of fibatt_cross_bwd, in bytes: two floats a query row, and in
- * 16 bits 32 bytes a row more (rows rounded up to 128 a head) and a counter. */
+ * 16 bits 32 bytes a row more (rows rounded up to 128 a head) and two counters. */
 size_t fibatt_cross_bwd_workspace_bytes(const fibatt_cross *d);
 
 /* Backward pass for the loss whose gradient with respect to O is dO:

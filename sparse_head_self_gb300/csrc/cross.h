@@ -3,6 +3,7 @@
 // operations and every argument rule are documented in include/fibatt.h.
 #pragma once
 
+#include <algorithm>
 #include <atomic>
 #include <cstdint>
 
@@ -56,6 +57,36 @@ bool fault(const char *kind);
 
 // Streaming multiprocessors of the current device.
 int sm_count();
+
+// CTAs of a cluster for `units` units that walk over `walk` tiles each: until
+// `places` CTAs, which the GPU holds at once, are taken, as long as each keeps a tile.
+inline int cluster_for(int64_t units, int64_t walk, int64_t places) {
+    int c = 1;
+    while (c < 8 && units * c * 2 <= places && walk >= 2 * c) c *= 2;
+    return c;
+}
+// A backward pass has two kinds of unit, whose walks may differ much (a few queries on
+// many keys: hundreds of units of one tile, and one of hundreds).  They go in one
+// launch, or in one of each kind with clusters of its own where the longest walk, or
+// all tiles over the places, is estimated to be over sooner.  In tiles: `unit`, what a
+// unit costs beside its walk, and `start`, another launch.
+struct Launches {
+    bool two;
+    int c, c_query, c_key;
+    Launches(int64_t query_units, int64_t query_walk, int64_t key_units, int64_t key_walk, int64_t places, int unit,
+             int start) {
+        const auto time = [&](int64_t units, int64_t walk, int c) {
+            return std::max((walk + c - 1) / c + unit, units * (walk + unit) / places);
+        };
+        c = cluster_for(query_units + key_units, std::max(query_walk, key_walk), places);
+        c_query = cluster_for(query_units, query_walk, places);
+        c_key = cluster_for(key_units, key_walk, places);
+        const int64_t longest = (std::max(query_walk, key_walk) + c - 1) / c + unit,
+                      all = query_units * (query_walk + unit) + key_units * (key_walk + unit),
+                      one = std::max(longest, all / places);
+        two = time(query_units, query_walk, c_query) + time(key_units, key_walk, c_key) + start < one;
+    }
+};
 
 // Launch `kern` on clusters of `c` CTAs along x, programmatic dependent when
 // the library launches that way.

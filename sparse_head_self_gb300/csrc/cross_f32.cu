@@ -390,6 +390,7 @@ struct BwdF32Args {
     float scale;
     int qtiles, ktiles;
     int key_units;        // units that hold keys; the others hold queries
+    int first;            // unit of the launch
 };
 
 // Holds 64 queries and walks over the keys.
@@ -499,17 +500,9 @@ __global__ void __launch_bounds__(kThreads, kBwdBlocks) cross_bwd_f32_kernel(con
     __shared__ __align__(16) float2 sst[kT];
     float *smem = reinterpret_cast<float *>(smem4);
     grid_dep_wait();
-    const int64_t unit = blockIdx.x / cluster_size();
+    const int64_t unit = a.first + blockIdx.x / cluster_size();
     if (unit < a.key_units) hold_keys(a, smem, sst, unit);
     else hold_queries(a, smem, unit - a.key_units);
-}
-
-// CTAs of a cluster for `units` units of `tiles` tiles each: until every SM has
-// its blocks, as long as each CTA keeps a tile.
-int split(int64_t units, int64_t tiles, int blocks) {
-    int c = 1;
-    while (c < 8 && units * c * 2 <= (int64_t)blocks * sm_count() && tiles >= 2 * c) c *= 2;
-    return c;
 }
 
 }  // namespace
@@ -520,7 +513,7 @@ cudaError_t launch_cross_fwd_f32(const CrossArgs &a) {
     if (e != cudaSuccess) return e;
     const int qtiles = (a.Nq + kT - 1) / kT;
     const int64_t units = (int64_t)a.B * a.Hq * qtiles;
-    const int c = split(units, (a.Nk + kT - 1) / kT, kFwdBlocks);
+    const int c = cluster_for(units, (a.Nk + kT - 1) / kT, kFwdBlocks * sm_count());
     return launch_clusters(cross_fwd_f32_kernel, (unsigned)(units * c), c, kThreads, smem, a.stream, a.Hq, a.Hkv, a.Nq,
                            a.keys, rows_of<const float>(a.Q), rows_of<const float>(a.K), rows_of<const float>(a.V),
                            rows_of<float>(a.O), a.LSE, a.scale * kLog2e, qtiles);
@@ -543,10 +536,19 @@ cudaError_t launch_cross_bwd_f32(const CrossArgs &a) {
     e = launch_clusters(cross_stats_kernel, (unsigned)((rows + 15) / 16), 1, 256, 0, a.stream, a.Hq, a.Nq, rows,
                         rows_of<const float>(a.O), f.dO, static_cast<const float *>(a.LSE), a.stats);
     if (e != cudaSuccess) return e;
-    const int64_t key_units = (int64_t)a.B * a.Hkv * f.ktiles, units = key_units + (int64_t)a.B * a.Hq * f.qtiles;
+    const int64_t key_units = (int64_t)a.B * a.Hkv * f.ktiles, query_units = (int64_t)a.B * a.Hq * f.qtiles;
     f.key_units = (int)key_units;
-    const int c = split(units, std::max<int64_t>(f.ktiles, (int64_t)(a.Hq / a.Hkv) * f.qtiles), kBwdBlocks);
-    return launch_clusters(cross_bwd_f32_kernel, (unsigned)(units * c), c, kThreads, smem, a.stream, f);
+    f.first = 0;
+    // (one head, 100 queries on 16385 keys: 270 us in two launches, 1937 in one)
+    const Launches l(query_units, f.ktiles, key_units, (int64_t)(a.Hq / a.Hkv) * f.qtiles, kBwdBlocks * sm_count(), 1,
+                     2);
+    if (!l.two)
+        return launch_clusters(cross_bwd_f32_kernel, (unsigned)((key_units + query_units) * l.c), l.c, kThreads, smem,
+                               a.stream, f);
+    e = launch_clusters(cross_bwd_f32_kernel, (unsigned)(key_units * l.c_key), l.c_key, kThreads, smem, a.stream, f);
+    if (e != cudaSuccess) return e;
+    f.first = f.key_units;
+    return launch_clusters(cross_bwd_f32_kernel, (unsigned)(query_units * l.c_query), l.c_query, kThreads, smem, a.stream, f);
 }
 
 FIBATT_DEFINE_ERROR_READER(read_error_cross_f32, "cross_f32.cu")

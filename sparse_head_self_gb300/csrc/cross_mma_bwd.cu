@@ -72,6 +72,7 @@ struct BwdMmaArgs {
     Rows<__nv_bfloat16> dQ, dK, dV;
     int B, Hq, Hkv, ktiles;
     int query_units, units;     // units that hold queries, which come first, and all of them
+    int first_unit;             // of the launch, which has those up to `units`
     int *next_unit;             // units given out behind every CTA's first
     float scale;
     float c;                    // scale log2 e, not 0
@@ -101,7 +102,7 @@ cross_parts_kernel(int Hq, int Nq, int npad, unsigned rows, Rows<const __nv_bflo
     grid_dep_launch();
     const unsigned row = blockIdx.x * 32 + (threadIdx.x >> 3);
     const int i = threadIdx.x & 7;
-    if (blockIdx.x == 0 && threadIdx.x == 0) *next_unit = 0;
+    if (blockIdx.x == 0 && threadIdx.x < 2) next_unit[threadIdx.x] = 0;
     if (row >= rows + kTileRows) return;   // whole groups of eight: the shuffles below stay within them
     const unsigned bh = row / (unsigned)npad, n = row - bh * npad;
     if (row >= rows || n >= (unsigned)Nq) {
@@ -167,7 +168,7 @@ cross_parts_few_kernel(int Hq, int Hkv, int Nq, int npad, unsigned heads, KeySet
     const int n0 = 16 * (int)(at - bh * groups);
     grid_dep_wait();
     grid_dep_launch();
-    if (at == 0 && lane == 0) *next_unit = 0;
+    if (at == 0 && lane < 2) next_unit[lane] = 0;
     if (bh >= heads) {      // rows of no query, behind the heads'
         const unsigned i = (at - heads * groups) * 16 + (lane >> 1);
         if (i >= (unsigned)kTileRows) return;
@@ -626,7 +627,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross_bwd_mma_kernel(const __grid
     // The CTA's units: its first, then what it draws from a counter, which the copying
     // warp does and passes on (CTAs that finish early take more; a unit's results do
     // not depend on who works on it).  A cluster has one unit.
-    const int CS = (int)cluster_size(), first = (int)(blockIdx.x / CS);
+    const int CS = (int)cluster_size(), first = a.first_unit + (int)(blockIdx.x / CS);
     const auto each = [&](auto next, auto queries, auto keys) {
         Unit u = next();
 #pragma unroll 1
@@ -662,7 +663,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross_bwd_mma_kernel(const __grid
                 Unit u;
                 u.enter(a, __shfl_sync(kFullMask, drawn, 0));
                 drawn = a.units;
-                if (CS == 1 && lane == 0 && u.index < a.units) drawn = (int)gridDim.x + atomicAdd(a.next_unit, 1);
+                if (CS == 1 && lane == 0 && u.index < a.units) drawn = a.first_unit + (int)gridDim.x + atomicAdd(a.next_unit, 1);
                 ok = ok && (passed < 2 || pipe_wait(&sh.unit_empty[i], ((passed >> 1) - 1) & 1, &sh.abort));
                 if (!ok) u.index = a.units;
                 else if (lane == 0) {
@@ -717,7 +718,7 @@ int padded_rows(int Nq) { return Nq < kTileRows ? Nq : (Nq + kTileRows - 1) / kT
 
 size_t cross_bwd_mma_workspace(int B, int Hq, int Nq) {
     const size_t rows = (size_t)B * Hq * padded_rows(Nq);
-    return 2 * (rows + kTileRows) * sizeof(uint4) + (size_t)B * Hq * Nq * sizeof(float2) + sizeof(int);
+    return 2 * (rows + kTileRows) * sizeof(uint4) + (size_t)B * Hq * Nq * sizeof(float2) + 2 * sizeof(int);
 }
 
 cudaError_t launch_cross_bwd_mma(const CrossArgs &a) {
@@ -757,14 +758,23 @@ cudaError_t launch_cross_bwd_mma(const CrossArgs &a) {
                             static_cast<const float *>(a.LSE), f.c, stats, lse_parts, d_parts, f.next_unit);
     }
     if (e != cudaSuccess) return e;
-    const int64_t query_units = (int64_t)a.B * a.Hkv * f.qt.tiles, units = query_units + (int64_t)a.B * a.Hkv * f.ktiles;
+    const int64_t query_units = (int64_t)a.B * a.Hkv * f.qt.tiles, key_units = (int64_t)a.B * a.Hkv * f.ktiles;
     f.query_units = (int)query_units;
-    f.units = (int)units;
     // clusters, one unit each, while they all find a place; else one wave of CTAs that walk over the units
-    int c = 1;
-    while (c < 8 && units * c * 2 <= sm_count() && std::max(f.ktiles, f.qt.tiles) >= 2 * c) c *= 2;
-    const int64_t grid = c > 1 ? units * c : std::min<int64_t>(units, sm_count());
-    return launch_clusters(cross_bwd_mma_kernel, (unsigned)grid, c, kThreads, kSmem, a.stream, f);
+    const auto launch = [&](int64_t from, int64_t units, int c) {
+        f.first_unit = (int)from;
+        f.units = (int)(from + units);
+        const int64_t grid = c > 1 ? units * c : std::min<int64_t>(units, sm_count());
+        return launch_clusters(cross_bwd_mma_kernel, (unsigned)grid, c, kThreads, kSmem, a.stream, f);
+    };
+    // (one head, 100 queries on 16385 keys: 27 us in two launches, 82 in one; 16 heads, 100 on 5000:
+    // 44 and 36)
+    const Launches l(query_units, f.ktiles, key_units, f.qt.tiles, sm_count(), 5, 12);
+    if (!l.two) return launch(0, query_units + key_units, l.c);
+    e = launch(0, query_units, l.c_query);
+    if (e != cudaSuccess) return e;
+    ++f.next_unit;
+    return launch(query_units, key_units, l.c_key);
 }
 
 FIBATT_DEFINE_ERROR_READER(read_error_cross_mma_bwd, "cross_mma_bwd.cu")

@@ -477,3 +477,14 @@ def test_gradients_of_few_keys_have_two_roundings(Nk, mask):
         check(name, got[name], want[name])
         err = float((got[name].double() - exact).norm() / exact.norm())
         assert err <= math.sqrt(2 / 3) * 2.0 ** -8, (name, err)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("size", [(1, 1, 1, 30, 9000), (1, 2, 1, 9000, 20), (2, 6, 2, 40, 16385), (1, 4, 1, 2000, 300), (4, 4, 4, 100, 5000)],
+                         ids=lambda s: "x".join(map(str, s)))
+@pytest.mark.parametrize("mask", ["none", "len"])
+def test_gradients_of_few_rows_on_many(dtype, size, mask):
+    # one side's units walk over hundreds of tiles, the other's over one
+    q, k, v, do = _inputs(dtype, *size, seed=59)
+    n = None if mask == "none" else torch.full((size[0],), size[4] * 2 // 3, dtype=torch.int32, device="cuda")
+    _check_all(q, k, v, do, 0.125, n)
