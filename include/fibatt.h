@@ -322,7 +322,8 @@ size_t fibatt_cross_bwd_workspace_bytes(const fibatt_cross *d);
  *     dQ_j = scale sum_k dS_jk K_k,   dK_k = scale sum_j dS_jk Q_j,   dV_k = sum_j P_jk dO_j,
  * the last two over the queries of every head that shares the key head.  No
  * atomics: results do not depend on scheduling.  For bf16, P and dS are
- * rounded to bf16 before the products that sum them.  O and LSE are
+ * rounded to bf16 before the products that sum them, and for at most 64 keys D
+ * is summed as sum_k P_jk <dO_j, V_k>, which O's rounding does not enter.  O and LSE are
  * fibatt_cross_fwd's.  workspace: 16-byte aligned, for one call at a time.
  * Errors as fibatt_cross_fwd, plus INVALID_ARG for a workspace too small. */
 fibatt_status fibatt_cross_bwd(const fibatt_cross *d, const fibatt_heads *Q, const fibatt_heads *K,

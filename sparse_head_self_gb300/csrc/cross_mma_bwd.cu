@@ -22,7 +22,8 @@
 //
 // Both kinds are units of one launch, one wave of CTAs that draw them from a
 // counter, queries first (each CTA every 152nd unit instead: 613 us where this
-// takes 595, below); the copies run ahead into the next unit.  Warps: 16 that turn
+// took 595), or two, one of each kind, where their walks differ much; the copies
+// run ahead into the next unit.  Warps: 16 that turn
 // S and dP into P and dS (a warp has 32 rows and 32 columns of the tile; four warps
 // on every scheduler hide each other's waits), one that copies and draws, one that
 // prepares what goes with a streamed tile (the keys attended, the clearing of the
@@ -31,11 +32,11 @@
 // product over rows is read from tensor memory, as bf16 (relative rounding 2^-8
 // a weight, averaging out over the sum).
 //
-// Measured: 2 sequences, 16 heads, 1569 x 16385: 594 us, 887 TFLOP/s of the 5
-// products (1241 of the 7), the small kernel 6 of them; 8 sequences, 12 heads on 4,
-// 197 x 1569 of several lengths: 39.5 us, the small kernel 4.5.  A tile takes about 1490
-// cycles, its 3 or 4 products 800 or 1090 of them; the tensor cores are 60% busy, the
-// issue slots 50%: what is left are the waits from S to dS to the products, which need
+// Measured: 2 sequences, 16 heads, 1569 x 16385: 583 us, 903 TFLOP/s of the 5
+// products (1264 of the 7), the small kernel 6 of them; 8 sequences, 12 heads on 4,
+// 197 x 1569 of several lengths: 37.6 us, the small kernel 4.5.  A tile takes about 1490
+// cycles, its 3 or 4 products 800 or 1090 of them; the tensor cores are 61% busy, the
+// issue slots 49%: what is left are the waits from S to dS to the products, which need
 // each other within a tile.
 #include <algorithm>
 

@@ -24,14 +24,14 @@
 // cut over a cluster, whose CTAs join their (m, l, O) through distributed shared
 // memory in rank order.  CTAs of one tile are one wave, two a SM, that walks over
 // the units: copies and scores run ahead into the next unit while the softmax
-// finishes this one (768 units of 65 x 197: 19.1 -> 17.6 us).  CTAs of two tiles
+// finishes this one (768 units of 65 x 197: 19.1 -> 16.5 us).  CTAs of two tiles
 // are not: their softmax has no register to spare for the walk, which cost 10% of
 // every tile.
 //
 // Measured: 2 sequences, 16 heads, 1569 x 16385: 227 us, 927 TFLOP/s (clusters of
-// two; one CTA a unit, 1.47 rounds: 266); 16 heads, 4096 x 4096: 75 us, 920; 8
+// two; one CTA a unit, 1.47 rounds: 266); 16 heads, 4096 x 4096: 75 us, 919; 8
 // sequences, 12 heads, 197 x 1569: 20 us; 64 sequences, 12 heads, 65 x 197, masked:
-// 21.5 us.  A pair of tiles takes about 1900 cycles: 1094 of matrix instructions
+// 20.0 us.  A pair of tiles takes about 1900 cycles: 1094 of matrix instructions
 // (128 x 128 x 64 from shared memory 257, 128 x 64 x 128 with P in tensor memory
 // 290), 1024 of exponentials (4 cycles a warp and scheduler), which overlap but for
 // the waits between them; the issue slots are 59% taken.  The short shapes are bound by the
@@ -562,7 +562,7 @@ int clusters_held(int i) {
 // two 229, of four 289; 8 sequences, 12 heads, 197 x 1569, 96 units: 20, 35, 48; one
 // sequence, 16 heads, 197 x 4096: one-tile CTAs, clusters of one 31, of four 16.5, of
 // eight 18, two-tile CTAs 37, 19 and 31; 768 units of one tile by two: one-tile CTAs
-// 17.6, two-tile ones 23.)
+// 16.5, two-tile ones 23.)
 struct Plan {
     int nt = 0, c = 1;
     float cost = 0.f;
