@@ -60,9 +60,9 @@ int sm_count();
 
 // CTAs of a cluster for `units` units that walk over `walk` tiles each: until
 // `places` CTAs, which the GPU holds at once, are taken, as long as each keeps a tile.
-inline int cluster_for(int64_t units, int64_t walk, int64_t places) {
+inline int cluster_for(int64_t units, int64_t walk, int64_t places, int most = 8) {
     int c = 1;
-    while (c < 8 && units * c * 2 <= places && walk >= 2 * c) c *= 2;
+    while (c < most && units * c * 2 <= places && walk >= 2 * c) c *= 2;
     return c;
 }
 // A backward pass has two kinds of unit, whose walks may differ much (a few queries on
@@ -74,13 +74,13 @@ struct Launches {
     bool two;
     int c, c_query, c_key;
     Launches(int64_t query_units, int64_t query_walk, int64_t key_units, int64_t key_walk, int64_t places, int unit,
-             int start) {
+             int start, int most = 8) {
         const auto time = [&](int64_t units, int64_t walk, int c) {
             return std::max((walk + c - 1) / c + unit, units * (walk + unit) / places);
         };
-        c = cluster_for(query_units + key_units, std::max(query_walk, key_walk), places);
-        c_query = cluster_for(query_units, query_walk, places);
-        c_key = cluster_for(key_units, key_walk, places);
+        c = cluster_for(query_units + key_units, std::max(query_walk, key_walk), places, most);
+        c_query = cluster_for(query_units, query_walk, places, most);
+        c_key = cluster_for(key_units, key_walk, places, most);
         const int64_t longest = (std::max(query_walk, key_walk) + c - 1) / c + unit,
                       all = query_units * (query_walk + unit) + key_units * (key_walk + unit),
                       one = std::max(longest, all / places);
