@@ -529,12 +529,14 @@ cross_fwd_mma_kernel(const __grid_constant__ FwdMmaArgs a) {
 template <int NT>
 int clusters_held(int i) {
     using C = Cfg<NT>;
-    static std::atomic<int> known[4];
+    static std::atomic<int> known[5];
     int held = known[i].load(std::memory_order_relaxed);
     if (held) return held;
     if (i == 0) {
         held = C::kMinBlocks * sm_count();
     } else {
+        if (i == 4)       // clusters of more than eight have to be asked for
+            (void)cudaFuncSetAttribute(cross_fwd_mma_kernel<NT>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
         cudaLaunchConfig_t cfg = {};
         cudaLaunchAttribute attr;
         attr.id = cudaLaunchAttributeClusterDimension;
@@ -545,9 +547,8 @@ int clusters_held(int i) {
         cfg.dynamicSmemBytes = C::kSmem;
         cfg.attrs = &attr;
         cfg.numAttrs = 1;
-        // none that size: as if it held one, which no plan prefers
         if (cudaOccupancyMaxActiveClusters(&held, cross_fwd_mma_kernel<NT>, &cfg) != cudaSuccess) (void)cudaGetLastError();
-        held = std::max(held, 1);
+        if (held < 1) held = -1;      // none of that size
     }
     known[i].store(held, std::memory_order_relaxed);
     return held;
@@ -562,7 +563,7 @@ int clusters_held(int i) {
 // two 229, of four 289; 8 sequences, 12 heads, 197 x 1569, 96 units: 20, 35, 48; one
 // sequence, 16 heads, 197 x 4096: one-tile CTAs, clusters of one 31, of four 16.5, of
 // eight 18, two-tile CTAs 37, 19 and 31; 768 units of one tile by two: one-tile CTAs
-// 16.5, two-tile ones 23.)
+// 16.5, two-tile ones 23; one head, 100 x 16385: clusters of eight 21.7, of sixteen 17.3.)
 struct Plan {
     int nt = 0, c = 1;
     float cost = 0.f;
@@ -574,8 +575,9 @@ cudaError_t consider(const CrossArgs &a, const QueryTiles &qt, Plan *best) {
     if (e != cudaSuccess) return e;
     const int64_t units = (int64_t)a.B * a.Hkv * ((qt.tiles + NT - 1) / NT);
     const int tiles = (a.Nk + kTileRows - 1) / kTileRows;
-    for (int i = 0; i < 4 && (i == 0 || tiles >= 1 << i); ++i) {
+    for (int i = 0; i < 5 && (i == 0 || tiles >= 1 << i); ++i) {
         const int c = 1 << i, held = clusters_held<NT>(i);
+        if (held < 1) break;
         const float tile = NT == 2 ? (qt.tiles > 1 ? 1.f : 0.78f) : units * c > sm_count() ? 1.28f : 0.83f;
         const float rounds = (float)((units + held - 1) / held), mine = (float)((tiles + c - 1) / c) * tile;
         const float cost = i > 0          ? rounds * (mine + 9.5f)
