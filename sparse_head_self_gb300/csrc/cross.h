@@ -11,6 +11,7 @@
 
 #include "fibatt.h"
 #include "fibatt_internal.h"
+#include "per_device.h"
 
 namespace fibatt {
 
@@ -57,6 +58,34 @@ bool fault(const char *kind);
 
 // Streaming multiprocessors of the current device.
 int sm_count();
+// The current device, -1 if it cannot be told.
+inline int current_device() {
+    int dev = -1;
+    return cudaGetDevice(&dev) == cudaSuccess ? dev : -1;
+}
+
+// How many clusters of `c` CTAs of kernel K the current device holds at once (-1:
+// none).  More than eight CTAs have to be asked for, on each device.
+template <auto K>
+int clusters_held(int c, unsigned threads, size_t smem) {
+    if (c > 8 && cudaFuncSetAttribute(K, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess) {
+        (void)cudaGetLastError();
+        return -1;
+    }
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = (unsigned)c;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cfg.gridDim = dim3((unsigned)c);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    int held = 0;
+    if (cudaOccupancyMaxActiveClusters(&held, K, &cfg) != cudaSuccess) (void)cudaGetLastError();
+    return held > 0 ? held : -1;
+}
 
 // CTAs of a cluster for `units` units that walk over `walk` tiles each: until
 // `places` CTAs, which the GPU holds at once, are taken, as long as each keeps a tile.

@@ -505,31 +505,11 @@ __global__ void __launch_bounds__(kThreads, kBwdBlocks) cross_bwd_f32_kernel(con
     else hold_queries(a, smem, unit - a.key_units);
 }
 
-// The largest cluster of this kernel: 16 CTAs where the GPU takes them (beyond 8 it has
-// to be asked for), else 8.
+// The largest cluster of this kernel: 16 CTAs where the current device takes them, else 8.
 template <auto Kernel>
 int largest_cluster(size_t smem) {
-    static std::atomic<int> known{0};
-    int most = known.load(std::memory_order_relaxed);
-    if (most) return most;
-    most = 8;
-    if (cudaFuncSetAttribute(Kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess) {
-        cudaLaunchConfig_t cfg = {};
-        cudaLaunchAttribute attr;
-        attr.id = cudaLaunchAttributeClusterDimension;
-        attr.val.clusterDim.x = 16;
-        attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-        cfg.gridDim = dim3(16);
-        cfg.blockDim = dim3(kThreads);
-        cfg.dynamicSmemBytes = smem;
-        cfg.attrs = &attr;
-        cfg.numAttrs = 1;
-        int held = 0;
-        if (cudaOccupancyMaxActiveClusters(&held, Kernel, &cfg) == cudaSuccess && held > 0) most = 16;
-    }
-    if (most == 8) (void)cudaGetLastError();
-    known.store(most, std::memory_order_relaxed);
-    return most;
+    static PerDevice known;
+    return known.get(current_device(), [=] { return clusters_held<Kernel>(16, kThreads, smem) > 0 ? 16 : 8; });
 }
 
 }  // namespace

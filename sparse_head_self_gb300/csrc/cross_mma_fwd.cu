@@ -525,33 +525,15 @@ cross_fwd_mma_kernel(const __grid_constant__ FwdMmaArgs a) {
     cluster_sync();   // the others may still read this CTA's part
 }
 
-// How many clusters of 2^i CTAs the GPU holds at once.
+// How many clusters of 2^i CTAs device `dev`, the current one, holds at once.
 template <int NT>
-int clusters_held(int i) {
+int held_clusters(int dev, int i) {
     using C = Cfg<NT>;
-    static std::atomic<int> known[5];
-    int held = known[i].load(std::memory_order_relaxed);
-    if (held) return held;
-    if (i == 0) {
-        held = C::kMinBlocks * sm_count();
-    } else {
-        if (i == 4)       // clusters of more than eight have to be asked for
-            (void)cudaFuncSetAttribute(cross_fwd_mma_kernel<NT>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-        cudaLaunchConfig_t cfg = {};
-        cudaLaunchAttribute attr;
-        attr.id = cudaLaunchAttributeClusterDimension;
-        attr.val.clusterDim.x = 1u << i;
-        attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-        cfg.gridDim = dim3(1u << i);
-        cfg.blockDim = dim3(C::kThreads);
-        cfg.dynamicSmemBytes = C::kSmem;
-        cfg.attrs = &attr;
-        cfg.numAttrs = 1;
-        if (cudaOccupancyMaxActiveClusters(&held, cross_fwd_mma_kernel<NT>, &cfg) != cudaSuccess) (void)cudaGetLastError();
-        if (held < 1) held = -1;      // none of that size
-    }
-    known[i].store(held, std::memory_order_relaxed);
-    return held;
+    static PerDevice known[5];
+    return known[i].get(dev, [=] {
+        return i == 0 ? C::kMinBlocks * sm_count()
+                      : clusters_held<cross_fwd_mma_kernel<NT>>(1 << i, C::kThreads, C::kSmem);
+    });
 }
 
 // Query tiles of a CTA and CTAs of a cluster: those with the shortest estimate
@@ -574,9 +556,9 @@ cudaError_t consider(const CrossArgs &a, const QueryTiles &qt, Plan *best) {
     const cudaError_t e = prepare_kernel<cross_fwd_mma_kernel<NT>>(C::kSmem, C::kRegs);
     if (e != cudaSuccess) return e;
     const int64_t units = (int64_t)a.B * a.Hkv * ((qt.tiles + NT - 1) / NT);
-    const int tiles = (a.Nk + kTileRows - 1) / kTileRows;
+    const int tiles = (a.Nk + kTileRows - 1) / kTileRows, dev = current_device();
     for (int i = 0; i < 5 && (i == 0 || tiles >= 1 << i); ++i) {
-        const int c = 1 << i, held = clusters_held<NT>(i);
+        const int c = 1 << i, held = held_clusters<NT>(dev, i);
         if (held < 1) break;
         const float tile = NT == 2 ? (qt.tiles > 1 ? 1.f : 0.78f) : units * c > sm_count() ? 1.28f : 0.83f;
         const float rounds = (float)((units + held - 1) / held), mine = (float)((tiles + c - 1) / c) * tile;
