@@ -464,14 +464,24 @@ def _readable(t):
     return t if ok else t.clone(memory_format=torch.contiguous_format)
 
 
+def _dense(t):
+    """t (or None), or a copy: contiguous and on 16 bytes, which a contiguous
+    part of a larger tensor need not be (a weight in a flat buffer of all
+    parameters, a gradient that comes through a concatenation)."""
+    if t is None or (t.is_contiguous() and t.data_ptr() % 16 == 0):
+        return t
+    return t.clone(memory_format=torch.contiguous_format)
+
+
 class QkNormFunction(torch.autograd.Function):
     """Autograd wrapper: forward = fibatt_qk_norm_fwd, backward = fibatt_qk_norm_bwd."""
 
     @staticmethod
     def forward(ctx, x, q_weight, k_weight, heads, eps, rotary, positions, interleaved):
-        x = _readable(x)
+        x, q_weight, k_weight = _readable(x), _dense(q_weight), _dense(k_weight)
         ctx.how = (tuple(heads), float(eps), bool(interleaved))
-        cos, sin = (None, None) if rotary is None else rotary
+        cos, sin = (None, None) if rotary is None else (_dense(t) for t in rotary)
+        rotary = None if rotary is None else (cos, sin)
         ctx.save_for_backward(x, q_weight, k_weight, cos, sin, positions)
         ctx.set_materialize_grads(False)
         out = qk_norm_fwd(x, heads, q_weight, k_weight, eps, rotary, positions, interleaved)
@@ -484,7 +494,7 @@ class QkNormFunction(torch.autograd.Function):
         x, q_weight, k_weight, cos, sin, positions = ctx.saved_tensors
         heads, eps, interleaved = ctx.how
         rotary = None if cos is None else (cos, sin)
-        grads = [g if s is None else torch.zeros(s, dtype=x.dtype, device=x.device) if g is None else g.contiguous()
+        grads = [g if s is None else torch.zeros(s, dtype=x.dtype, device=x.device) if g is None else _dense(g)
                  for g, s in zip(grads, ctx.shapes)]
         dx, dqw, dkw = qk_norm_bwd(x, heads, q_weight, k_weight, *grads, eps, rotary, positions, interleaved)
         return dx, dqw, dkw, None, None, None, None, None

@@ -245,3 +245,25 @@ def test_workspaces_of_other_places_are_refused():
     x, w, _, grads = _case(BF16, 2, 5, (2, 1, 1), 64)
     with pytest.raises(ValueError, match="workspace must be a CUDA tensor"):
         api.qk_norm_bwd(x, (2, 1, 1), *w, *grads, workspace=torch.empty(1 << 20, dtype=torch.uint8))
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
+def test_gradients_weights_and_tables_off_16_bytes(dtype):
+    # contiguous parts of larger tensors: a gradient through a concatenation behind one element,
+    # weights and tables in a flat buffer behind one
+    heads = (4, 2, 2)
+    x, w, rotary, grads = _case(dtype, 2, 13, heads, 64)
+    x.requires_grad_()
+    flat = torch.cat([w[0][:1], *w]).requires_grad_()
+    wide = [torch.cat([t.flatten()[:1], t.flatten()])[1:].view_as(t) for t in rotary]
+    assert flat[1:].data_ptr() % 16 and all(t.is_contiguous() and t.data_ptr() % 16 for t in wide)
+    out = api.qk_norm(x, heads, flat[1:65], flat[65:], rotary=wide)
+    joined = torch.cat([t for o in out for t in (x.new_zeros(1), o.flatten())])
+    joined.backward(torch.cat([t for g in grads for t in (x.new_zeros(1), g.flatten())]))
+    want = qk_norm(x.detach(), heads, *w, 1e-6, rotary, None, False)
+    for name, t in zip("QKV", out):
+        check(name, t.detach(), want[name])
+    want = qk_norm(x.detach(), heads, *w, 1e-6, rotary, None, False, grads)
+    check("dx", x.grad, want["dx"])
+    check("dwq", flat.grad[1:65], want["dwq"])
+    check("dwk", flat.grad[65:], want["dwk"])
