@@ -35,6 +35,13 @@ class _Rotary(nn.Module):
         return self.cos, self.sin
 
 
+def _weight(w, x: torch.Tensor):
+    """A norm's weight (or None) in the type of the projection x: under autocast x
+    has 16 bits and the parameter 32, and it is rounded as the projection's own
+    weights are (its gradient comes back through the cast)."""
+    return None if w is None else w.to(x.dtype)
+
+
 class FibottentionSelfAttention(nn.Module):
     """x [B, N, dim] -> [B, N, dim] with dim = heads * 64.
 
@@ -72,7 +79,7 @@ class FibottentionSelfAttention(nn.Module):
             raise ValueError(f"sequence length {N}, layer built for {self.N}")
         qkv = self.qkv(x)
         if self.q_norm is not None or self.rotary is not None:
-            q, k, v = qk_norm(qkv, (self.heads,) * 3, self.q_norm, self.k_norm, self.eps,
+            q, k, v = qk_norm(qkv, (self.heads,) * 3, _weight(self.q_norm, qkv), _weight(self.k_norm, qkv), self.eps,
                               None if self.rotary is None else self.rotary.tables(), self.positions)
         else:
             qkv = qkv.view(B, N, 3, self.heads, HEAD_DIM).permute(2, 0, 3, 1, 4)
@@ -114,7 +121,8 @@ class CrossAttention(nn.Module):
 
     def states(self, y: torch.Tensor, positions: torch.Tensor | None = None):
         """Keys and values [B, kv_heads, Nk, 64] of the encoder's states."""
-        return qk_norm(self.kv(y), (0, self.kv_heads, self.kv_heads), None, self.k_norm, self.eps,
+        kv = self.kv(y)
+        return qk_norm(kv, (0, self.kv_heads, self.kv_heads), None, _weight(self.k_norm, kv), self.eps,
                        None if self.state_rotary is None else self.state_rotary.tables(), positions)[1:]
 
     def forward(self, x: torch.Tensor, y: torch.Tensor | None = None, kv_len: torch.Tensor | None = None,
@@ -128,7 +136,7 @@ class CrossAttention(nn.Module):
         k, v = self.states(y) if kv is None else kv
         q = self.q(x)
         if self.q_norm is not None or self.rotary is not None:
-            q = qk_norm(q, (self.heads, 0, 0), self.q_norm, None, self.eps,
+            q = qk_norm(q, (self.heads, 0, 0), _weight(self.q_norm, q), None, self.eps,
                         None if self.rotary is None else self.rotary.tables(), positions)[0]
         else:
             q = q.view(B, Nq, self.heads, HEAD_DIM).transpose(1, 2)

@@ -169,6 +169,36 @@ def test_layers_in_16_bits_keep_their_angles():
     assert float((y.float() - wide).abs().mean()) <= 10 * 2.0 ** -8 * float(wide.abs().mean())
 
 
+@pytest.mark.parametrize("norm", [True, False])
+def test_layers_under_autocast(norm):
+    # autocast rounds inputs and weights where the layers in 16 bits hold them so: the same numbers
+    torch.manual_seed(5)
+    B, H, N, Nq = 2, 3, 65, 21
+    rot = api.rotary_angles(N)
+
+    def layers():
+        return (FibottentionSelfAttention(H * 64, H, N, 5, N, norm=norm, rotary=rot),
+                CrossAttention(H * 64, H, kv_heads=1, norm=norm, rotary=rot, state_rotary=rot))
+
+    wide, short = [m.cuda() for m in layers()], [m.cuda() for m in layers()]
+    for a, b in zip(wide, short):
+        with torch.no_grad():
+            for p in (a.q_norm, a.k_norm):
+                if p is not None:
+                    p.add_(0.2 * torch.randn(64, device="cuda"))
+        b.load_state_dict(a.state_dict())
+        b.bfloat16()
+    x, y = torch.randn(B, N, H * 64, device="cuda"), torch.randn(B, Nq, H * 64, device="cuda")
+    g = torch.randn(B, Nq, H * 64, device="cuda").bfloat16()
+    with torch.autocast("cuda", dtype=torch.bfloat16):
+        got = _run(lambda x, y: wide[1](y, wide[0](x)), [x, y], wide, g)
+    want = _run(lambda x, y: short[1](y, short[0](x)), [x.bfloat16(), y.bfloat16()], short, g)
+    assert len(got) == len(want) and got[0].dtype is torch.bfloat16
+    for i, (a, b) in enumerate(zip(got, want)):
+        assert a.dtype is (torch.bfloat16 if i == 0 else torch.float32), i
+        assert torch.equal(a.float(), b.float()), i
+
+
 FIRST_CALL = """
 import sys, torch
 from sparse_head_self_gb300 import api
