@@ -256,7 +256,8 @@ size_t fibatt_qk_norm_bwd_workspace_bytes(void);
  * (strides as X's; may not overlap X) and to the weights' gradients
  * dq_weight, dk_weight [64] in the I/O type, summed over all tokens and heads
  * in fp32 in a fixed order (written only where the weight is not NULL; either
- * may be NULL when its gradient is not wanted).  workspace: 16-byte aligned,
+ * may be NULL when its gradient is not wanted).  Heads of a kind without a
+ * weight are not read from X, on which their gradient does not depend.  workspace: 16-byte aligned,
  * for one call at a time. */
 fibatt_status fibatt_qk_norm_bwd(const fibatt_qk_norm *d, const void *X, int64_t x_stride_b,
                                  int64_t x_stride_n, const void *dQ, const void *dK, const void *dV,

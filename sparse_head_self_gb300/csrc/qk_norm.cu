@@ -401,7 +401,8 @@ qk_norm_bwd_kernel(const __grid_constant__ NormArgs<T> a, const T *__restrict__ 
 
     Tokens ahead, here;
     Place load(H, chunks), work(H, chunks);
-    // the next (unit, head): its rows of X (not those of values) and of the gradient
+    // the next (unit, head): its rows of the gradient and, where there is a norm, of X (what
+    // else X holds does not matter to the gradient: an infinity there would give 0 inf)
     const auto fetch = [&](int slot) {
         if (load.item < items && load.h < load.hi) {
             int hi, Hs;
@@ -410,7 +411,8 @@ qk_norm_bwd_kernel(const __grid_constant__ NormArgs<T> a, const T *__restrict__ 
             for (int s = 0; s < kSteps; ++s)
                 if (ahead.in[s]) {
                     T *dst = ring + (slot * 16 + 4 * s + grp) * 64;
-                    if (load.h < Hn) copy_row(dst, X + ahead.packed(s, load.h, x_sb, x_sn));
+                    if (load.h < Hn && (load.h < a.Hq ? a.wq : a.wk))
+                        copy_row(dst, X + ahead.packed(s, load.h, x_sb, x_sn));
                     copy_row(dst + 8 * 64, src + ahead.dense(s, hi, Hs, a.N));
                 }
             if (load.next(H, chunks)) ahead.set(load.unit, tokens, a.N);
@@ -449,30 +451,33 @@ qk_norm_bwd_kernel(const __grid_constant__ NormArgs<T> a, const T *__restrict__ 
                 Eight<T> grad;
                 grad.load(src + 8 * 64, a0, a1);
                 if (isn) {
-                    Eight<T> raw;
-                    raw.load(src, a0, a1);
-                    float2 x[4], dy[4];
-                    raw.get(x);
+                    float2 dy[4];
                     grad.get(dy);
                     if (a.rot) {
                         Turn<PAIRS_INSIDE> turn;
                         turn.load(angles + (buf * kTokens + (warp & 1) * 8 + 4 * s + grp) * 64, a.rot, sub);
                         turn.template apply<true>(dy);
                     }
-                    const float r = norm ? rsqrtf(sum8(squares(x)) * (1.f / 64.f) + a.eps) : 1.f;
-                    float2 dot = make_float2(0.f, 0.f);
-                    const bool in = here.in[s];      // the slot of no token holds anything: its sums are left out
+                    if (norm) {
+                        Eight<T> raw;
+                        raw.load(src, a0, a1);
+                        float2 x[4];
+                        raw.get(x);
+                        const float r = rsqrtf(sum8(squares(x)) * (1.f / 64.f) + a.eps);
+                        float2 dot = make_float2(0.f, 0.f);
+                        const bool in = here.in[s];      // the slot of no token holds anything: its sums are left out
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        x[e] = mul2(x[e], make_float2(r, r));
-                        if (in && isq) dwq[e] = fma2(dy[e], x[e], dwq[e]);
-                        else if (in) dwk[e] = fma2(dy[e], x[e], dwk[e]);
-                        dy[e] = mul2(dy[e], w[e]);
-                        dot = fma2(dy[e], x[e], dot);
+                        for (int e = 0; e < 4; ++e) {
+                            x[e] = mul2(x[e], make_float2(r, r));
+                            if (in && isq) dwq[e] = fma2(dy[e], x[e], dwq[e]);
+                            else if (in) dwk[e] = fma2(dy[e], x[e], dwk[e]);
+                            dy[e] = mul2(dy[e], w[e]);
+                            dot = fma2(dy[e], x[e], dot);
+                        }
+                        const float m = sum8(dot.x + dot.y) * (-1.f / 64.f);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) dy[e] = mul2(make_float2(r, r), fma2(x[e], make_float2(m, m), dy[e]));
                     }
-                    const float m = sum8(dot.x + dot.y) * (norm ? -1.f / 64.f : 0.f);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) dy[e] = mul2(make_float2(r, r), fma2(x[e], make_float2(m, m), dy[e]));
                     grad.put(dy);
                 }
                 if (here.in[s]) grad.store(dX + here.packed(s, work.h, dx_sb, dx_sn), a0, a1);

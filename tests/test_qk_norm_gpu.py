@@ -267,3 +267,26 @@ def test_gradients_weights_and_tables_off_16_bytes(dtype):
     check("dx", x.grad, want["dx"])
     check("dwq", flat.grad[1:65], want["dwq"])
     check("dwk", flat.grad[65:], want["dwk"])
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("weights", [(False, False), (True, False), (False, True)])
+@pytest.mark.parametrize("bad", [math.inf, -math.inf, math.nan])
+def test_gradient_without_a_norm_does_not_depend_on_the_input(dtype, weights, bad):
+    heads = (4, 3, 2)
+    x, w, rotary, grads = _case(dtype, 2, 21, heads, 32, weights)
+    want = api.qk_norm_bwd(x, heads, *w, *grads, rotary=rotary)
+    h = x.view(2, 21, 9, 64)
+    if not weights[0]:
+        h[:, 3::5, :4, 7] = bad
+    if not weights[1]:
+        h[:, ::4, 4:7, 50] = bad
+    h[:, :, 7:] = bad                # values: copied, whatever they are
+    got = api.qk_norm_bwd(x, heads, *w, *grads, rotary=rotary)
+    for a, b in zip(got, want):
+        assert (a is None) == (b is None) and (a is None or torch.equal(a, b))
+    # large finite gradients and inputs, whose product is beyond the type: dx is dy turned back
+    if not any(weights):
+        big = [g * 1e30 for g in grads]
+        ref = qk_norm(torch.zeros_like(x), heads, None, None, 1e-6, rotary, None, False, big)["dx"]
+        check("dx", api.qk_norm_bwd(torch.full_like(x, 1e30), heads, None, None, *big, rotary=rotary)[0], ref)
