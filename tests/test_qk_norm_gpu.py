@@ -290,3 +290,34 @@ def test_gradient_without_a_norm_does_not_depend_on_the_input(dtype, weights, ba
         big = [g * 1e30 for g in grads]
         ref = qk_norm(torch.zeros_like(x), heads, None, None, 1e-6, rotary, None, False, big)["dx"]
         check("dx", api.qk_norm_bwd(torch.full_like(x, 1e30), heads, None, None, *big, rotary=rotary)[0], ref)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("rot", [16, 32, 64])
+def test_what_is_not_rotated_keeps_its_infinities(dtype, interleaved, rot):
+    # dims behind rot_dims, and tokens at a negative position: copied when there is no norm, in both directions
+    heads = (3, 2, 1)
+    x, _, rotary, grads = _case(dtype, 2, 19, heads, rot)
+    pos = torch.arange(19, device="cuda", dtype=torch.int32) - 1        # a class token first
+    pos[7] = -5
+    off = pos < 0
+    h = x.view(2, 19, 6, 64)
+    for t in (h.transpose(1, 2), *grads):      # [B, H, N, 64]
+        t[:, :, off, 3::9] = math.inf
+        t[:, :, off, 5::11] = -math.inf
+        if rot < 64:
+            t[:, :, 2::5, rot::7] = math.inf
+            t[:, :, 2::5, rot + 1::7] = math.nan
+    how = dict(rotary=rotary, positions=pos, interleaved=interleaved)
+    out = api.qk_norm_fwd(x, heads, **how)
+    dx = api.qk_norm_bwd(x, heads, None, None, *grads, **how)[0].view(2, 19, 6, 64).transpose(1, 2)
+    first = 0
+    for i, n in enumerate(heads):
+        for got, src in ((out[i], h.transpose(1, 2)[:, first:first + n]), (dx[:, first:first + n], grads[i])):
+            kept = torch.ones_like(got, dtype=torch.bool)
+            if i < 2:                          # value heads are copied altogether
+                kept[:, :, ~off, :rot] = False
+            assert torch.equal(got[kept].nan_to_num(7.0, 9e9, -9e9), src[kept].nan_to_num(7.0, 9e9, -9e9))
+            assert bool(got[~kept].isfinite().all())
+        first += n
