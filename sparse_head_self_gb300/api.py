@@ -369,6 +369,11 @@ def _norm_desc(x, heads, q_weight, k_weight, eps, rotary, positions, interleaved
     sb, sn, sc = x.stride()
     if sc != 1:
         raise ValueError("x must have contiguous tokens")
+    # a dim of one element has no stride that matters
+    if B == 1:
+        sb = 0
+    if N == 1:
+        sn = 0
     wq = wk = cos_ptr = sin_ptr = rot = table = pos = pos_sb = 0
     if q_weight is not None:
         wq = _check_dense("q_weight", q_weight, _WEIGHT_SHAPE, dtype, index)

@@ -321,3 +321,19 @@ def test_what_is_not_rotated_keeps_its_infinities(dtype, interleaved, rot):
             assert torch.equal(got[kept].nan_to_num(7.0, 9e9, -9e9), src[kept].nan_to_num(7.0, 9e9, -9e9))
             assert bool(got[~kept].isfinite().all())
         first += n
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("B,N", [(1, 9), (3, 1), (1, 1)])
+def test_strides_of_one_sequence_or_one_token_do_not_matter(dtype, B, N):
+    heads = (2, 1, 1)
+    x, w, rotary, grads = _case(dtype, B, N, heads, 64)
+    C = 4 * 64
+    odd = torch.as_strided(x, (B, N, C), (N * C if B > 1 else N * C + 1, C if N > 1 else C + 3, 1))
+    assert torch.equal(odd, x) and odd.stride() != x.stride()
+    for a, b in zip(api.qk_norm_fwd(x, heads, *w, rotary=rotary) + api.qk_norm_bwd(x, heads, *w, *grads, rotary=rotary),
+                    api.qk_norm_fwd(odd, heads, *w, rotary=rotary) + api.qk_norm_bwd(odd, heads, *w, *grads, rotary=rotary)):
+        assert torch.equal(a, b)
+    odd.requires_grad_()
+    torch.autograd.backward(list(api.qk_norm(odd, heads, *w, rotary=rotary)), grads)
+    check("dx", odd.grad, qk_norm(x, heads, *w, 1e-6, rotary, None, False, grads)["dx"])
