@@ -127,11 +127,14 @@ class CrossAttention(nn.Module):
 
     def forward(self, x: torch.Tensor, y: torch.Tensor | None = None, kv_len: torch.Tensor | None = None,
                 key_mask: torch.Tensor | None = None, positions: torch.Tensor | None = None, kv=None) -> torch.Tensor:
-        """y: the states, or kv: what states() made of them; kv_len [B] int32 and
-        key_mask [B, Nk] say which of them each sequence attends; positions
-        (int32 [Nq] or [B, Nq]): the decoder tokens' places, 0.. if not given."""
+        """y: the states, at positions 0.., or kv: what states() made of them (which
+        takes positions of their own); kv_len [B] int32 and key_mask [B, Nk] say
+        which of them each sequence attends; positions (int32 [Nq] or [B, Nq]): the
+        decoder tokens' places, 0.. if not given."""
         if (y is None) == (kv is None):
             raise ValueError("either the states y or their kv")
+        if positions is not None and self.rotary is None:
+            raise ValueError("positions of a layer without rotary angles")
         B, Nq, dim = x.shape
         k, v = self.states(y) if kv is None else kv
         q = self.q(x)
