@@ -255,7 +255,8 @@ size_t fibatt_qk_norm_bwd_workspace_bytes(void);
 /* Gradient of the call above: from dQ, dK, dV (dense, as Q, K, V) to dX
  * (strides as X's; may not overlap X) and to the weights' gradients
  * dq_weight, dk_weight [64] in the I/O type, summed over all tokens and heads
- * in fp32 in a fixed order (written only where the weight is not NULL; either
+ * in fp32 in a fixed order, in fp32 I/O with what the additions of partial
+ * sums round off kept (written only where the weight is not NULL; either
  * may be NULL when its gradient is not wanted).  Heads of a kind without a
  * weight are not read from X, on which their gradient does not depend.  workspace: 16-byte aligned,
  * for one call at a time. */

@@ -337,3 +337,34 @@ def test_strides_of_one_sequence_or_one_token_do_not_matter(dtype, B, N):
     odd.requires_grad_()
     torch.autograd.backward(list(api.qk_norm(odd, heads, *w, rotary=rotary)), grads)
     check("dx", odd.grad, qk_norm(x, heads, *w, 1e-6, rotary, None, False, grads)["dx"])
+
+
+@pytest.mark.parametrize("B,N,heads,interleaved", [(2, 16385, (16, 16, 0), False), (256, 197, (12, 12, 0), False),
+                                                   (1, 6000, (7, 3, 2), True)])
+def test_weights_gradients_keep_their_digits_over_many_rows(B, N, heads, interleaved):
+    # In the mean square a rounding to 32 bits is 2^-24 / sqrt(3) of its value at most.  A term of dw
+    # has about 8 (its rotation 3, x r and r 4, its product 1); a lane adds the terms of a unit, n
+    # at most, whose partial sums add sqrt(n / 2) of a rounding; then two joins of lanes, and one
+    # rounding each of a warp's, a block's and the result's value.  No count grows with the rows.
+    x, w, rotary, _ = _case(F32, B, N, heads, 64)
+    g = torch.Generator(device="cuda").manual_seed(8)
+    grads = [torch.randn(B, h, N, 64, generator=g, device="cuda") if h else None for h in heads]
+    got = api.qk_norm_bwd(x, heads, *w, *grads, rotary=rotary, interleaved=interleaved)[1:]
+    want = [0.0, 0.0]
+    for lo in range(0, B, 64):
+        at = slice(lo, lo + 64)
+        part = qk_norm(x[at], heads, *w, 1e-6, rotary, None, interleaved, [None if t is None else t[at] for t in grads])
+        want = [a + part[n][0] for a, n in zip(want, ("dwq", "dwk"))]
+    for i, h in enumerate(heads[:2]):
+        n = 2 * -(-h // 4) if h > 4 else 2
+        bound = 2.0 ** -24 / math.sqrt(3) * math.sqrt(8 + n / 2 + 2 + 3)
+        err = float((got[i].double() - want[i]).norm() / want[i].norm())
+        assert err <= bound, (i, err, bound)
+
+
+def test_weights_gradients_that_overflow_are_infinite():
+    x, w, _, grads = _case(F32, 4, 200, (4, 4, 1), 0)
+    grads[0][..., 5] = 3e38 * x.view(4, 200, 9, 64)[:, :, :4, 5].transpose(1, 2).sign()
+    _, dwq, dwk = api.qk_norm_bwd(x, (4, 4, 1), *w, *grads)
+    assert float(dwq[5]) == math.inf and bool(dwq[:5].isfinite().all()) and bool(dwq[6:].isfinite().all())
+    assert bool(dwk.isfinite().all())
