@@ -324,8 +324,10 @@ size_t fibatt_cross_bwd_workspace_bytes(const fibatt_cross *d);
  *     dQ_j = scale sum_k dS_jk K_k,   dK_k = scale sum_j dS_jk Q_j,   dV_k = sum_j P_jk dO_j,
  * the last two over the queries of every head that shares the key head.  No
  * atomics: results do not depend on scheduling.  For bf16, P and dS are
- * rounded to bf16 before the products that sum them, and for at most 64 keys D
- * is summed as sum_k P_jk <dO_j, V_k>, which O's rounding does not enter.  O and LSE are
+ * rounded to bf16 before the products that sum them, and with Nk <= 64, or for
+ * a sequence of at most 8 keys by kv_len, D is summed as sum_k P_jk <dO_j, V_k>,
+ * which O's rounding does not enter (against 64 bits, 3 keys: dQ and dK 0.0024 off, otherwise
+ * 0.0032, as for 3 keys that key_mask leaves of a longer sequence).  O and LSE are
  * fibatt_cross_fwd's.  workspace: 16-byte aligned, for one call at a time.
  * Errors as fibatt_cross_fwd, plus INVALID_ARG for a workspace too small. */
 fibatt_status fibatt_cross_bwd(const fibatt_cross *d, const fibatt_heads *Q, const fibatt_heads *K,

@@ -92,13 +92,27 @@ __device__ __forceinline__ uint4 three_parts(float x) {
 // What stands for a query that does not exist: a weight of exp2(-1000) = 0.
 __device__ __forceinline__ uint4 no_query(float c) { return three_parts(-1000.f / c); }
 
-// (LSE log2 e, D = <dO, O>) of every query row, and -LSE log2 e / c and -D in
-// parts, rows padded to `npad` a head and 128 rows of no query at the end.  Eight
-// threads a row.
+// D of sequences with few keys is summed from the weights themselves,
+// D = sum_k P_k dP_k: O's rounding to bf16 is one of the larger errors of dS when a
+// row has few keys.  Against 64 bits, dQ and dK with <dO, O>: 3 keys 0.0032, 8 keys 0.0026,
+// from 64 keys on 0.0025; with the sum 0.0024.  Tensors of at most kFewKeys keys have a kernel
+// for it.  In longer ones (a padded batch) the first kernel sums a key at a time for the
+// sequences of at most kShort, where it matters most: 8 sequences of 393 to 1569 keys take
+// 39.7 us with it and without; 64 x 12 heads, 197 queries, with 3 or 8 of 197 keys each, 103
+// (<dO, O> 79; up to 16 keys a sequence 127; the other kernel, which takes 16 rows a warp, 99 for
+// 3 or 64 keys, but 41.6 for the long sequences).  Keys that a mask leaves are not counted: that
+// took 64 x 12 heads of 65 x 197 from 62 to 65 us.
+constexpr int kFewKeys = 64, kShort = 8;
+
+// (LSE log2 e, D) of every query row, and -LSE log2 e / c and -D in parts, rows
+// padded to `npad` a head and 128 rows of no query at the end.  Eight threads a row.
+// D is <dO, O>, but with LENGTHS the sum above for the sequences that are that short.
+template <bool LENGTHS>
 __global__ void __launch_bounds__(256)
-cross_parts_kernel(int Hq, int Nq, int npad, unsigned rows, Rows<const __nv_bfloat16> O, Rows<const __nv_bfloat16> dO,
-                   const float *__restrict__ LSE, float c, float2 *__restrict__ stats, uint4 *__restrict__ lse_parts,
-                   uint4 *__restrict__ d_parts, int *__restrict__ next_unit) {
+cross_parts_kernel(int Hq, int Hkv, int Nq, int npad, unsigned rows, KeySet ks, Rows<const __nv_bfloat16> Q,
+                   Rows<const __nv_bfloat16> K, Rows<const __nv_bfloat16> V, Rows<const __nv_bfloat16> O,
+                   Rows<const __nv_bfloat16> dO, const float *__restrict__ LSE, float c, float2 *__restrict__ stats,
+                   uint4 *__restrict__ lse_parts, uint4 *__restrict__ d_parts, int *__restrict__ next_unit) {
     grid_dep_wait();
     grid_dep_launch();
     const unsigned row = blockIdx.x * 32 + (threadIdx.x >> 3);
@@ -116,13 +130,34 @@ cross_parts_kernel(int Hq, int Nq, int npad, unsigned rows, Rows<const __nv_bflo
     const uint4 g = __ldg(reinterpret_cast<const uint4 *>(dO.row(b, h, n)) + i);
     const int64_t at = (int64_t)bh * Nq + n;
     const float lse = __ldg(LSE + at);
-    float d = dot2_bf16(o.x, g.x, dot2_bf16(o.y, g.y, 0.f)) + dot2_bf16(o.z, g.z, dot2_bf16(o.w, g.w, 0.f));
-    const unsigned eight = 0xffu << (threadIdx.x & 24);
-#pragma unroll
-    for (int m = 1; m < 8; m <<= 1) d += __shfl_xor_sync(eight, d, m);
     // a row without keys: its weights are exp2(s - inf) = 0 (and no block meets it)
     const bool none = lse == -kInf;
     const float lse2 = none ? kInf : lse * kLog2e;
+    const unsigned eight = 0xffu << (threadIdx.x & 24);
+    const auto share = [](const uint4 &x, const uint4 &y) {      // of <x, y>, this thread's
+        return dot2_bf16(x.x, y.x, dot2_bf16(x.y, y.y, 0.f)) + dot2_bf16(x.z, y.z, dot2_bf16(x.w, y.w, 0.f));
+    };
+    const auto sum = [&](float x) {
+#pragma unroll
+        for (int m = 1; m < 8; m <<= 1) x += __shfl_xor_sync(eight, x, m);
+        return x;
+    };
+    float d = share(o, g);
+    if (LENGTHS) {
+        const int bound = ks.bound((int)b), hk = (int)h / (Hq / Hkv);
+        if (bound <= kShort) {
+            const uint4 q = __ldg(reinterpret_cast<const uint4 *>(Q.row(b, h, n)) + i);
+            d = 0.f;
+#pragma unroll 1
+            for (int j = 0; j < bound; ++j) {
+                const uint4 k = __ldg(reinterpret_cast<const uint4 *>(K.row(b, hk, j)) + i);
+                const uint4 v = __ldg(reinterpret_cast<const uint4 *>(V.row(b, hk, j)) + i);
+                const float p = fast_exp2(fmaf(sum(share(q, k)), c, -lse2));
+                if (ks.has((int)b, j)) d = fmaf(p, share(g, v), d);
+            }
+        }
+    }
+    d = sum(d);
     if (i == 0) lse_parts[row] = none ? no_query(c) : three_parts(-lse2 / c);
     if (i == 1) d_parts[row] = three_parts(-d);
     if (i == 2) stats[at] = make_float2(lse2, d);
@@ -149,15 +184,12 @@ struct Dims {
     }
 };
 
-// The same for at most kFewKeys keys, with D summed from the weights themselves,
-// D = sum_k P_k dP_k: O's rounding to bf16 is one of the larger errors of dS when a
-// row has few keys (against 64 bits, 3 keys: dQ and dK 0.0032 with <dO, O>, 0.0024 with
-// this; from 64 keys on both 0.0025 to 0.0024, and 128 keys, 192 heads of 1000 queries, cost
-// 17 of 92 us).  A warp takes 16 queries of a head,
+// The same for tensors of at most kFewKeys keys (of 128, 192 heads of 1000 queries, it
+// would cost 17 of 92 us).  A warp takes 16 queries of a head,
 // its eight keys at a time by warp-wide products; lane (g, t) gives them dims 16 t
 // to 16 t + 15 of rows g and g + 8 and of key g, four at a time in both operands
 // (the order of a sum does not matter), so that it loads 16 bytes at once.
-constexpr int kFewWarps = 4, kFewKeys = 64;
+constexpr int kFewWarps = 4;
 __global__ void __launch_bounds__(32 * kFewWarps)
 cross_parts_few_kernel(int Hq, int Hkv, int Nq, int npad, unsigned heads, KeySet ks, Rows<const __nv_bfloat16> Q,
                        Rows<const __nv_bfloat16> K, Rows<const __nv_bfloat16> V, Rows<const __nv_bfloat16> dO,
@@ -754,9 +786,12 @@ cudaError_t launch_cross_bwd_mma(const CrossArgs &a) {
                             rows_of<const __nv_bfloat16>(a.V), rows_of<const __nv_bfloat16>(a.dO),
                             static_cast<const float *>(a.LSE), f.c, stats, lse_parts, d_parts, f.next_unit);
     } else {
-        e = launch_clusters(cross_parts_kernel, (unsigned)((rows + kTileRows + 31) / 32), 1, 256, 0, a.stream, a.Hq, a.Nq,
-                            f.npad, (unsigned)rows, rows_of<const __nv_bfloat16>(a.O), rows_of<const __nv_bfloat16>(a.dO),
-                            static_cast<const float *>(a.LSE), f.c, stats, lse_parts, d_parts, f.next_unit);
+        const auto kernel = a.keys.len ? cross_parts_kernel<true> : cross_parts_kernel<false>;
+        e = launch_clusters(kernel, (unsigned)((rows + kTileRows + 31) / 32), 1, 256, 0, a.stream, a.Hq, a.Hkv, a.Nq, f.npad,
+                            (unsigned)rows, a.keys, rows_of<const __nv_bfloat16>(a.Q), rows_of<const __nv_bfloat16>(a.K),
+                            rows_of<const __nv_bfloat16>(a.V), rows_of<const __nv_bfloat16>(a.O),
+                            rows_of<const __nv_bfloat16>(a.dO), static_cast<const float *>(a.LSE), f.c, stats, lse_parts,
+                            d_parts, f.next_unit);
     }
     if (e != cudaSuccess) return e;
     const int64_t query_units = (int64_t)a.B * a.Hkv * f.qt.tiles, key_units = (int64_t)a.B * a.Hkv * f.ktiles;

@@ -488,3 +488,45 @@ def test_gradients_of_few_rows_on_many(dtype, size, mask):
     q, k, v, do = _inputs(dtype, *size, seed=59)
     n = None if mask == "none" else torch.full((size[0],), size[4] * 2 // 3, dtype=torch.int32, device="cuda")
     _check_all(q, k, v, do, 0.125, n)
+
+
+@pytest.mark.parametrize("keys", [3, 4, 7, 8, 9, 64])
+@pytest.mark.parametrize("Nk", [90, 128, 600, 1569])
+@pytest.mark.parametrize("mask", ["none", "mask"])
+def test_padding_does_not_cost_the_gradients_of_short_sequences_their_digits(keys, Nk, mask):
+    # as above: two roundings of 2^-8 / sqrt(3), however long the tensors are
+    q, k, v, do = _inputs(BF16, 8, 4, 2, 60, Nk, layout="bhnd", seed=53)
+    n = torch.full((8,), keys, dtype=torch.int32, device="cuda")
+    n[1::2] = Nk                    # next to sequences with all keys
+    m, at = None, torch.arange(keys, device="cuda")
+    if mask == "mask":
+        m = torch.ones(8, Nk, dtype=torch.bool, device="cuda")
+        m[:, 1::3] = False
+        at = at[at % 3 != 1]
+    got = _run(q, k, v, do, 0.125, n, m)
+    want = cross(q, k, v, 0.125, n, m, do, got["O"])
+    for name in got:
+        check(name, got[name], want[name])
+    x, y, z, w = (t[::2].double() for t in (q, k, v, do))
+    y, z = (t[:, :, at].repeat_interleave(2, 1) for t in (y, z))
+    p, dp = (0.125 * x @ y.transpose(-1, -2)).softmax(-1), w @ z.transpose(-1, -2)
+    ds = p * (dp - (p * dp).sum(-1, keepdim=True))
+    dk = (0.125 * ds.transpose(-1, -2) @ x).view(4, 2, 2, len(at), 64).sum(2)
+    for name, g, exact in (("dQ", got["dQ"][::2], 0.125 * ds @ y), ("dK", got["dK"][::2][:, :, at], dk)):
+        err = float((g.double() - exact).norm() / exact.norm())
+        assert err <= math.sqrt(2 / 3) * 2.0 ** -8, (name, err)
+
+
+@pytest.mark.parametrize("size", [(40, 1, 1, 1, 70), (70, 1, 1, 3, 200), (9, 2, 1, 5, 1500), (3, 3, 3, 40, 3000)],
+                         ids=lambda s: "x".join(map(str, s)))
+def test_sequences_of_few_and_of_many_keys_side_by_side(size):
+    # sequences shorter than a block of the backward's first kernel, with none to all keys
+    B, Nk = size[0], size[4]
+    q, k, v, do = _inputs(BF16, *size, seed=61)
+    g = torch.Generator(device="cuda").manual_seed(6)
+    n = torch.randint(0, Nk + 1, (B,), generator=g, device="cuda", dtype=torch.int32)
+    n[::3] = torch.randint(0, 66, (len(n[::3]),), generator=g, device="cuda", dtype=torch.int32)
+    share = torch.tensor([0.0, 0.01, 0.05, 0.5, 1.0], device="cuda")[torch.arange(B, device="cuda") % 5]
+    m = torch.rand(B, Nk, generator=g, device="cuda") < share[:, None]
+    for lens, mask in ((n, None), (None, m), (n, m)):
+        _check_all(q, k, v, do, 0.125, lens, mask)
