@@ -212,13 +212,14 @@ __device__ __forceinline__ int part(int tiles, int r, int c) { return (int)((int
 
 __global__ void __launch_bounds__(kThreads, kFwdBlocks)
 cross_fwd_f32_kernel(int Hq, int Hkv, int Nq, KeySet ks, Rows<const float> Q, Rows<const float> K, Rows<const float> V,
-                     Rows<float> O, float *__restrict__ LSE, float scale_log2, int qtiles) {
+                     Rows<float> O, float *__restrict__ LSE, float scale_log2, int qtiles, int64_t units) {
     extern __shared__ float4 smem4[];
     float *sq = reinterpret_cast<float *>(smem4), *sk = sq + kTile, *sv = sk + kTile;
     __shared__ float sm[kT], sl[kT];
     const Lane ln;
     const int C = (int)cluster_size(), rank = (int)cluster_rank();
     const int64_t unit = blockIdx.x / C;
+    if (!FIBATT_CHECKED(unit < units)) return;      // whole clusters
     const int qt = (int)(unit % qtiles), h = (int)(unit / qtiles % Hq), b = (int)(unit / qtiles / Hq);
     const int hk = h / (Hq / Hkv), q0 = qt * kT;
 
@@ -390,6 +391,7 @@ struct BwdF32Args {
     float scale;
     int qtiles, ktiles;
     int key_units;        // units that hold keys; the others hold queries
+    int64_t units;        // all of them
     int first;            // unit of the launch
 };
 
@@ -501,6 +503,7 @@ __global__ void __launch_bounds__(kThreads, kBwdBlocks) cross_bwd_f32_kernel(con
     float *smem = reinterpret_cast<float *>(smem4);
     grid_dep_wait();
     const int64_t unit = a.first + blockIdx.x / cluster_size();
+    if (!FIBATT_CHECKED(unit < a.units)) return;    // whole clusters
     if (unit < a.key_units) hold_keys(a, smem, sst, unit);
     else hold_queries(a, smem, unit - a.key_units);
 }
@@ -524,7 +527,7 @@ cudaError_t launch_cross_fwd_f32(const CrossArgs &a) {
     const int c = cluster_for(units, (a.Nk + kT - 1) / kT, kFwdBlocks * sm_count(), largest_cluster<cross_fwd_f32_kernel>(smem));
     return launch_clusters(cross_fwd_f32_kernel, (unsigned)(units * c), c, kThreads, smem, a.stream, a.Hq, a.Hkv, a.Nq,
                            a.keys, rows_of<const float>(a.Q), rows_of<const float>(a.K), rows_of<const float>(a.V),
-                           rows_of<float>(a.O), a.LSE, a.scale * kLog2e, qtiles);
+                           rows_of<float>(a.O), a.LSE, a.scale * kLog2e, qtiles, units);
 }
 
 cudaError_t launch_cross_bwd_f32(const CrossArgs &a) {
@@ -546,6 +549,7 @@ cudaError_t launch_cross_bwd_f32(const CrossArgs &a) {
     if (e != cudaSuccess) return e;
     const int64_t key_units = (int64_t)a.B * a.Hkv * f.ktiles, query_units = (int64_t)a.B * a.Hq * f.qtiles;
     f.key_units = (int)key_units;
+    f.units = key_units + query_units;
     f.first = 0;
     // (one head, 100 queries on 16385 keys: 157 us in two launches, 275 with clusters of 8
     // at most, 1937 in one)

@@ -334,7 +334,8 @@ __device__ __forceinline__ int weights(const BwdMmaArgs &a, Shared &sh, uint8_t 
     const uint32_t lanes = (uint32_t)(warp & 3) << 21, tmem = sh.tmem;
     float row_lse = -kInf, row_d = 0.f;     // of a held query: -LSE log2 e, -D
     int g = 0, q = 0;
-    const bool row = KEYS ? u.mine * kTileRows + r < a.ks.Nk : a.qt.at(u.mine, r, g, q);
+    const bool row = (KEYS ? u.mine * kTileRows + r < a.ks.Nk : a.qt.at(u.mine, r, g, q)) &&
+                     FIBATT_CHECKED(u.b >= 0 && u.b < a.B && u.hk < a.Hkv);
     if (!KEYS && row) {
         const float2 st = __ldg(a.stats + ((int64_t)u.b * a.Hq + u.hk * a.qt.G + g) * a.qt.Nq + q);
         row_lse = -st.x;
@@ -465,8 +466,10 @@ __device__ __forceinline__ bool copies(const BwdMmaArgs &a, Shared &sh, const Ti
                 query_tile(tl.stage(s), t, &sh.full[s]);
                 for (int i = 0; i < a.qt.gb; ++i) {
                     const int g = a.qt.first_head(t) + i;
-                    const int64_t from = g < a.qt.G ? ((int64_t)u.b * a.Hq + u.hk * a.qt.G + g) * a.npad + a.qt.first_row(t)
-                                                    : (int64_t)a.B * a.Hq * a.npad;   // no such head
+                    const int64_t none = (int64_t)a.B * a.Hq * a.npad;      // rows of no query
+                    int64_t from = g < a.qt.G ? ((int64_t)u.b * a.Hq + u.hk * a.qt.G + g) * a.npad + a.qt.first_row(t)
+                                              : none;   // no such head
+                    if (!FIBATT_CHECKED(from >= 0 && from + rows <= none + kTileRows)) from = none;   // the workspace's rows
                     uint8_t *to = tl.part(s) + i * rows * 16;
                     bulk_g2s(to, a.lse_parts + from, rows * 16, &sh.full[s]);
                     bulk_g2s(to + kNarrow, a.d_parts + from, rows * 16, &sh.full[s]);
@@ -599,6 +602,7 @@ __device__ __forceinline__ void join(const BwdMmaArgs &a, const Tiles &tl, const
         const int acc = i / kTileRows, r = i % kTileRows;
         int g = 0, q = 0;
         if (KEYS ? u.mine * kTileRows + r >= a.ks.Nk : !a.qt.at(u.mine, r, g, q)) continue;
+        if (!FIBATT_CHECKED(u.b >= 0 && u.b < a.B && u.hk < a.Hkv)) continue;
         float2 x = make_float2(0.f, 0.f), y = x;
         for (int k = 0; k < CS; ++k) {
             const uint32_t at = cluster_addr(part + i * kJoinLd + c4, k);

@@ -303,6 +303,7 @@ cross_fwd_mma_kernel(const __grid_constant__ FwdMmaArgs a) {
                 int g, q;
                 if (!a.qt.at(u.t0 + t, r, g, q)) return;
                 const int h = u.hk * a.qt.G + g;
+                if (!FIBATT_CHECKED(h < a.Hq && u.b >= 0 && (int64_t)u.b * a.Hkv * a.pairs < a.units)) return;
                 const float inv = l == 0.f ? 0.f : 1.f / l;
                 uint4 *out = reinterpret_cast<uint4 *>(a.O.row(u.b, h, q) + 32 * half);
 #pragma unroll
@@ -517,6 +518,7 @@ cross_fwd_mma_kernel(const __grid_constant__ FwdMmaArgs a) {
             y = fma2(make_float2(w, w), ld_cluster2(at + 8), y);
         }
         const int h = u.hk * a.qt.G + g;
+        if (!FIBATT_CHECKED(h < a.Hq && u.b >= 0 && (int64_t)u.b * a.Hkv * a.pairs < a.units)) continue;
         const float inv = sum == 0.f ? 0.f : 1.f / sum;
         *reinterpret_cast<uint2 *>(a.O.row(u.b, h, q) + c4) =
             make_uint2(pack_bf16x2(x.x * inv, x.y * inv), pack_bf16x2(y.x * inv, y.y * inv));

@@ -127,7 +127,8 @@ struct Part {
     __device__ __forceinline__ void join(const float (*sm)[R], const float (*sl)[R], const float2 (*so)[R][32], float *cm,
                                          float *cl, float2 (*co)[32], Rows<T> O) {
         __syncthreads();
-        for (int i = threadIdx.x; i < a.rows * 32; i += kThreads) {
+        const int rows = FIBATT_CHECKED(a.rows <= R && a.rows == G * a.Nq) ? a.rows : 0;     // the kernel's room
+        for (int i = threadIdx.x; i < rows * 32; i += kThreads) {
             const int r = i >> 5, d = i & 31;
             float top = kNegInf;
 #pragma unroll
@@ -149,7 +150,7 @@ struct Part {
         }
         cluster_sync();
         // row r is finished by CTA r mod C
-        for (int i = threadIdx.x; i < a.rows * 32; i += kThreads) {
+        for (int i = threadIdx.x; i < rows * 32; i += kThreads) {
             const int r = i >> 5, d = i & 31;
             if (r % C != rank) continue;
             float top = kNegInf;

@@ -397,7 +397,7 @@ qk_norm_fwd_kernel(const __grid_constant__ NormArgs<T> a, const T *__restrict__ 
                     }
                     raw.put(x);
                 }
-                if (here.in[s]) raw.store(out + here.dense(s, hi, Hs, a.N), a0, a1);
+                if (here.in[s] && FIBATT_CHECKED(hi >= 0 && hi < Hs && here.n[s] < (unsigned)a.N)) raw.store(out + here.dense(s, hi, Hs, a.N), a0, a1);
             }
             __syncwarp();
             slot = (slot + 1) % kDepth;
@@ -521,7 +521,7 @@ qk_norm_bwd_kernel(const __grid_constant__ NormArgs<T> a, const T *__restrict__ 
                     }
                     grad.put(dy);
                 }
-                if (here.in[s]) grad.store(dX + here.packed(s, work.h, dx_sb, dx_sn), a0, a1);
+                if (here.in[s] && FIBATT_CHECKED(work.h < H && here.n[s] < (unsigned)a.N)) grad.store(dX + here.packed(s, work.h, dx_sb, dx_sn), a0, a1);
             }
             __syncwarp();
             slot = (slot + 1) % kDepth;
@@ -541,7 +541,7 @@ qk_norm_bwd_kernel(const __grid_constant__ NormArgs<T> a, const T *__restrict__ 
 #pragma unroll
     for (int i = 0; i < 4; ++i) part[warp][64 * (i >> 1) + d + (i & 1)] = total[i].value();
     __syncthreads();
-    if (threadIdx.x < 128) {
+    if (threadIdx.x < 128 && FIBATT_CHECKED(blockIdx.x < kMaxBlocks)) {      // the workspace's rows
         Total t;
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) t.add(part[w][threadIdx.x]);

@@ -241,3 +241,11 @@ def test_python_api_rejects_cpu_tensors():
     q = torch.zeros(1, 3, 65, 64)
     with pytest.raises(ValueError, match="CUDA"):
         api.fwd(sup, q, q, q, 0.125)
+
+
+def test_kernels_that_write_by_unit_or_scratch_row_check_it():
+    # the bounds-checked build: every kernel file whose accesses follow the host's plan has checks
+    import os
+    from sparse_head_self_gb300.build import CSRC
+    for f in ("resident.cu", "stream.cu", "qk_norm.cu", "cross_rows.cu", "cross_f32.cu", "cross_mma_fwd.cu", "cross_mma_bwd.cu"):
+        assert "FIBATT_CHECKED(" in open(os.path.join(CSRC, f)).read(), f

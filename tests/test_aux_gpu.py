@@ -83,6 +83,20 @@ def test_checks_build_runs_the_parity_cases_clean():
     assert re.search(r"\d+ passed", r.stdout), tail
 
 
+def test_checks_build_runs_the_norm_and_the_cross_attention_clean():
+    env = dict(os.environ, FIBATT_CHECKS="1")
+    env.pop("FIBATT_PROFILE", None)
+    sel = ("values_and_gradients or units or other_groups or few_rows or rows_are_written or strided_tokens or positions "
+           "or short_sequences or side_by_side")
+    r = subprocess.run([sys.executable, "-m", "pytest", "tests/test_cross_gpu.py", "tests/test_qk_norm_gpu.py", "-m", "gpu",
+                        "-x", "-q", "-p", "no:cacheprovider", "-k", sel], cwd=ROOT, env=env, capture_output=True, text=True,
+                       timeout=1800)
+    tail = "\n".join((r.stdout + r.stderr).splitlines()[-30:])
+    assert r.returncode == 0, tail
+    assert "libfibatt checks" not in r.stderr, tail
+    assert re.search(r"\d+ passed", r.stdout), tail
+
+
 def test_checks_build_is_the_library_loaded():
     # the child process of the test above loads the checks build
     code = ("import os; os.environ['FIBATT_CHECKS'] = '1'; "
