@@ -63,7 +63,8 @@ fibatt_status check_cross(const fibatt_cross *d) {
     if (!std::isfinite(d->scale)) return invalid("scale is not finite");
     if (off(d->kv_len, 4)) return invalid("kv_len is not 4-byte aligned");
     if (d->key_mask && d->key_mask_stride_b < 0) return invalid("key_mask_stride_b is negative");
-    // blocks of the kernels: one a 64-row tile and head at most, times a cluster of eight
+    // blocks of the kernels: one a 64-row tile and head at most, and an eighth of what a grid may
+    // have (clusters, of up to 16, are launched only while all of them find a place at once)
     const int64_t qb = (int64_t)d->B * d->Hq, kb = (int64_t)d->B * d->Hkv;
     if (qb > 0x7fffffffLL || qb * ((d->Nq + 63LL) / 64) > 0x7fffffffLL / 8 || kb * ((d->Nk + 63LL) / 64) > 0x7fffffffLL / 8 ||
         qb * ((d->Nq + 127LL) / 128 * 128) > 0x7fffffffLL - 256)

@@ -163,13 +163,6 @@ cross_parts_kernel(int Hq, int Hkv, int Nq, int npad, unsigned rows, KeySet ks, 
     if (i == 2) stats[at] = make_float2(lse2, d);
 }
 
-// c += A (16 x 16) B (16 x 8)
-__device__ __forceinline__ void warp_mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
 // A lane's 16 dims of a row: 32 bytes.
 struct Dims {
     uint32_t x[8];
