@@ -26,6 +26,7 @@ from __future__ import annotations
 
 import argparse
 import ctypes
+import fnmatch
 import hashlib
 import json
 import math
@@ -135,14 +136,21 @@ def measured_peaks():
         return FALLBACK_HBM_GBS, "fallback"
 
 
-# the files that the kernels of the traffic record are compiled from
-TRAFFIC_SOURCES = ("cluster.cuh", "dense_row.cuh", "device_common.cuh", "fibatt_internal.h", "resident.cu",
-                   "row_math.cuh", "row_run.cuh", "stream.cu", "tma_common.cuh")
+# Files of csrc/ that the recorded calls do not come from: the norm and the cross
+# attention.  Every other one, and so every new one, counts: the kernels, what they
+# include, and the host code that chooses and launches them.
+TRAFFIC_OTHERS = ("qk_norm.cu", "cross*", "tcgen05.cuh", "per_device.h")
+
+
+def traffic_sources() -> list:
+    """Names of the files of csrc/ that the traffic record belongs to."""
+    names = sorted(os.listdir(os.path.join(ROOT, "sparse_head_self_gb300", "csrc")))
+    return [n for n in names if not any(fnmatch.fnmatch(n, o) for o in TRAFFIC_OTHERS)]
 
 
 def kernel_source_hash() -> str:
     h = hashlib.sha256()
-    for name in TRAFFIC_SOURCES:
+    for name in traffic_sources():
         with open(os.path.join(ROOT, "sparse_head_self_gb300", "csrc", name), "rb") as f:
             h.update(name.encode())
             h.update(f.read())

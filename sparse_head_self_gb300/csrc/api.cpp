@@ -15,7 +15,6 @@
 #include <string>
 #include <vector>
 
-#include "cross.h"
 #include "fibatt_internal.h"
 
 struct fibatt_support {

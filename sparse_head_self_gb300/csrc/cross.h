@@ -53,9 +53,6 @@ struct CrossArgs {
     cudaStream_t stream;
 };
 
-// Whether FIBATT_FAULT injects a fault of this kind (api.cpp).
-bool fault(const char *kind);
-
 // Streaming multiprocessors of the current device.
 int sm_count();
 // The current device, -1 if it cannot be told.
@@ -194,12 +191,5 @@ struct QkNormArgs {
 size_t qk_norm_bwd_workspace();
 cudaError_t launch_qk_norm_fwd(const QkNormArgs &a);
 cudaError_t launch_qk_norm_bwd(const QkNormArgs &a);
-
-// Each kernel file's device error word (device_common.cuh).
-cudaError_t read_error_cross_f32(unsigned *code, bool clear);
-cudaError_t read_error_cross_mma_fwd(unsigned *code, bool clear);
-cudaError_t read_error_cross_mma_bwd(unsigned *code, bool clear);
-cudaError_t read_error_cross_rows(unsigned *code, bool clear);
-cudaError_t read_error_qk_norm(unsigned *code, bool clear);
 
 }  // namespace fibatt

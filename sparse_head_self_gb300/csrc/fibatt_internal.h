@@ -183,6 +183,15 @@ cudaError_t read_error_resident(unsigned *code, bool clear);
 cudaError_t read_error_stream(unsigned *code, bool clear);
 cudaError_t read_error_generic(unsigned *code, bool clear);
 cudaError_t read_error_global_token(unsigned *code, bool clear);
+// ... and those of the norm and the cross attention, which fibatt_device_error() adds
+cudaError_t read_error_cross_f32(unsigned *code, bool clear);
+cudaError_t read_error_cross_mma_fwd(unsigned *code, bool clear);
+cudaError_t read_error_cross_mma_bwd(unsigned *code, bool clear);
+cudaError_t read_error_cross_rows(unsigned *code, bool clear);
+cudaError_t read_error_qk_norm(unsigned *code, bool clear);
+
+// Whether FIBATT_FAULT injects a fault of this kind (api.cpp).
+bool fault(const char *kind);
 
 // Global first token (global_token.cu): the dense row of token 0 (forward,
 // after the banded kernel), its dense row before the banded backward, and

@@ -40,6 +40,37 @@ def test_traffic_record_follows_the_kernel_sources(monkeypatch, tmp_path):
     assert bench.recorded_traffic("fibatt_bwd", "vitb") is None
 
 
+def test_traffic_record_belongs_to_every_source_of_its_calls():
+    import re
+    csrc = bench.os.path.join(bench.ROOT, "sparse_head_self_gb300", "csrc")
+    sources = set(bench.traffic_sources())
+    assert {"api.cpp", "resident.cu", "stream.cu", "generic.cu", "global_token.cu", "fibatt_internal.h"} <= sources
+    others = set(bench.os.listdir(csrc)) - sources
+    assert others and all(re.match(r"cross|qk_norm|tcgen05|per_device", n) for n in others)
+    for name in sources:     # what they include is among them
+        with open(bench.os.path.join(csrc, name)) as f:
+            included = set(re.findall(r'#include "([^"]+)"', f.read())) & set(bench.os.listdir(csrc))
+        assert included <= sources, (name, included - sources)
+
+
+def test_a_change_of_any_source_of_its_calls_marks_the_traffic_record(monkeypatch, tmp_path):
+    import shutil
+    csrc = tmp_path / "sparse_head_self_gb300" / "csrc"
+    shutil.copytree(bench.os.path.join(bench.ROOT, "sparse_head_self_gb300", "csrc"), csrc)
+    before = bench.kernel_source_hash()
+    monkeypatch.setattr(bench, "ROOT", str(tmp_path))
+    assert bench.kernel_source_hash() == before
+    for name in ("api.cpp", "global_token.cu", "resident.cu", "row_math.cuh"):
+        text = (csrc / name).read_text()
+        (csrc / name).write_text(text + "\n")
+        assert bench.kernel_source_hash() != before, name
+        (csrc / name).write_text(text)
+    (csrc / "cross_rows.cu").write_text("")
+    assert bench.kernel_source_hash() == before
+    (csrc / "new.cuh").write_text("")
+    assert bench.kernel_source_hash() != before
+
+
 def test_committed_traffic_record_is_complete():
     with open(bench.os.path.join(bench.ROOT, "profiles", "traffic.json")) as f:
         record = json.load(f)
