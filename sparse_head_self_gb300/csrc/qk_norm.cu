@@ -19,22 +19,23 @@
 // every rotated pair are its own (halves: dims 4 i.. and rot / 2 + 4 i..),
 // which leaves the two sums over a head as the only exchange; the arithmetic
 // is on packed pairs of floats.  Rows arrive by asynchronous copies in a ring of
-// each warp's own, kDepth heads ahead and over the items' ends, without holding
+// each warp's own, two or three heads ahead and over the items' ends, without holding
 // registers; the tokens' angles are brought into shared memory once for all heads.
 // Every head row is a whole 128- or 256-byte segment, so all traffic is full
 // sectors.  The values' heads are copied unconverted.
 //
-// Measured: 64 sequences of 197 tokens, 36 heads, bf16, forward: 24.5 us, 4.7 TB/s
+// Measured: 64 sequences of 197 tokens, 36 heads, bf16, forward: 24.6 us, 4.7 TB/s
 // (70% of a copy's rate; the issue slots 64% taken, most stalls fixed latencies of
-// a head's chain of sums); 256 sequences, backward: 121 us, 5.1 TB/s; 2 x 16385
-// tokens, 48 heads, fp32, backward: 191 us, 5.6 TB/s; 8 tokens, forward: 3.0 us.
+// a head's chain of sums), fp32 41 us, 5.7 TB/s; 256 sequences, bf16, backward: 125 us,
+// 5.0 TB/s; 2 x 16385 tokens, 48 heads, fp32, half of each head rotated, backward: 189 us,
+// 5.7 TB/s; 8 tokens, forward: 2.9 us.
 //
 // dw: each lane sums its eight dims, the block joins its warps in shared memory, and
 // a second kernel adds the blocks' sums in block order: no atomics, the same result
 // on every run.  For a result of 32 bits a lane's sum goes over one unit only, and the
 // units' sums into totals that keep what their additions round off, so that the error
 // does not grow with the rows: against 64 bits, 2 x 16385 tokens, 16 heads of each
-// kind, dw 1.1e-7 (one sum a lane, and of the blocks: 3.0e-7); the time 184 us (178).
+// kind, dw 1.1e-7 (one sum a lane, and of the blocks: 3.0e-7); it costs 1 to 3 us of 190.
 // A result of 16 bits is rounded far above that: one sum a lane.
 #include <algorithm>
 
@@ -48,7 +49,13 @@ namespace {
 constexpr int kWarps = 8;
 constexpr int kTokens = 16;           // of a unit
 constexpr int kSteps = 2;             // four tokens each: a warp's half of a unit
-constexpr int kDepth = 4;             // heads in a warp's ring
+// Heads in a warp's ring, whose rows are of RT tensors.  The fp32 backward has three, with
+// which an SM holds two blocks: 2 x 16385 tokens, 48 heads, of which 32 dims are rotated, 187 us
+// where four and one block take 209; with all 64 rotated, halves paired, 190 and 183.
+template <typename T, int RT>
+constexpr int ring_depth() {
+    return sizeof(T) == 4 && RT == 2 ? 3 : 4;
+}
 constexpr int kMaxBlocks = 1024;      // rows of the dw partial sums
 constexpr unsigned kErrPosition = 8u; // a position at or behind the end of the tables
 
@@ -288,11 +295,11 @@ __device__ __forceinline__ void weights(const float *sw, int a0, int a1, float2 
     w[2] = make_float2(v.x, v.y), w[3] = make_float2(v.z, v.w);
 }
 
-// Shared memory of a block: two units' angles, and every warp's ring of kDepth
-// heads of RT tensors, eight rows each.
+// Shared memory of a block: two units' angles, and every warp's ring of heads of RT
+// tensors, eight rows each.
 template <typename T, int RT>
 constexpr size_t ring_bytes() {
-    return 2 * kTokens * 64 * sizeof(float) + (size_t)kWarps * kDepth * RT * 8 * 64 * sizeof(T);
+    return 2 * kTokens * 64 * sizeof(float) + (size_t)kWarps * ring_depth<T, RT>() * RT * 8 * 64 * sizeof(T);
 }
 
 // Where a warp is in its sequence of heads: an item is a unit's tokens and one of
@@ -326,6 +333,7 @@ qk_norm_fwd_kernel(const __grid_constant__ NormArgs<T> a, const T *__restrict__ 
     extern __shared__ float4 smem4[];
     __shared__ __align__(16) float sw[2][64];
     __shared__ uint8_t turned[2][kTokens];
+    constexpr int kDepth = ring_depth<T, 1>();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = lane & 7, grp = lane >> 3;
     float *angles = reinterpret_cast<float *>(smem4);
     T *ring = reinterpret_cast<T *>(angles + 2 * kTokens * 64) + (size_t)warp * kDepth * 8 * 64;
@@ -417,6 +425,7 @@ qk_norm_bwd_kernel(const __grid_constant__ NormArgs<T> a, const T *__restrict__ 
     __shared__ __align__(16) float sw[2][64];
     __shared__ uint8_t turned[2][kTokens];
     __shared__ float part[kWarps][128];
+    constexpr int kDepth = ring_depth<T, 2>();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = lane & 7, grp = lane >> 3;
     float *angles = reinterpret_cast<float *>(smem4);
     T *ring = reinterpret_cast<T *>(angles + 2 * kTokens * 64) + (size_t)warp * kDepth * 2 * 8 * 64;
