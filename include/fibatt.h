@@ -216,8 +216,9 @@ fibatt_status fibatt_bwd_noalloc(fibatt_support_t s, int B, int D, fibatt_dtype 
  * position p by the angle whose cosine and sine are c = cos[p, i], s = sin[p, i]:
  *     (y1, y2) -> (y1 c - y2 s, y1 s + y2 c)
  * Pairs are dims (i, i + rot_dims / 2), or neighbours (2 i, 2 i + 1) when
- * interleaved is set.  Value heads are copied.  Arithmetic in fp32, one
- * rounding to the I/O type. */
+ * interleaved is set.  Value heads are copied, and what is not
+ * rotated (dims behind rot_dims, tokens that positions leave out) is left as it is.
+ * Arithmetic in fp32, one rounding to the I/O type. */
 typedef struct {
     int B, N;                    /* sequences, tokens                               */
     int Hq, Hk, Hv;              /* heads of each kind, >= 0, one at least           */
@@ -306,8 +307,8 @@ typedef struct {
  * accumulation; for bf16 the softmax weights are rounded to bf16 before their
  * product with V (the sums and the LSE use the unrounded ones), and O once at
  * the end; for fp32 products keep 22 bits of each operand (with more than eight
- * query rows to a key head), so that an infinite value that is attended may
- * give NaN where 24-bit products give infinity.  INVALID_ARG: a size or stride out of its range, a NULL or
+ * query rows to a key head), so that a value that is attended and infinite, or within
+ * 2^-12 of the type's largest, may give NaN where 24-bit products do not.  INVALID_ARG: a size or stride out of its range, a NULL or
  * misaligned pointer, a scale that is not finite, 2^31 query rows (a head's
  * rounded up to 128) or more.
  * UNSUPPORTED: D, dtype. */

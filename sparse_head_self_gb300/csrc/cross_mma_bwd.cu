@@ -32,9 +32,10 @@
 // product over rows is read from tensor memory, as bf16 (relative rounding 2^-8
 // a weight, averaging out over the sum).
 //
-// Measured: 2 sequences, 16 heads, 1569 x 16385: 583 us, 903 TFLOP/s of the 5
-// products (1264 of the 7), the small kernel 6 of them; 8 sequences, 12 heads on 4,
-// 197 x 1569 of several lengths: 37.6 us, the small kernel 4.5.  A tile takes about 1490
+// Measured, back to back in a graph: 2 sequences, 16 heads, 1569 x 16385: 583 to 602 us,
+// 903 TFLOP/s of the 5 products at best (1264 of the 7), the small kernel 6 of them (called
+// from Python 602 to 617); 8 sequences, 12 heads on 4, 197 x 1569 of several lengths: 38.5 us,
+// the small kernel 4.5.  A tile takes about 1490
 // cycles, its 3 or 4 products 800 or 1090 of them; the tensor cores are 61% busy, the
 // issue slots 49%: what is left are the waits from S to dS to the products, which need
 // each other within a tile.

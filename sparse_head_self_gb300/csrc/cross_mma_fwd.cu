@@ -30,7 +30,7 @@
 //
 // Measured: 2 sequences, 16 heads, 1569 x 16385: 227 us, 927 TFLOP/s (clusters of
 // two; one CTA a unit, 1.47 rounds: 266); 16 heads, 4096 x 4096: 75 us, 919; 8
-// sequences, 12 heads, 197 x 1569: 20 us; 64 sequences, 12 heads, 65 x 197, masked:
+// sequences, 12 heads, 197 x 1569: 21 us; 64 sequences, 12 heads, 65 x 197, masked:
 // 20.0 us.  A pair of tiles takes about 1900 cycles: 1094 of matrix instructions
 // (128 x 128 x 64 from shared memory 257, 128 x 64 x 128 with P in tensor memory
 // 290), 1024 of exponentials (4 cycles a warp and scheduler), which overlap but for
