@@ -42,6 +42,11 @@ def _weight(w, x: torch.Tensor):
     return None if w is None else w.to(x.dtype)
 
 
+def _turned(rotary, positions):
+    """(tables, positions) for qk_norm; neither for a layer that does not rotate."""
+    return (None, None) if rotary is None else (rotary.tables(), positions)
+
+
 class FibottentionSelfAttention(nn.Module):
     """x [B, N, dim] -> [B, N, dim] with dim = heads * 64.
 
@@ -120,27 +125,26 @@ class CrossAttention(nn.Module):
         self.state_rotary = None if state_rotary is None else _Rotary(state_rotary)
 
     def states(self, y: torch.Tensor, positions: torch.Tensor | None = None):
-        """Keys and values [B, kv_heads, Nk, 64] of the encoder's states."""
+        """Keys and values [B, kv_heads, Nk, 64] of the encoder's states; positions
+        (int32 [Nk] or [B, Nk]): their places, 0.. if not given, -1 for a class token."""
         kv = self.kv(y)
         return qk_norm(kv, (0, self.kv_heads, self.kv_heads), None, _weight(self.k_norm, kv), self.eps,
-                       None if self.state_rotary is None else self.state_rotary.tables(), positions)[1:]
+                       *_turned(self.state_rotary, positions))[1:]
 
     def forward(self, x: torch.Tensor, y: torch.Tensor | None = None, kv_len: torch.Tensor | None = None,
                 key_mask: torch.Tensor | None = None, positions: torch.Tensor | None = None, kv=None) -> torch.Tensor:
         """y: the states, at positions 0.., or kv: what states() made of them (which
         takes positions of their own); kv_len [B] int32 and key_mask [B, Nk] say
         which of them each sequence attends; positions (int32 [Nq] or [B, Nq]): the
-        decoder tokens' places, 0.. if not given."""
+        decoder tokens' places, 0.. if not given (without rotary they make no
+        difference)."""
         if (y is None) == (kv is None):
             raise ValueError("either the states y or their kv")
-        if positions is not None and self.rotary is None:
-            raise ValueError("positions of a layer without rotary angles")
         B, Nq, dim = x.shape
         k, v = self.states(y) if kv is None else kv
         q = self.q(x)
         if self.q_norm is not None or self.rotary is not None:
-            q = qk_norm(q, (self.heads, 0, 0), _weight(self.q_norm, q), None, self.eps,
-                        None if self.rotary is None else self.rotary.tables(), positions)[0]
+            q = qk_norm(q, (self.heads, 0, 0), _weight(self.q_norm, q), None, self.eps, *_turned(self.rotary, positions))[0]
         else:
             q = q.view(B, Nq, self.heads, HEAD_DIM).transpose(1, 2)
         o = cross_attention(q, k, v, self.scale, kv_len, key_mask)     # [B, H, Nq, 64], in q's layout

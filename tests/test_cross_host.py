@@ -209,14 +209,3 @@ def test_rotary_angles():
     assert cos.dtype == torch.float32 and torch.equal(cos, a.cos().float()) and torch.equal(sin, a.sin().float())
     with pytest.raises(ValueError, match="pairs"):
         api.rotary_tables(torch.zeros(4, 5))
-
-
-@pytest.mark.parametrize("norm", [True, False])
-def test_positions_of_a_layer_that_does_not_rotate_are_refused(norm):
-    from sparse_head_self_gb300.block import CrossAttention
-    layer = CrossAttention(128, 2, norm=norm)
-    x, y, at = torch.zeros(1, 3, 128), torch.zeros(1, 5, 128), torch.arange(3, dtype=torch.int32)
-    with pytest.raises(ValueError, match="positions of a layer without rotary"):
-        layer(x, y, positions=at)
-    with pytest.raises(ValueError, match="positions of a layer without rotary"):
-        layer(x, kv=(torch.zeros(1, 2, 5, 64),) * 2, positions=at)

@@ -170,6 +170,18 @@ def test_layers_in_16_bits_keep_their_angles():
 
 
 @pytest.mark.parametrize("norm", [True, False])
+def test_places_make_no_difference_to_a_layer_that_does_not_rotate(norm):
+    torch.manual_seed(6)
+    layer = CrossAttention(128, 2, norm=norm).cuda()
+    x, y = torch.randn(2, 5, 128, device="cuda"), torch.randn(2, 9, 128, device="cuda")
+    at = torch.arange(5, device="cuda", dtype=torch.int32) + 100
+    want = layer(x, y)
+    assert torch.equal(layer(x, y, positions=at), want)
+    kv = layer.states(y, positions=torch.arange(9, device="cuda", dtype=torch.int32))
+    assert torch.equal(layer(x, kv=kv, positions=at), want)
+
+
+@pytest.mark.parametrize("norm", [True, False])
 def test_layers_under_autocast(norm):
     # autocast rounds inputs and weights where the layers in 16 bits hold them so: the same numbers
     torch.manual_seed(5)
