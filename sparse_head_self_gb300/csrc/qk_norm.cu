@@ -24,8 +24,8 @@
 // Every head row is a whole 128- or 256-byte segment, so all traffic is full
 // sectors.  The values' heads are copied unconverted.
 //
-// Measured: 64 sequences of 197 tokens, 36 heads, bf16, forward: 24.6 us, 4.7 TB/s
-// (70% of a copy's rate; the issue slots 64% taken, most stalls fixed latencies of
+// Measured: 64 sequences of 197 tokens, 36 heads, bf16, forward: 23.7 us, 4.9 TB/s
+// (72% of a copy's rate; the issue slots 61% taken, most stalls fixed latencies of
 // a head's chain of sums), fp32 41 us, 5.7 TB/s; 256 sequences, bf16, backward: 125 us,
 // 5.0 TB/s; 2 x 16385 tokens, 48 heads, fp32, half of each head rotated, backward: 189 us,
 // 5.7 TB/s; 8 tokens, forward: 2.9 us.
@@ -379,6 +379,9 @@ qk_norm_fwd_kernel(const __grid_constant__ NormArgs<T> a, const T *__restrict__ 
         bool turns[kSteps];       // this lane's dims of its two tokens are rotated
 #pragma unroll
         for (int s = 0; s < kSteps; ++s) turns[s] = 8 * sub < a.rot && turned[buf][(warp & 1) * 8 + 4 * s + grp] != 0;
+        // nearly always the whole warp's: a branch that all of it takes costs less (24.0 and 23.5 us; the
+        // backward is slower with it, 124.4 and 125.4)
+        const bool all = __all_sync(kFullMask, turns[0] && turns[1]);
         while (work.item == item && work.h < work.hi) {
             fetch((slot + kDepth - 1) % kDepth);     // also takes along the next unit's angles
             copies_wait<kDepth - 1>();
@@ -398,11 +401,13 @@ qk_norm_fwd_kernel(const __grid_constant__ NormArgs<T> a, const T *__restrict__ 
                     const float r = norm ? rsqrtf(sum8(squares(x)) * (1.f / 64.f) + a.eps) : 1.f;
 #pragma unroll
                     for (int e = 0; e < 4; ++e) x[e] = mul2(x[e], mul2(w[e], make_float2(r, r)));
-                    if (turns[s]) {
+                    const auto rotate = [&] {
                         Turn<PAIRS_INSIDE> turn;
                         turn.load(angles + (buf * kTokens + (warp & 1) * 8 + 4 * s + grp) * 64, sub);
                         turn.template apply<false>(x);
-                    }
+                    };
+                    if (all) rotate();
+                    else if (turns[s]) rotate();
                     raw.put(x);
                 }
                 if (here.in[s] && FIBATT_CHECKED(hi >= 0 && hi < Hs && here.n[s] < (unsigned)a.N)) raw.store(out + here.dense(s, hi, Hs, a.N), a0, a1);
