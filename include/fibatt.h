@@ -337,6 +337,51 @@ fibatt_status fibatt_cross_bwd(const fibatt_cross *d, const fibatt_heads *Q, con
                                const fibatt_heads *dV, void *workspace, size_t ws_bytes,
                                cudaStream_t stream);
 
+/* ------------------------------------ attention over a window, with sinks --- */
+
+/* Causal attention of a sequence's tokens to the last `window` of them, with
+ * the first `sinks` tokens visible to all (a decoder's self-attention; every
+ * query head h reads key/value head h / (Hq / Hkv)).  Query j of sequence b
+ * is at position
+ *     p = q_start[b] + j   (Nk - Nq + j when q_start is NULL: the last Nq of Nk tokens)
+ * and attends the keys k (at positions 0 to kv_len[b] - 1, all Nk when kv_len is NULL) with
+ *     k <= p   and   (k > p - window  or  k < sinks);
+ * a query at a negative position, or at kv_len[b] or behind it (padding), attends none and
+ * gets O = 0, LSE = -inf and dQ = 0.  s, LSE, O and the gradients are otherwise those of the
+ * cross attention above, summed over these pairs.  What memory holds in
+ * keys and values that no query of its sequence attends, and in queries and rows of dO that
+ * attend nothing (NaN, infinities), reaches no result.  A key or value that
+ * is not finite and is attended reaches the queries that attend it, and may reach
+ * those within 255 rows of them. */
+typedef struct {
+    int B, Hq, Hkv;              /* >= 1; Hkv divides Hq                             */
+    int Nq, Nk;                  /* >= 1, below 2^30; Nq <= Nk when q_start is NULL   */
+    int D;                       /* head dim, FIBATT_HEAD_DIM                        */
+    fibatt_dtype dtype;
+    float scale;                 /* any finite value                                 */
+    int window;                  /* >= 1 keys up to the query's own; Nk or more: all of them */
+    int sinks;                   /* >= 0                                             */
+    const int32_t *q_start;      /* device, [B], or NULL                              */
+    const int32_t *kv_len;       /* device, [B], or NULL; clamped to [0, Nk]          */
+} fibatt_window;
+
+/* Forward pass; tensors, arithmetic and errors as fibatt_cross_fwd, with
+ * INVALID_ARG for a window, sinks, Nq or Nk out of its range. */
+fibatt_status fibatt_window_fwd(const fibatt_window *d, const fibatt_heads *Q, const fibatt_heads *K,
+                                const fibatt_heads *V, const fibatt_heads *O, float *LSE,
+                                cudaStream_t stream);
+
+/* Device scratch of fibatt_window_bwd, in bytes. */
+size_t fibatt_window_bwd_workspace_bytes(const fibatt_window *d);
+
+/* Backward pass, as fibatt_cross_bwd; D_j = <dO_j, O_j> with the O that is given.
+ * Keys that no query attends get gradients of 0. */
+fibatt_status fibatt_window_bwd(const fibatt_window *d, const fibatt_heads *Q, const fibatt_heads *K,
+                                const fibatt_heads *V, const fibatt_heads *O, const float *LSE,
+                                const fibatt_heads *dO, const fibatt_heads *dQ, const fibatt_heads *dK,
+                                const fibatt_heads *dV, void *workspace, size_t ws_bytes,
+                                cudaStream_t stream);
+
 /* Message for the last failing call on this thread ("" if none). */
 const char *fibatt_last_error(void);
 

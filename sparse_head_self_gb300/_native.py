@@ -59,6 +59,7 @@ _SIGS = {
 # per call costs less than a ctypes structure.
 HEADS = struct.Struct("@Pqqq")                       # fibatt_heads: ptr, stride_b, stride_h, stride_n
 CROSS = struct.Struct("@7ifPPq")                     # fibatt_cross
+WINDOW = struct.Struct("@7ifiiPP")                   # fibatt_window
 QK_NORM = struct.Struct("@7iPPfiiPPiPq")             # fibatt_qk_norm
 
 _i64 = ctypes.c_int64
@@ -70,6 +71,9 @@ _SIGS.update({
     "fibatt_cross_fwd": (ctypes.c_int, [_vp] * 7),
     "fibatt_cross_bwd_workspace_bytes": (ctypes.c_size_t, [_vp]),
     "fibatt_cross_bwd": (ctypes.c_int, [_vp] * 11 + [ctypes.c_size_t, _vp]),
+    "fibatt_window_fwd": (ctypes.c_int, [_vp] * 7),
+    "fibatt_window_bwd_workspace_bytes": (ctypes.c_size_t, [_vp]),
+    "fibatt_window_bwd": (ctypes.c_int, [_vp] * 11 + [ctypes.c_size_t, _vp]),
 })
 
 

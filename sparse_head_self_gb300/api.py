@@ -7,6 +7,7 @@ calls on CPU tensors are rejected.
 from __future__ import annotations
 
 import ctypes
+import operator
 
 import torch
 from torch.autograd.function import once_differentiable
@@ -532,8 +533,8 @@ def _heads_arg(name: str, t, shape, dtype, index: int) -> bytes:
     return _pack_heads(t.data_ptr(), sb if b > 1 else 0, sh if h > 1 else 0, sn if n > 1 else 0)
 
 
-def _cross_desc(Q, K, V, scale, kv_len, key_mask):
-    """(packed fibatt_cross, Q, K, V as packed fibatt_heads, device index)."""
+def _attention_sizes(Q, K, V):
+    """(dtype, its code, device index) of four-dim tensors Q, K, V."""
     for name, t in (("Q", Q), ("K", K), ("V", V)):
         if not isinstance(t, torch.Tensor) or t.dim() != 4:
             raise ValueError(f"{name} must be a [B, H, N, D] tensor")
@@ -541,7 +542,12 @@ def _cross_desc(Q, K, V, scale, kv_len, key_mask):
     code = _DTYPES.get(dtype)
     if code is None:
         raise ValueError(f"dtype {dtype} unsupported (float32 or bfloat16)")
-    index = _index("Q", Q)
+    return dtype, code, _index("Q", Q)
+
+
+def _cross_desc(Q, K, V, scale, kv_len, key_mask):
+    """(packed fibatt_cross, Q, K, V as packed fibatt_heads, device index)."""
+    dtype, code, index = _attention_sizes(Q, K, V)
     B, Hq, Nq, D = shape = Q.shape
     _, Hkv, Nk, _ = K.shape
     lens = mask = mask_sb = 0
@@ -568,10 +574,10 @@ def cross_fwd(Q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, scale: float, k
     returns (O, LSE), O in Q's layout.  kv_len: int32 [B], the keys each
     sequence has; key_mask: bool [B, Nk], the keys it attends."""
     d, q, k, v, index = _cross_desc(Q, K, V, scale, kv_len, key_mask)
-    return _launch(index, stream, _cross_fwd, d, q, k, v, Q, O, LSE, index)
+    return _launch(index, stream, _attention_fwd, lib().fibatt_cross_fwd, d, q, k, v, Q, O, LSE, index)
 
 
-def _cross_fwd(d, q, k, v, Q, O, LSE, index, s):
+def _attention_fwd(call, d, q, k, v, Q, O, LSE, index, s):
     shape = Q.shape
     if O is None:
         O = torch.empty_like(Q)
@@ -580,7 +586,7 @@ def _cross_fwd(d, q, k, v, Q, O, LSE, index, s):
         lse = LSE.data_ptr()
     else:
         lse = _check_dense("LSE", LSE, shape[:3], torch.float32, index)
-    status = lib().fibatt_cross_fwd(d, q, k, v, _heads_arg("O", O, shape, Q.dtype, index), lse, s)
+    status = call(d, q, k, v, _heads_arg("O", O, shape, Q.dtype, index), lse, s)
     if status:
         check(status)
     return O, LSE
@@ -590,7 +596,13 @@ def cross_bwd(Q, K, V, O, LSE, dO, scale: float, kv_len=None, key_mask=None, dQ=
               workspace: torch.Tensor | None = None, stream=None):
     """fibatt_cross_bwd: (dQ, dK, dV) from cross_fwd's O and LSE and the
     gradient dO of O; each gradient in its input's layout unless given."""
-    d, q, k, v, index = _cross_desc(Q, K, V, scale, kv_len, key_mask)
+    L = lib()
+    return _attention_bwd(L.fibatt_cross_bwd, L.fibatt_cross_bwd_workspace_bytes,
+                          _cross_desc(Q, K, V, scale, kv_len, key_mask), Q, K, V, O, LSE, dO, dQ, dK, dV, workspace, stream)
+
+
+def _attention_bwd(bwd_call, workspace_bytes, desc, Q, K, V, O, LSE, dO, dQ, dK, dV, workspace, stream):
+    d, q, k, v, index = desc
     shape, dtype = Q.shape, Q.dtype
     _check_dense("LSE", LSE, shape[:3], torch.float32, index)
     o, do = _heads_arg("O", O, shape, dtype, index), _heads_arg("dO", dO, shape, dtype, index)
@@ -599,11 +611,10 @@ def cross_bwd(Q, K, V, O, LSE, dO, scale: float, kv_len=None, key_mask=None, dQ=
         dq = torch.empty_like(Q) if dQ is None else dQ
         dk = torch.empty_like(K) if dK is None else dK
         dv = torch.empty_like(V) if dV is None else dV
-        ws = _workspace(workspace, lib().fibatt_cross_bwd_workspace_bytes(d), index)
-        check(lib().fibatt_cross_bwd(d, q, k, v, o, LSE.data_ptr(), do, _heads_arg("dQ", dq, shape, dtype, index),
-                                     _heads_arg("dK", dk, K.shape, dtype, index),
-                                     _heads_arg("dV", dv, K.shape, dtype, index), ws.data_ptr(),
-                                     ws.numel() * ws.element_size(), s))
+        ws = _workspace(workspace, workspace_bytes(d), index)
+        check(bwd_call(d, q, k, v, o, LSE.data_ptr(), do, _heads_arg("dQ", dq, shape, dtype, index),
+                       _heads_arg("dK", dk, K.shape, dtype, index), _heads_arg("dV", dv, K.shape, dtype, index),
+                       ws.data_ptr(), ws.numel() * ws.element_size(), s))
         return dq, dk, dv
 
     return _launch(index, stream, call)
@@ -638,7 +649,85 @@ def cross_attention(Q, K, V, scale: float | None = None, kv_len=None, key_mask=N
     return CrossAttentionFunction.apply(Q, K, V, float(scale), kv_len, key_mask)
 
 
+# ------------------------------------------ attention over a window, with sinks
+
+def _window_desc(Q, K, V, scale, window, sinks, q_start, kv_len):
+    """(packed fibatt_window, Q, K, V as packed fibatt_heads, device index)."""
+    dtype, code, index = _attention_sizes(Q, K, V)
+    B, Hq, Nq, D = shape = Q.shape
+    _, Hkv, Nk, _ = K.shape
+    start = lens = 0
+    if q_start is not None:
+        start = _check_dense("q_start", q_start, (B,), torch.int32, index)
+    if kv_len is not None:
+        lens = _check_dense("kv_len", kv_len, (B,), torch.int32, index)
+    kv_shape = (B, Hkv, Nk, D)
+    return (_native.WINDOW.pack(B, Hq, Hkv, Nq, Nk, D, code, scale, *_band(window, sinks), start, lens),
+            _heads_arg("Q", Q, shape, dtype, index), _heads_arg("K", K, kv_shape, dtype, index),
+            _heads_arg("V", V, kv_shape, dtype, index), index)
+
+
+def _band(window, sinks):
+    """(window, sinks) as the library takes them: no window is one that holds every key."""
+    return _ALL if window is None else min(operator.index(window), _ALL), min(operator.index(sinks), _ALL)
+
+
+_ALL = 2**31 - 1
+
+
+def window_fwd(Q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, scale: float, window: int | None = None, sinks: int = 0,
+               q_start: torch.Tensor | None = None, kv_len: torch.Tensor | None = None, O: torch.Tensor | None = None,
+               LSE: torch.Tensor | None = None, stream=None):
+    """fibatt_window_fwd: causal attention of Q [B, Hq, Nq, 64] to K, V [B, Hkv,
+    Nk, 64] (Hkv divides Hq; any strides whose rows are contiguous), each query
+    to the `window` keys up to its own place (None: all) and to the first `sinks`; returns (O, LSE),
+    O in Q's layout.  q_start: int32 [B], the place of each sequence's first
+    query (Nk - Nq if not given); kv_len: int32 [B], the keys each sequence
+    has.  Queries outside their sequence attend nothing: O = 0, LSE = -inf."""
+    d, q, k, v, index = _window_desc(Q, K, V, scale, window, sinks, q_start, kv_len)
+    return _launch(index, stream, _attention_fwd, lib().fibatt_window_fwd, d, q, k, v, Q, O, LSE, index)
+
+
+def window_bwd(Q, K, V, O, LSE, dO, scale: float, window: int | None = None, sinks: int = 0, q_start=None, kv_len=None,
+               dQ=None, dK=None, dV=None, workspace: torch.Tensor | None = None, stream=None):
+    """fibatt_window_bwd: (dQ, dK, dV) from window_fwd's O and LSE and the
+    gradient dO of O; each gradient in its input's layout unless given."""
+    L = lib()
+    return _attention_bwd(L.fibatt_window_bwd, L.fibatt_window_bwd_workspace_bytes,
+                          _window_desc(Q, K, V, scale, window, sinks, q_start, kv_len), Q, K, V, O, LSE, dO, dQ, dK, dV,
+                          workspace, stream)
+
+
+class WindowAttentionFunction(torch.autograd.Function):
+    """Autograd wrapper: forward = fibatt_window_fwd, backward = fibatt_window_bwd."""
+
+    @staticmethod
+    def forward(ctx, Q, K, V, scale, window, sinks, q_start, kv_len):
+        Q, K, V = _readable(Q), _readable(K), _readable(V)
+        O, LSE = window_fwd(Q, K, V, scale, window, sinks, q_start, kv_len)
+        ctx.save_for_backward(Q, K, V, O, LSE, q_start, kv_len)
+        ctx.how = (scale, window, sinks)
+        return O
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dO):
+        Q, K, V, O, LSE, q_start, kv_len = ctx.saved_tensors
+        dQ, dK, dV = window_bwd(Q, K, V, O, LSE, _readable(dO), *ctx.how, q_start, kv_len)
+        return dQ, dK, dV, None, None, None, None, None
+
+
+def window_attention(Q, K, V, scale: float | None = None, window: int | None = None, sinks: int = 0, q_start=None,
+                     kv_len=None):
+    """Differentiable attention over a window with sinks (arguments as window_fwd; captured
+    as cross_attention)."""
+    if scale is None:
+        scale = Q.shape[-1] ** -0.5
+    return WindowAttentionFunction.apply(Q, K, V, float(scale), window, sinks, q_start, kv_len)
+
+
 __all__ = ["FibattError", "Support", "fwd", "bwd", "bwd_noalloc", "fibottention", "FibottentionFunction",
            "qk_norm_fwd", "qk_norm_bwd", "qk_norm", "QkNormFunction", "rotary_tables", "rotary_angles",
            "rotary_angles_2d", "cross_fwd", "cross_bwd", "cross_attention", "CrossAttentionFunction",
+           "window_fwd", "window_bwd", "window_attention", "WindowAttentionFunction",
            "wythoff_row", "wythoff_row_modified", "window_schedule", "HEAD_DIM"]

@@ -1,60 +1,16 @@
-// C ABI of the query/key norm and of the cross attention: argument checks and
-// dispatch.  The operations and every argument rule are documented in
+// C ABI of the query/key norm, of the cross attention and of the attention over a
+// window: argument checks and dispatch.  The operations and every argument rule are documented in
 // include/fibatt.h.
 #include <cmath>
-#include <cstdarg>
-#include <cstdio>
-#include <string>
 
-#include "cross.h"
+#include "cross_checks.h"
 
 namespace fibatt {
 namespace {
 
-std::string fmt(const char *f, ...) {
-    char buf[256];
-    va_list ap;
-    va_start(ap, f);
-    vsnprintf(buf, sizeof buf, f, ap);
-    va_end(ap);
-    return buf;
-}
-
-fibatt_status invalid(const std::string &m) { return set_error(FIBATT_ERR_INVALID_ARG, m); }
-fibatt_status unsupported(const std::string &m) { return set_error(FIBATT_ERR_UNSUPPORTED, m); }
-bool off(const void *p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a != 0; }
-
-fibatt_status check_type(int D, fibatt_dtype t) {
-    if (D != kHeadDim) return unsupported(fmt("head dim %d unsupported (only %d)", D, kHeadDim));
-    if (t != FIBATT_F32 && t != FIBATT_BF16) return unsupported(fmt("unknown dtype %d", (int)t));
-    return FIBATT_OK;
-}
-
-fibatt_status check_ptr(const void *p, const char *name, size_t a = 16) {
-    if (!p) return invalid(fmt("%s is NULL", name));
-    if (off(p, a)) return invalid(fmt("%s is not %zu-byte aligned", name, a));
-    return FIBATT_OK;
-}
-
-int64_t size_of(fibatt_dtype t) { return t == FIBATT_F32 ? 4 : 2; }
-
-// A head tensor of B sequences, H heads and N rows; `out`: the call writes it.
-fibatt_status check_heads(const fibatt_heads *v, const char *name, fibatt_dtype t, int B, int H, int N, bool out) {
-    if (!v) return invalid(fmt("%s is NULL", name));
-    if (fibatt_status st = check_ptr(v->ptr, name)) return st;
-    const int64_t strides[3] = {v->stride_b, v->stride_h, v->stride_n};
-    const int sizes[3] = {B, H, N};
-    for (int i = 0; i < 3; ++i) {
-        if (strides[i] < 0 || strides[i] > (int64_t)1 << 38 || strides[i] * size_of(t) % 16)
-            return invalid(fmt("%s: stride %lld is not a multiple of 16 bytes in [0, 2^38]", name, (long long)strides[i]));
-        if (i == 2 && N > 1 && strides[i] == 0) return invalid(fmt("%s: rows with a stride of 0", name));
-        if (out && sizes[i] > 1 && strides[i] < kHeadDim)
-            return invalid(fmt("%s is written, but a stride of %lld lets its rows overlap", name, (long long)strides[i]));
-    }
-    return FIBATT_OK;
-}
-
-fibatt_status check_cross(const fibatt_cross *d) {
+// What fibatt_cross and fibatt_window have in common.
+template <typename Desc>
+fibatt_status check_sizes(const Desc *d) {
     if (!d) return invalid("the description is NULL");
     if (fibatt_status st = check_type(d->D, d->dtype)) return st;
     if (d->B < 1 || d->Hq < 1 || d->Hkv < 1 || d->Nq < 1 || d->Nk < 1)
@@ -62,7 +18,11 @@ fibatt_status check_cross(const fibatt_cross *d) {
     if (d->Hq % d->Hkv) return invalid(fmt("Hkv=%d does not divide Hq=%d", d->Hkv, d->Hq));
     if (!std::isfinite(d->scale)) return invalid("scale is not finite");
     if (off(d->kv_len, 4)) return invalid("kv_len is not 4-byte aligned");
-    if (d->key_mask && d->key_mask_stride_b < 0) return invalid("key_mask_stride_b is negative");
+    return FIBATT_OK;
+}
+
+template <typename Desc>
+fibatt_status check_blocks(const Desc *d) {
     // blocks of the kernels: one a 64-row tile and head at most, and an eighth of what a grid may
     // have (clusters, of up to 16, are launched only while all of them find a place at once)
     const int64_t qb = (int64_t)d->B * d->Hq, kb = (int64_t)d->B * d->Hkv;
@@ -74,16 +34,100 @@ fibatt_status check_cross(const fibatt_cross *d) {
     return FIBATT_OK;
 }
 
-CrossArgs cross_args(const fibatt_cross *d, const fibatt_heads *Q, const fibatt_heads *K, const fibatt_heads *V,
+fibatt_status check_cross(const fibatt_cross *d) {
+    if (fibatt_status st = check_sizes(d)) return st;
+    if (d->key_mask && d->key_mask_stride_b < 0) return invalid("key_mask_stride_b is negative");
+    return check_blocks(d);
+}
+
+fibatt_status check_window(const fibatt_window *d) {
+    if (fibatt_status st = check_sizes(d)) return st;
+    if (d->window < 1) return invalid(fmt("window=%d must be >= 1", d->window));
+    if (d->sinks < 0) return invalid(fmt("sinks=%d must be >= 0", d->sinks));
+    if (off(d->q_start, 4)) return invalid("q_start is not 4-byte aligned");
+    if (!d->q_start && d->Nq > d->Nk)
+        return invalid(fmt("Nq=%d queries are not the last of Nk=%d tokens, and q_start is NULL", d->Nq, d->Nk));
+    if (d->Nq >= 1 << 30 || d->Nk >= 1 << 30) return invalid("Nq and Nk must be below 2^30");
+    return check_blocks(d);
+}
+
+KeySet key_set(const fibatt_cross *d) { return KeySet{d->kv_len, d->key_mask, d->key_mask_stride_b, d->Nk}; }
+KeySet key_set(const fibatt_window *d) { return KeySet{d->kv_len, nullptr, 0, d->Nk}; }
+
+template <typename Desc>
+CrossArgs cross_args(const Desc *d, const fibatt_heads *Q, const fibatt_heads *K, const fibatt_heads *V,
                      const fibatt_heads *O, cudaStream_t stream) {
     CrossArgs a = {};
     a.B = d->B, a.Hq = d->Hq, a.Hkv = d->Hkv, a.Nq = d->Nq, a.Nk = d->Nk;
     a.dtype = d->dtype;
     a.scale = d->scale;
-    a.keys = KeySet{d->kv_len, d->key_mask, d->key_mask_stride_b, d->Nk};
+    a.keys = key_set(d);
     a.Q = *Q, a.K = *K, a.V = *V, a.O = *O;
     a.stream = stream;
     return a;
+}
+
+CrossArgs window_args(const fibatt_window *d, const fibatt_heads *Q, const fibatt_heads *K, const fibatt_heads *V,
+                      const fibatt_heads *O, cudaStream_t stream) {
+    CrossArgs a = cross_args(d, Q, K, V, O, stream);
+    a.banded = true;
+    // (a window that reaches the first key makes sinks of no account)
+    const int window = std::min(d->window, d->Nk);
+    a.band = Band{d->q_start, d->Nq, d->Nk, window, window == d->Nk ? 0 : std::min(d->sinks, d->Nk)};
+    return a;
+}
+
+// The tensors of a forward and of a backward pass.
+template <typename Desc>
+fibatt_status check_fwd(const Desc *d, const fibatt_heads *Q, const fibatt_heads *K, const fibatt_heads *V,
+                        const fibatt_heads *O, const float *LSE) {
+    fibatt_status st;
+    if ((st = check_heads(Q, "Q", d->dtype, d->B, d->Hq, d->Nq, false)) ||
+        (st = check_heads(K, "K", d->dtype, d->B, d->Hkv, d->Nk, false)) ||
+        (st = check_heads(V, "V", d->dtype, d->B, d->Hkv, d->Nk, false)) ||
+        (st = check_heads(O, "O", d->dtype, d->B, d->Hq, d->Nq, true)) || (st = check_ptr(LSE, "LSE", 4)))
+        return st;
+    if (fault("launch")) return set_error(FIBATT_ERR_CUDA, "injected launch failure (FIBATT_FAULT=launch)");
+    return FIBATT_OK;
+}
+template <typename Desc>
+fibatt_status check_bwd(const Desc *d, const fibatt_heads *Q, const fibatt_heads *K, const fibatt_heads *V,
+                        const fibatt_heads *O, const float *LSE, const fibatt_heads *dO, const fibatt_heads *dQ,
+                        const fibatt_heads *dK, const fibatt_heads *dV, const void *workspace, size_t ws_bytes,
+                        size_t needed) {
+    fibatt_status st;
+    if ((st = check_heads(Q, "Q", d->dtype, d->B, d->Hq, d->Nq, false)) ||
+        (st = check_heads(K, "K", d->dtype, d->B, d->Hkv, d->Nk, false)) ||
+        (st = check_heads(V, "V", d->dtype, d->B, d->Hkv, d->Nk, false)) ||
+        (st = check_heads(O, "O", d->dtype, d->B, d->Hq, d->Nq, false)) ||
+        (st = check_heads(dO, "dO", d->dtype, d->B, d->Hq, d->Nq, false)) ||
+        (st = check_heads(dQ, "dQ", d->dtype, d->B, d->Hq, d->Nq, true)) ||
+        (st = check_heads(dK, "dK", d->dtype, d->B, d->Hkv, d->Nk, true)) ||
+        (st = check_heads(dV, "dV", d->dtype, d->B, d->Hkv, d->Nk, true)) || (st = check_ptr(LSE, "LSE", 4)) ||
+        (st = check_ptr(workspace, "workspace")))
+        return st;
+    if (ws_bytes < needed) return invalid(fmt("workspace holds %zu bytes, %zu needed", ws_bytes, needed));
+    if (fault("launch")) return set_error(FIBATT_ERR_CUDA, "injected launch failure (FIBATT_FAULT=launch)");
+    return FIBATT_OK;
+}
+
+fibatt_status run_fwd(const CrossArgs &a, const char *what) {
+    const cudaError_t e = cross_rows_takes(a)         ? launch_cross_rows(a)
+                          : a.dtype == FIBATT_BF16 ? launch_cross_fwd_mma(a)
+                                                   : launch_cross_fwd_f32(a);
+    return e == cudaSuccess ? FIBATT_OK : cuda_error(e, what);
+}
+fibatt_status run_bwd(const CrossArgs &a, const char *what) {
+    const cudaError_t e = a.dtype == FIBATT_BF16 ? launch_cross_bwd_mma(a) : launch_cross_bwd_f32(a);
+    return e == cudaSuccess ? FIBATT_OK : cuda_error(e, what);
+}
+
+template <typename Desc>
+size_t bwd_workspace(const Desc *d) {
+    if (!d || d->B < 1 || d->Hq < 1 || d->Nq < 1) return 0;
+    const size_t bytes = d->dtype == FIBATT_BF16 ? cross_bwd_mma_workspace(d->B, d->Hq, d->Nq)
+                                                 : (size_t)d->B * d->Hq * d->Nq * sizeof(float2);
+    return (bytes + 255) / 256 * 256;
 }
 
 fibatt_status check_norm(const fibatt_qk_norm *d, const void *X, int64_t sb, int64_t sn) {
@@ -199,27 +243,13 @@ fibatt_status fibatt_cross_fwd(const fibatt_cross *d, const fibatt_heads *Q, con
                                const fibatt_heads *V, const fibatt_heads *O, float *LSE, cudaStream_t stream) {
     const ProfileReport report("fibatt_cross_fwd");
     fibatt_status st = check_cross(d);
-    if (st != FIBATT_OK) return st;
-    if ((st = check_heads(Q, "Q", d->dtype, d->B, d->Hq, d->Nq, false)) ||
-        (st = check_heads(K, "K", d->dtype, d->B, d->Hkv, d->Nk, false)) ||
-        (st = check_heads(V, "V", d->dtype, d->B, d->Hkv, d->Nk, false)) ||
-        (st = check_heads(O, "O", d->dtype, d->B, d->Hq, d->Nq, true)) || (st = check_ptr(LSE, "LSE", 4)))
-        return st;
-    if (fault("launch")) return set_error(FIBATT_ERR_CUDA, "injected launch failure (FIBATT_FAULT=launch)");
+    if (st != FIBATT_OK || (st = check_fwd(d, Q, K, V, O, LSE))) return st;
     CrossArgs a = cross_args(d, Q, K, V, O, stream);
     a.LSE = LSE;
-    const cudaError_t e = cross_rows_takes(a)         ? launch_cross_rows(a)
-                          : a.dtype == FIBATT_BF16 ? launch_cross_fwd_mma(a)
-                                                   : launch_cross_fwd_f32(a);
-    return e == cudaSuccess ? FIBATT_OK : cuda_error(e, "fibatt_cross_fwd launch");
+    return run_fwd(a, "fibatt_cross_fwd launch");
 }
 
-size_t fibatt_cross_bwd_workspace_bytes(const fibatt_cross *d) {
-    if (!d || d->B < 1 || d->Hq < 1 || d->Nq < 1) return 0;
-    const size_t bytes = d->dtype == FIBATT_BF16 ? cross_bwd_mma_workspace(d->B, d->Hq, d->Nq)
-                                                 : (size_t)d->B * d->Hq * d->Nq * sizeof(float2);
-    return (bytes + 255) / 256 * 256;
-}
+size_t fibatt_cross_bwd_workspace_bytes(const fibatt_cross *d) { return bwd_workspace(d); }
 
 fibatt_status fibatt_cross_bwd(const fibatt_cross *d, const fibatt_heads *Q, const fibatt_heads *K,
                                const fibatt_heads *V, const fibatt_heads *O, const float *LSE, const fibatt_heads *dO,
@@ -227,26 +257,42 @@ fibatt_status fibatt_cross_bwd(const fibatt_cross *d, const fibatt_heads *Q, con
                                size_t ws_bytes, cudaStream_t stream) {
     const ProfileReport report("fibatt_cross_bwd");
     fibatt_status st = check_cross(d);
-    if (st != FIBATT_OK) return st;
-    if ((st = check_heads(Q, "Q", d->dtype, d->B, d->Hq, d->Nq, false)) ||
-        (st = check_heads(K, "K", d->dtype, d->B, d->Hkv, d->Nk, false)) ||
-        (st = check_heads(V, "V", d->dtype, d->B, d->Hkv, d->Nk, false)) ||
-        (st = check_heads(O, "O", d->dtype, d->B, d->Hq, d->Nq, false)) ||
-        (st = check_heads(dO, "dO", d->dtype, d->B, d->Hq, d->Nq, false)) ||
-        (st = check_heads(dQ, "dQ", d->dtype, d->B, d->Hq, d->Nq, true)) ||
-        (st = check_heads(dK, "dK", d->dtype, d->B, d->Hkv, d->Nk, true)) ||
-        (st = check_heads(dV, "dV", d->dtype, d->B, d->Hkv, d->Nk, true)) || (st = check_ptr(LSE, "LSE", 4)) ||
-        (st = check_ptr(workspace, "workspace")))
+    if (st != FIBATT_OK ||
+        (st = check_bwd(d, Q, K, V, O, LSE, dO, dQ, dK, dV, workspace, ws_bytes, bwd_workspace(d))))
         return st;
-    if (ws_bytes < fibatt_cross_bwd_workspace_bytes(d))
-        return invalid(fmt("workspace holds %zu bytes, %zu needed", ws_bytes, fibatt_cross_bwd_workspace_bytes(d)));
-    if (fault("launch")) return set_error(FIBATT_ERR_CUDA, "injected launch failure (FIBATT_FAULT=launch)");
     CrossArgs a = cross_args(d, Q, K, V, O, stream);
     a.LSE = const_cast<float *>(LSE);
     a.dO = *dO, a.dQ = *dQ, a.dK = *dK, a.dV = *dV;
     a.stats = static_cast<float2 *>(workspace);
-    const cudaError_t e = a.dtype == FIBATT_BF16 ? launch_cross_bwd_mma(a) : launch_cross_bwd_f32(a);
-    return e == cudaSuccess ? FIBATT_OK : cuda_error(e, "fibatt_cross_bwd launch");
+    return run_bwd(a, "fibatt_cross_bwd launch");
+}
+
+fibatt_status fibatt_window_fwd(const fibatt_window *d, const fibatt_heads *Q, const fibatt_heads *K,
+                                const fibatt_heads *V, const fibatt_heads *O, float *LSE, cudaStream_t stream) {
+    const ProfileReport report("fibatt_window_fwd");
+    fibatt_status st = check_window(d);
+    if (st != FIBATT_OK || (st = check_fwd(d, Q, K, V, O, LSE))) return st;
+    CrossArgs a = window_args(d, Q, K, V, O, stream);
+    a.LSE = LSE;
+    return run_fwd(a, "fibatt_window_fwd launch");
+}
+
+size_t fibatt_window_bwd_workspace_bytes(const fibatt_window *d) { return bwd_workspace(d); }
+
+fibatt_status fibatt_window_bwd(const fibatt_window *d, const fibatt_heads *Q, const fibatt_heads *K,
+                                const fibatt_heads *V, const fibatt_heads *O, const float *LSE, const fibatt_heads *dO,
+                                const fibatt_heads *dQ, const fibatt_heads *dK, const fibatt_heads *dV, void *workspace,
+                                size_t ws_bytes, cudaStream_t stream) {
+    const ProfileReport report("fibatt_window_bwd");
+    fibatt_status st = check_window(d);
+    if (st != FIBATT_OK ||
+        (st = check_bwd(d, Q, K, V, O, LSE, dO, dQ, dK, dV, workspace, ws_bytes, bwd_workspace(d))))
+        return st;
+    CrossArgs a = window_args(d, Q, K, V, O, stream);
+    a.LSE = const_cast<float *>(LSE);
+    a.dO = *dO, a.dQ = *dQ, a.dK = *dK, a.dV = *dV;
+    a.stats = static_cast<float2 *>(workspace);
+    return run_bwd(a, "fibatt_window_bwd launch");
 }
 
 }  // extern "C"

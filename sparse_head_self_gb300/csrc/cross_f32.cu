@@ -86,6 +86,12 @@ __device__ __forceinline__ uint64_t key_bits(const KeySet &ks, int b, int n0, in
     return (uint64_t)__ballot_sync(kFullMask, lo) | ((uint64_t)__ballot_sync(kFullMask, hi) << 32);
 }
 
+// The same for the keys that queries at positions lo to hi attend.
+__device__ __forceinline__ uint64_t band_bits(const Band &w, int lo, int hi, int n0) {
+    if (lo > hi) return 0ull;
+    return first_bits(hi + 1 - n0) & (~first_bits(lo + 1 - w.window - n0) | first_bits(w.sinks - n0));
+}
+
 // x = hi + lo, hi rounded to 11 bits (half a step added to the pattern, the
 // others cleared); of lo 11 are read.  With hi cut off instead, lo always has x's
 // sign, and the products lo lo that are left out add up: 1.4e-6 of the gradients'
@@ -210,8 +216,9 @@ __device__ __forceinline__ void clear(float (&o)[8][4]) {
 // The part of `tiles` that CTA `r` of `c` walks over.
 __device__ __forceinline__ int part(int tiles, int r, int c) { return (int)((int64_t)tiles * r / c); }
 
+template <bool BAND>
 __global__ void __launch_bounds__(kThreads, kFwdBlocks)
-cross_fwd_f32_kernel(int Hq, int Hkv, int Nq, KeySet ks, Rows<const float> Q, Rows<const float> K, Rows<const float> V,
+cross_fwd_f32_kernel(int Hq, int Hkv, int Nq, KeySet ks, Band band, Rows<const float> Q, Rows<const float> K, Rows<const float> V,
                      Rows<float> O, float *__restrict__ LSE, float scale_log2, int qtiles, int64_t units) {
     extern __shared__ float4 smem4[];
     float *sq = reinterpret_cast<float *>(smem4), *sk = sq + kTile, *sv = sk + kTile;
@@ -224,14 +231,27 @@ cross_fwd_f32_kernel(int Hq, int Hkv, int Nq, KeySet ks, Rows<const float> Q, Ro
     const int hk = h / (Hq / Hkv), q0 = qt * kT;
 
     grid_dep_wait();
-    const int bound = ks.bound(b), tiles = (bound + kT - 1) / kT;
+    const int bound = ks.bound(b);
+    int tiles = (bound + kT - 1) / kT, p[2] = {-1, -1}, first = 0, last = 0;   // positions: of the lane's rows, of the tile's
+    BandWalk<kT> walk;
+    if constexpr (BAND) {
+        const int p0 = band.first(b);
+        first = max(0, p0 + q0);
+        last = min(bound, p0 + min(Nq, q0 + kT)) - 1;
+        walk = BandWalk<kT>(band, first, last);
+        tiles = walk.n;
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            if (p0 + q0 + ln.row(i) <= last) p[i] = p0 + q0 + ln.row(i);
+    }
     const int lo = part(tiles, rank, C), hi = part(tiles, rank + 1, C);
     const bool mine = 16 * ln.w < Nq - q0;     // the warp's 16 rows begin within the queries
     stage(sq, Q.row(b, h, 0), Q.sn, q0, first_bits(Nq - q0));
     float m[2] = {kNegInf, kNegInf}, l[2] = {0.f, 0.f}, o[8][4];
     clear(o);
-    for (int t = lo; t < hi; ++t) {
-        const uint64_t ok = key_bits(ks, b, t * kT, bound);
+    for (int x = lo; x < hi; ++x) {
+        const int t = BAND ? walk.tile(x) : x;
+        const uint64_t ok = BAND ? band_bits(band, first, last, t * kT) : key_bits(ks, b, t * kT, bound);
         if (ok == 0) continue;
         __syncthreads();
         stage(sk, K.row(b, hk, 0), K.sn, t * kT, ok);
@@ -250,7 +270,8 @@ cross_fwd_f32_kernel(int Hq, int Hkv, int Nq, KeySet ks, Rows<const float> Q, Ro
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
                     float &x = s[j][2 * i + k];
-                    x = (ok >> ln.col(j, k)) & 1 ? x * scale_log2 : kNegInf;
+                    const bool in = BAND ? band.sees(p[i], t * kT + ln.col(j, k)) : (ok >> ln.col(j, k)) & 1;
+                    x = in ? x * scale_log2 : kNegInf;
                     top = fmaxf(top, x);
                 }
             const float next = fmaxf(m[i], row_max(top));
@@ -385,6 +406,7 @@ __device__ __forceinline__ void finish(const float (&o)[8][4], float *parts, Row
 struct BwdF32Args {
     int Hq, Hkv, Nq;
     KeySet ks;
+    Band band;            // BAND
     Rows<const float> Q, K, V, dO;
     const float2 *stats;
     Rows<float> dQ, dK, dV;
@@ -396,6 +418,7 @@ struct BwdF32Args {
 };
 
 // Holds 64 queries and walks over the keys.
+template <bool BAND>
 __device__ __forceinline__ void hold_queries(const BwdF32Args &a, float *smem, int64_t unit) {
     float *sq = smem, *sg = sq + kTile, *sk = sg + kTile, *sv = sk + kTile;
     const Lane ln;
@@ -403,7 +426,19 @@ __device__ __forceinline__ void hold_queries(const BwdF32Args &a, float *smem, i
     const int qt = (int)(unit % a.qtiles), h = (int)(unit / a.qtiles % a.Hq), b = (int)(unit / a.qtiles / a.Hq);
     const int hk = h / (a.Hq / a.Hkv), q0 = qt * kT;
     const float scale_log2 = a.scale * kLog2e;
-    const int bound = a.ks.bound(b), tiles = (bound + kT - 1) / kT;
+    const int bound = a.ks.bound(b);
+    int tiles = (bound + kT - 1) / kT, p[2] = {-1, -1}, first = 0, last = 0;   // positions: of the lane's rows, of the tile's
+    BandWalk<kT> walk;
+    if constexpr (BAND) {
+        const int p0 = a.band.first(b);
+        first = max(0, p0 + q0);
+        last = min(bound, p0 + min(a.Nq, q0 + kT)) - 1;
+        walk = BandWalk<kT>(a.band, first, last);
+        tiles = walk.n;
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            if (p0 + q0 + ln.row(i) <= last) p[i] = p0 + q0 + ln.row(i);
+    }
     const int lo = part(tiles, rank, C), hi = part(tiles, rank + 1, C);
     const bool mine = 16 * ln.w < a.Nq - q0;     // the warp's 16 rows begin within the queries
     stage(sq, a.Q.row(b, h, 0), a.Q.sn, q0, first_bits(a.Nq - q0));
@@ -416,8 +451,9 @@ __device__ __forceinline__ void hold_queries(const BwdF32Args &a, float *smem, i
         const int n = q0 + ln.row(i);
         st[i] = n < a.Nq ? a.stats[((int64_t)b * a.Hq + h) * a.Nq + n] : make_float2(-kNegInf, 0.f);
     }
-    for (int t = lo; t < hi; ++t) {
-        const uint64_t ok = key_bits(a.ks, b, t * kT, bound);
+    for (int y = lo; y < hi; ++y) {
+        const int t = BAND ? walk.tile(y) : y;
+        const uint64_t ok = BAND ? band_bits(a.band, first, last, t * kT) : key_bits(a.ks, b, t * kT, bound);
         if (ok == 0) continue;
         __syncthreads();
         stage(sk, a.K.row(b, hk, 0), a.K.sn, t * kT, ok);
@@ -434,8 +470,9 @@ __device__ __forceinline__ void hold_queries(const BwdF32Args &a, float *smem, i
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const float2 x = st[i >> 1];
-                const float p = exp2f(fmaf(s[j][i], scale_log2, -x.x));
-                s[j][i] = (ok >> ln.col(j, i & 1)) & 1 ? p * (dp[j][i] - x.y) : 0.f;
+                const float w = exp2f(fmaf(s[j][i], scale_log2, -x.x));
+                const bool in = BAND ? a.band.sees(p[i >> 1], t * kT + ln.col(j, i & 1)) : (ok >> ln.col(j, i & 1)) & 1;
+                s[j][i] = in ? w * (dp[j][i] - x.y) : 0.f;
             }
         nn(acc, s, sk, ln, cols);
     }
@@ -443,15 +480,29 @@ __device__ __forceinline__ void hold_queries(const BwdF32Args &a, float *smem, i
 }
 
 // Holds 64 keys and walks over the queries of every head that shares them.
+template <bool BAND>
 __device__ __forceinline__ void hold_keys(const BwdF32Args &a, float *smem, float2 *sst, int64_t unit) {
     float *sk = smem, *sv = sk + kTile, *sq = sv + kTile, *sg = sq + kTile;
     const Lane ln;
     const int C = (int)cluster_size(), rank = (int)cluster_rank();
     const int kt = (int)(unit % a.ktiles), hk = (int)(unit / a.ktiles % a.Hkv), b = (int)(unit / a.ktiles / a.Hkv);
-    const int G = a.Hq / a.Hkv, k0 = kt * kT, qtiles = a.qtiles;
+    const int G = a.Hq / a.Hkv, k0 = kt * kT;
     const float scale_log2 = a.scale * kLog2e;
     const int bound = a.ks.bound(b);
-    const uint64_t ok = key_bits(a.ks, b, k0, bound);
+    uint64_t ok;
+    int p0 = 0, first = 0, last = 0;      // positions: of query 0, of the queries that attend keys of the tile
+    int from = 0, qtiles = a.qtiles;      // the query tiles of a head that hold those
+    if constexpr (BAND) {
+        p0 = a.band.first(b);
+        const int k1 = min(k0 + kT, bound) - 1, end = min(bound, p0 + a.Nq);
+        first = max(p0, k0);
+        last = k0 > k1 ? first - 1 : (k0 < a.band.sinks ? end : min(end, k1 + a.band.window)) - 1;
+        from = first <= last ? (first - p0) / kT : 0;
+        qtiles = first <= last ? (last - p0) / kT + 1 - from : 0;
+        ok = band_bits(a.band, first, last, k0);
+    } else {
+        ok = key_bits(a.ks, b, k0, bound);
+    }
     const bool mine = 16 * ln.w < bound - k0;    // the warp's 16 rows begin within the keys
     // the walk: the query tiles of each of the G heads in turn; none for a tile without keys
     const int64_t tiles = ok ? (int64_t)G * qtiles : 0;
@@ -463,14 +514,15 @@ __device__ __forceinline__ void hold_keys(const BwdF32Args &a, float *smem, floa
     clear(av);
     const bool in[2] = {((ok >> ln.row(0)) & 1) != 0, ((ok >> ln.row(1)) & 1) != 0};
     for (int64_t t = lo; t < hi; ++t) {
-        const int h = hk * G + (int)(t / qtiles), q0 = (int)(t % qtiles) * kT;
-        const uint64_t rows = first_bits(a.Nq - q0);
+        const int h = hk * G + (int)(t / qtiles), q0 = (from + (int)(t % qtiles)) * kT;
+        uint64_t rows = first_bits(a.Nq - q0);
+        if constexpr (BAND) rows &= first_bits(bound - p0 - q0) & ~first_bits(-p0 - q0);    // queries of the sequence
         __syncthreads();
         stage(sq, a.Q.row(b, h, 0), a.Q.sn, q0, rows);
         stage(sg, a.dO.row(b, h, 0), a.dO.sn, q0, rows);
         if (threadIdx.x < kT) {
             const int n = q0 + (int)threadIdx.x;
-            sst[threadIdx.x] = n < a.Nq ? a.stats[((int64_t)b * a.Hq + h) * a.Nq + n] : make_float2(-kNegInf, 0.f);
+            sst[threadIdx.x] = (rows >> threadIdx.x) & 1 ? a.stats[((int64_t)b * a.Hq + h) * a.Nq + n] : make_float2(-kNegInf, 0.f);
         }
         staged();
         __syncthreads();
@@ -485,8 +537,10 @@ __device__ __forceinline__ void hold_keys(const BwdF32Args &a, float *smem, floa
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const float lse = i & 1 ? st.z : st.x, d = i & 1 ? st.w : st.y;
-                p[j][i] = in[i >> 1] ? exp2f(fmaf(p[j][i], scale_log2, -lse)) : 0.f;
-                ds[j][i] = in[i >> 1] ? p[j][i] * (ds[j][i] - d) : 0.f;
+                bool on = in[i >> 1];
+                if constexpr (BAND) on = on && a.band.sees(p0 + q0 + ln.col(j, i & 1), k0 + ln.row(i >> 1));
+                p[j][i] = on ? exp2f(fmaf(p[j][i], scale_log2, -lse)) : 0.f;
+                ds[j][i] = on ? p[j][i] * (ds[j][i] - d) : 0.f;
             }
         }
         nn(av, p, sg, ln, cols);
@@ -497,6 +551,7 @@ __device__ __forceinline__ void hold_keys(const BwdF32Args &a, float *smem, floa
 }
 
 // Both kinds of unit in one launch, those that hold keys first.
+template <bool BAND>
 __global__ void __launch_bounds__(kThreads, kBwdBlocks) cross_bwd_f32_kernel(const __grid_constant__ BwdF32Args a) {
     extern __shared__ float4 smem4[];
     __shared__ __align__(16) float2 sst[kT];
@@ -504,8 +559,8 @@ __global__ void __launch_bounds__(kThreads, kBwdBlocks) cross_bwd_f32_kernel(con
     grid_dep_wait();
     const int64_t unit = a.first + blockIdx.x / cluster_size();
     if (!FIBATT_CHECKED(unit < a.units)) return;    // whole clusters
-    if (unit < a.key_units) hold_keys(a, smem, sst, unit);
-    else hold_queries(a, smem, unit - a.key_units);
+    if (unit < a.key_units) hold_keys<BAND>(a, smem, sst, unit);
+    else hold_queries<BAND>(a, smem, unit - a.key_units);
 }
 
 // The largest cluster of this kernel: 16 CTAs where the current device takes them, else 8.
@@ -515,28 +570,36 @@ int largest_cluster(size_t smem) {
     return known.get(current_device(), [=] { return clusters_held<Kernel>(16, kThreads, smem) > 0 ? 16 : 8; });
 }
 
-}  // namespace
+// Key tiles that a query tile walks over, at most.
+template <bool BAND>
+int64_t key_tiles(const CrossArgs &a) {
+    const int64_t all = (a.Nk + kT - 1) / kT;
+    return BAND ? std::min<int64_t>(all, ((int64_t)a.band.window + kT) / kT + 1 + (a.band.sinks + kT - 1) / kT) : all;
+}
 
-cudaError_t launch_cross_fwd_f32(const CrossArgs &a) {
+template <bool BAND>
+cudaError_t fwd(const CrossArgs &a) {
     constexpr size_t smem = 3 * kTile * sizeof(float);
-    const cudaError_t e = prepare_kernel<cross_fwd_f32_kernel>(smem, 0);
+    const cudaError_t e = prepare_kernel<cross_fwd_f32_kernel<BAND>>(smem, 0);
     if (e != cudaSuccess) return e;
     const int qtiles = (a.Nq + kT - 1) / kT;
     const int64_t units = (int64_t)a.B * a.Hq * qtiles;
     // (one head, 100 queries on 16385 keys: clusters of 16 85 us, of 8 161)
-    const int c = cluster_for(units, (a.Nk + kT - 1) / kT, kFwdBlocks * sm_count(), largest_cluster<cross_fwd_f32_kernel>(smem));
-    return launch_clusters(cross_fwd_f32_kernel, (unsigned)(units * c), c, kThreads, smem, a.stream, a.Hq, a.Hkv, a.Nq,
-                           a.keys, rows_of<const float>(a.Q), rows_of<const float>(a.K), rows_of<const float>(a.V),
+    const int c = cluster_for(units, key_tiles<BAND>(a), kFwdBlocks * sm_count(), largest_cluster<cross_fwd_f32_kernel<BAND>>(smem));
+    return launch_clusters(cross_fwd_f32_kernel<BAND>, (unsigned)(units * c), c, kThreads, smem, a.stream, a.Hq, a.Hkv, a.Nq,
+                           a.keys, a.band, rows_of<const float>(a.Q), rows_of<const float>(a.K), rows_of<const float>(a.V),
                            rows_of<float>(a.O), a.LSE, a.scale * kLog2e, qtiles, units);
 }
 
-cudaError_t launch_cross_bwd_f32(const CrossArgs &a) {
+template <bool BAND>
+cudaError_t bwd(const CrossArgs &a) {
     constexpr size_t smem = 4 * kTile * sizeof(float);
-    cudaError_t e = prepare_kernel<cross_bwd_f32_kernel>(smem, 0);
+    cudaError_t e = prepare_kernel<cross_bwd_f32_kernel<BAND>>(smem, 0);
     if (e != cudaSuccess) return e;
     BwdF32Args f;
     f.Hq = a.Hq, f.Hkv = a.Hkv, f.Nq = a.Nq;
     f.ks = a.keys;
+    f.band = a.band;
     f.Q = rows_of<const float>(a.Q), f.K = rows_of<const float>(a.K), f.V = rows_of<const float>(a.V);
     f.dO = rows_of<const float>(a.dO);
     f.stats = a.stats;
@@ -553,16 +616,23 @@ cudaError_t launch_cross_bwd_f32(const CrossArgs &a) {
     f.first = 0;
     // (one head, 100 queries on 16385 keys: 157 us in two launches, 275 with clusters of 8
     // at most, 1937 in one)
-    const Launches l(query_units, f.ktiles, key_units, (int64_t)(a.Hq / a.Hkv) * f.qtiles, kBwdBlocks * sm_count(), 1,
-                     2, largest_cluster<cross_bwd_f32_kernel>(smem));
+    int64_t key_walk = f.qtiles;
+    if (BAND && a.band.sinks == 0) key_walk = std::min<int64_t>(key_walk, ((int64_t)a.band.window + kT) / kT + 1);
+    const Launches l(query_units, key_tiles<BAND>(a), key_units, (a.Hq / a.Hkv) * key_walk, kBwdBlocks * sm_count(), 1,
+                     2, largest_cluster<cross_bwd_f32_kernel<BAND>>(smem));
     if (!l.two)
-        return launch_clusters(cross_bwd_f32_kernel, (unsigned)((key_units + query_units) * l.c), l.c, kThreads, smem,
+        return launch_clusters(cross_bwd_f32_kernel<BAND>, (unsigned)((key_units + query_units) * l.c), l.c, kThreads, smem,
                                a.stream, f);
-    e = launch_clusters(cross_bwd_f32_kernel, (unsigned)(key_units * l.c_key), l.c_key, kThreads, smem, a.stream, f);
+    e = launch_clusters(cross_bwd_f32_kernel<BAND>, (unsigned)(key_units * l.c_key), l.c_key, kThreads, smem, a.stream, f);
     if (e != cudaSuccess) return e;
     f.first = f.key_units;
-    return launch_clusters(cross_bwd_f32_kernel, (unsigned)(query_units * l.c_query), l.c_query, kThreads, smem, a.stream, f);
+    return launch_clusters(cross_bwd_f32_kernel<BAND>, (unsigned)(query_units * l.c_query), l.c_query, kThreads, smem, a.stream, f);
 }
+
+}  // namespace
+
+cudaError_t launch_cross_fwd_f32(const CrossArgs &a) { return a.banded ? fwd<true>(a) : fwd<false>(a); }
+cudaError_t launch_cross_bwd_f32(const CrossArgs &a) { return a.banded ? bwd<true>(a) : bwd<false>(a); }
 
 FIBATT_DEFINE_ERROR_READER(read_error_cross_f32, "cross_f32.cu")
 

@@ -64,9 +64,10 @@ static_assert(4 * kRegsMany + kRegsFew == 5 * kRegs, "the shares add up");
 // columns of tensor memory
 constexpr uint32_t kColS = 0, kColDp = 128, kColP = 256, kColDs = 320, kColAcc0 = 384, kColAcc1 = 448, kCols = 512;
 
+template <bool BAND>
 struct BwdMmaArgs {
     TensorArg q, g, k, v;       // boxes of query tiles (Q, dO) and of key tiles (K, V)
-    QueryTiles qt;
+    TilesOf<BAND> qt;
     KeySet ks;
     const float2 *stats;        // (LSE log2 e, D) of every query row
     const uint4 *lse_parts, *d_parts;   // of every query row of whole tiles, then 128 rows of no query
@@ -78,6 +79,7 @@ struct BwdMmaArgs {
     int *next_unit;             // units given out behind every CTA's first
     float scale;
     float c;                    // scale log2 e, not 0
+    Band band;                  // BAND
     BwdMmaArgs() : qt(1, 1, false) {}
 };
 
@@ -159,6 +161,7 @@ cross_parts_kernel(int Hq, int Hkv, int Nq, int npad, unsigned rows, KeySet ks, 
         }
     }
     d = sum(d);
+    if (none) d = 0.f;      // (dO may hold anything)
     if (i == 0) lse_parts[row] = none ? no_query(c) : three_parts(-lse2 / c);
     if (i == 1) d_parts[row] = three_parts(-d);
     if (i == 2) stats[at] = make_float2(lse2, d);
@@ -261,13 +264,27 @@ cross_parts_few_kernel(int Hq, int Hkv, int Nq, int npad, unsigned heads, KeySet
 // the other side's tiles that this CTA of the cluster streams.  The copying warp works
 // it out and passes it on: its divisions and loads would otherwise stand at the start
 // of every unit in every warp.
-struct Unit {
+template <bool BAND>
+struct UnitBand {};
+template <>
+struct UnitBand<true> {
+    int p0, first, last;     // position of query 0; of the unit's queries, held or streamed, that attend keys of it
+    BandWalk<kTileRows> walk;    // held queries
+    __device__ __forceinline__ UnitBand() {}
+};
+template <bool BAND>
+struct Unit : UnitBand<BAND> {
     int index;               // queries held first, then keys held
     int mine, hk, b, bound, lo, n;
     uint4 keys;              // keys held: which rows are attended
     template <bool KEYS>
-    __device__ __forceinline__ void set(const BwdMmaArgs &a, int i) {
+    __device__ __forceinline__ void set(const BwdMmaArgs<BAND> &a, int i) {
         index = i;
+        if constexpr (BAND) set_band<KEYS>(a, KEYS ? i - a.query_units : i);
+        else set_all<KEYS>(a, i);
+    }
+    template <bool KEYS>
+    __device__ __forceinline__ void set_all(const BwdMmaArgs<BAND> &a, int i) {
         const int unit = KEYS ? i - a.query_units : i, held = KEYS ? a.ktiles : a.qt.tiles;
         mine = unit % held;
         hk = unit / held % a.Hkv;
@@ -286,19 +303,57 @@ struct Unit {
         lo = (int)(tiles * rank / CS);
         n = (int)(tiles * (rank + 1) / CS) - lo;
     }
+    // The units with the longest walks first: the last queries, the first keys.
+    template <bool KEYS>
+    __device__ __forceinline__ void set_band(const BwdMmaArgs<BAND> &a, int unit) {
+        const int heads = a.Hkv * a.B;
+        mine = KEYS ? unit / heads : a.qt.tiles - 1 - unit / heads;
+        hk = unit % heads % a.Hkv;
+        b = unit % heads / a.Hkv;
+        bound = a.ks.bound(b);
+        this->p0 = a.band.first(b);
+        keys = make_uint4(0, 0, 0, 0);
+        const int end = min(bound, this->p0 + a.qt.Nq);       // behind the last position of a query
+        int tiles, from = 0;
+        if (KEYS) {
+            const int k0 = mine * kTileRows, k1 = min(k0 + kTileRows, bound) - 1;
+            this->first = max(this->p0, k0);        // (k0 >= 0)
+            this->last = (k0 < a.band.sinks ? end : min(end, k1 + a.band.window)) - 1;
+            const bool some = k0 <= k1 && this->first <= this->last;
+            if (!some) this->last = this->first - 1;
+            from = some ? (this->first - this->p0) / a.qt.nb * a.qt.groups : 0;
+            tiles = some ? ((this->last - this->p0) / a.qt.nb + 1) * a.qt.groups - from : 0;
+            keys = band_keys(a.band, this->first, this->last, k0);
+        } else {
+            this->first = max(0, this->p0 + a.qt.first_row(mine));
+            this->last = min(end, this->p0 + a.qt.first_row(mine) + a.qt.nb) - 1;
+            this->walk = BandWalk<kTileRows>(a.band, this->first, this->last);
+            tiles = this->walk.n;
+        }
+        const int CS = (int)cluster_size(), rank = (int)cluster_rank();
+        lo = (int)((int64_t)tiles * rank / CS);
+        n = (int)((int64_t)tiles * (rank + 1) / CS) - lo;
+        lo += from;
+    }
+    // first key of tile j of held queries' walk
+    __device__ __forceinline__ int key(int j) const {
+        if constexpr (BAND) return this->walk.tile(lo + j) * kTileRows;
+        else return (lo + j) * kTileRows;
+    }
     // the whole warp calls it; an index behind the last unit stands for the end
-    __device__ __forceinline__ void enter(const BwdMmaArgs &a, int i) {
+    __device__ __forceinline__ void enter(const BwdMmaArgs<BAND> &a, int i) {
         if (i < a.query_units) set<false>(a, i);
         else if (i < a.units) set<true>(a, i);
         else index = i, mine = hk = b = bound = lo = n = 0, keys = make_uint4(0, 0, 0, 0);
     }
 };
 
+template <bool BAND>
 struct Shared {
     uint64_t held[2], held_free[2], full[kStages], ready[kStages], empty[kStages], s, sfree, p, done, end[2];
     uint64_t unit_full[2], unit_empty[2];
     uint4 keys[kStages];
-    Unit unit[2];               // the CTA's, in turn
+    Unit<BAND> unit[2];         // the CTA's, in turn
     uint32_t tmem;
     int abort;
 };
@@ -320,8 +375,8 @@ struct Tiles {
 // pipeline completes a phase per tile.
 
 // P and dS: row = lane of the quarter, 32 columns
-template <bool KEYS>
-__device__ __forceinline__ int weights(const BwdMmaArgs &a, Shared &sh, uint8_t *ring, const Unit &u, int it) {
+template <bool KEYS, bool BAND>
+__device__ __forceinline__ int weights(const BwdMmaArgs<BAND> &a, Shared<BAND> &sh, uint8_t *ring, const Unit<BAND> &u, int it) {
     volatile int *abort = &sh.abort;
     const int warp = warp_number(), lane = threadIdx.x & 31;
     const int cg = warp >> 2, r = (warp & 3) * 32 + lane;
@@ -338,6 +393,25 @@ __device__ __forceinline__ int weights(const BwdMmaArgs &a, Shared &sh, uint8_t 
     // keys that are not attended have no gradient, whatever their rows hold
     const uint32_t word = (warp & 3) == 0 ? u.keys.x : (warp & 3) == 1 ? u.keys.y : (warp & 3) == 2 ? u.keys.z : u.keys.w;
     const bool zero = u.n == 0 || (KEYS && !((word >> lane) & 1));
+    // BAND: the row's position, -1 for none (held queries); the tile's; held keys and tiles
+    // of several heads: which columns attend the row's key, the same for all of the walk
+    int p = -1, lowest = 0, highest = 0;
+    uint32_t same = 0;
+    if constexpr (BAND) {
+        if (!KEYS) {
+            lowest = u.p0 + a.qt.first_row(u.mine);
+            highest = u.p0 + min(a.qt.Nq, a.qt.first_row(u.mine) + a.qt.nb) - 1;
+            p = lowest + r % a.qt.nb;
+            if (p >= u.bound) p = -1;
+        } else if (a.qt.nb < kTileRows) {
+            const int k = u.mine * kTileRows + r;
+            for (int i = 0, n = 32 * cg % a.qt.nb; i < 32; ++i) {
+                const int at = u.p0 + n;
+                if (at >= u.first && at <= u.last && a.band.sees(at, k)) same |= 1u << i;
+                if (++n == a.qt.nb) n = 0;
+            }
+        }
+    }
     const float2 cc = make_float2(a.c, a.c);
     for (int j = 0; j < u.n; ++j, ++it) {
         pipe_wait(&sh.s, it & 1, abort);
@@ -351,14 +425,26 @@ __device__ __forceinline__ int weights(const BwdMmaArgs &a, Shared &sh, uint8_t 
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh.sfree);
         uint32_t keep = 0xffffffffu;
-        if (!KEYS && (a.ks.mask || (u.lo + j + 1) * kTileRows > u.bound)) {
+        if constexpr (BAND) {
+            if (KEYS) {
+                const int k0 = u.mine * kTileRows, k = k0 + r, q = a.qt.first_row(u.lo + j), at = u.p0 + q;
+                if (a.qt.nb < kTileRows) keep = same;
+                else if (!(at >= k0 + kTileRows - 1 && at + kTileRows <= min(u.bound, u.p0 + a.qt.Nq) &&
+                           (at + kTileRows - 1 < k0 + a.band.window || k0 + kTileRows <= a.band.sinks)))
+                    keep = queries_of(a.band, k, at + 32 * cg, u.last + 1);
+            } else {
+                const int k0 = u.key(j), k1 = k0 + kTileRows - 1;
+                if (!(k1 <= lowest && highest < u.bound && (k0 > highest - a.band.window || k1 < a.band.sinks)))
+                    keep = keys_of(a.band, p, k0 + 32 * cg);
+            }
+        } else if (!KEYS && (a.ks.mask || (u.lo + j + 1) * kTileRows > u.bound)) {
             const int s = it % kStages;
             pipe_wait(&sh.ready[s], (it / kStages) & 1, abort);     // keys[s] is written
             const uint4 w = sh.keys[s];
             keep = cg == 0 ? w.x : cg == 1 ? w.y : cg == 2 ? w.z : w.w;
         }
         const bool free = it == 0 || pipe_ready(&sh.done, (it - 1) & 1);
-        uint32_t p[16], ds[16];
+        uint32_t p16[16], ds[16];
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
             const float2 sx = make_float2(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1]));
@@ -366,20 +452,23 @@ __device__ __forceinline__ int weights(const BwdMmaArgs &a, Shared &sh, uint8_t 
             const float2 z = KEYS ? mul2(sx, cc) : fma2(sx, cc, make_float2(row_lse, row_lse));
             const float2 w = make_float2(fast_exp2(z.x), fast_exp2(z.y));
             const float2 t = mul2(w, KEYS ? dp : add2(dp, make_float2(row_d, row_d)));
-            if (KEYS) p[i] = pack_bf16x2(w.x, w.y);
+            if (KEYS) p16[i] = pack_bf16x2(w.x, w.y);
             ds[i] = pack_bf16x2(t.x, t.y);
         }
-        if (!KEYS && keep != 0xffffffffu) {
+        if ((BAND || !KEYS) && keep != 0xffffffffu) {
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
-                if (!((keep >> (2 * i)) & 1)) ds[i] &= 0xffff0000u;
-                if (!((keep >> (2 * i + 1)) & 1)) ds[i] &= 0x0000ffffu;
+                uint32_t in = 0xffffffffu;
+                if (!((keep >> (2 * i)) & 1)) in &= 0xffff0000u;
+                if (!((keep >> (2 * i + 1)) & 1)) in &= 0x0000ffffu;
+                ds[i] &= in;
+                if (KEYS) p16[i] &= in;
             }
         }
         // the products have read the last P and dS
         if (!free) pipe_wait(&sh.done, (it - 1) & 1, abort);
         tc_after_sync();
-        if (KEYS) tmem_st16(tmem + kColP + 16 * cg + lanes, p);
+        if (KEYS) tmem_st16(tmem + kColP + 16 * cg + lanes, p16);
         tmem_st16(tmem + kColDs + 16 * cg + lanes, ds);
         tmem_wait_st();
         tc_before_sync();
@@ -428,30 +517,30 @@ __device__ __forceinline__ int weights(const BwdMmaArgs &a, Shared &sh, uint8_t 
 
 // Copies; false: a wait gave up.  `units` counts the units with tiles, whose held
 // rows are in pairs of tiles in turn.
-template <bool KEYS>
-__device__ __forceinline__ bool copies(const BwdMmaArgs &a, Shared &sh, const Tiles &tl, const Unit &u, int &it, int &units) {
+template <bool KEYS, bool BAND>
+__device__ __forceinline__ bool copies(const BwdMmaArgs<BAND> &a, Shared<BAND> &sh, const Tiles &tl, const Unit<BAND> &u, int &it, int &units) {
     volatile int *abort = &sh.abort;
     if (u.n == 0) return true;
     const auto query_tile = [&](uint8_t *dst, int t, uint64_t *bar) {
         load_tile(dst, a.q, a.qt.first_row(t), u.hk * a.qt.G + a.qt.first_head(t), u.b, bar);
         load_tile(dst + kTileBytes, a.g, a.qt.first_row(t), u.hk * a.qt.G + a.qt.first_head(t), u.b, bar);
     };
-    const auto key_tile = [&](uint8_t *dst, int t, uint64_t *bar) {
-        load_tile(dst, a.k, t * kTileRows, u.hk, u.b, bar);
-        load_tile(dst + kTileBytes, a.v, t * kTileRows, u.hk, u.b, bar);
+    const auto key_tile = [&](uint8_t *dst, int k0, uint64_t *bar) {
+        load_tile(dst, a.k, k0, u.hk, u.b, bar);
+        load_tile(dst + kTileBytes, a.v, k0, u.hk, u.b, bar);
     };
     const int pair = units & 1;
     if (units >= 2 && !pipe_wait(&sh.held_free[pair], ((units >> 1) - 1) & 1, abort)) return false;
     if (elect_one()) {
         mbar_expect_tx(&sh.held[pair], 2 * (KEYS ? (uint32_t)kTileBytes : a.qt.bytes()));
-        if (KEYS) key_tile(tl.pair(pair), u.mine, &sh.held[pair]);
+        if (KEYS) key_tile(tl.pair(pair), u.mine * kTileRows, &sh.held[pair]);
         else query_tile(tl.pair(pair), u.mine, &sh.held[pair]);
     }
     __syncwarp();
     ++units;
     const uint32_t bytes = 2 * (KEYS ? a.qt.bytes() + a.qt.bytes() / 8 : (uint32_t)kTileBytes);
     for (int j = 0; j < u.n; ++j) {
-        const int s = it % kStages, t = u.lo + j;
+        const int s = it % kStages, t = u.lo + j;     // of streamed queries
         if (it >= kStages && !pipe_wait(&sh.empty[s], (it / kStages - 1) & 1, abort)) return false;
         if (elect_one()) {
             mbar_expect_tx(&sh.full[s], bytes);
@@ -469,7 +558,7 @@ __device__ __forceinline__ bool copies(const BwdMmaArgs &a, Shared &sh, const Ti
                     bulk_g2s(to + kNarrow, a.d_parts + from, rows * 16, &sh.full[s]);
                 }
             } else {
-                key_tile(tl.stage(s), t, &sh.full[s]);
+                key_tile(tl.stage(s), u.key(j), &sh.full[s]);
             }
         }
         __syncwarp();
@@ -478,20 +567,43 @@ __device__ __forceinline__ bool copies(const BwdMmaArgs &a, Shared &sh, const Ti
     return true;
 }
 
+// Bit r: row r of query tile t is a query of the sequence.  The same in every lane.
+__device__ __forceinline__ uint4 tile_queries(const BwdMmaArgs<true> &a, const Unit<true> &u, int t) {
+    if (a.qt.nb == kTileRows && u.p0 + a.qt.first_row(t) >= 0 &&
+        a.qt.first_row(t) + kTileRows <= min(a.qt.Nq, u.bound - u.p0))
+        return make_uint4(~0u, ~0u, ~0u, ~0u);
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        int g, n;
+        const bool in = a.qt.at(t, 32 * i + (int)(threadIdx.x & 31), g, n);
+        w[i] = __ballot_sync(kFullMask, in && u.p0 + n >= 0 && u.p0 + n < u.bound);
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
 // Which keys of a streamed tile are attended; K's other rows, which are read across
 // with weights of 0, cleared.  Of streamed queries, the rows behind the tile's last,
 // which hold what was there before or the next group's.  false: a wait gave up.
-template <bool KEYS>
-__device__ __forceinline__ bool prepare(const BwdMmaArgs &a, Shared &sh, const Tiles &tl, const Unit &u, int &it) {
+template <bool KEYS, bool BAND>
+__device__ __forceinline__ bool prepare(const BwdMmaArgs<BAND> &a, Shared<BAND> &sh, const Tiles &tl, const Unit<BAND> &u, int &it) {
     volatile int *abort = &sh.abort;
     for (int j = 0; j < u.n; ++j, ++it) {
         const int s = it % kStages;
         uint4 w = make_uint4(0, 0, 0, 0);
         int rows = kTileRows;
-        if (!KEYS) w = tile_keys(a.ks, u.b, (u.lo + j) * kTileRows, u.bound);
+        if constexpr (BAND) w = KEYS ? tile_queries(a, u, u.lo + j) : band_keys(a.band, u.first, u.last, u.key(j));
+        else if (!KEYS) w = tile_keys(a.ks, u.b, u.key(j), u.bound);
         else rows = min(a.qt.gb, a.qt.G - a.qt.first_head(u.lo + j)) * a.qt.nb;
         if (!pipe_wait(&sh.full[s], (it / kStages) & 1, abort)) return false;
-        if (KEYS) {
+        if (BAND && KEYS) {
+            if (!all_keys(w)) {     // queries outside their sequence: a weight of 0 meets no NaN
+                clear_rows(tl.stage(s), w);
+                clear_rows(tl.stage(s) + kTileBytes, w);
+                fence_smem_async();
+                __syncwarp();
+            }
+        } else if (KEYS) {
             if (rows < kTileRows) {
                 uint4 *q = reinterpret_cast<uint4 *>(tl.stage(s));       // 8 a row; dO's behind Q's
                 for (int i = 8 * rows + (int)(threadIdx.x & 31); i < 8 * kTileRows; i += 32)
@@ -526,8 +638,8 @@ struct Turn {   // a place in the ring
 };
 
 // S and dP
-template <bool KEYS>
-__device__ __forceinline__ void scores(const BwdMmaArgs &a, Shared &sh, const Tiles &tl, const Unit &u, int &it, int &units,
+template <bool KEYS, bool BAND>
+__device__ __forceinline__ void scores(const BwdMmaArgs<BAND> &a, Shared<BAND> &sh, const Tiles &tl, const Unit<BAND> &u, int &it, int &units,
                                        Turn &at) {
     volatile int *abort = &sh.abort;
     if (u.n == 0) return;
@@ -562,8 +674,8 @@ __device__ __forceinline__ void scores(const BwdMmaArgs &a, Shared &sh, const Ti
 }
 
 // dQ, or dK and dV
-template <bool KEYS>
-__device__ __forceinline__ void sums(const BwdMmaArgs &a, Shared &sh, const Tiles &tl, const Unit &u, int &it, Turn &at) {
+template <bool KEYS, bool BAND>
+__device__ __forceinline__ void sums(const BwdMmaArgs<BAND> &a, Shared<BAND> &sh, const Tiles &tl, const Unit<BAND> &u, int &it, Turn &at) {
     volatile int *abort = &sh.abort;
     const uint32_t id = mma_desc(128, 64, true), tmem = sh.tmem;
     for (int j = 0; j < u.n; ++j, ++it, at.next()) {
@@ -587,8 +699,8 @@ __device__ __forceinline__ void sums(const BwdMmaArgs &a, Shared &sh, const Tile
 }
 
 // Join of a cluster's partial sums: CTA r finishes every CS-th row.
-template <bool KEYS>
-__device__ __forceinline__ void join(const BwdMmaArgs &a, const Tiles &tl, const Unit &u) {
+template <bool KEYS, bool BAND>
+__device__ __forceinline__ void join(const BwdMmaArgs<BAND> &a, const Tiles &tl, const Unit<BAND> &u) {
     const int CS = (int)cluster_size(), rank = (int)cluster_rank();
     const float *part = reinterpret_cast<const float *>(tl.ring);
     const int c4 = (threadIdx.x & 15) * 4;
@@ -609,10 +721,11 @@ __device__ __forceinline__ void join(const BwdMmaArgs &a, const Tiles &tl, const
     }
 }
 
-__global__ void __launch_bounds__(kThreads, 1) cross_bwd_mma_kernel(const __grid_constant__ BwdMmaArgs a) {
+template <bool BAND>
+__global__ void __launch_bounds__(kThreads, 1) cross_bwd_mma_kernel(const __grid_constant__ BwdMmaArgs<BAND> a) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
-    __shared__ Shared sh;
+    __shared__ Shared<BAND> sh;
     const Tiles tl(smem);
     const int warp = warp_number(), lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
@@ -660,7 +773,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross_bwd_mma_kernel(const __grid
     // not depend on who works on it).  A cluster has one unit.
     const int CS = (int)cluster_size(), first = a.first_unit + (int)(blockIdx.x / CS);
     const auto each = [&](auto next, auto queries, auto keys) {
-        Unit u = next();
+        Unit<BAND> u = next();
 #pragma unroll 1
         for (; u.index < a.query_units; u = next()) queries(u);
 #pragma unroll 1
@@ -669,7 +782,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross_bwd_mma_kernel(const __grid
     int passed = 0;         // units handed over
     const auto take = [&] {
         const int i = passed & 1;
-        Unit u;
+        Unit<BAND> u;
         const bool ok = pipe_wait(&sh.unit_full[i], (passed >> 1) & 1, &sh.abort);
         u = sh.unit[i];
         u.index = __shfl_sync(kFullMask, ok ? u.index : a.units, 0);
@@ -682,8 +795,8 @@ __global__ void __launch_bounds__(kThreads, 1) cross_bwd_mma_kernel(const __grid
     int it = 0, units = 0;
     if (warp < kWeightWarps) {
         take_registers<kRegsMany>();
-        each(take, [&](const Unit &u) { it = weights<false>(a, sh, tl.ring, u, it); },
-             [&](const Unit &u) { it = weights<true>(a, sh, tl.ring, u, it); });
+        each(take, [&](const Unit<BAND> &u) { it = weights<false, BAND>(a, sh, tl.ring, u, it); },
+             [&](const Unit<BAND> &u) { it = weights<true, BAND>(a, sh, tl.ring, u, it); });
     } else {
         give_registers<kRegsFew>();
         if (warp == kCopyWarp) {
@@ -691,7 +804,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross_bwd_mma_kernel(const __grid
             int drawn = first;
             const auto pass = [&] {      // (its copies being out, the next unit's number has come meanwhile)
                 const int i = passed & 1;
-                Unit u;
+                Unit<BAND> u;
                 u.enter(a, __shfl_sync(kFullMask, drawn, 0));
                 drawn = a.units;
                 if (CS == 1 && lane == 0 && u.index < a.units) drawn = a.first_unit + (int)gridDim.x + atomicAdd(a.next_unit, 1);
@@ -705,23 +818,23 @@ __global__ void __launch_bounds__(kThreads, 1) cross_bwd_mma_kernel(const __grid
                 ++passed;
                 return u;
             };
-            each(pass, [&](const Unit &u) { ok = ok && copies<false>(a, sh, tl, u, it, units); },
-                 [&](const Unit &u) { ok = ok && copies<true>(a, sh, tl, u, it, units); });
+            each(pass, [&](const Unit<BAND> &u) { ok = ok && copies<false, BAND>(a, sh, tl, u, it, units); },
+                 [&](const Unit<BAND> &u) { ok = ok && copies<true, BAND>(a, sh, tl, u, it, units); });
             if (lane == 0) {   // leave no copy in flight
                 for (int i = max(0, units - 2); i < units; ++i) mbar_drain(&sh.held[i & 1], (i >> 1) & 1);
                 for (int i = max(0, it - kStages); i < it; ++i) mbar_drain(&sh.full[i % kStages], (i / kStages) & 1);
             }
         } else if (warp == kPrepWarp) {
             bool ok = true;
-            each(take, [&](const Unit &u) { ok = ok && prepare<false>(a, sh, tl, u, it); },
-                 [&](const Unit &u) { ok = ok && prepare<true>(a, sh, tl, u, it); });
+            each(take, [&](const Unit<BAND> &u) { ok = ok && prepare<false, BAND>(a, sh, tl, u, it); },
+                 [&](const Unit<BAND> &u) { ok = ok && prepare<true, BAND>(a, sh, tl, u, it); });
         } else {
             Turn at;
             if (warp == kScoreWarp)
-                each(take, [&](const Unit &u) { scores<false>(a, sh, tl, u, it, units, at); },
-                     [&](const Unit &u) { scores<true>(a, sh, tl, u, it, units, at); });
+                each(take, [&](const Unit<BAND> &u) { scores<false, BAND>(a, sh, tl, u, it, units, at); },
+                     [&](const Unit<BAND> &u) { scores<true, BAND>(a, sh, tl, u, it, units, at); });
             else
-                each(take, [&](const Unit &u) { sums<false>(a, sh, tl, u, it, at); }, [&](const Unit &u) { sums<true>(a, sh, tl, u, it, at); });
+                each(take, [&](const Unit<BAND> &u) { sums<false, BAND>(a, sh, tl, u, it, at); }, [&](const Unit<BAND> &u) { sums<true, BAND>(a, sh, tl, u, it, at); });
             // no matrix instruction in flight when the tensor memory is freed
             uint64_t *end = &sh.end[warp == kSumWarp];
             if (elect_one()) mma_commit(end);
@@ -735,10 +848,10 @@ __global__ void __launch_bounds__(kThreads, 1) cross_bwd_mma_kernel(const __grid
     if (warp == kSumWarp) tmem_free(sh.tmem, kCols);
     if (CS == 1) return;
     cluster_sync();
-    Unit u;
+    Unit<BAND> u;
     u.enter(a, first);
-    if (first < a.query_units) join<false>(a, tl, u);
-    else join<true>(a, tl, u);
+    if (first < a.query_units) join<false, BAND>(a, tl, u);
+    else join<true, BAND>(a, tl, u);
     cluster_sync();   // the others may still read this CTA's part
 }
 
@@ -752,15 +865,19 @@ size_t cross_bwd_mma_workspace(int B, int Hq, int Nq) {
     return 2 * (rows + kTileRows) * sizeof(uint4) + (size_t)B * Hq * Nq * sizeof(float2) + 2 * sizeof(int);
 }
 
-cudaError_t launch_cross_bwd_mma(const CrossArgs &a) {
-    BwdMmaArgs f;
-    f.qt = QueryTiles(a.Hq / a.Hkv, a.Nq, a.Hq > 1 && (a.Q.stride_h == 0 || a.dO.stride_h == 0));
+namespace {
+
+template <bool BAND>
+cudaError_t bwd(const CrossArgs &a) {
+    BwdMmaArgs<BAND> f;
+    f.qt = TilesOf<BAND>(a.Hq / a.Hkv, a.Nq, a.Hq > 1 && (a.Q.stride_h == 0 || a.dO.stride_h == 0));
     if (!make_tensor(&f.q, a.Q, a.B, a.Hq, a.Nq, f.qt.nb, f.qt.gb) ||
         !make_tensor(&f.g, a.dO, a.B, a.Hq, a.Nq, f.qt.nb, f.qt.gb) ||
         !make_tensor(&f.k, a.K, a.B, a.Hkv, a.Nk, kTileRows, 1) ||
         !make_tensor(&f.v, a.V, a.B, a.Hkv, a.Nk, kTileRows, 1))
         return cudaErrorInvalidValue;
     f.ks = a.keys;
+    f.band = a.band;
     f.npad = padded_rows(a.Nq);
     const int64_t rows = (int64_t)a.B * a.Hq * f.npad;
     uint4 *lse_parts = reinterpret_cast<uint4 *>(a.stats), *d_parts = lse_parts + rows + kTileRows;
@@ -774,9 +891,9 @@ cudaError_t launch_cross_bwd_mma(const CrossArgs &a) {
     f.scale = a.scale;
     // a scale of 0: any c this small leaves every finite score's weight at exp2(-LSE log2 e)
     f.c = std::copysign(std::max(std::fabs(a.scale) * kLog2e, 1e-36f), a.scale);
-    cudaError_t e = prepare_kernel<cross_bwd_mma_kernel>(kSmem, kRegs);
+    cudaError_t e = prepare_kernel<cross_bwd_mma_kernel<BAND>>(kSmem, kRegs);
     if (e != cudaSuccess) return e;
-    if (a.Nk <= kFewKeys) {
+    if (!BAND && a.Nk <= kFewKeys) {
         const int64_t warps = (int64_t)a.B * a.Hq * ((f.npad + 15) / 16) + kTileRows / 16;
         e = launch_clusters(cross_parts_few_kernel, (unsigned)((warps + kFewWarps - 1) / kFewWarps), 1, 32 * kFewWarps, 0,
                             a.stream, a.Hq, a.Hkv, a.Nq, f.npad, (unsigned)(a.B * a.Hq), a.keys,
@@ -784,7 +901,7 @@ cudaError_t launch_cross_bwd_mma(const CrossArgs &a) {
                             rows_of<const __nv_bfloat16>(a.V), rows_of<const __nv_bfloat16>(a.dO),
                             static_cast<const float *>(a.LSE), f.c, stats, lse_parts, d_parts, f.next_unit);
     } else {
-        const auto kernel = a.keys.len ? cross_parts_kernel<true> : cross_parts_kernel<false>;
+        const auto kernel = !BAND && a.keys.len ? cross_parts_kernel<true> : cross_parts_kernel<false>;
         e = launch_clusters(kernel, (unsigned)((rows + kTileRows + 31) / 32), 1, 256, 0, a.stream, a.Hq, a.Hkv, a.Nq, f.npad,
                             (unsigned)rows, a.keys, rows_of<const __nv_bfloat16>(a.Q), rows_of<const __nv_bfloat16>(a.K),
                             rows_of<const __nv_bfloat16>(a.V), rows_of<const __nv_bfloat16>(a.O),
@@ -799,17 +916,26 @@ cudaError_t launch_cross_bwd_mma(const CrossArgs &a) {
         f.first_unit = (int)from;
         f.units = (int)(from + units);
         const int64_t grid = c > 1 ? units * c : std::min<int64_t>(units, sm_count());
-        return launch_clusters(cross_bwd_mma_kernel, (unsigned)grid, c, kThreads, kSmem, a.stream, f);
+        return launch_clusters(cross_bwd_mma_kernel<BAND>, (unsigned)grid, c, kThreads, kSmem, a.stream, f);
     };
     // (one head, 100 queries on 16385 keys: 27 us in two launches, 82 in one; 16 heads, 100 on 5000:
     // 44 and 36)
-    const Launches l(query_units, f.ktiles, key_units, f.qt.tiles, sm_count(), 5, 12);
+    int64_t query_walk = f.ktiles, key_walk = f.qt.tiles;
+    if constexpr (BAND) {      // tiles that hold the windows of a tile's rows, and the sinks
+        query_walk = std::min<int64_t>(query_walk, ((int64_t)a.band.window + f.qt.nb) / kTileRows + 1 + (a.band.sinks + kTileRows - 1) / kTileRows);
+        if (a.band.sinks == 0) key_walk = std::min<int64_t>(key_walk, (((int64_t)a.band.window + kTileRows) / f.qt.nb + 2) * f.qt.groups);
+    }
+    const Launches l(query_units, query_walk, key_units, key_walk, sm_count(), 5, 12);
     if (!l.two) return launch(0, query_units + key_units, l.c);
     e = launch(0, query_units, l.c_query);
     if (e != cudaSuccess) return e;
     ++f.next_unit;
     return launch(query_units, key_units, l.c_key);
 }
+
+}  // namespace
+
+cudaError_t launch_cross_bwd_mma(const CrossArgs &a) { return a.banded ? bwd<true>(a) : bwd<false>(a); }
 
 FIBATT_DEFINE_ERROR_READER(read_error_cross_mma_bwd, "cross_mma_bwd.cu")
 

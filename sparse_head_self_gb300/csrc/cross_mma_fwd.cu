@@ -65,9 +65,10 @@ struct Cfg {
     static_assert(NT * kTileRows * kJoinLd * 4 <= NT * kTileBytes + kStages * 2 * kTileBytes, "partial O fits");
 };
 
+template <bool BAND>
 struct FwdMmaArgs {
     TensorArg q, k, v;
-    QueryTiles qt;
+    TilesOf<BAND> qt;
     KeySet ks;
     Rows<__nv_bfloat16> O;
     float *LSE;
@@ -76,35 +77,63 @@ struct FwdMmaArgs {
     int units;               // of all heads and sequences
     float c;                 // |scale| log2 e (> 0)
     int negative;            // scale < 0
+    Band band;               // BAND
     FwdMmaArgs() : qt(1, 1, false) {}
 };
 
 // One unit of work: NT query tiles of one key/value head, ...
-template <int NT>
+template <int NT, bool BAND>
 struct Place {
     int t0, nt, hk, b;
     __device__ __forceinline__ Place() {}
-    __device__ __forceinline__ Place(const FwdMmaArgs &a, int unit) {
-        t0 = unit % a.pairs * NT;
-        hk = unit / a.pairs % a.Hkv;
-        b = unit / a.pairs / a.Hkv;
+    __device__ __forceinline__ Place(const FwdMmaArgs<BAND> &a, int unit) {
+        if constexpr (BAND) {      // the last queries, which attend the most keys, first
+            const int heads = a.units / a.pairs;
+            t0 = (a.pairs - 1 - unit / heads) * NT;
+            hk = unit % heads % a.Hkv;
+            b = unit % heads / a.Hkv;
+        } else {
+            t0 = unit % a.pairs * NT;
+            hk = unit / a.pairs % a.Hkv;
+            b = unit / a.pairs / a.Hkv;
+        }
         nt = min(NT, a.qt.tiles - t0);      // tiles of this unit
     }
 };
 // ... and the part of its sequence's key tiles that this CTA of the cluster walks
 // over.  CTAs that walk over their units have them from the copying warp.
-template <int NT>
-struct Unit : Place<NT> {
+template <int NT, bool BAND>
+struct Unit : Place<NT, BAND> {
     int bound, lo, n;
     __device__ __forceinline__ Unit() {}
-    __device__ __forceinline__ Unit(const FwdMmaArgs &a, const Place<NT> &p) : Place<NT>(p) { set(a); }
-    __device__ __forceinline__ void set(const FwdMmaArgs &a) {
-        const Place<NT> &p = *this;
-        bound = a.ks.bound(p.b);
+    __device__ __forceinline__ Unit(const FwdMmaArgs<BAND> &a, const Place<NT, BAND> &p) : Place<NT, BAND>(p) { set(a); }
+    __device__ __forceinline__ void set(const FwdMmaArgs<BAND> &a) {
+        bound = a.ks.bound(this->b);
         const int ktiles = (bound + kTileRows - 1) / kTileRows, CS = (int)cluster_size(), rank = (int)cluster_rank();
         lo = (int)((int64_t)ktiles * rank / CS);
         n = (int)((int64_t)ktiles * (rank + 1) / CS) - lo;
     }
+    // first key of its tile j
+    __device__ __forceinline__ int key(int j) const { return (lo + j) * kTileRows; }
+};
+template <int NT>
+struct Unit<NT, true> : Place<NT, true> {
+    int bound, lo, n;
+    int p0, first, last;            // position of query 0; of the first and the last of this unit's that attend keys
+    BandWalk<kTileRows> walk;
+    __device__ __forceinline__ Unit() {}
+    __device__ __forceinline__ Unit(const FwdMmaArgs<true> &a, const Place<NT, true> &p) : Place<NT, true>(p) { set(a); }
+    __device__ __forceinline__ void set(const FwdMmaArgs<true> &a) {
+        bound = a.ks.bound(this->b);
+        p0 = a.band.first(this->b);
+        first = max(0, p0 + a.qt.first_row(this->t0));
+        last = min(bound, p0 + min(a.qt.Nq, a.qt.first_row(this->t0 + this->nt - 1) + a.qt.nb)) - 1;
+        walk = BandWalk<kTileRows>(a.band, first, last);
+        const int CS = (int)cluster_size(), rank = (int)cluster_rank();
+        lo = (int)((int64_t)walk.n * rank / CS);
+        n = (int)((int64_t)walk.n * (rank + 1) / CS) - lo;
+    }
+    __device__ __forceinline__ int key(int j) const { return walk.tile(lo + j) * kTileRows; }
 };
 
 // A named barrier of `threads` threads (whole warps), and whether `p` holds in all of them.
@@ -117,17 +146,19 @@ __device__ __forceinline__ bool all_of(int id, int threads, bool p) {
     return r != 0;
 }
 
-template <int NT>
+template <int NT, bool BAND>
 __global__ void __launch_bounds__(Cfg<NT>::kThreads, Cfg<NT>::kMinBlocks)
-cross_fwd_mma_kernel(const __grid_constant__ FwdMmaArgs a) {
+cross_fwd_mma_kernel(const __grid_constant__ FwdMmaArgs<BAND> a) {
     using C = Cfg<NT>;
+    using Work = Unit<NT, BAND>;
+    using Where = Place<NT, BAND>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
     uint8_t *sq = smem, *skv = smem + NT * kTileBytes;   // stage s: K at skv + 2 s tiles, V behind it
     __shared__ uint64_t bar_q, bar_qfree, bar_full[C::kStages], bar_ready[C::kStages], bar_empty[C::kStages];
     __shared__ uint64_t bar_s[NT], bar_sfree[NT], bar_p[NT], bar_o[NT], bar_end[2];
     __shared__ uint64_t bar_unit[2], bar_unitfree[2];
-    __shared__ Unit<NT> units[2];       // of a CTA that walks, in turn; n < 0: no more
+    __shared__ Work units[2];       // of a CTA that walks, in turn; n < 0: no more
     __shared__ uint4 keys[C::kStages];
     __shared__ uint32_t tmem_base;
     __shared__ int abort_flag;
@@ -140,7 +171,7 @@ cross_fwd_mma_kernel(const __grid_constant__ FwdMmaArgs a) {
     const int CS = (int)cluster_size(), rank = (int)cluster_rank();
     // the CTA's units: a cluster has one, the CTAs of one wave walk over all of them
     const int first = (int)(blockIdx.x / CS), step = (int)(gridDim.x / CS);
-    const Place<NT> first_place(a, first);
+    const Where first_place(a, first);
 
     if (threadIdx.x == 0) {
         mbar_init(&bar_q, 1);
@@ -191,7 +222,7 @@ cross_fwd_mma_kernel(const __grid_constant__ FwdMmaArgs a) {
                 if (lane == 0) mbar_arrive(&bar_unitfree[k & 1]);
             }
         } else {
-            body(Unit<NT>(a, first_place));
+            body(Work(a, first_place));
         }
     };
     // `ring` counts the key tiles over all units of the CTA: tile `ring` is in stage
@@ -208,12 +239,20 @@ cross_fwd_mma_kernel(const __grid_constant__ FwdMmaArgs a) {
         const uint32_t ts = col_s + t * 128 + 64 * half + lanes, tp = col_p + t * 64 + 32 * half + lanes;
         const uint32_t to = col_o + t * 64 + 32 * half + lanes;
         int it = 0, skipped = 0;
-        each([&](const Unit<NT> &u) {
+        each([&](const Work &u) {
             if (t >= u.nt) {
                 skipped += u.n;
                 return;
             }
             const int n = u.n, whole = a.ks.mask ? 0 : u.bound / kTileRows - u.lo;   // the tiles attended wholly come first
+            int p = -1, lowest = 0, highest = 0;     // positions: of the row, of the tile's rows
+            if constexpr (BAND) {
+                const int q = a.qt.first_row(u.t0 + t);
+                lowest = u.p0 + q;
+                highest = u.p0 + min(a.qt.Nq, q + a.qt.nb) - 1;
+                p = lowest + r % a.qt.nb;
+                if (p >= u.bound) p = -1;
+            }
             float m = kNegInf, l = 0.f;
             uint32_t o[32];
             for (int j = 0; j < n; ++j, ++it) {
@@ -227,7 +266,18 @@ cross_fwd_mma_kernel(const __grid_constant__ FwdMmaArgs a) {
                 tc_before_sync();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bar_sfree[t]);
-                if (j >= whole) {
+                if constexpr (BAND) {
+                    const int k0 = u.key(j), k1 = k0 + kTileRows - 1;
+                    const bool all = k1 <= lowest && highest < u.bound && (k0 > highest - a.band.window || k1 < a.band.sinks);
+                    if (!all) {
+                        const uint32_t words[2] = {keys_of(a.band, p, k0 + 64 * half), keys_of(a.band, p, k0 + 64 * half + 32)};
+#pragma unroll
+                        for (int i = 0; i < 2; ++i)
+#pragma unroll
+                            for (int k = 0; k < 32; ++k)
+                                if (!((words[i] >> k) & 1)) s[i][k] = __float_as_uint(kNegInf);
+                    }
+                } else if (j >= whole) {
                     const int ring = it + skipped, st = ring % C::kStages;
                     pipe_wait(&bar_ready[st], (ring / C::kStages) & 1, abort);   // keys[st] is written
                     const uint4 w = keys[st];
@@ -337,7 +387,7 @@ cross_fwd_mma_kernel(const __grid_constant__ FwdMmaArgs a) {
             // ---- copies: they run ahead into the next unit ------------------------------
             int ring = 0, loaded = 0;      // issued: key tiles, units' queries
             bool ok = true;
-            const auto queries = [&](const Unit<NT> &u) {
+            const auto queries = [&](const Work &u) {
                 if (elect_one()) {
                     mbar_expect_tx(&bar_q, u.nt * a.qt.bytes());
                     for (int t = 0; t < u.nt; ++t)
@@ -347,7 +397,7 @@ cross_fwd_mma_kernel(const __grid_constant__ FwdMmaArgs a) {
                 __syncwarp();
                 ++loaded;
             };
-            const auto copies = [&](const Unit<NT> &u) {
+            const auto copies = [&](const Work &u) {
                 const bool later = C::kWalks && loaded > 0;
                 for (int j = 0; ok && j < u.n; ++j) {
                     if (j == 0 && !later) queries(u);
@@ -356,8 +406,8 @@ cross_fwd_mma_kernel(const __grid_constant__ FwdMmaArgs a) {
                     if (!ok) break;
                     if (elect_one()) {
                         mbar_expect_tx(&bar_full[s], 2 * kTileBytes);
-                        load_tile(skv + (2 * s) * kTileBytes, a.k, (u.lo + j) * kTileRows, u.hk, u.b, &bar_full[s]);
-                        load_tile(skv + (2 * s + 1) * kTileBytes, a.v, (u.lo + j) * kTileRows, u.hk, u.b, &bar_full[s]);
+                        load_tile(skv + (2 * s) * kTileBytes, a.k, u.key(j), u.hk, u.b, &bar_full[s]);
+                        load_tile(skv + (2 * s + 1) * kTileBytes, a.v, u.key(j), u.hk, u.b, &bar_full[s]);
                     }
                     __syncwarp();
                     ++ring;
@@ -370,8 +420,8 @@ cross_fwd_mma_kernel(const __grid_constant__ FwdMmaArgs a) {
             if constexpr (C::kWalks) {
 #pragma unroll 1
                 for (int k = 0, unit = first; ok; ++k, unit += step) {
-                    Unit<NT> u;
-                    if (unit < a.units) u = Unit<NT>(a, k ? Place<NT>(a, unit) : first_place);
+                    Work u;
+                    if (unit < a.units) u = Work(a, k ? Where(a, unit) : first_place);
                     else u.n = -1;
                     ok = k < 2 || pipe_wait(&bar_unitfree[k & 1], ((k >> 1) - 1) & 1, abort);
                     if (!ok) break;
@@ -384,7 +434,7 @@ cross_fwd_mma_kernel(const __grid_constant__ FwdMmaArgs a) {
                     copies(u);
                 }
             } else {
-                copies(Unit<NT>(a, first_place));
+                copies(Work(a, first_place));
             }
             // leave no copy in flight
             if (lane == 0) {
@@ -396,11 +446,13 @@ cross_fwd_mma_kernel(const __grid_constant__ FwdMmaArgs a) {
             // ---- which keys of each tile are attended; the others' value rows cleared ----
             int ring = 0;
             bool ok = true;
-            each([&](const Unit<NT> &u) {
+            each([&](const Work &u) {
                 const int n = u.n;
                 for (int j = 0; ok && j < n; ++j, ++ring) {
                     const int s = ring % C::kStages;
-                    const uint4 w = tile_keys(a.ks, u.b, (u.lo + j) * kTileRows, u.bound);
+                    uint4 w;
+                    if constexpr (BAND) w = band_keys(a.band, u.first, u.last, u.key(j));
+                    else w = tile_keys(a.ks, u.b, u.key(j), u.bound);
                     ok = pipe_wait(&bar_full[s], (ring / C::kStages) & 1, abort);
                     if (!ok) break;
                     if (!all_keys(w)) {
@@ -426,7 +478,7 @@ cross_fwd_mma_kernel(const __grid_constant__ FwdMmaArgs a) {
                 const uint32_t id = mma_desc(128, 128, false, a.negative);
                 const uint64_t dq = tile_desc(sq), dk = tile_desc(skv);
                 int loaded = 0;
-                each([&](const Unit<NT> &u) {
+                each([&](const Work &u) {
                     const int n = __shfl_sync(kFullMask, u.n, 0), nt = __shfl_sync(kFullMask, u.nt, 0);
                     if (n > 0) pipe_wait(&bar_q, loaded++ & 1, abort);
                     for (int j = 0; j < n; ++j) {
@@ -457,7 +509,7 @@ cross_fwd_mma_kernel(const __grid_constant__ FwdMmaArgs a) {
             } else {
                 const uint32_t id = mma_desc(128, 64, true);
                 const uint64_t dv = tile_desc(skv + kTileBytes);
-                each([&](const Unit<NT> &u) {
+                each([&](const Work &u) {
                     const int n = __shfl_sync(kFullMask, u.n, 0), nt = __shfl_sync(kFullMask, u.nt, 0);
                     for (int j = 0; j < n; ++j) {
                         pipe_wait(&bar_ready[s], pass, abort);
@@ -499,7 +551,7 @@ cross_fwd_mma_kernel(const __grid_constant__ FwdMmaArgs a) {
 
     // ---- join: CTA r of the cluster finishes every CS-th row ------------------------
     cluster_sync();
-    const Unit<NT> u(a, first_place);
+    const Work u(a, first_place);
     const float *part = reinterpret_cast<const float *>(smem);
     const int groups = C::kThreads / 16, c4 = (threadIdx.x & 15) * 4;
     for (int i = rank + CS * (int)(threadIdx.x >> 4); i < u.nt * kTileRows; i += CS * groups) {
@@ -528,13 +580,13 @@ cross_fwd_mma_kernel(const __grid_constant__ FwdMmaArgs a) {
 }
 
 // How many clusters of 2^i CTAs device `dev`, the current one, holds at once.
-template <int NT>
+template <int NT, bool BAND>
 int held_clusters(int dev, int i) {
     using C = Cfg<NT>;
     static PerDevice known[5];
     return known[i].get(dev, [=] {
         return i == 0 ? C::kMinBlocks * sm_count()
-                      : clusters_held<cross_fwd_mma_kernel<NT>>(1 << i, C::kThreads, C::kSmem);
+                      : clusters_held<cross_fwd_mma_kernel<NT, BAND>>(1 << i, C::kThreads, C::kSmem);
     });
 }
 
@@ -552,15 +604,19 @@ struct Plan {
     int nt = 0, c = 1;
     float cost = 0.f;
 };
-template <int NT>
-cudaError_t consider(const CrossArgs &a, const QueryTiles &qt, Plan *best) {
+template <int NT, bool BAND>
+cudaError_t consider(const CrossArgs &a, const TilesOf<BAND> &qt, Plan *best) {
     using C = Cfg<NT>;
-    const cudaError_t e = prepare_kernel<cross_fwd_mma_kernel<NT>>(C::kSmem, C::kRegs);
+    const cudaError_t e = prepare_kernel<cross_fwd_mma_kernel<NT, BAND>>(C::kSmem, C::kRegs);
     if (e != cudaSuccess) return e;
     const int64_t units = (int64_t)a.B * a.Hkv * ((qt.tiles + NT - 1) / NT);
-    const int tiles = (a.Nk + kTileRows - 1) / kTileRows, dev = current_device();
+    int tiles = (a.Nk + kTileRows - 1) / kTileRows;
+    const int dev = current_device();
+    if constexpr (BAND)      // of the windows of a unit's rows, and of the sinks
+        tiles = (int)std::min<int64_t>(tiles, ((int64_t)a.band.window + (NT / qt.groups + 1) * qt.nb) / kTileRows + 1 +
+                                                  (a.band.sinks + kTileRows - 1) / kTileRows);
     for (int i = 0; i < 5 && (i == 0 || tiles >= 1 << i); ++i) {
-        const int c = 1 << i, held = held_clusters<NT>(dev, i);
+        const int c = 1 << i, held = held_clusters<NT, BAND>(dev, i);
         if (held < 1) break;
         const float tile = NT == 2 ? (qt.tiles > 1 ? 1.f : 0.78f) : units * c > sm_count() ? 1.28f : 0.83f;
         const float rounds = (float)((units + held - 1) / held), mine = (float)((tiles + c - 1) / c) * tile;
@@ -572,15 +628,16 @@ cudaError_t consider(const CrossArgs &a, const QueryTiles &qt, Plan *best) {
     return cudaSuccess;
 }
 
-template <int NT>
-cudaError_t fwd(const CrossArgs &a, const QueryTiles &qt, int c) {
+template <int NT, bool BAND>
+cudaError_t fwd(const CrossArgs &a, const TilesOf<BAND> &qt, int c) {
     using C = Cfg<NT>;
-    FwdMmaArgs f;
+    FwdMmaArgs<BAND> f;
     f.qt = qt;
     if (!make_tensor(&f.q, a.Q, a.B, a.Hq, a.Nq, qt.nb, qt.gb) || !make_tensor(&f.k, a.K, a.B, a.Hkv, a.Nk, kTileRows, 1) ||
         !make_tensor(&f.v, a.V, a.B, a.Hkv, a.Nk, kTileRows, 1))
         return cudaErrorInvalidValue;
     f.ks = a.keys;
+    f.band = a.band;
     f.O = rows_of<__nv_bfloat16>(a.O);
     f.LSE = a.LSE;
     f.Hq = a.Hq, f.Hkv = a.Hkv;
@@ -592,19 +649,22 @@ cudaError_t fwd(const CrossArgs &a, const QueryTiles &qt, int c) {
     const int64_t units = (int64_t)a.B * a.Hkv * f.pairs;
     f.units = (int)units;
     const int64_t grid = c > 1 || !C::kWalks ? units * c : std::min<int64_t>(units, C::kMinBlocks * sm_count());
-    return launch_clusters(cross_fwd_mma_kernel<NT>, (unsigned)grid, c, C::kThreads, C::kSmem, a.stream, f);
+    return launch_clusters(cross_fwd_mma_kernel<NT, BAND>, (unsigned)grid, c, C::kThreads, C::kSmem, a.stream, f);
+}
+
+template <bool BAND>
+cudaError_t launch(const CrossArgs &a) {
+    const TilesOf<BAND> qt(a.Hq / a.Hkv, a.Nq, a.Hq > 1 && a.Q.stride_h == 0);
+    Plan plan;
+    cudaError_t e = consider<1, BAND>(a, qt, &plan);
+    if (e == cudaSuccess) e = consider<2, BAND>(a, qt, &plan);
+    if (e != cudaSuccess) return e;
+    return plan.nt == 2 ? fwd<2, BAND>(a, qt, plan.c) : fwd<1, BAND>(a, qt, plan.c);
 }
 
 }  // namespace
 
-cudaError_t launch_cross_fwd_mma(const CrossArgs &a) {
-    const QueryTiles qt(a.Hq / a.Hkv, a.Nq, a.Hq > 1 && a.Q.stride_h == 0);
-    Plan plan;
-    cudaError_t e = consider<1>(a, qt, &plan);
-    if (e == cudaSuccess) e = consider<2>(a, qt, &plan);
-    if (e != cudaSuccess) return e;
-    return plan.nt == 2 ? fwd<2>(a, qt, plan.c) : fwd<1>(a, qt, plan.c);
-}
+cudaError_t launch_cross_fwd_mma(const CrossArgs &a) { return a.banded ? launch<true>(a) : launch<false>(a); }
 
 FIBATT_DEFINE_ERROR_READER(read_error_cross_mma_fwd, "cross_mma_fwd.cu")
 

@@ -67,16 +67,21 @@ struct RowsArgs {
     KeySet ks;
     float *LSE;
     float c;
+    Band band;           // BAND
 };
 
-// What both kernels have around their products.
-template <int R, int KEYS>
+// What both kernels have around their products.  BAND: the keys are those of the sinks, rounded
+// up to 32, with the windows' behind them; a CTA has a contiguous part of that, in
+// stages of one or the other.
+template <int R, int KEYS, bool BAND>
 struct Part {
     const RowsArgs &a;
     uint8_t *ring;
     uint64_t *full, *empty;
     volatile int *abort;
     int hk, b, G, rank, C, bound, lo, hi, stages;
+    int p0, last;                        // BAND: positions of query 0 and of the last that attends keys;
+    int sink_stages, first_sink, sink_end, oldest;   // the sinks' part: stages and keys; the windows' first key
 
     __device__ __forceinline__ Part(const RowsArgs &a, uint8_t *smem_raw, uint64_t *full, uint64_t *empty, int *abort_flag)
         : a(a), full(full), empty(empty), abort(abort_flag) {
@@ -100,10 +105,40 @@ struct Part {
         grid_dep_wait();
         grid_dep_launch();
         bound = a.ks.bound(b);
+        if constexpr (BAND) {
+            p0 = a.band.first(b);
+            last = min(bound, p0 + a.Nq) - 1;
+            const int first = max(0, p0);
+            oldest = max(0, first - a.band.window + 1);
+            sink_end = min(a.band.sinks, oldest);
+            const int sinks = (sink_end + 31) / 32 * 32, keys = first <= last ? sinks + last + 1 - oldest : 0;
+            const int per = ((keys + C - 1) / C + 31) / 32 * 32;
+            const int from = (int)min((int64_t)keys, (int64_t)per * rank), to = min(keys, from + per);
+            // the part within the sinks, then lo and hi: that within the windows
+            sink_end = min(sink_end, to);
+            lo = min(from, sinks);
+            sink_stages = sink_end > lo ? (sink_end - lo + KEYS - 1) / KEYS : 0;
+            first_sink = lo;
+            lo = oldest + max(0, from - sinks);
+            hi = max(lo, oldest + to - sinks);
+            stages = sink_stages + (hi - lo + KEYS - 1) / KEYS;
+            return;
+        }
         const int per = ((bound + C - 1) / C + 31) / 32 * 32;            // keys of a CTA
         lo = (int)min((int64_t)bound, (int64_t)per * rank);
         hi = min(bound, lo + per);
         stages = (hi - lo + KEYS - 1) / KEYS;
+    }
+    // first key of stage j, and the end of the keys that it is part of
+    __device__ __forceinline__ int key(int j) const {
+        if constexpr (BAND) return j < sink_stages ? first_sink + j * KEYS : lo + (j - sink_stages) * KEYS;
+        else return lo + j * KEYS;
+    }
+    __device__ __forceinline__ int end(int j) const { return BAND && j < sink_stages ? sink_end : hi; }
+    // the position of row r, -1 for none
+    __device__ __forceinline__ int position(int r) const {
+        const int p = p0 + r % a.Nq;
+        return p <= last ? p : -1;
     }
     // the copying warp
     __device__ __forceinline__ void copy() {
@@ -114,8 +149,8 @@ struct Part {
             if (elect_one()) {
                 uint8_t *dst = ring + s * kStageBytes;
                 mbar_expect_tx(&full[s], kStageBytes);
-                load_tile(dst, a.k, lo + j * KEYS, hk, b, &full[s]);
-                load_tile(dst + kStageBytes / 2, a.v, lo + j * KEYS, hk, b, &full[s]);
+                load_tile(dst, a.k, key(j), hk, b, &full[s]);
+                load_tile(dst + kStageBytes / 2, a.v, key(j), hk, b, &full[s]);
             }
             __syncwarp();
         }
@@ -189,7 +224,7 @@ __device__ __forceinline__ void load_matrices(uint32_t (&r)[4], const void *row)
 }
 
 // R: 8 (the products' lower rows are not looked at) or 16.
-template <int R>
+template <int R, bool BAND>
 __global__ void __launch_bounds__(kThreads, 2)
 cross_rows_mma_kernel(const __grid_constant__ RowsArgs a, Rows<const __nv_bfloat16> Q, Rows<__nv_bfloat16> O) {
     constexpr int kKeys = 128, kHalves = R / 8;
@@ -199,7 +234,7 @@ cross_rows_mma_kernel(const __grid_constant__ RowsArgs a, Rows<const __nv_bfloat
     __shared__ float sm[kWarps][R], sl[kWarps][R];
     __shared__ float cm[R], cl[R];            // the CTA's, read by the cluster
     __shared__ float2 co[R][32];
-    Part<R, kKeys> p(a, smem_raw, full, empty, &abort_flag);
+    Part<R, kKeys, BAND> p(a, smem_raw, full, empty, &abort_flag);
     const int warp = warp_number(), lane = threadIdx.x & 31, row = lane >> 2, pair = lane & 3;
 
     float m[kHalves], l[kHalves], o[8][4];
@@ -227,11 +262,14 @@ cross_rows_mma_kernel(const __grid_constant__ RowsArgs a, Rows<const __nv_bfloat
                 q[k][2 + i] = src ? __ldg(src + 8 * k + 4 + pair) : 0u;
             }
         }
+        int at[kHalves];                      // BAND: the rows' positions
+#pragma unroll
+        for (int i = 0; i < kHalves; ++i) at[i] = BAND && row + 8 * i < a.rows ? p.position(row + 8 * i) : -1;
         for (int j = 0; j < p.stages; ++j) {
-            const int st = j % kStages, k0 = p.lo + j * kKeys + 16 * warp;
+            const int st = j % kStages, k0 = p.key(j) + 16 * warp, end = p.end(j);
             const int key = k0 + (lane & 15);
             const uint32_t in =
-                __ballot_sync(kFullMask, key < p.hi && a.ks.has(p.b, min(key, p.hi - 1))) & 0xffffu;
+                __ballot_sync(kFullMask, key < end && (BAND || a.ks.has(p.b, min(key, end - 1)))) & 0xffffu;
             pipe_wait(&full[st], (j / kStages) & 1, p.abort);
             uint8_t *kt = p.ring + st * kStageBytes + 16 * warp * 128, *vt = kt + kStageBytes / 2;
             if (in != 0xffffu && lane < 16 && !((in >> lane) & 1)) {   // a weight of 0 meets no NaN
@@ -259,7 +297,12 @@ cross_rows_mma_kernel(const __grid_constant__ RowsArgs a, Rows<const __nv_bfloat
 #pragma unroll
             for (int i = 0; i < kHalves; ++i) {
                 float x[4] = {s[0][2 * i] * a.c, s[0][2 * i + 1] * a.c, s[1][2 * i] * a.c, s[1][2 * i + 1] * a.c};
-                if (in != 0xffffu) {
+                if constexpr (BAND) {
+                    const uint32_t seen = in & keys_of(a.band, at[i], k0);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        if (!((seen >> (2 * pair + (k & 1) + 8 * (k >> 1))) & 1)) x[k] = kNegInf;
+                } else if (in != 0xffffu) {
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
                         if (!((in >> (2 * pair + (k & 1) + 8 * (k >> 1))) & 1)) x[k] = kNegInf;
@@ -318,7 +361,7 @@ cross_rows_mma_kernel(const __grid_constant__ RowsArgs a, Rows<const __nv_bfloat
 
 // ---- 32 bits ---------------------------------------------------------------------
 // R rows (the last ones may be copies of the last real row).
-template <int R>
+template <int R, bool BAND>
 __global__ void __launch_bounds__(kThreads, R > 4 ? 1 : 2)
 cross_rows_kernel(const __grid_constant__ RowsArgs a, Rows<const float> Q, Rows<float> O) {
     constexpr int kKeys = 64, U = kKeys / kWarps / 4;     // keys of a stage, of a group of lanes
@@ -329,26 +372,28 @@ cross_rows_kernel(const __grid_constant__ RowsArgs a, Rows<const float> Q, Rows<
     __shared__ float2 so[kWarps][R][32];
     __shared__ float cm[R], cl[R];            // the CTA's, read by the cluster
     __shared__ float2 co[R][32];
-    Part<R, kKeys> p(a, smem_raw, full, empty, &abort_flag);
+    Part<R, kKeys, BAND> p(a, smem_raw, full, empty, &abort_flag);
     const int warp = warp_number(), lane = threadIdx.x & 31, sub = lane & 7, grp = lane >> 3;
     if (warp == kWarps) p.copy();
     Share q[R];
     float m[R], l[R];
     float2 acc[R][4];
+    int at[R];                                // BAND: the rows' positions
 #pragma unroll
     for (int r = 0; r < R; ++r) {
         const int i = min(r, a.rows - 1);
         q[r].load(Q.row(p.b, p.hk * p.G + i / a.Nq, i % a.Nq), sub);
+        at[r] = BAND ? p.position(i) : 0;
         m[r] = kNegInf;
         l[r] = 0.f;
 #pragma unroll
         for (int i = 0; i < 4; ++i) acc[r][i] = make_float2(0.f, 0.f);
     }
     for (int j = 0; warp < kWarps && j < p.stages; ++j) {
-        const int st = j % kStages, k0 = p.lo + j * kKeys + warp * 4 * U + grp;
+        const int st = j % kStages, k0 = p.key(j) + warp * 4 * U + grp, end = p.end(j);
         bool in[U];
 #pragma unroll
-        for (int u = 0; u < U; ++u) in[u] = k0 + 4 * u < p.hi && a.ks.has(p.b, min(k0 + 4 * u, p.hi - 1));
+        for (int u = 0; u < U; ++u) in[u] = k0 + 4 * u < end && (BAND || a.ks.has(p.b, min(k0 + 4 * u, end - 1)));
         pipe_wait(&full[st], (j / kStages) & 1, p.abort);
         const float *kr = reinterpret_cast<const float *>(p.ring + st * kStageBytes) + (warp * 4 * U + grp) * 64;
         const float *vr = kr + kKeys * 64;
@@ -371,7 +416,7 @@ cross_rows_kernel(const __grid_constant__ RowsArgs a, Rows<const float> Q, Rows<
             float top = kNegInf;
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                s[r][u] = in[u] ? s[r][u] * a.c : kNegInf;
+                s[r][u] = in[u] && (!BAND || a.band.sees(at[r], k0 + 4 * u)) ? s[r][u] * a.c : kNegInf;
                 top = fmaxf(top, s[r][u]);
             }
             if (top > m[r]) {
@@ -446,15 +491,29 @@ cudaError_t run(const CrossArgs &a, int rows) {
     f.ks = a.keys;
     f.LSE = a.LSE;
     f.c = a.scale * kLog2e;
+    f.band = a.band;
     const cudaError_t e = prepare_kernel<Kernel>(kSmem, 0);
     if (e != cudaSuccess) return e;
     const int64_t units = (int64_t)a.B * a.Hkv;
     // CTAs of a cluster: as many as the GPU holds at once (two a SM), as long as a CTA
     // keeps a stage (64 units: clusters of four 33.6 us, of eight, in two waves, 35.2)
+    const int keys = a.banded ? (int)std::min<int64_t>(a.Nk, (int64_t)a.band.window + a.Nq + a.band.sinks) : a.Nk;
     int c = 1;
-    while (c < 8 && units * c * 2 <= 2 * sm_count() && a.Nk > c * kKeys) c *= 2;
+    while (c < 8 && units * c * 2 <= 2 * sm_count() && keys > c * kKeys) c *= 2;
     return launch_clusters(Kernel, (unsigned)(units * c), c, kThreads, kSmem, a.stream, f, rows_of<const T>(a.Q),
                            rows_of<T>(a.O));
+}
+
+template <bool BAND>
+cudaError_t launch(const CrossArgs &a) {
+    const int rows = a.Hq / a.Hkv * a.Nq;
+    if (a.dtype == FIBATT_F32)
+        return rows == 1   ? run<float, cross_rows_kernel<1, BAND>>(a, rows)
+               : rows == 2 ? run<float, cross_rows_kernel<2, BAND>>(a, rows)
+               : rows <= 4 ? run<float, cross_rows_kernel<4, BAND>>(a, rows)
+                           : run<float, cross_rows_kernel<8, BAND>>(a, rows);
+    return rows <= 8 ? run<__nv_bfloat16, cross_rows_mma_kernel<8, BAND>>(a, rows)
+                     : run<__nv_bfloat16, cross_rows_mma_kernel<16, BAND>>(a, rows);
 }
 
 }  // namespace
@@ -464,16 +523,7 @@ bool cross_rows_takes(const CrossArgs &a) {
     return rows <= (a.dtype == FIBATT_F32 ? 8 : 16) && (int64_t)a.B * a.Hkv < 0x7fffffff / 8;
 }
 
-cudaError_t launch_cross_rows(const CrossArgs &a) {
-    const int rows = a.Hq / a.Hkv * a.Nq;
-    if (a.dtype == FIBATT_F32)
-        return rows == 1   ? run<float, cross_rows_kernel<1>>(a, rows)
-               : rows == 2 ? run<float, cross_rows_kernel<2>>(a, rows)
-               : rows <= 4 ? run<float, cross_rows_kernel<4>>(a, rows)
-                           : run<float, cross_rows_kernel<8>>(a, rows);
-    return rows <= 8 ? run<__nv_bfloat16, cross_rows_mma_kernel<8>>(a, rows)
-                     : run<__nv_bfloat16, cross_rows_mma_kernel<16>>(a, rows);
-}
+cudaError_t launch_cross_rows(const CrossArgs &a) { return a.banded ? launch<true>(a) : launch<false>(a); }
 
 FIBATT_DEFINE_ERROR_READER(read_error_cross_rows, "cross_rows.cu")
 

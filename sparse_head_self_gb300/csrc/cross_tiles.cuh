@@ -2,6 +2,8 @@
 // tiles, which keys of a tile are attended, and the tensor maps.
 #pragma once
 
+#include <type_traits>
+
 #include <cuda.h>
 
 #include "cross.h"
@@ -46,6 +48,25 @@ struct QueryTiles {
 #endif
 };
 
+// The same tiles in another order, that of a window's queries: tile t has the rows
+// of step t / groups and the heads of group t mod groups, so that tiles next to each other
+// attend the same keys, or nearly, and a range of positions is a range of tiles.
+struct BandTiles : QueryTiles {
+    int groups;
+    BandTiles(int G, int Nq, bool shared_rows) : QueryTiles(G, Nq, shared_rows), groups((G + gb - 1) / gb) {}
+#ifdef __CUDACC__
+    __device__ __forceinline__ int first_head(int t) const { return t % groups * gb; }
+    __device__ __forceinline__ int first_row(int t) const { return t / groups * nb; }
+    __device__ __forceinline__ bool at(int t, int r, int &g, int &n) const {
+        g = first_head(t) + r / nb;
+        n = first_row(t) + r % nb;
+        return r < nb * gb && g < G && n < Nq;
+    }
+#endif
+};
+template <bool BAND>
+using TilesOf = std::conditional_t<BAND, BandTiles, QueryTiles>;
+
 // A head tensor as the copies see it.  Heads or sequences with a stride of 0
 // (a broadcast) become a dimension of one element and a coordinate of 0.
 struct TensorArg {
@@ -73,6 +94,16 @@ __device__ __forceinline__ uint4 tile_keys(const KeySet &ks, int b, int n0, int 
         w[i] = __ballot_sync(kFullMask, k < bound && ks.has(b, k));
     }
     return make_uint4(w[0], w[1], w[2], w[3]);
+}
+// Bit k: a query at one of the positions lo to hi attends key n0 + k.
+__device__ __forceinline__ uint4 band_keys(const Band &w, int lo, int hi, int n0) {
+    uint32_t x[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int k0 = n0 + 32 * i;
+        x[i] = lo > hi ? 0u : bits_below(hi + 1 - k0) & (~bits_below(lo + 1 - w.window - k0) | bits_below(w.sinks - k0));
+    }
+    return make_uint4(x[0], x[1], x[2], x[3]);
 }
 __device__ __forceinline__ bool all_keys(const uint4 &w) { return (w.x & w.y & w.z & w.w) == 0xffffffffu; }
 __device__ __forceinline__ bool no_keys(const uint4 &w) { return (w.x | w.y | w.z | w.w) == 0u; }
