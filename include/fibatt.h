@@ -73,6 +73,7 @@ typedef struct fibatt_support *fibatt_support_t;
 
 /* Limits of this build (UNSUPPORTED beyond them). */
 #define FIBATT_HEAD_DIM 64        /* D                                         */
+#define FIBATT_CACHE_PAGE 64      /* tokens of a page of the 8-bit cache       */
 #define FIBATT_MAX_HEADS 64       /* H                                         */
 #define FIBATT_MAX_ENTRIES 1024   /* signed offsets summed over all heads      */
 
@@ -382,6 +383,73 @@ fibatt_status fibatt_window_bwd(const fibatt_window *d, const fibatt_heads *Q, c
                                 const fibatt_heads *dV, void *workspace, size_t ws_bytes,
                                 cudaStream_t stream);
 
+/* ------------------------------------------------- paged cache in 8 bits --- */
+
+/* Keys and values of tokens in 8 bits, in pages of FIBATT_CACHE_PAGE = 64
+ * tokens that a table hands to sequences: token p of sequence b is row p mod 64
+ * of page table[b, p / 64].  A key/value head's part of a page is two pieces of 4096
+ * e4m3 bytes, the keys as [64 tokens][64 dims] and behind them the values as
+ * [64 dims][64 tokens], each with a scale: a byte stands for its e4m3 value
+ * times the scale.  Scales are powers of two from 2^-100 to 2^120 (what else stands
+ * there is read as the power of two at or below its size, within those bounds, NaN and
+ * infinities as the largest).
+ *
+ * A call has N tokens of every sequence, token n of them at position
+ * start[b] + n (n when start is NULL); of sequence b the first count[b] count (all
+ * when count is NULL; clamped to [0, N]).  The caller keeps the table, and which pages are free; a
+ * page may be in several sequences' tables as long as none of them stores
+ * into it.  Table entries that no token of a call needs may hold anything.
+ * A token whose position is outside the table, or whose entry there is not a
+ * page of the cache, is not stored, loads as zeros, is attended by nobody and
+ * (as a query) attends nothing, and sets bit 4 of the device error word. */
+typedef struct {
+    int B, Hkv, N;               /* >= 1; N below 2^30                               */
+    int D;                       /* head dim, FIBATT_HEAD_DIM                        */
+    fibatt_dtype dtype;          /* of the tensors beside the cache                  */
+    int pages;                   /* of the cache, >= 1                               */
+    int table_len;               /* entries of a sequence's row of the table, >= 1, below 2^24 */
+    void *data;                  /* device, [pages, Hkv, 2, 4096] bytes, 16-byte aligned */
+    float *scales;               /* device, [pages, Hkv, 2], 8-byte aligned          */
+    const int32_t *table;        /* device, [B, table_len]                           */
+    int64_t table_stride_b;      /* entries between the table's rows                 */
+    const int32_t *start;        /* device, [B], or NULL                             */
+    const int32_t *count;        /* device, [B], or NULL                             */
+} fibatt_cache;
+
+/* Stores tokens: K, V Hkv heads of N rows.  A page's scale is the smallest power of two
+ * whose 448th multiple reaches the largest finite value stored in that piece of
+ * it, and a value becomes the nearest e4m3 multiple of it (ties to
+ * even; infinities the largest, NaN stays NaN).  A call that begins a page sets its
+ * scale anew; one that continues it (a first position that is not a multiple
+ * of 64) raises the scale where its tokens need that, and rounds the page's older
+ * tokens again, which changes only values below 2^-6 of the new scale; the
+ * page's rows behind the call's tokens are left as they were.  Two
+ * sequences of a call may not store into one page.  INVALID_ARG: a size or stride out of its range, a NULL or
+ * misaligned pointer, 2^31 blocks (two a page and head) or more.  UNSUPPORTED: D, dtype. */
+fibatt_status fibatt_cache_store(const fibatt_cache *d, const fibatt_heads *K, const fibatt_heads *V,
+                                 cudaStream_t stream);
+
+/* Loads tokens into K, V: the values that the bytes stand for (exact in bf16
+ * and fp32), zeros from count[b] on.  Errors as above. */
+fibatt_status fibatt_cache_load(const fibatt_cache *d, const fibatt_heads *K, const fibatt_heads *V,
+                                cudaStream_t stream);
+
+/* Attention of the N tokens' queries (Hq heads, Hkv divides Hq) to the
+ * cache, which holds their own keys already: a query at position p attends the
+ * keys k <= p with k > p - window or k < sinks (window >= 1: one of 64 table_len or
+ * more is all keys), as in fibatt_window_fwd; a query that count leaves out attends
+ * none: O = 0, LSE = -inf.  Made for single tokens and a handful (up to 16 query rows
+ * of a key head read its pages once, more read them again); a long prompt's own part is
+ * fibatt_window_fwd's, on fibatt_cache_load's keys where the cache holds earlier ones.
+ * Arithmetic: products of halves with fp32 sums (queries exact in bf16, 22 bits in fp32,
+ * relative to their row's largest; weights 11 bits in bf16 I/O, 22 in fp32), O rounded
+ * once.  What the pages hold behind the last token, or in
+ * keys that no query attends, reaches no result.  Errors as above, and
+ * INVALID_ARG for Hq, scale, window, sinks out of their range. */
+fibatt_status fibatt_cache_fwd(const fibatt_cache *d, int Hq, float scale, int window, int sinks,
+                               const fibatt_heads *Q, const fibatt_heads *O, float *LSE,
+                               cudaStream_t stream);
+
 /* Message for the last failing call on this thread ("" if none). */
 const char *fibatt_last_error(void);
 
@@ -395,8 +463,9 @@ const char *fibatt_version(void);
  * about 2 s); bit 2 (4), in the bounds-checked debug build only (built with
  * -DFIBATT_CHECKS), when a kernel's bounds check failed and it skipped the
  * access (the first failing source line is then printed to stderr); bit 3
- * (8) when fibatt_qk_norm_fwd or _bwd met a position behind its tables.
- * (fibatt_cross_fwd and _bwd may write outputs after bit 0 or 1: not to be
+ * (8) when fibatt_qk_norm_fwd or _bwd met a position behind its tables; bit 4
+ * (16) when a call on the 8-bit cache met a token without a page.
+ * (fibatt_cross_fwd and _bwd, fibatt_window_fwd and _bwd and fibatt_cache_fwd may write outputs after bit 0 or 1: not to be
  * trusted.)  The word is the OR over every kernel file's copy.  This call synchronises with
  * the device.  With clear != 0 the word is reset.  CUDA on a failed copy. */
 fibatt_status fibatt_device_error(int clear, unsigned *code);

@@ -60,6 +60,7 @@ _SIGS = {
 HEADS = struct.Struct("@Pqqq")                       # fibatt_heads: ptr, stride_b, stride_h, stride_n
 CROSS = struct.Struct("@7ifPPq")                     # fibatt_cross
 WINDOW = struct.Struct("@7ifiiPP")                   # fibatt_window
+CACHE = struct.Struct("@7iPPPqPP")                    # fibatt_cache
 QK_NORM = struct.Struct("@7iPPfiiPPiPq")             # fibatt_qk_norm
 
 _i64 = ctypes.c_int64
@@ -71,6 +72,9 @@ _SIGS.update({
     "fibatt_cross_fwd": (ctypes.c_int, [_vp] * 7),
     "fibatt_cross_bwd_workspace_bytes": (ctypes.c_size_t, [_vp]),
     "fibatt_cross_bwd": (ctypes.c_int, [_vp] * 11 + [ctypes.c_size_t, _vp]),
+    "fibatt_cache_store": (ctypes.c_int, [_vp] * 4),
+    "fibatt_cache_load": (ctypes.c_int, [_vp] * 4),
+    "fibatt_cache_fwd": (ctypes.c_int, [_vp, ctypes.c_int, ctypes.c_float, ctypes.c_int, ctypes.c_int, _vp, _vp, _vp, _vp]),
     "fibatt_window_fwd": (ctypes.c_int, [_vp] * 7),
     "fibatt_window_bwd_workspace_bytes": (ctypes.c_size_t, [_vp]),
     "fibatt_window_bwd": (ctypes.c_int, [_vp] * 11 + [ctypes.c_size_t, _vp]),

@@ -8,6 +8,7 @@ from __future__ import annotations
 
 import ctypes
 import operator
+from typing import NamedTuple
 
 import torch
 from torch.autograd.function import once_differentiable
@@ -726,8 +727,131 @@ def window_attention(Q, K, V, scale: float | None = None, window: int | None = N
     return WindowAttentionFunction.apply(Q, K, V, float(scale), window, sinks, q_start, kv_len)
 
 
+# ------------------------------------------------ paged cache in 8 bits
+
+PAGE = 64                    # tokens of a page
+
+
+class Cache(NamedTuple):
+    """A cache's memory: data [pages, Hkv, 2, 4096] uint8 (a page's keys
+    [64 tokens][64 dims], then its values [64 dims][64 tokens], as e4m3) and
+    scales [pages, Hkv, 2] fp32.  Which sequence has which pages is a table that
+    the caller keeps: int32 [B, pages of a sequence]."""
+
+    data: torch.Tensor
+    scales: torch.Tensor
+
+    @classmethod
+    def new(cls, pages: int, kv_heads: int, device=None) -> "Cache":
+        """A cache of so many pages, of 64 tokens each."""
+        device = torch.device("cuda") if device is None else device
+        return cls(torch.zeros(pages, kv_heads, 2, PAGE * HEAD_DIM, dtype=torch.uint8, device=device),
+                   torch.ones(pages, kv_heads, 2, device=device))
+
+
+def _cache_desc(cache, table, start, count, dtype, B, N, D, index):
+    """A packed fibatt_cache."""
+    data, scales = cache
+    code = _DTYPES.get(dtype)
+    if code is None:
+        raise ValueError(f"dtype {dtype} unsupported (float32 or bfloat16)")
+    _check_tensor("data", data, torch.uint8, index)
+    if data.dim() != 4 or data.shape[2:] != _CACHE_SHAPE or not data.is_contiguous():
+        raise ValueError(f"data must be a contiguous [pages, Hkv, 2, {PAGE * HEAD_DIM}] tensor, got {tuple(data.shape)}")
+    pages, Hkv = data.shape[:2]
+    scales_ptr = _check_dense("scales", scales, (pages, Hkv, 2), torch.float32, index)
+    _check_tensor("table", table, torch.int32, index)
+    if table.dim() != 2 or table.shape[0] != B or (table.shape[1] > 1 and table.stride(1) != 1):
+        raise ValueError(f"table must be [B, pages of a sequence] with B={B} and contiguous rows, got {tuple(table.shape)}")
+    first = n = 0
+    if start is not None:
+        first = _check_dense("start", start, (B,), torch.int32, index)
+    if count is not None:
+        n = _check_dense("count", count, (B,), torch.int32, index)
+    return _native.CACHE.pack(B, Hkv, N, D, code, pages, table.shape[1], data.data_ptr(), scales_ptr, table.data_ptr(),
+                              table.stride(0) if B > 1 else 0, first, n), Hkv
+
+
+_CACHE_SHAPE = (2, PAGE * HEAD_DIM)
+
+
+def _cache_states(cache, table, K, V, start, count):
+    """(packed fibatt_cache, K, V as packed fibatt_heads, device index)."""
+    for name, t in (("K", K), ("V", V)):
+        if not isinstance(t, torch.Tensor) or t.dim() != 4:
+            raise ValueError(f"{name} must be a [B, H, N, D] tensor")
+    index = _index("K", K)
+    B, _, N, D = K.shape
+    d, Hkv = _cache_desc(cache, table, start, count, K.dtype, B, N, D, index)
+    shape = (B, Hkv, N, D)
+    return d, _heads_arg("K", K, shape, K.dtype, index), _heads_arg("V", V, shape, K.dtype, index), index
+
+
+def cache_store(cache: Cache, table: torch.Tensor, K: torch.Tensor, V: torch.Tensor, start: torch.Tensor | None = None,
+                count: torch.Tensor | None = None, stream=None) -> None:
+    """fibatt_cache_store: keys and values K, V [B, Hkv, N, 64] of N tokens into
+    the sequences' pages, token n of them at place start[b] + n (int32 [B]; from 0
+    if not given); count: int32 [B], how many of the N each sequence has."""
+    d, k, v, index = _cache_states(cache, table, K, V, start, count)
+    check(_launch(index, stream, lib().fibatt_cache_store, d, k, v))
+
+
+def cache_load(cache: Cache, table: torch.Tensor, N: int, start: torch.Tensor | None = None,
+               count: torch.Tensor | None = None, dtype: torch.dtype = torch.bfloat16, K: torch.Tensor | None = None,
+               V: torch.Tensor | None = None, stream=None):
+    """fibatt_cache_load: (K, V), [B, Hkv, N, 64] each, of the N tokens from
+    place start[b] on, zeros from count[b] on."""
+    index = _index("data", cache[0])
+    if not isinstance(table, torch.Tensor) or table.dim() != 2:
+        raise ValueError("table must be [B, pages of a sequence]")
+    shape = (table.shape[0], cache[0].shape[1], operator.index(N), HEAD_DIM)
+    if K is not None:
+        dtype = K.dtype
+    d, _ = _cache_desc(cache, table, start, count, dtype, shape[0], shape[2], HEAD_DIM, index)
+
+    def call(s):
+        k = torch.empty(shape, dtype=dtype, device=cache[0].device) if K is None else K
+        v = torch.empty(shape, dtype=dtype, device=cache[0].device) if V is None else V
+        check(lib().fibatt_cache_load(d, _heads_arg("K", k, shape, dtype, index), _heads_arg("V", v, shape, dtype, index), s))
+        return k, v
+
+    return _launch(index, stream, call)
+
+
+def cache_fwd(Q: torch.Tensor, cache: Cache, table: torch.Tensor, start: torch.Tensor | None, scale: float,
+              window: int | None = None, sinks: int = 0, count: torch.Tensor | None = None, O: torch.Tensor | None = None,
+              LSE: torch.Tensor | None = None, stream=None):
+    """fibatt_cache_fwd: attention of Q [B, Hq, N, 64], the queries of the tokens
+    at start[b] + n, to the cache that holds their keys (cache_store comes
+    first); window, sinks as window_fwd; returns (O, LSE), O in Q's layout.  A
+    query that count[b] leaves out attends nothing: O = 0, LSE = -inf."""
+    if not isinstance(Q, torch.Tensor) or Q.dim() != 4:
+        raise ValueError("Q must be a [B, H, N, D] tensor")
+    index = _index("Q", Q)
+    B, Hq, N, D = shape = Q.shape
+    d, _ = _cache_desc(cache, table, start, count, Q.dtype, B, N, D, index)
+    return _launch(index, stream, _cache_fwd, d, Hq, scale, *_band(window, sinks), _heads_arg("Q", Q, shape, Q.dtype, index),
+                   Q, O, LSE, index)
+
+
+def _cache_fwd(d, Hq, scale, window, sinks, q, Q, O, LSE, index, s):
+    shape = Q.shape
+    if O is None:
+        O = torch.empty_like(Q)
+    if LSE is None:
+        LSE = torch.empty(shape[:3], dtype=torch.float32, device=Q.device)
+        lse = LSE.data_ptr()
+    else:
+        lse = _check_dense("LSE", LSE, shape[:3], torch.float32, index)
+    status = lib().fibatt_cache_fwd(d, Hq, scale, window, sinks, q, _heads_arg("O", O, shape, Q.dtype, index), lse, s)
+    if status:
+        check(status)
+    return O, LSE
+
+
 __all__ = ["FibattError", "Support", "fwd", "bwd", "bwd_noalloc", "fibottention", "FibottentionFunction",
            "qk_norm_fwd", "qk_norm_bwd", "qk_norm", "QkNormFunction", "rotary_tables", "rotary_angles",
            "rotary_angles_2d", "cross_fwd", "cross_bwd", "cross_attention", "CrossAttentionFunction",
            "window_fwd", "window_bwd", "window_attention", "WindowAttentionFunction",
+           "Cache", "cache_store", "cache_load", "cache_fwd", "PAGE",
            "wythoff_row", "wythoff_row_modified", "window_schedule", "HEAD_DIM"]

@@ -8,14 +8,16 @@ through ``fibottention`` (forward fibatt_fwd, backward fibatt_bwd).  Head i of
 the layer uses Wythoff row pi(i) with the linear window schedule (paper
 Sec. 3: a per-layer permutation pi of the heads is allowed).  Query/key norms
 and a position rotation can go between the projection and the attention, and
-``CrossAttention`` is a decoder's layer on such an encoder's states.
+``CrossAttention`` is a decoder's layer on such an encoder's states,
+``WindowSelfAttention`` one on the decoder's own tokens.
 """
 from __future__ import annotations
 
 import torch
 from torch import nn
 
-from .api import HEAD_DIM, Support, cross_attention, fibottention, qk_norm, rotary_tables
+from .api import (HEAD_DIM, PAGE, Support, cache_fwd, cache_load, cache_store, cross_attention, fibottention, qk_norm,
+                  rotary_tables, window_attention, window_fwd)
 
 
 class _Rotary(nn.Module):
@@ -151,4 +153,75 @@ class CrossAttention(nn.Module):
         return self.proj(o.transpose(1, 2).reshape(B, Nq, dim))
 
 
-__all__ = ["FibottentionSelfAttention", "CrossAttention"]
+class WindowSelfAttention(nn.Module):
+    """Decoder tokens x [B, N, dim] on themselves -> [B, N, dim], dim = heads *
+    64: causal, each token on the `window` tokens up to itself (None: all) and on the
+    first `sinks`.
+
+    kv_heads: key/value heads, shared by heads / kv_heads query heads each.
+    norm: RMS norm of every query and key head.  rotary: a table of angles for the
+    tokens' places (None: not rotated).  forward() is for whole sequences, in
+    training; step() decodes on a paged 8-bit cache (api.Cache)."""
+
+    # up to so many query rows of a key head are attended page by page; more take the cache's
+    # tokens as 16 or 32 bits first
+    FEW_ROWS = 64
+
+    def __init__(self, dim: int, heads: int, kv_heads: int | None = None, window: int | None = None, sinks: int = 0,
+                 bias: bool = True, norm: bool = False, rotary: torch.Tensor | None = None, eps: float = 1e-6):
+        super().__init__()
+        if dim != heads * HEAD_DIM:
+            raise ValueError(f"dim must be heads * {HEAD_DIM}")
+        self.heads = heads
+        self.kv_heads = heads if kv_heads is None else kv_heads
+        if self.kv_heads < 1 or heads % self.kv_heads:
+            raise ValueError(f"kv_heads {kv_heads} does not divide {heads} heads")
+        if (window is not None and window < 1) or sinks < 0:
+            raise ValueError(f"window {window} must be at least 1, sinks {sinks} at least 0")
+        self.window, self.sinks = window, sinks
+        self.qkv = nn.Linear(dim, (heads + 2 * self.kv_heads) * HEAD_DIM, bias=bias)
+        self.proj = nn.Linear(dim, dim, bias=bias)
+        self.scale = HEAD_DIM ** -0.5
+        self.q_norm = nn.Parameter(torch.ones(HEAD_DIM)) if norm else None
+        self.k_norm = nn.Parameter(torch.ones(HEAD_DIM)) if norm else None
+        self.eps = eps
+        self.rotary = None if rotary is None else _Rotary(rotary)
+
+    def _split(self, x, positions):
+        """Queries, keys and values [B, H, N, 64] of the tokens x."""
+        heads = (self.heads, self.kv_heads, self.kv_heads)
+        qkv = self.qkv(x)
+        if self.q_norm is None and self.rotary is None:
+            qkv = qkv.unflatten(-1, (sum(heads), HEAD_DIM)).transpose(1, 2)
+            return qkv.split(heads, 1)
+        return qk_norm(qkv, heads, _weight(self.q_norm, qkv), _weight(self.k_norm, qkv), self.eps,
+                       *_turned(self.rotary, positions))
+
+    def _join(self, o):
+        return self.proj(o.transpose(1, 2).flatten(2))
+
+    def forward(self, x: torch.Tensor, kv_len: torch.Tensor | None = None) -> torch.Tensor:
+        """kv_len [B] int32: the sequences' lengths where they are padded behind (the
+        padding's outputs are the projection's bias)."""
+        q, k, v = self._split(x, None)
+        return self._join(window_attention(q, k, v, self.scale, self.window, self.sinks, None, kv_len))
+
+    @torch.no_grad()
+    def step(self, x: torch.Tensor, cache, table: torch.Tensor, start: torch.Tensor,
+             count: torch.Tensor | None = None) -> torch.Tensor:
+        """The next N tokens x [B, N, dim] of sequences that have start[b] tokens in
+        `cache` (int32 [B]; the table [B, pages] has pages for the new ones too), into
+        which theirs go.  count [B] int32: how many of the N each sequence has.
+        Without gradients; start is the caller's to move on."""
+        N = x.shape[1]
+        places = start[:, None] + torch.arange(N, dtype=torch.int32, device=x.device)
+        q, k, v = self._split(x, places)
+        cache_store(cache, table, k, v, start, count)
+        if self.heads // self.kv_heads * N <= self.FEW_ROWS:
+            return self._join(cache_fwd(q, cache, table, start, self.scale, self.window, self.sinks, count)[0])
+        held = start + (N if count is None else count.clamp(0, N))
+        k, v = cache_load(cache, table, table.shape[1] * PAGE, None, held, dtype=x.dtype)
+        return self._join(window_fwd(q, k, v, self.scale, self.window, self.sinks, start, held)[0])
+
+
+__all__ = ["FibottentionSelfAttention", "CrossAttention", "WindowSelfAttention"]

@@ -42,34 +42,52 @@ struct KeySet {
 #endif
 };
 
+// A number that a call reads on the device.
+__host__ __device__ __forceinline__ int32_t load_number(const int32_t *p) {
+#ifdef __CUDA_ARCH__
+    return __ldg(p);
+#else
+    return *p;
+#endif
+}
+__host__ __device__ __forceinline__ int least(int a, int b) { return a < b ? a : b; }
+__host__ __device__ __forceinline__ int most(int a, int b) { return a < b ? b : a; }
+
 // Attention over a sliding window with sinks: the query at position p of its
 // sequence attends the keys k <= p with k > p - window or k < sinks.  Positions
 // outside the sequence attend nothing, which p = -1 stands for below.  (Sizes and
-// the window are below 2^30, so that sums of two stay in 32 bits.)
+// the window are at most 2^30, so that sums of two stay in 32 bits.)
 struct Band {
     const int32_t *start;    // [B]: position of a sequence's first query, or null: Nk - Nq
     int Nq, Nk, window, sinks;
-#ifdef __CUDACC__
     // (a start further out leaves no query a position, wherever it is)
-    __device__ __forceinline__ int first(int b) const { return start ? max(-Nq, min(__ldg(start + b), Nk)) : Nk - Nq; }
-    __device__ __forceinline__ bool sees(int p, int k) const { return k <= p && (k > p - window || k < sinks); }
-#endif
+    __host__ __device__ __forceinline__ int first(int b) const {
+        return start ? most(-Nq, least(load_number(start + b), Nk)) : Nk - Nq;
+    }
+    __host__ __device__ __forceinline__ bool sees(int p, int k) const { return k <= p && (k > p - window || k < sinks); }
 };
 
-#ifdef __CUDACC__
 // Bits below n: none for n <= 0, all for n >= 32.
-__device__ __forceinline__ uint32_t bits_below(int n) {
+__host__ __device__ __forceinline__ uint32_t bits_below(int n) {
+#ifdef __CUDA_ARCH__
     uint32_t above;
     asm("shl.b32 %0, 0xffffffff, %1;" : "=r"(above) : "r"(max(n, 0)));     // (0 from 32 on)
     return ~above;
+#else
+    return n <= 0 ? 0u : n >= 32 ? ~0u : ~(~0u << n);
+#endif
 }
 // Bit i: the query at position p attends key k0 + i.
-__device__ __forceinline__ uint32_t keys_of(const Band &w, int p, int k0) {
+__host__ __device__ __forceinline__ uint32_t keys_of(const Band &w, int p, int k0) {
     return bits_below(p + 1 - k0) & (~bits_below(p + 1 - w.window - k0) | bits_below(w.sinks - k0));
 }
+// Bit i: a query at one of the positions lo to hi attends key k0 + i.
+__host__ __device__ __forceinline__ uint32_t keys_between(const Band &w, int lo, int hi, int k0) {
+    return lo > hi ? 0u : bits_below(hi + 1 - k0) & (~bits_below(lo + 1 - w.window - k0) | bits_below(w.sinks - k0));
+}
 // Bit i: the query at position p0 + i, if that is below `end`, attends key k.
-__device__ __forceinline__ uint32_t queries_of(const Band &w, int k, int p0, int end) {
-    return bits_below((k < w.sinks ? end : min(end, k + w.window)) - p0) & ~bits_below(k - p0);
+__host__ __device__ __forceinline__ uint32_t queries_of(const Band &w, int k, int p0, int end) {
+    return bits_below((k < w.sinks ? end : least(end, k + w.window)) - p0) & ~bits_below(k - p0);
 }
 
 // The T-key tiles that hold the keys of the queries at positions lo to hi: first
@@ -77,17 +95,16 @@ __device__ __forceinline__ uint32_t queries_of(const Band &w, int k, int p0, int
 template <int T>
 struct BandWalk {
     int sinks, gap, n;       // tiles of the sinks, tiles between them and the windows', tiles of the walk
-    __device__ __forceinline__ BandWalk() {}
-    __device__ __forceinline__ BandWalk(const Band &w, int lo, int hi) : sinks(0), gap(0), n(0) {
+    __host__ __device__ __forceinline__ BandWalk() {}
+    __host__ __device__ __forceinline__ BandWalk(const Band &w, int lo, int hi) : sinks(0), gap(0), n(0) {
         if (lo > hi) return;
-        const int oldest = max(0, lo - w.window + 1) / T;
-        sinks = min((w.sinks + T - 1) / T, oldest);
+        const int oldest = most(0, lo - w.window + 1) / T;
+        sinks = least((w.sinks + T - 1) / T, oldest);
         gap = oldest - sinks;
         n = hi / T + 1 - gap;
     }
-    __device__ __forceinline__ int tile(int i) const { return i < sinks ? i : i + gap; }
+    __host__ __device__ __forceinline__ int tile(int i) const { return i < sinks ? i : i + gap; }
 };
-#endif
 
 struct CrossArgs {
     int B, Hq, Hkv, Nq, Nk;

@@ -21,6 +21,7 @@
 #include <algorithm>
 
 #include "cluster.cuh"
+#include "cross_cache.h"
 #include "cross_tiles.cuh"
 
 namespace fibatt {
@@ -525,6 +526,15 @@ bool cross_rows_takes(const CrossArgs &a) {
 
 cudaError_t launch_cross_rows(const CrossArgs &a) { return a.banded ? launch<true>(a) : launch<false>(a); }
 
-FIBATT_DEFINE_ERROR_READER(read_error_cross_rows, "cross_rows.cu")
+FIBATT_DEFINE_ERROR_READER(read_error_rows, "cross_rows.cu")
+
+// This file's word with that of cross_cache.cu, whose attention is also one of a few rows.
+cudaError_t read_error_cross_rows(unsigned *code, bool clear) {
+    unsigned cache = 0;
+    cudaError_t e = read_error_rows(code, clear);
+    if (e == cudaSuccess) e = read_error_cross_cache(&cache, clear);
+    *code |= cache;
+    return e;
+}
 
 }  // namespace fibatt

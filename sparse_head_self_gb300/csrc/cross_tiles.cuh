@@ -99,10 +99,7 @@ __device__ __forceinline__ uint4 tile_keys(const KeySet &ks, int b, int n0, int 
 __device__ __forceinline__ uint4 band_keys(const Band &w, int lo, int hi, int n0) {
     uint32_t x[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int k0 = n0 + 32 * i;
-        x[i] = lo > hi ? 0u : bits_below(hi + 1 - k0) & (~bits_below(lo + 1 - w.window - k0) | bits_below(w.sinks - k0));
-    }
+    for (int i = 0; i < 4; ++i) x[i] = keys_between(w, lo, hi, n0 + 32 * i);
     return make_uint4(x[0], x[1], x[2], x[3]);
 }
 __device__ __forceinline__ bool all_keys(const uint4 &w) { return (w.x & w.y & w.z & w.w) == 0xffffffffu; }
