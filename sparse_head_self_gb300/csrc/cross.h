@@ -230,6 +230,7 @@ cudaError_t launch_cross_bwd_f32(const CrossArgs &a);
 cudaError_t launch_cross_fwd_mma(const CrossArgs &a);   // bf16
 cudaError_t launch_cross_bwd_mma(const CrossArgs &a);   // bf16
 size_t cross_bwd_mma_workspace(int B, int Hq, int Nq);
+size_t window_bwd_mma_workspace(int B, int Hq, int Hkv, int Nq, int Nk, int window, int sinks);
 bool cross_rows_takes(const CrossArgs &a);               // few enough query rows for the next
 cudaError_t launch_cross_rows(const CrossArgs &a);
 

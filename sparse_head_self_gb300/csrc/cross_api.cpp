@@ -67,13 +67,17 @@ CrossArgs cross_args(const Desc *d, const fibatt_heads *Q, const fibatt_heads *K
     return a;
 }
 
+Band band(const fibatt_window *d) {
+    // (a window that reaches the first key makes sinks of no account)
+    const int window = std::min(d->window, d->Nk);
+    return Band{d->q_start, d->Nq, d->Nk, window, window == d->Nk ? 0 : std::min(d->sinks, d->Nk)};
+}
+
 CrossArgs window_args(const fibatt_window *d, const fibatt_heads *Q, const fibatt_heads *K, const fibatt_heads *V,
                       const fibatt_heads *O, cudaStream_t stream) {
     CrossArgs a = cross_args(d, Q, K, V, O, stream);
     a.banded = true;
-    // (a window that reaches the first key makes sinks of no account)
-    const int window = std::min(d->window, d->Nk);
-    a.band = Band{d->q_start, d->Nq, d->Nk, window, window == d->Nk ? 0 : std::min(d->sinks, d->Nk)};
+    a.band = band(d);
     return a;
 }
 
@@ -122,12 +126,18 @@ fibatt_status run_bwd(const CrossArgs &a, const char *what) {
     return e == cudaSuccess ? FIBATT_OK : cuda_error(e, what);
 }
 
-template <typename Desc>
-size_t bwd_workspace(const Desc *d) {
+size_t round_256(size_t bytes) { return (bytes + 255) / 256 * 256; }
+size_t bwd_workspace(const fibatt_cross *d) {
     if (!d || d->B < 1 || d->Hq < 1 || d->Nq < 1) return 0;
-    const size_t bytes = d->dtype == FIBATT_BF16 ? cross_bwd_mma_workspace(d->B, d->Hq, d->Nq)
-                                                 : (size_t)d->B * d->Hq * d->Nq * sizeof(float2);
-    return (bytes + 255) / 256 * 256;
+    return round_256(d->dtype == FIBATT_BF16 ? cross_bwd_mma_workspace(d->B, d->Hq, d->Nq)
+                                             : (size_t)d->B * d->Hq * d->Nq * sizeof(float2));
+}
+size_t bwd_workspace(const fibatt_window *d) {
+    if (check_window(d)) return 0;
+    const Band w = band(d);
+    return round_256(d->dtype == FIBATT_BF16
+                         ? window_bwd_mma_workspace(d->B, d->Hq, d->Hkv, d->Nq, d->Nk, w.window, w.sinks)
+                         : (size_t)d->B * d->Hq * d->Nq * sizeof(float2));
 }
 
 fibatt_status check_norm(const fibatt_qk_norm *d, const void *X, int64_t sb, int64_t sn) {

@@ -55,6 +55,7 @@ constexpr int kThreads = 32 * (kWeightWarps + 4);
 constexpr int kStages = 4;
 constexpr int kNarrow = kTileRows * 16;           // bytes of half a k-step of a tile (the other half: zeros for all)
 constexpr size_t kSmem = 1024 + (4 + 2 * kStages) * kTileBytes + (2 + 2 * kStages) * kNarrow;
+constexpr int kPartSums = 8 * 32 * kWeightWarps;  // float4s of a part's sums, of dK and dV
 constexpr int kJoinLd = 68;                       // floats between rows of a partial sum in shared memory
 static_assert(2 * kTileRows * kJoinLd * 4 <= 2 * kStages * kTileBytes, "partial sums fit");
 // registers a thread: at launch, and after the weight warps took what the others gave
@@ -75,6 +76,9 @@ struct BwdMmaArgs {
     Rows<__nv_bfloat16> dQ, dK, dV;
     int B, Hq, Hkv, ktiles;
     int query_units, units;     // units that hold queries, which come first, and all of them
+    int chunks, chunk_tiles;    // BAND: parts of a sinks' walk and the query tiles of each, ...
+    int sink_tiles, sink_units; // ... key tiles that have such walks, units of those parts
+    float4 *parts;              // their partial sums, one after another
     int first_unit;             // of the launch, which has those up to `units`
     int *next_unit;             // units given out behind every CTA's first
     float scale;
@@ -269,6 +273,7 @@ struct UnitBand {};
 template <>
 struct UnitBand<true> {
     int p0, first, last;     // position of query 0; of the unit's queries, held or streamed, that attend keys of it
+    int chunk;               // keys held: the part of the walk that this unit has, -1: all of it
     BandWalk<kTileRows> walk;    // held queries
     __device__ __forceinline__ UnitBand() {}
 };
@@ -304,9 +309,17 @@ struct Unit : UnitBand<BAND> {
         n = (int)(tiles * (rank + 1) / CS) - lo;
     }
     // The units with the longest walks first: the last queries, the first keys.
+    // Tiles with sinks, whose keys all later queries attend, have their walks cut into parts
+    // about as long as the others' walks.
     template <bool KEYS>
     __device__ __forceinline__ void set_band(const BwdMmaArgs<BAND> &a, int unit) {
         const int heads = a.Hkv * a.B;
+        this->chunk = -1;
+        if (KEYS) {
+            const int tiles = a.sink_tiles * heads;
+            if (unit < a.sink_units) this->chunk = unit / tiles, unit %= tiles;
+            else unit += tiles - a.sink_units;
+        }
         mine = KEYS ? unit / heads : a.qt.tiles - 1 - unit / heads;
         hk = unit % heads % a.Hkv;
         b = unit % heads / a.Hkv;
@@ -329,6 +342,12 @@ struct Unit : UnitBand<BAND> {
             this->last = min(end, this->p0 + a.qt.first_row(mine) + a.qt.nb) - 1;
             this->walk = BandWalk<kTileRows>(a.band, this->first, this->last);
             tiles = this->walk.n;
+        }
+        if (KEYS && this->chunk >= 0) {      // (a walk may be shorter than its parts)
+            const int at = this->chunk * a.chunk_tiles;
+            lo = from + at;
+            n = max(0, min(a.chunk_tiles, tiles - at));
+            return;
         }
         const int CS = (int)cluster_size(), rank = (int)cluster_rank();
         lo = (int)((int64_t)tiles * rank / CS);
@@ -487,6 +506,19 @@ __device__ __forceinline__ int weights(const BwdMmaArgs<BAND> &a, Shared<BAND> &
         tc_before_sync();
     }
     const float f = acc ? 1.f : a.scale;
+    if constexpr (BAND && KEYS) {
+        if (u.chunk >= 0 && FIBATT_CHECKED(u.mine < a.sink_tiles && u.chunk < a.chunks)) {       // (see window_sum_kernel)
+            const int tile = (u.mine * a.B + u.b) * a.Hkv + u.hk;
+            float4 *mine = a.parts + ((int64_t)tile * a.chunks + u.chunk) * kPartSums + threadIdx.x;
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                __stcg(mine + i * 32 * kWeightWarps,
+                       u.n > 0 ? make_float4(__uint_as_float(o[4 * i]), __uint_as_float(o[4 * i + 1]),
+                                             __uint_as_float(o[4 * i + 2]), __uint_as_float(o[4 * i + 3]))
+                               : make_float4(0.f, 0.f, 0.f, 0.f));
+            return it;
+        }
+    }
     if (cluster_size() == 1) {
         if (!row) return it;
         __nv_bfloat16 *out = KEYS ? (acc ? a.dV : a.dK).row(u.b, u.hk, u.mine * kTileRows + r)
@@ -855,14 +887,69 @@ __global__ void __launch_bounds__(kThreads, 1) cross_bwd_mma_kernel(const __grid
     cluster_sync();   // the others may still read this CTA's part
 }
 
+// dK and dV of the key tiles whose walks were cut: the parts' sums, in their order.  A thread
+// adds the four values that thread t of the weight warps left at i.
+__global__ void __launch_bounds__(256)
+window_sum_kernel(const __grid_constant__ BwdMmaArgs<true> a) {
+    grid_dep_wait();
+    grid_dep_launch();
+    const int tile = blockIdx.x / (kPartSums / 256), e = blockIdx.x % (kPartSums / 256) * 256 + threadIdx.x;
+    const int i = e / (32 * kWeightWarps), t = e % (32 * kWeightWarps), warp = t >> 5, acc = warp >> 3;
+    const int hk = tile % a.Hkv, b = tile / a.Hkv % a.B, k = tile / a.Hkv / a.B * kTileRows + (warp & 3) * 32 + (t & 31);
+    if (k >= a.ks.Nk) return;
+    const float4 *from = a.parts + (int64_t)tile * a.chunks * kPartSums + e;
+    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int c = 0; c < a.chunks; ++c) {
+        const float4 y = __ldg(from + (int64_t)c * kPartSums);
+        x.x += y.x, x.y += y.y, x.z += y.z, x.w += y.w;
+    }
+    const float f = acc ? 1.f : a.scale;
+    *reinterpret_cast<uint2 *>((acc ? a.dV : a.dK).row(b, hk, k) + 32 * ((warp >> 2) & 1) + 4 * i) =
+        make_uint2(pack_bf16x2(x.x * f, x.y * f), pack_bf16x2(x.z * f, x.w * f));
+}
+
 // Rows of a head with the last of its query tiles whole.
 int padded_rows(int Nq) { return Nq < kTileRows ? Nq : (Nq + kTileRows - 1) / kTileRows * kTileRows; }
+
+}  // namespace
+
+namespace {
+
+// How the walks of key tiles with sinks are cut: into parts about as long as the other
+// tiles' walks, as long as there are no more than kParts of them in all (two a SM, each
+// with 64 KB of partial sums).  (One sequence of 16385 tokens, 16 heads on 4, window 1024, 4
+// sinks: walks of 516 tiles next to others of 36; in one part 673 us.)
+struct SinkParts {
+    static constexpr int64_t kParts = 304;
+    int64_t tiles = 0, chunks = 1, length = 0;       // key tiles of a head; parts of each, query tiles of a part
+    SinkParts(int B, int Hkv, int Nk, const Band &w, const BandTiles &qt) {
+        tiles = std::min<int64_t>((w.sinks + kTileRows - 1) / kTileRows, (Nk + kTileRows - 1) / kTileRows);
+        if (tiles == 0) return;
+        const int64_t other = ((int64_t)(w.window + kTileRows) / qt.nb + 1) * qt.groups, heads = (int64_t)B * Hkv * tiles;
+        length = std::max({other, (heads * qt.tiles + kParts - 1) / kParts, (qt.tiles + 255) / (int64_t)256});
+        chunks = (qt.tiles + length - 1) / length;
+    }
+    size_t bytes(int B, int Hkv) const {
+        return chunks > 1 ? (size_t)B * Hkv * tiles * chunks * kPartSums * sizeof(float4) : 0;
+    }
+};
+
+size_t round_16(size_t x) { return (x + 15) / 16 * 16; }
 
 }  // namespace
 
 size_t cross_bwd_mma_workspace(int B, int Hq, int Nq) {
     const size_t rows = (size_t)B * Hq * padded_rows(Nq);
     return 2 * (rows + kTileRows) * sizeof(uint4) + (size_t)B * Hq * Nq * sizeof(float2) + 2 * sizeof(int);
+}
+
+size_t window_bwd_mma_workspace(int B, int Hq, int Hkv, int Nq, int Nk, int window, int sinks) {
+    // (heads with rows of their own or broadcast ones, whose tiles are others)
+    const Band w{nullptr, Nq, Nk, window, sinks};
+    size_t most = 0;
+    for (const bool shared : {false, true}) most = std::max(most, SinkParts(B, Hkv, Nk, w, BandTiles(Hq / Hkv, Nq, shared)).bytes(B, Hkv));
+    return round_16(cross_bwd_mma_workspace(B, Hq, Nq)) + most;
 }
 
 namespace {
@@ -885,6 +972,19 @@ cudaError_t bwd(const CrossArgs &a) {
     f.stats = stats;
     f.next_unit = reinterpret_cast<int *>(stats + (int64_t)a.B * a.Hq * a.Nq);
     f.lse_parts = lse_parts, f.d_parts = d_parts;
+    f.chunks = 1, f.chunk_tiles = f.sink_tiles = f.sink_units = 0;
+    f.parts = nullptr;
+    if constexpr (BAND) {
+        const SinkParts p(a.B, a.Hkv, a.Nk, a.band, f.qt);
+        if (p.chunks > 1) {
+            f.chunks = (int)p.chunks;
+            f.chunk_tiles = (int)p.length;
+            f.sink_tiles = (int)p.tiles;
+            f.sink_units = (int)((int64_t)a.B * a.Hkv * p.tiles * p.chunks);
+            f.parts = reinterpret_cast<float4 *>(reinterpret_cast<char *>(a.stats) +
+                                                 round_16(cross_bwd_mma_workspace(a.B, a.Hq, a.Nq)));
+        }
+    }
     f.dQ = rows_of<__nv_bfloat16>(a.dQ), f.dK = rows_of<__nv_bfloat16>(a.dK), f.dV = rows_of<__nv_bfloat16>(a.dV);
     f.B = a.B, f.Hq = a.Hq, f.Hkv = a.Hkv;
     f.ktiles = (a.Nk + kTileRows - 1) / kTileRows;
@@ -909,7 +1009,8 @@ cudaError_t bwd(const CrossArgs &a) {
                             d_parts, f.next_unit);
     }
     if (e != cudaSuccess) return e;
-    const int64_t query_units = (int64_t)a.B * a.Hkv * f.qt.tiles, key_units = (int64_t)a.B * a.Hkv * f.ktiles;
+    const int64_t query_units = (int64_t)a.B * a.Hkv * f.qt.tiles;
+    const int64_t key_units = (int64_t)a.B * a.Hkv * (f.ktiles - f.sink_tiles) + f.sink_units;
     f.query_units = (int)query_units;
     // clusters, one unit each, while they all find a place; else one wave of CTAs that walk over the units
     const auto launch = [&](int64_t from, int64_t units, int c) {
@@ -923,9 +1024,17 @@ cudaError_t bwd(const CrossArgs &a) {
     int64_t query_walk = f.ktiles, key_walk = f.qt.tiles;
     if constexpr (BAND) {      // tiles that hold the windows of a tile's rows, and the sinks
         query_walk = std::min<int64_t>(query_walk, ((int64_t)a.band.window + f.qt.nb) / kTileRows + 1 + (a.band.sinks + kTileRows - 1) / kTileRows);
-        if (a.band.sinks == 0) key_walk = std::min<int64_t>(key_walk, (((int64_t)a.band.window + kTileRows) / f.qt.nb + 2) * f.qt.groups);
+        if (a.band.sinks == 0 || f.chunks > 1) key_walk = std::min<int64_t>(key_walk, (((int64_t)a.band.window + kTileRows) / f.qt.nb + 2) * f.qt.groups);
     }
     const Launches l(query_units, query_walk, key_units, key_walk, sm_count(), 5, 12);
+    if constexpr (BAND) {
+        if (f.chunks > 1) {      // (no clusters: there are units enough)
+            e = launch(0, query_units + key_units, 1);
+            if (e != cudaSuccess) return e;
+            const unsigned blocks = (unsigned)(a.B * a.Hkv * f.sink_tiles * (kPartSums / 256));
+            return launch_clusters(window_sum_kernel, blocks, 1, 256, 0, a.stream, f);
+        }
+    }
     if (!l.two) return launch(0, query_units + key_units, l.c);
     e = launch(0, query_units, l.c_query);
     if (e != cudaSuccess) return e;

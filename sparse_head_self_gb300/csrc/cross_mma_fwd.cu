@@ -48,7 +48,7 @@ constexpr float kNegInf = -__builtin_inff();
 constexpr float kRaise = 8.f;    // log2 units
 constexpr int kJoinLd = 68;      // floats between rows of a partial O in shared memory
 
-template <int NT>
+template <int NT, bool BAND>
 struct Cfg {
     static constexpr int kSoftmaxWarps = 8 * NT;
     static constexpr int kCopyWarp = kSoftmaxWarps, kKeysWarp = kSoftmaxWarps + 1;
@@ -58,7 +58,7 @@ struct Cfg {
     static constexpr uint32_t kCols = NT * 256;        // S 128, P 64, O 64 a tile
     static constexpr size_t kSmem = 1024 + NT * kTileBytes + kStages * 2 * kTileBytes;
     static constexpr int kMinBlocks = NT == 2 ? 1 : 2;
-    static constexpr bool kWalks = NT == 1;            // one wave of CTAs for all units
+    static constexpr bool kWalks = NT == 1 || BAND;    // one wave of CTAs for all units
     // registers a thread: at launch, and after the softmax warps took what the others gave
     static constexpr int kRegs = NT == 2 ? 96 : 80, kRegsFew = 32, kRegsMany = NT == 2 ? 112 : 104;
     static_assert(2 * NT * kRegsMany + kRegsFew == (2 * NT + 1) * kRegs, "the shares add up");
@@ -147,9 +147,9 @@ __device__ __forceinline__ bool all_of(int id, int threads, bool p) {
 }
 
 template <int NT, bool BAND>
-__global__ void __launch_bounds__(Cfg<NT>::kThreads, Cfg<NT>::kMinBlocks)
+__global__ void __launch_bounds__(Cfg<NT, BAND>::kThreads, Cfg<NT, BAND>::kMinBlocks)
 cross_fwd_mma_kernel(const __grid_constant__ FwdMmaArgs<BAND> a) {
-    using C = Cfg<NT>;
+    using C = Cfg<NT, BAND>;
     using Work = Unit<NT, BAND>;
     using Where = Place<NT, BAND>;
     extern __shared__ uint8_t smem_raw[];
@@ -214,8 +214,8 @@ cross_fwd_mma_kernel(const __grid_constant__ FwdMmaArgs<BAND> a) {
             for (int k = 0;; ++k) {
                 bool go = pipe_wait(&bar_unit[k & 1], (k >> 1) & 1, abort);
                 __syncwarp();
-                // the softmax warps meet at barriers within a unit: all of them go on, or none
-                if (warp < C::kSoftmaxWarps) go = all_of(2, 32 * C::kSoftmaxWarps, go);
+                // the softmax warps of a tile meet at barriers within a unit: all of them go on, or none
+                if (warp < C::kSoftmaxWarps) go = all_of(NT == 1 ? 2 : 11 + (warp >> 3), 32 * 8, go);
                 if (!go || units[k & 1].n < 0) break;
                 body(units[k & 1]);
                 __syncwarp();
@@ -487,6 +487,8 @@ cross_fwd_mma_kernel(const __grid_constant__ FwdMmaArgs<BAND> a) {
 #pragma unroll
                         for (int t = 0; t < NT; ++t) {   // S_t = Q_t K_j^T
                             if (t >= nt) break;
+                            // the CTA's first tile: its second softmax begins behind the first, and stays there
+                            if (BAND && t == 1 && it[0] == 1 && it[1] == 0) pipe_wait(&bar_p[0], 0, abort);
                             if (it[t] > 0) pipe_wait(&bar_sfree[t], (it[t] - 1) & 1, abort);
                             ++it[t];
                             tc_after_sync();
@@ -582,7 +584,7 @@ cross_fwd_mma_kernel(const __grid_constant__ FwdMmaArgs<BAND> a) {
 // How many clusters of 2^i CTAs device `dev`, the current one, holds at once.
 template <int NT, bool BAND>
 int held_clusters(int dev, int i) {
-    using C = Cfg<NT>;
+    using C = Cfg<NT, BAND>;
     static PerDevice known[5];
     return known[i].get(dev, [=] {
         return i == 0 ? C::kMinBlocks * sm_count()
@@ -606,7 +608,7 @@ struct Plan {
 };
 template <int NT, bool BAND>
 cudaError_t consider(const CrossArgs &a, const TilesOf<BAND> &qt, Plan *best) {
-    using C = Cfg<NT>;
+    using C = Cfg<NT, BAND>;
     const cudaError_t e = prepare_kernel<cross_fwd_mma_kernel<NT, BAND>>(C::kSmem, C::kRegs);
     if (e != cudaSuccess) return e;
     const int64_t units = (int64_t)a.B * a.Hkv * ((qt.tiles + NT - 1) / NT);
@@ -630,7 +632,7 @@ cudaError_t consider(const CrossArgs &a, const TilesOf<BAND> &qt, Plan *best) {
 
 template <int NT, bool BAND>
 cudaError_t fwd(const CrossArgs &a, const TilesOf<BAND> &qt, int c) {
-    using C = Cfg<NT>;
+    using C = Cfg<NT, BAND>;
     FwdMmaArgs<BAND> f;
     f.qt = qt;
     if (!make_tensor(&f.q, a.Q, a.B, a.Hq, a.Nq, qt.nb, qt.gb) || !make_tensor(&f.k, a.K, a.B, a.Hkv, a.Nk, kTileRows, 1) ||
