@@ -54,9 +54,10 @@ struct Cfg {
     static constexpr int kCopyWarp = kSoftmaxWarps, kKeysWarp = kSoftmaxWarps + 1;
     static constexpr int kScoreWarp = kSoftmaxWarps + 2, kValueWarp = kSoftmaxWarps + 3;
     static constexpr int kThreads = 32 * (kSoftmaxWarps + 4);   // whole warp groups
-    static constexpr int kStages = NT == 2 ? 5 : 2;
+    static constexpr int kQueries = BAND ? 2 : 1;      // units whose queries are held
+    static constexpr int kStages = NT == 1 ? 2 : BAND ? 4 : 5;
     static constexpr uint32_t kCols = NT * 256;        // S 128, P 64, O 64 a tile
-    static constexpr size_t kSmem = 1024 + NT * kTileBytes + kStages * 2 * kTileBytes;
+    static constexpr size_t kSmem = 1024 + kQueries * NT * kTileBytes + kStages * 2 * kTileBytes;
     static constexpr int kMinBlocks = NT == 2 ? 1 : 2;
     static constexpr bool kWalks = NT == 1 || BAND;    // one wave of CTAs for all units
     // registers a thread: at launch, and after the softmax warps took what the others gave
@@ -78,6 +79,7 @@ struct FwdMmaArgs {
     float c;                 // |scale| log2 e (> 0)
     int negative;            // scale < 0
     Band band;               // BAND
+    TensorArg o;             // BAND, tiles of 128 queries: O as tensor copies write it
     FwdMmaArgs() : qt(1, 1, false) {}
 };
 
@@ -154,8 +156,8 @@ cross_fwd_mma_kernel(const __grid_constant__ FwdMmaArgs<BAND> a) {
     using Where = Place<NT, BAND>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
-    uint8_t *sq = smem, *skv = smem + NT * kTileBytes;   // stage s: K at skv + 2 s tiles, V behind it
-    __shared__ uint64_t bar_q, bar_qfree, bar_full[C::kStages], bar_ready[C::kStages], bar_empty[C::kStages];
+    uint8_t *sq = smem, *skv = smem + C::kQueries * NT * kTileBytes;   // stage s: K at skv + 2 s tiles, V behind it
+    __shared__ uint64_t bar_q[C::kQueries], bar_qfree[C::kQueries], bar_full[C::kStages], bar_ready[C::kStages], bar_empty[C::kStages];
     __shared__ uint64_t bar_s[NT], bar_sfree[NT], bar_p[NT], bar_o[NT], bar_end[2];
     __shared__ uint64_t bar_unit[2], bar_unitfree[2];
     __shared__ Work units[2];       // of a CTA that walks, in turn; n < 0: no more
@@ -174,8 +176,10 @@ cross_fwd_mma_kernel(const __grid_constant__ FwdMmaArgs<BAND> a) {
     const Where first_place(a, first);
 
     if (threadIdx.x == 0) {
-        mbar_init(&bar_q, 1);
-        mbar_init(&bar_qfree, 1);
+        for (int i = 0; i < C::kQueries; ++i) {
+            mbar_init(&bar_q[i], 1);
+            mbar_init(&bar_qfree[i], BAND ? 1 + NT : 1);
+        }
         for (int s = 0; s < C::kStages; ++s) {
             mbar_init(&bar_full[s], 1);
             mbar_init(&bar_ready[s], 1);
@@ -239,9 +243,23 @@ cross_fwd_mma_kernel(const __grid_constant__ FwdMmaArgs<BAND> a) {
         const uint32_t ts = col_s + t * 128 + 64 * half + lanes, tp = col_p + t * 64 + 32 * half + lanes;
         const uint32_t to = col_o + t * 64 + 32 * half + lanes;
         int it = 0, skipped = 0;
+        // BAND: the unit's O leaves by a tensor copy from where its queries were.  `loaded` counts units with queries;
+        // one thread of a tile stores, and hands the place on when it has been read.
+        int loaded = 0, held = -1;
+        const auto hand_on = [&] {
+            if (held < 0) return;
+            stores_read();
+            mbar_arrive(&bar_qfree[held]);
+            held = -1;
+        };
         each([&](const Work &u) {
             if (t >= u.nt) {
                 skipped += u.n;
+                if (BAND && u.n > 0) {
+                    hand_on();
+                    if (threadIdx.x == 256 * t) mbar_arrive(&bar_qfree[loaded % C::kQueries]);
+                    ++loaded;
+                }
                 return;
             }
             const int n = u.n, whole = a.ks.mask ? 0 : u.bound / kTileRows - u.lo;   // the tiles attended wholly come first
@@ -335,6 +353,10 @@ cross_fwd_mma_kernel(const __grid_constant__ FwdMmaArgs<BAND> a) {
                 tc_before_sync();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bar_p[t]);
+                if (BAND && j == 0) {
+                    hand_on();
+                    __syncwarp();
+                }
             }
             if (n > 0) {
                 sum_of[half][at] = l;
@@ -348,6 +370,33 @@ cross_fwd_mma_kernel(const __grid_constant__ FwdMmaArgs<BAND> a) {
             } else {
 #pragma unroll
                 for (int k = 0; k < 32; ++k) o[k] = 0u;
+            }
+            if (BAND && n > 0 && CS == 1) {
+                const int place = loaded++ % C::kQueries;
+                if (a.qt.nb == kTileRows) {
+                    uint8_t *tile = sq + (place * NT + t) * kTileBytes;
+                    const float inv = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        uint32_t w[4];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            w[k] = pack_bf16x2(__uint_as_float(o[8 * i + 2 * k]) * inv, __uint_as_float(o[8 * i + 2 * k + 1]) * inv);
+                        *reinterpret_cast<uint4 *>(tile + r * 128 + (((4 * half + i) ^ (r & 7)) << 4)) =
+                            make_uint4(w[0], w[1], w[2], w[3]);
+                    }
+                    fence_smem_async();
+                    named_sync(13 + t, 256);
+                    const int q = a.qt.first_row(u.t0 + t), h = u.hk * a.qt.G + a.qt.first_head(u.t0 + t);
+                    if (threadIdx.x == 256 * t && FIBATT_CHECKED(h < a.Hq && u.b >= 0 && q < a.qt.Nq)) {
+                        tile_store(&a.o.map, q, h * a.o.head_step, u.b * a.o.seq_step, tile);
+                        held = place;
+                    }
+                    if (half == 0 && q + r < a.qt.Nq)
+                        a.LSE[((int64_t)u.b * a.Hq + h) * a.qt.Nq + q + r] = l == 0.f ? kNegInf : (m + log2f(l)) * kLn2;
+                    return;
+                }
+                if (threadIdx.x == 256 * t) mbar_arrive(&bar_qfree[place]);
             }
             if (CS == 1) {
                 int g, q;
@@ -381,6 +430,7 @@ cross_fwd_mma_kernel(const __grid_constant__ FwdMmaArgs<BAND> a) {
                 }
             }
         });
+        if (BAND && held >= 0) stores_done();
     } else {
         give_registers<C::kRegsFew>();
         if (warp == C::kCopyWarp) {
@@ -388,17 +438,22 @@ cross_fwd_mma_kernel(const __grid_constant__ FwdMmaArgs<BAND> a) {
             int ring = 0, loaded = 0;      // issued: key tiles, units' queries
             bool ok = true;
             const auto queries = [&](const Work &u) {
+                uint64_t *bar = &bar_q[loaded % C::kQueries];
+                uint8_t *dst = sq + loaded % C::kQueries * NT * kTileBytes;
                 if (elect_one()) {
-                    mbar_expect_tx(&bar_q, u.nt * a.qt.bytes());
+                    mbar_expect_tx(bar, u.nt * a.qt.bytes());
                     for (int t = 0; t < u.nt; ++t)
-                        load_tile(sq + t * kTileBytes, a.q, a.qt.first_row(u.t0 + t), u.hk * a.qt.G + a.qt.first_head(u.t0 + t),
-                                  u.b, &bar_q);
+                        load_tile(dst + t * kTileBytes, a.q, a.qt.first_row(u.t0 + t), u.hk * a.qt.G + a.qt.first_head(u.t0 + t),
+                                  u.b, bar);
                 }
                 __syncwarp();
                 ++loaded;
             };
             const auto copies = [&](const Work &u) {
-                const bool later = C::kWalks && loaded > 0;
+                // (with one place for queries: behind the first keys, once the scores have read the last queries)
+                const bool later = C::kWalks && !BAND && loaded > 0;
+                if (BAND && u.n > 0 && loaded >= C::kQueries)
+                    ok = pipe_wait(&bar_qfree[loaded % C::kQueries], (loaded / C::kQueries - 1) & 1, abort);
                 for (int j = 0; ok && j < u.n; ++j) {
                     if (j == 0 && !later) queries(u);
                     const int s = ring % C::kStages;
@@ -411,8 +466,8 @@ cross_fwd_mma_kernel(const __grid_constant__ FwdMmaArgs<BAND> a) {
                     }
                     __syncwarp();
                     ++ring;
-                    if (j == 0 && later) {      // once the scores have read the last queries
-                        ok = pipe_wait(&bar_qfree, (loaded - 1) & 1, abort);
+                    if (j == 0 && later) {
+                        ok = pipe_wait(&bar_qfree[0], (loaded - 1) & 1, abort);
                         if (ok) queries(u);
                     }
                 }
@@ -438,7 +493,8 @@ cross_fwd_mma_kernel(const __grid_constant__ FwdMmaArgs<BAND> a) {
             }
             // leave no copy in flight
             if (lane == 0) {
-                if (loaded > 0) mbar_drain(&bar_q, (loaded - 1) & 1);
+                for (int i = max(0, loaded - C::kQueries); i < loaded; ++i)
+                    mbar_drain(&bar_q[i % C::kQueries], (i / C::kQueries) & 1);
                 for (int i = max(0, ring - C::kStages); i < ring; ++i)
                     mbar_drain(&bar_full[i % C::kStages], (i / C::kStages) & 1);
             }
@@ -480,7 +536,8 @@ cross_fwd_mma_kernel(const __grid_constant__ FwdMmaArgs<BAND> a) {
                 int loaded = 0;
                 each([&](const Work &u) {
                     const int n = __shfl_sync(kFullMask, u.n, 0), nt = __shfl_sync(kFullMask, u.nt, 0);
-                    if (n > 0) pipe_wait(&bar_q, loaded++ & 1, abort);
+                    const int place = loaded % C::kQueries;
+                    if (n > 0) pipe_wait(&bar_q[place], (loaded++ / C::kQueries) & 1, abort);
                     for (int j = 0; j < n; ++j) {
                         pipe_wait(&bar_full[s], pass, abort);      // masked keys' scores are not looked at
                         const uint64_t dks = dk + (uint64_t)(s * (2 * kTileBytes >> 4));
@@ -492,13 +549,13 @@ cross_fwd_mma_kernel(const __grid_constant__ FwdMmaArgs<BAND> a) {
                             if (it[t] > 0) pipe_wait(&bar_sfree[t], (it[t] - 1) & 1, abort);
                             ++it[t];
                             tc_after_sync();
-                            const uint64_t dqt = dq + (uint64_t)(t * (kTileBytes >> 4));
+                            const uint64_t dqt = dq + (uint64_t)((place * NT + t) * (kTileBytes >> 4));
                             if (elect_one()) {
 #pragma unroll
                                 for (int i = 0; i < 4; ++i)
                                     mma_ss(col_s + t * 128, dqt + i * kStepRowwise, dks + i * kStepRowwise, id, i > 0);
                                 mma_commit(&bar_s[t]);
-                                if (j == n - 1 && t == nt - 1) mma_commit(&bar_qfree);
+                                if (j == n - 1 && t == nt - 1) mma_commit(&bar_qfree[place]);
                             }
                             __syncwarp();
                         }
@@ -638,6 +695,7 @@ cudaError_t fwd(const CrossArgs &a, const TilesOf<BAND> &qt, int c) {
     if (!make_tensor(&f.q, a.Q, a.B, a.Hq, a.Nq, qt.nb, qt.gb) || !make_tensor(&f.k, a.K, a.B, a.Hkv, a.Nk, kTileRows, 1) ||
         !make_tensor(&f.v, a.V, a.B, a.Hkv, a.Nk, kTileRows, 1))
         return cudaErrorInvalidValue;
+    if (BAND && qt.nb == kTileRows && !make_tensor(&f.o, a.O, a.B, a.Hq, a.Nq, kTileRows, 1)) return cudaErrorInvalidValue;
     f.ks = a.keys;
     f.band = a.band;
     f.O = rows_of<__nv_bfloat16>(a.O);

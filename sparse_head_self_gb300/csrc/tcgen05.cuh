@@ -211,6 +211,17 @@ __device__ __forceinline__ void tile_load(void *dst, const CUtensorMap *map, int
         "l"(map), "r"(0), "r"(row), "r"(head), "r"(seq), "r"(smem_u32(bar))
         : "memory");
 }
+// The box back to memory (rows behind the tensor's end are left out), as one of the
+// thread's bulk operations; waits for its operations: until they have read shared
+// memory, until they are complete.
+__device__ __forceinline__ void tile_store(const CUtensorMap *map, int row, int head, int seq, const void *src) {
+    asm volatile("cp.async.bulk.tensor.4d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3, %4}], [%5];" ::"l"(map), "r"(0),
+                 "r"(row), "r"(head), "r"(seq), "r"(smem_u32(src))
+                 : "memory");
+    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+__device__ __forceinline__ void stores_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+__device__ __forceinline__ void stores_done() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 __device__ __forceinline__ void prefetch_map(const CUtensorMap *map) {
     asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
 }
