@@ -50,16 +50,17 @@ constexpr int kJoinLd = 68;      // floats between rows of a partial O in shared
 
 template <int NT, bool BAND>
 struct Cfg {
+    static_assert(NT == 1 || !BAND, "two tiles of a window's queries are two CTAs");
     static constexpr int kSoftmaxWarps = 8 * NT;
     static constexpr int kCopyWarp = kSoftmaxWarps, kKeysWarp = kSoftmaxWarps + 1;
     static constexpr int kScoreWarp = kSoftmaxWarps + 2, kValueWarp = kSoftmaxWarps + 3;
     static constexpr int kThreads = 32 * (kSoftmaxWarps + 4);   // whole warp groups
     static constexpr int kQueries = BAND ? 2 : 1;      // units whose queries are held
-    static constexpr int kStages = NT == 1 ? 2 : BAND ? 4 : 5;
+    static constexpr int kStages = NT == 2 ? 5 : 2;
     static constexpr uint32_t kCols = NT * 256;        // S 128, P 64, O 64 a tile
     static constexpr size_t kSmem = 1024 + kQueries * NT * kTileBytes + kStages * 2 * kTileBytes;
     static constexpr int kMinBlocks = NT == 2 ? 1 : 2;
-    static constexpr bool kWalks = NT == 1 || BAND;    // one wave of CTAs for all units
+    static constexpr bool kWalks = NT == 1;            // one wave of CTAs for all units
     // registers a thread: at launch, and after the softmax warps took what the others gave
     static constexpr int kRegs = NT == 2 ? 96 : 80, kRegsFew = 32, kRegsMany = NT == 2 ? 112 : 104;
     static_assert(2 * NT * kRegsMany + kRegsFew == (2 * NT + 1) * kRegs, "the shares add up");
@@ -160,6 +161,8 @@ cross_fwd_mma_kernel(const __grid_constant__ FwdMmaArgs<BAND> a) {
     __shared__ uint64_t bar_q[C::kQueries], bar_qfree[C::kQueries], bar_full[C::kStages], bar_ready[C::kStages], bar_empty[C::kStages];
     __shared__ uint64_t bar_s[NT], bar_sfree[NT], bar_p[NT], bar_o[NT], bar_end[2];
     __shared__ uint64_t bar_unit[2], bar_unitfree[2];
+    __shared__ __align__(16) uint4 drawn[2];    // BAND: the hardware's answers, in turn
+    __shared__ uint64_t bar_drawn[2];
     __shared__ Work units[2];       // of a CTA that walks, in turn; n < 0: no more
     __shared__ uint4 keys[C::kStages];
     __shared__ uint32_t tmem_base;
@@ -178,7 +181,7 @@ cross_fwd_mma_kernel(const __grid_constant__ FwdMmaArgs<BAND> a) {
     if (threadIdx.x == 0) {
         for (int i = 0; i < C::kQueries; ++i) {
             mbar_init(&bar_q[i], 1);
-            mbar_init(&bar_qfree[i], BAND ? 1 + NT : 1);
+            mbar_init(&bar_qfree[i], BAND ? 2 : 1);
         }
         for (int s = 0; s < C::kStages; ++s) {
             mbar_init(&bar_full[s], 1);
@@ -194,6 +197,7 @@ cross_fwd_mma_kernel(const __grid_constant__ FwdMmaArgs<BAND> a) {
         for (int i = 0; i < 2; ++i) {
             mbar_init(&bar_end[i], 1);
             mbar_init(&bar_unit[i], 1);
+            mbar_init(&bar_drawn[i], 1);
             mbar_init(&bar_unitfree[i], C::kSoftmaxWarps + 3);
         }
         abort_flag = 0;
@@ -218,8 +222,8 @@ cross_fwd_mma_kernel(const __grid_constant__ FwdMmaArgs<BAND> a) {
             for (int k = 0;; ++k) {
                 bool go = pipe_wait(&bar_unit[k & 1], (k >> 1) & 1, abort);
                 __syncwarp();
-                // the softmax warps of a tile meet at barriers within a unit: all of them go on, or none
-                if (warp < C::kSoftmaxWarps) go = all_of(NT == 1 ? 2 : 11 + (warp >> 3), 32 * 8, go);
+                // the softmax warps meet at barriers within a unit: all of them go on, or none
+                if (warp < C::kSoftmaxWarps) go = all_of(2, 32 * C::kSoftmaxWarps, go);
                 if (!go || units[k & 1].n < 0) break;
                 body(units[k & 1]);
                 __syncwarp();
@@ -244,7 +248,7 @@ cross_fwd_mma_kernel(const __grid_constant__ FwdMmaArgs<BAND> a) {
         const uint32_t to = col_o + t * 64 + 32 * half + lanes;
         int it = 0, skipped = 0;
         // BAND: the unit's O leaves by a tensor copy from where its queries were.  `loaded` counts units with queries;
-        // one thread of a tile stores, and hands the place on when it has been read.
+        // one thread stores, and hands the place on when it has been read.
         int loaded = 0, held = -1;
         const auto hand_on = [&] {
             if (held < 0) return;
@@ -255,11 +259,6 @@ cross_fwd_mma_kernel(const __grid_constant__ FwdMmaArgs<BAND> a) {
         each([&](const Work &u) {
             if (t >= u.nt) {
                 skipped += u.n;
-                if (BAND && u.n > 0) {
-                    hand_on();
-                    if (threadIdx.x == 256 * t) mbar_arrive(&bar_qfree[loaded % C::kQueries]);
-                    ++loaded;
-                }
                 return;
             }
             const int n = u.n, whole = a.ks.mask ? 0 : u.bound / kTileRows - u.lo;   // the tiles attended wholly come first
@@ -374,7 +373,7 @@ cross_fwd_mma_kernel(const __grid_constant__ FwdMmaArgs<BAND> a) {
             if (BAND && n > 0 && CS == 1) {
                 const int place = loaded++ % C::kQueries;
                 if (a.qt.nb == kTileRows) {
-                    uint8_t *tile = sq + (place * NT + t) * kTileBytes;
+                    uint8_t *tile = sq + place * kTileBytes;
                     const float inv = l == 0.f ? 0.f : 1.f / l;
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
@@ -386,9 +385,9 @@ cross_fwd_mma_kernel(const __grid_constant__ FwdMmaArgs<BAND> a) {
                             make_uint4(w[0], w[1], w[2], w[3]);
                     }
                     fence_smem_async();
-                    named_sync(13 + t, 256);
+                    named_sync(2, 32 * C::kSoftmaxWarps);
                     const int q = a.qt.first_row(u.t0 + t), h = u.hk * a.qt.G + a.qt.first_head(u.t0 + t);
-                    if (threadIdx.x == 256 * t && FIBATT_CHECKED(h < a.Hq && u.b >= 0 && q < a.qt.Nq)) {
+                    if (threadIdx.x == 0 && FIBATT_CHECKED(h < a.Hq && u.b >= 0 && q < a.qt.Nq)) {
                         tile_store(&a.o.map, q, h * a.o.head_step, u.b * a.o.seq_step, tile);
                         held = place;
                     }
@@ -396,7 +395,7 @@ cross_fwd_mma_kernel(const __grid_constant__ FwdMmaArgs<BAND> a) {
                         a.LSE[((int64_t)u.b * a.Hq + h) * a.qt.Nq + q + r] = l == 0.f ? kNegInf : (m + log2f(l)) * kLn2;
                     return;
                 }
-                if (threadIdx.x == 256 * t) mbar_arrive(&bar_qfree[place]);
+                if (threadIdx.x == 0) mbar_arrive(&bar_qfree[place]);
             }
             if (CS == 1) {
                 int g, q;
@@ -449,13 +448,26 @@ cross_fwd_mma_kernel(const __grid_constant__ FwdMmaArgs<BAND> a) {
                 __syncwarp();
                 ++loaded;
             };
+            // BAND: the next unit is that of a CTA that has not started, which the hardware strikes off for us.  It
+            // is asked for ahead of the last copies of this one.
+            int asked = 0;
+            const auto ask = [&] {
+                if (lane == 0) {
+                    fence_smem_async();
+                    draw_cta(&drawn[asked & 1], &bar_drawn[asked & 1]);
+                }
+                ++asked;
+                __syncwarp();
+            };
             const auto copies = [&](const Work &u) {
                 // (with one place for queries: behind the first keys, once the scores have read the last queries)
                 const bool later = C::kWalks && !BAND && loaded > 0;
                 if (BAND && u.n > 0 && loaded >= C::kQueries)
                     ok = pipe_wait(&bar_qfree[loaded % C::kQueries], (loaded / C::kQueries - 1) & 1, abort);
+                if (BAND && CS == 1 && u.n <= 1) ask();
                 for (int j = 0; ok && j < u.n; ++j) {
                     if (j == 0 && !later) queries(u);
+                    if (BAND && CS == 1 && u.n > 1 && j == u.n - 1) ask();
                     const int s = ring % C::kStages;
                     ok = ring < C::kStages || pipe_wait(&bar_empty[s], (ring / C::kStages - 1) & 1, abort);
                     if (!ok) break;
@@ -476,6 +488,15 @@ cross_fwd_mma_kernel(const __grid_constant__ FwdMmaArgs<BAND> a) {
 #pragma unroll 1
                 for (int k = 0, unit = first; ok; ++k, unit += step) {
                     Work u;
+                    if (BAND && k > 0) {
+                        unit = a.units;
+                        if (CS == 1) {
+                            ok = pipe_wait(&bar_drawn[(k - 1) & 1], ((k - 1) >> 1) & 1, abort);
+                            if (!ok) break;
+                            const int next = drawn_cta(&drawn[(k - 1) & 1]);
+                            if (next >= 0) unit = next;
+                        }
+                    }
                     if (unit < a.units) u = Work(a, k ? Where(a, unit) : first_place);
                     else u.n = -1;
                     ok = k < 2 || pipe_wait(&bar_unitfree[k & 1], ((k >> 1) - 1) & 1, abort);
@@ -493,6 +514,7 @@ cross_fwd_mma_kernel(const __grid_constant__ FwdMmaArgs<BAND> a) {
             }
             // leave no copy in flight
             if (lane == 0) {
+                for (int i = max(0, asked - 2); i < asked; ++i) mbar_drain(&bar_drawn[i & 1], (i >> 1) & 1);
                 for (int i = max(0, loaded - C::kQueries); i < loaded; ++i)
                     mbar_drain(&bar_q[i % C::kQueries], (i / C::kQueries) & 1);
                 for (int i = max(0, ring - C::kStages); i < ring; ++i)
@@ -544,8 +566,6 @@ cross_fwd_mma_kernel(const __grid_constant__ FwdMmaArgs<BAND> a) {
 #pragma unroll
                         for (int t = 0; t < NT; ++t) {   // S_t = Q_t K_j^T
                             if (t >= nt) break;
-                            // the CTA's first tile: its second softmax begins behind the first, and stays there
-                            if (BAND && t == 1 && it[0] == 1 && it[1] == 0) pipe_wait(&bar_p[0], 0, abort);
                             if (it[t] > 0) pipe_wait(&bar_sfree[t], (it[t] - 1) & 1, abort);
                             ++it[t];
                             tc_after_sync();
@@ -708,7 +728,7 @@ cudaError_t fwd(const CrossArgs &a, const TilesOf<BAND> &qt, int c) {
     f.negative = a.scale < 0.f;
     const int64_t units = (int64_t)a.B * a.Hkv * f.pairs;
     f.units = (int)units;
-    const int64_t grid = c > 1 || !C::kWalks ? units * c : std::min<int64_t>(units, C::kMinBlocks * sm_count());
+    const int64_t grid = c > 1 || !C::kWalks || BAND ? units * c : std::min<int64_t>(units, C::kMinBlocks * sm_count());
     return launch_clusters(cross_fwd_mma_kernel<NT, BAND>, (unsigned)grid, c, C::kThreads, C::kSmem, a.stream, f);
 }
 
@@ -717,9 +737,11 @@ cudaError_t launch(const CrossArgs &a) {
     const TilesOf<BAND> qt(a.Hq / a.Hkv, a.Nq, a.Hq > 1 && a.Q.stride_h == 0);
     Plan plan;
     cudaError_t e = consider<1, BAND>(a, qt, &plan);
-    if (e == cudaSuccess) e = consider<2, BAND>(a, qt, &plan);
-    if (e != cudaSuccess) return e;
-    return plan.nt == 2 ? fwd<2, BAND>(a, qt, plan.c) : fwd<1, BAND>(a, qt, plan.c);
+    if constexpr (!BAND) {
+        if (e == cudaSuccess) e = consider<2, BAND>(a, qt, &plan);
+        if (e == cudaSuccess && plan.nt == 2) return fwd<2, BAND>(a, qt, plan.c);
+    }
+    return e == cudaSuccess ? fwd<1, BAND>(a, qt, plan.c) : e;
 }
 
 }  // namespace

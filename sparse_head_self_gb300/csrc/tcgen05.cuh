@@ -200,6 +200,29 @@ __device__ __forceinline__ void mma_commit(uint64_t *bar) {
                  : "memory");
 }
 
+// ---- CTAs that have not started -----------------------------------------------------
+// Strikes one of the grid's off, whose work the caller then has; the answer and 16
+// bytes of the barrier's phase come when it is decided.  Not to be asked again once
+// there was none.
+__device__ __forceinline__ void draw_cta(uint4 *answer, uint64_t *bar) {
+    mbar_expect_tx(bar, 16);
+    asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
+                     smem_u32(answer)),
+                 "r"(smem_u32(bar))
+                 : "memory");
+}
+// Its number along x, -1: there was none.
+__device__ __forceinline__ int drawn_cta(const uint4 *answer) {
+    int x;
+    asm volatile(
+        "{ .reg .b128 r; .reg .pred p; ld.shared.b128 r, [%1]; clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, r; "
+        "mov.b32 %0, -1; @p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %0, r; }"
+        : "=r"(x)
+        : "r"(smem_u32(answer))
+        : "memory");
+    return x;
+}
+
 // ---- tiled tensor copies -------------------------------------------------------
 // A box of the 4-D tensor (element, row, head, sequence) to shared memory.
 // The element coordinate is always 0; rows and heads behind the tensor's end
