@@ -209,23 +209,22 @@ __global__ void __launch_bounds__(kStoreThreads) cache_load_kernel(const __grid_
 // ---- attention ---------------------------------------------------------------------
 // Up to 16 rows (query heads of a key head by tokens) read a sequence's pages once, and
 // the time is that of reading them.  A cluster of CTAs takes such a block of rows, its
-// warps every so many-th page each: a warp has its own ring of stages, which a bulk copy
-// of 8 KB fills, and keeps the running maximum, sum and weighted values of its own
-// keys until the end, when they are joined in shared memory and over the cluster,
-// in a fixed order.
+// pairs of warps every so many-th page each: a pair has a ring of stages of its own, which bulk
+// copies of 8 KB fill, a warp 32 tokens of each page, of which it keeps the running maximum, sum and
+// weighted values until the end, when the warps are joined in shared memory and the
+// CTAs over the cluster, in a fixed order.
 //
 // Scores and weighted values are warp-wide products of halves: an e4m3 value is
 // one exactly, a bf16 query too, after a power of two has moved its row's largest to
 // [2^8, 2^9) (32-bit queries and weights are two halves, 22 bits), a 16-bit call's weight is rounded to
-// 11 bits.  The layout of a page makes every operand's fragment a piece of 16 bytes in
-// it: lane (g, c) of a product has keys 16 (g / 2) + 2 t + (g mod 2) of tile t with
+// 11 bits.  The layout of a page makes every operand's fragment one piece of
+// it: lane (g, c) of a product has keys 8 (g / 2) + 2 t + (g mod 2) of its 32 in tile t with
 // dims 16 c to 16 c + 15, four at a time in the order in which the rows have them;
-// its scores are then those of keys 16 c to 16 c + 15, and its 16 bytes of a dim's line of values
+// its scores are then those of keys 8 c to 8 c + 7, and its 8 bytes of a dim's line of values
 // are those same keys.  No shuffles, and no conflicts in shared memory.
-constexpr int kWarps = 4, kStages = 3;
-constexpr int kThreads = 32 * kWarps;
-constexpr int kBlocks = 2;                           // CTAs a SM
-constexpr size_t kSmem = 128 + (size_t)kWarps * kStages * 2 * kPageBytes;
+constexpr int kPairs = 4, kStages = 3;
+constexpr int kWarps = 2 * kPairs, kThreads = 32 * kWarps;
+constexpr size_t kSmem = 128 + (size_t)kPairs * kStages * 2 * kPageBytes;
 constexpr float kLift = 7.f;                         // weights are held times 2^7, ...
 constexpr float kRaise = 15.f;                       // and stay below 2^15: within a half's range, far from its smallest step
 
@@ -238,8 +237,7 @@ struct AttendArgs {
 };
 
 __device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
@@ -255,11 +253,11 @@ __device__ __forceinline__ float2 unpack_f16x2(uint32_t h) {
 }
 __device__ __forceinline__ void store2(__nv_bfloat16 *p, float2 v) { *reinterpret_cast<uint32_t *>(p) = pack_bf16x2(v.x, v.y); }
 __device__ __forceinline__ void store2(float *p, float2 v) { *reinterpret_cast<float2 *>(p) = v; }
-__device__ __forceinline__ void load4(const __nv_bfloat16 *p, float (&x)[4]) {
+__device__ __forceinline__ void load4(const __nv_bfloat16 *p, float *x) {
     const uint2 t = __ldg(reinterpret_cast<const uint2 *>(p));
     x[0] = bf16_lo(t.x), x[1] = bf16_hi(t.x), x[2] = bf16_lo(t.y), x[3] = bf16_hi(t.y);
 }
-__device__ __forceinline__ void load4(const float *p, float (&x)[4]) {
+__device__ __forceinline__ void load4(const float *p, float *x) {
     const float4 t = __ldg(reinterpret_cast<const float4 *>(p));
     x[0] = t.x, x[1] = t.y, x[2] = t.z, x[3] = t.w;
 }
@@ -270,65 +268,79 @@ __device__ __forceinline__ uint32_t bytes_of(uint32_t four) {
 
 // HALVES: 1 (at most 8 rows; the products' lower rows are not looked at) or 2.
 template <typename T, int HALVES>
-__global__ void __launch_bounds__(kThreads, kBlocks)
+struct Attend {
+    static constexpr int kParts = sizeof(T) == 4 ? 2 : 1;             // halves of an operand
+    static constexpr int kBlocks = kParts * HALVES == 4 ? 1 : 2;      // CTAs a SM
+};
+
+template <typename T, int HALVES>
+__global__ void __launch_bounds__(kThreads, Attend<T, HALVES>::kBlocks)
 cache_fwd_kernel(const __grid_constant__ AttendArgs a, Rows<const T> Q, Rows<T> O) {
-    constexpr int R = 8 * HALVES, kParts = sizeof(T) == 4 ? 2 : 1;     // halves of an operand
+    constexpr int R = 8 * HALVES, kParts = Attend<T, HALVES>::kParts;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *ring = smem_raw + ((128 - (smem_u32(smem_raw) & 127)) & 127);
-    __shared__ uint64_t full[kWarps][kStages];
-    __shared__ float2 scale_of[kWarps][kStages];      // of a stage's keys and values; 0: no page
+    __shared__ uint64_t full[kPairs][kStages];
     __shared__ int abort_flag;
-    __shared__ float sm[kWarps][R], sl[kWarps][R];
+    __shared__ float sm[kWarps][R], sl[kWarps][R], sf[kWarps][R];     // the warps' maxima, sums and factors
     __shared__ float cm[R], cl[R];                    // the CTA's, read by the cluster
     __shared__ float2 co[R][32];
+    __shared__ float inv_of[R];                       // a row's 1 / sum, 0 for one that attends nothing
     static_assert(kWarps * R * 32 * sizeof(float2) <= kSmem - 128, "the warps' sums fit");
     volatile int *abort = &abort_flag;
-    const int warp = warp_number(), lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
-    const int C = (int)cluster_size(), rank = (int)cluster_rank();
-    if (threadIdx.x < kWarps * kStages) mbar_init(&full[0][0] + threadIdx.x, 1);
+    const int warp = warp_number(), pair = warp >> 1, sub = warp & 1, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
+    const unsigned C = cluster_size(), rank = cluster_rank();
+    if (threadIdx.x < kPairs * kStages) mbar_init(&full[0][0] + threadIdx.x, 1);
     if (threadIdx.x == 0) abort_flag = 0;
     __syncthreads();
     grid_dep_wait();
     grid_dep_launch();
 
-    const int unit = blockIdx.x / C, rb = unit % a.blocks, hk = unit / a.blocks % a.c.Hkv, b = unit / a.blocks / a.c.Hkv;
+    const unsigned unit = blockIdx.x / C, bh = unit / (unsigned)a.blocks;
+    const int rb = (int)(unit - bh * a.blocks), b = (int)(bh / (unsigned)a.c.Hkv), hk = (int)(bh - (unsigned)b * a.c.Hkv);
     const int r0 = 16 * rb, rows = min(R, a.rows - r0);
+    const auto token = [&](int r) { return (int)((unsigned)(r0 + r) / (unsigned)a.G); };      // of the block's row r
+    // the rows' values are on their way while the pages are looked up
+    float x[2][16];
+#pragma unroll
+    for (int i = 0; i < HALVES; ++i) {
+        const int r = min(g + 8 * i, rows - 1), n = token(r);
+        const T *src = Q.row(b, hk * a.G + (r0 + r - n * a.G), n) + 16 * c;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) load4(src + 4 * j, x[i] + 4 * j);
+    }
     const int start = a.c.first(b), n = a.c.tokens(b), end = a.c.table_len * kPage;
     // positions of the block's first and last queries that attend keys
-    const int first = max(0, start + r0 / a.G), last = min(end, start + min(n, (r0 + rows - 1) / a.G + 1)) - 1;
+    const int first = max(0, start + token(0)), last = min(end, start + min(n, token(rows - 1) + 1)) - 1;
     if (start + n > end && threadIdx.x == 0) atomicOr(&g_device_error, kErrPage);
     const BandWalk<kPage> walk(a.band, first, last);
-    const int at = rank * kWarps + warp, step = C * kWarps, mine = max(0, (walk.n - at + step - 1) / step);
-
-    // row r of the block: query head g(r) of the group at token n(r), tokens apart
+    const int at = (int)rank * kPairs + pair, step = (int)C * kPairs, mine = max(0, (walk.n - at + step - 1) / step);
     const auto position = [&](int r) {
-        const int p = start + (r0 + r) / a.G;
+        const int p = start + token(r);
         return r < rows && p <= last ? p : -1;
     };
-    // ---- copies: this warp's pages in turn
-    uint8_t *stages = ring + (size_t)warp * kStages * 2 * kPageBytes;
-    int pages = -1;                                  // of page numbers 32 and 32 on, one a lane, with its scales
-    float2 scales = make_float2(0.f, 0.f);
+
+    // ---- copies: the pair's pages in turn.  A lane has the number and the scales of every 32nd.
+    uint8_t *stages = ring + (size_t)pair * kStages * 2 * kPageBytes;
+    int pages = -1;                                  // of those being copied
+    float2 scales = make_float2(0.f, 0.f), used = scales;    // of those, and of those being used; 0: no page
     const auto issue = [&](int k) {
         if ((k & 31) == 0) {
             pages = -1;
-            scales = make_float2(0.f, 0.f);
             if (k + lane < mine) {
                 pages = a.c.page(b, walk.tile(at + (k + lane) * step));
-                if (pages >= 0) scales = __ldg(reinterpret_cast<const float2 *>(a.c.scales) + a.c.place(pages, hk));
-                else atomicOr(&g_device_error, kErrPage);
+                if (pages < 0 && sub == 0) atomicOr(&g_device_error, kErrPage);
             }
+            scales = make_float2(0.f, 0.f);
+            if (pages >= 0) scales = __ldg(reinterpret_cast<const float2 *>(a.c.scales) + a.c.place(pages, hk));
         }
         const int page = __shfl_sync(kFullMask, pages, k & 31), s = k % kStages;
-        const float sk = __shfl_sync(kFullMask, scales.x, k & 31), sv = __shfl_sync(kFullMask, scales.y, k & 31);
-        if (lane == 0) {
-            scale_of[warp][s] = page < 0 ? make_float2(0.f, 0.f) : make_float2(two_to(stored_exponent(sk)), two_to(stored_exponent(sv)));
+        if (sub == 0 && lane == 0) {
             if (page < 0) {
-                mbar_arrive(&full[warp][s]);
+                mbar_arrive(&full[pair][s]);
             } else {
-                mbar_expect_tx(&full[warp][s], 2 * kPageBytes);
+                mbar_expect_tx(&full[pair][s], 2 * kPageBytes);
                 bulk_g2s(stages + (size_t)s * 2 * kPageBytes, a.c.data + a.c.place(page, hk) * 2 * kPageBytes, 2 * kPageBytes,
-                         &full[warp][s]);
+                         &full[pair][s]);
             }
         }
         __syncwarp();
@@ -338,44 +350,29 @@ cache_fwd_kernel(const __grid_constant__ AttendArgs a, Rows<const T> Q, Rows<T> 
 
     // ---- the rows as operands of four steps of 16 dims, and what their scores are multiplied with
     uint32_t q[kParts][4][4];
-    float factor[HALVES], m[HALVES], l[HALVES], o[8][4];
+    float factor[HALVES], m[HALVES], l[HALVES], o[8][2 * HALVES];
     int p[HALVES];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-        float x[16];
-        float top = 0.f;
-        const int r = g + 8 * i;
-        if (i < HALVES && r < rows) {
-            const T *src = Q.row(b, hk * a.G + (r0 + r) % a.G, (r0 + r) / a.G) + 16 * c;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                float y[4];
-                load4(src + 4 * j, y);
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    x[4 * j + k] = y[k];
-                    top = fmaxf(top, fabsf(y[k]));
-                }
-            }
-        } else {
-#pragma unroll
-            for (int j = 0; j < 16; ++j) x[j] = 0.f;
-        }
-        top = fmaxf(top, __shfl_xor_sync(kFullMask, top, 1));
-        top = fmaxf(top, __shfl_xor_sync(kFullMask, top, 2));
-        const int e = max(-100, min(exponent_of(top), 120)) - 8;
-        const float f = two_to(-e);
+        float f = 0.f;
         if (i < HALVES) {
+            float top = 0.f;
+#pragma unroll
+            for (int k = 0; k < 16; ++k) top = fmaxf(top, fabsf(x[i][k]));
+            top = fmaxf(top, __shfl_xor_sync(kFullMask, top, 1));
+            top = fmaxf(top, __shfl_xor_sync(kFullMask, top, 2));
+            const int e = max(-100, min(exponent_of(top), 120)) - 8;
+            f = two_to(-e);
             factor[i] = a.scale_log2 * two_to(e);
             m[i] = kNegInf;
             l[i] = 0.f;
-            p[i] = position(r);
+            p[i] = position(g + 8 * i);
         }
 #pragma unroll
         for (int j = 0; j < 4; ++j)
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
-                const float u = x[4 * j + 2 * k] * f, v = x[4 * j + 2 * k + 1] * f;
+                const float u = i < HALVES ? x[i][4 * j + 2 * k] * f : 0.f, v = i < HALVES ? x[i][4 * j + 2 * k + 1] * f : 0.f;
                 const uint32_t hi = pack_f16x2(u, v);
                 q[0][j][i + 2 * k] = hi;
                 if (kParts == 2) {
@@ -387,50 +384,63 @@ cache_fwd_kernel(const __grid_constant__ AttendArgs a, Rows<const T> Q, Rows<T> 
 #pragma unroll
     for (int d = 0; d < 8; ++d)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) o[d][i] = 0.f;
+        for (int i = 0; i < 2 * HALVES; ++i) o[d][i] = 0.f;
 
-    int done = 0;
-    for (; done < mine; ++done) {
+    // (No wait's failure ends the loop: a warp's partner at the named barrier must find it there.  What
+    // follows is not trusted, since the error word is set.)
+    for (int done = 0; done < mine; ++done) {
         const int s = done % kStages;
-        if (!pipe_wait(&full[warp][s], (done / kStages) & 1, abort)) break;
+        if ((done & 31) == 0) {
+            used = make_float2(0.f, 0.f);
+            if (pages >= 0) used = make_float2(two_to(stored_exponent(scales.x)), two_to(stored_exponent(scales.y)));
+        }
+        const float sk = __shfl_sync(kFullMask, used.x, done & 31), sv = __shfl_sync(kFullMask, used.y, done & 31);
+        pipe_wait(&full[pair][s], (done / kStages) & 1, abort);
         __syncwarp();
-        const float2 scale = scale_of[warp][s];
-        if (scale.x > 0.f) {
-            const uint8_t *keys = stages + (size_t)s * 2 * kPageBytes, *values = keys + kPageBytes;
-            const int k0 = walk.tile(at + done * step) * kPage, k1 = k0 + kPage - 1;
+        if (sk > 0.f) {
+            const uint8_t *keys = stages + (size_t)s * 2 * kPageBytes + 32 * sub * kHeadDim;
+            const uint8_t *values = stages + (size_t)s * 2 * kPageBytes + kPageBytes + 32 * sub;
+            const int k0 = walk.tile(at + done * step) * kPage + 32 * sub, k1 = k0 + 31;
             const bool whole = k1 <= first && (k0 > last - a.band.window || k1 < a.band.sinks);
-            float x[8][4];
+            // (products that add to one sum lie apart: each waits for the one before it)
+            float y[4][4];
+            uint32_t four[4][4];
 #pragma unroll
-            for (int t = 0; t < 8; ++t) {
-                const uint4 w = *reinterpret_cast<const uint4 *>(keys + (16 * (g >> 1) + 2 * t + (g & 1)) * kHeadDim + 16 * c);
-                const uint32_t four[4] = {w.x, w.y, w.z, w.w};
+            for (int t = 0; t < 4; ++t) {
+                const uint4 w = *reinterpret_cast<const uint4 *>(keys + (8 * (g >> 1) + 2 * t + (g & 1)) * kHeadDim + 16 * c);
+                four[t][0] = w.x, four[t][1] = w.y, four[t][2] = w.z, four[t][3] = w.w;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) x[t][i] = 0.f;
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const uint32_t b0 = halves_of(four[j] & 0xffff), b1 = halves_of(four[j] >> 16);
-                    if (kParts == 2) mma_f16(x[t], q[kParts - 1][j], b0, b1);
-                    mma_f16(x[t], q[0][j], b0, b1);
-                }
+                for (int i = 0; i < 4; ++i) y[t][i] = 0.f;
             }
-            uint32_t live = 0xffffu;              // this lane's keys that a row of the block attends
-            uint32_t w[kParts][4][4];             // the weights as operands of four steps of 16 keys
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+#pragma unroll
+                for (int k = kParts - 1; k >= 0; --k)
+#pragma unroll
+                    for (int t = 0; t < 4; ++t)
+                        mma_f16(y[t], q[k][j], halves_of(four[t][j] & 0xffff), halves_of(four[t][j] >> 16));
+            uint2 v[8];
+#pragma unroll
+            for (int d = 0; d < 8; ++d) v[d] = *reinterpret_cast<const uint2 *>(values + (8 * d + g) * kPage + 8 * c);
+            if (!whole) {                         // a weight of 0 meets no NaN
+                const uint32_t live = keys_between(a.band, first, last, k0 + 8 * c);
+                const uint32_t lo = bytes_of(live & 15), hi = bytes_of(live >> 4 & 15);
+#pragma unroll
+                for (int d = 0; d < 8; ++d) v[d].x &= lo, v[d].y &= hi;
+            }
+            uint32_t w[kParts][2][4];             // the weights as operands of two steps of 16 keys
 #pragma unroll
             for (int i = 0; i < HALVES; ++i) {
-                const float f = factor[i] * scale.x;
-                uint32_t seen = 0xffffu;
-                if (!whole) {
-                    seen = keys_of(a.band, p[i], k0 + 16 * c);
-                    live = keys_between(a.band, first, last, k0 + 16 * c);
-                }
+                const float f = factor[i] * sk;
+                const uint32_t seen = whole ? 0xffu : keys_of(a.band, p[i], k0 + 8 * c);
                 float top = kNegInf;
 #pragma unroll
-                for (int t = 0; t < 8; ++t)
+                for (int t = 0; t < 4; ++t)
 #pragma unroll
                     for (int k = 0; k < 2; ++k) {
-                        float &y = x[t][2 * i + k];
-                        y = (seen >> (2 * t + k)) & 1 ? y * f : kNegInf;
-                        top = fmaxf(top, y);
+                        float &z = y[t][2 * i + k];
+                        z = (seen >> (2 * t + k)) & 1 ? z * f : kNegInf;
+                        top = fmaxf(top, z);
                     }
                 top = fmaxf(top, __shfl_xor_sync(kFullMask, top, 1));
                 top = fmaxf(top, __shfl_xor_sync(kFullMask, top, 2));
@@ -447,49 +457,52 @@ cache_fwd_kernel(const __grid_constant__ AttendArgs a, Rows<const T> Q, Rows<T> 
                 const float base = m[i] == kNegInf ? 0.f : m[i];
                 float sum[2] = {0.f, 0.f};
 #pragma unroll
-                for (int t = 0; t < 8; ++t) {
-                    const float u = fast_exp2(x[t][2 * i] - base), v = fast_exp2(x[t][2 * i + 1] - base);
-                    sum[t & 1] += u + v;
-                    const uint32_t hi = pack_f16x2(u, v);
+                for (int t = 0; t < 4; ++t) {
+                    const float u = fast_exp2(y[t][2 * i] - base), e = fast_exp2(y[t][2 * i + 1] - base);
+                    sum[t & 1] += u + e;
+                    const uint32_t hi = pack_f16x2(u, e);
                     w[0][t >> 1][i + 2 * (t & 1)] = hi;
                     if (kParts == 2) {
                         const float2 h = unpack_f16x2(hi);
-                        w[kParts - 1][t >> 1][i + 2 * (t & 1)] = pack_f16x2(u - h.x, v - h.y);
+                        w[kParts - 1][t >> 1][i + 2 * (t & 1)] = pack_f16x2(u - h.x, e - h.y);
                     }
                 }
                 l[i] += sum[0] + sum[1];
             }
             if (HALVES == 1) {
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
+                for (int j = 0; j < 2; ++j)
 #pragma unroll
                     for (int k = 0; k < kParts; ++k) w[k][j][1] = w[k][j][3] = 0u;
             }
+            // a page's sums by themselves, and into the running ones by additions that round
 #pragma unroll
-            for (int d = 0; d < 8; ++d) {
-                const uint4 v = *reinterpret_cast<const uint4 *>(values + (8 * d + g) * kPage + 16 * c);
-                uint32_t four[4] = {v.x, v.y, v.z, v.w};
-                if (!whole) {                     // a weight of 0 meets no NaN
+            for (int d0 = 0; d0 < 8; d0 += 4) {
+                float part[4][4];
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) four[j] &= bytes_of(live >> (4 * j) & 15);
-                }
-                // a page's sum by itself, and into the running one by an addition that rounds
-                float part[4] = {0.f, 0.f, 0.f, 0.f};
+                for (int d = 0; d < 4; ++d)
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const uint32_t b0 = halves_of(four[j] & 0xffff), b1 = halves_of(four[j] >> 16);
-                    if (kParts == 2) mma_f16(part, w[kParts - 1][j], b0, b1);
-                    mma_f16(part, w[0][j], b0, b1);
-                }
+                    for (int i = 0; i < 4; ++i) part[d][i] = 0.f;
 #pragma unroll
-                for (int i = 0; i < 2 * HALVES; ++i) o[d][i] = fmaf(part[i], scale.y, o[d][i]);
+                for (int j = 0; j < 2; ++j)
+#pragma unroll
+                    for (int k = kParts - 1; k >= 0; --k)
+#pragma unroll
+                        for (int d = 0; d < 4; ++d) {
+                            const uint32_t two = j ? v[d0 + d].y : v[d0 + d].x;
+                            mma_f16(part[d], w[k][j], halves_of(two & 0xffff), halves_of(two >> 16));
+                        }
+#pragma unroll
+                for (int d = 0; d < 4; ++d)
+#pragma unroll
+                    for (int i = 0; i < 2 * HALVES; ++i) o[d0 + d][i] = fmaf(part[d][i], sv, o[d0 + d][i]);
             }
         }
-        __syncwarp();
+        named_sync(1 + pair, 64);       // both have read the stage
         if (issued < mine) issue(issued++);
     }
-    if (lane == 0)   // leave no copy in flight
-        for (int i = done; i < issued; ++i) mbar_drain(&full[warp][i % kStages], (i / kStages) & 1);
+    if (sub == 0 && lane == 0)   // leave no copy in flight
+        for (int i = max(0, issued - kStages); i < issued; ++i) mbar_drain(&full[pair][i % kStages], (i / kStages) & 1);
     __syncthreads();      // the ring is free: it takes the warps' sums
 
     float2(*so)[R][32] = reinterpret_cast<float2(*)[R][32]>(ring);
@@ -506,46 +519,66 @@ cache_fwd_kernel(const __grid_constant__ AttendArgs a, Rows<const T> Q, Rows<T> 
         }
     }
     __syncthreads();
-    for (int i = threadIdx.x; i < rows * 32; i += kThreads) {
-        const int r = i >> 5, d = i & 31;
-        float top = kNegInf;
+    // each row's maximum, factors and sum: the CTA's, then the cluster's
+    const auto finish = [&](int r, float top, float sum) {
+        const bool none = position(r) < 0 || sum == 0.f;
+        const int n = token(r);
+        inv_of[r] = none ? 0.f : 1.f / sum;
+        if (r % C == rank)
+            a.c.LSE[((int64_t)b * a.c.Hq + hk * a.G + (r0 + r - n * a.G)) * a.c.N + n] = none ? kNegInf : (top + log2f(sum)) * kLn2;
+    };
+    if (threadIdx.x < rows) {
+        const int r = threadIdx.x;
+        float top = kNegInf, sum = 0.f;
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) top = fmaxf(top, sm[w][r]);
         const float base = top == kNegInf ? 0.f : top;
-        float sum = 0.f;
-        float2 x = make_float2(0.f, 0.f);
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) {
             const float f = fast_exp2(sm[w][r] - base);
+            sf[w][r] = f;
             sum = fmaf(f, sl[w][r], sum);
-            x = fma2(make_float2(f, f), so[w][r][d], x);
         }
-        co[r][d] = x;
-        if (d == 0) {
-            cm[r] = top;
-            cl[r] = sum;
-        }
+        cm[r] = top;
+        cl[r] = sum;
+        if (C == 1) finish(r, top, sum);
     }
+    __syncthreads();
+    const auto write = [&](int r, int d, float2 x) {
+        const int n = token(r);
+        const float inv = inv_of[r];
+        store2(O.row(b, hk * a.G + (r0 + r - n * a.G), n) + 2 * d, inv == 0.f ? make_float2(0.f, 0.f) : make_float2(x.x * inv, x.y * inv));
+    };
+    for (int i = threadIdx.x; i < rows * 32; i += kThreads) {
+        const int r = i >> 5, d = i & 31;
+        float2 x = make_float2(0.f, 0.f);
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) x = fma2(make_float2(sf[w][r], sf[w][r]), so[w][r][d], x);
+        if (C == 1) write(r, d, x);
+        else co[r][d] = x;
+    }
+    if (C == 1) return;
     cluster_sync();
     // row r is finished by CTA r mod C
+    if (threadIdx.x < rows && threadIdx.x % C == rank) {
+        const int r = threadIdx.x;
+        float top = kNegInf, sum = 0.f;
+        for (unsigned k = 0; k < C; ++k) top = fmaxf(top, ld_cluster(cluster_addr(cm + r, k)));
+        const float base = top == kNegInf ? 0.f : top;
+        for (unsigned k = 0; k < C; ++k) {
+            const float f = fast_exp2(ld_cluster(cluster_addr(cm + r, k)) - base);
+            sf[k][r] = f;
+            sum = fmaf(f, ld_cluster(cluster_addr(cl + r, k)), sum);
+        }
+        finish(r, top, sum);
+    }
+    __syncthreads();
     for (int i = threadIdx.x; i < rows * 32; i += kThreads) {
         const int r = i >> 5, d = i & 31;
         if (r % C != rank) continue;
-        float top = kNegInf;
-        for (int k = 0; k < C; ++k) top = fmaxf(top, ld_cluster(cluster_addr(cm + r, k)));
-        const float base = top == kNegInf ? 0.f : top;
-        float sum = 0.f;
         float2 x = make_float2(0.f, 0.f);
-        for (int k = 0; k < C; ++k) {
-            const float f = fast_exp2(ld_cluster(cluster_addr(cm + r, k)) - base);
-            sum = fmaf(f, ld_cluster(cluster_addr(cl + r, k)), sum);
-            x = fma2(make_float2(f, f), ld_cluster2(cluster_addr(&co[r][d], k)), x);
-        }
-        const int h = hk * a.G + (r0 + r) % a.G, at_n = (r0 + r) / a.G;
-        const bool none = position(r) < 0 || sum == 0.f;
-        const float inv = none ? 0.f : 1.f / sum;
-        store2(O.row(b, h, at_n) + 2 * d, none ? make_float2(0.f, 0.f) : make_float2(x.x * inv, x.y * inv));
-        if (d == 0) a.c.LSE[((int64_t)b * a.c.Hq + h) * a.c.N + at_n] = none ? kNegInf : (top + log2f(sum)) * kLn2;
+        for (unsigned k = 0; k < C; ++k) x = fma2(make_float2(sf[k][r], sf[k][r]), ld_cluster2(cluster_addr(&co[r][d], k)), x);
+        write(r, d, x);
     }
     cluster_sync();   // the others may still read this CTA's part
 }
@@ -554,10 +587,10 @@ template <typename T, int HALVES>
 cudaError_t attend(const AttendArgs &f) {
     const cudaError_t e = prepare_kernel<cache_fwd_kernel<T, HALVES>>(kSmem, 0);
     if (e != cudaSuccess) return e;
-    // CTAs of a cluster: as many as the GPU holds at once, as long as a warp keeps a page
+    // CTAs of a cluster: as many as the GPU holds at once, as long as a pair of warps keeps a page
     const int64_t keys = std::min<int64_t>((int64_t)f.c.table_len * kPage, (int64_t)f.band.window + f.band.sinks + f.c.N);
     int c = 1;
-    while (c < 8 && (int64_t)f.units * c * 2 <= kBlocks * sm_count() && keys > (int64_t)c * kWarps * kPage) c *= 2;
+    while (c < 8 && (int64_t)f.units * c * 2 <= Attend<T, HALVES>::kBlocks * sm_count() && keys > (int64_t)c * kPairs * kPage) c *= 2;
     return launch_clusters(cache_fwd_kernel<T, HALVES>, (unsigned)(f.units * c), c, kThreads, kSmem, f.c.stream, f,
                            rows_of<const T>(f.c.Q), rows_of<T>(f.c.O));
 }
