@@ -523,8 +523,12 @@ _pack_heads = _native.HEADS.pack
 
 def _heads_arg(name: str, t, shape, dtype, index: int) -> bytes:
     """t as a packed fibatt_heads."""
-    _check_tensor(name, t, dtype, index)
-    if t.shape != shape:
+    try:
+        good = t.dtype is dtype and t.get_device() == index and t.shape == shape
+    except AttributeError:
+        good = False
+    if not good:
+        _check_tensor(name, t, dtype, index)
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
     sb, sh, sn, sd = t.stride()
     if sd != 1:
@@ -534,16 +538,33 @@ def _heads_arg(name: str, t, shape, dtype, index: int) -> bytes:
     return _pack_heads(t.data_ptr(), sb if b > 1 else 0, sh if h > 1 else 0, sn if n > 1 else 0)
 
 
+def _numbers(name: str, t, B: int, index: int) -> int:
+    """The address of one int32 a sequence."""
+    try:
+        if t.dtype is _INT32 and t.get_device() == index and t.shape == (B,) and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    return _check_dense(name, t, (B,), _INT32, index)
+
+
+_INT32 = torch.int32
+
+
 def _attention_sizes(Q, K, V):
     """(dtype, its code, device index) of four-dim tensors Q, K, V."""
+    try:
+        dtype = Q.dtype
+        if Q.dim() == 4 and K.dim() == 4 and V.dim() == 4 and Q.is_cuda:
+            return dtype, _DTYPES[dtype], Q.get_device()
+    except (AttributeError, KeyError):
+        pass
     for name, t in (("Q", Q), ("K", K), ("V", V)):
         if not isinstance(t, torch.Tensor) or t.dim() != 4:
             raise ValueError(f"{name} must be a [B, H, N, D] tensor")
-    dtype = Q.dtype
-    code = _DTYPES.get(dtype)
-    if code is None:
-        raise ValueError(f"dtype {dtype} unsupported (float32 or bfloat16)")
-    return dtype, code, _index("Q", Q)
+    if Q.dtype not in _DTYPES:
+        raise ValueError(f"dtype {Q.dtype} unsupported (float32 or bfloat16)")
+    return Q.dtype, _DTYPES[Q.dtype], _index("Q", Q)
 
 
 def _cross_desc(Q, K, V, scale, kv_len, key_mask):
@@ -657,13 +678,11 @@ def _window_desc(Q, K, V, scale, window, sinks, q_start, kv_len):
     dtype, code, index = _attention_sizes(Q, K, V)
     B, Hq, Nq, D = shape = Q.shape
     _, Hkv, Nk, _ = K.shape
-    start = lens = 0
-    if q_start is not None:
-        start = _check_dense("q_start", q_start, (B,), torch.int32, index)
-    if kv_len is not None:
-        lens = _check_dense("kv_len", kv_len, (B,), torch.int32, index)
+    window, sinks = _band(window, sinks)
     kv_shape = (B, Hkv, Nk, D)
-    return (_native.WINDOW.pack(B, Hq, Hkv, Nq, Nk, D, code, scale, *_band(window, sinks), start, lens),
+    return (_native.WINDOW.pack(B, Hq, Hkv, Nq, Nk, D, code, scale, window, sinks,
+                                0 if q_start is None else _numbers("q_start", q_start, B, index),
+                                0 if kv_len is None else _numbers("kv_len", kv_len, B, index)),
             _heads_arg("Q", Q, shape, dtype, index), _heads_arg("K", K, kv_shape, dtype, index),
             _heads_arg("V", V, kv_shape, dtype, index), index)
 
@@ -750,26 +769,36 @@ class Cache(NamedTuple):
 
 
 def _cache_desc(cache, table, start, count, dtype, B, N, D, index):
-    """A packed fibatt_cache."""
+    """(packed fibatt_cache, key heads)."""
     data, scales = cache
-    code = _DTYPES.get(dtype)
-    if code is None:
+    try:
+        code = _DTYPES[dtype]
+        pages, Hkv, two, piece = data.shape
+        rows, entries = table.shape
+        good = (data.dtype is torch.uint8 and data.get_device() == index and (two, piece) == _CACHE_SHAPE
+                and data.is_contiguous() and scales.dtype is torch.float32 and scales.get_device() == index
+                and scales.shape == (pages, Hkv, 2) and scales.is_contiguous()
+                and table.dtype is _INT32 and table.get_device() == index and rows == B
+                and (entries == 1 or table.stride(1) == 1))
+    except (AttributeError, KeyError, ValueError):
+        good = False
+    if not good:
+        _refuse_cache(data, scales, table, dtype, B, index)
+    return _native.CACHE.pack(B, Hkv, N, D, code, pages, entries, data.data_ptr(), scales.data_ptr(), table.data_ptr(),
+                              table.stride(0) if B > 1 else 0,
+                              0 if start is None else _numbers("start", start, B, index),
+                              0 if count is None else _numbers("count", count, B, index)), Hkv
+
+
+def _refuse_cache(data, scales, table, dtype, B, index):
+    if dtype not in _DTYPES:
         raise ValueError(f"dtype {dtype} unsupported (float32 or bfloat16)")
     _check_tensor("data", data, torch.uint8, index)
     if data.dim() != 4 or data.shape[2:] != _CACHE_SHAPE or not data.is_contiguous():
         raise ValueError(f"data must be a contiguous [pages, Hkv, 2, {PAGE * HEAD_DIM}] tensor, got {tuple(data.shape)}")
-    pages, Hkv = data.shape[:2]
-    scales_ptr = _check_dense("scales", scales, (pages, Hkv, 2), torch.float32, index)
-    _check_tensor("table", table, torch.int32, index)
-    if table.dim() != 2 or table.shape[0] != B or (table.shape[1] > 1 and table.stride(1) != 1):
-        raise ValueError(f"table must be [B, pages of a sequence] with B={B} and contiguous rows, got {tuple(table.shape)}")
-    first = n = 0
-    if start is not None:
-        first = _check_dense("start", start, (B,), torch.int32, index)
-    if count is not None:
-        n = _check_dense("count", count, (B,), torch.int32, index)
-    return _native.CACHE.pack(B, Hkv, N, D, code, pages, table.shape[1], data.data_ptr(), scales_ptr, table.data_ptr(),
-                              table.stride(0) if B > 1 else 0, first, n), Hkv
+    _check_dense("scales", scales, (*data.shape[:2], 2), torch.float32, index)
+    _check_tensor("table", table, _INT32, index)
+    raise ValueError(f"table must be [B, pages of a sequence] with B={B} and contiguous rows, got {tuple(table.shape)}")
 
 
 _CACHE_SHAPE = (2, PAGE * HEAD_DIM)
@@ -825,12 +854,10 @@ def cache_fwd(Q: torch.Tensor, cache: Cache, table: torch.Tensor, start: torch.T
     at start[b] + n, to the cache that holds their keys (cache_store comes
     first); window, sinks as window_fwd; returns (O, LSE), O in Q's layout.  A
     query that count[b] leaves out attends nothing: O = 0, LSE = -inf."""
-    if not isinstance(Q, torch.Tensor) or Q.dim() != 4:
-        raise ValueError("Q must be a [B, H, N, D] tensor")
-    index = _index("Q", Q)
+    dtype, _, index = _attention_sizes(Q, Q, Q)
     B, Hq, N, D = shape = Q.shape
-    d, _ = _cache_desc(cache, table, start, count, Q.dtype, B, N, D, index)
-    return _launch(index, stream, _cache_fwd, d, Hq, scale, *_band(window, sinks), _heads_arg("Q", Q, shape, Q.dtype, index),
+    d, _ = _cache_desc(cache, table, start, count, dtype, B, N, D, index)
+    return _launch(index, stream, _cache_fwd, d, Hq, scale, *_band(window, sinks), _heads_arg("Q", Q, shape, dtype, index),
                    Q, O, LSE, index)
 
 
