@@ -90,8 +90,32 @@ __host__ __device__ __forceinline__ uint32_t queries_of(const Band &w, int k, in
     return bits_below((k < w.sinks ? end : least(end, k + w.window)) - p0) & ~bits_below(k - p0);
 }
 
-// The T-key tiles that hold the keys of the queries at positions lo to hi: first
-// those of the sinks, then the windows', as far as they are not the same.
+// The T-key tiles that hold the keys of the queries at positions lo to hi: first those of
+// the sinks, then the windows', from the oldest key in one of them on, so that they are as few as can
+// be.
+template <int T>
+struct KeyWalk {
+    int sinks, oldest, n;    // tiles of the sinks, first key behind them, tiles of the walk
+    __host__ __device__ __forceinline__ KeyWalk() {}
+    __host__ __device__ __forceinline__ KeyWalk(const Band &w, int lo, int hi) : sinks(0), oldest(0), n(0) {
+        if (lo > hi) return;
+        oldest = most(0, lo - w.window + 1);
+        sinks = (w.sinks + T - 1) / T;
+        n = sinks + (hi - oldest) / T + 1;
+        if (oldest > w.sinks && n < hi / T + 1) return;
+        sinks = oldest = 0;          // from the first key on: no more tiles than in two parts
+        n = hi / T + 1;
+    }
+    __host__ __device__ __forceinline__ int key(int i) const { return i < sinks ? i * T : oldest + (i - sinks) * T; }
+    // By which tile i's keys are attended: a tile of the sinks by them alone (its other keys come again
+    // with the windows).
+    __host__ __device__ __forceinline__ Band band(Band w, int i) const {
+        if (i < sinks) w.window = 0;
+        return w;
+    }
+};
+
+// The same in whole pages: those that hold sinks, then the others of the windows.
 template <int T>
 struct BandWalk {
     int sinks, gap, n;       // tiles of the sinks, tiles between them and the windows', tiles of the walk

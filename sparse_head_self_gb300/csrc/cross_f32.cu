@@ -146,9 +146,15 @@ struct Lane {
     __device__ __forceinline__ int col(int j, int k) const { return 8 * j + 2 * t + k; }
 };
 
-// c = A B^T: rows of A from the warp's first; columns: the first `cols` rows of B
-// (to the next 32; 0 for the others).
-__device__ __forceinline__ void nt(float (&c)[8][4], const float *A, const float *B, const Lane &l, int cols) {
+// The columns [from, cols) of a tile of keys from k0 on that 16 queries from position p on may attend.
+__device__ __forceinline__ void seen_columns(const Band &w, int p, int k0, int &from, int &cols) {
+    if (k0 >= w.sinks) from = max(0, p + 1 - w.window - k0);
+    cols = min(cols, p + 16 - k0);
+}
+
+// c = A B^T: rows of A from the warp's first; columns: rows `from` to `cols` of B
+// (from the 32 before, to the next 32; 0 for the others).
+__device__ __forceinline__ void nt(float (&c)[8][4], const float *A, const float *B, const Lane &l, int cols, int from = 0) {
 #pragma unroll
     for (int j = 0; j < 8; ++j)
 #pragma unroll
@@ -166,6 +172,7 @@ __device__ __forceinline__ void nt(float (&c)[8][4], const float *A, const float
 #pragma unroll
         for (int j = 0; j < 8; j += 4) {
             if (8 * j >= cols) break;
+            if (8 * j + 32 <= from) continue;
             float2 b[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) b[i] = *reinterpret_cast<const float2 *>(pb + 8 * (j + i) * kLd + k);
@@ -174,12 +181,13 @@ __device__ __forceinline__ void nt(float (&c)[8][4], const float *A, const float
     }
 }
 
-// o += W B over the first `rows` rows of B (to the next eight); W as nt leaves it.
-__device__ __forceinline__ void nn(float (&o)[8][4], const float (&W)[8][4], const float *B, const Lane &l, int rows) {
+// o += W B over rows `from` to `rows` of B (from the eight before, to the next eight); W as nt leaves it.
+__device__ __forceinline__ void nn(float (&o)[8][4], const float (&W)[8][4], const float *B, const Lane &l, int rows, int from = 0) {
     const float *pb = B + 2 * l.t * kLd + l.g;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
         if (8 * j >= rows) break;
+        if (8 * j + 8 <= from) continue;
         uint32_t ah[4], al[4];
         cut(W[j][0], ah[0], al[0]);
         cut(W[j][2], ah[1], al[1]);
@@ -232,13 +240,13 @@ cross_fwd_f32_kernel(int Hq, int Hkv, int Nq, KeySet ks, Band band, Rows<const f
 
     grid_dep_wait();
     const int bound = ks.bound(b);
-    int tiles = (bound + kT - 1) / kT, p[2] = {-1, -1}, first = 0, last = 0;   // positions: of the lane's rows, of the tile's
-    BandWalk<kT> walk;
+    int tiles = (bound + kT - 1) / kT, p[2] = {-1, -1}, p0 = 0, first = 0, last = 0;   // positions: of the lane's rows, of query 0, of the tile's
+    KeyWalk<kT> walk;
     if constexpr (BAND) {
-        const int p0 = band.first(b);
+        p0 = band.first(b);
         first = max(0, p0 + q0);
         last = min(bound, p0 + min(Nq, q0 + kT)) - 1;
-        walk = BandWalk<kT>(band, first, last);
+        walk = KeyWalk<kT>(band, first, last);
         tiles = walk.n;
 #pragma unroll
         for (int i = 0; i < 2; ++i)
@@ -250,18 +258,20 @@ cross_fwd_f32_kernel(int Hq, int Hkv, int Nq, KeySet ks, Band band, Rows<const f
     float m[2] = {kNegInf, kNegInf}, l[2] = {0.f, 0.f}, o[8][4];
     clear(o);
     for (int x = lo; x < hi; ++x) {
-        const int t = BAND ? walk.tile(x) : x;
-        const uint64_t ok = BAND ? band_bits(band, first, last, t * kT) : key_bits(ks, b, t * kT, bound);
+        const int k0 = BAND ? walk.key(x) : x * kT;
+        const Band w = BAND ? walk.band(band, x) : band;
+        const uint64_t ok = BAND ? band_bits(w, first, last, k0) : key_bits(ks, b, k0, bound);
         if (ok == 0) continue;
         __syncthreads();
-        stage(sk, K.row(b, hk, 0), K.sn, t * kT, ok);
-        stage(sv, V.row(b, hk, 0), V.sn, t * kT, ok);
+        stage(sk, K.row(b, hk, 0), K.sn, k0, ok);
+        stage(sv, V.row(b, hk, 0), V.sn, k0, ok);
         staged();
         __syncthreads();
         if (!mine) continue;
-        const int cols = min(kT, bound - t * kT);
+        int cols = min(kT, bound - k0), from = 0;
+        if constexpr (BAND) seen_columns(w, p0 + q0 + 16 * ln.w, k0, from, cols);
         float s[8][4];
-        nt(s, sq, sk, ln, cols);
+        nt(s, sq, sk, ln, cols, from);
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             float top = kNegInf;
@@ -270,7 +280,7 @@ cross_fwd_f32_kernel(int Hq, int Hkv, int Nq, KeySet ks, Band band, Rows<const f
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
                     float &x = s[j][2 * i + k];
-                    const bool in = BAND ? band.sees(p[i], t * kT + ln.col(j, k)) : (ok >> ln.col(j, k)) & 1;
+                    const bool in = BAND ? w.sees(p[i], k0 + ln.col(j, k)) : (ok >> ln.col(j, k)) & 1;
                     x = in ? x * scale_log2 : kNegInf;
                     top = fmaxf(top, x);
                 }
@@ -290,7 +300,7 @@ cross_fwd_f32_kernel(int Hq, int Hkv, int Nq, KeySet ks, Band band, Rows<const f
             l[i] = l[i] * keep + sum;      // this lane's columns only
             m[i] = next;
         }
-        nn(o, s, sv, ln, cols);
+        nn(o, s, sv, ln, cols, from);
     }
     l[0] = row_sum(l[0]);
     l[1] = row_sum(l[1]);
@@ -427,13 +437,13 @@ __device__ __forceinline__ void hold_queries(const BwdF32Args &a, float *smem, i
     const int hk = h / (a.Hq / a.Hkv), q0 = qt * kT;
     const float scale_log2 = a.scale * kLog2e;
     const int bound = a.ks.bound(b);
-    int tiles = (bound + kT - 1) / kT, p[2] = {-1, -1}, first = 0, last = 0;   // positions: of the lane's rows, of the tile's
-    BandWalk<kT> walk;
+    int tiles = (bound + kT - 1) / kT, p[2] = {-1, -1}, p0 = 0, first = 0, last = 0;   // positions: of the lane's rows, of query 0, of the tile's
+    KeyWalk<kT> walk;
     if constexpr (BAND) {
-        const int p0 = a.band.first(b);
+        p0 = a.band.first(b);
         first = max(0, p0 + q0);
         last = min(bound, p0 + min(a.Nq, q0 + kT)) - 1;
-        walk = BandWalk<kT>(a.band, first, last);
+        walk = KeyWalk<kT>(a.band, first, last);
         tiles = walk.n;
 #pragma unroll
         for (int i = 0; i < 2; ++i)
@@ -452,29 +462,31 @@ __device__ __forceinline__ void hold_queries(const BwdF32Args &a, float *smem, i
         st[i] = n < a.Nq ? a.stats[((int64_t)b * a.Hq + h) * a.Nq + n] : make_float2(-kNegInf, 0.f);
     }
     for (int y = lo; y < hi; ++y) {
-        const int t = BAND ? walk.tile(y) : y;
-        const uint64_t ok = BAND ? band_bits(a.band, first, last, t * kT) : key_bits(a.ks, b, t * kT, bound);
+        const int k0 = BAND ? walk.key(y) : y * kT;
+        const Band w = BAND ? walk.band(a.band, y) : a.band;
+        const uint64_t ok = BAND ? band_bits(w, first, last, k0) : key_bits(a.ks, b, k0, bound);
         if (ok == 0) continue;
         __syncthreads();
-        stage(sk, a.K.row(b, hk, 0), a.K.sn, t * kT, ok);
-        stage(sv, a.V.row(b, hk, 0), a.V.sn, t * kT, ok);
+        stage(sk, a.K.row(b, hk, 0), a.K.sn, k0, ok);
+        stage(sv, a.V.row(b, hk, 0), a.V.sn, k0, ok);
         staged();
         __syncthreads();
         if (!mine) continue;
-        const int cols = min(kT, bound - t * kT);
+        int cols = min(kT, bound - k0), from = 0;
+        if constexpr (BAND) seen_columns(w, p0 + q0 + 16 * ln.w, k0, from, cols);
         float s[8][4], dp[8][4];
-        nt(s, sq, sk, ln, cols);
-        nt(dp, sg, sv, ln, cols);
+        nt(s, sq, sk, ln, cols, from);
+        nt(dp, sg, sv, ln, cols, from);
 #pragma unroll
         for (int j = 0; j < 8; ++j)
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const float2 x = st[i >> 1];
-                const float w = exp2f(fmaf(s[j][i], scale_log2, -x.x));
-                const bool in = BAND ? a.band.sees(p[i >> 1], t * kT + ln.col(j, i & 1)) : (ok >> ln.col(j, i & 1)) & 1;
-                s[j][i] = in ? w * (dp[j][i] - x.y) : 0.f;
+                const float e = exp2f(fmaf(s[j][i], scale_log2, -x.x));
+                const bool in = BAND ? w.sees(p[i >> 1], k0 + ln.col(j, i & 1)) : (ok >> ln.col(j, i & 1)) & 1;
+                s[j][i] = in ? e * (dp[j][i] - x.y) : 0.f;
             }
-        nn(acc, s, sk, ln, cols);
+        nn(acc, s, sk, ln, cols, from);
     }
     finish(acc, sv, a.dQ, b, h, q0, a.Nq, a.scale, ln);
 }
@@ -527,10 +539,15 @@ __device__ __forceinline__ void hold_keys(const BwdF32Args &a, float *smem, floa
         staged();
         __syncthreads();
         if (!mine) continue;
-        const int cols = min(kT, a.Nq - q0);
+        int cols = min(kT, a.Nq - q0), since = 0;
+        if constexpr (BAND) {       // the queries that attend one of the warp's 16 keys
+            const int k = k0 + 16 * ln.w;
+            since = max(0, k - p0 - q0);
+            if (k >= a.band.sinks) cols = min(cols, k + 15 + a.band.window - p0 - q0);
+        }
         float p[8][4], ds[8][4];
-        nt(p, sk, sq, ln, cols);
-        nt(ds, sv, sg, ln, cols);
+        nt(p, sk, sq, ln, cols, since);
+        nt(ds, sv, sg, ln, cols, since);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
             const float4 st = *reinterpret_cast<const float4 *>(sst + ln.col(j, 0));     // of both columns
@@ -543,8 +560,8 @@ __device__ __forceinline__ void hold_keys(const BwdF32Args &a, float *smem, floa
                 ds[j][i] = on ? p[j][i] * (ds[j][i] - d) : 0.f;
             }
         }
-        nn(av, p, sg, ln, cols);
-        nn(ak, ds, sq, ln, cols);
+        nn(av, p, sg, ln, cols, since);
+        nn(ak, ds, sq, ln, cols, since);
     }
     finish(av, sg, a.dV, b, hk, k0, a.ks.Nk, 1.f, ln);
     finish(ak, sq, a.dK, b, hk, k0, a.ks.Nk, a.scale, ln);

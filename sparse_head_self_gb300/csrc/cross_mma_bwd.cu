@@ -274,7 +274,7 @@ template <>
 struct UnitBand<true> {
     int p0, first, last;     // position of query 0; of the unit's queries, held or streamed, that attend keys of it
     int chunk;               // keys held: the part of the walk that this unit has, -1: all of it
-    BandWalk<kTileRows> walk;    // held queries
+    KeyWalk<kTileRows> walk;    // held queries
     __device__ __forceinline__ UnitBand() {}
 };
 template <bool BAND>
@@ -340,7 +340,7 @@ struct Unit : UnitBand<BAND> {
         } else {
             this->first = max(0, this->p0 + a.qt.first_row(mine));
             this->last = min(end, this->p0 + a.qt.first_row(mine) + a.qt.nb) - 1;
-            this->walk = BandWalk<kTileRows>(a.band, this->first, this->last);
+            this->walk = KeyWalk<kTileRows>(a.band, this->first, this->last);
             tiles = this->walk.n;
         }
         if (KEYS && this->chunk >= 0) {      // (a walk may be shorter than its parts)
@@ -356,7 +356,7 @@ struct Unit : UnitBand<BAND> {
     }
     // first key of tile j of held queries' walk
     __device__ __forceinline__ int key(int j) const {
-        if constexpr (BAND) return this->walk.tile(lo + j) * kTileRows;
+        if constexpr (BAND) return this->walk.key(lo + j);
         else return (lo + j) * kTileRows;
     }
     // the whole warp calls it; an index behind the last unit stands for the end
@@ -420,7 +420,7 @@ __device__ __forceinline__ int weights(const BwdMmaArgs<BAND> &a, Shared<BAND> &
         if (!KEYS) {
             lowest = u.p0 + a.qt.first_row(u.mine);
             highest = u.p0 + min(a.qt.Nq, a.qt.first_row(u.mine) + a.qt.nb) - 1;
-            p = lowest + r % a.qt.nb;
+            p = lowest + (a.qt.nb == kTileRows ? r : r % a.qt.nb);
             if (p >= u.bound) p = -1;
         } else if (a.qt.nb < kTileRows) {
             const int k = u.mine * kTileRows + r;
@@ -452,9 +452,10 @@ __device__ __forceinline__ int weights(const BwdMmaArgs<BAND> &a, Shared<BAND> &
                            (at + kTileRows - 1 < k0 + a.band.window || k0 + kTileRows <= a.band.sinks)))
                     keep = queries_of(a.band, k, at + 32 * cg, u.last + 1);
             } else {
+                const Band w = u.walk.band(a.band, u.lo + j);
                 const int k0 = u.key(j), k1 = k0 + kTileRows - 1;
-                if (!(k1 <= lowest && highest < u.bound && (k0 > highest - a.band.window || k1 < a.band.sinks)))
-                    keep = keys_of(a.band, p, k0 + 32 * cg);
+                if (!(k1 <= lowest && highest < u.bound && (k0 > highest - w.window || k1 < w.sinks)))
+                    keep = keys_of(w, p, k0 + 32 * cg);
             }
         } else if (!KEYS && (a.ks.mask || (u.lo + j + 1) * kTileRows > u.bound)) {
             const int s = it % kStages;
@@ -624,7 +625,7 @@ __device__ __forceinline__ bool prepare(const BwdMmaArgs<BAND> &a, Shared<BAND> 
         const int s = it % kStages;
         uint4 w = make_uint4(0, 0, 0, 0);
         int rows = kTileRows;
-        if constexpr (BAND) w = KEYS ? tile_queries(a, u, u.lo + j) : band_keys(a.band, u.first, u.last, u.key(j));
+        if constexpr (BAND) w = KEYS ? tile_queries(a, u, u.lo + j) : band_keys(u.walk.band(a.band, u.lo + j), u.first, u.last, u.key(j));
         else if (!KEYS) w = tile_keys(a.ks, u.b, u.key(j), u.bound);
         else rows = min(a.qt.gb, a.qt.G - a.qt.first_head(u.lo + j)) * a.qt.nb;
         if (!pipe_wait(&sh.full[s], (it / kStages) & 1, abort)) return false;

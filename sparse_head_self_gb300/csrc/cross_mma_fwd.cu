@@ -122,21 +122,25 @@ struct Unit : Place<NT, BAND> {
 template <int NT>
 struct Unit<NT, true> : Place<NT, true> {
     int bound, lo, n;
-    int p0, first, last;            // position of query 0; of the first and the last of this unit's that attend keys
-    BandWalk<kTileRows> walk;
+    int row, head;                  // of the tile's first query
+    int p0, first, last;            // position of that query; of the first and the last of the tile's that attend keys
+    KeyWalk<kTileRows> walk;
     __device__ __forceinline__ Unit() {}
     __device__ __forceinline__ Unit(const FwdMmaArgs<true> &a, const Place<NT, true> &p) : Place<NT, true>(p) { set(a); }
     __device__ __forceinline__ void set(const FwdMmaArgs<true> &a) {
         bound = a.ks.bound(this->b);
-        p0 = a.band.first(this->b);
-        first = max(0, p0 + a.qt.first_row(this->t0));
-        last = min(bound, p0 + min(a.qt.Nq, a.qt.first_row(this->t0 + this->nt - 1) + a.qt.nb)) - 1;
-        walk = BandWalk<kTileRows>(a.band, first, last);
+        row = a.qt.first_row(this->t0);
+        head = this->hk * a.qt.G + a.qt.first_head(this->t0);
+        p0 = a.band.first(this->b) + row;
+        first = max(0, p0);
+        last = min(bound, p0 + min(a.qt.Nq - row, a.qt.nb)) - 1;
+        walk = KeyWalk<kTileRows>(a.band, first, last);
         const int CS = (int)cluster_size(), rank = (int)cluster_rank();
         lo = (int)((int64_t)walk.n * rank / CS);
         n = (int)((int64_t)walk.n * (rank + 1) / CS) - lo;
     }
-    __device__ __forceinline__ int key(int j) const { return walk.tile(lo + j) * kTileRows; }
+    __device__ __forceinline__ int key(int j) const { return walk.key(lo + j); }
+    __device__ __forceinline__ Band band(const FwdMmaArgs<true> &a, int j) const { return walk.band(a.band, lo + j); }
 };
 
 // A named barrier of `threads` threads (whole warps), and whether `p` holds in all of them.
@@ -262,12 +266,10 @@ cross_fwd_mma_kernel(const __grid_constant__ FwdMmaArgs<BAND> a) {
                 return;
             }
             const int n = u.n, whole = a.ks.mask ? 0 : u.bound / kTileRows - u.lo;   // the tiles attended wholly come first
-            int p = -1, lowest = 0, highest = 0;     // positions: of the row, of the tile's rows
+            int p = -1, highest = 0;                 // positions: of the row, of the tile's last
             if constexpr (BAND) {
-                const int q = a.qt.first_row(u.t0 + t);
-                lowest = u.p0 + q;
-                highest = u.p0 + min(a.qt.Nq, q + a.qt.nb) - 1;
-                p = lowest + r % a.qt.nb;
+                highest = u.p0 + min(a.qt.Nq - u.row, a.qt.nb) - 1;
+                p = u.p0 + (a.qt.nb == kTileRows ? r : r % a.qt.nb);
                 if (p >= u.bound) p = -1;
             }
             float m = kNegInf, l = 0.f;
@@ -284,10 +286,11 @@ cross_fwd_mma_kernel(const __grid_constant__ FwdMmaArgs<BAND> a) {
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bar_sfree[t]);
                 if constexpr (BAND) {
+                    const Band w = u.band(a, j);
                     const int k0 = u.key(j), k1 = k0 + kTileRows - 1;
-                    const bool all = k1 <= lowest && highest < u.bound && (k0 > highest - a.band.window || k1 < a.band.sinks);
+                    const bool all = k1 <= u.p0 && highest < u.bound && (k0 > highest - w.window || k1 < w.sinks);
                     if (!all) {
-                        const uint32_t words[2] = {keys_of(a.band, p, k0 + 64 * half), keys_of(a.band, p, k0 + 64 * half + 32)};
+                        const uint32_t words[2] = {keys_of(w, p, k0 + 64 * half), keys_of(w, p, k0 + 64 * half + 32)};
 #pragma unroll
                         for (int i = 0; i < 2; ++i)
 #pragma unroll
@@ -370,7 +373,7 @@ cross_fwd_mma_kernel(const __grid_constant__ FwdMmaArgs<BAND> a) {
 #pragma unroll
                 for (int k = 0; k < 32; ++k) o[k] = 0u;
             }
-            if (BAND && n > 0 && CS == 1) {
+            if constexpr (BAND) if (n > 0 && CS == 1) {
                 const int place = loaded++ % C::kQueries;
                 if (a.qt.nb == kTileRows) {
                     uint8_t *tile = sq + place * kTileBytes;
@@ -386,7 +389,7 @@ cross_fwd_mma_kernel(const __grid_constant__ FwdMmaArgs<BAND> a) {
                     }
                     fence_smem_async();
                     named_sync(2, 32 * C::kSoftmaxWarps);
-                    const int q = a.qt.first_row(u.t0 + t), h = u.hk * a.qt.G + a.qt.first_head(u.t0 + t);
+                    const int q = u.row, h = u.head;
                     if (threadIdx.x == 0 && FIBATT_CHECKED(h < a.Hq && u.b >= 0 && q < a.qt.Nq)) {
                         tile_store(&a.o.map, q, h * a.o.head_step, u.b * a.o.seq_step, tile);
                         held = place;
@@ -441,9 +444,12 @@ cross_fwd_mma_kernel(const __grid_constant__ FwdMmaArgs<BAND> a) {
                 uint8_t *dst = sq + loaded % C::kQueries * NT * kTileBytes;
                 if (elect_one()) {
                     mbar_expect_tx(bar, u.nt * a.qt.bytes());
-                    for (int t = 0; t < u.nt; ++t)
-                        load_tile(dst + t * kTileBytes, a.q, a.qt.first_row(u.t0 + t), u.hk * a.qt.G + a.qt.first_head(u.t0 + t),
-                                  u.b, bar);
+                    if constexpr (BAND)
+                        load_tile(dst, a.q, u.row, u.head, u.b, bar);
+                    else
+                        for (int t = 0; t < u.nt; ++t)
+                            load_tile(dst + t * kTileBytes, a.q, a.qt.first_row(u.t0 + t),
+                                      u.hk * a.qt.G + a.qt.first_head(u.t0 + t), u.b, bar);
                 }
                 __syncwarp();
                 ++loaded;
@@ -529,7 +535,7 @@ cross_fwd_mma_kernel(const __grid_constant__ FwdMmaArgs<BAND> a) {
                 for (int j = 0; ok && j < n; ++j, ++ring) {
                     const int s = ring % C::kStages;
                     uint4 w;
-                    if constexpr (BAND) w = band_keys(a.band, u.first, u.last, u.key(j));
+                    if constexpr (BAND) w = band_keys(u.band(a, j), u.first, u.last, u.key(j));
                     else w = tile_keys(a.ks, u.b, u.key(j), u.bound);
                     ok = pipe_wait(&bar_full[s], (ring / C::kStages) & 1, abort);
                     if (!ok) break;

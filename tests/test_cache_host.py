@@ -109,6 +109,28 @@ template <int T> int walks(const Band &w, int lo, int hi, int end) {
     wrong += got.size() > want.size() + 1;      // (a tile may hold the window's start only in part)
     return wrong;
 }
+// From the oldest key on: every pair once, in a tile that is met once.
+template <int T> int pairs(const Band &w, int lo, int hi, int end) {
+    const KeyWalk<T> walk(w, lo, hi);
+    std::set<std::pair<int, int>> got;
+    int wrong = 0;
+    for (int i = 0; i < walk.n; ++i) {
+        const Band x = walk.band(w, i);
+        const int k0 = walk.key(i);
+        wrong += k0 < 0 || k0 > hi;
+        for (int p = lo; p <= hi; ++p)
+            for (int k = 0; k < T; k += 32)
+                for (uint32_t m = keys_of(x, p, k0 + k); m; m &= m - 1) {
+                    const int key = k0 + k + __builtin_ctz(m);
+                    wrong += !got.insert({p, key}).second || !(keys_between(x, lo, hi, k0 + k) >> __builtin_ctz(m) & 1);
+                }
+        wrong += keys_of(x, -1, k0) != 0;
+    }
+    for (int p = lo; p <= hi; ++p)
+        for (int k = 0; k < end; ++k) wrong += w.sees(p, k) != (bool)got.count({p, k});
+    if (lo <= hi) wrong += walk.n > (w.sinks + T - 1) / T + (w.window + hi - lo) / T + 1;
+    return wrong;
+}
 int main() {
     std::mt19937 r(1);
     const auto in = [&](int a, int b) { return a + (int)(r() % (unsigned)(b - a + 1)); };
@@ -156,6 +178,10 @@ int main() {
         const Band w = {nullptr, a.N, 64 * a.table_len, in(1, 400), in(0, 200)};
         const int lo = in(0, 64 * a.table_len - 1), hi = in(0, 7) ? lo + in(0, 64 * a.table_len - 1 - lo) : lo - 1;
         wrong += walks<64>(w, lo, hi, 64 * a.table_len) + walks<128>(w, lo, hi, 64 * a.table_len);
+        if (turn % 100 == 0) {
+            const int up = least(hi, lo + in(0, 140));
+            wrong += pairs<64>(w, lo, up, 64 * a.table_len) + pairs<128>(w, lo, up, 64 * a.table_len);
+        }
         const int k0 = 16 * in(0, 4 * a.table_len - 1), p = in(-1, 64 * a.table_len - 1);
         for (int i = 0; i < 32; ++i) {
             wrong += (keys_of(w, p, k0) >> i & 1) != w.sees(p, k0 + i);
