@@ -637,9 +637,25 @@ cudaError_t bwd(const CrossArgs &a) {
     if (BAND && a.band.sinks == 0) key_walk = std::min<int64_t>(key_walk, ((int64_t)a.band.window + kT) / kT + 1);
     const Launches l(query_units, key_tiles<BAND>(a), key_units, (a.Hq / a.Hkv) * key_walk, kBwdBlocks * sm_count(), 1,
                      2, largest_cluster<cross_bwd_f32_kernel<BAND>>(smem));
-    if (!l.two)
-        return launch_clusters(cross_bwd_f32_kernel<BAND>, (unsigned)((key_units + query_units) * l.c), l.c, kThreads, smem,
+    if (!l.two) {
+        int c = l.c;
+        if constexpr (BAND) {
+            // Walks differ (a tile with sinks meets every later query): cut over more CTAs than find a place
+            // at once, while that ends the longest before all of them, in tiles, with a quarter for a CTA.
+            // (4 sequences, 12 heads, 197 tokens, window 65, 1 sink: clusters of two 54 us, of one 63,
+            // of four 74; 8 sequences, 12 heads on 4, 600 tokens, window 128, 4 sinks: 358, 502, 331.)
+            const int64_t group = a.Hq / a.Hkv, query_walk = key_tiles<BAND>(a),
+                          others = group * std::min<int64_t>(f.qtiles, ((int64_t)a.band.window + kT) / kT + 1),
+                          longest = std::max(query_walk, a.band.sinks ? group * f.qtiles : others),
+                          all = (query_units * query_walk + key_units * others) * 3 / 4;
+            const auto time = [&](int n) {
+                return std::max<double>((double)longest / n + 1, (all + 0.25 * (double)(query_units + key_units) * n) / (kBwdBlocks * sm_count()));
+            };
+            while (c < 8 && time(2 * c) < time(c)) c *= 2;
+        }
+        return launch_clusters(cross_bwd_f32_kernel<BAND>, (unsigned)((key_units + query_units) * c), c, kThreads, smem,
                                a.stream, f);
+    }
     e = launch_clusters(cross_bwd_f32_kernel<BAND>, (unsigned)(key_units * l.c_key), l.c_key, kThreads, smem, a.stream, f);
     if (e != cudaSuccess) return e;
     f.first = f.key_units;
