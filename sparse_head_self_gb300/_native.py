@@ -7,12 +7,13 @@ There is no fallback implementation.
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import os
 import re
 import struct
 import threading
 
-from .build import LIB, LIB_CHECKS, ROOT
+from .build import CALLS, LIB, LIB_CHECKS, ROOT
 
 HEADER = os.path.join(ROOT, "include", "fibatt.h")
 
@@ -115,6 +116,25 @@ def lib():
             fn.argtypes = args
         _lib = L
         return L
+
+
+_CALLS = ("fibatt_window_fwd", "fibatt_window_bwd", "fibatt_window_bwd_workspace_bytes", "fibatt_cache_store",
+          "fibatt_cache_load", "fibatt_cache_fwd")
+
+
+def calls():
+    """The module of binding/calls.cpp, which calls into the loaded library
+    (raises if it has not been built)."""
+    L = lib()
+    if not os.path.exists(CALLS):
+        raise RuntimeError(f"libfibatt's binding is not built ({CALLS} missing); run "
+                           "`python -c 'import __graft_entry__ as g; g.build()'`")
+    import torch  # noqa: F401  (whose libraries the module needs)
+    spec = importlib.util.spec_from_file_location("_calls", CALLS)
+    module = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(module)
+    module.use(*(ctypes.cast(getattr(L, name), ctypes.c_void_p).value for name in _CALLS))
+    return module
 
 
 def check(status: int) -> None:

@@ -673,6 +673,17 @@ def cross_attention(Q, K, V, scale: float | None = None, kv_len=None, key_mask=N
 
 # ------------------------------------------ attention over a window, with sinks
 
+# The calls below first try the short way in C++ (binding/calls.cpp), which takes those of the
+# usual form; None from there: the steps here, which take every form and say what is wrong with a call.
+_calls = None
+
+
+def _short():
+    global _calls
+    _calls = _native.calls()
+    return _calls
+
+
 def _window_desc(Q, K, V, scale, window, sinks, q_start, kv_len):
     """(packed fibatt_window, Q, K, V as packed fibatt_heads, device index)."""
     dtype, code, index = _attention_sizes(Q, K, V)
@@ -704,6 +715,12 @@ def window_fwd(Q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, scale: float, 
     O in Q's layout.  q_start: int32 [B], the place of each sequence's first
     query (Nk - Nq if not given); kv_len: int32 [B], the keys each sequence
     has.  Queries outside their sequence attend nothing: O = 0, LSE = -inf."""
+    if O is None and LSE is None and stream is None:
+        r = (_calls or _short()).window_fwd(Q, K, V, scale, window, sinks, q_start, kv_len)
+        if r.__class__ is tuple:
+            return r
+        if r is not None:
+            check(r)
     d, q, k, v, index = _window_desc(Q, K, V, scale, window, sinks, q_start, kv_len)
     return _launch(index, stream, _attention_fwd, lib().fibatt_window_fwd, d, q, k, v, Q, O, LSE, index)
 
@@ -712,6 +729,12 @@ def window_bwd(Q, K, V, O, LSE, dO, scale: float, window: int | None = None, sin
                dQ=None, dK=None, dV=None, workspace: torch.Tensor | None = None, stream=None):
     """fibatt_window_bwd: (dQ, dK, dV) from window_fwd's O and LSE and the
     gradient dO of O; each gradient in its input's layout unless given."""
+    if dQ is None and dK is None and dV is None and workspace is None and stream is None:
+        r = (_calls or _short()).window_bwd(Q, K, V, O, LSE, dO, scale, window, sinks, q_start, kv_len)
+        if r.__class__ is tuple:
+            return r
+        if r is not None:
+            check(r)
     L = lib()
     return _attention_bwd(L.fibatt_window_bwd, L.fibatt_window_bwd_workspace_bytes,
                           _window_desc(Q, K, V, scale, window, sinks, q_start, kv_len), Q, K, V, O, LSE, dO, dQ, dK, dV,
@@ -821,6 +844,10 @@ def cache_store(cache: Cache, table: torch.Tensor, K: torch.Tensor, V: torch.Ten
     """fibatt_cache_store: keys and values K, V [B, Hkv, N, 64] of N tokens into
     the sequences' pages, token n of them at place start[b] + n (int32 [B]; from 0
     if not given); count: int32 [B], how many of the N each sequence has."""
+    if stream is None:
+        r = (_calls or _short()).cache_store(*cache, table, K, V, start, count)
+        if r is not None:
+            return check(r)
     d, k, v, index = _cache_states(cache, table, K, V, start, count)
     check(_launch(index, stream, lib().fibatt_cache_store, d, k, v))
 
@@ -830,6 +857,12 @@ def cache_load(cache: Cache, table: torch.Tensor, N: int, start: torch.Tensor | 
                V: torch.Tensor | None = None, stream=None):
     """fibatt_cache_load: (K, V), [B, Hkv, N, 64] each, of the N tokens from
     place start[b] on, zeros from count[b] on."""
+    if K is None and V is None and stream is None and dtype in _DTYPES:
+        r = (_calls or _short()).cache_load(*cache, table, N, start, count, dtype is torch.float32)
+        if r.__class__ is tuple:
+            return r
+        if r is not None:
+            check(r)
     index = _index("data", cache[0])
     if not isinstance(table, torch.Tensor) or table.dim() != 2:
         raise ValueError("table must be [B, pages of a sequence]")
@@ -854,6 +887,12 @@ def cache_fwd(Q: torch.Tensor, cache: Cache, table: torch.Tensor, start: torch.T
     at start[b] + n, to the cache that holds their keys (cache_store comes
     first); window, sinks as window_fwd; returns (O, LSE), O in Q's layout.  A
     query that count[b] leaves out attends nothing: O = 0, LSE = -inf."""
+    if O is None and LSE is None and stream is None:
+        r = (_calls or _short()).cache_fwd(Q, *cache, table, start, scale, window, sinks, count)
+        if r.__class__ is tuple:
+            return r
+        if r is not None:
+            check(r)
     dtype, _, index = _attention_sizes(Q, Q, Q)
     B, Hq, N, D = shape = Q.shape
     d, _ = _cache_desc(cache, table, start, count, dtype, B, N, D, index)

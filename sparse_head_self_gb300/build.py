@@ -11,6 +11,10 @@ whose kernels check the bounds of their shared-memory stages, windows and
 scratch rows and record a failure in the device error word instead of
 making the access.  ``FIBATT_CHECKS=1`` in the environment makes the
 binding load it.
+
+``build_binding()`` compiles ``binding/calls.cpp``, the short way from Python into some of
+the calls, against this Python and torch into ``_build/_calls.so`` (with the
+host compiler; the library itself knows neither).
 """
 from __future__ import annotations
 
@@ -26,6 +30,8 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(BUILD, "libfibatt.so")
+BINDING = os.path.join(PKG, "binding", "calls.cpp")
+CALLS = os.path.join(BUILD, "_calls.so")
 BUILD_CHECKS = os.path.join(PKG, "_build_checks")
 LIB_CHECKS = os.path.join(BUILD_CHECKS, "libfibatt.so")
 
@@ -94,10 +100,44 @@ def build_library(force: bool = False, verbose: bool = False, ptxas_verbose: boo
     return lib_path
 
 
+def build_binding(force: bool = False) -> str:
+    """Compile binding/calls.cpp; returns the module's path.  It is built anew
+    when it, the header, torch or Python has changed."""
+    import sysconfig
+
+    import torch
+
+    home = os.path.dirname(torch.__file__)
+    include = [os.path.join(home, "include"), os.path.join(home, "include", "torch", "csrc", "api", "include"),
+               sysconfig.get_paths()["include"], os.path.join(os.path.dirname(os.path.dirname(_nvcc())), "include"),
+               os.path.join(ROOT, "include")]
+    cmd = [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-shared", "-fPIC",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"]
+    cmd += [x for i in include for x in ("-isystem", i)] + [BINDING]
+    cmd += ["-L", os.path.join(home, "lib"), f"-Wl,-rpath,{home}/lib", "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch",
+            "-ltorch_python"]
+    made_with, record = f"{sys.version}\n{torch.__version__}\n{' '.join(cmd)}\n", CALLS + ".txt"
+    newest = max(os.path.getmtime(f) for f in (BINDING, os.path.join(ROOT, "include", "fibatt.h")))
+    if not force and os.path.exists(CALLS) and os.path.exists(record) and os.path.getmtime(CALLS) >= newest:
+        with open(record) as f:
+            if f.read() == made_with:
+                return CALLS
+    os.makedirs(BUILD, exist_ok=True)
+    tmp = CALLS + f".tmp{os.getpid()}"
+    r = subprocess.run(cmd + ["-o", tmp], capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed for {BINDING}:\n{' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, CALLS)
+    with open(record, "w") as f:
+        f.write(made_with)
+    return CALLS
+
+
 def build_all(force: bool = False) -> None:
-    """The library and its checks build, compiled side by side."""
-    with ThreadPoolExecutor(max_workers=2) as ex:
-        for f in [ex.submit(build_library, force, False, False, c) for c in (False, True)]:
+    """The library, its checks build and the binding, compiled side by side."""
+    with ThreadPoolExecutor(max_workers=3) as ex:
+        jobs = [ex.submit(build_library, force, False, False, c) for c in (False, True)] + [ex.submit(build_binding, force)]
+        for f in jobs:
             f.result()
 
 
