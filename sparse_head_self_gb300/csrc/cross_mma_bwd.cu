@@ -75,7 +75,7 @@ struct BwdMmaArgs {
     int npad;                   // rows of a head there
     Rows<__nv_bfloat16> dQ, dK, dV;
     int B, Hq, Hkv, ktiles;
-    int query_units, units;     // units that hold queries, which come first, and all of them
+    int first_kind, units;      // units of the kind that comes first (queries held; BAND: keys held), and all of them
     int chunks, chunk_tiles;    // BAND: parts of a sinks' walk and the query tiles of each, ...
     int sink_tiles, sink_units; // ... key tiles that have such walks, units of those parts
     float4 *parts;              // their partial sums, one after another
@@ -279,18 +279,18 @@ struct UnitBand<true> {
 };
 template <bool BAND>
 struct Unit : UnitBand<BAND> {
-    int index;               // queries held first, then keys held
+    int index;               // queries held first, then keys held (BAND: keys first, whose walks are longer)
     int mine, hk, b, bound, lo, n;
     uint4 keys;              // keys held: which rows are attended
     template <bool KEYS>
     __device__ __forceinline__ void set(const BwdMmaArgs<BAND> &a, int i) {
         index = i;
-        if constexpr (BAND) set_band<KEYS>(a, KEYS ? i - a.query_units : i);
+        if constexpr (BAND) set_band<KEYS>(a, KEYS ? i : i - a.first_kind);
         else set_all<KEYS>(a, i);
     }
     template <bool KEYS>
     __device__ __forceinline__ void set_all(const BwdMmaArgs<BAND> &a, int i) {
-        const int unit = KEYS ? i - a.query_units : i, held = KEYS ? a.ktiles : a.qt.tiles;
+        const int unit = KEYS ? i - a.first_kind : i, held = KEYS ? a.ktiles : a.qt.tiles;
         mine = unit % held;
         hk = unit / held % a.Hkv;
         b = unit / held / a.Hkv;
@@ -361,8 +361,8 @@ struct Unit : UnitBand<BAND> {
     }
     // the whole warp calls it; an index behind the last unit stands for the end
     __device__ __forceinline__ void enter(const BwdMmaArgs<BAND> &a, int i) {
-        if (i < a.query_units) set<false>(a, i);
-        else if (i < a.units) set<true>(a, i);
+        if (i < a.first_kind) set<BAND>(a, i);
+        else if (i < a.units) set<!BAND>(a, i);
         else index = i, mine = hk = b = bound = lo = n = 0, keys = make_uint4(0, 0, 0, 0);
     }
 };
@@ -808,9 +808,15 @@ __global__ void __launch_bounds__(kThreads, 1) cross_bwd_mma_kernel(const __grid
     const auto each = [&](auto next, auto queries, auto keys) {
         Unit<BAND> u = next();
 #pragma unroll 1
-        for (; u.index < a.query_units; u = next()) queries(u);
+        for (; u.index < a.first_kind; u = next()) {
+            if constexpr (BAND) keys(u);
+            else queries(u);
+        }
 #pragma unroll 1
-        for (; u.index < a.units; u = next()) keys(u);
+        for (; u.index < a.units; u = next()) {
+            if constexpr (BAND) queries(u);
+            else keys(u);
+        }
     };
     int passed = 0;         // units handed over
     const auto take = [&] {
@@ -883,8 +889,8 @@ __global__ void __launch_bounds__(kThreads, 1) cross_bwd_mma_kernel(const __grid
     cluster_sync();
     Unit<BAND> u;
     u.enter(a, first);
-    if (first < a.query_units) join<false, BAND>(a, tl, u);
-    else join<true, BAND>(a, tl, u);
+    if (first < a.first_kind) join<BAND, BAND>(a, tl, u);
+    else join<!BAND, BAND>(a, tl, u);
     cluster_sync();   // the others may still read this CTA's part
 }
 
@@ -1012,7 +1018,7 @@ cudaError_t bwd(const CrossArgs &a) {
     if (e != cudaSuccess) return e;
     const int64_t query_units = (int64_t)a.B * a.Hkv * f.qt.tiles;
     const int64_t key_units = (int64_t)a.B * a.Hkv * (f.ktiles - f.sink_tiles) + f.sink_units;
-    f.query_units = (int)query_units;
+    f.first_kind = (int)(BAND ? key_units : query_units);
     // clusters, one unit each, while they all find a place; else one wave of CTAs that walk over the units
     const auto launch = [&](int64_t from, int64_t units, int c) {
         f.first_unit = (int)from;
@@ -1037,10 +1043,10 @@ cudaError_t bwd(const CrossArgs &a) {
         }
     }
     if (!l.two) return launch(0, query_units + key_units, l.c);
-    e = launch(0, query_units, l.c_query);
+    e = BAND ? launch(0, key_units, l.c_key) : launch(0, query_units, l.c_query);
     if (e != cudaSuccess) return e;
     ++f.next_unit;
-    return launch(query_units, key_units, l.c_key);
+    return BAND ? launch(key_units, query_units, l.c_query) : launch(query_units, key_units, l.c_key);
 }
 
 }  // namespace
