@@ -84,6 +84,7 @@ struct BwdMmaArgs {
     float scale;
     float c;                    // scale log2 e, not 0
     Band band;                  // BAND
+    TensorArg dq, dk, dv;       // BAND: the gradients as tensor copies write them (dQ: tiles of 128 queries)
     BwdMmaArgs() : qt(1, 1, false) {}
 };
 
@@ -274,6 +275,7 @@ template <>
 struct UnitBand<true> {
     int p0, first, last;     // position of query 0; of the unit's queries, held or streamed, that attend keys of it
     int chunk;               // keys held: the part of the walk that this unit has, -1: all of it
+    int leaves;              // the pair of places for held rows from where its gradients leave by tensor copies, -1: none
     KeyWalk<kTileRows> walk;    // held queries
     __device__ __forceinline__ UnitBand() {}
 };
@@ -372,6 +374,7 @@ struct Shared {
     uint64_t held[2], held_free[2], full[kStages], ready[kStages], empty[kStages], s, sfree, p, done, end[2];
     uint64_t unit_full[2], unit_empty[2];
     uint4 keys[kStages];
+    uint64_t out[2];            // BAND: a unit is over, in turn; ...
     Unit<BAND> unit[2];         // the CTA's, in turn
     uint32_t tmem;
     int abort;
@@ -393,9 +396,20 @@ struct Tiles {
 // units of the CTA: tile it is in stage it mod kStages, and each barrier of the
 // pipeline completes a phase per tile.
 
-// P and dS: row = lane of the quarter, 32 columns
-template <bool KEYS, bool BAND>
-__device__ __forceinline__ int weights(const BwdMmaArgs<BAND> &a, Shared<BAND> &sh, uint8_t *ring, const Unit<BAND> &u, int it) {
+// (LSE log2 e, D) of a thread's row of held queries.
+__device__ __forceinline__ float2 row_stats(const BwdMmaArgs<true> &a, const Unit<true> &u) {
+    const int r = (int)(warp_number() & 3) * 32 + (int)(threadIdx.x & 31);
+    int g, q;
+    if (u.index < a.first_kind || u.index >= a.units || !a.qt.at(u.mine, r, g, q)) return make_float2(kInf, 0.f);
+    return __ldg(a.stats + ((int64_t)u.b * a.Hq + u.hk * a.qt.G + g) * a.qt.Nq + q);
+}
+
+// P and dS: row = lane of the quarter, 32 columns.  BAND: `stats` of the unit's rows; `ahead` before the
+// unit's end, which hides what the next one has to wait for.
+template <bool KEYS, bool BAND, typename Ahead>
+__device__ __forceinline__ int weights(const BwdMmaArgs<BAND> &a, Shared<BAND> &sh, const Tiles &tl, const Unit<BAND> &u, int it,
+                                       float2 &stats, Ahead ahead) {
+    uint8_t *const ring = tl.ring;
     volatile int *abort = &sh.abort;
     const int warp = warp_number(), lane = threadIdx.x & 31;
     const int cg = warp >> 2, r = (warp & 3) * 32 + lane;
@@ -405,9 +419,9 @@ __device__ __forceinline__ int weights(const BwdMmaArgs<BAND> &a, Shared<BAND> &
     const bool row = (KEYS ? u.mine * kTileRows + r < a.ks.Nk : a.qt.at(u.mine, r, g, q)) &&
                      FIBATT_CHECKED(u.b >= 0 && u.b < a.B && u.hk < a.Hkv);
     if (!KEYS && row) {
-        const float2 st = __ldg(a.stats + ((int64_t)u.b * a.Hq + u.hk * a.qt.G + g) * a.qt.Nq + q);
-        row_lse = -st.x;
-        row_d = -st.y;
+        if (!BAND) stats = __ldg(a.stats + ((int64_t)u.b * a.Hq + u.hk * a.qt.G + g) * a.qt.Nq + q);
+        row_lse = -stats.x;
+        row_d = -stats.y;
     }
     // keys that are not attended have no gradient, whatever their rows hold
     const uint32_t word = (warp & 3) == 0 ? u.keys.x : (warp & 3) == 1 ? u.keys.y : (warp & 3) == 2 ? u.keys.z : u.keys.w;
@@ -495,6 +509,7 @@ __device__ __forceinline__ int weights(const BwdMmaArgs<BAND> &a, Shared<BAND> &
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh.p);
     }
+    ahead();
     if (u.n > 0) pipe_wait(&sh.done, (it - 1) & 1, abort);
     tc_after_sync();
     // groups 0, 1: the halves of the first sum (dQ or dK); 2, 3: of the second (dV)
@@ -507,8 +522,8 @@ __device__ __forceinline__ int weights(const BwdMmaArgs<BAND> &a, Shared<BAND> &
         tc_before_sync();
     }
     const float f = acc ? 1.f : a.scale;
-    if constexpr (BAND && KEYS) {
-        if (u.chunk >= 0 && FIBATT_CHECKED(u.mine < a.sink_tiles && u.chunk < a.chunks)) {       // (see window_sum_kernel)
+    if constexpr (BAND) {
+        if (KEYS && u.chunk >= 0 && FIBATT_CHECKED(u.mine < a.sink_tiles && u.chunk < a.chunks)) {       // (see window_sum_kernel)
             const int tile = (u.mine * a.B + u.b) * a.Hkv + u.hk;
             float4 *mine = a.parts + ((int64_t)tile * a.chunks + u.chunk) * kPartSums + threadIdx.x;
 #pragma unroll
@@ -517,6 +532,20 @@ __device__ __forceinline__ int weights(const BwdMmaArgs<BAND> &a, Shared<BAND> &
                        u.n > 0 ? make_float4(__uint_as_float(o[4 * i]), __uint_as_float(o[4 * i + 1]),
                                              __uint_as_float(o[4 * i + 2]), __uint_as_float(o[4 * i + 3]))
                                : make_float4(0.f, 0.f, 0.f, 0.f));
+            return it;
+        }
+        if (u.leaves >= 0) {
+            uint8_t *const tile = tl.pair(u.leaves) + acc * kTileBytes;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                uint32_t w[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    w[k] = zero ? 0u
+                                : pack_bf16x2(__uint_as_float(o[8 * i + 2 * k]) * f, __uint_as_float(o[8 * i + 2 * k + 1]) * f);
+                *reinterpret_cast<uint4 *>(tile + r * 128 + (((4 * half + i) ^ (r & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+            fence_smem_async();
             return it;
         }
     }
@@ -546,6 +575,20 @@ __device__ __forceinline__ int weights(const BwdMmaArgs<BAND> &a, Shared<BAND> &
         }
     }
     return it;
+}
+
+// BAND, one lane: the gradients of a unit that is over leave.
+__device__ __forceinline__ void send(const BwdMmaArgs<true> &a, const Tiles &tl, const Unit<true> &u) {
+    if (u.leaves < 0 || !FIBATT_CHECKED(u.b >= 0 && u.b < a.B && u.hk < a.Hkv)) return;
+    const uint8_t *tile = tl.pair(u.leaves);
+    if (u.index >= a.first_kind) {
+        tile_store(&a.dq.map, a.qt.first_row(u.mine), (u.hk * a.qt.G + a.qt.first_head(u.mine)) * a.dq.head_step,
+                   u.b * a.dq.seq_step, tile);
+    } else {
+        tile_store(&a.dk.map, u.mine * kTileRows, u.hk * a.dk.head_step, u.b * a.dk.seq_step, tile);
+        tile_store(&a.dv.map, u.mine * kTileRows, u.hk * a.dv.head_step, u.b * a.dv.seq_step, tile + kTileBytes);
+    }
+    stores_read();
 }
 
 // Copies; false: a wait gave up.  `units` counts the units with tiles, whose held
@@ -765,6 +808,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross_bwd_mma_kernel(const __grid
         for (int i = 0; i < 2; ++i) {
             mbar_init(&sh.held[i], 1);
             mbar_init(&sh.held_free[i], 1);
+            mbar_init(&sh.out[i], kWeightWarps);
             mbar_init(&sh.end[i], 1);
             mbar_init(&sh.unit_full[i], 1);
             mbar_init(&sh.unit_empty[i], kWeightWarps + 3);
@@ -834,8 +878,29 @@ __global__ void __launch_bounds__(kThreads, 1) cross_bwd_mma_kernel(const __grid
     int it = 0, units = 0;
     if (warp < kWeightWarps) {
         take_registers<kRegsMany>();
-        each(take, [&](const Unit<BAND> &u) { it = weights<false, BAND>(a, sh, tl.ring, u, it); },
-             [&](const Unit<BAND> &u) { it = weights<true, BAND>(a, sh, tl.ring, u, it); });
+        float2 stats = make_float2(kInf, 0.f);       // BAND: of the next unit's rows
+        const auto ahead = [&] {
+            if constexpr (BAND) {
+                if (pipe_wait(&sh.unit_full[passed & 1], (passed >> 1) & 1, &sh.abort)) stats = row_stats(a, sh.unit[passed & 1]);
+                __syncwarp();
+            }
+        };
+        ahead();
+        const auto over = [&] {
+            if constexpr (BAND) {
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sh.out[(passed - 1) & 1]);
+            }
+        };
+        each(take,
+             [&](const Unit<BAND> &u) {
+                 it = weights<false, BAND>(a, sh, tl, u, it, stats, ahead);
+                 over();
+             },
+             [&](const Unit<BAND> &u) {
+                 it = weights<true, BAND>(a, sh, tl, u, it, stats, ahead);
+                 over();
+             });
     } else {
         give_registers<kRegsFew>();
         if (warp == kCopyWarp) {
@@ -848,6 +913,12 @@ __global__ void __launch_bounds__(kThreads, 1) cross_bwd_mma_kernel(const __grid
                 drawn = a.units;
                 if (CS == 1 && lane == 0 && u.index < a.units) drawn = a.first_unit + (int)gridDim.x + atomicAdd(a.next_unit, 1);
                 ok = ok && (passed < 2 || pipe_wait(&sh.unit_empty[i], ((passed >> 1) - 1) & 1, &sh.abort));
+                if constexpr (BAND) {      // (the unit before last is over by now, or nearly)
+                    ok = ok && (passed < 2 || pipe_wait(&sh.out[i], ((passed >> 1) - 1) & 1, &sh.abort));
+                    if (ok && passed >= 2 && lane == 0) send(a, tl, sh.unit[i]);
+                    const bool rows = u.index < a.first_kind ? u.chunk < 0 : a.qt.nb == kTileRows;
+                    u.leaves = u.index < a.units && u.n > 0 && CS == 1 && rows ? units & 1 : -1;
+                }
                 if (!ok) u.index = a.units;
                 else if (lane == 0) {
                     sh.unit[i] = u;
@@ -859,6 +930,14 @@ __global__ void __launch_bounds__(kThreads, 1) cross_bwd_mma_kernel(const __grid
             };
             each(pass, [&](const Unit<BAND> &u) { ok = ok && copies<false, BAND>(a, sh, tl, u, it, units); },
                  [&](const Unit<BAND> &u) { ok = ok && copies<true, BAND>(a, sh, tl, u, it, units); });
+            if constexpr (BAND) {      // the last units' gradients
+                for (int i = max(0, passed - 2); ok && i < passed - 1; ++i) {      // (the last one passed is the end)
+                    ok = pipe_wait(&sh.out[i & 1], (i >> 1) & 1, &sh.abort);
+                    if (ok && lane == 0) send(a, tl, sh.unit[i & 1]);
+                }
+                if (lane == 0) stores_done();
+                __syncwarp();
+            }
             if (lane == 0) {   // leave no copy in flight
                 for (int i = max(0, units - 2); i < units; ++i) mbar_drain(&sh.held[i & 1], (i >> 1) & 1);
                 for (int i = max(0, it - kStages); i < it; ++i) mbar_drain(&sh.full[i % kStages], (i / kStages) & 1);
@@ -982,6 +1061,9 @@ cudaError_t bwd(const CrossArgs &a) {
     f.chunks = 1, f.chunk_tiles = f.sink_tiles = f.sink_units = 0;
     f.parts = nullptr;
     if constexpr (BAND) {
+        if ((f.qt.nb == kTileRows && !make_tensor(&f.dq, a.dQ, a.B, a.Hq, a.Nq, kTileRows, 1)) ||
+            !make_tensor(&f.dk, a.dK, a.B, a.Hkv, a.Nk, kTileRows, 1) || !make_tensor(&f.dv, a.dV, a.B, a.Hkv, a.Nk, kTileRows, 1))
+            return cudaErrorInvalidValue;
         const SinkParts p(a.B, a.Hkv, a.Nk, a.band, f.qt);
         if (p.chunks > 1) {
             f.chunks = (int)p.chunks;
