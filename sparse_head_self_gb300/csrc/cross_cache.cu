@@ -261,6 +261,12 @@ __device__ __forceinline__ void load4(const float *p, float *x) {
     const float4 t = __ldg(reinterpret_cast<const float4 *>(p));
     x[0] = t.x, x[1] = t.y, x[2] = t.z, x[3] = t.w;
 }
+// A write to another CTA's shared memory; the two halves of the cluster's barrier.
+__device__ __forceinline__ void st_cluster2(uint32_t at, float2 v) {
+    asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(at), "f"(v.x), "f"(v.y) : "memory");
+}
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 // Bytes whose bit is set.
 __device__ __forceinline__ uint32_t bytes_of(uint32_t four) {
     return ((four & 1) | (four & 2) << 7 | (four & 4) << 14 | (four & 8) << 21) * 0xffu;
@@ -282,15 +288,15 @@ cache_fwd_kernel(const __grid_constant__ AttendArgs a, Rows<const T> Q, Rows<T> 
     __shared__ uint64_t full[kPairs][kStages];
     __shared__ int abort_flag;
     __shared__ float sm[kWarps][R], sl[kWarps][R], sf[kWarps][R];     // the warps' maxima, sums and factors
-    __shared__ float cm[R], cl[R];                    // the CTA's, read by the cluster
-    __shared__ float2 co[R][32];
-    __shared__ float inv_of[R];                       // a row's 1 / sum, 0 for one that attends nothing
+    __shared__ float2 cml[R], co[R][32];              // from the cluster's CTAs: maxima and sums, weighted values
+    __shared__ float2 row_ml[R];                      // a row's maximum and sum
     static_assert(kWarps * R * 32 * sizeof(float2) <= kSmem - 128, "the warps' sums fit");
     volatile int *abort = &abort_flag;
     const int warp = warp_number(), pair = warp >> 1, sub = warp & 1, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
     const unsigned C = cluster_size(), rank = cluster_rank();
     if (threadIdx.x < kPairs * kStages) mbar_init(&full[0][0] + threadIdx.x, 1);
     if (threadIdx.x == 0) abort_flag = 0;
+    if (C > 1) cluster_arrive();      // (waited for below, before the first write to another CTA)
     __syncthreads();
     grid_dep_wait();
     grid_dep_launch();
@@ -519,14 +525,9 @@ cache_fwd_kernel(const __grid_constant__ AttendArgs a, Rows<const T> Q, Rows<T> 
         }
     }
     __syncthreads();
-    // each row's maximum, factors and sum: the CTA's, then the cluster's
-    const auto finish = [&](int r, float top, float sum) {
-        const bool none = position(r) < 0 || sum == 0.f;
-        const int n = token(r);
-        inv_of[r] = none ? 0.f : 1.f / sum;
-        if (r % C == rank)
-            a.c.LSE[((int64_t)b * a.c.Hq + hk * a.G + (r0 + r - n * a.G)) * a.c.N + n] = none ? kNegInf : (top + log2f(sum)) * kLn2;
-    };
+    // The CTA's maximum, factors and sum of each row; the cluster's, of those it finishes: row r is CTA
+    // r mod C's, to whose shared memory the others write what they have of it.
+    const unsigned share = R / C;        // rows that a CTA finishes (of R, a multiple of C)
     if (threadIdx.x < rows) {
         const int r = threadIdx.x;
         float top = kNegInf, sum = 0.f;
@@ -539,48 +540,52 @@ cache_fwd_kernel(const __grid_constant__ AttendArgs a, Rows<const T> Q, Rows<T> 
             sf[w][r] = f;
             sum = fmaf(f, sl[w][r], sum);
         }
-        cm[r] = top;
-        cl[r] = sum;
-        if (C == 1) finish(r, top, sum);
+        row_ml[r] = make_float2(top, sum);
     }
     __syncthreads();
-    const auto write = [&](int r, int d, float2 x) {
-        const int n = token(r);
-        const float inv = inv_of[r];
-        store2(O.row(b, hk * a.G + (r0 + r - n * a.G), n) + 2 * d, inv == 0.f ? make_float2(0.f, 0.f) : make_float2(x.x * inv, x.y * inv));
+    if (C > 1) cluster_wait();
+    const auto finish = [&](int r, int d, float2 x) {
+        const float2 ml = row_ml[r];
+        const int n = token(r), h = hk * a.G + (r0 + r - n * a.G), p = start + n;
+        const bool none = p > last || ml.y == 0.f;
+        const float inv = none ? 0.f : 1.f / ml.y;
+        store2(O.row(b, h, n) + 2 * d, none ? make_float2(0.f, 0.f) : make_float2(x.x * inv, x.y * inv));
+        if (d == 0) a.c.LSE[((int64_t)b * a.c.Hq + h) * a.c.N + n] = none ? kNegInf : (ml.x + log2f(ml.y)) * kLn2;
     };
     for (int i = threadIdx.x; i < rows * 32; i += kThreads) {
         const int r = i >> 5, d = i & 31;
         float2 x = make_float2(0.f, 0.f);
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) x = fma2(make_float2(sf[w][r], sf[w][r]), so[w][r][d], x);
-        if (C == 1) write(r, d, x);
-        else co[r][d] = x;
+        if (C == 1) {
+            finish(r, d, x);
+        } else {
+            const unsigned to = rank * share + r / C;
+            st_cluster2(cluster_addr(&co[to][d], r % C), x);
+            if (d == 0) st_cluster2(cluster_addr(&cml[to], r % C), row_ml[r]);
+        }
     }
     if (C == 1) return;
+    __syncwarp();
     cluster_sync();
-    // row r is finished by CTA r mod C
-    if (threadIdx.x < rows && threadIdx.x % C == rank) {
-        const int r = threadIdx.x;
+    for (int i = threadIdx.x; i < (int)share * 32; i += kThreads) {
+        const int j = i >> 5, d = i & 31, r = j * (int)C + (int)rank;
+        if (r >= rows) continue;
         float top = kNegInf, sum = 0.f;
-        for (unsigned k = 0; k < C; ++k) top = fmaxf(top, ld_cluster(cluster_addr(cm + r, k)));
+        for (unsigned k = 0; k < C; ++k) top = fmaxf(top, cml[k * share + j].x);
         const float base = top == kNegInf ? 0.f : top;
-        for (unsigned k = 0; k < C; ++k) {
-            const float f = fast_exp2(ld_cluster(cluster_addr(cm + r, k)) - base);
-            sf[k][r] = f;
-            sum = fmaf(f, ld_cluster(cluster_addr(cl + r, k)), sum);
-        }
-        finish(r, top, sum);
-    }
-    __syncthreads();
-    for (int i = threadIdx.x; i < rows * 32; i += kThreads) {
-        const int r = i >> 5, d = i & 31;
-        if (r % C != rank) continue;
         float2 x = make_float2(0.f, 0.f);
-        for (unsigned k = 0; k < C; ++k) x = fma2(make_float2(sf[k][r], sf[k][r]), ld_cluster2(cluster_addr(&co[r][d], k)), x);
-        write(r, d, x);
+        for (unsigned k = 0; k < C; ++k) {
+            const float2 ml = cml[k * share + j], y = co[k * share + j][d];
+            const float f = fast_exp2(ml.x - base);
+            sum = fmaf(f, ml.y, sum);
+            x = fma2(make_float2(f, f), y, x);
+        }
+        __syncwarp();
+        if (d == 0) row_ml[r] = make_float2(top, sum);
+        __syncwarp();
+        finish(r, d, x);
     }
-    cluster_sync();   // the others may still read this CTA's part
 }
 
 template <typename T, int HALVES>
