@@ -375,7 +375,8 @@ fibatt_status fibatt_window_fwd(const fibatt_window *d, const fibatt_heads *Q, c
 /* Device scratch of fibatt_window_bwd, in bytes. */
 size_t fibatt_window_bwd_workspace_bytes(const fibatt_window *d);
 
-/* Backward pass, as fibatt_cross_bwd; D_j = <dO_j, O_j> with the O that is given.
+/* Backward pass, as fibatt_cross_bwd; for bf16, D_j is summed from the weights with Nk
+ * <= 64 or window + sinks <= 64, and is <dO_j, O_j> with the O that is given otherwise.
  * Keys that no query attends get gradients of 0. */
 fibatt_status fibatt_window_bwd(const fibatt_window *d, const fibatt_heads *Q, const fibatt_heads *K,
                                 const fibatt_heads *V, const fibatt_heads *O, const float *LSE,

@@ -191,9 +191,12 @@ struct Dims {
 // its eight keys at a time by warp-wide products; lane (g, t) gives them dims 16 t
 // to 16 t + 15 of rows g and g + 8 and of key g, four at a time in both operands
 // (the order of a sum does not matter), so that it loads 16 bytes at once.
+// BAND: also for windows of so few keys, sinks among them (a long sequence's first rows, of few keys too,
+// have <dO, O>: with the sum for those of up to 8 keys the first kernel took 4 us more, whose rows it all slows).
 constexpr int kFewWarps = 4;
+template <bool BAND>
 __global__ void __launch_bounds__(32 * kFewWarps)
-cross_parts_few_kernel(int Hq, int Hkv, int Nq, int npad, unsigned heads, KeySet ks, Rows<const __nv_bfloat16> Q,
+cross_parts_few_kernel(int Hq, int Hkv, int Nq, int npad, unsigned heads, KeySet ks, Band band, Rows<const __nv_bfloat16> Q,
                        Rows<const __nv_bfloat16> K, Rows<const __nv_bfloat16> V, Rows<const __nv_bfloat16> dO,
                        const float *__restrict__ LSE, float c, float2 *__restrict__ stats, uint4 *__restrict__ lse_parts,
                        uint4 *__restrict__ d_parts, int *__restrict__ next_unit) {
@@ -230,10 +233,20 @@ cross_parts_few_kernel(int Hq, int Hkv, int Nq, int npad, unsigned heads, KeySet
         none[i] = lse == -kInf;        // a row without keys: weights of exp2(s - inf) = 0
         lse2[i] = none[i] ? kInf : lse * kLog2e;
     }
-    const int bound = ks.bound((int)b);
+    int bound = ks.bound((int)b), front = 0, oldest = 0, at_p[2] = {-1, -1};
+    if constexpr (BAND) {      // the eights with keys of the 16 queries: those of the sinks, and from the oldest on
+        const int p = band.first((int)b) + n0, last = min(bound, p + min(16, Nq - n0)) - 1;
+        bound = last >= max(0, p) ? last + 1 : 0;
+        oldest = max(0, p - band.window + 1) & ~7;
+        front = min(band.sinks, oldest);
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            if (p + g + 8 * i <= last) at_p[i] = p + g + 8 * i;
+    }
     for (int k0 = 0; k0 < bound; k0 += 8) {
+        if (BAND && k0 >= front) k0 = max(k0, oldest);
         const int mine = k0 + (lane & 7);
-        const uint32_t in = __ballot_sync(kFullMask, mine < bound && ks.has((int)b, min(mine, bound - 1)));
+        const uint32_t in = __ballot_sync(kFullMask, mine < bound && (BAND || ks.has((int)b, min(mine, bound - 1))));
         Dims k, v;
         k.load(K.row(b, hk, min(k0 + g, bound - 1)), t);
         v.load(V.row(b, hk, min(k0 + g, bound - 1)), t);
@@ -248,7 +261,8 @@ cross_parts_few_kernel(int Hq, int Hkv, int Nq, int npad, unsigned heads, KeySet
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const float p = fast_exp2(fmaf(s[i], c, -lse2[i >> 1]));
-            if ((in >> (2 * t + (i & 1))) & 1) d[i >> 1] = fmaf(p, dp[i], d[i >> 1]);
+            const bool on = BAND ? band.sees(at_p[i >> 1], k0 + 2 * t + (i & 1)) : (in >> (2 * t + (i & 1))) & 1;
+            if (on) d[i >> 1] = fmaf(p, dp[i], d[i >> 1]);
         }
     }
 #pragma unroll
@@ -1082,10 +1096,10 @@ cudaError_t bwd(const CrossArgs &a) {
     f.c = std::copysign(std::max(std::fabs(a.scale) * kLog2e, 1e-36f), a.scale);
     cudaError_t e = prepare_kernel<cross_bwd_mma_kernel<BAND>>(kSmem, kRegs);
     if (e != cudaSuccess) return e;
-    if (!BAND && a.Nk <= kFewKeys) {
+    if (a.Nk <= kFewKeys || (BAND && (int64_t)a.band.window + a.band.sinks <= kFewKeys)) {
         const int64_t warps = (int64_t)a.B * a.Hq * ((f.npad + 15) / 16) + kTileRows / 16;
-        e = launch_clusters(cross_parts_few_kernel, (unsigned)((warps + kFewWarps - 1) / kFewWarps), 1, 32 * kFewWarps, 0,
-                            a.stream, a.Hq, a.Hkv, a.Nq, f.npad, (unsigned)(a.B * a.Hq), a.keys,
+        e = launch_clusters(cross_parts_few_kernel<BAND>, (unsigned)((warps + kFewWarps - 1) / kFewWarps), 1, 32 * kFewWarps, 0,
+                            a.stream, a.Hq, a.Hkv, a.Nq, f.npad, (unsigned)(a.B * a.Hq), a.keys, a.band,
                             rows_of<const __nv_bfloat16>(a.Q), rows_of<const __nv_bfloat16>(a.K),
                             rows_of<const __nv_bfloat16>(a.V), rows_of<const __nv_bfloat16>(a.dO),
                             static_cast<const float *>(a.LSE), f.c, stats, lse_parts, d_parts, f.next_unit);

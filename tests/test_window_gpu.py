@@ -404,6 +404,27 @@ def test_a_long_walk_next_to_short_ones():
             check(name, t, want[name])
 
 
+@pytest.mark.parametrize("size,band", [((8, 4, 4, 60, 60), (3, 0)), ((8, 4, 4, 60, 60), (8, 1)), ((8, 4, 2, 5, 300), (4, 2)),
+                                       ((8, 4, 2, 700, 700), (6, 2)), ((8, 4, 2, 40, 500), (40, 4)), ((200, 4, 2, 7, 7), (None, 0)),
+                                       ((60, 4, 4, 20, 20), (None, 0)), ((2, 4, 2, 1000, 1000), (50, 14)), ((20, 4, 2, 33, 64), (64, 0))],
+                         ids=_ids)
+def test_gradients_of_few_keys_have_two_roundings(size, band):
+    # dS and the result are each rounded once to 16 bits: at most 2^-8 of the value, uniform below
+    # that, so 2^-8 / sqrt(3) in the mean square; two independent ones are sqrt(2) of it
+    q, k, v, do = _inputs(BF16, *size, layout="bhnd", seed=53)
+    how = {"window": band[0], "sinks": band[1]}
+    got = _check_all(q, k, v, do, 0.125, **how)
+    G = size[1] // size[2]
+    x, y, z, w = q.double(), *(t.double().repeat_interleave(G, 1) for t in (k, v)), do.double()
+    s = (0.125 * x @ y.transpose(-1, -2)).masked_fill(~_seen(q, k, how)[:, None], -math.inf)
+    p, dp = s.softmax(-1), w @ z.transpose(-1, -2)
+    ds = p * (dp - (p * dp).sum(-1, keepdim=True))
+    dk = (0.125 * ds.transpose(-1, -2) @ x).view(size[0], size[2], G, size[4], 64).sum(2)
+    for name, exact in (("dQ", 0.125 * ds @ y), ("dK", dk)):
+        err = float((got[name].double() - exact).norm() / exact.norm())
+        assert err <= math.sqrt(2 / 3) * 2.0 ** -8, (name, err)
+
+
 def test_gradients_of_gradients_are_refused():
     q, k, v, _ = (t.detach().clone().requires_grad_() for t in _inputs(F32, 1, 2, 2, 5, 9))
     dq, = torch.autograd.grad(api.window_attention(q, k, v).square().sum(), q, create_graph=True)
