@@ -80,7 +80,11 @@ struct FwdMmaArgs {
     float c;                 // |scale| log2 e (> 0)
     int negative;            // scale < 0
     Band band;               // BAND
-    TensorArg o;             // BAND, tiles of 128 queries: O as tensor copies write it
+    TensorArg o;             // BAND, tiles of one head: O as tensor copies write it
+    // BAND: few sinks lie in front of the windows' first tile, in `front` rows of it (0: in tiles of their
+    // own); boxes of those and of the other rows
+    int front;
+    TensorArg kv_front[2], kv_rest[2];
     FwdMmaArgs() : qt(1, 1, false) {}
 };
 
@@ -124,6 +128,7 @@ struct Unit<NT, true> : Place<NT, true> {
     int bound, lo, n;
     int row, head;                  // of the tile's first query
     int p0, first, last;            // position of that query; of the first and the last of the tile's that attend keys
+    int front;                      // rows of the walk's first tile that are the sinks'
     KeyWalk<kTileRows> walk;
     __device__ __forceinline__ Unit() {}
     __device__ __forceinline__ Unit(const FwdMmaArgs<true> &a, const Place<NT, true> &p) : Place<NT, true>(p) { set(a); }
@@ -135,12 +140,22 @@ struct Unit<NT, true> : Place<NT, true> {
         first = max(0, p0);
         last = min(bound, p0 + min(a.qt.Nq - row, a.qt.nb)) - 1;
         walk = KeyWalk<kTileRows>(a.band, first, last);
+        front = 0;
+        if (a.front && walk.n > 0) {
+            const int from = max(0, first - a.band.window + 1) - a.front, n = (last - from) / kTileRows + 1;
+            if (from + a.front > a.band.sinks && n < walk.n) {
+                front = a.front;
+                walk.sinks = 0, walk.oldest = from, walk.n = n;
+            }
+        }
         const int CS = (int)cluster_size(), rank = (int)cluster_rank();
         lo = (int)((int64_t)walk.n * rank / CS);
         n = (int)((int64_t)walk.n * (rank + 1) / CS) - lo;
     }
     __device__ __forceinline__ int key(int j) const { return walk.key(lo + j); }
     __device__ __forceinline__ Band band(const FwdMmaArgs<true> &a, int j) const { return walk.band(a.band, lo + j); }
+    // tile j's first rows are the sinks'
+    __device__ __forceinline__ bool fronted(int j) const { return front && lo + j == 0; }
 };
 
 // A named barrier of `threads` threads (whole warps), and whether `p` holds in all of them.
@@ -153,7 +168,8 @@ __device__ __forceinline__ bool all_of(int id, int threads, bool p) {
     return r != 0;
 }
 
-template <int NT, bool BAND>
+// FRONT: sinks lie in front of the windows' first tiles.
+template <int NT, bool BAND, bool FRONT = false>
 __global__ void __launch_bounds__(Cfg<NT, BAND>::kThreads, Cfg<NT, BAND>::kMinBlocks)
 cross_fwd_mma_kernel(const __grid_constant__ FwdMmaArgs<BAND> a) {
     using C = Cfg<NT, BAND>;
@@ -269,8 +285,8 @@ cross_fwd_mma_kernel(const __grid_constant__ FwdMmaArgs<BAND> a) {
             int p = -1, highest = 0;                 // positions: of the row, of the tile's last
             if constexpr (BAND) {
                 highest = u.p0 + min(a.qt.Nq - u.row, a.qt.nb) - 1;
-                p = u.p0 + (a.qt.nb == kTileRows ? r : r % a.qt.nb);
-                if (p >= u.bound) p = -1;
+                p = u.p0 + (a.qt.gb == 1 ? r : r % a.qt.nb);
+                if (p > highest || p >= u.bound) p = -1;
             }
             float m = kNegInf, l = 0.f;
             uint32_t o[32];
@@ -289,8 +305,10 @@ cross_fwd_mma_kernel(const __grid_constant__ FwdMmaArgs<BAND> a) {
                     const Band w = u.band(a, j);
                     const int k0 = u.key(j), k1 = k0 + kTileRows - 1;
                     const bool all = k1 <= u.p0 && highest < u.bound && (k0 > highest - w.window || k1 < w.sinks);
-                    if (!all) {
-                        const uint32_t words[2] = {keys_of(w, p, k0 + 64 * half), keys_of(w, p, k0 + 64 * half + 32)};
+                    if (!all) {       // (nor is a fronted one)
+                        uint32_t words[2] = {keys_of(w, p, k0 + 64 * half), keys_of(w, p, k0 + 64 * half + 32)};
+                        if constexpr (FRONT)
+                            if (half == 0 && u.fronted(j)) words[0] = (words[0] & ~bits_below(u.front)) | (p < 0 ? 0u : bits_below(w.sinks));
 #pragma unroll
                         for (int i = 0; i < 2; ++i)
 #pragma unroll
@@ -375,7 +393,7 @@ cross_fwd_mma_kernel(const __grid_constant__ FwdMmaArgs<BAND> a) {
             }
             if constexpr (BAND) if (n > 0 && CS == 1) {
                 const int place = loaded++ % C::kQueries;
-                if (a.qt.nb == kTileRows) {
+                if (a.qt.gb == 1) {
                     uint8_t *tile = sq + place * kTileBytes;
                     const float inv = l == 0.f ? 0.f : 1.f / l;
 #pragma unroll
@@ -394,7 +412,7 @@ cross_fwd_mma_kernel(const __grid_constant__ FwdMmaArgs<BAND> a) {
                         tile_store(&a.o.map, q, h * a.o.head_step, u.b * a.o.seq_step, tile);
                         held = place;
                     }
-                    if (half == 0 && q + r < a.qt.Nq)
+                    if (half == 0 && r < a.qt.nb && q + r < a.qt.Nq)
                         a.LSE[((int64_t)u.b * a.Hq + h) * a.qt.Nq + q + r] = l == 0.f ? kNegInf : (m + log2f(l)) * kLn2;
                     return;
                 }
@@ -479,8 +497,19 @@ cross_fwd_mma_kernel(const __grid_constant__ FwdMmaArgs<BAND> a) {
                     if (!ok) break;
                     if (elect_one()) {
                         mbar_expect_tx(&bar_full[s], 2 * kTileBytes);
-                        load_tile(skv + (2 * s) * kTileBytes, a.k, u.key(j), u.hk, u.b, &bar_full[s]);
-                        load_tile(skv + (2 * s + 1) * kTileBytes, a.v, u.key(j), u.hk, u.b, &bar_full[s]);
+                        bool whole = true;
+                        if constexpr (FRONT) whole = !u.fronted(j);
+                        if (whole) {
+                            load_tile(skv + (2 * s) * kTileBytes, a.k, u.key(j), u.hk, u.b, &bar_full[s]);
+                            load_tile(skv + (2 * s + 1) * kTileBytes, a.v, u.key(j), u.hk, u.b, &bar_full[s]);
+                        } else if constexpr (FRONT) {
+#pragma unroll
+                            for (int i = 0; i < 2; ++i) {
+                                uint8_t *dst = skv + (2 * s + i) * kTileBytes;
+                                load_tile(dst, a.kv_front[i], 0, u.hk, u.b, &bar_full[s]);
+                                load_tile(dst + u.front * 128, a.kv_rest[i], u.key(j) + u.front, u.hk, u.b, &bar_full[s]);
+                            }
+                        }
                     }
                     __syncwarp();
                     ++ring;
@@ -535,8 +564,10 @@ cross_fwd_mma_kernel(const __grid_constant__ FwdMmaArgs<BAND> a) {
                 for (int j = 0; ok && j < n; ++j, ++ring) {
                     const int s = ring % C::kStages;
                     uint4 w;
-                    if constexpr (BAND) w = band_keys(u.band(a, j), u.first, u.last, u.key(j));
-                    else w = tile_keys(a.ks, u.b, u.key(j), u.bound);
+                    if constexpr (BAND) {
+                        w = band_keys(u.band(a, j), u.first, u.last, u.key(j));
+                        if (FRONT && u.fronted(j)) w.x = (w.x & ~bits_below(u.front)) | bits_below(a.band.sinks);
+                    } else w = tile_keys(a.ks, u.b, u.key(j), u.bound);
                     ok = pipe_wait(&bar_full[s], (ring / C::kStages) & 1, abort);
                     if (!ok) break;
                     if (!all_keys(w)) {
@@ -665,13 +696,13 @@ cross_fwd_mma_kernel(const __grid_constant__ FwdMmaArgs<BAND> a) {
 }
 
 // How many clusters of 2^i CTAs device `dev`, the current one, holds at once.
-template <int NT, bool BAND>
+template <int NT, bool BAND, bool FRONT>
 int held_clusters(int dev, int i) {
     using C = Cfg<NT, BAND>;
     static PerDevice known[5];
     return known[i].get(dev, [=] {
         return i == 0 ? C::kMinBlocks * sm_count()
-                      : clusters_held<cross_fwd_mma_kernel<NT, BAND>>(1 << i, C::kThreads, C::kSmem);
+                      : clusters_held<cross_fwd_mma_kernel<NT, BAND, FRONT>>(1 << i, C::kThreads, C::kSmem);
     });
 }
 
@@ -689,10 +720,10 @@ struct Plan {
     int nt = 0, c = 1;
     float cost = 0.f;
 };
-template <int NT, bool BAND>
+template <int NT, bool BAND, bool FRONT = false>
 cudaError_t consider(const CrossArgs &a, const TilesOf<BAND> &qt, Plan *best) {
     using C = Cfg<NT, BAND>;
-    const cudaError_t e = prepare_kernel<cross_fwd_mma_kernel<NT, BAND>>(C::kSmem, C::kRegs);
+    const cudaError_t e = prepare_kernel<cross_fwd_mma_kernel<NT, BAND, FRONT>>(C::kSmem, C::kRegs);
     if (e != cudaSuccess) return e;
     const int64_t units = (int64_t)a.B * a.Hkv * ((qt.tiles + NT - 1) / NT);
     int tiles = (a.Nk + kTileRows - 1) / kTileRows;
@@ -701,7 +732,7 @@ cudaError_t consider(const CrossArgs &a, const TilesOf<BAND> &qt, Plan *best) {
         tiles = (int)std::min<int64_t>(tiles, ((int64_t)a.band.window + (NT / qt.groups + 1) * qt.nb) / kTileRows + 1 +
                                                   (a.band.sinks + kTileRows - 1) / kTileRows);
     for (int i = 0; i < 5 && (i == 0 || tiles >= 1 << i); ++i) {
-        const int c = 1 << i, held = held_clusters<NT, BAND>(dev, i);
+        const int c = 1 << i, held = held_clusters<NT, BAND, FRONT>(dev, i);
         if (held < 1) break;
         const float tile = NT == 2 ? (qt.tiles > 1 ? 1.f : 0.78f) : units * c > sm_count() ? 1.28f : 0.83f;
         const float rounds = (float)((units + held - 1) / held), mine = (float)((tiles + c - 1) / c) * tile;
@@ -713,7 +744,23 @@ cudaError_t consider(const CrossArgs &a, const TilesOf<BAND> &qt, Plan *best) {
     return cudaSuccess;
 }
 
-template <int NT, bool BAND>
+// Rows that few sinks take in front of a tile of keys, 0: none (in eights, after which the tiles'
+// swizzle repeats).  Query tiles are as many rows shorter, so that their windows and the sinks
+// fill whole tiles; taken where all of them then take less, by 1.5%, than with a tile for the sinks: counted
+// in key tiles, of which a unit's start and end cost 3, over the windows' mean length (they
+// grow up to the first `window` queries, which need no such tile).  (16 heads on 4, 16385 tokens, 4 sinks: window
+// 128 45.5 -> 40.6 us, 512 68 -> 64, 1024 97.7 -> 94.4; 8 sequences, 12 heads on 4, window 512:
+// 1680 tokens 40.2 -> 37.3, 1569 tokens, 14 units for 13, 37.0 -> 37.2: not taken.)
+int front_rows(const CrossArgs &a) {
+    const int front = (a.band.sinks + 7) / 8 * 8, rows = kTileRows - front;
+    if (front == 0 || front > 32 || a.Nq < 2 * kTileRows) return 0;
+    const double first = a.Nk - a.Nq, window = a.band.window, grow = std::min<double>(std::max(window - first, 0.), a.Nq);
+    const double mean = (window - grow * grow / (2. * a.Nq)) / kTileRows, late = 1. - grow / a.Nq;
+    const auto cost = [&](int rows, double tiles) { return (a.Nq + rows - 1) / rows * (mean + 1. + tiles + 3.); };
+    return 1.015 * cost(rows, 0.) < cost(kTileRows, late) ? front : 0;
+}
+
+template <int NT, bool BAND, bool FRONT = false>
 cudaError_t fwd(const CrossArgs &a, const TilesOf<BAND> &qt, int c) {
     using C = Cfg<NT, BAND>;
     FwdMmaArgs<BAND> f;
@@ -721,7 +768,15 @@ cudaError_t fwd(const CrossArgs &a, const TilesOf<BAND> &qt, int c) {
     if (!make_tensor(&f.q, a.Q, a.B, a.Hq, a.Nq, qt.nb, qt.gb) || !make_tensor(&f.k, a.K, a.B, a.Hkv, a.Nk, kTileRows, 1) ||
         !make_tensor(&f.v, a.V, a.B, a.Hkv, a.Nk, kTileRows, 1))
         return cudaErrorInvalidValue;
-    if (BAND && qt.nb == kTileRows && !make_tensor(&f.o, a.O, a.B, a.Hq, a.Nq, kTileRows, 1)) return cudaErrorInvalidValue;
+    f.front = FRONT ? kTileRows - qt.nb : 0;
+    if constexpr (BAND) {
+        if (qt.gb == 1 && !make_tensor(&f.o, a.O, a.B, a.Hq, a.Nq, qt.nb, 1)) return cudaErrorInvalidValue;
+        const fibatt_heads *kv[2] = {&a.K, &a.V};
+        for (int i = 0; f.front && i < 2; ++i)
+            if (!make_tensor(&f.kv_front[i], *kv[i], a.B, a.Hkv, a.Nk, f.front, 1) ||
+                !make_tensor(&f.kv_rest[i], *kv[i], a.B, a.Hkv, a.Nk, kTileRows - f.front, 1))
+                return cudaErrorInvalidValue;
+    }
     f.ks = a.keys;
     f.band = a.band;
     f.O = rows_of<__nv_bfloat16>(a.O);
@@ -735,24 +790,33 @@ cudaError_t fwd(const CrossArgs &a, const TilesOf<BAND> &qt, int c) {
     const int64_t units = (int64_t)a.B * a.Hkv * f.pairs;
     f.units = (int)units;
     const int64_t grid = c > 1 || !C::kWalks || BAND ? units * c : std::min<int64_t>(units, C::kMinBlocks * sm_count());
-    return launch_clusters(cross_fwd_mma_kernel<NT, BAND>, (unsigned)grid, c, C::kThreads, C::kSmem, a.stream, f);
+    return launch_clusters(cross_fwd_mma_kernel<NT, BAND, FRONT>, (unsigned)grid, c, C::kThreads, C::kSmem, a.stream, f);
 }
 
-template <bool BAND>
-cudaError_t launch(const CrossArgs &a) {
-    const TilesOf<BAND> qt(a.Hq / a.Hkv, a.Nq, a.Hq > 1 && a.Q.stride_h == 0);
+template <bool FRONT>
+cudaError_t launch_band(const CrossArgs &a, int front) {
+    const BandTiles qt(a.Hq / a.Hkv, a.Nq, a.Hq > 1 && a.Q.stride_h == 0, kTileRows - front);
     Plan plan;
-    cudaError_t e = consider<1, BAND>(a, qt, &plan);
-    if constexpr (!BAND) {
-        if (e == cudaSuccess) e = consider<2, BAND>(a, qt, &plan);
-        if (e == cudaSuccess && plan.nt == 2) return fwd<2, BAND>(a, qt, plan.c);
-    }
-    return e == cudaSuccess ? fwd<1, BAND>(a, qt, plan.c) : e;
+    const cudaError_t e = consider<1, true, FRONT>(a, qt, &plan);
+    return e == cudaSuccess ? fwd<1, true, FRONT>(a, qt, plan.c) : e;
+}
+
+cudaError_t launch(const CrossArgs &a) {
+    const QueryTiles qt(a.Hq / a.Hkv, a.Nq, a.Hq > 1 && a.Q.stride_h == 0);
+    Plan plan;
+    cudaError_t e = consider<1, false>(a, qt, &plan);
+    if (e == cudaSuccess) e = consider<2, false>(a, qt, &plan);
+    if (e != cudaSuccess) return e;
+    return plan.nt == 2 ? fwd<2, false>(a, qt, plan.c) : fwd<1, false>(a, qt, plan.c);
 }
 
 }  // namespace
 
-cudaError_t launch_cross_fwd_mma(const CrossArgs &a) { return a.banded ? launch<true>(a) : launch<false>(a); }
+cudaError_t launch_cross_fwd_mma(const CrossArgs &a) {
+    if (!a.banded) return launch(a);
+    const int front = front_rows(a);
+    return front ? launch_band<true>(a, front) : launch_band<false>(a, 0);
+}
 
 FIBATT_DEFINE_ERROR_READER(read_error_cross_mma_fwd, "cross_mma_fwd.cu")
 

@@ -29,8 +29,9 @@ struct QueryTiles {
     int tiles;       // of one key/value head
     // shared_rows: the heads' rows are one and the same in memory (a stride of
     // 0), so no copy can bring several of them
-    QueryTiles(int G, int Nq, bool shared_rows) : G(G), Nq(Nq) {
-        nb = Nq < kTileRows ? Nq : kTileRows;
+    // rows: queries of a tile at most
+    QueryTiles(int G, int Nq, bool shared_rows, int rows = kTileRows) : G(G), Nq(Nq) {
+        nb = Nq < rows ? Nq : rows;
         gb = shared_rows ? 1 : kTileRows / nb < G ? kTileRows / nb : G;
         ntiles = (Nq + nb - 1) / nb;
         tiles = ntiles * ((G + gb - 1) / gb);
@@ -53,7 +54,8 @@ struct QueryTiles {
 // attend the same keys, or nearly, and a range of positions is a range of tiles.
 struct BandTiles : QueryTiles {
     int groups;
-    BandTiles(int G, int Nq, bool shared_rows) : QueryTiles(G, Nq, shared_rows), groups((G + gb - 1) / gb) {}
+    BandTiles(int G, int Nq, bool shared_rows, int rows = kTileRows)
+        : QueryTiles(G, Nq, shared_rows, rows), groups((G + gb - 1) / gb) {}
 #ifdef __CUDACC__
     __device__ __forceinline__ int first_head(int t) const { return t % groups * gb; }
     __device__ __forceinline__ int first_row(int t) const { return t / groups * nb; }
