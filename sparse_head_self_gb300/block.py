@@ -215,12 +215,14 @@ class WindowSelfAttention(nn.Module):
         Without gradients; start is the caller's to move on."""
         N = x.shape[1]
         places = start[:, None] + torch.arange(N, dtype=torch.int32, device=x.device)
+        held = start + (N if count is None else count.clamp(0, N))
+        if count is not None:      # tokens that are left out stand at the last place that there is
+            places = torch.minimum(places, held[:, None] - 1)
         q, k, v = self._split(x, places)
         cache_store(cache, table, k, v, start, count)
         if self.heads // self.kv_heads * N <= self.FEW_ROWS:
             return self._join(cache_fwd(q, cache, table, start, self.scale, self.window, self.sinks, count)[0])
-        held = start + (N if count is None else count.clamp(0, N))
-        k, v = cache_load(cache, table, table.shape[1] * PAGE, None, held, dtype=x.dtype)
+        k, v = cache_load(cache, table, table.shape[1] * PAGE, None, held, dtype=q.dtype)
         return self._join(window_fwd(q, k, v, self.scale, self.window, self.sinks, start, held)[0])
 
 
