@@ -424,9 +424,10 @@ typedef struct {
  * scale anew; one that continues it (a first position that is not a multiple
  * of 64) raises the scale where its tokens need that, and rounds the page's older
  * tokens again, which changes only values below 2^-6 of the new scale; the
- * page's rows behind the call's tokens are left as they were.  Two
- * sequences of a call may not store into one page.  INVALID_ARG: a size or stride out of its range, a NULL or
- * misaligned pointer, 2^31 blocks (two a page and head) or more.  UNSUPPORTED: D, dtype. */
+ * page's rows behind the call's tokens are left as they were.  No page may be stored
+ * into twice in a call, by two sequences or by one whose table names it twice.  INVALID_ARG:
+ * a size or stride out of its range, a NULL or misaligned pointer, 2^31 blocks (two a
+ * page and head) or more.  UNSUPPORTED: D, dtype. */
 fibatt_status fibatt_cache_store(const fibatt_cache *d, const fibatt_heads *K, const fibatt_heads *V,
                                  cudaStream_t stream);
 
@@ -445,7 +446,8 @@ fibatt_status fibatt_cache_load(const fibatt_cache *d, const fibatt_heads *K, co
  * Arithmetic: products of halves with fp32 sums (queries exact in bf16, 22 bits in fp32,
  * relative to their row's largest; weights 11 bits in bf16 I/O, 22 in fp32), O rounded
  * once.  What the pages hold behind the last token, or in
- * keys that no query attends, reaches no result.  Errors as above, and
+ * keys that no query attends, reaches no result (one that is not finite and is
+ * attended may reach the other queries of its block of 16 rows).  Errors as above, and
  * INVALID_ARG for Hq, scale, window, sinks out of their range. */
 fibatt_status fibatt_cache_fwd(const fibatt_cache *d, int Hq, float scale, int window, int sinks,
                                const fibatt_heads *Q, const fibatt_heads *O, float *LSE,

@@ -96,9 +96,9 @@ __global__ void __launch_bounds__(kStoreThreads) cache_store_kernel(const __grid
     grid_dep_launch();
     const Spot s(a, blockIdx.x);
     if (s.lost && threadIdx.x == 0) atomicOr(&g_device_error, kErrPage);
-    if (s.page < 0) return;
+    if (s.page < 0 || !FIBATT_CHECKED(s.b < a.B && s.page < a.pages && s.lo >= 0 && s.hi <= kPage)) return;
     const int t = threadIdx.x >> 1, half = threadIdx.x & 1;
-    const bool mine = t >= s.lo && t < s.hi;
+    const bool mine = t >= s.lo && t < s.hi && FIBATT_CHECKED(s.token + t >= 0 && s.token + t < a.N);
     float x[32], top = 0.f;
     if (mine) {
         const Rows<const T> rows{static_cast<const T *>(s.kind ? a.V.ptr : a.K.ptr), s.kind ? a.V.stride_b : a.K.stride_b,
@@ -200,7 +200,7 @@ __global__ void __launch_bounds__(kStoreThreads) cache_load_kernel(const __grid_
             }
         }
     }
-    if (n < 0 || n >= a.N) return;
+    if (n < 0 || n >= a.N || !FIBATT_CHECKED(s.b < a.B && s.page < a.pages)) return;
     const Rows<T> rows{static_cast<T *>(s.kind ? a.V.ptr : a.K.ptr), s.kind ? a.V.stride_b : a.K.stride_b,
                        s.kind ? a.V.stride_h : a.K.stride_h, s.kind ? a.V.stride_n : a.K.stride_n};
     store32(rows.row(s.b, s.hk, n) + 32 * half, x);
@@ -294,6 +294,7 @@ cache_fwd_kernel(const __grid_constant__ AttendArgs a, Rows<const T> Q, Rows<T> 
     volatile int *abort = &abort_flag;
     const int warp = warp_number(), pair = warp >> 1, sub = warp & 1, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
     const unsigned C = cluster_size(), rank = cluster_rank();
+    if (!FIBATT_CHECKED(blockIdx.x / C < (unsigned)a.units)) return;       // whole clusters
     if (threadIdx.x < kPairs * kStages) mbar_init(&full[0][0] + threadIdx.x, 1);
     if (threadIdx.x == 0) abort_flag = 0;
     if (C > 1) cluster_arrive();      // (waited for below, before the first write to another CTA)
@@ -335,6 +336,7 @@ cache_fwd_kernel(const __grid_constant__ AttendArgs a, Rows<const T> Q, Rows<T> 
             if (k + lane < mine) {
                 pages = a.c.page(b, walk.tile(at + (k + lane) * step));
                 if (pages < 0 && sub == 0) atomicOr(&g_device_error, kErrPage);
+                if (!FIBATT_CHECKED(pages < a.c.pages)) pages = -1;
             }
             scales = make_float2(0.f, 0.f);
             if (pages >= 0) scales = __ldg(reinterpret_cast<const float2 *>(a.c.scales) + a.c.place(pages, hk));
@@ -545,6 +547,7 @@ cache_fwd_kernel(const __grid_constant__ AttendArgs a, Rows<const T> Q, Rows<T> 
     __syncthreads();
     if (C > 1) cluster_wait();
     const auto finish = [&](int r, int d, float2 x) {
+        if (!FIBATT_CHECKED(r < rows && token(r) < a.c.N)) return;
         const float2 ml = row_ml[r];
         const int n = token(r), h = hk * a.G + (r0 + r - n * a.G), p = start + n;
         const bool none = p > last || ml.y == 0.f;
