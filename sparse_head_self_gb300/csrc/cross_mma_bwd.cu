@@ -39,6 +39,17 @@
 // cycles, its 3 or 4 products 800 or 1090 of them; the tensor cores are 61% busy, the
 // issue slots 49%: what is left are the waits from S to dS to the products, which need
 // each other within a tile.
+//
+// Attention over a window with sinks (BAND): walks over the tiles that the held rows' windows meet, masked at
+// their ends from the positions.  Key tiles first, whose walks are longer (a head group's queries: 36
+// tiles next to 9, at window 1024 and 4 heads a key head; queries first: 96 us for 89 on eight clips).  The
+// keys of a tile with sinks meet every later query: such walks are cut into parts (SinkParts), whose sums
+// a small kernel adds in their order.  Walks being short, what lies between units counts: a unit's
+// results are put where its held rows were and leave by tensor copies that the copying warp sends, and
+// its rows' statistics are asked for one unit ahead.
+// Measured (4 sinks): 16 heads on 4, 16385 tokens, window 1024: 261 us, 639 TFLOP/s of the 5 products (tensor
+// cores 54% busy, issue slots 59%; the small kernels about 20 us of it); 8 sequences, 12 heads on 4, up to
+// 1569 tokens, window 512: 82.8, 327 (the first small kernel about 9; units of 5 or 6 tiles of keys, 16 of queries).
 #include <algorithm>
 
 #include "cluster.cuh"
@@ -1059,18 +1070,25 @@ int padded_rows(int Nq) { return Nq < kTileRows ? Nq : (Nq + kTileRows - 1) / kT
 
 namespace {
 
-// How the walks of key tiles with sinks are cut: into parts about as long as the other
-// tiles' walks, as long as there are no more than kParts of them in all (two a SM, each
-// with 64 KB of partial sums).  (One sequence of 16385 tokens, 16 heads on 4, window 1024, 4
-// sinks: walks of 516 tiles next to others of 36; in one part 673 us.)
+// How the walks of key tiles with sinks are cut: into parts as long as the other tiles' walks, or as half of
+// what an SM has in all where that is more (they come first, so that the rest evens them out), as
+// long as there are no more than kParts of them in all (two a SM, each with 64 KB of partial sums).  (One
+// sequence of 16385 tokens, 16 heads on 4, window 1024, 4 sinks: walks of 516 tiles next to others of
+// 36; in one part 673 us, in parts of 36 266, as here 261; window 128: 151 and 129; eight sequences of
+// 1569, 12 heads on 4, window 512, in one part here: 107 and 101.6.)
 struct SinkParts {
     static constexpr int64_t kParts = 304;
     int64_t tiles = 0, chunks = 1, length = 0;       // key tiles of a head; parts of each, query tiles of a part
     SinkParts(int B, int Hkv, int Nk, const Band &w, const BandTiles &qt) {
-        tiles = std::min<int64_t>((w.sinks + kTileRows - 1) / kTileRows, (Nk + kTileRows - 1) / kTileRows);
+        const int64_t ktiles = (Nk + kTileRows - 1) / kTileRows;
+        tiles = std::min<int64_t>((w.sinks + kTileRows - 1) / kTileRows, ktiles);
         if (tiles == 0) return;
         const int64_t other = ((int64_t)(w.window + kTileRows) / qt.nb + 1) * qt.groups, heads = (int64_t)B * Hkv * tiles;
-        length = std::max({other, (heads * qt.tiles + kParts - 1) / kParts, (qt.tiles + 255) / (int64_t)256});
+        // tiles that all walks have, of keys that the windows meet and of queries
+        const int64_t met = std::min<int64_t>(ktiles, ((int64_t)qt.Nq + w.window) / kTileRows + 1);
+        const int64_t all = (int64_t)B * Hkv * (met * std::min<int64_t>(other, qt.tiles) +
+                                                qt.tiles * std::min<int64_t>(ktiles, w.window / kTileRows + 2));
+        length = std::max({other, all / kParts, (heads * qt.tiles + kParts - 1) / kParts, (qt.tiles + 255) / (int64_t)256});
         chunks = (qt.tiles + length - 1) / length;
     }
     size_t bytes(int B, int Hkv) const {

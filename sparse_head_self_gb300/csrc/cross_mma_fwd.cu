@@ -36,6 +36,24 @@
 // 290), 1024 of exponentials (4 cycles a warp and scheduler), which overlap but for
 // the waits between them; the issue slots are 59% taken.  The short shapes are bound by the
 // latencies of a unit's start and end.
+//
+// Attention over a window with sinks (BAND): a query tile's walk is over the tiles from the
+// oldest key that its queries attend to the newest, and over those of the sinks, so that 128 queries
+// with a window of w cost about (w + 127) / 128 rounded up, and one; only the tiles at the
+// window's two ends and the sinks' are masked, from the positions, without memory.  Such walks are short
+// (2 to 9 tiles), and what a unit costs besides, about 1.8 us of a SM's time, decides.  Hence:
+//   one tile of queries a CTA, two CTAs a SM, each of which goes on with the unit of a CTA that has not
+//     started, struck off by the hardware (the third shape below 44 -> 35 us, the second 98 -> 78)
+//   the next unit's queries are copied to a second place while this one's are in use, and O leaves from
+//     its queries' place by a tensor copy that nobody waits for (the third 49 -> 44)
+//   walks start at the oldest key, not at a multiple of 128 (the third 34 -> 32)
+//   tiles of neighbouring positions and of heads that share keys are neighbours in the grid: L2 serves 81% of the reads
+//   few sinks in front of the window's first tile, and 32 columns left out, where that pays (below)
+// Measured (4 sinks): 16 heads on 4 key heads, 16385 tokens, window 1024: 95.4 us, 700 TFLOP/s of
+// the pairs attended (36% and 37% of the time tensor cores and exponentials work, issue slots 63% taken); 2 times 1569
+// queries on 16385 keys, window 4096: 73.9, 713; 8 sequences, 12 heads on 4, up to 1569 tokens, window
+// 512: 31.5, 344 (units of 5 or 6 tiles, two or three of them masked); 64 sequences, 12 heads, up
+// to 197 tokens, window 64, 1 sink: 24.9, 2.5 TB/s.
 #include <algorithm>
 
 #include "cluster.cuh"
