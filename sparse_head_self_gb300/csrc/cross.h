@@ -67,6 +67,26 @@ struct Band {
     __host__ __device__ __forceinline__ bool sees(int p, int k) const { return k <= p && (k > p - window || k < sinks); }
 };
 
+// Division of numbers below 2^31 by a divisor that a call has once: with s = ceil(log2 d) and m = 2^32 (2^s - d) / d
+// rounded down, plus 1, the quotient is (n m / 2^32 + n) / 2^s, both rounded down (Granlund and Montgomery,
+// Division by Invariant Integers using Multiplication, 1994).  The processors have no division: one takes 30
+// instructions or so.
+struct Div {
+    uint32_t d, m, s;
+    explicit Div(uint32_t by = 1) : d(by), s(0) {
+        while ((1ull << s) < d) ++s;
+        m = (uint32_t)((((1ull << s) - d) << 32) / d + 1);
+    }
+    __host__ __device__ __forceinline__ int of(int n) const {
+#ifdef __CUDA_ARCH__
+        return (int)((__umulhi(m, (uint32_t)n) + (uint32_t)n) >> s);
+#else
+        return (int)((((uint64_t)m * (uint32_t)n >> 32) + (uint32_t)n) >> s);
+#endif
+    }
+    __host__ __device__ __forceinline__ int rest(int n) const { return n - of(n) * (int)d; }
+};
+
 // Bits below n: none for n <= 0, all for n >= 32.
 __host__ __device__ __forceinline__ uint32_t bits_below(int n) {
 #ifdef __CUDA_ARCH__

@@ -95,6 +95,7 @@ struct BwdMmaArgs {
     float scale;
     float c;                    // scale log2 e, not 0
     Band band;                  // BAND
+    Div by_heads, by_hkv, by_sinks;     // BAND: heads of keys of all sequences, of one, and the sinks' tiles of all
     TensorArg dq, dk, dv;       // BAND: the gradients as tensor copies write them (dQ: tiles of 128 queries)
     BwdMmaArgs() : qt(1, 1, false) {}
 };
@@ -387,12 +388,14 @@ struct Unit : UnitBand<BAND> {
         this->chunk = -1;
         if (KEYS) {
             const int tiles = a.sink_tiles * heads;
-            if (unit < a.sink_units) this->chunk = unit / tiles, unit %= tiles;
+            if (unit < a.sink_units) this->chunk = a.by_sinks.of(unit), unit = a.by_sinks.rest(unit);
             else unit += tiles - a.sink_units;
         }
-        mine = KEYS ? unit / heads : a.qt.tiles - 1 - unit / heads;
-        hk = unit % heads % a.Hkv;
-        b = unit % heads / a.Hkv;
+        mine = a.by_heads.of(unit);
+        unit -= mine * heads;
+        if (!KEYS) mine = a.qt.tiles - 1 - mine;
+        b = a.by_hkv.of(unit);
+        hk = unit - b * a.Hkv;
         bound = a.ks.bound(b);
         this->p0 = a.band.first(b);
         keys = make_uint4(0, 0, 0, 0);
@@ -404,8 +407,8 @@ struct Unit : UnitBand<BAND> {
             this->last = (k0 < a.band.sinks ? end : min(end, k1 + a.band.window)) - 1;
             const bool some = k0 <= k1 && this->first <= this->last;
             if (!some) this->last = this->first - 1;
-            from = some ? (this->first - this->p0) / a.qt.nb * a.qt.groups : 0;
-            tiles = some ? ((this->last - this->p0) / a.qt.nb + 1) * a.qt.groups - from : 0;
+            from = some ? a.qt.by_rows.of(this->first - this->p0) * a.qt.groups : 0;
+            tiles = some ? (a.qt.by_rows.of(this->last - this->p0) + 1) * a.qt.groups - from : 0;
             keys = band_keys(a.band, this->first, this->last, k0);
         } else {
             this->first = max(0, this->p0 + a.qt.first_row(mine));
@@ -420,8 +423,11 @@ struct Unit : UnitBand<BAND> {
             return;
         }
         const int CS = (int)cluster_size(), rank = (int)cluster_rank();
-        lo = (int)((int64_t)tiles * rank / CS);
-        n = (int)((int64_t)tiles * (rank + 1) / CS) - lo;
+        lo = 0, n = tiles;
+        if (CS > 1) {
+            lo = (int)((int64_t)tiles * rank / CS);
+            n = (int)((int64_t)tiles * (rank + 1) / CS) - lo;
+        }
         lo += from;
     }
     // first key of tile j of held queries' walk
@@ -502,11 +508,11 @@ __device__ __forceinline__ int weights(const BwdMmaArgs<BAND> &a, Shared<BAND> &
         if (!KEYS) {
             lowest = u.p0 + a.qt.first_row(u.mine);
             highest = u.p0 + min(a.qt.Nq, a.qt.first_row(u.mine) + a.qt.nb) - 1;
-            p = lowest + (a.qt.nb == kTileRows ? r : r % a.qt.nb);
+            p = lowest + a.qt.by_rows.rest(r);
             if (p >= u.bound) p = -1;
         } else if (a.qt.nb < kTileRows) {
             const int k = u.mine * kTileRows + r;
-            for (int i = 0, n = 32 * cg % a.qt.nb; i < 32; ++i) {
+            for (int i = 0, n = a.qt.by_rows.rest(32 * cg); i < 32; ++i) {
                 const int at = u.p0 + n;
                 if (at >= u.first && at <= u.last && a.band.sees(at, k)) same |= 1u << i;
                 if (++n == a.qt.nb) n = 0;
@@ -1139,12 +1145,14 @@ cudaError_t bwd(const CrossArgs &a) {
         if ((f.qt.nb == kTileRows && !make_tensor(&f.dq, a.dQ, a.B, a.Hq, a.Nq, kTileRows, 1)) ||
             !make_tensor(&f.dk, a.dK, a.B, a.Hkv, a.Nk, kTileRows, 1) || !make_tensor(&f.dv, a.dV, a.B, a.Hkv, a.Nk, kTileRows, 1))
             return cudaErrorInvalidValue;
+        f.by_heads = Div((uint32_t)(a.B * a.Hkv)), f.by_hkv = Div((uint32_t)a.Hkv);
         const SinkParts p(a.B, a.Hkv, a.Nk, a.band, f.qt);
         if (p.chunks > 1) {
             f.chunks = (int)p.chunks;
             f.chunk_tiles = (int)p.length;
             f.sink_tiles = (int)p.tiles;
             f.sink_units = (int)((int64_t)a.B * a.Hkv * p.tiles * p.chunks);
+            f.by_sinks = Div((uint32_t)(a.B * a.Hkv * (int)p.tiles));
             f.parts = reinterpret_cast<float4 *>(reinterpret_cast<char *>(a.stats) +
                                                  round_16(cross_bwd_mma_workspace(a.B, a.Hq, a.Nq)));
         }

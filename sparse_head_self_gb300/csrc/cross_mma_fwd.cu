@@ -98,6 +98,7 @@ struct FwdMmaArgs {
     float c;                 // |scale| log2 e (> 0)
     int negative;            // scale < 0
     Band band;               // BAND
+    Div by_heads, by_hkv;    // BAND: heads of keys of all sequences, of one
     TensorArg o;             // BAND, tiles of one head: O as tensor copies write it
     // BAND: few sinks lie in front of the windows' first tile, in `front` rows of it (0: in tiles of their
     // own); boxes of those and of the other rows
@@ -113,10 +114,10 @@ struct Place {
     __device__ __forceinline__ Place() {}
     __device__ __forceinline__ Place(const FwdMmaArgs<BAND> &a, int unit) {
         if constexpr (BAND) {      // the last queries, which attend the most keys, first
-            const int heads = a.units / a.pairs;
-            t0 = (a.pairs - 1 - unit / heads) * NT;
-            hk = unit % heads % a.Hkv;
-            b = unit % heads / a.Hkv;
+            const int step = a.by_heads.of(unit), head = unit - step * (int)a.by_heads.d;
+            t0 = (a.pairs - 1 - step) * NT;
+            b = a.by_hkv.of(head);
+            hk = head - b * a.Hkv;
         } else {
             t0 = unit % a.pairs * NT;
             hk = unit / a.pairs % a.Hkv;
@@ -167,8 +168,11 @@ struct Unit<NT, true> : Place<NT, true> {
             }
         }
         const int CS = (int)cluster_size(), rank = (int)cluster_rank();
-        lo = (int)((int64_t)walk.n * rank / CS);
-        n = (int)((int64_t)walk.n * (rank + 1) / CS) - lo;
+        lo = 0, n = walk.n;
+        if (CS > 1) {
+            lo = (int)((int64_t)walk.n * rank / CS);
+            n = (int)((int64_t)walk.n * (rank + 1) / CS) - lo;
+        }
     }
     __device__ __forceinline__ int key(int j) const { return walk.key(lo + j); }
     __device__ __forceinline__ Band band(const FwdMmaArgs<true> &a, int j) const { return walk.band(a.band, lo + j); }
@@ -303,7 +307,7 @@ cross_fwd_mma_kernel(const __grid_constant__ FwdMmaArgs<BAND> a) {
             int p = -1, highest = 0;                 // positions: of the row, of the tile's last
             if constexpr (BAND) {
                 highest = u.p0 + min(a.qt.Nq - u.row, a.qt.nb) - 1;
-                p = u.p0 + (a.qt.gb == 1 ? r : r % a.qt.nb);
+                p = u.p0 + (a.qt.gb == 1 ? r : a.qt.by_rows.rest(r));
                 if (p > highest || p >= u.bound) p = -1;
             }
             float m = kNegInf, l = 0.f;
@@ -798,6 +802,7 @@ cudaError_t fwd(const CrossArgs &a, const TilesOf<BAND> &qt, int c) {
     if (!make_tensor(&f.q, a.Q, a.B, a.Hq, a.Nq, qt.nb, qt.gb) || !make_tensor(&f.k, a.K, a.B, a.Hkv, a.Nk, kTileRows, 1) ||
         !make_tensor(&f.v, a.V, a.B, a.Hkv, a.Nk, kTileRows, 1))
         return cudaErrorInvalidValue;
+    f.by_heads = Div((uint32_t)(a.B * a.Hkv)), f.by_hkv = Div((uint32_t)a.Hkv);
     f.front = FRONT ? kTileRows - qt.nb : 0;
     if constexpr (BAND) {
         if (qt.gb == 1 && !make_tensor(&f.o, a.O, a.B, a.Hq, a.Nq, qt.nb, 1)) return cudaErrorInvalidValue;

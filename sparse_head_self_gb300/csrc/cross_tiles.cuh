@@ -54,14 +54,16 @@ struct QueryTiles {
 // attend the same keys, or nearly, and a range of positions is a range of tiles.
 struct BandTiles : QueryTiles {
     int groups;
+    Div by_groups, by_rows;
     BandTiles(int G, int Nq, bool shared_rows, int rows = kTileRows)
-        : QueryTiles(G, Nq, shared_rows, rows), groups((G + gb - 1) / gb) {}
+        : QueryTiles(G, Nq, shared_rows, rows), groups((G + gb - 1) / gb), by_groups(groups), by_rows(nb) {}
 #ifdef __CUDACC__
-    __device__ __forceinline__ int first_head(int t) const { return t % groups * gb; }
-    __device__ __forceinline__ int first_row(int t) const { return t / groups * nb; }
+    __device__ __forceinline__ int first_head(int t) const { return by_groups.rest(t) * gb; }
+    __device__ __forceinline__ int first_row(int t) const { return by_groups.of(t) * nb; }
     __device__ __forceinline__ bool at(int t, int r, int &g, int &n) const {
-        g = first_head(t) + r / nb;
-        n = first_row(t) + r % nb;
+        const int step = by_groups.of(t), head = by_rows.of(r);
+        g = (t - step * groups) * gb + head;
+        n = step * nb + r - head * nb;
         return r < nb * gb && g < G && n < Nq;
     }
 #endif
