@@ -90,6 +90,7 @@ struct BwdMmaArgs {
     int chunks, chunk_tiles;    // BAND: parts of a sinks' walk and the query tiles of each, ...
     int sink_tiles, sink_units; // ... key tiles that have such walks, units of those parts
     float4 *parts;              // their partial sums, one after another
+    int cleared;                // BAND: dQ of queries outside their sequence is, and units of such alone are left out
     int first_unit;             // of the launch, which has those up to `units`
     int *next_unit;             // units given out behind every CTA's first
     float scale;
@@ -185,13 +186,15 @@ cross_parts_kernel(int Hq, int Hkv, int Nq, int npad, unsigned rows, KeySet ks, 
 }
 
 // The same for a window's queries where a head has rows enough: a block has 64 rows of one head,
-// four threads each, and rows outside their sequence are not read.  (The gradient of 16 heads of
+// four threads each, and rows outside their sequence are not read; their dQ is cleared, which
+// leaves the next kernel no units of queries without tiles.  (The gradient of 16 heads of
 // 16385 tokens 268 us, 270 with the kernel above; of eight clips of several lengths 86.7 and 89.2.)
 constexpr int kPartRows = 64;
 __global__ void __launch_bounds__(4 * kPartRows)
 window_parts_kernel(int Hq, int Nq, int npad, unsigned heads, KeySet ks, Band band, Rows<const __nv_bfloat16> O,
                     Rows<const __nv_bfloat16> dO, const float *__restrict__ LSE, float c, float2 *__restrict__ stats,
-                    uint4 *__restrict__ lse_parts, uint4 *__restrict__ d_parts, int *__restrict__ next_unit) {
+                    uint4 *__restrict__ lse_parts, uint4 *__restrict__ d_parts, int *__restrict__ next_unit,
+                    Rows<__nv_bfloat16> dQ) {
     grid_dep_wait();
     grid_dep_launch();
     if (blockIdx.x == 0 && threadIdx.x < 2) next_unit[threadIdx.x] = 0;
@@ -217,6 +220,9 @@ window_parts_kernel(int Hq, int Nq, int npad, unsigned heads, KeySet ks, Band ba
             d = dot2_bf16(o0.x, g0.x, dot2_bf16(o0.y, g0.y, 0.f)) + dot2_bf16(o0.z, g0.z, dot2_bf16(o0.w, g0.w, 0.f)) +
                 (dot2_bf16(o1.x, g1.x, dot2_bf16(o1.y, g1.y, 0.f)) + dot2_bf16(o1.z, g1.z, dot2_bf16(o1.w, g1.w, 0.f)));
         }
+    } else if (n < Nq) {
+        uint4 *to = reinterpret_cast<uint4 *>(dQ.row(b, h, n)) + 2 * i;
+        to[0] = to[1] = make_uint4(0, 0, 0, 0);
     }
     const unsigned four = 0xfu << (threadIdx.x & 28);
     d += __shfl_xor_sync(four, d, 1);
@@ -470,12 +476,13 @@ struct Tiles {
 // units of the CTA: tile it is in stage it mod kStages, and each barrier of the
 // pipeline completes a phase per tile.
 
-// (LSE log2 e, D) of a thread's row of held queries.
+// (LSE log2 e, D) of a thread's row of held queries; anything where it has none.  (No branch, at whose end the
+// value would be waited for.)
 __device__ __forceinline__ float2 row_stats(const BwdMmaArgs<true> &a, const Unit<true> &u) {
     const int r = (int)(warp_number() & 3) * 32 + (int)(threadIdx.x & 31);
     int g, q;
-    if (u.index < a.first_kind || u.index >= a.units || !a.qt.at(u.mine, r, g, q)) return make_float2(kInf, 0.f);
-    return __ldg(a.stats + ((int64_t)u.b * a.Hq + u.hk * a.qt.G + g) * a.qt.Nq + q);
+    const bool row = u.index >= a.first_kind && u.index < a.units && a.qt.at(u.mine, r, g, q);
+    return __ldg(a.stats + (row ? ((int64_t)u.b * a.Hq + u.hk * a.qt.G + g) * a.qt.Nq + q : 0));
 }
 
 // P and dS: row = lane of the quarter, 32 columns.  BAND: `stats` of the unit's rows; `ahead` before the
@@ -983,9 +990,11 @@ __global__ void __launch_bounds__(kThreads, 1) cross_bwd_mma_kernel(const __grid
             const auto pass = [&] {      // (its copies being out, the next unit's number has come meanwhile)
                 const int i = passed & 1;
                 Unit<BAND> u;
-                u.enter(a, __shfl_sync(kFullMask, drawn, 0));
-                drawn = a.units;
-                if (CS == 1 && lane == 0 && u.index < a.units) drawn = a.first_unit + (int)gridDim.x + atomicAdd(a.next_unit, 1);
+                do {
+                    u.enter(a, __shfl_sync(kFullMask, drawn, 0));
+                    drawn = a.units;
+                    if (CS == 1 && lane == 0 && u.index < a.units) drawn = a.first_unit + (int)gridDim.x + atomicAdd(a.next_unit, 1);
+                } while (BAND && a.cleared && CS == 1 && u.n == 0 && u.index >= a.first_kind && u.index < a.units);
                 ok = ok && (passed < 2 || pipe_wait(&sh.unit_empty[i], ((passed >> 1) - 1) & 1, &sh.abort));
                 if constexpr (BAND) {      // (the unit before last is over by now, or nearly)
                     ok = ok && (passed < 2 || pipe_wait(&sh.out[i], ((passed >> 1) - 1) & 1, &sh.abort));
@@ -1139,7 +1148,7 @@ cudaError_t bwd(const CrossArgs &a) {
     f.stats = stats;
     f.next_unit = reinterpret_cast<int *>(stats + (int64_t)a.B * a.Hq * a.Nq);
     f.lse_parts = lse_parts, f.d_parts = d_parts;
-    f.chunks = 1, f.chunk_tiles = f.sink_tiles = f.sink_units = 0;
+    f.chunks = 1, f.chunk_tiles = f.sink_tiles = f.sink_units = f.cleared = 0;
     f.parts = nullptr;
     if constexpr (BAND) {
         if ((f.qt.nb == kTileRows && !make_tensor(&f.dq, a.dQ, a.B, a.Hq, a.Nq, kTileRows, 1)) ||
@@ -1177,7 +1186,8 @@ cudaError_t bwd(const CrossArgs &a) {
         e = launch_clusters(window_parts_kernel, heads * steps + kTileRows / kPartRows, 1, 4 * kPartRows, 0, a.stream, a.Hq, a.Nq,
                             f.npad, heads, a.keys, a.band, rows_of<const __nv_bfloat16>(a.O),
                             rows_of<const __nv_bfloat16>(a.dO), static_cast<const float *>(a.LSE), f.c, stats, lse_parts,
-                            d_parts, f.next_unit);
+                            d_parts, f.next_unit, f.dQ);
+        f.cleared = 1;
     } else {
         const auto kernel = !BAND && a.keys.len ? cross_parts_kernel<true> : cross_parts_kernel<false>;
         e = launch_clusters(kernel, (unsigned)((rows + kTileRows + 31) / 32), 1, 256, 0, a.stream, a.Hq, a.Hkv, a.Nq, f.npad,
