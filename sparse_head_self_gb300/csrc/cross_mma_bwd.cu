@@ -46,10 +46,12 @@
 // keys of a tile with sinks meet every later query: such walks are cut into parts (SinkParts), whose sums
 // a small kernel adds in their order.  Walks being short, what lies between units counts: a unit's
 // results are put where its held rows were and leave by tensor copies that the copying warp sends, and
-// its rows' statistics are asked for one unit ahead.
-// Measured (4 sinks): 16 heads on 4, 16385 tokens, window 1024: 261 us, 639 TFLOP/s of the 5 products (tensor
-// cores 54% busy, issue slots 59%; the small kernels about 20 us of it); 8 sequences, 12 heads on 4, up to
-// 1569 tokens, window 512: 82.8, 327 (the first small kernel about 9; units of 5 or 6 tiles of keys, 16 of queries).
+// its rows' statistics are asked for one unit ahead; no thread divides (Div: 261 -> 251 us, and 82.8 -> 78.5 below, where
+// a tile of keys took 2140 cycles for 1600).
+// Measured (4 sinks): 16 heads on 4, 16385 tokens, window 1024: 250 us, 669 TFLOP/s of the 5 products (about 1600
+// cycles a tile of either kind, 2150 between units of 9 or 10 tiles; the small kernels about 20 us of it); 8 sequences,
+// 12 heads on 4, up to 1569 tokens, window 512: 75.1, 360 (the first small kernel about 9; units of 5 or 6 tiles of
+// keys, 16 of queries).
 #include <algorithm>
 
 #include "cluster.cuh"
