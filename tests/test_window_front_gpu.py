@@ -97,3 +97,35 @@ def test_captured_and_replayed_on_new_inputs():
 def test_more_units_than_the_gpu_holds():
     q, k, v, do = _inputs(BF16, 9, 12, 4, 1000, 1000, seed=12)
     _check_all(q, k, v, do, 0.125, window=128, sinks=4, **_ragged("padded", 9, 1000, 1000))
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, BF16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("size", [(2, 4, 2, 300, 3), (3, 2, 2, 700, 129), (1, 6, 2, 65, 64), (2, 2, 1, 257, 33)], ids=_ids)
+@pytest.mark.parametrize("band", [(None, 0), (2, 1), (20, 3), (32, 32)], ids=_ids)
+def test_more_queries_than_keys(dtype, size, band):
+    # most queries are outside their sequence, before it or behind it
+    B, Hq, Hkv, Nq, Nk = size
+    q, k, v, do = _inputs(dtype, *size, seed=13)
+    for start in (0, -Nq + Nk, -Nq // 2, Nk - 1):
+        got = _check_all(q, k, v, do, 0.125, window=band[0], sinks=band[1], q_start=_int32(*[start] * B))
+        out = torch.arange(Nq, device="cuda") + start
+        out = (out < 0) | (out >= Nk)
+        assert bool((got["O"][:, :, out] == 0).all()) and bool((got["dQ"][:, :, out] == 0).all())
+        assert bool((got["LSE"][:, :, out] == -math.inf).all())
+
+
+@pytest.mark.parametrize("size", [(8, 6, 2, 640, 640), (3, 4, 4, 400, 400)], ids=_ids)
+def test_gradients_of_padding_overwrite_what_was_there(size):
+    # dQ of queries outside their sequence is cleared whatever its memory held, at its rows alone
+    B, Hq, Hkv, Nq, Nk = size
+    q, k, v, do = _inputs(BF16, *size, seed=14)
+    how = {"window": 100, "sinks": 2, "kv_len": _int32(*[max(0, Nk - 97 * b) for b in range(B)])}
+    o, lse = api.window_fwd(q, k, v, 0.125, **how)
+    wide = torch.full((B, Nq, Hq, 72), math.nan, dtype=BF16, device="cuda")
+    dq = wide[..., :64].transpose(1, 2)
+    want = api.window_bwd(q, k, v, o, lse, do, 0.125, **how)
+    got = api.window_bwd(q, k, v, o, lse, do, 0.125, **how, dQ=dq)
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
+    out = torch.arange(Nq, device="cuda") >= how["kv_len"][:, None]
+    assert bool((dq.transpose(1, 2)[out] == 0).all()) and bool(wide[..., 64:].isnan().all())
