@@ -8,7 +8,7 @@
 // gave 34 here, held up by the shared memory's bandwidth.  (The 5th-generation
 // cores' TF32 form reads its second operand along the summed index only, which
 // P V and dS K do not have, and needs every tile twice in shared memory.)
-// Measured: gradient of 4 sequences, 12 heads, 197 x 197, masked: 65 us (FP32 units:
+// Measured: gradient of 4 sequences, 12 heads, 197 x 197, masked: 64 us (FP32 units:
 // 85.5), 384 blocks of which some SMs have three and some two, the warp-wide
 // instructions 33% busy: a scheduler's three warps wait for their own chains of cuts and
 // products, for their copies, and for instructions.
@@ -37,9 +37,9 @@
 // Attention over a window with sinks (BAND): walks over the tiles that the windows meet; within a tile
 // each warp's products start and end at the columns that its 16 rows may attend, in steps of 32 and 8,
 // since at three instructions a product what is left out counts (gradient of 4 sequences, 12
-// heads, up to 197 tokens, window 65, 1 sink: 54 -> 45.2 us).  There a SM has 3 CTAs of 4 warps, the warp-wide
+// heads, up to 197 tokens, window 65, 1 sink: 54 -> 45.2 us; units worked out without divisions and shorter code, 43.5).  There a SM has 3 CTAs of 4 warps, the warp-wide
 // instructions are 17% busy, and the time goes to the waits for copies at the CTA's barriers: walks have 2 or 3 tiles.
-// 2 sequences, 16 heads on 4, 1569 tokens, window 512, 4 sinks: forward 181 us, gradient 968.
+// 2 sequences, 16 heads on 4, 1569 tokens, window 512, 4 sinks: forward 178 us, gradient 957.
 #include <algorithm>
 
 #include "cluster.cuh"
@@ -160,14 +160,16 @@ __device__ __forceinline__ void seen_columns(const Band &w, int p, int k0, int &
 }
 
 // c = A B^T: rows of A from the warp's first; columns: rows `from` to `cols` of B
-// (from the 32 before, to the next 32; 0 for the others).
+// (from the 32 before, to the next 32; 0 for the others).  TURNS of the loop laid out: 2 for the forward; the
+// gradients, whose longer code waits for its instructions, are 1 to 4% faster with 1.
+template <int TURNS>
 __device__ __forceinline__ void nt(float (&c)[8][4], const float *A, const float *B, const Lane &l, int cols, int from = 0) {
 #pragma unroll
     for (int j = 0; j < 8; ++j)
 #pragma unroll
         for (int i = 0; i < 4; ++i) c[j][i] = 0.f;
     const float *pa = A + l.row(0) * kLd + 2 * l.t, *pb = B + l.g * kLd + 2 * l.t;
-#pragma unroll 2
+#pragma unroll TURNS
     for (int k = 0; k < 64; k += 8) {
         const float2 u = *reinterpret_cast<const float2 *>(pa + k);
         const float2 v = *reinterpret_cast<const float2 *>(pa + 8 * kLd + k);
@@ -228,22 +230,28 @@ __device__ __forceinline__ void clear(float (&o)[8][4]) {
         for (int i = 0; i < 4; ++i) o[j][i] = 0.f;
 }
 
-// The part of `tiles` that CTA `r` of `c` walks over.
-__device__ __forceinline__ int part(int tiles, int r, int c) { return (int)((int64_t)tiles * r / c); }
+// The part of `tiles` that CTA `r` of `c`, a power of two, walks over.
+__device__ __forceinline__ int part(int tiles, int r, int c) { return (int)((int64_t)tiles * r >> (__ffs(c) - 1)); }
 
 template <bool BAND>
 __global__ void __launch_bounds__(kThreads, kFwdBlocks)
-cross_fwd_f32_kernel(int Hq, int Hkv, int Nq, KeySet ks, Band band, Rows<const float> Q, Rows<const float> K, Rows<const float> V,
-                     Rows<float> O, float *__restrict__ LSE, float scale_log2, int qtiles, int64_t units) {
+cross_fwd_f32_kernel(int Hq, int Nq, KeySet ks, Band band, Rows<const float> Q, Rows<const float> K, Rows<const float> V,
+                     Rows<float> O, float *__restrict__ LSE, float scale_log2, Div by_qtiles, Div by_hq, Div by_group, int units) {
     extern __shared__ float4 smem4[];
     float *sq = reinterpret_cast<float *>(smem4), *sk = sq + kTile, *sv = sk + kTile;
     __shared__ float sm[kT], sl[kT];
     const Lane ln;
     const int C = (int)cluster_size(), rank = (int)cluster_rank();
-    const int64_t unit = blockIdx.x / C;
+    const int unit = (int)(blockIdx.x >> (__ffs(C) - 1));
     if (!FIBATT_CHECKED(unit < units)) return;      // whole clusters
-    const int qt = (int)(unit % qtiles), h = (int)(unit / qtiles % Hq), b = (int)(unit / qtiles / Hq);
-    const int hk = h / (Hq / Hkv), q0 = qt * kT;
+    int qt, b, h, hk;
+    if constexpr (BAND) {      // (without a window 1% slower so, for registers)
+        const int bh = by_qtiles.of(unit);
+        qt = by_qtiles.rest(unit), b = by_hq.of(bh), h = by_hq.rest(bh), hk = by_group.of(h);
+    } else {
+        qt = unit % (int)by_qtiles.d, h = unit / (int)by_qtiles.d % Hq, b = unit / (int)by_qtiles.d / Hq, hk = h / (int)by_group.d;
+    }
+    const int q0 = qt * kT;
 
     grid_dep_wait();
     const int bound = ks.bound(b);
@@ -278,7 +286,7 @@ cross_fwd_f32_kernel(int Hq, int Hkv, int Nq, KeySet ks, Band band, Rows<const f
         int cols = min(kT, bound - k0), from = 0;
         if constexpr (BAND) seen_columns(w, p0 + q0 + 16 * ln.w, k0, from, cols);
         float s[8][4];
-        nt(s, sq, sk, ln, cols, from);
+        nt<2>(s, sq, sk, ln, cols, from);
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             float top = kNegInf;
@@ -364,13 +372,13 @@ cross_fwd_f32_kernel(int Hq, int Hkv, int Nq, KeySet ks, Band band, Rows<const f
 // (LSE log2 e, D = <dO, O>) of every query row; a row without keys gets
 // +infinity, which makes each of its weights exp2(s - inf) = 0.
 __global__ void __launch_bounds__(256)
-cross_stats_kernel(int Hq, int Nq, int64_t rows, Rows<const float> O, Rows<const float> dO, const float *__restrict__ LSE,
+cross_stats_kernel(Div by_hq, Div by_nq, int64_t rows, Rows<const float> O, Rows<const float> dO, const float *__restrict__ LSE,
                    float2 *__restrict__ stats) {
     grid_dep_wait();
     const int64_t row = (int64_t)blockIdx.x * 16 + (threadIdx.x >> 4);
     const int c = (threadIdx.x & 15) * 4;
     if (row >= rows) return;   // whole half warps: the shuffles below stay within 16 lanes
-    const int64_t n = row % Nq, h = row / Nq % Hq, b = row / Nq / Hq;
+    const int bh = by_nq.of((int)row), n = by_nq.rest((int)row), b = by_hq.of(bh), h = by_hq.rest(bh);
     const float4 o = load4(O.row(b, h, n) + c), g = load4(dO.row(b, h, n) + c);
     float d = o.x * g.x + o.y * g.y + (o.z * g.z + o.w * g.w);
     const unsigned half = 0xffffu << (threadIdx.x & 16);
@@ -421,27 +429,28 @@ __device__ __forceinline__ void finish(const float (&o)[8][4], float *parts, Row
 }
 
 struct BwdF32Args {
-    int Hq, Hkv, Nq;
+    int Hq, Nq;
     KeySet ks;
     Band band;            // BAND
     Rows<const float> Q, K, V, dO;
     const float2 *stats;
     Rows<float> dQ, dK, dV;
     float scale;
-    int qtiles, ktiles;
+    int qtiles;
+    Div by_qtiles, by_ktiles, by_hq, by_hkv, by_group;
     int key_units;        // units that hold keys; the others hold queries
-    int64_t units;        // all of them
+    int units;            // all of them
     int first;            // unit of the launch
 };
 
 // Holds 64 queries and walks over the keys.
 template <bool BAND>
-__device__ __forceinline__ void hold_queries(const BwdF32Args &a, float *smem, int64_t unit) {
+__device__ __forceinline__ void hold_queries(const BwdF32Args &a, float *smem, int unit) {
     float *sq = smem, *sg = sq + kTile, *sk = sg + kTile, *sv = sk + kTile;
     const Lane ln;
     const int C = (int)cluster_size(), rank = (int)cluster_rank();
-    const int qt = (int)(unit % a.qtiles), h = (int)(unit / a.qtiles % a.Hq), b = (int)(unit / a.qtiles / a.Hq);
-    const int hk = h / (a.Hq / a.Hkv), q0 = qt * kT;
+    const int bh = a.by_qtiles.of(unit), qt = a.by_qtiles.rest(unit), b = a.by_hq.of(bh), h = a.by_hq.rest(bh);
+    const int hk = a.by_group.of(h), q0 = qt * kT;
     const float scale_log2 = a.scale * kLog2e;
     const int bound = a.ks.bound(b);
     int tiles = (bound + kT - 1) / kT, p[2] = {-1, -1}, p0 = 0, first = 0, last = 0;   // positions: of the lane's rows, of query 0, of the tile's
@@ -482,8 +491,8 @@ __device__ __forceinline__ void hold_queries(const BwdF32Args &a, float *smem, i
         int cols = min(kT, bound - k0), from = 0;
         if constexpr (BAND) seen_columns(w, p0 + q0 + 16 * ln.w, k0, from, cols);
         float s[8][4], dp[8][4];
-        nt(s, sq, sk, ln, cols, from);
-        nt(dp, sg, sv, ln, cols, from);
+        nt<1>(s, sq, sk, ln, cols, from);
+        nt<1>(dp, sg, sv, ln, cols, from);
 #pragma unroll
         for (int j = 0; j < 8; ++j)
 #pragma unroll
@@ -500,12 +509,12 @@ __device__ __forceinline__ void hold_queries(const BwdF32Args &a, float *smem, i
 
 // Holds 64 keys and walks over the queries of every head that shares them.
 template <bool BAND>
-__device__ __forceinline__ void hold_keys(const BwdF32Args &a, float *smem, float2 *sst, int64_t unit) {
+__device__ __forceinline__ void hold_keys(const BwdF32Args &a, float *smem, float2 *sst, int unit) {
     float *sk = smem, *sv = sk + kTile, *sq = sv + kTile, *sg = sq + kTile;
     const Lane ln;
     const int C = (int)cluster_size(), rank = (int)cluster_rank();
-    const int kt = (int)(unit % a.ktiles), hk = (int)(unit / a.ktiles % a.Hkv), b = (int)(unit / a.ktiles / a.Hkv);
-    const int G = a.Hq / a.Hkv, k0 = kt * kT;
+    const int bh = a.by_ktiles.of(unit), kt = a.by_ktiles.rest(unit), b = a.by_hkv.of(bh), hk = a.by_hkv.rest(bh);
+    const int G = (int)a.by_group.d, k0 = kt * kT;
     const float scale_log2 = a.scale * kLog2e;
     const int bound = a.ks.bound(b);
     uint64_t ok;
@@ -524,16 +533,16 @@ __device__ __forceinline__ void hold_keys(const BwdF32Args &a, float *smem, floa
     }
     const bool mine = 16 * ln.w < bound - k0;    // the warp's 16 rows begin within the keys
     // the walk: the query tiles of each of the G heads in turn; none for a tile without keys
-    const int64_t tiles = ok ? (int64_t)G * qtiles : 0;
-    const int64_t lo = tiles * rank / C, hi = tiles * (rank + 1) / C;
+    const int tiles = ok ? G * qtiles : 0, lo = part(tiles, rank, C), hi = part(tiles, rank + 1, C);
     stage(sk, a.K.row(b, hk, 0), a.K.sn, k0, ok);
     stage(sv, a.V.row(b, hk, 0), a.V.sn, k0, ok);
     float ak[8][4], av[8][4];
     clear(ak);
     clear(av);
     const bool in[2] = {((ok >> ln.row(0)) & 1) != 0, ((ok >> ln.row(1)) & 1) != 0};
-    for (int64_t t = lo; t < hi; ++t) {
-        const int h = hk * G + (int)(t / qtiles), q0 = (from + (int)(t % qtiles)) * kT;
+    for (int t = lo, g = lo < hi ? lo / qtiles : 0, at = lo - g * qtiles; t < hi; ++t) {
+        const int h = hk * G + g, q0 = (from + at) * kT;
+        if (++at == qtiles) at = 0, ++g;
         uint64_t rows = first_bits(a.Nq - q0);
         if constexpr (BAND) rows &= first_bits(bound - p0 - q0) & ~first_bits(-p0 - q0);    // queries of the sequence
         __syncthreads();
@@ -553,8 +562,8 @@ __device__ __forceinline__ void hold_keys(const BwdF32Args &a, float *smem, floa
             if (k >= a.band.sinks) cols = min(cols, k + 15 + a.band.window - p0 - q0);
         }
         float p[8][4], ds[8][4];
-        nt(p, sk, sq, ln, cols, since);
-        nt(ds, sv, sg, ln, cols, since);
+        nt<1>(p, sk, sq, ln, cols, since);
+        nt<1>(ds, sv, sg, ln, cols, since);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
             const float4 st = *reinterpret_cast<const float4 *>(sst + ln.col(j, 0));     // of both columns
@@ -581,7 +590,7 @@ __global__ void __launch_bounds__(kThreads, kBwdBlocks) cross_bwd_f32_kernel(con
     __shared__ __align__(16) float2 sst[kT];
     float *smem = reinterpret_cast<float *>(smem4);
     grid_dep_wait();
-    const int64_t unit = a.first + blockIdx.x / cluster_size();
+    const int unit = a.first + (int)(blockIdx.x >> (__ffs(cluster_size()) - 1));
     if (!FIBATT_CHECKED(unit < a.units)) return;    // whole clusters
     if (unit < a.key_units) hold_keys<BAND>(a, smem, sst, unit);
     else hold_queries<BAND>(a, smem, unit - a.key_units);
@@ -610,9 +619,10 @@ cudaError_t fwd(const CrossArgs &a) {
     const int64_t units = (int64_t)a.B * a.Hq * qtiles;
     // (one head, 100 queries on 16385 keys: clusters of 16 85 us, of 8 161)
     const int c = cluster_for(units, key_tiles<BAND>(a), kFwdBlocks * sm_count(), largest_cluster<cross_fwd_f32_kernel<BAND>>(smem));
-    return launch_clusters(cross_fwd_f32_kernel<BAND>, (unsigned)(units * c), c, kThreads, smem, a.stream, a.Hq, a.Hkv, a.Nq,
+    return launch_clusters(cross_fwd_f32_kernel<BAND>, (unsigned)(units * c), c, kThreads, smem, a.stream, a.Hq, a.Nq,
                            a.keys, a.band, rows_of<const float>(a.Q), rows_of<const float>(a.K), rows_of<const float>(a.V),
-                           rows_of<float>(a.O), a.LSE, a.scale * kLog2e, qtiles, units);
+                           rows_of<float>(a.O), a.LSE, a.scale * kLog2e, Div((uint32_t)qtiles), Div((uint32_t)a.Hq),
+                           Div((uint32_t)(a.Hq / a.Hkv)), (int)units);
 }
 
 template <bool BAND>
@@ -621,7 +631,7 @@ cudaError_t bwd(const CrossArgs &a) {
     cudaError_t e = prepare_kernel<cross_bwd_f32_kernel<BAND>>(smem, 0);
     if (e != cudaSuccess) return e;
     BwdF32Args f;
-    f.Hq = a.Hq, f.Hkv = a.Hkv, f.Nq = a.Nq;
+    f.Hq = a.Hq, f.Nq = a.Nq;
     f.ks = a.keys;
     f.band = a.band;
     f.Q = rows_of<const float>(a.Q), f.K = rows_of<const float>(a.K), f.V = rows_of<const float>(a.V);
@@ -629,16 +639,19 @@ cudaError_t bwd(const CrossArgs &a) {
     f.stats = a.stats;
     f.dQ = rows_of<float>(a.dQ), f.dK = rows_of<float>(a.dK), f.dV = rows_of<float>(a.dV);
     f.scale = a.scale;
-    f.qtiles = (a.Nq + kT - 1) / kT, f.ktiles = (a.Nk + kT - 1) / kT;
+    const int ktiles = (a.Nk + kT - 1) / kT;
+    f.qtiles = (a.Nq + kT - 1) / kT;
+    f.by_qtiles = Div((uint32_t)f.qtiles), f.by_ktiles = Div((uint32_t)ktiles), f.by_hq = Div((uint32_t)a.Hq);
+    f.by_hkv = Div((uint32_t)a.Hkv), f.by_group = Div((uint32_t)(a.Hq / a.Hkv));
     const int64_t rows = (int64_t)a.B * a.Hq * a.Nq;
-    e = launch_clusters(cross_stats_kernel, (unsigned)((rows + 15) / 16), 1, 256, 0, a.stream, a.Hq, a.Nq, rows,
+    e = launch_clusters(cross_stats_kernel, (unsigned)((rows + 15) / 16), 1, 256, 0, a.stream, f.by_hq, Div((uint32_t)a.Nq), rows,
                         rows_of<const float>(a.O), f.dO, static_cast<const float *>(a.LSE), a.stats);
     if (e != cudaSuccess) return e;
-    const int64_t key_units = (int64_t)a.B * a.Hkv * f.ktiles, query_units = (int64_t)a.B * a.Hq * f.qtiles;
+    const int64_t key_units = (int64_t)a.B * a.Hkv * ktiles, query_units = (int64_t)a.B * a.Hq * f.qtiles;
     f.key_units = (int)key_units;
-    f.units = key_units + query_units;
+    f.units = (int)(key_units + query_units);
     f.first = 0;
-    // (one head, 100 queries on 16385 keys: 157 us in two launches, 275 with clusters of 8
+    // (one head, 100 queries on 16385 keys: 147 us in two launches, 275 with clusters of 8
     // at most, 1937 in one)
     int64_t key_walk = f.qtiles;
     if (BAND && a.band.sinks == 0) key_walk = std::min<int64_t>(key_walk, ((int64_t)a.band.window + kT) / kT + 1);
