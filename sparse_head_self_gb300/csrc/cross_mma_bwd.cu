@@ -612,9 +612,9 @@ __device__ __forceinline__ int weights(const BwdMmaArgs<BAND> &a, Shared<BAND> &
 #pragma unroll
             for (int i = 0; i < 8; ++i)
                 __stcg(mine + i * 32 * kWeightWarps,
-                       u.n > 0 ? make_float4(__uint_as_float(o[4 * i]), __uint_as_float(o[4 * i + 1]),
-                                             __uint_as_float(o[4 * i + 2]), __uint_as_float(o[4 * i + 3]))
-                               : make_float4(0.f, 0.f, 0.f, 0.f));
+                       zero ? make_float4(0.f, 0.f, 0.f, 0.f)
+                            : make_float4(__uint_as_float(o[4 * i]), __uint_as_float(o[4 * i + 1]),
+                                          __uint_as_float(o[4 * i + 2]), __uint_as_float(o[4 * i + 3])));
             return it;
         }
         if (u.leaves >= 0) {
