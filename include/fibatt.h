@@ -353,7 +353,9 @@ fibatt_status fibatt_cross_bwd(const fibatt_cross *d, const fibatt_heads *Q, con
  * keys and values that no query of its sequence attends, and in queries and rows of dO that
  * attend nothing (NaN, infinities), reaches no result.  A key or value that
  * is not finite and is attended reaches the queries that attend it, and may reach
- * those within 255 rows of them. */
+ * those within 255 rows of them; a query or a row of dO that is not finite
+ * reaches the gradients of the keys that it attends, and may reach those of attended keys
+ * within 255 of them. */
 typedef struct {
     int B, Hq, Hkv;              /* >= 1; Hkv divides Hq                             */
     int Nq, Nk;                  /* >= 1, below 2^30; Nq <= Nk when q_start is NULL   */

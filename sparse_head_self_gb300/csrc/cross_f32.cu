@@ -579,6 +579,13 @@ __device__ __forceinline__ void hold_keys(const BwdF32Args &a, float *smem, floa
         nn(av, p, sg, ln, cols, since);
         nn(ak, ds, sq, ln, cols, since);
     }
+    // keys that are not attended have no gradient, whatever the rows that others' weights are for hold (0 times a NaN)
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        if (in[i]) continue;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) ak[j][2 * i] = ak[j][2 * i + 1] = av[j][2 * i] = av[j][2 * i + 1] = 0.f;
+    }
     finish(av, sg, a.dV, b, hk, k0, a.ks.Nk, 1.f, ln);
     finish(ak, sq, a.dK, b, hk, k0, a.ks.Nk, a.scale, ln);
 }

@@ -13,8 +13,8 @@ from sparse_head_self_gb300 import api
 
 pytestmark = pytest.mark.gpu
 
-BF16 = torch.bfloat16
-TYPES = pytest.mark.parametrize("dtype", [BF16], ids=["bf16"])
+BF16, F32 = torch.bfloat16, torch.float32
+TYPES = pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
 
 
 def _ids(s):
