@@ -213,7 +213,10 @@ class WindowSelfAttention(nn.Module):
         """The next N tokens x [B, N, dim] of sequences that have start[b] tokens in
         `cache` (int32 [B]; the table [B, pages] has pages for the new ones too), into
         which theirs go.  count [B] int32: how many of the N each sequence has.
-        Without gradients; start is the caller's to move on."""
+        Without gradients; start is the caller's to move on.  Pages of tokens that the window has left behind, and
+        that are no sinks', may be given back.  Many tokens at once on a layer without a window take
+        scratch memory for the keys and values of as many tokens as the table has places for; with one, for
+        those of the window, the sinks and the new tokens."""
         N = x.shape[1]
         places = start[:, None] + torch.arange(N, dtype=torch.int32, device=x.device)
         held = start + (N if count is None else count.clamp(0, N))
@@ -223,8 +226,28 @@ class WindowSelfAttention(nn.Module):
         cache_store(cache, table, k, v, start, count)
         if self.heads // self.kv_heads * N <= self.FEW_ROWS:
             return self._join(cache_fwd(q, cache, table, start, self.scale, self.window, self.sinks, count)[0])
-        k, v = cache_load(cache, table, table.shape[1] * PAGE, None, held, dtype=q.dtype)
-        return self._join(window_fwd(q, k, v, self.scale, self.window, self.sinks, start, held)[0])
+        return self._join(self._attend_loaded(q, cache, table, start, held))
+
+    def _attend_loaded(self, q, cache, table, start, held):
+        """Attention of the queries from place start[b] on to the cache's tokens, up to held[b], as 16
+        or 32 bits.  With a window the tokens that are attended alone: those of the sinks, and behind
+        them those from the oldest key that the first query's window reaches on, so that the queries' places in
+        what is loaded are their own less what lies between.  Entries of the table that no query needs
+        are not looked at, and what is loaded does not grow with the table."""
+        B, _, N, _ = q.shape
+        places = table.shape[1] * PAGE
+        held = torch.where(held > start, held.clamp(max=places), 0)       # (a sequence without tokens needs no pages)
+        if self.window is None or self.sinks >= places:
+            k, v = cache_load(cache, table, places, None, held, dtype=q.dtype)
+            return window_fwd(q, k, v, self.scale, self.window, self.sinks, start, held)[0]
+        S, last = self.sinks, min(self.window + N - 1, places - self.sinks)
+        oldest = (start.clamp(min=-N) - (self.window - 1)).clamp(min=S)
+        k, v = (q.new_empty(B, self.kv_heads, S + last, HEAD_DIM) for _ in range(2))
+        if S:
+            cache_load(cache, table, S, None, held, K=k[:, :, :S], V=v[:, :, :S])
+        n = held - oldest
+        cache_load(cache, table, last, oldest, n, K=k[:, :, S:], V=v[:, :, S:])
+        return window_fwd(q, k, v, self.scale, self.window, S, start - oldest + S, n + S)[0]
 
 
 __all__ = ["FibottentionSelfAttention", "CrossAttention", "WindowSelfAttention"]
