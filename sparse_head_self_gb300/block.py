@@ -163,11 +163,6 @@ class WindowSelfAttention(nn.Module):
     tokens' places (None: not rotated).  forward() is for whole sequences, in
     training; step() decodes on a paged 8-bit cache (api.Cache)."""
 
-    # Up to so many query rows of a key head are attended page by page; more take the cache's
-    # tokens as 16 or 32 bits first.  (8 sequences, 16 heads on 4, 128 rows: of 1569 tokens 14.8 us
-    # and 22.2, of 16385 89 and 105, window 1024 12.5 and 65; 256 rows: 27.5 and 25, 174 and 140, 23 and 69.)
-    FEW_ROWS = 128
-
     def __init__(self, dim: int, heads: int, kv_heads: int | None = None, window: int | None = None, sinks: int = 0,
                  bias: bool = True, norm: bool = False, rotary: torch.Tensor | None = None, eps: float = 1e-6):
         super().__init__()
@@ -224,9 +219,29 @@ class WindowSelfAttention(nn.Module):
             places = torch.minimum(places, held[:, None] - 1)
         q, k, v = self._split(x, places)
         cache_store(cache, table, k, v, start, count)
-        if self.heads // self.kv_heads * N <= self.FEW_ROWS:
+        if self._page_by_page(x.shape[0], N, table.shape[1] * PAGE, q.dtype):
             return self._join(cache_fwd(q, cache, table, start, self.scale, self.window, self.sinks, count)[0])
         return self._join(self._attend_loaded(q, cache, table, start, held))
+
+    def _page_by_page(self, B, N, places, dtype):
+        """Whether the queries of N tokens attend the cache's pages as they are, 16 rows of a key head at a
+        time (_attend_loaded's way otherwise).
+
+        In 32 bits always: the products of the loaded tokens cost more than the pages read again (8 sequences,
+        16 heads on 4, 1024 rows, 16448 places: window 1024 126 us and 245, none 799 and 2858; at worst, 32
+        sequences, window 128: 259 and 201).  In 16 bits where an estimate says so, in ns: a block of 16
+        rows costs 15, and 1.1 a page that it reads; loading 20000, and 0.16 a token and head; without a
+        window all of the table's places are taken to be held.  (us, pages and loaded, 16
+        heads on 4; 1 sequence, 16448 places, no window, 512 rows 28.7 and 34.2, 1024 rows 49.5 and 35.3;
+        8 sequences, window 128, 256 rows 13.0 and 21.2, 512 rows 22.4 and 22.1; window 1024 22.5 and 30.7, 38.9
+        and 31.9; no window, 128 rows 75.5 and 89.5, 256 rows 139 and 119; 32 sequences, window 1024, 128 rows 38.7
+        and 39.6, 256 rows 73.5 and 44.8.)"""
+        if dtype == torch.float32:
+            return True
+        heads, rows = B * self.kv_heads, self.heads // self.kv_heads * N
+        seen = places if self.window is None else min(places, self.window + self.sinks)
+        loaded = places if self.window is None else min(places, self.window + self.sinks + N)
+        return heads * ((rows + 15) // 16) * (15 + 1.1 * seen / PAGE) <= 20000 + 0.16 * heads * loaded
 
     def _attend_loaded(self, q, cache, table, start, held):
         """Attention of the queries from place start[b] on to the cache's tokens, up to held[b], as 16
