@@ -333,7 +333,7 @@ cache_fwd_kernel(const __grid_constant__ AttendArgs a, Rows<const T> Q, Rows<T> 
     const int start = a.c.first(b), n = a.c.tokens(b), end = a.c.table_len * kPage;
     // positions of the block's first and last queries that attend keys
     const int first = max(0, start + token(0)), last = min(end, start + min(n, token(rows - 1) + 1)) - 1;
-    if (start + n > end && threadIdx.x == 0) atomicOr(&g_device_error, kErrPage);
+    if (n > 0 && (start < 0 || start + n > end) && threadIdx.x == 0) atomicOr(&g_device_error, kErrPage);
     const BandWalk<kPage> walk(a.band, first, last);
     const int at = (int)rank * kPairs + pair, step = (int)C * kPairs, mine = max(0, (walk.n - at + step - 1) / step);
     const auto position = [&](int r) {
