@@ -404,7 +404,8 @@ fibatt_status fibatt_window_bwd(const fibatt_window *d, const fibatt_heads *Q, c
  * into it.  Table entries that no token of a call needs may hold anything.
  * A token whose position is outside the table, or whose entry there is not a
  * page of the cache, is not stored, loads as zeros, is attended by nobody and
- * (as a query) attends nothing, and sets bit 4 of the device error word. */
+ * sets bit 4 of the device error word.  As a query one outside the table attends
+ * nothing; one inside it attends the keys of the pages that are there. */
 typedef struct {
     int B, Hkv, N;               /* >= 1; N below 2^30                               */
     int D;                       /* head dim, FIBATT_HEAD_DIM                        */
