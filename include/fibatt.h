@@ -423,7 +423,8 @@ typedef struct {
 /* Stores tokens: K, V Hkv heads of N rows.  A page's scale is the smallest power of two
  * whose 448th multiple reaches the largest finite value stored in that piece of
  * it, and a value becomes the nearest e4m3 multiple of it (ties to
- * even; infinities the largest, NaN stays NaN).  A call that begins a page sets its
+ * even; infinities the largest, NaN stays NaN; at the scale of 2^120 finite values to 240 of
+ * it at most, the largest multiple that bf16 and fp32 hold).  A call that begins a page sets its
  * scale anew; one that continues it (a first position that is not a multiple
  * of 64) raises the scale where its tokens need that, and rounds the page's older
  * tokens again, which changes only values below 2^-6 of the new scale; the
@@ -435,7 +436,7 @@ fibatt_status fibatt_cache_store(const fibatt_cache *d, const fibatt_heads *K, c
                                  cudaStream_t stream);
 
 /* Loads tokens into K, V: the values that the bytes stand for (exact in bf16
- * and fp32), zeros from count[b] on.  Errors as above. */
+ * and fp32; infinite at 2^128 and beyond, which finite values are not stored as), zeros from count[b] on.  Errors as above. */
 fibatt_status fibatt_cache_load(const fibatt_cache *d, const fibatt_heads *K, const fibatt_heads *V,
                                 cudaStream_t stream);
 
@@ -448,7 +449,8 @@ fibatt_status fibatt_cache_load(const fibatt_cache *d, const fibatt_heads *K, co
  * fibatt_window_fwd's, on fibatt_cache_load's keys where the cache holds earlier ones.
  * Arithmetic: products of halves with fp32 sums (queries exact in bf16, 22 bits in fp32,
  * relative to their row's largest; weights 11 bits in bf16 I/O, 22 in fp32), O rounded
- * once.  What the pages hold behind the last token, or in
+ * once; weights are held times up to 2^15, so that of n attended keys values above 2^112 / n may
+ * give infinities.  What the pages hold behind the last token, or in
  * keys that no query attends, reaches no result (one that is not finite and is
  * attended may reach the other queries of its block of 16 rows).  Errors as above, and
  * INVALID_ARG for Hq, scale, window, sinks out of their range. */

@@ -46,7 +46,10 @@ __device__ __forceinline__ int scale_exponent(float x) {
     return max(e, -100);
 }
 // A page's scale as the store wrote it: a power of two.  (Whatever else stands there is read as one.)
-__device__ __forceinline__ int stored_exponent(float s) { return max(-100, min(exponent_of(s), 120)); }
+constexpr int kLargestScale = 120;
+__device__ __forceinline__ int stored_exponent(float s) { return max(-100, min(exponent_of(s), kLargestScale)); }
+// The largest multiple of the largest scale that 16 and 32 bits hold.
+constexpr float kLargestValue = 0x1.ep127f;
 
 // ---- storing and loading -----------------------------------------------------------
 constexpr int kStoreThreads = 128;       // two a token, 32 dims each
@@ -129,6 +132,11 @@ __global__ void __launch_bounds__(kStoreThreads) cache_store_kernel(const __grid
     if (threadIdx.x == 0 && (s.lo == 0 || raised)) *scale = two_to(e);
     uint8_t *page = a.data + (a.place(s.page, s.hk) * 2 + s.kind) * kPageBytes;
     uint32_t y[8];
+    if (mine && e == kLargestScale) {     // finite values come back as such
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+            if (fabsf(x[i]) < __builtin_inff()) x[i] = fmaxf(-kLargestValue, fminf(x[i], kLargestValue));
+    }
     if (mine) {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
