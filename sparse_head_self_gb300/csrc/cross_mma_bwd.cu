@@ -78,8 +78,22 @@ static_assert(4 * kRegsMany + kRegsFew == 5 * kRegs, "the shares add up");
 // columns of tensor memory
 constexpr uint32_t kColS = 0, kColDp = 128, kColP = 256, kColDs = 320, kColAcc0 = 384, kColAcc1 = 448, kCols = 512;
 
+// What only a window's calls have.  (Other launches do not carry it.)
 template <bool BAND>
-struct BwdMmaArgs {
+struct BwdBandArgs {};
+template <>
+struct BwdBandArgs<true> {
+    Band band;
+    Div by_heads, by_hkv, by_sinks;     // heads of keys of all sequences, of one, and the sinks' tiles of all
+    int chunks, chunk_tiles;    // parts of a sinks' walk and the query tiles of each, ...
+    int sink_tiles, sink_units; // ... key tiles that have such walks, units of those parts
+    float4 *parts;              // their partial sums, one after another
+    int cleared;                // dQ of queries outside their sequence is, and units of such alone are left out
+    TensorArg dq, dk, dv;       // the gradients as tensor copies write them (dQ: tiles of 128 queries)
+};
+
+template <bool BAND>
+struct BwdMmaArgs : BwdBandArgs<BAND> {
     TensorArg q, g, k, v;       // boxes of query tiles (Q, dO) and of key tiles (K, V)
     TilesOf<BAND> qt;
     KeySet ks;
@@ -89,17 +103,10 @@ struct BwdMmaArgs {
     Rows<__nv_bfloat16> dQ, dK, dV;
     int B, Hq, Hkv, ktiles;
     int first_kind, units;      // units of the kind that comes first (queries held; BAND: keys held), and all of them
-    int chunks, chunk_tiles;    // BAND: parts of a sinks' walk and the query tiles of each, ...
-    int sink_tiles, sink_units; // ... key tiles that have such walks, units of those parts
-    float4 *parts;              // their partial sums, one after another
-    int cleared;                // BAND: dQ of queries outside their sequence is, and units of such alone are left out
     int first_unit;             // of the launch, which has those up to `units`
     int *next_unit;             // units given out behind every CTA's first
     float scale;
     float c;                    // scale log2 e, not 0
-    Band band;                  // BAND
-    Div by_heads, by_hkv, by_sinks;     // BAND: heads of keys of all sequences, of one, and the sinks' tiles of all
-    TensorArg dq, dk, dv;       // BAND: the gradients as tensor copies write them (dQ: tiles of 128 queries)
     BwdMmaArgs() : qt(1, 1, false) {}
 };
 
@@ -989,6 +996,11 @@ __global__ void __launch_bounds__(kThreads, 1) cross_bwd_mma_kernel(const __grid
         if (warp == kCopyWarp) {
             bool ok = true;
             int drawn = first;
+            // BAND: a unit of queries outside their sequence alone, whose dQ is cleared already
+            const auto outside = [&](const Unit<BAND> &u) {
+                if constexpr (BAND) return a.cleared && CS == 1 && u.n == 0 && u.index >= a.first_kind && u.index < a.units;
+                else return false;
+            };
             const auto pass = [&] {      // (its copies being out, the next unit's number has come meanwhile)
                 const int i = passed & 1;
                 Unit<BAND> u;
@@ -996,7 +1008,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross_bwd_mma_kernel(const __grid
                     u.enter(a, __shfl_sync(kFullMask, drawn, 0));
                     drawn = a.units;
                     if (CS == 1 && lane == 0 && u.index < a.units) drawn = a.first_unit + (int)gridDim.x + atomicAdd(a.next_unit, 1);
-                } while (BAND && a.cleared && CS == 1 && u.n == 0 && u.index >= a.first_kind && u.index < a.units);
+                } while (outside(u));
                 ok = ok && (passed < 2 || pipe_wait(&sh.unit_empty[i], ((passed >> 1) - 1) & 1, &sh.abort));
                 if constexpr (BAND) {      // (the unit before last is over by now, or nearly)
                     ok = ok && (passed < 2 || pipe_wait(&sh.out[i], ((passed >> 1) - 1) & 1, &sh.abort));
@@ -1142,7 +1154,6 @@ cudaError_t bwd(const CrossArgs &a) {
         !make_tensor(&f.v, a.V, a.B, a.Hkv, a.Nk, kTileRows, 1))
         return cudaErrorInvalidValue;
     f.ks = a.keys;
-    f.band = a.band;
     f.npad = padded_rows(a.Nq);
     const int64_t rows = (int64_t)a.B * a.Hq * f.npad;
     uint4 *lse_parts = reinterpret_cast<uint4 *>(a.stats), *d_parts = lse_parts + rows + kTileRows;
@@ -1150,9 +1161,10 @@ cudaError_t bwd(const CrossArgs &a) {
     f.stats = stats;
     f.next_unit = reinterpret_cast<int *>(stats + (int64_t)a.B * a.Hq * a.Nq);
     f.lse_parts = lse_parts, f.d_parts = d_parts;
-    f.chunks = 1, f.chunk_tiles = f.sink_tiles = f.sink_units = f.cleared = 0;
-    f.parts = nullptr;
     if constexpr (BAND) {
+        f.band = a.band;
+        f.chunks = 1, f.chunk_tiles = f.sink_tiles = f.sink_units = f.cleared = 0;
+        f.parts = nullptr;
         if ((f.qt.nb == kTileRows && !make_tensor(&f.dq, a.dQ, a.B, a.Hq, a.Nq, kTileRows, 1)) ||
             !make_tensor(&f.dk, a.dK, a.B, a.Hkv, a.Nk, kTileRows, 1) || !make_tensor(&f.dv, a.dV, a.B, a.Hkv, a.Nk, kTileRows, 1))
             return cudaErrorInvalidValue;
@@ -1189,7 +1201,7 @@ cudaError_t bwd(const CrossArgs &a) {
                             f.npad, heads, a.keys, a.band, rows_of<const __nv_bfloat16>(a.O),
                             rows_of<const __nv_bfloat16>(a.dO), static_cast<const float *>(a.LSE), f.c, stats, lse_parts,
                             d_parts, f.next_unit, f.dQ);
-        f.cleared = 1;
+        if constexpr (BAND) f.cleared = 1;
     } else {
         const auto kernel = !BAND && a.keys.len ? cross_parts_kernel<true> : cross_parts_kernel<false>;
         e = launch_clusters(kernel, (unsigned)((rows + kTileRows + 31) / 32), 1, 256, 0, a.stream, a.Hq, a.Hkv, a.Nq, f.npad,
@@ -1200,7 +1212,8 @@ cudaError_t bwd(const CrossArgs &a) {
     }
     if (e != cudaSuccess) return e;
     const int64_t query_units = (int64_t)a.B * a.Hkv * f.qt.tiles;
-    const int64_t key_units = (int64_t)a.B * a.Hkv * (f.ktiles - f.sink_tiles) + f.sink_units;
+    int64_t key_units = (int64_t)a.B * a.Hkv * f.ktiles;
+    if constexpr (BAND) key_units += f.sink_units - (int64_t)a.B * a.Hkv * f.sink_tiles;
     f.first_kind = (int)(BAND ? key_units : query_units);
     // clusters, one unit each, while they all find a place; else one wave of CTAs that walk over the units
     const auto launch = [&](int64_t from, int64_t units, int c) {

@@ -85,8 +85,22 @@ struct Cfg {
     static_assert(NT * kTileRows * kJoinLd * 4 <= NT * kTileBytes + kStages * 2 * kTileBytes, "partial O fits");
 };
 
+// What only a window's calls have.  (Other launches do not carry it: the tensor maps alone are 0.6 KB.)
 template <bool BAND>
-struct FwdMmaArgs {
+struct FwdBandArgs {};
+template <>
+struct FwdBandArgs<true> {
+    Band band;
+    Div by_heads, by_hkv;    // heads of keys of all sequences, of one
+    TensorArg o;             // tiles of one head: O as tensor copies write it
+    // few sinks lie in front of the windows' first tile, in `front` rows of it (0: in tiles of their
+    // own); boxes of those and of the other rows
+    int front;
+    TensorArg kv_front[2], kv_rest[2];
+};
+
+template <bool BAND>
+struct FwdMmaArgs : FwdBandArgs<BAND> {
     TensorArg q, k, v;
     TilesOf<BAND> qt;
     KeySet ks;
@@ -97,13 +111,6 @@ struct FwdMmaArgs {
     int units;               // of all heads and sequences
     float c;                 // |scale| log2 e (> 0)
     int negative;            // scale < 0
-    Band band;               // BAND
-    Div by_heads, by_hkv;    // BAND: heads of keys of all sequences, of one
-    TensorArg o;             // BAND, tiles of one head: O as tensor copies write it
-    // BAND: few sinks lie in front of the windows' first tile, in `front` rows of it (0: in tiles of their
-    // own); boxes of those and of the other rows
-    int front;
-    TensorArg kv_front[2], kv_rest[2];
     FwdMmaArgs() : qt(1, 1, false) {}
 };
 
@@ -802,9 +809,10 @@ cudaError_t fwd(const CrossArgs &a, const TilesOf<BAND> &qt, int c) {
     if (!make_tensor(&f.q, a.Q, a.B, a.Hq, a.Nq, qt.nb, qt.gb) || !make_tensor(&f.k, a.K, a.B, a.Hkv, a.Nk, kTileRows, 1) ||
         !make_tensor(&f.v, a.V, a.B, a.Hkv, a.Nk, kTileRows, 1))
         return cudaErrorInvalidValue;
-    f.by_heads = Div((uint32_t)(a.B * a.Hkv)), f.by_hkv = Div((uint32_t)a.Hkv);
-    f.front = FRONT ? kTileRows - qt.nb : 0;
     if constexpr (BAND) {
+        f.band = a.band;
+        f.by_heads = Div((uint32_t)(a.B * a.Hkv)), f.by_hkv = Div((uint32_t)a.Hkv);
+        f.front = FRONT ? kTileRows - qt.nb : 0;
         if (qt.gb == 1 && !make_tensor(&f.o, a.O, a.B, a.Hq, a.Nq, qt.nb, 1)) return cudaErrorInvalidValue;
         const fibatt_heads *kv[2] = {&a.K, &a.V};
         for (int i = 0; f.front && i < 2; ++i)
@@ -813,7 +821,6 @@ cudaError_t fwd(const CrossArgs &a, const TilesOf<BAND> &qt, int c) {
                 return cudaErrorInvalidValue;
     }
     f.ks = a.keys;
-    f.band = a.band;
     f.O = rows_of<__nv_bfloat16>(a.O);
     f.LSE = a.LSE;
     f.Hq = a.Hq, f.Hkv = a.Hkv;
