@@ -668,15 +668,17 @@ cudaError_t bwd(const CrossArgs &a) {
         int c = l.c;
         if constexpr (BAND) {
             // Walks differ (a tile with sinks meets every later query): cut over more CTAs than find a place
-            // at once, while that ends the longest before all of them, in tiles, with a quarter for a CTA.
-            // (4 sequences, 12 heads, 197 tokens, window 65, 1 sink: clusters of two 54 us, of one 63,
-            // of four 74; 8 sequences, 12 heads on 4, 600 tokens, window 128, 4 sinks: 358, 502, 331.)
+            // at once, while that ends the longest before all of them, in tiles, with 1.3 for a CTA (its held
+            // rows, the join).  (us with clusters of 1, 2, 4, 8, - the one taken -: 4 sequences, 12 heads, 197 tokens,
+            // window 65, 1 sink 51, -41-, 55, 112; 4, 4 heads, 246, all keys 53, 35, -30-, 59; 8, 16 heads on 8, 495, window
+            // 53 -142-, 161, 261, 554; 8, 12 heads on 4, 600, window 128, 4 sinks 461, -329-, 309, 523.  Over 25 forms 4.5% off
+            // the best in the mean; with a quarter for a CTA 21%.)
             const int64_t group = a.Hq / a.Hkv, query_walk = key_tiles<BAND>(a),
                           others = group * std::min<int64_t>(f.qtiles, ((int64_t)a.band.window + kT) / kT + 1),
                           longest = std::max(query_walk, a.band.sinks ? group * f.qtiles : others),
                           all = (query_units * query_walk + key_units * others) * 3 / 4;
             const auto time = [&](int n) {
-                return std::max<double>((double)longest / n + 1, (all + 0.25 * (double)(query_units + key_units) * n) / (kBwdBlocks * sm_count()));
+                return std::max<double>((double)longest / n + 1, (all + 1.3 * (double)(query_units + key_units) * n) / (kBwdBlocks * sm_count()));
             };
             while (c < 8 && time(2 * c) < time(c)) c *= 2;
         }
