@@ -93,9 +93,9 @@ __device__ __forceinline__ uint32_t rescale4(uint32_t w, float f) {
 // has it raised and those tokens rounded again.  One block for each page, head and kind, since the
 // scale is of them all: it reads its tokens once, holds them in registers, finds the largest,
 // and writes the bytes; values go through shared memory, to leave dim by dim in pieces of 16 tokens.
-// Bound by bytes where there are many tokens, by a chain of reads (start, table, scale) where there are few:
-// 2 x 16385 tokens of 4 heads 12.8 us (3.9 TB/s), 8 x 1569 7.1 (1664 blocks, one after another on 9 places a SM;
-// 42% of issue slots), 64 x 1 4.1.  fp32: 21.3 us (4.0 TB/s), 10.6, 4.0.
+// Far from the bytes' time: a block has a chain of reads (start, table, scale), then one round of loads in flight, and
+// nothing of another page asked for meanwhile.  2 x 16385 tokens of 4 heads 15.1 us (3.3 TB/s, half of a copy's
+// rate), 8 x 1569 7.0 (1664 blocks on 9 places a SM, 42% of issue slots), 64 x 1 3.8.  fp32: 22.3 us (3.8 TB/s), 11.8, 3.8.
 template <typename T>
 __global__ void __launch_bounds__(kStoreThreads) cache_store_kernel(const __grid_constant__ CacheArgs a) {
     __shared__ float tops[kStoreThreads / 32];
@@ -179,7 +179,7 @@ __global__ void __launch_bounds__(kStoreThreads) cache_store_kernel(const __grid
 }
 
 // Tokens from a page's keys or values, as the values they stand for; zeros from the sequence's count on.
-// The store's blocks the other way round, and bound as they are: 12.8 us, 6.6, 3.0; fp32 22.9, 10.9, 3.0.
+// The store's blocks the other way round, and held up as they are: 13.4 us, 6.4, 2.8; fp32 24.5, 10.5, 2.8.
 template <typename T>
 __global__ void __launch_bounds__(kStoreThreads) cache_load_kernel(const __grid_constant__ CacheArgs a) {
     __shared__ __align__(16) uint8_t lines[kHeadDim * kLine];
@@ -239,11 +239,11 @@ __global__ void __launch_bounds__(kStoreThreads) cache_load_kernel(const __grid_
 //
 // (The warp-wide instructions, since the rows would leave a tile of 128 unused 7/8 and more, and e4m3
 // becomes half in registers by one conversion of two values, which needs no second copy in shared memory.  Three
-// stages a pair: 48 KB on the way for each, 384 KB a SM.)
-// Measured: 16 sequences of 16384 or so, 16 heads on 4, one token: 23.5 us, 4.3 TB/s (50% of the DRAM's cycles under the
-// profiler, issue slots 37%; 256 CTAs have 304 places); 64 sequences, 4
-// tokens, window 1024, 4 sinks: 13.5, 2.6 TB/s (5 pages a pair of warps: start, join and end are half of it); one sequence
-// 10.4; fp32 34.4 (twice the products), 20.7, 13.5.
+// stages a pair: 24 KB on the way for each, 192 KB a SM; in 32 bits with 16 rows 96.)
+// Measured: 16 sequences of up to 16385, 16 heads on 4, one token: 23.1 us, 4.4 TB/s (50% of the DRAM's cycles under the
+// profiler, issue slots 37%; 256 CTAs have 304 places, and a cluster has one sequence, whose mean length is 3/4 of the
+// longest); 64 sequences, 4 tokens, window 1024, 4 sinks: 13.6, 2.6 TB/s (5 pages a pair of warps: start, join and
+// end are half of it); one sequence 10.2; fp32 31.9 (twice the products), 21.1, 13.3.
 constexpr int kPairs = 4, kStages = 3;
 constexpr int kWarps = 2 * kPairs, kThreads = 32 * kWarps;
 constexpr size_t kSmem = 128 + (size_t)kPairs * kStages * 2 * kPageBytes;
@@ -295,7 +295,7 @@ __device__ __forceinline__ uint32_t bytes_of(uint32_t four) {
 }
 
 // HALVES: 1 (at most 8 rows; the products' lower rows are not looked at) or 2.  (One token of 16
-// heads on 4, 16 sequences of 16385: 25.9 us with 1, 28.8 with 2; 64 of 1569: 11.4 and 14.0; fp32 34.4 and 44.3.)
+// heads on 4, 16 sequences of 16385: 23.0 us with 1, 26.6 with 2; 64 of 1569: 13.1 and 14.9; fp32 31.9 and 43.5.)
 template <typename T, int HALVES>
 struct Attend {
     static constexpr int kParts = sizeof(T) == 4 ? 2 : 1;             // halves of an operand
@@ -619,7 +619,7 @@ cudaError_t attend(const AttendArgs &f) {
     const cudaError_t e = prepare_kernel<cache_fwd_kernel<T, HALVES>>(kSmem, 0);
     if (e != cudaSuccess) return e;
     // CTAs of a cluster: as many as the GPU holds at once, as long as a pair of warps keeps a page.  (Us with 1, 2, 4, 8:
-    // 16 sequences of 16385 54, 31, 25.7, 31; one 53, 29, 16, 10.4; 64 of 1569 11.4, 17, 24, 38; 4 of them 8.5, 6.9, 5.5, 5.3.)
+    // 16 sequences of 16385 52, 29, 22.7, 26.5; one 50, 29, 16, 10.1; 64 of 1569 13.2, 19, 27, 42; 4 of them 8.2, 6.6, 5.3, 5.0.)
     const int64_t keys = std::min<int64_t>((int64_t)f.c.table_len * kPage, (int64_t)f.band.window + f.band.sinks + f.c.N);
     int c = 1;
     while (c < 8 && (int64_t)f.units * c * 2 <= Attend<T, HALVES>::kBlocks * sm_count() && keys > (int64_t)c * kPairs * kPage) c *= 2;

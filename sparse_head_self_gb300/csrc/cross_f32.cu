@@ -6,8 +6,9 @@
 // lo lo, is below 2^-22 of the product.  At 301 TFLOP/s of these instructions
 // (measured) that is 100 TFLOP/s of products, where the FP32 units give 80 at most and
 // gave 34 here, held up by the shared memory's bandwidth.  (The 5th-generation
-// cores' TF32 form reads its second operand along the summed index only, which
-// P V and dS K do not have, and needs every tile twice in shared memory.)
+// cores' TF32 form would need every tile twice in shared memory, its upper and its lower bits, and for P V
+// and dS K, whose second operand lies across the summed index, the swizzle in pieces of 32
+// bytes that there is for 32-bit types.  Not built.)
 // Measured: gradient of 4 sequences, 12 heads, 197 x 197, masked: 64 us (FP32 units:
 // 85.5), 384 blocks of which some SMs have three and some two, the warp-wide
 // instructions 33% busy: a scheduler's three warps wait for their own chains of cuts and
@@ -37,9 +38,10 @@
 // Attention over a window with sinks (BAND): walks over the tiles that the windows meet; within a tile
 // each warp's products start and end at the columns that its 16 rows may attend, in steps of 32 and 8,
 // since at three instructions a product what is left out counts (gradient of 4 sequences, 12
-// heads, up to 197 tokens, window 65, 1 sink: 54 -> 45.2 us; units worked out without divisions and shorter code, 43.5).  There a SM has 3 CTAs of 4 warps, the warp-wide
-// instructions are 17% busy, and the time goes to the waits for copies at the CTA's barriers: walks have 2 or 3 tiles.
-// 2 sequences, 16 heads on 4, 1569 tokens, window 512, 4 sinks: forward 178 us, gradient 957.
+// heads, up to 197 tokens, window 65, 1 sink: 54 -> 45.2 us; units worked out without divisions and shorter code, 43.1).
+// There a SM has 3 CTAs of 4 warps, the warp-wide instructions are 17% busy, and the time goes to the waits for copies at the
+// CTA's barriers: walks have 2 or 3 tiles.  2 sequences, 16 heads on 4, 1569 tokens, window 512, 4 sinks: forward
+// 179 us (31 TFLOP/s of 100), gradient 920.
 #include <algorithm>
 
 #include "cluster.cuh"

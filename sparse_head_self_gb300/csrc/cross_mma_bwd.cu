@@ -48,9 +48,9 @@
 // results are put where its held rows were and leave by tensor copies that the copying warp sends, and
 // its rows' statistics are asked for one unit ahead; no thread divides (Div: 261 -> 251 us, and 82.8 -> 78.5 below, where
 // a tile of keys took 2140 cycles for 1600).
-// Measured (4 sinks): 16 heads on 4, 16385 tokens, window 1024: 250 us, 669 TFLOP/s of the 5 products (about 1600
+// Measured (4 sinks): 16 heads on 4, 16385 tokens, window 1024: 249 us, 670 TFLOP/s of the 5 products (about 1600
 // cycles a tile of either kind, 2150 between units of 9 or 10 tiles; the small kernels about 20 us of it); 8 sequences,
-// 12 heads on 4, up to 1569 tokens, window 512: 75.1, 360 (the first small kernel about 9; units of 5 or 6 tiles of
+// 12 heads on 4, up to 1569 tokens, window 512: 74.7, 362 (the first small kernel about 9; units of 5 or 6 tiles of
 // keys, 16 of queries).
 #include <algorithm>
 
@@ -1101,7 +1101,8 @@ namespace {
 
 // How the walks of key tiles with sinks are cut: into parts as long as the other tiles' walks, or as half of
 // what an SM has in all where that is more (they come first, so that the rest evens them out), as
-// long as there are no more than kParts of them in all (two a SM, each with 64 KB of partial sums).  (One
+// long as there are no more than kParts of them in all (two a SM, each with 64 KB of partial sums; a number of its
+// own, so that the workspace that a call asks for and the one it uses agree whatever device is current).  (One
 // sequence of 16385 tokens, 16 heads on 4, window 1024, 4 sinks: walks of 516 tiles next to others of
 // 36; in one part 673 us, in parts of 36 266, as here 261; window 128: 151 and 129; eight sequences of
 // 1569, 12 heads on 4, window 512, in one part here: 107 and 101.6.)

@@ -49,11 +49,11 @@
 //   walks start at the oldest key, not at a multiple of 128 (the third 34 -> 32)
 //   tiles of neighbouring positions and of heads that share keys are neighbours in the grid: L2 serves 81% of the reads
 //   few sinks in front of the window's first tile, and 32 columns left out, where that pays (below)
-// Measured (4 sinks): 16 heads on 4 key heads, 16385 tokens, window 1024: 95.4 us, 700 TFLOP/s of
+// Measured (4 sinks): 16 heads on 4 key heads, 16385 tokens, window 1024: 95.1 us, 703 TFLOP/s of
 // the pairs attended (36% and 37% of the time tensor cores and exponentials work, issue slots 63% taken); 2 times 1569
-// queries on 16385 keys, window 4096: 73.9, 713; 8 sequences, 12 heads on 4, up to 1569 tokens, window
-// 512: 30.7, 353 (units of 5 or 6 tiles, two or three of them masked); 64 sequences, 12 heads, up
-// to 197 tokens, window 64, 1 sink: 23.9, 2.6 TB/s.
+// queries on 16385 keys, window 4096: 75.2, 701; 8 sequences, 12 heads on 4, up to 1569 tokens, window
+// 512: 30.2, 358 (units of 5 or 6 tiles, two or three of them masked); 64 sequences, 12 heads, up
+// to 197 tokens, window 64, 1 sink: 23.2, 2.7 TB/s.
 #include <algorithm>
 
 #include "cluster.cuh"

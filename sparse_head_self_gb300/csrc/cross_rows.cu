@@ -21,8 +21,8 @@
 //
 // Attention over a window with sinks (BAND): the same over the keys of the sinks and of the rows' windows alone, cut
 // over the cluster as if they lay together.  (16 sequences, 16 heads on 4, one token, window
-// 1024 of up to 16385, 4 sinks: 6.7 us, 2.4 TB/s: the launch, one copy's latency and the join
-// are 4 of them; in 32 bits 11.9.)
+// 1024 of up to 16385, 4 sinks: 8.3 us, 1.9 TB/s, 6.7 with the keys in L2: the launch, one copy's latency and the join
+// are 4 of them; in 32 bits 14.1.)
 #include <algorithm>
 
 #include "cluster.cuh"
