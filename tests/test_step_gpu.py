@@ -169,3 +169,32 @@ def test_the_way_that_is_taken():
     assert pages(1, 1024, 1600, 128) and not pages(1, 1024, 16448, None)
     assert not pages(1, 4 * 16384, 16448, 4096) and pages(1, 1024, 16448, None, F32)
     assert pages(64, 4, 16448, 1024) and pages(16, 4, 16448, None)
+
+
+@pytest.mark.parametrize("band", [(None, 0), (90, 3)], ids=str)
+def test_captured_and_replayed_chunk_by_chunk(band, way):
+    # one graph takes a chunk and moves on, on another stream than the layer's memory came from
+    layer = _layer(4, 2, True, True, *band, seed=29)
+    B, M, N = 2, 6, 64
+    x = torch.randn(B, 5 * N, 256, device="cuda")
+    table = torch.randperm(B * M, generator=torch.Generator().manual_seed(1)).to(torch.int32).view(B, M).cuda()
+    plain, cache = (api.Cache.new(B * M, 2) for _ in range(2))
+    want = [layer.step(x[:, i * N:(i + 1) * N], plain, table, _int32(i * N, i * N)) for i in range(5)]
+    part, at = torch.zeros(B, N, 256, device="cuda"), _int32(0, 0)
+    count = _int32(N, N)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        layer.step(part, cache, table, at, count)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=side):
+            out = layer.step(part, cache, table, at, count)
+            at += count
+        for i in range(5):
+            part.copy_(x[:, i * N:(i + 1) * N])
+            graph.replay()
+            torch.testing.assert_close(out, want[i], rtol=0, atol=1e-5 * float(want[i].abs().max()))
+    side.synchronize()
+    assert at.tolist() == [5 * N, 5 * N]
+    for a, b in zip(cache, plain):
+        assert torch.equal(a, b)
